@@ -67,8 +67,10 @@ typedef enum {
     S4_ERR_SINGULAR_BILINEAR = 8,    /* G = I - (Delta/2) A not solved: I_r + (Delta/2) Q^* D^{-1} P is
                                         exactly singular; or, where some d_j = 1 - (Delta/2) lambda_j is
                                         exactly 0, more such d_j than r, or a singular bordered matrix */
-    S4_ERR_TIMEOUT = 9               /* a kernel's bounded wait for an asynchronous copy into shared
+    S4_ERR_TIMEOUT = 9,              /* a kernel's bounded wait for an asynchronous copy into shared
                                         memory ran out (the affected output is zeros) */
+    S4_ERR_INVALID_INDEX = 10        /* a sequence's length or state slot (device arrays of the selective
+                                        block) is out of range; that sequence's output is zeros */
 } s4_status;
 
 /* Bytes of scratch that s4_kernel_gen, s4_conv_fwd and s4_layer_fwd need for
@@ -239,6 +241,137 @@ s4_status s4_recurrent_fwd(const s4_c32* Lambda, const s4_c32* P, const s4_c32* 
 typedef enum { S4_HIPPO_LEGS = 0, S4_HIPPO_LEGT = 1, S4_HIPPO_LAGT = 2 } s4_hippo_kind;
 s4_status s4_hippo_dplr(int kind, int N, double theta, const double* B, const double* C,
                         double* Lambda, double* P, double* Bt, double* Ct, int* rank);
+
+/* ======================================================================
+ * The selective state-space block: a short causal convolution, the selective
+ * scan and the norms around the block, with backward passes, for prompts and
+ * for single tokens.
+ *
+ * Conventions, beside those above
+ *  - Arrays of activations are [batch][L][channels] (a token's channels are
+ *    contiguous, as matrix products before and after the block leave them),
+ *    given as s4_rows: the address of element (0, 0, 0) and the strides of
+ *    the batch and of the tokens in elements.  A slice of a wider array (one
+ *    half of a projection) is passed as it lies.  All activations of a call
+ *    have one type, `dtype`; parameters, their gradients and the scan's
+ *    states are fp32.  Accesses are 16 bytes wide where addresses and strides
+ *    are multiples of that, and narrower elsewhere.
+ *  - All sums, norms, states and exponents are fp32; each output is rounded
+ *    once.
+ *  - `lengths` [batch] (device, may be NULL): the sequences' real lengths, 0
+ *    to L.  Tokens from there on are padding: what they hold (infinities and
+ *    NaN too) is not used, their outputs and gradients are zeros, and the state
+ *    stays as after the last real token.
+ *  - `state`, `state_out` (may be NULL): the state on entry (NULL: zeros) and
+ *    where the state after the last real token goes (NULL: nowhere); they may
+ *    be the same array (in place).  `index` [batch] (device, may be NULL):
+ *    the slot of each sequence in both, 0 to slots - 1; a negative slot marks
+ *    a row of the batch that is not in use: its outputs are zeros and no state
+ *    is touched.  Slots of one call must differ from each other.  index = NULL:
+ *    sequence b has slot b (slots >= batch).
+ *  - A length outside 0..L or a slot >= slots makes that sequence's outputs
+ *    zeros, touches no state, and is recorded as S4_ERR_INVALID_INDEX in the
+ *    status block of `ws` (read with s4_get_status).
+ *  - Results are the same on every run: no sum goes through atomics.
+ *  - Sizes: 1 <= batch <= 65535, 1 <= L <= 2^24, 1 <= H <= 65536,
+ *    2 <= W <= 8, 1 <= N <= 256; offsets are 64 bits wide.
+ * ====================================================================== */
+typedef enum { S4_F32 = 0, S4_BF16 = 1, S4_F16 = 2 } s4_dtype;
+
+/* A [batch][L][channels] array, channels contiguous; strides in elements. */
+typedef struct {
+    const void* p;
+    long long batch, row;
+} s4_rows;
+typedef struct {
+    void* p;
+    long long batch, row;
+} s4_rows_out;
+
+/*
+ * s4_short_conv_fwd -- causal convolution along time with a filter of W taps per
+ * channel, and SiLU:  v_t = bias + sum_{k<W} w[k] x[t-W+1+k],  y = v sigmoid(v)
+ * (silu = 0: y = v).  The W-1 inputs before the first token are the state (oldest
+ * first); the state after the call is the last W-1 inputs.  L = 1 is the
+ * single-token form.
+ */
+typedef struct {
+    s4_rows x;                /* [batch][L][H] */
+    s4_rows_out y;            /* [batch][L][H] */
+    const float* w;           /* [H][W] */
+    const float* bias;        /* [H] or NULL */
+    const int* lengths;       /* [batch] or NULL */
+    const int* index;         /* [batch] or NULL */
+    const void* state;        /* [slots][W-1][H] of the activations' type, or NULL */
+    void* state_out;          /* likewise */
+    void* ws;                 /* the status block (256 bytes, 256-byte aligned), or NULL: not recorded */
+    size_t ws_bytes;
+    int batch, L, H, W, slots, dtype, silu;
+} s4_short_conv_args;
+s4_status s4_short_conv_fwd(const s4_short_conv_args* a, void* stream);
+
+/*
+ * s4_short_conv_bwd -- gradients of s4_short_conv_fwd: with dv = dy silu'(v),
+ *   dx_t = sum_k w[k] dv[t+W-1-k],  dw[k] = sum_{b,t} dv_t x[t-W+1+k],  dbias = sum_{b,t} dv_t.
+ * v is computed again from x.  state0, dstate, dstate0 [batch][W-1][H] (of the
+ * activations' type, each may be NULL): the state on entry (zeros), the gradient
+ * of the state on return (zeros) and where the gradient of the state on entry goes.
+ */
+typedef struct {
+    s4_rows x, dy;
+    s4_rows_out dx;
+    const float *w, *bias;
+    const int* lengths;
+    const void *state0, *dstate;
+    void* dstate0;            /* not the array dstate */
+    float* dw;                /* [H][W] */
+    float* dbias;             /* [H], or NULL where bias is NULL */
+    void* ws;                 /* s4_short_conv_bwd_workspace_bytes */
+    size_t ws_bytes;
+    int batch, L, H, W, dtype, silu;
+} s4_short_conv_bwd_args;
+size_t s4_short_conv_bwd_workspace_bytes(int batch, int L, int H, int W);
+s4_status s4_short_conv_bwd(const s4_short_conv_bwd_args* a, void* stream);
+
+/*
+ * s4_block_norm_fwd -- what joins two blocks: the gate and norm after a block, its residual
+ * scale, the residual sum, and the norm before the next block.  Per row of H channels,
+ *     v = o silu(gate),  p = v rsqrt(mean v^2 + eps) w_post,
+ *     h_out = h + scale p,  y = h_out rsqrt(mean h_out^2 + eps) w_pre
+ * where gate, w_post (then p = v), scale (1), h (0) and w_pre (then no y) may each be
+ * absent.  h and h_out are fp32 (res_f32 = 1) or of the activations' type; y is
+ * formed from h_out before its rounding.  h_out may be h.  1 <= H <= 16384.
+ */
+typedef struct {
+    const void *o, *gate, *h;       /* [rows][H], row strides below in elements */
+    void *h_out, *y;
+    const float *w_post, *scale, *w_pre;   /* [H] */
+    long long o_row, gate_row, h_row, h_out_row, y_row;
+    long long rows;
+    float eps;
+    int H, dtype, res_f32;
+} s4_block_norm_args;
+s4_status s4_block_norm_fwd(const s4_block_norm_args* a, void* stream);
+
+/*
+ * s4_block_norm_bwd -- gradients of s4_block_norm_fwd from dy and dh_out (either may be
+ * NULL: zeros), everything else computed again from the forward's inputs (h as it was
+ * on entry).  dh [rows][H] has h's type, do_ and dgate the activations'.
+ */
+typedef struct {
+    const void *o, *gate, *h, *dy, *dh_out;
+    void *do_, *dgate, *dh;
+    const float *w_post, *scale, *w_pre;
+    float *dw_post, *dscale, *dw_pre;      /* [H], NULL where the parameter is */
+    void* ws;                       /* s4_block_norm_bwd_workspace_bytes */
+    size_t ws_bytes;
+    long long o_row, gate_row, h_row, dy_row, dh_out_row, do_row, dgate_row, dh_row;
+    long long rows;
+    float eps;
+    int H, dtype, res_f32;
+} s4_block_norm_bwd_args;
+size_t s4_block_norm_bwd_workspace_bytes(long long rows, int H);
+s4_status s4_block_norm_bwd(const s4_block_norm_bwd_args* a, void* stream);
 
 /* Synchronises `stream`, then returns the device-detected status recorded in
  * `ws` by the last entry point that used it (S4_OK if none), or

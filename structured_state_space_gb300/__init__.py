@@ -15,6 +15,9 @@ Entry points (same names as the C ABI):
     s4_recurrent_fwd(Lambda, P, Q, B, C, dt, D, u, x)  -> (y, x)   (recurrent mode)
     s4_workspace_bytes(H, N, r, L, batch)
     s4_get_status(ws), s4_status_str(code)
+and the selective block's operators (block.py, imported on first use):
+    s4_short_conv_fwd / _step / _bwd                   short causal convolution with SiLU
+    s4_block_norm_fwd / _bwd                           norms around a block, gate, residual scale and sum
 """
 from __future__ import annotations
 
@@ -31,7 +34,7 @@ __all__ = [
 STATUS = {
     0: "S4_OK", 1: "S4_ERR_INVALID_ARG", 2: "S4_ERR_WORKSPACE", 3: "S4_ERR_RESONANT_DIAGONAL",
     4: "S4_ERR_RESONANT_CORRECTION", 5: "S4_ERR_NONFINITE", 6: "S4_ERR_INVALID_STEP", 7: "S4_ERR_CUDA",
-    8: "S4_ERR_SINGULAR_BILINEAR", 9: "S4_ERR_TIMEOUT",
+    8: "S4_ERR_SINGULAR_BILINEAR", 9: "S4_ERR_TIMEOUT", 10: "S4_ERR_INVALID_INDEX",
 }
 STATUS_CODE = {v: k for k, v in STATUS.items()}
 
@@ -41,6 +44,8 @@ ABI_FUNCTIONS = [
     "s4_status_str", "s4_timing_enable", "s4_timing_reset", "s4_timing_read",
     "s4_conv_fwd_noalloc", "s4_ctilde", "s4_recurrent_fwd", "s4_conv_fwd_real",
     "s4_hippo_dplr", "s4_fp32_probe", "s4_set_wait_limit", "s4_bounds_violations",
+    "s4_short_conv_fwd", "s4_short_conv_bwd", "s4_short_conv_bwd_workspace_bytes",
+    "s4_block_norm_fwd", "s4_block_norm_bwd", "s4_block_norm_bwd_workspace_bytes",
 ]
 
 HIPPO_KINDS = {"legs": 0, "legt": 1, "lagt": 2}
@@ -51,6 +56,20 @@ class S4Error(RuntimeError):
         self.code = int(code)
         self.name = STATUS.get(self.code, f"status {code}")
         super().__init__(f"{where}: {self.name} ({s4_status_str(self.code)})")
+
+
+# The selective block's operators, defined in block.py (which needs torch, loaded on first use).
+_BLOCK = ["s4_short_conv_fwd", "s4_short_conv_step", "s4_short_conv_bwd", "s4_block_norm_fwd", "s4_block_norm_bwd"]
+__all__ += _BLOCK
+
+
+def __getattr__(name):
+    if name in _BLOCK:
+        from . import block
+        for n in _BLOCK:
+            globals()[n] = getattr(block, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 _lib = None

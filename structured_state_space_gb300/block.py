@@ -1,0 +1,294 @@
+"""The selective block's operators over the C ABI: the short causal convolution and the
+norms around a block, forward and backward.
+
+Activations are [batch, L, channels] tensors (float32, bfloat16 or float16) whose channels are
+contiguous; any batch and row strides are taken as they are, so slices of a projection's
+output need no copy.  Parameters are float32.  As in the rest of the binding there is no
+fallback: a tensor that does not fit raises, and the library's kernels do all the work.
+
+With ``stream`` given, results and workspaces are allocated for that stream; the caller orders
+it after the work that fills the inputs.
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+
+import torch
+
+from . import S4Error, load
+
+__all__ = ["s4_short_conv_fwd", "s4_short_conv_step", "s4_short_conv_bwd", "s4_block_norm_fwd", "s4_block_norm_bwd"]
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_F32, _I32 = torch.float32, torch.int32
+_empty = torch.empty
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+# The argument structs of include/s4.h, packed as C lays them out.
+_CONV = struct.Struct("@6q7PN7i0q")
+_CONV_BWD = struct.Struct("@9q9PN6i0q")
+_NORM = struct.Struct("@8P6qf3i0q")
+_NORM_BWD = struct.Struct("@15PN9qf3i0q")
+
+_fn = {}
+
+
+def _lib():
+    """The library's entry points by name, with their argument types set once."""
+    lib = load()
+    vp, i32, sz, ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
+    for name in ("s4_short_conv_fwd", "s4_short_conv_bwd", "s4_block_norm_fwd", "s4_block_norm_bwd"):
+        f = getattr(lib, name)
+        f.argtypes, f.restype = [ctypes.c_char_p, vp], i32
+        _fn[name] = f
+    for name, args in (("s4_short_conv_bwd_workspace_bytes", [i32] * 4), ("s4_block_norm_bwd_workspace_bytes", [ll, i32])):
+        f = getattr(lib, name)
+        f.argtypes, f.restype = args, sz
+        _fn[name] = f
+    return _fn
+
+
+def _call(name, args, x):
+    f = _fn.get(name) or _lib()[name]
+    code = f(args, _raw_stream(x.get_device()))
+    if code:
+        raise S4Error(code, name)
+
+
+def _bytes(name, *sizes):
+    n = (_fn.get(name) or _lib()[name])(*sizes)
+    if n == 0:
+        raise S4Error(1, name)
+    return n
+
+
+def _ws(ws, need, x):
+    return _empty(need, dtype=torch.uint8, device=x.device) if ws is None else ws
+
+
+def _bad(t, name, dtype, shape):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    raise ValueError(f"{name}: its last dimension must be contiguous" if t.dim() > 1 and not t.is_contiguous()
+                     else f"{name} must be contiguous")
+
+
+def _dense(t, dtype, shape, name):
+    """Address of a contiguous tensor of this type and shape; 0 for None."""
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _bad(t, name, dtype, shape)
+    return t.data_ptr()
+
+
+def _rows(t, dtype, shape, name):
+    """(address, batch stride, row stride) of [batch, L, channels]; zeros for None."""
+    if t is None:
+        return 0, 0, 0
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_cuda:
+        _bad(t, name, dtype, shape)
+    sb, sr, sc = t.stride()
+    if sc != 1 and shape[2] != 1:
+        raise ValueError(f"{name}: its channels must be contiguous")
+    return t.data_ptr(), sb, sr
+
+
+def _tokens(t, dtype, shape, name):
+    """The same of one token per sequence, [batch, channels]."""
+    if t is None:
+        return 0, 0, 0
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_cuda:
+        _bad(t, name, dtype, shape)
+    sb, sc = t.stride()
+    if sc != 1 and shape[1] != 1:
+        raise ValueError(f"{name}: its channels must be contiguous")
+    return t.data_ptr(), sb, sb
+
+
+def _code(x):
+    c = _DTYPES.get(x.dtype) if isinstance(x, torch.Tensor) else None
+    if c is None:
+        raise TypeError("activations must be float32, bfloat16 or float16 tensors")
+    return c
+
+
+def _on(stream, f, *args, **kw):
+    with torch.cuda.stream(stream):
+        return f(*args, **kw)
+
+
+def _slots(state, state_out, batch, index):
+    n = state.shape[0] if state is not None else state_out.shape[0] if state_out is not None else 0
+    if n < batch and index is None and (state is not None or state_out is not None):
+        raise ValueError(f"state: {n} slots for {batch} sequences and no index")
+    return n
+
+
+def s4_short_conv_fwd(x, w, bias=None, *, silu=True, lengths=None, state=None, state_out=None, index=None, y=None,
+                      ws=None, stream=None):
+    """y = silu(causal convolution of x [batch, L, H] with w [H, W] along L, plus bias).
+
+    lengths [batch] int32: real tokens of each sequence.  state, state_out [slots, W-1, H] (x's type):
+    the inputs before the first token and where the last ones go (the same tensor for in place;
+    neither is needed); index [batch] int32: each sequence's slot, negative for none.  ws (256 bytes, see
+    s4_get_status) records a length or slot out of range."""
+    if stream is not None:
+        return _on(stream, s4_short_conv_fwd, x, w, bias, silu=silu, lengths=lengths, state=state, state_out=state_out,
+                   index=index, y=y, ws=ws)
+    code, dt, shape = _code(x), x.dtype, x.shape
+    batch, L, H = shape
+    W = w.shape[1]
+    if y is None:
+        y = _empty(shape, dtype=dt, device=x.device)
+    slots = _slots(state, state_out, batch, index)
+    args = _CONV.pack(*_rows(x, dt, shape, "x"), *_rows(y, dt, shape, "y"), _dense(w, _F32, (H, W), "w"),
+                      _dense(bias, _F32, (H,), "bias"), _dense(lengths, _I32, (batch,), "lengths"),
+                      _dense(index, _I32, (batch,), "index"), _dense(state, dt, (slots, W - 1, H), "state"),
+                      _dense(state_out, dt, (slots, W - 1, H), "state_out"),
+                      0 if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                      batch, L, H, W, slots, code, 1 if silu else 0)
+    _call("s4_short_conv_fwd", args, x)
+    return y
+
+
+def s4_short_conv_step(x, w, bias, state, *, silu=True, state_out=None, index=None, y=None, ws=None, stream=None):
+    """One token per sequence: x [batch, H] -> y [batch, H].  The state is updated in place, or
+    written to state_out (the old one then stays, as for tokens that may be rejected)."""
+    if stream is not None:
+        return _on(stream, s4_short_conv_step, x, w, bias, state, silu=silu, state_out=state_out, index=index, y=y, ws=ws)
+    code, dt, shape = _code(x), x.dtype, x.shape
+    batch, H = shape
+    W = w.shape[1]
+    if y is None:
+        y = _empty(shape, dtype=dt, device=x.device)
+    slots = _slots(state, state, batch, index)
+    old = _dense(state, dt, (slots, W - 1, H), "state")
+    args = _CONV.pack(*_tokens(x, dt, shape, "x"), *_tokens(y, dt, shape, "y"), _dense(w, _F32, (H, W), "w"),
+                      _dense(bias, _F32, (H,), "bias"), 0, _dense(index, _I32, (batch,), "index"), old,
+                      old if state_out is None else _dense(state_out, dt, (slots, W - 1, H), "state_out"),
+                      0 if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                      batch, 1, H, W, slots, code, 1 if silu else 0)
+    _call("s4_short_conv_fwd", args, x)
+    return y
+
+
+def s4_short_conv_bwd(x, w, bias, dy, *, silu=True, lengths=None, state=None, dstate=None, want_dstate0=False, ws=None,
+                      stream=None):
+    """Gradients of s4_short_conv_fwd from dy: a dict of dx, dw, dbias (with a bias), and dstate0, the
+    gradient of the state on entry, where asked for.  state, dstate [batch, W-1, H]: the state on
+    entry and the gradient of the state on return (None: zeros)."""
+    if stream is not None:
+        return _on(stream, s4_short_conv_bwd, x, w, bias, dy, silu=silu, lengths=lengths, state=state, dstate=dstate,
+                   want_dstate0=want_dstate0, ws=ws)
+    code, dt, shape, dev = _code(x), x.dtype, x.shape, x.device
+    batch, L, H = shape
+    W = w.shape[1]
+    ws = _ws(ws, _bytes("s4_short_conv_bwd_workspace_bytes", batch, L, H, W), x)
+    out = {"dx": _empty(shape, dtype=dt, device=dev), "dw": _empty((H, W), dtype=_F32, device=dev)}
+    if bias is not None:
+        out["dbias"] = _empty((H,), dtype=_F32, device=dev)
+    if want_dstate0:
+        out["dstate0"] = _empty((batch, W - 1, H), dtype=dt, device=dev)
+    past = (batch, W - 1, H)
+    args = _CONV_BWD.pack(*_rows(x, dt, shape, "x"), *_rows(dy, dt, shape, "dy"), *_rows(out["dx"], dt, shape, "dx"),
+                          _dense(w, _F32, (H, W), "w"), _dense(bias, _F32, (H,), "bias"),
+                          _dense(lengths, _I32, (batch,), "lengths"), _dense(state, dt, past, "state"),
+                          _dense(dstate, dt, past, "dstate"), _dense(out.get("dstate0"), dt, past, "dstate0"),
+                          out["dw"].data_ptr(), _dense(out.get("dbias"), _F32, (H,), "dbias"),
+                          ws.data_ptr(), ws.numel(), batch, L, H, W, code, 1 if silu else 0)
+    _call("s4_short_conv_bwd", args, x)
+    return out
+
+
+def _flat(t, dtype, shape, name):
+    """(address, row stride) of [rows, H], or of leading dimensions that make rows of one stride."""
+    if t is None:
+        return 0, 0
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_cuda:
+        _bad(t, name, dtype, shape)
+    if len(shape) != 2:
+        t = t.view(-1, shape[-1])
+    sr, sc = t.stride()
+    if sc != 1 and shape[-1] != 1:
+        raise ValueError(f"{name}: its channels must be contiguous")
+    return t.data_ptr(), sr
+
+
+def _residual(h, dtype):
+    if h is not None and h.dtype != dtype and h.dtype != _F32:
+        raise TypeError(f"h: dtype {h.dtype}, expected {dtype} or float32")
+    return dtype if h is None else h.dtype
+
+
+def s4_block_norm_fwd(o, *, w_post=None, gate=None, scale=None, h=None, w_pre=None, eps=1e-5, h_out=None, y=None,
+                      stream=None):
+    """What joins two blocks: h_out = h + scale * norm(o * silu(gate)) * w_post and
+    y = norm(h_out) * w_pre, norm(v) = v / sqrt(mean(v^2) + eps) over the last dimension.
+
+    o, gate [..., H] of one type; h [..., H] of that type or float32, and h_out of h's (h_out may be h);
+    w_post, scale, w_pre [H].  What is None is left out: without gate no gating, without w_post no
+    first norm, without h nothing is added.  Returns (h_out, y), y None without w_pre."""
+    if stream is not None:
+        return _on(stream, s4_block_norm_fwd, o, w_post=w_post, gate=gate, scale=scale, h=h, w_pre=w_pre, eps=eps,
+                   h_out=h_out, y=y)
+    code, dt, shape, dev = _code(o), o.dtype, o.shape, o.device
+    H = shape[-1]
+    res = _residual(h if h is not None else h_out, dt)
+    if h_out is None:
+        h_out = _empty(shape, dtype=res, device=dev)
+    if y is None and w_pre is not None:
+        y = _empty(shape, dtype=dt, device=dev)
+    po, so = _flat(o, dt, shape, "o")
+    pg, sg = _flat(gate, dt, shape, "gate")
+    ph, sh = _flat(h, res, shape, "h")
+    pq, sq = _flat(h_out, res, shape, "h_out")
+    py, sy = _flat(y, dt, shape, "y")
+    args = _NORM.pack(po, pg, ph, pq, py, _dense(w_post, _F32, (H,), "w_post"), _dense(scale, _F32, (H,), "scale"),
+                      _dense(w_pre, _F32, (H,), "w_pre"), so, sg, sh, sq, sy, o.numel() // H if H else 0, eps, H, code,
+                      1 if res is _F32 else 0)
+    _call("s4_block_norm_fwd", args, o)
+    return h_out, y
+
+
+def s4_block_norm_bwd(o, dy=None, *, dh_out=None, w_post=None, gate=None, scale=None, h=None, w_pre=None, eps=1e-5,
+                      ws=None, stream=None):
+    """Gradients of s4_block_norm_fwd from dy and dh_out (None: zeros; not both): a dict of do and, for
+    what was given, dgate, dh, dw_post, dscale and dw_pre."""
+    if stream is not None:
+        return _on(stream, s4_block_norm_bwd, o, dy, dh_out=dh_out, w_post=w_post, gate=gate, scale=scale, h=h,
+                   w_pre=w_pre, eps=eps, ws=ws)
+    code, dt, shape, dev = _code(o), o.dtype, o.shape, o.device
+    H = shape[-1]
+    rows = o.numel() // H if H else 0
+    res = _residual(h if h is not None else dh_out, dt)
+    ws = _ws(ws, _bytes("s4_block_norm_bwd_workspace_bytes", rows, H), o)
+    out = {"do": _empty(shape, dtype=dt, device=dev)}
+    if gate is not None:
+        out["dgate"] = _empty(shape, dtype=dt, device=dev)
+    if h is not None:
+        out["dh"] = _empty(shape, dtype=res, device=dev)
+    for k, v in (("dw_post", w_post), ("dscale", scale), ("dw_pre", w_pre)):
+        if v is not None:
+            out[k] = _empty((H,), dtype=_F32, device=dev)
+    po, so = _flat(o, dt, shape, "o")
+    pg, sg = _flat(gate, dt, shape, "gate")
+    ph, sh = _flat(h, res, shape, "h")
+    py, sy = _flat(dy, dt, shape, "dy")
+    pq, sq = _flat(dh_out, res, shape, "dh_out")
+    get = out.get
+    args = _NORM_BWD.pack(po, pg, ph, py, pq, out["do"].data_ptr(), _dense(get("dgate"), dt, shape, "dgate"),
+                          _dense(get("dh"), res, shape, "dh"), _dense(w_post, _F32, (H,), "w_post"),
+                          _dense(scale, _F32, (H,), "scale"), _dense(w_pre, _F32, (H,), "w_pre"),
+                          _dense(get("dw_post"), _F32, (H,), "dw_post"), _dense(get("dscale"), _F32, (H,), "dscale"),
+                          _dense(get("dw_pre"), _F32, (H,), "dw_pre"), ws.data_ptr(), ws.numel(),
+                          so, sg, sh, sy, sq, H, H, H, rows, eps, H, code, 1 if res is _F32 else 0)
+    _call("s4_block_norm_bwd", args, o)
+    return out

@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "s4.h"
+#include "s4_block.h"
 #include "s4_dev.cuh"
 #include "s4_internal.h"
 
@@ -87,6 +88,10 @@ unsigned next_generation() {
   return g;
 }
 
+}  // namespace
+
+namespace s4impl {
+
 // The status of a call on `s`: a fresh generation, with no reset of the block
 // and the call's first kernel chained to the previous kernel (`chain`) -- unless
 // `s` is being captured into a graph.  A captured call would replay its
@@ -106,6 +111,12 @@ bool call_status(void* ws, cudaStream_t s, s4impl::St* st, bool* chain) {
   *chain = true;
   return true;
 }
+
+}  // namespace s4impl
+
+namespace {
+
+using s4impl::call_status;
 
 // Root values in the blocked order of 2^logC (logC < 0: the order the inverse
 // transform of s4_kernel_gen reads, khat_cluster_log).
@@ -267,7 +278,8 @@ long long s4_bounds_violations(void) {
 #ifdef S4_BOUNDS_CHECK
   if (cudaDeviceSynchronize() != cudaSuccess) return -2;
   const unsigned long long c[] = {s4impl::oob_rows(), s4impl::oob_cluster(), s4impl::oob_fourstep(),
-                                  s4impl::oob_cauchy(), s4impl::oob_recurrent(), s4impl::oob_bordered()};
+                                  s4impl::oob_cauchy(), s4impl::oob_recurrent(), s4impl::oob_bordered(),
+                                  s4impl::oob_short_conv(), s4impl::oob_block_norm()};
   unsigned long long t = 0;
   for (unsigned long long v : c) {
     if (v == ~0ull) return -2;
@@ -467,6 +479,7 @@ s4_status s4_get_status(const void* ws, void* stream) {
   if (cudaMemcpy(blk, ws, sizeof(blk), cudaMemcpyDeviceToHost) != cudaSuccess) return S4_ERR_CUDA;
   const unsigned word = blk[1] == blk[2] ? blk[0] : 0u;  // older flags are stale
   if (word & s4dev::ST_STALL) return S4_ERR_TIMEOUT;
+  if (word & s4impl::ST_BAD_INDEX) return S4_ERR_INVALID_INDEX;
   if (word & s4dev::ST_BAD_STEP) return S4_ERR_INVALID_STEP;
   if (word & s4dev::ST_RES_DIAG) return S4_ERR_RESONANT_DIAGONAL;
   if (word & s4dev::ST_RES_CORR) return S4_ERR_RESONANT_CORRECTION;
@@ -487,6 +500,7 @@ const char* s4_status_str(s4_status st) {
     case S4_ERR_CUDA: return "CUDA error";
     case S4_ERR_SINGULAR_BILINEAR: return "singular-bilinear-matrix";
     case S4_ERR_TIMEOUT: return "timeout";
+    case S4_ERR_INVALID_INDEX: return "length or state slot out of range";
   }
   return "unknown status";
 }

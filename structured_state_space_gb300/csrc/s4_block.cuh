@@ -1,0 +1,146 @@
+// Device building blocks of the selective block's kernels: element types, row
+// accesses of one to sixteen bytes, activations, column sums.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "s4_block.h"
+#include "s4_dev.cuh"
+
+namespace s4blk {
+
+using s4impl::St;
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+
+// V elements of T as they lie in memory; accessed whole where aligned.
+template <typename T, int V>
+struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Pack {
+  T e[V];
+};
+
+// V consecutive elements at p, of which `n` exist (the others read as 0 and are not
+// written).  `vec`: p is a multiple of the pack's alignment.
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> ld_pack(const T* p, int n, bool vec) {
+  Pack<T, V> r;
+  if (vec && n >= V) {
+    r = *reinterpret_cast<const Pack<T, V>*>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.e[i] = i < n ? p[i] : from_f<T>(0.f);
+  }
+  return r;
+}
+template <typename T, int V>
+__device__ __forceinline__ void st_pack(T* p, int n, bool vec, const Pack<T, V>& r) {
+  if (vec && n >= V) {
+    *reinterpret_cast<Pack<T, V>*>(p) = r;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) p[i] = r.e[i];
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void ld_f(const T* p, int n, bool vec, float (&v)[V]) {
+  const Pack<T, V> r = ld_pack<T, V>(p, n, vec);
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = to_f(r.e[i]);
+}
+template <typename T, int V>
+__device__ __forceinline__ void st_f(T* p, int n, bool vec, const float (&v)[V]) {
+  Pack<T, V> r;
+#pragma unroll
+  for (int i = 0; i < V; ++i) r.e[i] = from_f<T>(v[i]);
+  st_pack<T, V>(p, n, vec, r);
+}
+
+// v sigmoid(v) and its derivative; sigmoid = 1/(1 + e^-v) tends to 0 and 1 without
+// overflow trouble (e^-v = inf gives 0).
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + expf(-v)); }
+__device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
+__device__ __forceinline__ float silu_grad(float v) {
+  const float s = sigmoid(v);
+  return s * fmaf(v, 1.f - s, 1.f);
+}
+
+// The status block is optional in these calls (a null one records nothing).
+__device__ __forceinline__ void record_gen(St st) {
+  if (st.w) s4dev::st_record_gen(st);
+}
+
+// The state slot of sequence b (-1: none) and its real length.  A value out of range is
+// recorded in the status and read as no slot and length 0.
+struct Seq {
+  long long slot;
+  int len;
+};
+__device__ __forceinline__ Seq seq_of(const int* lengths, const int* index, int b, int L, int slots, St st) {
+  Seq q;
+  q.slot = index ? index[b] : b;
+  q.len = lengths ? lengths[b] : L;
+  const bool bad = q.len < 0 || q.len > L || (index && q.slot >= slots);
+  if (bad && st.w && threadIdx.x == 0) s4dev::st_flag(st, s4impl::ST_BAD_INDEX);
+  if (bad || q.slot < 0) {
+    q.slot = -1;
+    q.len = 0;
+  }
+  return q;
+}
+
+// Sums over the lanes of a warp, in every lane.
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// part[row][col] summed over the rows, columns in chunks of 32 per CTA, 8 row groups of
+// one warp each; put(col, sum).
+template <typename Put>
+__device__ __forceinline__ void column_sums(const float* part, int rows, long long cols, Put put) {
+  __shared__ float s[8][33];
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const long long c = (long long)blockIdx.x * 32 + lane;
+  float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+  if (c < cols) {
+    int r = wid;
+    for (; r + 24 < rows; r += 32) {
+      a0 += part[r * cols + c];
+      a1 += part[(r + 8) * cols + c];
+      a2 += part[(r + 16) * cols + c];
+      a3 += part[(r + 24) * cols + c];
+    }
+    for (; r < rows; r += 8) a0 += part[r * cols + c];
+  }
+  s[wid][lane] = (a0 + a1) + (a2 + a3);
+  __syncthreads();
+  if (wid == 0 && c < cols) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += s[i][lane];
+    put(c, t);
+  }
+}
+
+// ---- host side ----------------------------------------------------------------------
+// Whether an array's accesses of `bytes` bytes are aligned: its address and its strides
+// (in elements of `e` bytes).
+inline bool vec_ok(const void* p, int e, int bytes, long long s0 = 0, long long s1 = 0) {
+  return p == nullptr || ((uintptr_t)p % bytes == 0 && s0 * e % bytes == 0 && s1 * e % bytes == 0);
+}
+
+}  // namespace s4blk
