@@ -334,6 +334,35 @@ size_t s4_short_conv_bwd_workspace_bytes(int batch, int L, int H, int W);
 s4_status s4_short_conv_bwd(const s4_short_conv_bwd_args* a, void* stream);
 
 /*
+ * s4_selective_scan_fwd -- the state-space recurrence with a step size and input and
+ * output vectors of each token's own:  per sequence, channel h (of group g = h / (H/G))
+ * and state n,
+ *     d_t = softplus(dt_t + dt_bias)          (softplus = 0: d_t = dt_t + dt_bias)
+ *     s_t,n = exp(d_t A[h][n]) s_{t-1},n + d_t B_t[g][n] x_t
+ *     y_t = (sum_n C_t[g][n] s_t,n + D x_t) z_t sigmoid(z_t)      (no z: without the gate)
+ * L = 1 is the single-token form.  Stable for A <= 0 (not checked).
+ */
+typedef struct {
+    s4_rows x, dt, z;         /* [batch][L][H]; z.p may be NULL */
+    s4_rows B, C;             /* [batch][L][G][N]: group stride below */
+    s4_rows_out y;            /* [batch][L][H] */
+    const float* A;           /* [H][N] */
+    const float *D, *dt_bias; /* [H] or NULL */
+    const int *lengths, *index;
+    const float* state;       /* [slots][H][N] or NULL */
+    float* state_out;
+    void* ws;                 /* s4_selective_scan_workspace_bytes */
+    size_t ws_bytes;
+    long long B_group, C_group;
+    int batch, L, H, N, G, slots, dtype, softplus;
+} s4_selective_args;
+s4_status s4_selective_scan_fwd(const s4_selective_args* a, void* stream);
+
+/* Bytes of scratch of s4_selective_scan_fwd; 0 if the sizes are out of range.  Where it is
+ * 256 (the status block alone; always for L = 1) ws may be NULL. */
+size_t s4_selective_scan_workspace_bytes(int batch, int L, int H, int N, int G);
+
+/*
  * s4_block_norm_fwd -- what joins two blocks: the gate and norm after a block, its residual
  * scale, the residual sum, and the norm before the next block.  Per row of H channels,
  *     v = o silu(gate),  p = v rsqrt(mean v^2 + eps) w_post,

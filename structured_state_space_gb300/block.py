@@ -1,5 +1,5 @@
-"""The selective block's operators over the C ABI: the short causal convolution and the
-norms around a block, forward and backward.
+"""The selective block's operators over the C ABI: the short causal convolution, the selective
+scan and the norms around a block.
 
 Activations are [batch, L, channels] tensors (float32, bfloat16 or float16) whose channels are
 contiguous; any batch and row strides are taken as they are, so slices of a projection's
@@ -18,7 +18,8 @@ import torch
 
 from . import S4Error, load
 
-__all__ = ["s4_short_conv_fwd", "s4_short_conv_step", "s4_short_conv_bwd", "s4_block_norm_fwd", "s4_block_norm_bwd"]
+__all__ = ["s4_short_conv_fwd", "s4_short_conv_step", "s4_short_conv_bwd", "s4_selective_scan_fwd", "s4_selective_step",
+           "s4_block_norm_fwd", "s4_block_norm_bwd"]
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _F32, _I32 = torch.float32, torch.int32
@@ -28,6 +29,7 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 # The argument structs of include/s4.h, packed as C lays them out.
 _CONV = struct.Struct("@6q7PN7i0q")
 _CONV_BWD = struct.Struct("@9q9PN6i0q")
+_SCAN = struct.Struct("@18q8PN2q8i")
 _NORM = struct.Struct("@8P6qf3i0q")
 _NORM_BWD = struct.Struct("@15PN9qf3i0q")
 
@@ -38,11 +40,13 @@ def _lib():
     """The library's entry points by name, with their argument types set once."""
     lib = load()
     vp, i32, sz, ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
-    for name in ("s4_short_conv_fwd", "s4_short_conv_bwd", "s4_block_norm_fwd", "s4_block_norm_bwd"):
+    for name in ("s4_short_conv_fwd", "s4_short_conv_bwd", "s4_selective_scan_fwd", "s4_block_norm_fwd",
+                 "s4_block_norm_bwd"):
         f = getattr(lib, name)
         f.argtypes, f.restype = [ctypes.c_char_p, vp], i32
         _fn[name] = f
-    for name, args in (("s4_short_conv_bwd_workspace_bytes", [i32] * 4), ("s4_block_norm_bwd_workspace_bytes", [ll, i32])):
+    for name, args in (("s4_short_conv_bwd_workspace_bytes", [i32] * 4),
+                       ("s4_selective_scan_workspace_bytes", [i32] * 5), ("s4_block_norm_bwd_workspace_bytes", [ll, i32])):
         f = getattr(lib, name)
         f.argtypes, f.restype = args, sz
         _fn[name] = f
@@ -206,6 +210,76 @@ def s4_short_conv_bwd(x, w, bias, dy, *, silu=True, lengths=None, state=None, ds
                           ws.data_ptr(), ws.numel(), batch, L, H, W, code, 1 if silu else 0)
     _call("s4_short_conv_bwd", args, x)
     return out
+
+
+def _groups(t, dtype, shape, name):
+    """(address, batch, row and group strides) of [batch, L, G, N], or of one token's [batch, G, N]."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_cuda:
+        _bad(t, name, dtype, shape)
+    s = t.stride()
+    if s[-1] != 1 and shape[-1] != 1:
+        raise ValueError(f"{name}: its states must be contiguous")
+    return t.data_ptr(), s[0], s[-3], s[-2]
+
+
+def s4_selective_scan_fwd(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, softplus=True, lengths=None, state=None,
+                          state_out=None, index=None, y=None, ws=None, stream=None):
+    """The selective state-space scan: s = exp(d A) s + d x B, y = (C.s + D x) silu(z) with
+    d = softplus(dt + dt_bias), along L.
+
+    x, dt, z [batch, L, H]; A [H, N]; B, C [batch, L, G, N] (channels in G equal groups);
+    D, dt_bias [H].  lengths, index as for s4_short_conv_fwd; state, state_out [slots, H, N]
+    float32.  ws: s4_selective_scan_workspace_bytes (allocated per call when None)."""
+    if stream is not None:
+        return _on(stream, s4_selective_scan_fwd, x, dt, A, B, C, D=D, z=z, dt_bias=dt_bias, softplus=softplus,
+                   lengths=lengths, state=state, state_out=state_out, index=index, y=y, ws=ws)
+    code, ty, shape = _code(x), x.dtype, x.shape
+    batch, L, H = shape
+    G, N = B.shape[2:]
+    if y is None:
+        y = _empty(shape, dtype=ty, device=x.device)
+    slots = _slots(state, state_out, batch, index)
+    if ws is None:
+        need = _bytes("s4_selective_scan_workspace_bytes", batch, L, H, N, G)
+        ws = _ws(None, need, x) if need > 256 else None
+    bp, bb, br, bg = _groups(B, ty, (batch, L, G, N), "B")
+    cp, cb, cr, cg = _groups(C, ty, (batch, L, G, N), "C")
+    args = _SCAN.pack(*_rows(x, ty, shape, "x"), *_rows(dt, ty, shape, "dt"), *_rows(z, ty, shape, "z"),
+                      bp, bb, br, cp, cb, cr, *_rows(y, ty, shape, "y"), _dense(A, _F32, (H, N), "A"),
+                      _dense(D, _F32, (H,), "D"), _dense(dt_bias, _F32, (H,), "dt_bias"),
+                      _dense(lengths, _I32, (batch,), "lengths"), _dense(index, _I32, (batch,), "index"),
+                      _dense(state, _F32, (slots, H, N), "state"), _dense(state_out, _F32, (slots, H, N), "state_out"),
+                      0 if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), bg, cg,
+                      batch, L, H, N, G, slots, code, 1 if softplus else 0)
+    _call("s4_selective_scan_fwd", args, x)
+    return y
+
+
+def s4_selective_step(x, dt, A, B, C, state, *, D=None, z=None, dt_bias=None, softplus=True, state_out=None, index=None,
+                      y=None, ws=None, stream=None):
+    """One token per sequence: x, dt, z [batch, H], B, C [batch, G, N] -> y [batch, H].  The state is
+    updated in place, or written to state_out."""
+    if stream is not None:
+        return _on(stream, s4_selective_step, x, dt, A, B, C, state, D=D, z=z, dt_bias=dt_bias, softplus=softplus,
+                   state_out=state_out, index=index, y=y, ws=ws)
+    code, ty, shape = _code(x), x.dtype, x.shape
+    batch, H = shape
+    G, N = B.shape[1:]
+    if y is None:
+        y = _empty(shape, dtype=ty, device=x.device)
+    slots = _slots(state, state, batch, index)
+    old = _dense(state, _F32, (slots, H, N), "state")
+    bp, bb, br, bg = _groups(B, ty, (batch, G, N), "B")
+    cp, cb, cr, cg = _groups(C, ty, (batch, G, N), "C")
+    args = _SCAN.pack(*_tokens(x, ty, shape, "x"), *_tokens(dt, ty, shape, "dt"), *_tokens(z, ty, shape, "z"),
+                      bp, bb, br, cp, cb, cr, *_tokens(y, ty, shape, "y"), _dense(A, _F32, (H, N), "A"),
+                      _dense(D, _F32, (H,), "D"), _dense(dt_bias, _F32, (H,), "dt_bias"), 0,
+                      _dense(index, _I32, (batch,), "index"), old,
+                      old if state_out is None else _dense(state_out, _F32, (slots, H, N), "state_out"),
+                      0 if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), bg, cg,
+                      batch, 1, H, N, G, slots, code, 1 if softplus else 0)
+    _call("s4_selective_scan_fwd", args, x)
+    return y
 
 
 def _flat(t, dtype, shape, name):

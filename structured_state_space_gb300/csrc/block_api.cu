@@ -22,6 +22,9 @@ template <typename Rows>
 bool rows_ok(const Rows& r, int dtype) {
   return r.p && aligned(r.p, s4impl::dtype_bytes(dtype)) && r.batch >= 0 && r.row >= 0;
 }
+bool scan_sizes_ok(int batch, int L, int H, int N, int G) {
+  return sizes_ok(batch, L, H) && N >= 1 && N <= 256 && G >= 1 && G <= H && H % G == 0;
+}
 s4_status ws_ok(const void* ws, size_t bytes, size_t need) {
   return ws != nullptr && aligned(ws, 256) && bytes >= need ? S4_OK : S4_ERR_WORKSPACE;
 }
@@ -71,6 +74,31 @@ s4_status s4_short_conv_bwd(const s4_short_conv_bwd_args* a, void* stream) {
   bool chain;
   if (!s4impl::call_status(a->ws, s, &st, &chain)) return S4_ERR_CUDA;
   return cuda_status(s4impl::launch_short_conv_bwd(*a, st, s));
+}
+
+size_t s4_selective_scan_workspace_bytes(int batch, int L, int H, int N, int G) {
+  if (!scan_sizes_ok(batch, L, H, N, G)) return 0;
+  return s4impl::kStatusBytes + s4impl::align256(s4impl::selective_scratch(batch, L, H, N, G));
+}
+
+s4_status s4_selective_scan_fwd(const s4_selective_args* a, void* stream) {
+  if (!a || !s4impl::dtype_ok(a->dtype) || !scan_sizes_ok(a->batch, a->L, a->H, a->N, a->G)) return S4_ERR_INVALID_ARG;
+  if (!rows_ok(a->x, a->dtype) || !rows_ok(a->dt, a->dtype) || (a->z.p && !rows_ok(a->z, a->dtype)) ||
+      !rows_ok(a->B, a->dtype) || !rows_ok(a->C, a->dtype) || !rows_ok(a->y, a->dtype) || a->B_group < 0 ||
+      a->C_group < 0 || !a->A || !aligned(a->A, 4) || !aligned(a->D, 4) || !aligned(a->dt_bias, 4) ||
+      !aligned(a->lengths, 4) || !aligned(a->index, 4) || !aligned(a->state, 4) || !aligned(a->state_out, 4))
+    return S4_ERR_INVALID_ARG;
+  if ((a->state || a->state_out) && (a->slots < 1 || (!a->index && a->slots < a->batch))) return S4_ERR_INVALID_ARG;
+  const size_t need = s4_selective_scan_workspace_bytes(a->batch, a->L, a->H, a->N, a->G);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  s4impl::St st{nullptr, 0u};
+  if (a->ws || need > s4impl::kStatusBytes) {
+    const s4_status w = ws_ok(a->ws, a->ws_bytes, need);
+    if (w != S4_OK) return w;
+    bool chain;
+    if (!s4impl::call_status(a->ws, s, &st, &chain)) return S4_ERR_CUDA;
+  }
+  return cuda_status(s4impl::launch_selective_scan(*a, st, s));
 }
 
 s4_status s4_block_norm_fwd(const s4_block_norm_args* a, void* stream) {

@@ -92,7 +92,7 @@ __device__ __forceinline__ Seq seq_of(const int* lengths, const int* index, int 
   Seq q;
   q.slot = index ? index[b] : b;
   q.len = lengths ? lengths[b] : L;
-  const bool bad = q.len < 0 || q.len > L || (index && q.slot >= slots);
+  const bool bad = q.len < 0 || q.len > L || (index && slots > 0 && q.slot >= slots);
   if (bad && st.w && threadIdx.x == 0) s4dev::st_flag(st, s4impl::ST_BAD_INDEX);
   if (bad || q.slot < 0) {
     q.slot = -1;

@@ -28,12 +28,15 @@ inline size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
 cudaError_t launch_short_conv(const s4_short_conv_args& a, St st, cudaStream_t s);
 size_t short_conv_bwd_scratch(int batch, int L, int H, int W);
 cudaError_t launch_short_conv_bwd(const s4_short_conv_bwd_args& a, St st, cudaStream_t s);
+size_t selective_scratch(int batch, int L, int H, int N, int G);
+cudaError_t launch_selective_scan(const s4_selective_args& a, St st, cudaStream_t s);
 cudaError_t launch_block_norm(const s4_block_norm_args& a, cudaStream_t s);
 size_t block_norm_bwd_scratch(long long rows, int H);
 cudaError_t launch_block_norm_bwd(const s4_block_norm_bwd_args& a, cudaStream_t s);
 
 #ifdef S4_BOUNDS_CHECK
 unsigned long long oob_short_conv();
+unsigned long long oob_selective();
 unsigned long long oob_block_norm();
 #endif
 

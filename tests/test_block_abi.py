@@ -13,7 +13,7 @@ from structured_state_space_gb300 import build as s4build
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 STRUCTS = {"s4_short_conv_args": block._CONV, "s4_short_conv_bwd_args": block._CONV_BWD,
-           "s4_block_norm_args": block._NORM, "s4_block_norm_bwd_args": block._NORM_BWD}
+           "s4_selective_args": block._SCAN, "s4_block_norm_args": block._NORM, "s4_block_norm_bwd_args": block._NORM_BWD}
 A = 0x10000  # an aligned stand-in address; validation rejects before any use
 
 
@@ -53,6 +53,24 @@ def conv(**kw):
     ({"state": A + 1}, 1), ({"index": A + 2}, 1), ({"nws": 255}, 2), ({"ws": A + 64}, 2)])
 def test_short_conv_refuses(lib, kw, code):
     assert call(lib, "s4_short_conv_fwd", block._CONV, *conv(**kw)) == code
+
+
+def scan(**kw):
+    v = dict(x=(A, 8, 8), dt=(A, 8, 8), z=(0, 0, 0), B=(A, 8, 8), C=(A, 8, 8), y=(A, 8, 8), A=A, D=A, bias=A, lengths=0,
+             index=0, state=A, out=A, ws=A, nws=256, bg=4, cg=4, batch=1, L=1, H=8, N=4, G=1, slots=1, dtype=1,
+             softplus=1) | kw
+    return (*v["x"], *v["dt"], *v["z"], *v["B"], *v["C"], *v["y"], *(v[k] for k in (
+        "A", "D", "bias", "lengths", "index", "state", "out", "ws", "nws", "bg", "cg", "batch", "L", "H", "N", "G", "slots",
+        "dtype", "softplus")))
+
+
+@pytest.mark.parametrize("kw,code", [
+    ({"x": (0, 8, 8)}, 1), ({"dt": (A + 1, 8, 8)}, 1), ({"z": (A + 1, 8, 8)}, 1), ({"B": (0, 8, 8)}, 1), ({"C": (A, 8, -1)}, 1),
+    ({"y": (0, 8, 8)}, 1), ({"A": 0}, 1), ({"D": A + 1}, 1), ({"state": A + 2}, 1), ({"N": 0}, 1), ({"N": 257}, 1), ({"G": 0}, 1),
+    ({"G": 3}, 1), ({"batch": 2}, 1), ({"slots": 0}, 1), ({"dtype": -1}, 1), ({"bg": -1}, 1), ({"nws": 100}, 2),
+    ({"ws": A + 8}, 2), ({"L": 100000, "ws": 0}, 2), ({"L": 100000, "nws": 256}, 2)])
+def test_selective_scan_refuses(lib, kw, code):
+    assert call(lib, "s4_selective_scan_fwd", block._SCAN, *scan(**kw)) == code
 
 
 def test_null_structs_and_workspace_sizes(lib):
