@@ -363,6 +363,35 @@ s4_status s4_selective_scan_fwd(const s4_selective_args* a, void* stream);
 size_t s4_selective_scan_workspace_bytes(int batch, int L, int H, int N, int G);
 
 /*
+ * s4_selective_scan_bwd -- gradients of s4_selective_scan_fwd with respect to all its
+ * inputs, from dy (the gradient of y).  With dyp = dy silu(z), a_t = exp(d_t A) and the
+ * states computed again from the inputs (nothing is kept from the forward call),
+ *     g_t = C_t dyp_t + a_{t+1} g_{t+1}
+ *     dC_t = sum_h dyp_t s_t,   dB_t = sum_h d_t x_t g_t          (over a group's channels)
+ *     q_t = a_t s_{t-1} g_t,    dA = sum_{b,t} d_t q_t,  u_t = sum_n B_t g_t
+ *     dx_t = d_t u_t + D dyp_t, ddt_t = (x_t u_t + sum_n A q_t) softplus'(.)
+ *     dD = sum_{b,t} dyp_t x_t, ddt_bias = sum_{b,t} ddt_t,  dz_t = dy_t ypre_t silu'(z_t).
+ * state0, dstate, dstate0 [batch][H][N] fp32 as for s4_short_conv_bwd.
+ */
+typedef struct {
+    s4_rows x, dt, z, B, C, dy;
+    s4_rows_out dx, ddt, dz;  /* dz.p NULL where z.p is */
+    void *dB, *dC;            /* [batch][L][G][N], dense, of the activations' type */
+    const float *A, *D, *dt_bias;
+    const int* lengths;
+    const float *state0, *dstate;
+    float* dstate0;           /* not the array dstate */
+    float* dA;                /* [H][N] */
+    float *dD, *ddt_bias;     /* [H], NULL where D, dt_bias are */
+    void* ws;                 /* s4_selective_scan_bwd_workspace_bytes */
+    size_t ws_bytes;
+    long long B_group, C_group;
+    int batch, L, H, N, G, dtype, softplus;
+} s4_selective_bwd_args;
+size_t s4_selective_scan_bwd_workspace_bytes(int batch, int L, int H, int N, int G);
+s4_status s4_selective_scan_bwd(const s4_selective_bwd_args* a, void* stream);
+
+/*
  * s4_block_norm_fwd -- what joins two blocks: the gate and norm after a block, its residual
  * scale, the residual sum, and the norm before the next block.  Per row of H channels,
  *     v = o silu(gate),  p = v rsqrt(mean v^2 + eps) w_post,

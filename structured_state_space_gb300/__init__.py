@@ -17,7 +17,7 @@ Entry points (same names as the C ABI):
     s4_get_status(ws), s4_status_str(code)
 and the selective block's operators (block.py, imported on first use):
     s4_short_conv_fwd / _step / _bwd                   short causal convolution with SiLU
-    s4_selective_scan_fwd, s4_selective_step           selective state-space scan, prompts and single tokens
+    s4_selective_scan_fwd / _bwd, s4_selective_step    selective state-space scan, prompts and single tokens
     s4_block_norm_fwd / _bwd                           norms around a block, gate, residual scale and sum
 """
 from __future__ import annotations
@@ -47,6 +47,7 @@ ABI_FUNCTIONS = [
     "s4_hippo_dplr", "s4_fp32_probe", "s4_set_wait_limit", "s4_bounds_violations",
     "s4_short_conv_fwd", "s4_short_conv_bwd", "s4_short_conv_bwd_workspace_bytes",
     "s4_selective_scan_fwd", "s4_selective_scan_workspace_bytes",
+    "s4_selective_scan_bwd", "s4_selective_scan_bwd_workspace_bytes",
     "s4_block_norm_fwd", "s4_block_norm_bwd", "s4_block_norm_bwd_workspace_bytes",
 ]
 
@@ -62,7 +63,7 @@ class S4Error(RuntimeError):
 
 # The selective block's operators, defined in block.py (which needs torch, loaded on first use).
 _BLOCK = ["s4_short_conv_fwd", "s4_short_conv_step", "s4_short_conv_bwd", "s4_selective_scan_fwd", "s4_selective_step",
-          "s4_block_norm_fwd", "s4_block_norm_bwd"]
+          "s4_selective_scan_bwd", "s4_block_norm_fwd", "s4_block_norm_bwd"]
 __all__ += _BLOCK
 
 

@@ -1,5 +1,5 @@
 """The selective block's operators over the C ABI: the short causal convolution, the selective
-scan and the norms around a block.
+scan and the norms around a block, each with its backward pass.
 
 Activations are [batch, L, channels] tensors (float32, bfloat16 or float16) whose channels are
 contiguous; any batch and row strides are taken as they are, so slices of a projection's
@@ -19,7 +19,7 @@ import torch
 from . import S4Error, load
 
 __all__ = ["s4_short_conv_fwd", "s4_short_conv_step", "s4_short_conv_bwd", "s4_selective_scan_fwd", "s4_selective_step",
-           "s4_block_norm_fwd", "s4_block_norm_bwd"]
+           "s4_selective_scan_bwd", "s4_block_norm_fwd", "s4_block_norm_bwd"]
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _F32, _I32 = torch.float32, torch.int32
@@ -30,6 +30,7 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _CONV = struct.Struct("@6q7PN7i0q")
 _CONV_BWD = struct.Struct("@9q9PN6i0q")
 _SCAN = struct.Struct("@18q8PN2q8i")
+_SCAN_BWD = struct.Struct("@27q13PN2q7i0q")
 _NORM = struct.Struct("@8P6qf3i0q")
 _NORM_BWD = struct.Struct("@15PN9qf3i0q")
 
@@ -40,13 +41,14 @@ def _lib():
     """The library's entry points by name, with their argument types set once."""
     lib = load()
     vp, i32, sz, ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
-    for name in ("s4_short_conv_fwd", "s4_short_conv_bwd", "s4_selective_scan_fwd", "s4_block_norm_fwd",
-                 "s4_block_norm_bwd"):
+    for name in ("s4_short_conv_fwd", "s4_short_conv_bwd", "s4_selective_scan_fwd", "s4_selective_scan_bwd",
+                 "s4_block_norm_fwd", "s4_block_norm_bwd"):
         f = getattr(lib, name)
         f.argtypes, f.restype = [ctypes.c_char_p, vp], i32
         _fn[name] = f
     for name, args in (("s4_short_conv_bwd_workspace_bytes", [i32] * 4),
-                       ("s4_selective_scan_workspace_bytes", [i32] * 5), ("s4_block_norm_bwd_workspace_bytes", [ll, i32])):
+                       ("s4_selective_scan_workspace_bytes", [i32] * 5),
+                       ("s4_selective_scan_bwd_workspace_bytes", [i32] * 5), ("s4_block_norm_bwd_workspace_bytes", [ll, i32])):
         f = getattr(lib, name)
         f.argtypes, f.restype = args, sz
         _fn[name] = f
@@ -280,6 +282,48 @@ def s4_selective_step(x, dt, A, B, C, state, *, D=None, z=None, dt_bias=None, so
                       batch, 1, H, N, G, slots, code, 1 if softplus else 0)
     _call("s4_selective_scan_fwd", args, x)
     return y
+
+
+def s4_selective_scan_bwd(x, dt, A, B, C, dy, *, D=None, z=None, dt_bias=None, softplus=True, lengths=None, state=None,
+                          dstate=None, want_dstate0=False, ws=None, stream=None):
+    """Gradients of s4_selective_scan_fwd from dy: a dict of dx, ddt, dA, dB, dC and, for what was given, dD, dz,
+    ddt_bias; dstate0, the gradient of the state on entry, where asked for.  state, dstate [batch, H, N]: the
+    state on entry and the gradient of the state on return (None: zeros).  Nothing is kept from the
+    forward call: its states are formed again.  ws: s4_selective_scan_bwd_workspace_bytes."""
+    if stream is not None:
+        return _on(stream, s4_selective_scan_bwd, x, dt, A, B, C, dy, D=D, z=z, dt_bias=dt_bias, softplus=softplus,
+                   lengths=lengths, state=state, dstate=dstate, want_dstate0=want_dstate0, ws=ws)
+    code, ty, shape, dev = _code(x), x.dtype, x.shape, x.device
+    batch, L, H = shape
+    vec = B.shape
+    G, N = vec[2:]
+    ws = _ws(ws, _bytes("s4_selective_scan_bwd_workspace_bytes", batch, L, H, N, G), x)
+    out = {"dx": _empty(shape, dtype=ty, device=dev), "ddt": _empty(shape, dtype=ty, device=dev),
+           "dA": _empty((H, N), dtype=_F32, device=dev), "dB": _empty(vec, dtype=ty, device=dev),
+           "dC": _empty(vec, dtype=ty, device=dev)}
+    if D is not None:
+        out["dD"] = _empty((H,), dtype=_F32, device=dev)
+    if z is not None:
+        out["dz"] = _empty(shape, dtype=ty, device=dev)
+    if dt_bias is not None:
+        out["ddt_bias"] = _empty((H,), dtype=_F32, device=dev)
+    if want_dstate0:
+        out["dstate0"] = _empty((batch, H, N), dtype=_F32, device=dev)
+    get = out.get
+    bp, bb, br, bg = _groups(B, ty, (batch, L, G, N), "B")
+    cp, cb, cr, cg = _groups(C, ty, (batch, L, G, N), "C")
+    past = (batch, H, N)
+    args = _SCAN_BWD.pack(
+        *_rows(x, ty, shape, "x"), *_rows(dt, ty, shape, "dt"), *_rows(z, ty, shape, "z"), bp, bb, br, cp, cb, cr,
+        *_rows(dy, ty, shape, "dy"), *_rows(out["dx"], ty, shape, "dx"), *_rows(out["ddt"], ty, shape, "ddt"),
+        *_rows(get("dz"), ty, shape, "dz"), out["dB"].data_ptr(), out["dC"].data_ptr(), _dense(A, _F32, (H, N), "A"),
+        _dense(D, _F32, (H,), "D"), _dense(dt_bias, _F32, (H,), "dt_bias"), _dense(lengths, _I32, (batch,), "lengths"),
+        _dense(state, _F32, past, "state"), _dense(dstate, _F32, past, "dstate"),
+        _dense(get("dstate0"), _F32, past, "dstate0"), out["dA"].data_ptr(), _dense(get("dD"), _F32, (H,), "dD"),
+        _dense(get("ddt_bias"), _F32, (H,), "ddt_bias"), ws.data_ptr(), ws.numel(), bg, cg,
+        batch, L, H, N, G, code, 1 if softplus else 0)
+    _call("s4_selective_scan_bwd", args, x)
+    return out
 
 
 def _flat(t, dtype, shape, name):

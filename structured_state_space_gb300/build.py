@@ -20,7 +20,8 @@ LIBDIR = os.path.join(PKG, "lib")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(LIBDIR, "libs4.so")
 SOURCES = ["s4_api.cu", "cauchy.cu", "fft_rows.cu", "fft_cluster.cu", "fft_fourstep.cu", "s4_noalloc.cu", "recurrent.cu", "bordered.cu",
-           "hippo.cpp", "block_api.cu", "short_conv.cu", "selective_scan.cu", "block_norm.cu"]
+           "hippo.cpp", "block_api.cu", "short_conv.cu", "selective_scan.cu",
+           "selective_scan_bwd.cu", "block_norm.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 GENDIR = os.path.join(OBJDIR, "gen")

@@ -101,6 +101,35 @@ s4_status s4_selective_scan_fwd(const s4_selective_args* a, void* stream) {
   return cuda_status(s4impl::launch_selective_scan(*a, st, s));
 }
 
+size_t s4_selective_scan_bwd_workspace_bytes(int batch, int L, int H, int N, int G) {
+  if (!scan_sizes_ok(batch, L, H, N, G)) return 0;
+  return s4impl::selective_bwd_bytes(batch, L, H, N, G);
+}
+
+s4_status s4_selective_scan_bwd(const s4_selective_bwd_args* a, void* stream) {
+  if (!a || !s4impl::dtype_ok(a->dtype) || !scan_sizes_ok(a->batch, a->L, a->H, a->N, a->G)) return S4_ERR_INVALID_ARG;
+  const int e = s4impl::dtype_bytes(a->dtype);
+  if (!rows_ok(a->x, a->dtype) || !rows_ok(a->dt, a->dtype) || (a->z.p && !rows_ok(a->z, a->dtype)) ||
+      !rows_ok(a->B, a->dtype) || !rows_ok(a->C, a->dtype) || !rows_ok(a->dy, a->dtype) || !rows_ok(a->dx, a->dtype) ||
+      !rows_ok(a->ddt, a->dtype) || (a->z.p && !rows_ok(a->dz, a->dtype)) || (!a->z.p && a->dz.p) || a->B_group < 0 ||
+      a->C_group < 0)
+    return S4_ERR_INVALID_ARG;
+  if (!a->dB || !a->dC || !a->A || !a->dA || !a->D != !a->dD || !a->dt_bias != !a->ddt_bias || !aligned(a->dB, e) ||
+      !aligned(a->dC, e) || !aligned(a->A, 4) || !aligned(a->dA, 4) || !aligned(a->D, 4) || !aligned(a->dD, 4) ||
+      !aligned(a->dt_bias, 4) || !aligned(a->ddt_bias, 4) || !aligned(a->lengths, 4) || !aligned(a->state0, 4) ||
+      !aligned(a->dstate, 4) || !aligned(a->dstate0, 4) || (a->dstate0 && a->dstate0 == a->dstate))
+    return S4_ERR_INVALID_ARG;
+  const size_t need = s4_selective_scan_bwd_workspace_bytes(a->batch, a->L, a->H, a->N, a->G);
+  if (need == 0) return S4_ERR_INVALID_ARG;
+  const s4_status w = ws_ok(a->ws, a->ws_bytes, need);
+  if (w != S4_OK) return w;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  s4impl::St st;
+  bool chain;
+  if (!s4impl::call_status(a->ws, s, &st, &chain)) return S4_ERR_CUDA;
+  return cuda_status(s4impl::launch_selective_bwd(*a, st, s));
+}
+
 s4_status s4_block_norm_fwd(const s4_block_norm_args* a, void* stream) {
   if (!a || !s4impl::dtype_ok(a->dtype) || a->rows < 1 || a->rows > INT_MAX || a->H < 1 || a->H > kMaxNormChannels ||
       !(a->eps >= 0.f))

@@ -279,7 +279,8 @@ long long s4_bounds_violations(void) {
   if (cudaDeviceSynchronize() != cudaSuccess) return -2;
   const unsigned long long c[] = {s4impl::oob_rows(), s4impl::oob_cluster(), s4impl::oob_fourstep(),
                                   s4impl::oob_cauchy(), s4impl::oob_recurrent(), s4impl::oob_bordered(),
-                                  s4impl::oob_short_conv(), s4impl::oob_selective(), s4impl::oob_block_norm()};
+                                  s4impl::oob_short_conv(), s4impl::oob_selective(), s4impl::oob_selective_bwd(),
+                                  s4impl::oob_block_norm()};
   unsigned long long t = 0;
   for (unsigned long long v : c) {
     if (v == ~0ull) return -2;

@@ -30,6 +30,8 @@ size_t short_conv_bwd_scratch(int batch, int L, int H, int W);
 cudaError_t launch_short_conv_bwd(const s4_short_conv_bwd_args& a, St st, cudaStream_t s);
 size_t selective_scratch(int batch, int L, int H, int N, int G);
 cudaError_t launch_selective_scan(const s4_selective_args& a, St st, cudaStream_t s);
+size_t selective_bwd_bytes(int batch, int L, int H, int N, int G);
+cudaError_t launch_selective_bwd(const s4_selective_bwd_args& a, St st, cudaStream_t s);
 cudaError_t launch_block_norm(const s4_block_norm_args& a, cudaStream_t s);
 size_t block_norm_bwd_scratch(long long rows, int H);
 cudaError_t launch_block_norm_bwd(const s4_block_norm_bwd_args& a, cudaStream_t s);
@@ -37,6 +39,7 @@ cudaError_t launch_block_norm_bwd(const s4_block_norm_bwd_args& a, cudaStream_t 
 #ifdef S4_BOUNDS_CHECK
 unsigned long long oob_short_conv();
 unsigned long long oob_selective();
+unsigned long long oob_selective_bwd();
 unsigned long long oob_block_norm();
 #endif
 

@@ -13,7 +13,8 @@ from structured_state_space_gb300 import build as s4build
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 STRUCTS = {"s4_short_conv_args": block._CONV, "s4_short_conv_bwd_args": block._CONV_BWD,
-           "s4_selective_args": block._SCAN, "s4_block_norm_args": block._NORM, "s4_block_norm_bwd_args": block._NORM_BWD}
+           "s4_selective_args": block._SCAN, "s4_selective_bwd_args": block._SCAN_BWD,
+           "s4_block_norm_args": block._NORM, "s4_block_norm_bwd_args": block._NORM_BWD}
 A = 0x10000  # an aligned stand-in address; validation rejects before any use
 
 
@@ -71,6 +72,17 @@ def scan(**kw):
     ({"ws": A + 8}, 2), ({"L": 100000, "ws": 0}, 2), ({"L": 100000, "nws": 256}, 2)])
 def test_selective_scan_refuses(lib, kw, code):
     assert call(lib, "s4_selective_scan_fwd", block._SCAN, *scan(**kw)) == code
+
+
+def test_selective_scan_bwd_refuses(lib):
+    # nine strided arrays; dB, dC, A, D, dt_bias, lengths, state0, dstate, dstate0, dA, dD, ddt_bias, ws
+    ok = [A, 8, 8] * 9 + [A] * 8 + [A + 256] + [A] * 4 + [256, 4, 4, 1, 1, 8, 4, 1, 1, 1]
+    assert call(lib, "s4_selective_scan_bwd", block._SCAN_BWD, *ok) == 2  # workspace too small
+    # x, dz without z, z without dz, dB, D without dD, dstate0 = dstate, dA, batch, N, G, a stride
+    for at, bad in [(0, 0), (6, 0), (24, 0), (27, 0), (37, 0), (35, A), (36, 0), (43, 0), (46, 257), (47, 3), (1, -1)]:
+        v = list(ok)
+        v[at] = bad
+        assert call(lib, "s4_selective_scan_bwd", block._SCAN_BWD, *v) == 1, (at, bad)
 
 
 def test_null_structs_and_workspace_sizes(lib):

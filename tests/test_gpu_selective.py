@@ -223,6 +223,115 @@ def test_other_stream_graph_and_determinism():
     assert torch.equal(y3, s4.s4_selective_scan_fwd(*pos, **named)) and s4.s4_get_status(ws) == 0
 
 
+# Gradients: as the state, and dA, ddt sum products of two of them over up to 10^3 remembered steps; the
+# sums over channels and tokens have up to 10^4 terms of either sign: 4e-5.
+GRAD_TOL = 4e-5
+
+
+def check_gradients(a, dy, tol=GRAD_TOL, **kw):
+    pos, named = split(a)
+    t = {k: (lens(v) if k == "lengths" else v) for k, v in kw.items()}
+    g = s4.s4_selective_scan_bwd(*pos, dy, **named, **t)
+    pos, named = split({k: to64(v) for k, v in a.items()})
+    r = {k: (to64(v) if torch.is_tensor(v) else v) for k, v in kw.items() if k != "want_dstate0"}
+    ref = O.selective_scan_grad(*pos, to64(dy), **named, **r)
+    for k in g:
+        close(g[k], ref[k], k, tol if g[k].dtype == torch.float32 else None)
+    return g
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("batch,L,H,N,G", SIZES)
+def test_gradients(dtype, batch, L, H, N, G):
+    dt = DTYPES[dtype]
+    a, r = scan_inputs(L * N + H + 1, batch, L, H, N, G, dt)
+    dy = r.normal(batch, L, H, dtype=dt)
+    g = check_gradients(a, dy, state=r.normal(batch, H, N), dstate=r.normal(batch, H, N), want_dstate0=True)
+    assert set(g) == {"dx", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dstate0"}
+
+
+@pytest.mark.parametrize("parts", [(), ("D",), ("z",), ("dt_bias",)])
+@pytest.mark.parametrize("soft", [True, False])
+def test_gradients_with_absent_parts(parts, soft):
+    a, r = scan_inputs(8, 2, 45, 36, 16, 1, torch.float32)
+    for k in ("D", "z", "dt_bias"):
+        if k not in parts:
+            del a[k]
+    a["dt"] = a["dt"].abs() * 0.1
+    if "dt_bias" in a:
+        a["dt_bias"] = a["dt_bias"].abs() * 0.1
+    pos, named = split(a)
+    dy = r.normal(2, 45, 36)
+    g = s4.s4_selective_scan_bwd(*pos, dy, **named, softplus=soft)
+    pos, named = split({k: to64(v) for k, v in a.items()})
+    ref = O.selective_scan_grad(*pos, to64(dy), **named, soft=soft)
+    for k in g:
+        close(g[k], ref[k], k, GRAD_TOL)
+    assert set(g) == {"dx", "ddt", "dA", "dB", "dC"} | {{"z": "dz", "D": "dD", "dt_bias": "ddt_bias"}[k] for k in parts}
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("L,H,N,G", [(75, 48, 16, 1), (75, 36, 16, 2), (40, 20, 64, 2), (500, 32, 16, 1)])
+def test_ragged_gradients_and_strides(dtype, L, H, N, G):
+    n = [L, 0, 1, L // 2, 20, L - 1]
+    a, r = scan_inputs(L + H + N + 1, 6, L, H, N, G, DTYPES[dtype], wide=True)
+    dy = r.wide(6, L, H, dtype=DTYPES[dtype], left=8, right=0)
+    for b in range(6):
+        for k in ("x", "dt", "z", "B", "C"):
+            a[k][b, n[b]:] = 0
+        dy[b, n[b]:] = 0
+    kw = dict(lengths=n, state=r.normal(6, H, N), dstate=r.normal(6, H, N), want_dstate0=True)
+    g = check_gradients(a, dy, **kw)
+    for b in range(6):  # padding holds what may not be used
+        for k in ("x", "dt", "z", "B", "C"):
+            a[k][b, n[b]:] = float("nan") if b % 2 else float("inf")
+        dy[b, n[b]:] = float("nan")
+    pos, named = split(a)
+    again = s4.s4_selective_scan_bwd(*pos, dy, **named, **{**kw, "lengths": lens(n)})
+    for k in g:
+        assert torch.equal(g[k], again[k]), k
+        if k in ("dx", "ddt", "dz", "dB", "dC"):
+            assert all((again[k][b, n[b]:] == 0).all() for b in range(6)), k
+
+
+def test_gradients_over_segments():
+    # few channels and many tokens: the first kernel runs in several segments, joined by the second
+    a, r = scan_inputs(21, 1, 3001, 24, 16, 1, torch.float32)
+    check_gradients(a, r.normal(1, 3001, 24), state=r.normal(1, 24, 16), dstate=r.normal(1, 24, 16), want_dstate0=True)
+
+
+def test_gradient_against_differences_of_the_forward_definition():
+    # float64 central differences along random directions (error ~1e-9); float32 gradients are off by ~1e-5 at most
+    a, r = scan_inputs(22, 2, 30, 12, 16, 2, torch.float32)
+    dy = r.normal(2, 30, 12)
+    pos, named = split(a)
+    g = s4.s4_selective_scan_bwd(*pos, dy, **named)
+    for k in a:
+        v = r.rng.standard_normal(a[k].shape)
+        val = []
+        for sign in (1, -1):
+            p = {n: to64(t) for n, t in a.items()}
+            p[k] = p[k] + sign * 1e-5 * v
+            pos, named = split(p)
+            val.append((O.selective_scan(*pos, **named)[0] * to64(dy)).sum())
+        gk = to64(g["d" + k])
+        assert abs((val[0] - val[1]) / 2e-5 - (gk * v).sum()) <= 1e-4 * np.linalg.norm(gk) * np.linalg.norm(v), k
+
+
+def test_gradients_on_another_stream_and_deterministic():
+    a, r = scan_inputs(23, 2, 300, 96, 16, 1, torch.bfloat16)
+    dy = r.normal(2, 300, 96, dtype=torch.bfloat16)
+    pos, named = split(a)
+    g = s4.s4_selective_scan_bwd(*pos, dy, **named)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g2 = s4.s4_selective_scan_bwd(*pos, dy, **named, stream=side)
+    side.synchronize()
+    assert all(torch.equal(g[k], g2[k]) for k in g)
+    with pytest.raises(s4.S4Error):
+        s4.s4_selective_scan_bwd(*pos, dy, **named, ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
 def test_refusals():
     a, r = scan_inputs(15, 2, 8, 16, 16, 2, torch.float32)
     pos, named = split(a)
