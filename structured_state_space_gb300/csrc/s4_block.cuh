@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "s4_block.h"
 #include "s4_dev.cuh"
 
@@ -25,52 +27,116 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return
 template <>
 __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
 
-// V elements of T as they lie in memory; accessed whole where aligned.
+// V elements of T as they lie in memory, in words of 32 bits (16 where a pack is one 16-bit
+// element): a load can then be waited for where its values are used, which packs of separate
+// 16-bit values, taken apart where the load's branches meet, do not allow.
+template <typename T>
+__device__ __forceinline__ unsigned bits_of(T v) {
+  if constexpr (sizeof(T) == 4)
+    return __float_as_uint(v);
+  else
+    return *reinterpret_cast<const unsigned short*>(&v);
+}
 template <typename T, int V>
-struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Pack {
-  T e[V];
+struct Pack {
+  static constexpr int BYTES = (int)sizeof(T) * V;
+  using W = std::conditional_t<BYTES % 4 == 0, unsigned, unsigned short>;
+  static constexpr int NW = BYTES / (int)sizeof(W), PER = (int)(sizeof(W) / sizeof(T));
+  alignas(BYTES < 16 ? BYTES : 16) W w[NW];
+
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (std::is_same_v<T, float>) {
+      return __uint_as_float(w[i]);
+    } else {
+      const unsigned v = w[i / PER] >> (16 * (i % PER));
+      if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+        // a bfloat16 is the upper half of a float
+        return __uint_as_float(PER == 2 && i % 2 ? w[i / PER] & 0xffff0000u : v << 16);
+      } else {
+        const unsigned short h = (unsigned short)v;
+        return __half2float(*reinterpret_cast<const __half*>(&h));
+      }
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < NW; ++i) w[i] = 0;
+  }
+  // the i-th element, of a pack that is zero there
+  __device__ __forceinline__ void put(int i, T v) { w[i / PER] |= (W)(bits_of(v) << (16 * (i % PER))); }
 };
 
 // V consecutive elements at p, of which `n` exist (the others read as 0 and are not
-// written).  `vec`: p is a multiple of the pack's alignment.
+// written).  `vec`: p is a multiple of the pack's size, up to 16 bytes.
 template <typename T, int V>
 __device__ __forceinline__ Pack<T, V> ld_pack(const T* p, int n, bool vec) {
   Pack<T, V> r;
+  using P = Pack<T, V>;
   if (vec && n >= V) {
-    r = *reinterpret_cast<const Pack<T, V>*>(p);
-  } else {
+    if constexpr (P::BYTES >= 16) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) r.e[i] = i < n ? p[i] : from_f<T>(0.f);
+      for (int i = 0; i < P::BYTES / 16; ++i)
+        *reinterpret_cast<uint4*>(r.w + 4 * i) = reinterpret_cast<const uint4*>(p)[i];
+    } else if constexpr (P::BYTES == 8) {
+      *reinterpret_cast<uint2*>(r.w) = *reinterpret_cast<const uint2*>(p);
+    } else {
+      r.w[0] = *reinterpret_cast<const typename P::W*>(p);
+    }
+  } else {
+    r.zero();
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) r.put(i, p[i]);
   }
   return r;
 }
 template <typename T, int V>
 __device__ __forceinline__ void st_pack(T* p, int n, bool vec, const Pack<T, V>& r) {
+  using P = Pack<T, V>;
   if (vec && n >= V) {
-    *reinterpret_cast<Pack<T, V>*>(p) = r;
+    if constexpr (P::BYTES >= 16) {
+#pragma unroll
+      for (int i = 0; i < P::BYTES / 16; ++i)
+        reinterpret_cast<uint4*>(p)[i] = make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]);
+    } else if constexpr (P::BYTES == 8) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
+    } else {
+      *reinterpret_cast<typename P::W*>(p) = r.w[0];
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (i < n) p[i] = r.e[i];
+    for (int i = 0; i < V; ++i) {
+      if (i >= n) continue;
+      if constexpr (sizeof(T) == 4)
+        reinterpret_cast<unsigned*>(p)[i] = r.w[i];
+      else
+        reinterpret_cast<unsigned short*>(p)[i] = (unsigned short)(r.w[i / P::PER] >> (16 * (i % P::PER)));
+    }
   }
 }
 template <typename T, int V>
 __device__ __forceinline__ void ld_f(const T* p, int n, bool vec, float (&v)[V]) {
   const Pack<T, V> r = ld_pack<T, V>(p, n, vec);
 #pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = to_f(r.e[i]);
+  for (int i = 0; i < V; ++i) v[i] = r.get(i);
 }
 template <typename T, int V>
 __device__ __forceinline__ void st_f(T* p, int n, bool vec, const float (&v)[V]) {
   Pack<T, V> r;
+  r.zero();
 #pragma unroll
-  for (int i = 0; i < V; ++i) r.e[i] = from_f<T>(v[i]);
+  for (int i = 0; i < V; ++i) r.put(i, from_f<T>(v[i]));
   st_pack<T, V>(p, n, vec, r);
 }
 
-// v sigmoid(v) and its derivative; sigmoid = 1/(1 + e^-v) tends to 0 and 1 without
-// overflow trouble (e^-v = inf gives 0).
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + expf(-v)); }
+// v sigmoid(v) and its derivative.  sigmoid = 1 / (1 + 2^(-v log2 e)) to about 2^-22, more for
+// large negative v by |v| 2^-24 (the exponent's rounding); it tends to 0 and 1 without
+// overflow trouble (2^.. = inf gives 0).
+__device__ __forceinline__ float sigmoid(float v) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.44269504088896340736f));
+  return s4dev::rcp_approx(1.f + e);
+}
 __device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
 __device__ __forceinline__ float silu_grad(float v) {
   const float s = sigmoid(v);

@@ -1,8 +1,10 @@
 // Shared by the selective scan's kernels (forward, single token, backward): how a CTA's threads
-// map to channels and states, the tiles it stages and the sums over lanes.
+// map to channels and states, activations, packed arithmetic and the sums over lanes.
 //
 // A channel's N states lie on LPC neighbouring lanes of a warp, SPT consecutive states each
-// (N <= LPC SPT, the rest padded with zeros); a thread serves CPT consecutive channels.  All
+// (N <= LPC SPT, the rest padded with zeros).  A thread serves two neighbouring channels, the
+// two halves of packed fp32 operations, which issue two multiplications or additions at once
+// (the rate of 128 a clock per SM is the same: packing saves issue slots, not arithmetic).  All
 // channels of a CTA belong to one group of B and C.
 #pragma once
 #include "s4_block.cuh"
@@ -14,14 +16,46 @@ using s4impl::St;
 constexpr int kThreads = 128;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
+// ---- packed pairs -----------------------------------------------------------------------
+__device__ __forceinline__ unsigned long long u64(float2 v) { return *reinterpret_cast<unsigned long long*>(&v); }
+__device__ __forceinline__ float2 f2(unsigned long long v) { return *reinterpret_cast<float2*>(&v); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(u64(a)), "l"(u64(b)));
+  return f2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(u64(a)), "l"(u64(b)));
+  return f2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(u64(a)), "l"(u64(b)), "l"(u64(c)));
+  return f2(r);
+}
+
+// ---- functions ----------------------------------------------------------------------------
 // 2^v (relative error 2^-22, 0 for results below the normal range)
 __device__ __forceinline__ float ex2(float v) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
-// log(1 + e^v) without overflow and with its relative precision for very negative v
-__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
+__device__ __forceinline__ float2 ex2(float2 v) { return make_float2(ex2(v.x), ex2(v.y)); }
+// log(1 + e^v) = max(v, 0) + log1p(u), u = e^-|v|: no overflow, and the relative precision of
+// log1p for small u.  log1p(u) = 2 atanh(s) with s = u / (2 + u) <= 1/3; 2 atanh(s) / s is a
+// polynomial in s^2 on [0, 1/9], here its interpolation at the Chebyshev points of degree 4
+// (relative error 8e-9, below the rounding of s).
+__device__ __forceinline__ float softplus(float v) {
+  const float u = ex2(-fabsf(v) * kLog2e), s = u * s4dev::rcp_approx(2.f + u), q = s * s;
+  float p = 0.2817465662956238f;
+  p = fmaf(p, q, 0.2796141803264618f);
+  p = fmaf(p, q, 0.40024852752685547f);
+  p = fmaf(p, q, 0.6666631698608398f);
+  p = fmaf(p, q, 2.f);
+  return fmaf(s, p, fmaxf(v, 0.f));
+}
 
 // A CTA's channels: blocks of HB within a group.
 struct Chan {
@@ -65,6 +99,20 @@ __device__ __forceinline__ void sum_lanes(float (&v)[4], int lane) {
 #pragma unroll
     for (int o = 4; o < LPC; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
   }
+}
+// The same for a pair of channels.
+template <int LPC>
+__device__ __forceinline__ void sum_lanes(float2 (&v)[4], int lane) {
+  float a[4], b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[i] = v[i].x;
+    b[i] = v[i].y;
+  }
+  sum_lanes<LPC>(a, lane);
+  sum_lanes<LPC>(b, lane);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = make_float2(a[i], b[i]);
 }
 // Tokens (of four) a lane holds after sum_lanes, and the i-th of them.
 template <int LPC>

@@ -19,15 +19,19 @@
 namespace {
 using namespace s4sel;
 
-template <int LPC_, int SPT_, int CPT_>
+template <int LPC_, int SPT_>
 struct Geo {
-  static constexpr int LPC = LPC_, SPT = SPT_, CPT = CPT_;
-  static constexpr int NP = LPC * SPT, SLOTS = kThreads / LPC, HB = SLOTS * CPT;
-  static constexpr int TT = 32;                        // tokens of a tile
-  static constexpr int CELLS = TT * HB / kThreads;     // (token, channel) cells a thread stages
-  // shared memory: (step, step x) [TT][HB] | B [TT][NP] | C [TT][NP] | y [TT][HB + 1]
-  static constexpr int B0 = 2 * TT * HB, C0 = B0 + TT * NP, Y0 = C0 + TT * NP;
-  static constexpr int bytes(int mode) { return 4 * (mode ? Y0 + TT * (HB + 1) : C0); }
+  static constexpr int LPC = LPC_, SPT = SPT_, NP = LPC * SPT;
+  static constexpr int HB = 2 * kThreads / LPC;      // channels of a CTA
+  static constexpr int TT = 16;                      // tokens of a tile
+  static constexpr int CELLS = TT * HB / kThreads;   // (token, channel) cells a thread stages
+  static constexpr int VECS = TT * NP / kThreads;    // and elements of B, of C
+  // Shared memory in floats: step and step x of channel pairs [TT][HB / 2][4] | B and C, each
+  // element twice (for both halves of a pair) [TT][NP][2] | y [TT][YROW].  The rows of y are 8
+  // floats longer than HB: the 4 tokens and 8 channel pairs a warp writes lie in different banks.
+  static constexpr int YROW = HB + 8;
+  static constexpr int B0 = 2 * TT * HB, C0 = B0 + 2 * TT * NP, Y0 = C0 + 2 * TT * NP;
+  static constexpr int bytes(int mode) { return 4 * (mode ? Y0 + TT * YROW : C0); }
 };
 
 struct Chunks {
@@ -36,115 +40,158 @@ struct Chunks {
   float *total;     // [batch][count][H]: sums of the step sizes
 };
 
+// V consecutive elements per access, of `count` a thread takes.
+template <typename T>
+constexpr int pack_of(int count, int row) {
+  int v = 16 / (int)sizeof(T);
+  v = v < row ? v : row;
+  return v < count ? v : count;
+}
+
 // MODE 0: states from a zero start and total steps of chunks 0 .. count - 2; MODE 1: outputs.
+// A tile's global reads are issued before the tile ahead of it is computed and wait in
+// registers until that is done.
 template <typename T, typename G, int MODE>
-__global__ void __launch_bounds__(kThreads) selective_scan_kernel(s4_selective_args a, Chunks ck, bool vec, St st) {
-  constexpr int LPC = G::LPC, SPT = G::SPT, CPT = G::CPT, NP = G::NP, HB = G::HB, TT = G::TT;
-  constexpr int V0 = 16 / (int)sizeof(T), V1 = V0 < HB ? V0 : HB, V = V1 < G::CELLS ? V1 : G::CELLS;
-  constexpr int NV = G::CELLS / V;  // packs a thread stages
+__global__ void __launch_bounds__(kThreads) selective_scan_kernel(s4_selective_args a, Chunks ck, bool vec, bool vecbc,
+                                                                 St st) {
+  constexpr int LPC = G::LPC, SPT = G::SPT, NP = G::NP, HB = G::HB, TT = G::TT;
+  constexpr int V = pack_of<T>(G::CELLS, HB), NV = G::CELLS / V, STEP = kThreads * V / HB;  // tokens between packs
+  constexpr int VB = pack_of<T>(G::VECS, NP), NB = G::VECS / VB;
   extern __shared__ __align__(16) float smem[];
-  float2(*sd)[HB] = reinterpret_cast<float2(*)[HB]>(smem);
-  float(*sb)[NP] = reinterpret_cast<float(*)[NP]>(smem + G::B0);
-  float(*sc)[NP] = reinterpret_cast<float(*)[NP]>(smem + G::C0);
-  float(*sy)[HB + 1] = reinterpret_cast<float(*)[HB + 1]>(smem + G::Y0);
+  float4(*sd)[HB / 2] = reinterpret_cast<float4(*)[HB / 2]>(smem);
+  float2(*sb)[NP] = reinterpret_cast<float2(*)[NP]>(smem + G::B0);
+  float2(*sc)[NP] = reinterpret_cast<float2(*)[NP]>(smem + G::C0);
+  float(*sy)[G::YROW] = reinterpret_cast<float(*)[G::YROW]>(smem + G::Y0);
   record_gen(st);
   const int b = blockIdx.z, chunk = blockIdx.y;
   const Chan c = chan_of<HB>(blockIdx.x, a.H / a.G);
   const Seq q = seq_of(a.lengths, a.index, b, a.L, a.slots, st);
   const int t0 = chunk * ck.len, t1 = min(a.L, t0 + ck.len), live = min(t1, q.len);
+  if (MODE == 0 && t0 >= q.len) return;
   const int lane = threadIdx.x % LPC, slot = threadIdx.x / LPC, n0 = lane * SPT;
-  const T* x = static_cast<const T*>(a.x.p) + b * a.x.batch;
-  const T* dt = static_cast<const T*>(a.dt.p) + b * a.dt.batch;
-  const T* z = a.z.p ? static_cast<const T*>(a.z.p) + b * a.z.batch : nullptr;
+  // the cells this thread stages: channels h .. h + V of tokens row, row + STEP, ...
+  const int hl = threadIdx.x * V % HB, row = threadIdx.x * V / HB, h = c.h0 + hl, nh = c.hend - h;
+  const T* x = static_cast<const T*>(a.x.p) + b * a.x.batch + h;
+  const T* dt = static_cast<const T*>(a.dt.p) + b * a.dt.batch + h;
+  const T* z = MODE && a.z.p ? static_cast<const T*>(a.z.p) + b * a.z.batch + h : nullptr;
   const T* B = static_cast<const T*>(a.B.p) + b * a.B.batch + c.g * a.B_group;
   const T* C = static_cast<const T*>(a.C.p) + b * a.C.batch + c.g * a.C_group;
-  T* y = MODE ? static_cast<T*>(a.y.p) + b * a.y.batch : nullptr;
-  if (MODE == 0 && t0 >= q.len) return;
-
-  float A[CPT][SPT], s[CPT][SPT], sum[CPT];
+  T* y = MODE ? static_cast<T*>(a.y.p) + b * a.y.batch + h : nullptr;
+  float bias[V], skip[V];
 #pragma unroll
-  for (int j = 0; j < CPT; ++j) {
-    const int h = c.h0 + slot * CPT + j;
-    sum[j] = 0.f;
-#pragma unroll
-    for (int i = 0; i < SPT; ++i) {
-      const int n = n0 + i;
-      const bool in = h < c.hend && n < a.N;
-      A[j][i] = in ? a.A[(long long)h * a.N + n] * kLog2e : 0.f;
-      s[j][i] = 0.f;
-      if (MODE == 1 && in) {
-        if (ck.count > 1)
-          s[j][i] = t0 < q.len || chunk == 0
-                        ? ck.start[(((long long)b * ck.count + chunk) * a.H + h) * a.N + n] : 0.f;
-        else if (a.state && q.slot >= 0)
-          s[j][i] = a.state[(q.slot * a.H + h) * a.N + n];
-      }
-    }
+  for (int i = 0; i < V; ++i) {
+    bias[i] = a.dt_bias && i < nh ? a.dt_bias[h + i] : 0.f;
+    skip[i] = MODE && a.D && i < nh ? a.D[h + i] : 0.f;
   }
 
-  for (int tb = t0; tb < t1; tb += TT) {
-    Pack<T, V> px[NV], pz[NV];
+  float2 A[SPT], s[SPT], sum = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < SPT; ++i) {
+    float Av[2], sv[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int hs = c.h0 + 2 * slot + j, n = n0 + i;
+      const bool in = hs < c.hend && n < a.N;
+      Av[j] = in ? a.A[(long long)hs * a.N + n] * kLog2e : 0.f;
+      sv[j] = 0.f;
+      if (MODE == 1 && in && (t0 < q.len || chunk == 0)) {
+        if (ck.count > 1)
+          sv[j] = ck.start[(((long long)b * ck.count + chunk) * a.H + hs) * a.N + n];
+        else if (a.state && q.slot >= 0)
+          sv[j] = a.state[(q.slot * a.H + hs) * a.N + n];
+      }
+    }
+    A[i] = make_float2(Av[0], Av[1]);
+    s[i] = make_float2(sv[0], sv[1]);
+  }
+
+  Pack<T, V> px[NV], pz[NV], nx[NV], nz[NV], nd[NV];
+  Pack<T, VB> nb[NB], nc[NB];
+  const auto fetch = [&](int tb) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int t = tb + row + k * STEP;
+      const int n = t < live && S4_IN(t, a.L) ? nh : 0;
+      nx[k] = ld_pack<T, V>(x + t * a.x.row, n, vec);
+      nd[k] = ld_pack<T, V>(dt + t * a.dt.row, n, vec);
+      if (z) nz[k] = ld_pack<T, V>(z + t * a.z.row, n, vec);
+    }
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int i = (k * kThreads + threadIdx.x) * VB, t = tb + i / NP;
+      const int n = t < live && S4_IN(t, a.L) ? a.N - i % NP : 0;
+      nb[k] = ld_pack<T, VB>(B + t * a.B.row + i % NP, n, vecbc);
+      if (MODE == 1) nc[k] = ld_pack<T, VB>(C + t * a.C.row + i % NP, n, vecbc);
+    }
+  };
+  if (t0 < live) fetch(t0);
+  for (int tb = t0; tb < (MODE ? t1 : live); tb += TT) {
     if (tb < live) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int cell = (k * kThreads + threadIdx.x) * V, t = tb + cell / HB, hl = cell % HB, h = c.h0 + hl;
-        const int n = c.hend - h;
+        px[k] = nx[k];
+        pz[k] = nz[k];
         float d[V];
-        if (t < live && n > 0 && S4_IN(t, a.L) && S4_IN(h, a.H)) {
-          px[k] = ld_pack<T, V>(x + t * a.x.row + h, n, vec);
-          if (MODE == 1 && z) pz[k] = ld_pack<T, V>(z + t * a.z.row + h, n, vec);
-          ld_f<T, V>(dt + t * a.dt.row + h, n, vec, d);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            if (a.dt_bias && i < n) d[i] += a.dt_bias[h + i];
-            if (a.softplus) d[i] = softplus(d[i]);
-            if (i >= n) d[i] = 0.f;
-          }
+        for (int i = 0; i < V; ++i) {
+          d[i] = nd[k].get(i) + bias[i];
+          if (a.softplus) d[i] = softplus(d[i]);
+          if (tb + row + k * STEP >= live || i >= nh) d[i] = 0.f;
+        }
+        float* to = reinterpret_cast<float*>(&sd[row + k * STEP][0]) + 2 * hl;
+        if constexpr (V == 1) {
+          // (step, step x) of one half of a pair
+          to = reinterpret_cast<float*>(&sd[row + k * STEP][hl / 2]) + hl % 2;
+          to[0] = d[0];
+          to[2] = d[0] * px[k].get(0);
         } else {
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            d[i] = 0.f;
-            px[k].e[i] = from_f<T>(0.f);
+          for (int i = 0; i < V; i += 2)
+            *reinterpret_cast<float4*>(to + 2 * i) =
+                make_float4(d[i], d[i + 1], d[i] * px[k].get(i), d[i + 1] * px[k].get(i + 1));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const int i = (k * kThreads + threadIdx.x) * VB;
+#pragma unroll
+        for (int e = 0; e < VB; ++e) {
+          const float vb = nb[k].get(e);
+          (&sb[0][0])[i + e] = make_float2(vb, vb);
+          if (MODE == 1) {
+            const float vc = nc[k].get(e);
+            (&sc[0][0])[i + e] = make_float2(vc, vc);
           }
         }
-#pragma unroll
-        for (int i = 0; i < V; ++i) sd[cell / HB][hl + i] = make_float2(d[i], d[i] * to_f(px[k].e[i]));
       }
-      stage_vectors<T, TT, NP>(&sb[0][0], B, a.B.row, tb, live, a.N);
-      if (MODE == 1) stage_vectors<T, TT, NP>(&sc[0][0], C, a.C.row, tb, live, a.N);
       __syncthreads();
-#pragma unroll 2
+      if (tb + TT < live) fetch(tb + TT);
+#pragma unroll
       for (int u = 0; u < TT; u += 4) {
-        float v[CPT][4];
+        float2 v[4];
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          float Bv[SPT], Cv[SPT];
+          const float4 d = sd[u + w][slot];
+          const float2 dd = make_float2(d.x, d.y), dx = make_float2(d.z, d.w);
+          if (MODE == 0) sum = add2(sum, dd);
 #pragma unroll
-          for (int i = 0; i < SPT; ++i) {
-            Bv[i] = sb[u + w][n0 + i];
-            Cv[i] = MODE ? sc[u + w][n0 + i] : 0.f;
-          }
-#pragma unroll
-          for (int j = 0; j < CPT; ++j) {
-            const float2 d = sd[u + w][slot * CPT + j];
-            if (MODE == 0) sum[j] += d.x;
-            float acc = 0.f;
-#pragma unroll
-            for (int i = 0; i < SPT; ++i) {
-              s[j][i] = fmaf(ex2(d.x * A[j][i]), s[j][i], d.y * Bv[i]);
-              if (MODE == 1) acc = fmaf(Cv[i], s[j][i], acc);
+          for (int i = 0; i < SPT; i += 2) {
+            const float4 b4 = *reinterpret_cast<const float4*>(&sb[u + w][n0 + i]);
+            s[i] = fma2(ex2(mul2(dd, A[i])), s[i], mul2(dx, make_float2(b4.x, b4.y)));
+            s[i + 1] = fma2(ex2(mul2(dd, A[i + 1])), s[i + 1], mul2(dx, make_float2(b4.z, b4.w)));
+            if (MODE == 1) {
+              const float4 c4 = *reinterpret_cast<const float4*>(&sc[u + w][n0 + i]);
+              v[w] = i ? fma2(make_float2(c4.x, c4.y), s[i], v[w]) : mul2(make_float2(c4.x, c4.y), s[i]);
+              v[w] = fma2(make_float2(c4.z, c4.w), s[i + 1], v[w]);
             }
-            v[j][w] = acc;
           }
         }
         if (MODE == 1) {
+          sum_lanes<LPC>(v, lane);
+          if (lane < 4) {
 #pragma unroll
-          for (int j = 0; j < CPT; ++j) {
-            sum_lanes<LPC>(v[j], lane);
-            if (lane < 4) {
-#pragma unroll
-              for (int i = 0; i < kOwn<LPC>; ++i) sy[u + own_token<LPC>(lane, i)][slot * CPT + j] = v[j][i];
-            }
+            for (int i = 0; i < kOwn<LPC>; ++i)
+              *reinterpret_cast<float2*>(&sy[u + own_token<LPC>(lane, i)][2 * slot]) = v[i];
           }
         }
       }
@@ -154,20 +201,18 @@ __global__ void __launch_bounds__(kThreads) selective_scan_kernel(s4_selective_a
       // the outputs of this thread's cells: skip term, gate, one rounding
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int cell = (k * kThreads + threadIdx.x) * V, t = tb + cell / HB, hl = cell % HB, h = c.h0 + hl;
-        const int n = c.hend - h;
-        if (t >= t1 || n <= 0) continue;
+        const int t = tb + row + k * STEP;
+        if (t >= t1 || nh <= 0 || !S4_IN(t, a.L)) continue;
         float out[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           out[i] = 0.f;
-          if (t < live && i < n) {
-            float v = sy[cell / HB][hl + i];
-            if (a.D) v = fmaf(a.D[h + i], to_f(px[k].e[i]), v);
-            out[i] = z ? v * silu(to_f(pz[k].e[i])) : v;
+          if (t < live) {
+            const float v = fmaf(skip[i], px[k].get(i), sy[row + k * STEP][hl + i]);
+            out[i] = z ? v * silu(pz[k].get(i)) : v;
           }
         }
-        if (S4_IN(t, a.L)) st_f<T, V>(y + t * a.y.row + h, n, vec, out);
+        st_f<T, V>(y + t * a.y.row, nh, vec, out);
       }
     }
   }
@@ -180,13 +225,13 @@ __global__ void __launch_bounds__(kThreads) selective_scan_kernel(s4_selective_a
     out = a.state_out + q.slot * a.H * a.N;
   if (out) {
 #pragma unroll
-    for (int j = 0; j < CPT; ++j) {
-      const int h = c.h0 + slot * CPT + j;
-      if (h >= c.hend) continue;
+    for (int j = 0; j < 2; ++j) {
+      const int hs = c.h0 + 2 * slot + j;
+      if (hs >= c.hend) continue;
 #pragma unroll
       for (int i = 0; i < SPT; ++i)
-        if (n0 + i < a.N) out[(long long)h * a.N + n0 + i] = s[j][i];
-      if (MODE == 0 && lane == 0) ck.total[((long long)b * ck.count + chunk) * a.H + h] = sum[j];
+        if (n0 + i < a.N) out[(long long)hs * a.N + n0 + i] = j ? s[i].y : s[i].x;
+      if (MODE == 0 && lane == 0) ck.total[((long long)b * ck.count + chunk) * a.H + hs] = j ? sum.y : sum.x;
     }
   }
 }
@@ -258,7 +303,7 @@ __global__ void __launch_bounds__(256) selective_step_kernel(s4_selective_args a
 
 // Chunks: enough warps to fill the GPU (kWarps per SM), none shorter than kMinChunk tokens, and
 // only where one chunk would leave more than half of them missing (chunks read the inputs twice).
-constexpr int kWarps = 16, kMinChunk = 128, kTile = 32;
+constexpr int kWarps = 16, kMinChunk = 128, kTile = 16;
 Chunks plan(int batch, int L, int H, int N, int G, int HB) {
   const long long ctas = (long long)batch * G * ((H / G + HB - 1) / HB);
   const long long want = (long long)s4impl::num_sms() * kWarps / (kThreads / 32);
@@ -274,13 +319,12 @@ Chunks plan(int batch, int L, int H, int N, int G, int HB) {
 // The lanes and states per lane that hold N states.
 template <typename F>
 auto with_states(int N, F f) {
-  if (N <= 4) return f(Geo<1, 4, 1>{});
-  if (N <= 8) return f(Geo<2, 4, 1>{});
-  if (N <= 16) return f(Geo<4, 4, 1>{});
-  if (N <= 32) return f(Geo<8, 4, 1>{});
-  if (N <= 64) return f(Geo<16, 4, 1>{});
-  if (N <= 128) return f(Geo<32, 4, 1>{});
-  return f(Geo<32, 8, 1>{});
+  if (N <= 8) return f(Geo<2, 4>{});
+  if (N <= 16) return f(Geo<4, 4>{});
+  if (N <= 32) return f(Geo<8, 4>{});
+  if (N <= 64) return f(Geo<16, 4>{});
+  if (N <= 128) return f(Geo<32, 4>{});
+  return f(Geo<32, 8>{});
 }
 
 template <typename T>
@@ -305,6 +349,9 @@ cudaError_t scan_t(const s4_selective_args& a, St st, cudaStream_t s) {
     const bool vec = vec_ok(a.x.p, e, 16, a.x.batch, a.x.row) && vec_ok(a.dt.p, e, 16, a.dt.batch, a.dt.row) &&
                      vec_ok(a.z.p, e, 16, a.z.batch, a.z.row) && vec_ok(a.y.p, e, 16, a.y.batch, a.y.row) &&
                      (a.G == 1 || (a.H / a.G) * e % 16 == 0);
+    constexpr int pb = sizeof(T) * pack_of<T>(G::VECS, G::NP);
+    const bool vecbc = vec_ok(a.B.p, e, pb, a.B.batch, a.B.row) && vec_ok(a.C.p, e, pb, a.C.batch, a.C.row) &&
+                       a.B_group * e % pb == 0 && a.C_group * e % pb == 0;
     Chunks ck = plan(a.batch, a.L, a.H, a.N, a.G, G::HB);
     ck.start = reinterpret_cast<float*>(static_cast<char*>(a.ws) + s4impl::kStatusBytes);
     ck.total = ck.start + (long long)a.batch * ck.count * a.H * a.N;
@@ -315,14 +362,14 @@ cudaError_t scan_t(const s4_selective_args& a, St st, cudaStream_t s) {
       {
         s4impl::TimedLaunch tl("selective_scan", s);
         selective_scan_kernel<T, G, 0>
-            <<<dim3(blocks, ck.count - 1, a.batch), kThreads, G::bytes(0), s>>>(a, ck, vec, st);
+            <<<dim3(blocks, ck.count - 1, a.batch), kThreads, G::bytes(0), s>>>(a, ck, vec, vecbc, st);
       }
       s4impl::TimedLaunch tl("selective_scan", s);
       const long long HN = (long long)a.H * a.N;
       selective_join_kernel<<<dim3((unsigned)((HN + 255) / 256), a.batch), 256, 0, s>>>(a, ck, st);
     }
     s4impl::TimedLaunch tl("selective_scan", s);
-    selective_scan_kernel<T, G, 1><<<dim3(blocks, ck.count, a.batch), kThreads, G::bytes(1), s>>>(a, ck, vec, st);
+    selective_scan_kernel<T, G, 1><<<dim3(blocks, ck.count, a.batch), kThreads, G::bytes(1), s>>>(a, ck, vec, vecbc, st);
   });
   return cudaGetLastError();
 }

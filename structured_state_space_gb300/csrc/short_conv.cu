@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(s4_short_conv_args
       if (t + u < q.len) {
         // the window is a ring: the input of token t + u replaces that of t + u - KW
 #pragma unroll
-        for (int i = 0; i < V; ++i) win[(KW - 1 + u) % KW][i] = to_f(in[u].e[i]);
+        for (int i = 0; i < V; ++i) win[(KW - 1 + u) % KW][i] = in[u].get(i);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           float v = bias[i];
@@ -89,8 +89,7 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(s4_short_conv_args
     for (int j = 0; j < a.W - 1; ++j) {
       const int t = q.len - (a.W - 1) + j;
       Pack<T, V> r;
-#pragma unroll
-      for (int i = 0; i < V; ++i) r.e[i] = from_f<T>(0.f);
+      r.zero();
       if (t >= 0)
         r = ld_pack<T, V>(x + t * a.x.row, n, vec);
       else if (state)
@@ -165,10 +164,10 @@ __global__ void __launch_bounds__(32 * kWarpsBwd) short_conv_bwd_kernel(s4_short
         const bool own = t < t1;
         if (t < q.len) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) win[(KW - 1 + u) % KW][i] = to_f(xi[u].e[i]);
+          for (int i = 0; i < V; ++i) win[(KW - 1 + u) % KW][i] = xi[u].get(i);
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            float d = to_f(di[u].e[i]);
+            float d = di[u].get(i);
             if (a.silu) {
               float v = bias[i];
 #pragma unroll
