@@ -2,10 +2,10 @@
 // map to channels and states, activations, packed arithmetic and the sums over lanes.
 //
 // A channel's N states lie on LPC neighbouring lanes of a warp, SPT consecutive states each
-// (N <= LPC SPT, the rest padded with zeros).  A thread serves two neighbouring channels, the
-// two halves of packed fp32 operations, which issue two multiplications or additions at once
-// (the rate of 128 a clock per SM is the same: packing saves issue slots, not arithmetic).  All
-// channels of a CTA belong to one group of B and C.
+// (N <= LPC SPT, the rest padded with zeros).  A thread serves several neighbouring channels.  Packed
+// fp32 operations issue two multiplications or additions at once (the rate of 128 a clock per
+// SM is the same: packing saves issue slots, not arithmetic).  All channels of a warp or CTA
+// that works together belong to one group of B and C.
 #pragma once
 #include "s4_block.cuh"
 
@@ -62,6 +62,10 @@ struct Chan {
   int g, h0, hend;  // group, first channel, end of the group's channels
 };
 template <int HB>
+__host__ __device__ __forceinline__ int chan_blocks(int H, int G) {
+  return G * ((H / G + HB - 1) / HB);
+}
+template <int HB>
 __device__ __forceinline__ Chan chan_of(int block, int Hg) {
   const int per = (Hg + HB - 1) / HB;
   Chan c;
@@ -99,20 +103,6 @@ __device__ __forceinline__ void sum_lanes(float (&v)[4], int lane) {
 #pragma unroll
     for (int o = 4; o < LPC; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
   }
-}
-// The same for a pair of channels.
-template <int LPC>
-__device__ __forceinline__ void sum_lanes(float2 (&v)[4], int lane) {
-  float a[4], b[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    a[i] = v[i].x;
-    b[i] = v[i].y;
-  }
-  sum_lanes<LPC>(a, lane);
-  sum_lanes<LPC>(b, lane);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = make_float2(a[i], b[i]);
 }
 // Tokens (of four) a lane holds after sum_lanes, and the i-th of them.
 template <int LPC>
