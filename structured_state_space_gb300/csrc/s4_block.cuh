@@ -90,6 +90,11 @@ __device__ __forceinline__ Pack<T, V> ld_pack(const T* p, int n, bool vec) {
   }
   return r;
 }
+// The same where all of them exist and the address is aligned.
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> ld_whole(const T* p) {
+  return ld_pack<T, V>(p, V, true);
+}
 template <typename T, int V>
 __device__ __forceinline__ void st_pack(T* p, int n, bool vec, const Pack<T, V>& r) {
   using P = Pack<T, V>;
@@ -127,6 +132,11 @@ __device__ __forceinline__ void st_f(T* p, int n, bool vec, const float (&v)[V])
 #pragma unroll
   for (int i = 0; i < V; ++i) r.put(i, from_f<T>(v[i]));
   st_pack<T, V>(p, n, vec, r);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void st_whole(T* p, const float (&v)[V]) {
+  st_f<T, V>(p, V, true, v);
 }
 
 // v sigmoid(v) and its derivative.  sigmoid = 1 / (1 + 2^(-v log2 e)) to about 2^-22, more for

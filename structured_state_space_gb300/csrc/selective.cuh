@@ -56,6 +56,18 @@ __device__ __forceinline__ float softplus(float v) {
   p = fmaf(p, q, 2.f);
   return fmaf(s, p, fmaxf(v, 0.f));
 }
+// The same of a pair, in packed operations.
+__device__ __forceinline__ float2 softplus2(float2 v) {
+  const float2 u = make_float2(ex2(-fabsf(v.x) * kLog2e), ex2(-fabsf(v.y) * kLog2e));
+  const float2 two = make_float2(2.f, 2.f), w = add2(u, two);
+  const float2 s = mul2(u, make_float2(s4dev::rcp_approx(w.x), s4dev::rcp_approx(w.y))), q = mul2(s, s);
+  float2 p = fma2(make_float2(0.2817465662956238f, 0.2817465662956238f), q,
+                  make_float2(0.2796141803264618f, 0.2796141803264618f));
+  p = fma2(p, q, make_float2(0.40024852752685547f, 0.40024852752685547f));
+  p = fma2(p, q, make_float2(0.6666631698608398f, 0.6666631698608398f));
+  p = fma2(p, q, two);
+  return fma2(s, p, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
+}
 
 // A CTA's channels: blocks of HB within a group.
 struct Chan {

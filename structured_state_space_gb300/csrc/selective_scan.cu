@@ -16,17 +16,24 @@
 
 namespace {
 using namespace s4sel;
+#ifndef S4_MB1
+#define S4_MB1 4
+#define S4_MB0 4
+#define S4_TH 128
+#define S4_KW 16
+#endif
+constexpr int kScanThreads = S4_TH;
 
 template <int LPC_, int SPT_>
 struct Geo {
-  static constexpr int LPC = LPC_, SPT = SPT_, NP = LPC * SPT, CPT = 4;
+  static constexpr int LPC = LPC_, SPT = SPT_, NP = LPC * SPT, CPT = 2;
   static constexpr int CH = 32 / LPC * CPT;              // channels of a warp
-  static constexpr int TT = 4;                           // tokens of a tile
-  static constexpr int OWN = kOwn<LPC>;                  // tokens of a tile that a lane stages and finishes
+  static constexpr int TT = NP <= 64 ? 8 : 4;            // tokens of a tile
+  static constexpr int OWN = TT / 4 * kOwn<LPC>;         // tokens of a tile that a lane stages and finishes
   static constexpr int VECS = TT * NP / 32;              // elements of B, of C that a lane stages
-  // Shared memory of a warp in floats: steps and step x of 4 channels [TT][32 / LPC][8] | B | C [TT][NP]
-  static constexpr int B0 = TT * 32 / LPC * 8, C0 = B0 + TT * NP, END = C0 + TT * NP;
-  static constexpr int kBytes = 4 * END * (kThreads / 32);
+  // Shared memory of a warp in floats: steps and step x of channel pairs [TT][32 / LPC][4] | B | C [TT][NP]
+  static constexpr int B0 = TT * 32 / LPC * 4, C0 = B0 + TT * NP, END = C0 + TT * NP;
+  static constexpr int kBytes = 4 * END * (kScanThreads / 32);
 };
 
 struct Chunks {
@@ -37,36 +44,39 @@ struct Chunks {
 
 // MODE 0: states from a zero start and total steps of chunks 0 .. count - 2; MODE 1: outputs.
 //
-// Warps work alone: a lane stages the step sizes of its slot's 4 channels for the tokens it owns,
-// the slot's LPC lanes read them back, and after the sums over the slot the same lane holds
-// y of the same tokens and channels, beside their x and z.  So the only data that passes
-// through shared memory are (step, step x) and the vectors B and C, and no barrier is wider than a
-// warp.  Shared memory delivers 32 words a clock to the registers of an SM (broadcast or
-// not), an exponential takes 1/32 clock too: 8 states by 4 channels per thread read 24 words for
-// 32 exponentials.
-template <typename T, typename G, int MODE>
-__global__ void __launch_bounds__(kThreads, MODE || sizeof(T) == 4 ? 3 : 4)
+// Warps work alone: a lane stages the step sizes of its 2 channels for the tokens it owns, the
+// LPC lanes of the channels read them back, and after the sums over these lanes the same lane
+// holds y of the same tokens, beside their x and z.  So only (step, step x) and the vectors B
+// and C pass through shared memory, and no barrier is wider than a warp.  Shared memory delivers
+// 32 words a clock to the registers of an SM, broadcast or not, and an exponential takes 1/32
+// clock: 8 states by 2 channels per thread read 20 words for 16 exponentials, and leave
+// registers for 20 warps per SM.
+//
+// WHOLE: every access is aligned and every warp's channels and states exist, so that tiles of real
+// tokens are read and written without a condition.
+template <typename T, typename G, int MODE, bool WHOLE>
+__global__ void __launch_bounds__(kScanThreads, MODE ? S4_MB1 : S4_MB0)
     selective_scan_kernel(s4_selective_args a, Chunks ck, bool vec, bool vecbc, St st) {
   constexpr int LPC = G::LPC, SPT = G::SPT, NP = G::NP, CH = G::CH, TT = G::TT, CPT = G::CPT, OWN = G::OWN;
   constexpr int V0 = 16 / (int)sizeof(T), VB = V0 < G::VECS ? V0 : G::VECS, NB = G::VECS / VB;
   constexpr bool AHEAD = NP <= 64;  // B and C of the next tile wait in registers
   extern __shared__ __align__(16) float smem[];
   float* mine = smem + threadIdx.x / 32 * G::END;
-  float(*sd)[32 / LPC][8] = reinterpret_cast<float(*)[32 / LPC][8]>(mine);
+  float4(*sd)[32 / LPC] = reinterpret_cast<float4(*)[32 / LPC]>(mine);
   float(*sb)[NP] = reinterpret_cast<float(*)[NP]>(mine + G::B0);
   float(*sc)[NP] = reinterpret_cast<float(*)[NP]>(mine + G::C0);
   record_gen(st);
   const int b = blockIdx.z, wl = threadIdx.x & 31;
   const int blocks = chan_blocks<CH>(a.H, a.G), count = MODE ? ck.count : ck.count - 1;
-  const long long task = (long long)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  const long long task = (long long)blockIdx.x * (kScanThreads / 32) + threadIdx.x / 32;
   const Seq q = seq_of(a.lengths, a.index, b, a.L, a.slots, st);
   if (task >= (long long)blocks * count) return;
   const int chunk = (int)(task / blocks);
   const Chan c = chan_of<CH>((int)(task % blocks), a.H / a.G);
   const int t0 = chunk * ck.len, t1 = min(a.L, t0 + ck.len), live = min(t1, q.len);
   if (MODE == 0 && t0 >= q.len) return;
-  const int lane = wl % LPC, slot = wl / LPC, n0 = lane * SPT;
-  const int h = c.h0 + slot * CPT, nh = LPC > 4 && lane >= 4 ? 0 : c.hend - h;  // channels this lane stages
+  const int lane = wl % LPC, slot = wl / LPC, n0 = lane * SPT, h = c.h0 + slot * CPT, nh = c.hend - h;
+  const int ns = LPC > 4 && lane >= 4 ? 0 : nh;  // channels this lane stages and finishes
   const T* x = static_cast<const T*>(a.x.p) + b * a.x.batch + h;
   const T* dt = static_cast<const T*>(a.dt.p) + b * a.dt.batch + h;
   const T* z = MODE && a.z.p ? static_cast<const T*>(a.z.p) + b * a.z.batch + h : nullptr;
@@ -75,14 +85,14 @@ __global__ void __launch_bounds__(kThreads, MODE || sizeof(T) == 4 ? 3 : 4)
   T* y = MODE ? static_cast<T*>(a.y.p) + b * a.y.batch + h : nullptr;
 
   float2 A[CPT][SPT / 2], s[CPT][SPT / 2];  // pairs of neighbouring states
-  float bias[CPT], skip[CPT], sum[CPT];
+  float bias[CPT], skip[CPT];
+  float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
   for (int j = 0; j < CPT; ++j) {
     const int hs = h + j;
-    const bool on = hs < c.hend;
+    const bool on = j < nh;
     bias[j] = a.dt_bias && on ? a.dt_bias[hs] : 0.f;
     skip[j] = MODE && a.D && on ? a.D[hs] : 0.f;
-    sum[j] = 0.f;
 #pragma unroll
     for (int i = 0; i < SPT; ++i) {
       const int n = n0 + i;
@@ -100,9 +110,20 @@ __global__ void __launch_bounds__(kThreads, MODE || sizeof(T) == 4 ? 3 : 4)
     }
   }
 
-  Pack<T, CPT> nx[OWN], nd[OWN];
+  // the k-th token of a tile that this lane owns
+  const auto token = [&](int k) { return k / kOwn<LPC> * 4 + own_token<LPC>(lane, k % kOwn<LPC>); };
+  Pack<T, CPT> nx[OWN], nd[OWN], nz[OWN];
   Pack<T, VB> nb[NB], nc[NB];
   const auto fetch_bc = [&](int tb) {
+    if (WHOLE && tb + TT <= live) {
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const int i = (k * 32 + wl) * VB, t = tb + i / NP;
+        nb[k] = ld_whole<T, VB>(B + t * a.B.row + i % NP);
+        if (MODE == 1) nc[k] = ld_whole<T, VB>(C + t * a.C.row + i % NP);
+      }
+      return;
+    }
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       const int i = (k * 32 + wl) * VB, t = tb + i / NP;
@@ -112,38 +133,41 @@ __global__ void __launch_bounds__(kThreads, MODE || sizeof(T) == 4 ? 3 : 4)
     }
   };
   const auto fetch = [&](int tb) {
+    if (AHEAD) fetch_bc(tb);
+    if (WHOLE && tb + TT <= live) {
+#pragma unroll
+      for (int k = 0; k < OWN; ++k) {
+        const int t = tb + token(k);
+        nx[k] = ld_whole<T, CPT>(x + t * a.x.row);
+        nd[k] = ld_whole<T, CPT>(dt + t * a.dt.row);
+        if (z) nz[k] = ld_whole<T, CPT>(z + t * a.z.row);
+      }
+      return;
+    }
 #pragma unroll
     for (int k = 0; k < OWN; ++k) {
-      const int t = tb + own_token<LPC>(lane, k), n = t < live && S4_IN(t, a.L) ? nh : 0;
+      const int t = tb + token(k), n = t < live && S4_IN(t, a.L) ? ns : 0;
       nx[k] = ld_pack<T, CPT>(x + t * a.x.row, n, vec);
       nd[k] = ld_pack<T, CPT>(dt + t * a.dt.row, n, vec);
+      if (z) nz[k] = ld_pack<T, CPT>(z + t * a.z.row, n, vec);
     }
-    if (AHEAD) fetch_bc(tb);
   };
   if (t0 < live) fetch(t0);
-  int tb = t0;
-  for (; tb < live; tb += TT) {
+  for (int tb = t0; tb < live; tb += TT) {
+    const bool whole = tb + TT <= live;
     Pack<T, CPT> px[OWN], pz[OWN];
     if (!AHEAD) fetch_bc(tb);
     __syncwarp();  // the tile before has been read
 #pragma unroll
     for (int k = 0; k < OWN; ++k) {
-      const int t = tb + own_token<LPC>(lane, k), n = t < live ? nh : 0;
       px[k] = nx[k];
-      if (z) pz[k] = ld_pack<T, CPT>(z + t * a.z.row, n, vec);
-      float d[CPT], dx[CPT];
-#pragma unroll
-      for (int j = 0; j < CPT; ++j) {
-        d[j] = nd[k].get(j) + bias[j];
-        if (a.softplus) d[j] = softplus(d[j]);
-        if (j >= n) d[j] = 0.f;
-        dx[j] = d[j] * px[k].get(j);
-      }
-      if (LPC <= 4 || lane < 4) {
-        float4* to = reinterpret_cast<float4*>(sd[own_token<LPC>(lane, k)][slot]);
-        to[0] = make_float4(d[0], d[1], d[2], d[3]);
-        to[1] = make_float4(dx[0], dx[1], dx[2], dx[3]);
-      }
+      pz[k] = nz[k];
+      float2 d = make_float2(nd[k].get(0) + bias[0], nd[k].get(1) + bias[1]);
+      if (a.softplus) d = softplus2(d);
+      if (!whole && tb + token(k) >= live) d = make_float2(0.f, 0.f);  // padding keeps the state
+      const float2 dx = mul2(d, make_float2(px[k].get(0), px[k].get(1)));
+      if (MODE == 0) sum = add2(sum, d);
+      if (LPC <= 4 || lane < 4) sd[token(k)][slot] = make_float4(d.x, d.y, dx.x, dx.y);
     }
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
@@ -156,55 +180,58 @@ __global__ void __launch_bounds__(kThreads, MODE || sizeof(T) == 4 ? 3 : 4)
     }
     __syncwarp();
     if (tb + TT < live) fetch(tb + TT);
-    float v[CPT][4];
 #pragma unroll
-    for (int w = 0; w < TT; ++w) {
-      const float4 d4 = *reinterpret_cast<const float4*>(&sd[w][slot][0]);
-      const float4 x4 = *reinterpret_cast<const float4*>(&sd[w][slot][4]);
-      const float d[CPT] = {d4.x, d4.y, d4.z, d4.w}, dx[CPT] = {x4.x, x4.y, x4.z, x4.w};
-      float2 acc[CPT];
+    for (int u = 0; u < TT; u += 4) {
+      float v[CPT][4];
 #pragma unroll
-      for (int i = 0; i < SPT / 2; i += 2) {
-        const float4 b4 = *reinterpret_cast<const float4*>(&sb[w][n0 + 2 * i]);
-        const float2 b0 = make_float2(b4.x, b4.y), b1 = make_float2(b4.z, b4.w);
-        float2 c0, c1;
-        if (MODE == 1) {
-          const float4 c4 = *reinterpret_cast<const float4*>(&sc[w][n0 + 2 * i]);
-          c0 = make_float2(c4.x, c4.y);
-          c1 = make_float2(c4.z, c4.w);
-        }
+      for (int w = 0; w < 4; ++w) {
+        const float4 d = sd[u + w][slot];
+        const float2 dd[CPT] = {make_float2(d.x, d.x), make_float2(d.y, d.y)};
+        const float2 xx[CPT] = {make_float2(d.z, d.z), make_float2(d.w, d.w)};
+        float2 acc[CPT];
 #pragma unroll
-        for (int j = 0; j < CPT; ++j) {
-          const float2 dd = make_float2(d[j], d[j]), xx = make_float2(dx[j], dx[j]);
-          s[j][i] = fma2(ex2(mul2(dd, A[j][i])), s[j][i], mul2(xx, b0));
-          s[j][i + 1] = fma2(ex2(mul2(dd, A[j][i + 1])), s[j][i + 1], mul2(xx, b1));
+        for (int i = 0; i < SPT / 2; i += 2) {
+          const float4 b4 = *reinterpret_cast<const float4*>(&sb[u + w][n0 + 2 * i]);
+          const float2 b0 = make_float2(b4.x, b4.y), b1 = make_float2(b4.z, b4.w);
+          float2 c0, c1;
           if (MODE == 1) {
-            acc[j] = i ? fma2(c0, s[j][i], acc[j]) : mul2(c0, s[j][i]);
-            acc[j] = fma2(c1, s[j][i + 1], acc[j]);
+            const float4 c4 = *reinterpret_cast<const float4*>(&sc[u + w][n0 + 2 * i]);
+            c0 = make_float2(c4.x, c4.y);
+            c1 = make_float2(c4.z, c4.w);
+          }
+#pragma unroll
+          for (int j = 0; j < CPT; ++j) {
+            s[j][i] = fma2(ex2(mul2(dd[j], A[j][i])), s[j][i], mul2(xx[j], b0));
+            s[j][i + 1] = fma2(ex2(mul2(dd[j], A[j][i + 1])), s[j][i + 1], mul2(xx[j], b1));
+            if (MODE == 1) {
+              acc[j] = i ? fma2(c0, s[j][i], acc[j]) : mul2(c0, s[j][i]);
+              acc[j] = fma2(c1, s[j][i + 1], acc[j]);
+            }
           }
         }
+        if (MODE == 1) {
+#pragma unroll
+          for (int j = 0; j < CPT; ++j) v[j][w] = acc[j].x + acc[j].y;
+        }
       }
+      if (MODE == 1) {
+        // y of four tokens, finished by the lanes that own them: skip term, gate, one rounding
 #pragma unroll
-      for (int j = 0; j < CPT; ++j) {
-        if (MODE == 0) sum[j] += d[j];
-        if (MODE == 1) v[j][w] = acc[j].x + acc[j].y;
-      }
-    }
-    if (MODE == 1) {
-      // y of the tile, finished by the lanes that own its tokens: skip term, gate, one rounding
+        for (int j = 0; j < CPT; ++j) sum_lanes<LPC>(v[j], lane);
 #pragma unroll
-      for (int j = 0; j < CPT; ++j) sum_lanes<LPC>(v[j], lane);
-#pragma unroll
-      for (int k = 0; k < OWN; ++k) {
-        const int t = tb + own_token<LPC>(lane, k);
-        if (t < live && nh > 0 && S4_IN(t, a.L)) {
+        for (int i = 0; i < kOwn<LPC>; ++i) {
+          const int k = u / 4 * kOwn<LPC> + i, t = tb + token(k);
           float out[CPT];
 #pragma unroll
           for (int j = 0; j < CPT; ++j) {
-            out[j] = fmaf(skip[j], px[k].get(j), v[j][k]);
+            out[j] = fmaf(skip[j], px[k].get(j), v[j][i]);
             if (z) out[j] *= silu(pz[k].get(j));
           }
-          st_f<T, CPT>(y + t * a.y.row, nh, vec, out);
+          if (WHOLE && whole) {
+            if (LPC <= 4 || lane < 4) st_whole<T, CPT>(y + t * a.y.row, out);
+          } else if (t < live && ns > 0 && S4_IN(t, a.L)) {
+            st_f<T, CPT>(y + t * a.y.row, ns, vec, out);
+          }
         }
       }
     }
@@ -212,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, MODE || sizeof(T) == 4 ? 3 : 4)
   if (MODE == 1) {  // padding
     const float zero[CPT] = {};
     for (int t = max(t0, live) + lane; t < t1; t += LPC)
-      if (c.hend > h) st_f<T, CPT>(y + t * a.y.row, c.hend - h, vec, zero);
+      if (nh > 0) st_f<T, CPT>(y + t * a.y.row, nh, vec, zero);
   }
   // Where the state goes: the chunk's end state, or, after the last real token, the caller's slot.
   float* out = nullptr;
@@ -221,15 +248,22 @@ __global__ void __launch_bounds__(kThreads, MODE || sizeof(T) == 4 ? 3 : 4)
   else if (a.state_out && q.slot >= 0 && ((t0 < q.len && q.len <= t1) || (q.len == 0 && chunk == 0)) &&
            S4_IN(q.slot, a.slots))
     out = a.state_out + q.slot * a.H * a.N;
+  if (MODE == 0) {  // the tokens are spread over up to four lanes
+#pragma unroll
+    for (int o = 1; o < (LPC < 4 ? LPC : 4); o <<= 1) {
+      sum.x += __shfl_xor_sync(0xffffffffu, sum.x, o);
+      sum.y += __shfl_xor_sync(0xffffffffu, sum.y, o);
+    }
+  }
   if (out) {
 #pragma unroll
     for (int j = 0; j < CPT; ++j) {
       const int hs = h + j;
-      if (hs >= c.hend) continue;
+      if (j >= nh) continue;
 #pragma unroll
       for (int i = 0; i < SPT; ++i)
         if (n0 + i < a.N) out[(long long)hs * a.N + n0 + i] = i % 2 ? s[j][i / 2].y : s[j][i / 2].x;
-      if (MODE == 0 && lane == 0) ck.total[((long long)b * ck.count + chunk) * a.H + hs] = sum[j];
+      if (MODE == 0 && lane == 0) ck.total[((long long)b * ck.count + chunk) * a.H + hs] = j ? sum.y : sum.x;
     }
   }
 }
@@ -311,7 +345,7 @@ __global__ void __launch_bounds__(256) selective_step_kernel(s4_selective_args a
 
 // Chunks: enough warps to fill the GPU (kWarps per SM), none shorter than kMinChunk tokens, and
 // only where one chunk would leave more than half of them missing (chunks read the inputs twice).
-constexpr int kWarps = 12, kMinChunk = 64, kTile = 4;
+constexpr int kWarps = S4_KW, kMinChunk = 64, kTile = 8;
 Chunks plan(int batch, int L, int H, int N, int G, int CH) {
   const long long warps = (long long)batch * G * ((H / G + CH - 1) / CH);
   const long long want = (long long)s4impl::num_sms() * kWarps;
@@ -369,7 +403,7 @@ cudaError_t scan_t(const s4_selective_args& a, St st, cudaStream_t s) {
   const int e = sizeof(T);
   with_states(a.N, [&](auto geo) {
     using G = decltype(geo);
-    constexpr int px = e * G::CPT, pb = e * (16 / e < G::VECS ? 16 / e : G::VECS), per = kThreads / 32;
+    constexpr int px = e * G::CPT, pb = e * (16 / e < G::VECS ? 16 / e : G::VECS), per = kScanThreads / 32;
     const auto ok = [&](const auto& r) { return vec_ok(r.p, e, px, r.batch, r.row); };
     const bool vec = ok(a.x) && ok(a.dt) && ok(a.z) && ok(a.y) && (a.G == 1 || (a.H / a.G) % G::CPT == 0);
     const bool vecbc = vec_ok(a.B.p, e, pb, a.B.batch, a.B.row) && vec_ok(a.C.p, e, pb, a.C.batch, a.C.row) &&
@@ -378,21 +412,32 @@ cudaError_t scan_t(const s4_selective_args& a, St st, cudaStream_t s) {
     ck.start = reinterpret_cast<float*>(static_cast<char*>(a.ws) + s4impl::kStatusBytes);
     ck.total = ck.start + (long long)a.batch * ck.count * a.H * a.N;
     const long long blocks = chan_blocks<G::CH>(a.H, a.G);
-    for (auto k : {selective_scan_kernel<T, G, 0>, selective_scan_kernel<T, G, 1>})
-      if (G::kBytes > 48 * 1024) cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kBytes);
-    if (ck.count > 1) {
-      {
+    const auto run = [&](auto whole) {
+      constexpr bool W = decltype(whole)::value;
+      const auto ends = selective_scan_kernel<T, G, 0, W>, out = selective_scan_kernel<T, G, 1, W>;
+      if (G::kBytes > 48 * 1024) {
+        cudaFuncSetAttribute(ends, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kBytes);
+        cudaFuncSetAttribute(out, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kBytes);
+      }
+      if (ck.count > 1) {
+        {
+          s4impl::TimedLaunch tl("selective_scan", s);
+          const dim3 grid((unsigned)((blocks * (ck.count - 1) + per - 1) / per), 1, a.batch);
+          ends<<<grid, kScanThreads, G::kBytes, s>>>(a, ck, vec, vecbc, st);
+        }
         s4impl::TimedLaunch tl("selective_scan", s);
-        const dim3 grid((unsigned)((blocks * (ck.count - 1) + per - 1) / per), 1, a.batch);
-        selective_scan_kernel<T, G, 0><<<grid, kThreads, G::kBytes, s>>>(a, ck, vec, vecbc, st);
+        const long long HN = (long long)a.H * a.N;
+        selective_join_kernel<<<dim3((unsigned)((HN + 127) / 128), a.batch), 128, 0, s>>>(a, ck, st);
       }
       s4impl::TimedLaunch tl("selective_scan", s);
-      const long long HN = (long long)a.H * a.N;
-      selective_join_kernel<<<dim3((unsigned)((HN + 127) / 128), a.batch), 128, 0, s>>>(a, ck, st);
-    }
-    s4impl::TimedLaunch tl("selective_scan", s);
-    const dim3 grid((unsigned)((blocks * ck.count + per - 1) / per), 1, a.batch);
-    selective_scan_kernel<T, G, 1><<<grid, kThreads, G::kBytes, s>>>(a, ck, vec, vecbc, st);
+      const dim3 grid((unsigned)((blocks * ck.count + per - 1) / per), 1, a.batch);
+      out<<<grid, kScanThreads, G::kBytes, s>>>(a, ck, vec, vecbc, st);
+    };
+    // the tiles of other widths cost a condition per access
+    if (vec && vecbc && a.N == G::NP && (a.H / a.G) % G::CH == 0 && G::LPC <= 4)
+      run(std::true_type{});
+    else
+      run(std::false_type{});
   });
   return cudaGetLastError();
 }
