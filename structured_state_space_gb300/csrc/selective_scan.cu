@@ -16,13 +16,11 @@
 
 namespace {
 using namespace s4sel;
-#ifndef S4_MB1
-#define S4_MB1 4
-#define S4_MB0 4
-#define S4_TH 128
-#define S4_KW 16
-#endif
-constexpr int kScanThreads = S4_TH;
+
+// Four CTAs of four warps per SM: 128 registers a thread.  At 20 warps per SM the registers
+// left do not hold enough exponentials in flight (650 us instead of 564 on one sequence of
+// 65536 tokens, 1024 channels, 16 states, bfloat16), at 14 there are too few warps (647 us).
+constexpr int kScanThreads = 128, kScanCtas = 4;
 
 template <int LPC_, int SPT_>
 struct Geo {
@@ -55,7 +53,7 @@ struct Chunks {
 // WHOLE: every access is aligned and every warp's channels and states exist, so that tiles of real
 // tokens are read and written without a condition.
 template <typename T, typename G, int MODE, bool WHOLE>
-__global__ void __launch_bounds__(kScanThreads, MODE ? S4_MB1 : S4_MB0)
+__global__ void __launch_bounds__(kScanThreads, kScanCtas)
     selective_scan_kernel(s4_selective_args a, Chunks ck, bool vec, bool vecbc, St st) {
   constexpr int LPC = G::LPC, SPT = G::SPT, NP = G::NP, CH = G::CH, TT = G::TT, CPT = G::CPT, OWN = G::OWN;
   constexpr int V0 = 16 / (int)sizeof(T), VB = V0 < G::VECS ? V0 : G::VECS, NB = G::VECS / VB;
@@ -343,14 +341,16 @@ __global__ void __launch_bounds__(256) selective_step_kernel(s4_selective_args a
   }
 }
 
-// Chunks: enough warps to fill the GPU (kWarps per SM), none shorter than kMinChunk tokens, and
-// only where one chunk would leave more than half of them missing (chunks read the inputs twice).
-constexpr int kWarps = S4_KW, kMinChunk = 64, kTile = 8;
+// Chunks: kWarps warps per SM (two rounds of what runs at once: with one, ragged sequences leave
+// SMs idle, 105 us instead of 96 on four sequences of up to 1500 tokens, 2048 channels; with
+// more, the joins grow), none shorter than kMinChunk tokens, and only where one chunk
+// would leave more than half of a round missing (chunks take the exponentials twice).
+constexpr int kWarps = 32, kMinChunk = 64, kTile = 8;
 Chunks plan(int batch, int L, int H, int N, int G, int CH) {
   const long long warps = (long long)batch * G * ((H / G + CH - 1) / CH);
   const long long want = (long long)s4impl::num_sms() * kWarps;
   Chunks ck{L, 1, nullptr, nullptr};
-  if (2 * warps > want || L < 2 * kMinChunk) return ck;
+  if (4 * warps > want || L < 2 * kMinChunk) return ck;
   long long n = want / warps;
   if (n > L / kMinChunk) n = L / kMinChunk;
   ck.len = (int)(((L + n - 1) / n + kTile - 1) / kTile * kTile);
