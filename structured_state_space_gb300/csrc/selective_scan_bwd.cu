@@ -5,16 +5,17 @@
 //   dC_t = sum_h dyp_t s_t,  dB_t = sum_h d_t x_t g_t,  u_t = sum_n B_t g_t,  w_t = a_t g_t s_{t-1}
 //   dx = d u + D dyp,  draw = (x u + sum_n A w) softplus',  dA = sum d w,  dz = dy ypre silu'(z)
 //
-// Per (token, channel, state) about 20 multiplications and additions, three exponentials and the
-// sums of dB and dC over channels; per (token, channel) 14 bytes in 16 bits.  Arithmetic and the
-// sums over lanes bound it.
+// Per (token, channel, state) 22 multiplications and additions, four exponentials and the sums of dB
+// and dC over channels; per (token, channel) 14 bytes in 16 bits.  The arithmetic and what
+// shared memory and the shuffles deliver to registers bound it, about 20 clocks of an SM quarter
+// each for 32 (token, channel, state).
 //
-// Three kernels.  (1) per segment of tokens, walking forward: each tile's state at its start and
-// the gradient that reaches its end from later tiles, both from zero at the segment's ends;
-// (2) where there are several segments, their joins; (3) per tile, independent of all others:
-// states at every block of TB tokens, then backwards block by block, the block's states and
-// factors again in registers.  Channels are summed over a CTA in a fixed order and leave
-// as partial sums, which (4) adds up.
+// Three kernels.  (1) per segment of tokens, walking forward: the state at each tile's start, from
+// a zero start, and the gradient at the segment's start from a zero end; (2) joins the
+// segments; (3) per segment, walking backward tile by tile with the gradient in registers:
+// the states at every block of TB tokens, then block by block the states again, in registers,
+// and the gradients.  Channels and tokens are summed in a fixed order: over a thread's channels,
+// its warp, its CTA, then as partial sums, which (4) adds up.
 #include <limits.h>
 
 #include "selective.cuh"
@@ -22,384 +23,606 @@
 namespace {
 using namespace s4sel;
 
-template <int LPC_, int SPT_, int CPT_>
+template <int LPC_, int SPT_>
 struct Geo {
-  static constexpr int LPC = LPC_, SPT = SPT_, CPT = CPT_;
-  static constexpr int NP = LPC * SPT, SLOTS = kThreads / LPC, HB = SLOTS * CPT;
-  static constexpr int TC = 32, TB = 4;                // tokens of a tile, of a block in registers
-  static constexpr int CELLS = TC * HB / kThreads;     // (token, channel) cells a thread stages
-  static constexpr int WARPS = kThreads / 32;
-  // shared memory in floats: cells [TC][HB][4] | B [TC][NP] | C [TC][NP] | block states | sums of dB, dC
-  static constexpr int B0 = 4 * TC * HB, C0 = B0 + TC * NP, S0 = C0 + TC * NP;
-  static constexpr int R0 = S0 + (TC / TB) * kThreads * CPT * SPT;
-  static constexpr int END = R0 + WARPS * TB * 2 * NP;
-  static constexpr int kSegBytes = 4 * (S0), kBytes = 4 * END;
+  static constexpr int LPC = LPC_, SPT = SPT_, NP = LPC * SPT, CPT = 2, SLOTS = 32 / LPC;
+  static constexpr int CH = SLOTS * CPT;                 // channels of a warp
+  static constexpr int WARPS = kThreads / 32, HB = WARPS * CH;  // and of a CTA
+  static constexpr int TC = LPC == 1 ? 8 : 16, TB = 4;   // tokens of a tile, of a block in registers
+  static constexpr int OWN = TC / 4 * kOwn<LPC>;         // tokens of a tile that a lane stages and finishes
+  // shared memory in floats: cells [TC][WARPS * SLOTS][2][4] | B, C [TC][NP] | states at blocks | sums of dB, dC
+  static constexpr int B0 = TC * WARPS * SLOTS * 8, C0 = B0 + TC * NP, S0 = C0 + TC * NP;
+  static constexpr int R0 = S0 + TC / TB * kThreads * CPT * SPT, END = R0 + WARPS * TB * 2 * NP;
+  static constexpr int kBytes = 4 * END;
+  // (1): a warp's tile of 4 tokens: steps, inputs, dyp [4][SLOTS][6 of 8] | B, C [4][NP]
+  static constexpr int EB = 4 * SLOTS * 8, EC = EB + 4 * NP, EEND = EC + 4 * NP;
+  static constexpr int kEndsBytes = 4 * EEND * WARPS;
+  static constexpr int VECS = 4 * NP / 32;               // elements of B, of C that a lane stages there
 };
 
 struct Work {
   int tiles, seg_tiles, segs;  // tiles of TC tokens, per segment, segments
-  int blocks;                  // channel blocks
-  float *s_tile, *g_tile;      // [batch][tiles][H][N]: state at a tile's start, gradient at its end
-  float *d_before, *d_after;   // [batch][tiles][H]: step sums from the segment's start / to its end
-  float *s_seg, *g_seg;        // [batch][segs][H][N]: the segment's end values, then its start values
+  int blocks;                  // CTAs over the channels
+  float *s_tile, *d_before;    // [batch][tiles][H][N], [batch][tiles][H]: state and step sum at a tile's start
+  float *s_seg, *g_seg;        // [batch][segs][H][N]: a segment's ends from zero, then its corrections
   float *d_seg;                // [batch][segs][H]
-  float *part_h;               // [batch * tiles][H][N + 2]: dA, dD, ddt_bias
+  float *part_h;               // [batch * segs][H][N + 2]: dA, dD, ddt_bias
   float *part_bc;              // [blocks][batch][L][2 NP]
 };
 
-// The cells of a tile: step, x, dyp and dy silu'(z) of (token, channel), zeros beyond the
-// sequence; softplus and gate are evaluated here, once.
-template <typename T, typename G>
-__device__ __forceinline__ void stage_cells(float4* cells, const s4_selective_bwd_args& a, const Chan& c, int b, int tb,
-                                            int len, bool vec) {
-  constexpr int HB = G::HB;
-  constexpr int V0 = 16 / (int)sizeof(T), V1 = V0 < HB ? V0 : HB, V = V1 < G::CELLS ? V1 : G::CELLS;
-  const T* x = static_cast<const T*>(a.x.p) + b * a.x.batch;
-  const T* dt = static_cast<const T*>(a.dt.p) + b * a.dt.batch;
-  const T* z = a.z.p ? static_cast<const T*>(a.z.p) + b * a.z.batch : nullptr;
-  const T* dy = static_cast<const T*>(a.dy.p) + b * a.dy.batch;
-#pragma unroll
-  for (int k = 0; k < G::CELLS / V; ++k) {
-    const int cell = (k * kThreads + threadIdx.x) * V, t = tb + cell / HB, hl = cell % HB, h = c.h0 + hl;
-    const int n = c.hend - h;
-    if (t < len && n > 0 && S4_IN(t, a.L) && S4_IN(h, a.H)) {
-      float xv[V], dv[V], zv[V], gv[V];
-      ld_f<T, V>(x + t * a.x.row + h, n, vec, xv);
-      ld_f<T, V>(dt + t * a.dt.row + h, n, vec, dv);
-      ld_f<T, V>(dy + t * a.dy.row + h, n, vec, gv);
-      if (z) ld_f<T, V>(z + t * a.z.row + h, n, vec, zv);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float d = dv[i], dyp = gv[i], dzf = 0.f;
-        if (a.dt_bias && i < n) d += a.dt_bias[h + i];
-        if (a.softplus) d = softplus(d);
-        if (z) {
-          dzf = gv[i] * silu_grad(zv[i]);
-          dyp = gv[i] * silu(zv[i]);
-        }
-        cells[cell + i] = i < n ? make_float4(d, xv[i], dyp, dzf) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) cells[cell + i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+// What a lane reads of one token and its 2 channels.
+template <typename T>
+struct Cell {
+  Pack<T, 2> x, dt, z, dy;
+};
+template <typename T, bool WHOLE>
+__device__ __forceinline__ Cell<T> ld_cell(const s4_selective_bwd_args& a, const T* x, const T* dt, const T* z, const T* dy,
+                                           long long t, int n, bool vec) {
+  Cell<T> c;
+  if (WHOLE) {
+    c.x = ld_whole<T, 2>(x + t * a.x.row);
+    c.dt = ld_whole<T, 2>(dt + t * a.dt.row);
+    c.dy = ld_whole<T, 2>(dy + t * a.dy.row);
+    if (z) c.z = ld_whole<T, 2>(z + t * a.z.row);
+  } else {
+    c.x = ld_pack<T, 2>(x + t * a.x.row, n, vec);
+    c.dt = ld_pack<T, 2>(dt + t * a.dt.row, n, vec);
+    c.dy = ld_pack<T, 2>(dy + t * a.dy.row, n, vec);
+    if (z) c.z = ld_pack<T, 2>(z + t * a.z.row, n, vec);
+  }
+  return c;
+}
+// Step sizes, inputs, dyp and dy silu'(z) of a cell.
+template <typename T>
+__device__ __forceinline__ void eval_cell(const Cell<T>& c, bool gate, bool soft, float2 bias, float2& d, float2& x,
+                                          float2& p, float2& zf) {
+  d = add2(make_float2(c.dt.get(0), c.dt.get(1)), bias);
+  if (soft) d = softplus2(d);
+  x = make_float2(c.x.get(0), c.x.get(1));
+  p = make_float2(c.dy.get(0), c.dy.get(1));
+  zf = make_float2(0.f, 0.f);
+  if (gate) {
+    const float2 z = make_float2(c.z.get(0), c.z.get(1));
+    const float2 s = make_float2(sigmoid(z.x), sigmoid(z.y));
+    // silu = z s, silu' = s + silu (1 - s)
+    const float2 q = mul2(z, s);
+    zf = mul2(p, make_float2(fmaf(q.x, 1.f - s.x, s.x), fmaf(q.y, 1.f - s.y, s.y)));
+    p = mul2(p, q);
   }
 }
 
-// (1) A segment's tiles in order: the state at each tile's start (from zero at the segment's
-// start), and each tile's own contribution to the gradient at its start,
-// R = sum_t (prod_{j<=t} a_j) C_t dyp_t; then backwards over the tiles the gradient
-// that reaches each tile's end from the segment's later tiles.
-template <typename T, typename G>
-__global__ void __launch_bounds__(kThreads) selective_ends_kernel(s4_selective_bwd_args a, Work w, bool vec, St st) {
-  constexpr int LPC = G::LPC, SPT = G::SPT, CPT = G::CPT, NP = G::NP, HB = G::HB, TC = G::TC;
+// SPT states of a channel, as pairs; the states beyond N as zeros.
+template <int SPT>
+__device__ __forceinline__ void ld_states(float2 (&v)[SPT / 2], const float* p, int n, bool vec) {
+  float f[SPT];
+  ld_f<float, SPT>(p, n, vec, f);
+#pragma unroll
+  for (int i = 0; i < SPT / 2; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+}
+template <int SPT>
+__device__ __forceinline__ void st_states(float* p, int n, bool vec, const float2 (&v)[SPT / 2]) {
+  float f[SPT];
+#pragma unroll
+  for (int i = 0; i < SPT / 2; ++i) {
+    f[2 * i] = v[i].x;
+    f[2 * i + 1] = v[i].y;
+  }
+  st_f<float, SPT>(p, n, vec, f);
+}
+
+// A warp's task and its lane's place in it.
+template <typename G>
+struct Place {
+  int lane, slot, n0, h, nh, ns;  // lane of the channels, slot, first state, first channel, channels there are / it stages
+  __device__ __forceinline__ Place(int h0, int hend) {
+    const int wl = threadIdx.x & 31;
+    lane = wl % G::LPC;
+    slot = wl / G::LPC;
+    n0 = lane * G::SPT;
+    h = h0 + slot * G::CPT;
+    nh = hend - h;
+    ns = G::LPC > 4 && lane >= 4 ? 0 : nh;
+  }
+  // the k-th token of a tile that this lane owns
+  __device__ __forceinline__ int token(int k) const {
+    return k / kOwn<G::LPC> * 4 + own_token<G::LPC>(lane, k % kOwn<G::LPC>);
+  }
+};
+
+// (1) A warp per channel block and segment, in tiles of 4 tokens read ahead by one.  The gradient
+// at the segment's start is R = sum_t (prod_{j<=t} a_j) C_t dyp_t.
+template <typename T, typename G, bool WHOLE>
+__global__ void __launch_bounds__(kThreads, 4) selective_ends_kernel(s4_selective_bwd_args a, Work w, bool vec, bool vecbc,
+                                                                     bool vecn, St st) {
+  constexpr int LPC = G::LPC, SPT = G::SPT, CPT = G::CPT, NP = G::NP, CH = G::CH, TT = 4, OWN = kOwn<LPC>;
+  constexpr int V0 = 16 / (int)sizeof(T), VB = V0 < G::VECS ? V0 : G::VECS, NB = G::VECS / VB;
   extern __shared__ __align__(16) float smem[];
-  float4* cells = reinterpret_cast<float4*>(smem);
-  float(*sb)[NP] = reinterpret_cast<float(*)[NP]>(smem + G::B0);
-  float(*sc)[NP] = reinterpret_cast<float(*)[NP]>(smem + G::C0);
+  float* mine = smem + threadIdx.x / 32 * G::EEND;
+  float4(*sd)[G::SLOTS][2] = reinterpret_cast<float4(*)[G::SLOTS][2]>(mine);
+  float(*sb)[NP] = reinterpret_cast<float(*)[NP]>(mine + G::EB);
+  float(*sc)[NP] = reinterpret_cast<float(*)[NP]>(mine + G::EC);
   record_gen(st);
-  const int b = blockIdx.z, seg = blockIdx.y;
-  const Chan c = chan_of<HB>(blockIdx.x, a.H / a.G);
+  const int b = blockIdx.y, wl = threadIdx.x & 31, blocks = chan_blocks<CH>(a.H, a.G);
   const Seq q = seq_of(a.lengths, nullptr, b, a.L, 0, st);
-  const int lane = threadIdx.x % LPC, slot = threadIdx.x / LPC, n0 = lane * SPT;
+  const long long task = (long long)blockIdx.x * G::WARPS + threadIdx.x / 32;
+  if (task >= (long long)blocks * w.segs) return;
+  const int seg = (int)(task / blocks);
+  const Chan c = chan_of<CH>((int)(task % blocks), a.H / a.G);
+  const Place<G> p(c.h0, c.hend);
+  const int lane = p.lane, slot = p.slot, n0 = p.n0, h = p.h, nh = p.nh, nn = a.N - n0;
+  const T* x = static_cast<const T*>(a.x.p) + b * a.x.batch + h;
+  const T* dt = static_cast<const T*>(a.dt.p) + b * a.dt.batch + h;
+  const T* z = a.z.p ? static_cast<const T*>(a.z.p) + b * a.z.batch + h : nullptr;
+  const T* dy = static_cast<const T*>(a.dy.p) + b * a.dy.batch + h;
   const T* B = static_cast<const T*>(a.B.p) + b * a.B.batch + c.g * a.B_group;
   const T* C = static_cast<const T*>(a.C.p) + b * a.C.batch + c.g * a.C_group;
-  const int first = seg * w.seg_tiles, last = min(w.tiles, first + w.seg_tiles);
-  float A[CPT][SPT], s[CPT][SPT], sum[CPT];
-  bool in[CPT][SPT];
+  const int t0 = seg * w.seg_tiles * G::TC, t1 = min(a.L, t0 + w.seg_tiles * G::TC), live = min(t1, q.len);
+  float2 A[CPT][SPT / 2], s[CPT][SPT / 2], P[CPT][SPT / 2], R[CPT][SPT / 2], sum = make_float2(0.f, 0.f);
+  const float2 bias = make_float2(a.dt_bias && nh > 0 ? a.dt_bias[h] : 0.f, a.dt_bias && nh > 1 ? a.dt_bias[h + 1] : 0.f);
 #pragma unroll
   for (int j = 0; j < CPT; ++j) {
-    const int h = c.h0 + slot * CPT + j;
-    sum[j] = 0.f;
+    const int n = j < nh ? nn : 0;
+    ld_states<SPT>(A[j], a.A + (long long)(h + j) * a.N + n0, n, vecn);
+    if (seg == 0 && a.state0)
+      ld_states<SPT>(s[j], a.state0 + ((long long)b * a.H + h + j) * a.N + n0, n, vecn);
 #pragma unroll
-    for (int i = 0; i < SPT; ++i) {
-      in[j][i] = h < c.hend && n0 + i < a.N;
-      A[j][i] = in[j][i] ? a.A[(long long)h * a.N + n0 + i] * kLog2e : 0.f;
-      s[j][i] = 0.f;
-      if (in[j][i] && seg == 0 && a.state0) s[j][i] = a.state0[((long long)b * a.H + h) * a.N + n0 + i];
+    for (int i = 0; i < SPT / 2; ++i) {
+      A[j][i] = mul2(A[j][i], make_float2(kLog2e, kLog2e));
+      if (!(seg == 0 && a.state0)) s[j][i] = make_float2(0.f, 0.f);
+      P[j][i] = make_float2(1.f, 1.f);
+      R[j][i] = make_float2(0.f, 0.f);
     }
   }
-  for (int tile = first; tile < last; ++tile) {
-    const int tb = tile * TC;
-    const long long row = ((long long)b * w.tiles + tile) * a.H;
-    float P[CPT][SPT], R[CPT][SPT], before[CPT];
+  Cell<T> next[OWN];
+  Pack<T, VB> nb[NB], nc[NB];
+  const auto fetch = [&](int tb) {
+    const bool whole = WHOLE && tb + TT <= live;
 #pragma unroll
-    for (int j = 0; j < CPT; ++j) {
-      const int h = c.h0 + slot * CPT + j;
-      before[j] = sum[j];
-#pragma unroll
-      for (int i = 0; i < SPT; ++i) {
-        P[j][i] = 1.f;
-        R[j][i] = 0.f;
-        if (in[j][i]) w.s_tile[(row + h) * a.N + n0 + i] = s[j][i];
-      }
-      if (lane == 0 && h < c.hend) w.d_before[row + h] = sum[j];
-    }
-    if (tb < q.len) {
-      __syncthreads();
-      stage_cells<T, G>(cells, a, c, b, tb, q.len, vec);
-      stage_vectors<T, TC, NP>(&sb[0][0], B, a.B.row, tb, q.len, a.N);
-      stage_vectors<T, TC, NP>(&sc[0][0], C, a.C.row, tb, q.len, a.N);
-      __syncthreads();
-#pragma unroll 4
-      for (int t = 0; t < TC; ++t) {
-#pragma unroll
-        for (int j = 0; j < CPT; ++j) {
-          const float4 d = cells[t * HB + slot * CPT + j];
-          const float dx = d.x * d.y;
-          sum[j] += d.x;
-#pragma unroll
-          for (int i = 0; i < SPT; ++i) {
-            const float f = ex2(d.x * A[j][i]);
-            s[j][i] = fmaf(f, s[j][i], dx * sb[t][n0 + i]);
-            P[j][i] *= f;
-            R[j][i] = fmaf(P[j][i], sc[t][n0 + i] * d.z, R[j][i]);
-          }
-        }
+    for (int k = 0; k < NB; ++k) {
+      const int i = (k * 32 + wl) * VB, t = tb + i / NP;
+      if (whole) {
+        nb[k] = ld_whole<T, VB>(B + t * a.B.row + i % NP);
+        nc[k] = ld_whole<T, VB>(C + t * a.C.row + i % NP);
+      } else {
+        const int n = t < live && S4_IN(t, a.L) ? a.N - i % NP : 0;
+        nb[k] = ld_pack<T, VB>(B + t * a.B.row + i % NP, n, vecbc);
+        nc[k] = ld_pack<T, VB>(C + t * a.C.row + i % NP, n, vecbc);
       }
     }
-    // the tile's own R now, the gradient at its end below
 #pragma unroll
-    for (int j = 0; j < CPT; ++j) {
-      const int h = c.h0 + slot * CPT + j;
-#pragma unroll
-      for (int i = 0; i < SPT; ++i)
-        if (in[j][i]) w.g_tile[(row + h) * a.N + n0 + i] = R[j][i];
-      if (lane == 0 && h < c.hend) w.d_after[row + h] = sum[j] - before[j];
+    for (int k = 0; k < OWN; ++k) {
+      const int t = tb + own_token<LPC>(lane, k);
+      next[k] = whole ? ld_cell<T, true>(a, x, dt, z, dy, t, 2, true)
+                      : ld_cell<T, false>(a, x, dt, z, dy, t, t < live && S4_IN(t, a.L) ? p.ns : 0, vec);
     }
-  }
-  float g[CPT][SPT], after[CPT];
+  };
+  if (t0 < live) fetch(t0);
+  for (int tb = t0; tb < t1; tb += TT) {
+    if (tb % G::TC == 0) {  // a tile of (3) starts
+      const long long row = ((long long)b * w.tiles + tb / G::TC) * a.H + h;
+      float2 all = sum;  // over the lanes that own tokens
 #pragma unroll
-  for (int j = 0; j < CPT; ++j) {
-    const int h = c.h0 + slot * CPT + j;
-    after[j] = 0.f;
+      for (int o = 1; o < (LPC < 4 ? LPC : 4); o <<= 1) {
+        all.x += __shfl_xor_sync(0xffffffffu, all.x, o);
+        all.y += __shfl_xor_sync(0xffffffffu, all.y, o);
+      }
 #pragma unroll
-    for (int i = 0; i < SPT; ++i) {
-      g[j][i] = 0.f;
-      if (in[j][i] && seg == w.segs - 1 && a.dstate) g[j][i] = a.dstate[((long long)b * a.H + h) * a.N + n0 + i];
+      for (int j = 0; j < CPT; ++j) {
+        if (j >= nh) continue;
+        st_states<SPT>(w.s_tile + (row + j) * a.N + n0, nn, vecn, s[j]);
+        if (lane == 0) w.d_before[row + j] = j ? all.y : all.x;
+      }
+      if (tb >= live) continue;
     }
-  }
-  __syncthreads();  // d_after, written by one lane, is read by all that share the channel
-  for (int tile = last - 1; tile >= first; --tile) {
-    const long long row = ((long long)b * w.tiles + tile) * a.H;
-    float own[CPT];
+    if (tb >= live) continue;
+    __syncwarp();  // the tile before has been read
 #pragma unroll
-    for (int j = 0; j < CPT; ++j) {
-      const int h = c.h0 + slot * CPT + j;
-      own[j] = h < c.hend ? w.d_after[row + h] : 0.f;
+    for (int k = 0; k < OWN; ++k) {
+      float2 d, xv, pv, zf;
+      eval_cell<T>(next[k], z != nullptr, a.softplus, bias, d, xv, pv, zf);
+      const int t = own_token<LPC>(lane, k);
+      if (tb + t >= live) d = make_float2(0.f, 0.f);  // padding keeps the state
+      sum = add2(sum, d);
+      const float2 dx = mul2(d, xv);
+      if (LPC <= 4 || lane < 4) {
+        sd[t][slot][0] = make_float4(d.x, d.y, dx.x, dx.y);
+        *reinterpret_cast<float2*>(&sd[t][slot][1]) = pv;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int i = (k * 32 + wl) * VB;
+#pragma unroll
+      for (int e = 0; e < VB; ++e) {
+        (&sb[0][0])[i + e] = nb[k].get(e);
+        (&sc[0][0])[i + e] = nc[k].get(e);
+      }
     }
     __syncwarp();
+    if (tb + TT < live) fetch(tb + TT);
 #pragma unroll
-    for (int j = 0; j < CPT; ++j) {
-      const int h = c.h0 + slot * CPT + j;
+    for (int t = 0; t < TT; ++t) {
+      const float4 d = sd[t][slot][0];
+      const float2 pv = *reinterpret_cast<const float2*>(&sd[t][slot][1]);
+      const float2 dd[CPT] = {make_float2(d.x, d.x), make_float2(d.y, d.y)};
+      const float2 xx[CPT] = {make_float2(d.z, d.z), make_float2(d.w, d.w)};
+      const float2 pp[CPT] = {make_float2(pv.x, pv.x), make_float2(pv.y, pv.y)};
 #pragma unroll
-      for (int i = 0; i < SPT; ++i) {
-        if (!in[j][i]) continue;
-        float* p = w.g_tile + (row + h) * a.N + n0 + i;
-        const float r = *p;
-        *p = g[j][i];
-        g[j][i] = fmaf(ex2(own[j] * A[j][i]), g[j][i], r);
+      for (int i = 0; i < SPT / 2; i += 2) {
+        const float4 b4 = *reinterpret_cast<const float4*>(&sb[t][n0 + 2 * i]);
+        const float4 c4 = *reinterpret_cast<const float4*>(&sc[t][n0 + 2 * i]);
+        const float2 bv[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
+        const float2 cv[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int j = 0; j < CPT; ++j) {
+            const float2 f = ex2(mul2(dd[j], A[j][i + e]));
+            s[j][i + e] = fma2(f, s[j][i + e], mul2(xx[j], bv[e]));
+            P[j][i + e] = mul2(P[j][i + e], f);
+            R[j][i + e] = fma2(P[j][i + e], mul2(pp[j], cv[e]), R[j][i + e]);
+          }
       }
-      if (lane == 0 && h < c.hend) w.d_after[row + h] = after[j];
-      after[j] += own[j];
     }
   }
 #pragma unroll
-  for (int j = 0; j < CPT; ++j) {
-    const int h = c.h0 + slot * CPT + j;
-    const long long row = ((long long)b * w.segs + seg) * a.H;
+  for (int o = 1; o < (LPC < 4 ? LPC : 4); o <<= 1) {
+    sum.x += __shfl_xor_sync(0xffffffffu, sum.x, o);
+    sum.y += __shfl_xor_sync(0xffffffffu, sum.y, o);
+  }
+  const long long row = ((long long)b * w.segs + seg) * a.H + h;
 #pragma unroll
-    for (int i = 0; i < SPT; ++i) {
-      if (!in[j][i]) continue;
-      if (w.segs > 1) {
-        w.s_seg[(row + h) * a.N + n0 + i] = s[j][i];
-        w.g_seg[(row + h) * a.N + n0 + i] = g[j][i];
-      } else if (a.dstate0) {
-        a.dstate0[((long long)b * a.H + h) * a.N + n0 + i] = g[j][i];
-      }
-    }
-    if (w.segs > 1 && lane == 0 && h < c.hend) w.d_seg[row + h] = sum[j];
+  for (int j = 0; j < CPT; ++j) {
+    if (j >= nh) continue;
+    st_states<SPT>(w.s_seg + (row + j) * a.N + n0, nn, vecn, s[j]);
+    st_states<SPT>(w.g_seg + (row + j) * a.N + n0, nn, vecn, R[j]);
+    if (lane == 0) w.d_seg[row + j] = j ? sum.y : sum.x;
   }
 }
 
-// (2) Joins the segments: the correction of each segment's states at its start (its predecessors'
-// end state) and of its gradients at its end.
-__global__ void __launch_bounds__(256) selective_joins_kernel(s4_selective_bwd_args a, Work w) {
+// (2) Joins the segments: what to add to each segment's states for its predecessors, times
+// 2^(A steps since its start), and the gradient at its end.  A thread per state, 8 segments'
+// loads under way at a time.
+__global__ void __launch_bounds__(128) selective_joins_kernel(s4_selective_bwd_args a, Work w) {
   const int b = blockIdx.y;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, HN = (long long)a.H * a.N;
+  const long long i = (long long)blockIdx.x * 128 + threadIdx.x, HN = (long long)a.H * a.N;
   if (i >= HN) return;
-  const int h = (int)(i / a.N);
   const float A = a.A[i] * kLog2e;
-  float s = 0.f, g = 0.f;
-  for (int k = 0; k < w.segs; ++k) {
-    const long long row = (long long)b * w.segs + k;
-    const float end = w.s_seg[row * HN + i];
-    w.s_seg[row * HN + i] = s;
-    s = fmaf(ex2(w.d_seg[row * a.H + h] * A), s, end);
-  }
-  for (int k = w.segs - 1; k >= 0; --k) {
-    const long long row = (long long)b * w.segs + k;
-    const float r = w.g_seg[row * HN + i];
-    w.g_seg[row * HN + i] = g;
-    g = fmaf(ex2(w.d_seg[row * a.H + h] * A), g, r);
+  float* sp = w.s_seg + (long long)b * w.segs * HN + i;
+  float* gp = w.g_seg + (long long)b * w.segs * HN + i;
+  const float* dp = w.d_seg + (long long)b * w.segs * a.H + i / a.N;
+  float s = 0.f, g = a.dstate ? a.dstate[(long long)b * HN + i] : 0.f;
+  for (int k0 = 0; k0 < w.segs; k0 += 8) {
+    float sv[8], gv[8], ds[8], dg[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int k = k0 + e, r = w.segs - 1 - k;
+      const bool in = k < w.segs;
+      sv[e] = in ? sp[k * HN] : 0.f;
+      gv[e] = in ? gp[r * HN] : 0.f;
+      ds[e] = in ? dp[(long long)k * a.H] : 0.f;
+      dg[e] = in ? dp[(long long)r * a.H] : 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int k = k0 + e, r = w.segs - 1 - k;
+      if (k >= w.segs) break;
+      sp[k * HN] = s;
+      gp[r * HN] = g;
+      s = fmaf(ex2(ds[e] * A), s, sv[e]);
+      g = fmaf(ex2(dg[e] * A), g, gv[e]);
+    }
   }
   if (a.dstate0) a.dstate0[(long long)b * HN + i] = g;
 }
 
-// (3) One tile's gradients.
-template <typename T, typename G>
-__global__ void __launch_bounds__(kThreads) selective_tile_bwd_kernel(s4_selective_bwd_args a, Work w, bool vec, St st) {
-  constexpr int LPC = G::LPC, SPT = G::SPT, CPT = G::CPT, NP = G::NP, HB = G::HB, TC = G::TC, TB = G::TB;
+// 16 values per lane summed over the warp's channel slots: halves are exchanged over the lanes'
+// highest bit first, so that a lane comes to hold 16 / SLOTS of the sums (one, twice, with 32
+// slots), the k-th being value kept(k).
+template <int LPC>
+struct SumSlots {
+  static constexpr int SLOTS = 32 / LPC, KEEP = SLOTS >= 16 ? 1 : 16 / SLOTS;
+  static __device__ __forceinline__ void run(float (&r)[16], int wl) {
+    int m = 8;
+#pragma unroll
+    for (int o = 16; o >= LPC; o >>= 1) {
+      if (m == 0) {
+        r[0] += __shfl_xor_sync(0xffffffffu, r[0], o);
+        continue;
+      }
+      const bool up = wl & o;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i >= m) continue;
+        const float keep = up ? r[i + m] : r[i], send = up ? r[i] : r[i + m];
+        r[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+      }
+      m >>= 1;
+    }
+  }
+  static __device__ __forceinline__ int kept(int wl, int k) {
+    const int slot = wl / LPC;
+    return SLOTS == 32 ? slot / 2 : slot * KEEP + k;
+  }
+};
+
+// (1 - e^-d) / d is the softplus' derivative over the softplus d.  For d < 1/2 a polynomial, the
+// interpolation at the Chebyshev points of degree 4 (relative error 1e-7), which keeps the
+// relative precision that 1 - e^-d loses there.
+__device__ __forceinline__ float softplus_slope(float d) {
+  float p = 0.006785358767956495f;
+  p = fmaf(p, d, -0.041015710681676865f);
+  p = fmaf(p, d, 0.16655270755290985f);
+  p = fmaf(p, d, -0.4999929666519165f);
+  p = fmaf(p, d, 0.9999999403953552f);
+  return d < 0.5f ? p * d : 1.f - ex2(-d * kLog2e);
+}
+
+// (3) A CTA per HB channels and segment.
+template <typename T, typename G, bool WHOLE>
+__global__ void __launch_bounds__(kThreads, 3) selective_tiles_kernel(s4_selective_bwd_args a, Work w, bool vec, bool vecbc,
+                                                                      bool vecn, St st) {
+  constexpr int LPC = G::LPC, SPT = G::SPT, CPT = G::CPT, NP = G::NP, CH = G::CH, TC = G::TC, TB = G::TB, OWN = G::OWN;
+  using Sum = SumSlots<LPC>;
   extern __shared__ __align__(16) float smem[];
-  float4* cells = reinterpret_cast<float4*>(smem);
+  float4(*cells)[G::WARPS * G::SLOTS][2] = reinterpret_cast<float4(*)[G::WARPS * G::SLOTS][2]>(smem);
   float(*sb)[NP] = reinterpret_cast<float(*)[NP]>(smem + G::B0);
   float(*sc)[NP] = reinterpret_cast<float(*)[NP]>(smem + G::C0);
-  float* keep = smem + G::S0;
+  float4* keep = reinterpret_cast<float4*>(smem + G::S0) + threadIdx.x;
   float(*red)[TB][2 * NP] = reinterpret_cast<float(*)[TB][2 * NP]>(smem + G::R0);
-  const int b = blockIdx.y, tile = blockIdx.x / w.blocks, block = blockIdx.x % w.blocks, tb = tile * TC;
-  const Chan c = chan_of<HB>(block, a.H / a.G);
+  const int b = blockIdx.y, seg = blockIdx.x / w.blocks, block = blockIdx.x % w.blocks;
+  const int wid = threadIdx.x / 32, wl = threadIdx.x & 31;
+  const Chan c = chan_of<G::HB>(block, a.H / a.G);
   const Seq q = seq_of(a.lengths, nullptr, b, a.L, 0, st);
-  const int lane = threadIdx.x % LPC, slot = threadIdx.x / LPC, n0 = lane * SPT, wid = threadIdx.x / 32;
-  const int wl = threadIdx.x & 31;
+  const Place<G> p(c.h0 + wid * CH, c.hend);
+  const int lane = p.lane, n0 = p.n0, h = p.h, nh = p.nh, nn = a.N - n0, cs = wid * G::SLOTS + p.slot;
+  const T* x = static_cast<const T*>(a.x.p) + b * a.x.batch + h;
+  const T* dt = static_cast<const T*>(a.dt.p) + b * a.dt.batch + h;
+  const T* z = a.z.p ? static_cast<const T*>(a.z.p) + b * a.z.batch + h : nullptr;
+  const T* dy = static_cast<const T*>(a.dy.p) + b * a.dy.batch + h;
   const T* B = static_cast<const T*>(a.B.p) + b * a.B.batch + c.g * a.B_group;
   const T* C = static_cast<const T*>(a.C.p) + b * a.C.batch + c.g * a.C_group;
-  const long long row = ((long long)b * w.tiles + tile) * a.H;
-  const int live = min(TC, q.len - tb);  // <= 0: a tile of padding
+  T* dxo = static_cast<T*>(a.dx.p) + b * a.dx.batch + h;
+  T* dto = static_cast<T*>(a.ddt.p) + b * a.ddt.batch + h;
+  T* dzo = z ? static_cast<T*>(a.dz.p) + b * a.dz.batch + h : nullptr;
+  const int first = seg * w.seg_tiles, last = min(w.tiles, first + w.seg_tiles);
 
-  float A[CPT][SPT], g[CPT][SPT], dA[CPT][SPT], dD[CPT], db[CPT], Dv[CPT];
-  float s0[CPT][SPT];
+  float2 A[CPT][SPT / 2], g[CPT][SPT / 2], dA[CPT][SPT / 2];
+  float2 dD = make_float2(0.f, 0.f), db = dD;
+  const float2 bias = make_float2(a.dt_bias && nh > 0 ? a.dt_bias[h] : 0.f, a.dt_bias && nh > 1 ? a.dt_bias[h + 1] : 0.f);
+  const float2 Dv = make_float2(a.D && nh > 0 ? a.D[h] : 0.f, a.D && nh > 1 ? a.D[h + 1] : 0.f);
+  const long long srow = ((long long)b * w.segs + seg) * a.H + h;
 #pragma unroll
   for (int j = 0; j < CPT; ++j) {
-    const int h = c.h0 + slot * CPT + j;
-    dD[j] = db[j] = 0.f;
-    Dv[j] = a.D && h < c.hend ? a.D[h] : 0.f;
-    const float before = w.segs > 1 && h < c.hend ? w.d_before[row + h] : 0.f;
-    const float after = w.segs > 1 && h < c.hend ? w.d_after[row + h] : 0.f;
+    const int n = j < nh ? nn : 0;
+    ld_states<SPT>(A[j], a.A + (long long)(h + j) * a.N + n0, n, vecn);
+    ld_states<SPT>(g[j], w.g_seg + (srow + j) * a.N + n0, n, vecn);
 #pragma unroll
-    for (int i = 0; i < SPT; ++i) {
-      const bool in = h < c.hend && n0 + i < a.N;
-      A[j][i] = in ? a.A[(long long)h * a.N + n0 + i] * kLog2e : 0.f;
-      dA[j][i] = g[j][i] = s0[j][i] = 0.f;
-      if (in && live > 0) {
-        s0[j][i] = w.s_tile[(row + h) * a.N + n0 + i];
-        g[j][i] = w.g_tile[(row + h) * a.N + n0 + i];
-        if (w.segs > 1) {
-          const long long at = (((long long)b * w.segs + tile / w.seg_tiles) * a.H + h) * a.N + n0 + i;
-          s0[j][i] = fmaf(ex2(before * A[j][i]), w.s_seg[at], s0[j][i]);
-          g[j][i] = fmaf(ex2(after * A[j][i]), w.g_seg[at], g[j][i]);
+    for (int i = 0; i < SPT / 2; ++i) {
+      A[j][i] = mul2(A[j][i], make_float2(kLog2e, kLog2e));
+      dA[j][i] = make_float2(0.f, 0.f);
+    }
+  }
+  for (int tile = last - 1; tile >= first; --tile) {
+    const int tb = tile * TC, live = min(TC, q.len - tb);  // <= 0: a tile of padding
+    float* bc = w.part_bc + (((long long)block * a.batch + b) * a.L + tb) * 2 * NP;
+    if (live <= 0) {
+      const float zero[2] = {};
+#pragma unroll 1
+      for (int k = 0; k < OWN; ++k) {
+        const int t = tb + p.token(k);
+        if (t >= a.L || p.ns <= 0) continue;
+        st_f<T, 2>(dxo + t * a.dx.row, p.ns, vec, zero);
+        st_f<T, 2>(dto + t * a.ddt.row, p.ns, vec, zero);
+        if (dzo) st_f<T, 2>(dzo + t * a.dz.row, p.ns, vec, zero);
+      }
+      for (int i = threadIdx.x; i < min(TC, a.L - tb) * 2 * NP; i += kThreads) bc[i] = 0.f;
+      continue;
+    }
+    __syncthreads();  // the tile after this one is done with shared memory
+    const bool whole = WHOLE && live == TC;
+#pragma unroll 4
+    for (int k = 0; k < OWN; ++k) {
+      const int t = p.token(k);
+      const bool on = t < live;
+      const Cell<T> cell = whole ? ld_cell<T, true>(a, x, dt, z, dy, tb + t, 2, true)
+                                 : ld_cell<T, false>(a, x, dt, z, dy, tb + t, on && S4_IN(tb + t, a.L) ? p.ns : 0, vec);
+      float2 d, xv, pv, zf;
+      eval_cell<T>(cell, z != nullptr, a.softplus, bias, d, xv, pv, zf);
+      if (!on) d = make_float2(0.f, 0.f);
+      if (LPC <= 4 || lane < 4) {
+        cells[t][cs][0] = make_float4(d.x, d.y, xv.x, xv.y);
+        cells[t][cs][1] = make_float4(pv.x, pv.y, zf.x, zf.y);
+      }
+    }
+    for (int i = threadIdx.x; i < TC * NP; i += kThreads) {
+      const int t = i / NP, n = i % NP;
+      const bool on = t < live && n < a.N && S4_IN(tb + t, a.L);
+      (&sb[0][0])[i] = on ? to_f(B[(tb + t) * a.B.row + n]) : 0.f;
+      (&sc[0][0])[i] = on ? to_f(C[(tb + t) * a.C.row + n]) : 0.f;
+    }
+    // the state at the tile's start: from the segment's zero start, and what came before it
+    {
+      float2 s[CPT][SPT / 2];
+      const long long row = ((long long)b * w.tiles + tile) * a.H + h;
+#pragma unroll
+      for (int j = 0; j < CPT; ++j) {
+        const int n = j < nh ? nn : 0;
+        ld_states<SPT>(s[j], w.s_tile + (row + j) * a.N + n0, n, vecn);
+        if (seg > 0) {
+          float2 e[SPT / 2];
+          ld_states<SPT>(e, w.s_seg + (srow + j) * a.N + n0, n, vecn);
+          const float before = j < nh ? w.d_before[row + j] : 0.f;
+#pragma unroll
+          for (int i = 0; i < SPT / 2; ++i)
+            s[j][i] = fma2(ex2(mul2(make_float2(before, before), A[j][i])), e[i], s[j][i]);
+        }
+      }
+      __syncthreads();
+      // and at the start of each block
+#pragma unroll 1
+      for (int k = 0;; ++k) {
+#pragma unroll
+        for (int i = 0; i < SPT / 2; ++i)
+          keep[(k * SPT / 2 + i) * kThreads] = make_float4(s[0][i].x, s[0][i].y, s[1][i].x, s[1][i].y);
+        if (k + 1 == TC / TB) break;
+#pragma unroll
+        for (int u = 0; u < TB; ++u) {
+          const int t = k * TB + u;
+          const float4 d = cells[t][cs][0];
+          const float2 dd[CPT] = {make_float2(d.x, d.x), make_float2(d.y, d.y)};
+          const float2 dx = mul2(make_float2(d.x, d.y), make_float2(d.z, d.w));
+          const float2 xx[CPT] = {make_float2(dx.x, dx.x), make_float2(dx.y, dx.y)};
+#pragma unroll
+          for (int i = 0; i < SPT / 2; i += 2) {
+            const float4 b4 = *reinterpret_cast<const float4*>(&sb[t][n0 + 2 * i]);
+            const float2 bv[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int j = 0; j < CPT; ++j)
+                s[j][i + e] = fma2(ex2(mul2(dd[j], A[j][i + e])), s[j][i + e], mul2(xx[j], bv[e]));
+          }
         }
       }
     }
-  }
-  if (live > 0) {
-    stage_cells<T, G>(cells, a, c, b, tb, q.len, vec);
-    stage_vectors<T, TC, NP>(&sb[0][0], B, a.B.row, tb, q.len, a.N);
-    stage_vectors<T, TC, NP>(&sc[0][0], C, a.C.row, tb, q.len, a.N);
-    __syncthreads();
-    // states at the start of each block
-    {
-      float s[CPT][SPT];
-#pragma unroll
-      for (int j = 0; j < CPT; ++j)
-#pragma unroll
-        for (int i = 0; i < SPT; ++i) s[j][i] = s0[j][i];
-      for (int k = 0; k < TC / TB; ++k) {
-#pragma unroll
-        for (int j = 0; j < CPT; ++j)
-#pragma unroll
-          for (int i = 0; i < SPT; ++i) keep[((k * CPT + j) * SPT + i) * kThreads + threadIdx.x] = s[j][i];
-        if (k + 1 == TC / TB) break;
-#pragma unroll
-        for (int t = k * TB; t < k * TB + TB; ++t)
-#pragma unroll
-          for (int j = 0; j < CPT; ++j) {
-            const float4 d = cells[t * HB + slot * CPT + j];
-#pragma unroll
-            for (int i = 0; i < SPT; ++i)
-              s[j][i] = fmaf(ex2(d.x * A[j][i]), s[j][i], d.x * d.y * sb[t][n0 + i]);
-          }
-      }
-    }
+#pragma unroll 1
     for (int k = TC / TB - 1; k >= 0; --k) {
-      float s[TB + 1][CPT][SPT], f[TB][CPT][SPT], vy[CPT][TB], vu[CPT][TB], vw[CPT][TB];
+      float2 s[TB][CPT][SPT / 2];  // before each token
+      float vy[CPT][TB], vu[CPT][TB], vw[CPT][TB];
 #pragma unroll
-      for (int j = 0; j < CPT; ++j)
-#pragma unroll
-        for (int i = 0; i < SPT; ++i) s[0][j][i] = keep[((k * CPT + j) * SPT + i) * kThreads + threadIdx.x];
+      for (int i = 0; i < SPT / 2; ++i) {
+        const float4 v = keep[(k * SPT / 2 + i) * kThreads];
+        s[0][0][i] = make_float2(v.x, v.y);
+        s[0][1][i] = make_float2(v.z, v.w);
+      }
+      // forward: the block's states, y, and dC
+      float r[16];
 #pragma unroll
       for (int u = 0; u < TB; ++u) {
         const int t = k * TB + u;
+        const float4 d = cells[t][cs][0];
+        const float2 pv = *reinterpret_cast<const float2*>(&cells[t][cs][1]);
+        const float2 dd[CPT] = {make_float2(d.x, d.x), make_float2(d.y, d.y)};
+        const float2 dx = mul2(make_float2(d.x, d.y), make_float2(d.z, d.w));
+        const float2 xx[CPT] = {make_float2(dx.x, dx.x), make_float2(dx.y, dx.y)};
+        const float2 pp[CPT] = {make_float2(pv.x, pv.x), make_float2(pv.y, pv.y)};
+        float2 y[CPT];
 #pragma unroll
-        for (int j = 0; j < CPT; ++j) {
-          const float4 d = cells[t * HB + slot * CPT + j];
-          float y = 0.f;
+        for (int i = 0; i < SPT / 2; i += 2) {
+          const float4 b4 = *reinterpret_cast<const float4*>(&sb[t][n0 + 2 * i]);
+          const float4 c4 = *reinterpret_cast<const float4*>(&sc[t][n0 + 2 * i]);
+          const float2 bv[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
+          const float2 cv[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
 #pragma unroll
-          for (int i = 0; i < SPT; ++i) {
-            f[u][j][i] = ex2(d.x * A[j][i]);
-            s[u + 1][j][i] = fmaf(f[u][j][i], s[u][j][i], d.x * d.y * sb[t][n0 + i]);
-            y = fmaf(sc[t][n0 + i], s[u + 1][j][i], y);
+          for (int e = 0; e < 2; ++e) {
+            float2 rc;
+#pragma unroll
+            for (int j = 0; j < CPT; ++j) {
+              const float2 now = fma2(ex2(mul2(dd[j], A[j][i + e])), s[u][j][i + e], mul2(xx[j], bv[e]));
+              if (u + 1 < TB) s[u + 1][j][i + e] = now;
+              y[j] = i + e ? fma2(cv[e], now, y[j]) : mul2(cv[e], now);
+              rc = j ? fma2(pp[j], now, rc) : mul2(pp[j], now);
+            }
+            r[(u & 1) * SPT + 2 * (i + e)] = rc.x;
+            r[(u & 1) * SPT + 2 * (i + e) + 1] = rc.y;
           }
-          vy[j][u] = y;
+        }
+#pragma unroll
+        for (int j = 0; j < CPT; ++j) vy[j][u] = y[j].x + y[j].y;
+        if (u & 1) {  // two tokens' dC
+          Sum::run(r, wl);
+#pragma unroll
+          for (int e = 0; e < Sum::KEEP; ++e) {
+            const int v = Sum::kept(wl, e);
+            red[wid][u - 1 + v / SPT][NP + n0 + v % SPT] = r[e];
+          }
         }
       }
+      // backward: the gradients of the states, dB, u, w, dA
 #pragma unroll
       for (int u = TB - 1; u >= 0; --u) {
         const int t = k * TB + u;
-        float r[2 * SPT];  // dB, dC of this thread's states, over its channels
+        const float4 d = cells[t][cs][0];
+        const float2 pv = *reinterpret_cast<const float2*>(&cells[t][cs][1]);
+        const float2 dd[CPT] = {make_float2(d.x, d.x), make_float2(d.y, d.y)};
+        const float2 dx = mul2(make_float2(d.x, d.y), make_float2(d.z, d.w));
+        const float2 xx[CPT] = {make_float2(dx.x, dx.x), make_float2(dx.y, dx.y)};
+        const float2 pp[CPT] = {make_float2(pv.x, pv.x), make_float2(pv.y, pv.y)};
+        float2 uu[CPT], ww[CPT];
 #pragma unroll
-        for (int i = 0; i < 2 * SPT; ++i) r[i] = 0.f;
+        for (int i = 0; i < SPT / 2; i += 2) {
+          const float4 b4 = *reinterpret_cast<const float4*>(&sb[t][n0 + 2 * i]);
+          const float4 c4 = *reinterpret_cast<const float4*>(&sc[t][n0 + 2 * i]);
+          const float2 bv[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
+          const float2 cv[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float2 rb;
+#pragma unroll
+            for (int j = 0; j < CPT; ++j) {
+              const float2 gv = fma2(cv[e], pp[j], g[j][i + e]);
+              rb = j ? fma2(xx[j], gv, rb) : mul2(xx[j], gv);
+              uu[j] = i + e ? fma2(bv[e], gv, uu[j]) : mul2(bv[e], gv);
+              g[j][i + e] = mul2(gv, ex2(mul2(dd[j], A[j][i + e])));
+              const float2 q1 = mul2(g[j][i + e], s[u][j][i + e]);
+              ww[j] = i + e ? fma2(A[j][i + e], q1, ww[j]) : mul2(A[j][i + e], q1);
+              dA[j][i + e] = fma2(dd[j], q1, dA[j][i + e]);
+            }
+            r[(u & 1) * SPT + 2 * (i + e)] = rb.x;
+            r[(u & 1) * SPT + 2 * (i + e) + 1] = rb.y;
+          }
+        }
 #pragma unroll
         for (int j = 0; j < CPT; ++j) {
-          const float4 d = cells[t * HB + slot * CPT + j];
-          const float dx = d.x * d.y;
-          float uu = 0.f, ww = 0.f;
-#pragma unroll
-          for (int i = 0; i < SPT; ++i) {
-            g[j][i] = fmaf(sc[t][n0 + i], d.z, g[j][i]);
-            r[i] = fmaf(dx, g[j][i], r[i]);
-            r[SPT + i] = fmaf(d.z, s[u + 1][j][i], r[SPT + i]);
-            uu = fmaf(sb[t][n0 + i], g[j][i], uu);
-            g[j][i] *= f[u][j][i];
-            const float q1 = g[j][i] * s[u][j][i];
-            ww = fmaf(A[j][i], q1, ww);
-            dA[j][i] = fmaf(d.x, q1, dA[j][i]);
-          }
-          vu[j][u] = uu;
-          vw[j][u] = ww;
+          vu[j][u] = uu[j].x + uu[j].y;
+          vw[j][u] = ww[j].x + ww[j].y;
         }
-        // over the warp's channel slots (lanes LPC, 2 LPC, ... apart)
+        if (!(u & 1)) {
+          Sum::run(r, wl);
 #pragma unroll
-        for (int i = 0; i < 2 * SPT; ++i) {
-#pragma unroll
-          for (int o = LPC; o < 32; o <<= 1) r[i] += __shfl_xor_sync(0xffffffffu, r[i], o);
-        }
-        if (wl < LPC) {
-#pragma unroll
-          for (int i = 0; i < SPT; ++i) {
-            red[wid][u][n0 + i] = r[i];
-            red[wid][u][NP + n0 + i] = r[SPT + i];
+          for (int e = 0; e < Sum::KEEP; ++e) {
+            const int v = Sum::kept(wl, e);
+            red[wid][u + v / SPT][n0 + v % SPT] = r[e];
           }
         }
       }
-      // the block's cells: each lane finishes the tokens it holds the sums of
+      // the block's tokens, each finished by the lane that owns it
 #pragma unroll
       for (int j = 0; j < CPT; ++j) {
         sum_lanes<LPC>(vy[j], lane);
         sum_lanes<LPC>(vu[j], lane);
         sum_lanes<LPC>(vw[j], lane);
-        __syncwarp();  // every lane of the channel has read the block's cells
-        if (lane < 4) {
+      }
 #pragma unroll
-          for (int i = 0; i < kOwn<LPC>; ++i) {
-            const int t = k * TB + own_token<LPC>(lane, i);
-            float4& cell = cells[t * HB + slot * CPT + j];
-            const float4 d = cell;
-            const float sig = a.softplus ? -expm1f(-d.x) : 1.f;  // softplus' = 1 - e^-d
-            const float draw = t < live ? (d.y * vu[j][i] + kLn2 * vw[j][i]) * sig : 0.f;
-            dD[j] = fmaf(d.z, d.y, dD[j]);
-            db[j] += draw;
-            cell = make_float4(d.x * vu[j][i] + Dv[j] * d.z, draw, d.w * (vy[j][i] + Dv[j] * d.y), 0.f);
+      for (int i = 0; i < kOwn<LPC>; ++i) {
+        const int t = k * TB + own_token<LPC>(lane, i);
+        const float4 c0 = cells[t][cs][0], c1 = cells[t][cs][1];
+        const float d[2] = {c0.x, c0.y}, xv[2] = {c0.z, c0.w}, pv[2] = {c1.x, c1.y}, zf[2] = {c1.z, c1.w};
+        const float Dj[2] = {Dv.x, Dv.y};
+        float o1[2], o2[2], o3[2], od[2];
+#pragma unroll
+        for (int j = 0; j < CPT; ++j) {
+          o1[j] = fmaf(d[j], vu[j][i], Dj[j] * pv[j]);
+          o2[j] = fmaf(xv[j], vu[j][i], kLn2 * vw[j][i]);
+          if (a.softplus) o2[j] *= softplus_slope(d[j]);
+          if (t >= live) o2[j] = 0.f;
+          o3[j] = zf[j] * fmaf(Dj[j], xv[j], vy[j][i]);
+          od[j] = pv[j] * xv[j];
+        }
+        dD = add2(dD, make_float2(od[0], od[1]));
+        db = add2(db, make_float2(o2[0], o2[1]));
+        const long long tt = tb + t;
+        if (whole) {
+          if (LPC <= 4 || lane < 4) {
+            st_whole<T, 2>(dxo + tt * a.dx.row, o1);
+            st_whole<T, 2>(dto + tt * a.ddt.row, o2);
+            if (dzo) st_whole<T, 2>(dzo + tt * a.dz.row, o3);
           }
+        } else if (tt < a.L && p.ns > 0 && S4_IN(tt, a.L)) {
+          st_f<T, 2>(dxo + tt * a.dx.row, p.ns, vec, o1);
+          st_f<T, 2>(dto + tt * a.ddt.row, p.ns, vec, o2);
+          if (dzo) st_f<T, 2>(dzo + tt * a.dz.row, p.ns, vec, o3);
         }
       }
       __syncthreads();
@@ -407,58 +630,35 @@ __global__ void __launch_bounds__(kThreads) selective_tile_bwd_kernel(s4_selecti
         const int u = i / (2 * NP), n = i % (2 * NP);
         float v = 0.f;
 #pragma unroll
-        for (int x = 0; x < G::WARPS; ++x) v += red[x][u][n];
-        const int t = tb + k * TB + u;
-        if (t < a.L && S4_IN(t, a.L)) w.part_bc[(((long long)block * a.batch + b) * a.L + t) * 2 * NP + n] = v;
+        for (int e = 0; e < G::WARPS; ++e) v += red[e][u][n];
+        const int t = k * TB + u;
+        if (tb + t < a.L && S4_IN(tb + t, a.L)) bc[t * 2 * NP + n] = v;
       }
       __syncthreads();
     }
   }
-  // outputs
-  constexpr int V0 = 16 / (int)sizeof(T), V1 = V0 < HB ? V0 : HB, V = V1 < G::CELLS ? V1 : G::CELLS;
+  // the segment's part of dA, dD, ddt_bias (lanes that own no tokens hold the sums of none)
+  float* ph = w.part_h + ((long long)b * w.segs + seg) * a.H * (a.N + 2);
+  if (LPC > 4 && lane >= 4) dD = db = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int k = 0; k < G::CELLS / V; ++k) {
-    const int cell = (k * kThreads + threadIdx.x) * V, t = tb + cell / HB, h = c.h0 + cell % HB, n = c.hend - h;
-    if (t >= a.L || n <= 0 || !S4_IN(t, a.L)) continue;
-    float o[3][V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const bool on = t < q.len;
-      const float4 d = on ? cells[cell + i] : make_float4(0.f, 0.f, 0.f, 0.f);
-      o[0][i] = d.x;
-      o[1][i] = d.y;
-      o[2][i] = d.z;
-    }
-    st_f<T, V>(static_cast<T*>(a.dx.p) + b * a.dx.batch + t * a.dx.row + h, n, vec, o[0]);
-    st_f<T, V>(static_cast<T*>(a.ddt.p) + b * a.ddt.batch + t * a.ddt.row + h, n, vec, o[1]);
-    if (a.dz.p) st_f<T, V>(static_cast<T*>(a.dz.p) + b * a.dz.batch + t * a.dz.row + h, n, vec, o[2]);
+  for (int o = 1; o < (LPC < 4 ? LPC : 4); o <<= 1) {
+    dD.x += __shfl_xor_sync(0xffffffffu, dD.x, o);
+    dD.y += __shfl_xor_sync(0xffffffffu, dD.y, o);
+    db.x += __shfl_xor_sync(0xffffffffu, db.x, o);
+    db.y += __shfl_xor_sync(0xffffffffu, db.y, o);
   }
-  if (live <= 0) {
-    for (int i = threadIdx.x; i < min(TC, a.L - tb) * 2 * NP; i += kThreads)
-      w.part_bc[(((long long)block * a.batch + b) * a.L + tb) * 2 * NP + i] = 0.f;
-  }
-  // this tile's part of dA, dD, ddt_bias
-  float* ph = w.part_h + row * (a.N + 2);
 #pragma unroll
   for (int j = 0; j < CPT; ++j) {
-    const int h = c.h0 + slot * CPT + j;
-#pragma unroll
-    for (int o = 1; o < (LPC < 4 ? LPC : 4); o <<= 1) {
-      dD[j] += __shfl_xor_sync(0xffffffffu, dD[j], o);
-      db[j] += __shfl_xor_sync(0xffffffffu, db[j], o);
-    }
-    if (h >= c.hend) continue;
-#pragma unroll
-    for (int i = 0; i < SPT; ++i)
-      if (n0 + i < a.N) ph[(long long)h * a.N + n0 + i] = dA[j][i];
+    if (j >= nh) continue;
+    st_states<SPT>(ph + (long long)(h + j) * a.N + n0, nn, vecn, dA[j]);
     if (lane == 0) {
-      ph[(long long)a.H * a.N + h] = dD[j];
-      ph[(long long)a.H * (a.N + 1) + h] = db[j];
+      ph[(long long)a.H * a.N + h + j] = j ? dD.y : dD.x;
+      ph[(long long)a.H * (a.N + 1) + h + j] = j ? db.y : db.x;
     }
   }
 }
 
-// (4) The partial sums: over tiles and sequences ...
+// (4) The partial sums: over segments and sequences ...
 __global__ void __launch_bounds__(256) selective_sums_kernel(const float* part, int rows, int H, int N, float* dA, float* dD,
                                                              float* db) {
   column_sums(part, rows, (long long)H * (N + 2), [=](long long c, float v) {
@@ -488,27 +688,26 @@ __global__ void __launch_bounds__(256) selective_vectors_kernel(s4_selective_bwd
   out[(row * a.G + g) * a.N + state] = from_f<T>(v);
 }
 
-// The lanes, states per lane and channels per thread that hold N states.
+// The lanes that hold N states, 8 each.
 template <typename F>
 auto with_states(int N, F f) {
-  if (N <= 4) return f(Geo<1, 4, 1>{});
-  if (N <= 8) return f(Geo<2, 4, 1>{});
-  if (N <= 16) return f(Geo<4, 4, 2>{});
-  if (N <= 32) return f(Geo<8, 4, 2>{});
-  if (N <= 64) return f(Geo<16, 4, 2>{});
-  if (N <= 128) return f(Geo<32, 4, 2>{});
-  return f(Geo<32, 8, 1>{});
+  if (N <= 8) return f(Geo<1, 8>{});
+  if (N <= 16) return f(Geo<2, 8>{});
+  if (N <= 32) return f(Geo<4, 8>{});
+  if (N <= 64) return f(Geo<8, 8>{});
+  if (N <= 128) return f(Geo<16, 8>{});
+  return f(Geo<32, 8>{});
 }
 
-constexpr int kWarps = 16;  // per SM that the first kernel's segments are meant to fill
+constexpr int kCtas = 6;  // per SM that the segments are meant to give: two rounds of (3)
 
 // Sizes and the workspace's layout (pointers relative to a null base when ws is null).
 template <typename G>
 Work layout(int batch, int L, int H, int N, int Gr, char* ws, size_t* total) {
   Work w;
   w.tiles = (L + G::TC - 1) / G::TC;
-  w.blocks = Gr * ((H / Gr + G::HB - 1) / G::HB);
-  const long long ctas = (long long)batch * w.blocks, want = (long long)s4impl::num_sms() * kWarps / (kThreads / 32);
+  w.blocks = chan_blocks<G::HB>(H, Gr);
+  const long long ctas = (long long)batch * w.blocks, want = (long long)s4impl::num_sms() * kCtas;
   long long segs = (want + ctas - 1) / ctas;
   if (segs > w.tiles / 4) segs = w.tiles / 4;
   if (segs < 1) segs = 1;
@@ -522,47 +721,58 @@ Work layout(int batch, int L, int H, int N, int Gr, char* ws, size_t* total) {
     return p;
   };
   w.s_tile = take(bt * HN);
-  w.g_tile = take(bt * HN);
   w.d_before = take(bt * H);
-  w.d_after = take(bt * H);
-  w.s_seg = take(w.segs > 1 ? bs * HN : 0);
-  w.g_seg = take(w.segs > 1 ? bs * HN : 0);
-  w.d_seg = take(w.segs > 1 ? bs * H : 0);
-  w.part_h = take(bt * H * (N + 2));
+  w.s_seg = take(bs * HN);
+  w.g_seg = take(bs * HN);
+  w.d_seg = take(bs * H);
+  w.part_h = take(bs * H * (N + 2));
   w.part_bc = take((size_t)w.blocks * batch * L * 2 * G::NP);
-  if (total) *total = (long long)w.blocks * w.tiles > INT_MAX ? 0 : at;  // CTAs of one launch
+  // CTAs of one launch
+  if (total) *total = (long long)chan_blocks<G::CH>(H, Gr) * w.segs > INT_MAX ? 0 : at;
   return w;
 }
 
 template <typename T>
 cudaError_t bwd_t(const s4_selective_bwd_args& a, St st, cudaStream_t s) {
   const int e = sizeof(T);
-  const auto ok = [&](const auto& r) { return vec_ok(r.p, e, 16, r.batch, r.row); };
-  const bool vec = ok(a.x) && ok(a.dt) && ok(a.z) && ok(a.dy) && ok(a.dx) && ok(a.ddt) && ok(a.dz) &&
-                   (a.G == 1 || (a.H / a.G) * e % 16 == 0);
   with_states(a.N, [&](auto geo) {
     using G = decltype(geo);
+    const auto ok = [&](const auto& r) { return vec_ok(r.p, e, 2 * e, r.batch, r.row); };
+    const bool vec = ok(a.x) && ok(a.dt) && ok(a.z) && ok(a.dy) && ok(a.dx) && ok(a.ddt) && ok(a.dz) &&
+                     (a.G == 1 || (a.H / a.G) % 2 == 0);
+    constexpr int pb = e * (16 / e < G::VECS ? 16 / e : G::VECS);
+    const bool vecbc = vec_ok(a.B.p, e, pb, a.B.batch, a.B.row) && vec_ok(a.C.p, e, pb, a.C.batch, a.C.row) &&
+                       a.B_group * e % pb == 0 && a.C_group * e % pb == 0;
+    const bool vecn = a.N % 4 == 0 && vec_ok(a.A, 4, 16) && vec_ok(a.state0, 4, 16);
     const Work w = layout<G>(a.batch, a.L, a.H, a.N, a.G, static_cast<char*>(a.ws), nullptr);
-    cudaFuncSetAttribute(selective_ends_kernel<T, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSegBytes);
-    cudaFuncSetAttribute(selective_tile_bwd_kernel<T, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kBytes);
-    {
+    const auto run = [&](auto whole) {
+      constexpr bool W = decltype(whole)::value;
+      const auto ends = selective_ends_kernel<T, G, W>, tiles = selective_tiles_kernel<T, G, W>;
+      cudaFuncSetAttribute(ends, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kEndsBytes);
+      cudaFuncSetAttribute(tiles, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kBytes);
+      {
+        s4impl::TimedLaunch tl("selective_bwd", s);
+        const long long tasks = (long long)chan_blocks<G::CH>(a.H, a.G) * w.segs;
+        ends<<<dim3((unsigned)((tasks + G::WARPS - 1) / G::WARPS), a.batch), kThreads, G::kEndsBytes, s>>>(a, w, vec, vecbc,
+                                                                                                       vecn, st);
+      }
+      {
+        s4impl::TimedLaunch tl("selective_bwd", s);
+        const long long HN = (long long)a.H * a.N;
+        selective_joins_kernel<<<dim3((unsigned)((HN + 127) / 128), a.batch), 128, 0, s>>>(a, w);
+      }
       s4impl::TimedLaunch tl("selective_bwd", s);
-      selective_ends_kernel<T, G><<<dim3(w.blocks, w.segs, a.batch), kThreads, G::kSegBytes, s>>>(a, w, vec, st);
-    }
-    const long long HN = (long long)a.H * a.N;
-    if (w.segs > 1) {
-      s4impl::TimedLaunch tl("selective_bwd", s);
-      selective_joins_kernel<<<dim3((unsigned)((HN + 255) / 256), a.batch), 256, 0, s>>>(a, w);
-    }
-    {
-      s4impl::TimedLaunch tl("selective_bwd", s);
-      selective_tile_bwd_kernel<T, G>
-          <<<dim3((unsigned)w.blocks * w.tiles, a.batch), kThreads, G::kBytes, s>>>(a, w, vec, st);
-    }
+      tiles<<<dim3((unsigned)(w.blocks * w.segs), a.batch), kThreads, G::kBytes, s>>>(a, w, vec, vecbc, vecn, st);
+    };
+    // the tiles of other widths cost a condition per access
+    if (vec && vecbc && a.N == G::NP && (a.H / a.G) % G::HB == 0 && G::LPC <= 4)
+      run(std::true_type{});
+    else
+      run(std::false_type{});
     {
       s4impl::TimedLaunch tl("selective_bwd", s);
       const long long cols = (long long)a.H * (a.N + 2);
-      selective_sums_kernel<<<(unsigned)((cols + 31) / 32), 256, 0, s>>>(w.part_h, a.batch * w.tiles, a.H, a.N, a.dA, a.dD,
+      selective_sums_kernel<<<(unsigned)((cols + 31) / 32), 256, 0, s>>>(w.part_h, a.batch * w.segs, a.H, a.N, a.dA, a.dD,
                                                                         a.ddt_bias);
     }
     s4impl::TimedLaunch tl("selective_bwd", s);
