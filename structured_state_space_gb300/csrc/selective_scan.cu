@@ -20,7 +20,10 @@ using namespace s4sel;
 // Four CTAs of four warps per SM: 128 registers a thread.  At 20 warps per SM the registers
 // left do not hold enough exponentials in flight (650 us instead of 564 on one sequence of
 // 65536 tokens, 1024 channels, 16 states, bfloat16), at 14 there are too few warps (647 us).
-constexpr int kScanThreads = 128, kScanCtas = 4;
+#ifndef S4_MB
+#define S4_MB 4
+#endif
+constexpr int kScanThreads = 128, kScanCtas = S4_MB;
 
 template <int LPC_, int SPT_>
 struct Geo {
@@ -30,7 +33,9 @@ struct Geo {
   static constexpr int OWN = TT / 4 * kOwn<LPC>;         // tokens of a tile that a lane stages and finishes
   static constexpr int VECS = TT * NP / 32;              // elements of B, of C that a lane stages
   // Shared memory of a warp in floats: steps and step x of channel pairs [TT][32 / LPC][4] | B | C [TT][NP]
-  static constexpr int B0 = TT * 32 / LPC * 4, C0 = B0 + TT * NP, END = C0 + TT * NP;
+  // | the next tile's x, dt, z [3][OWN][32] packs of 2 | its B, C
+  static constexpr int B0 = TT * 32 / LPC * 4, C0 = B0 + TT * NP, X0 = C0 + TT * NP;
+  static constexpr int V0 = X0 + 3 * OWN * 32 * 2, END = V0 + 2 * TT * NP;
   static constexpr int kBytes = 4 * END * (kScanThreads / 32);
 };
 
@@ -57,7 +62,6 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas)
     selective_scan_kernel(s4_selective_args a, Chunks ck, bool vec, bool vecbc, St st) {
   constexpr int LPC = G::LPC, SPT = G::SPT, NP = G::NP, CH = G::CH, TT = G::TT, CPT = G::CPT, OWN = G::OWN;
   constexpr int V0 = 16 / (int)sizeof(T), VB = V0 < G::VECS ? V0 : G::VECS, NB = G::VECS / VB;
-  constexpr bool AHEAD = NP <= 64;  // B and C of the next tile wait in registers
   extern __shared__ __align__(16) float smem[];
   float* mine = smem + threadIdx.x / 32 * G::END;
   float4(*sd)[32 / LPC] = reinterpret_cast<float4(*)[32 / LPC]>(mine);
@@ -110,57 +114,53 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas)
 
   // the k-th token of a tile that this lane owns
   const auto token = [&](int k) { return k / kOwn<LPC> * 4 + own_token<LPC>(lane, k % kOwn<LPC>); };
-  Pack<T, CPT> nx[OWN], nd[OWN], nz[OWN];
-  Pack<T, VB> nb[NB], nc[NB];
-  const auto fetch_bc = [&](int tb) {
-    if (WHOLE && tb + TT <= live) {
-#pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        const int i = (k * 32 + wl) * VB, t = tb + i / NP;
-        nb[k] = ld_whole<T, VB>(B + t * a.B.row + i % NP);
-        if (MODE == 1) nc[k] = ld_whole<T, VB>(C + t * a.C.row + i % NP);
-      }
-      return;
-    }
-#pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      const int i = (k * 32 + wl) * VB, t = tb + i / NP;
-      const int n = t < live && S4_IN(t, a.L) ? a.N - i % NP : 0;
-      nb[k] = ld_pack<T, VB>(B + t * a.B.row + i % NP, n, vecbc);
-      if (MODE == 1) nc[k] = ld_pack<T, VB>(C + t * a.C.row + i % NP, n, vecbc);
-    }
-  };
+  // this lane's slots of the next tile
+  Pack<T, CPT>* next = reinterpret_cast<Pack<T, CPT>*>(mine + G::X0) + wl;
+  Pack<T, VB>* nextv = reinterpret_cast<Pack<T, VB>*>(mine + G::V0) + wl;
   const auto fetch = [&](int tb) {
-    if (AHEAD) fetch_bc(tb);
     if (WHOLE && tb + TT <= live) {
 #pragma unroll
       for (int k = 0; k < OWN; ++k) {
         const int t = tb + token(k);
-        nx[k] = ld_whole<T, CPT>(x + t * a.x.row);
-        nd[k] = ld_whole<T, CPT>(dt + t * a.dt.row);
-        if (z) nz[k] = ld_whole<T, CPT>(z + t * a.z.row);
+        fetch_whole<T, CPT>(next + k * 32, x + t * a.x.row);
+        fetch_whole<T, CPT>(next + (OWN + k) * 32, dt + t * a.dt.row);
+        if (z) fetch_whole<T, CPT>(next + (2 * OWN + k) * 32, z + t * a.z.row);
+      }
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const int i = (k * 32 + wl) * VB, t = tb + i / NP;
+        fetch_whole<T, VB>(nextv + k * 32, B + t * a.B.row + i % NP);
+        if (MODE == 1) fetch_whole<T, VB>(nextv + (NB + k) * 32, C + t * a.C.row + i % NP);
       }
       return;
     }
 #pragma unroll
     for (int k = 0; k < OWN; ++k) {
       const int t = tb + token(k), n = t < live && S4_IN(t, a.L) ? ns : 0;
-      nx[k] = ld_pack<T, CPT>(x + t * a.x.row, n, vec);
-      nd[k] = ld_pack<T, CPT>(dt + t * a.dt.row, n, vec);
-      if (z) nz[k] = ld_pack<T, CPT>(z + t * a.z.row, n, vec);
+      next[k * 32] = ld_pack<T, CPT>(x + t * a.x.row, n, vec);
+      next[(OWN + k) * 32] = ld_pack<T, CPT>(dt + t * a.dt.row, n, vec);
+      if (z) next[(2 * OWN + k) * 32] = ld_pack<T, CPT>(z + t * a.z.row, n, vec);
+    }
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int i = (k * 32 + wl) * VB, t = tb + i / NP;
+      const int n = t < live && S4_IN(t, a.L) ? a.N - i % NP : 0;
+      nextv[k * 32] = ld_pack<T, VB>(B + t * a.B.row + i % NP, n, vecbc);
+      if (MODE == 1) nextv[(NB + k) * 32] = ld_pack<T, VB>(C + t * a.C.row + i % NP, n, vecbc);
     }
   };
   if (t0 < live) fetch(t0);
   for (int tb = t0; tb < live; tb += TT) {
     const bool whole = tb + TT <= live;
     Pack<T, CPT> px[OWN], pz[OWN];
-    if (!AHEAD) fetch_bc(tb);
+    fetched();
     __syncwarp();  // the tile before has been read
 #pragma unroll
     for (int k = 0; k < OWN; ++k) {
-      px[k] = nx[k];
-      pz[k] = nz[k];
-      float2 d = make_float2(nd[k].get(0) + bias[0], nd[k].get(1) + bias[1]);
+      px[k] = next[k * 32];
+      if (z) pz[k] = next[(2 * OWN + k) * 32];
+      const Pack<T, CPT> pd = next[(OWN + k) * 32];
+      float2 d = make_float2(pd.get(0) + bias[0], pd.get(1) + bias[1]);
       if (a.softplus) d = softplus2(d);
       if (!whole && tb + token(k) >= live) d = make_float2(0.f, 0.f);  // padding keeps the state
       const float2 dx = mul2(d, make_float2(px[k].get(0), px[k].get(1)));
@@ -170,10 +170,13 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas)
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       const int i = (k * 32 + wl) * VB;
+      const Pack<T, VB> pb = nextv[k * 32];
 #pragma unroll
-      for (int e = 0; e < VB; ++e) {
-        (&sb[0][0])[i + e] = nb[k].get(e);
-        if (MODE == 1) (&sc[0][0])[i + e] = nc[k].get(e);
+      for (int e = 0; e < VB; ++e) (&sb[0][0])[i + e] = pb.get(e);
+      if (MODE == 1) {
+        const Pack<T, VB> pc = nextv[(NB + k) * 32];
+#pragma unroll
+        for (int e = 0; e < VB; ++e) (&sc[0][0])[i + e] = pc.get(e);
       }
     }
     __syncwarp();
@@ -434,10 +437,12 @@ cudaError_t scan_t(const s4_selective_args& a, St st, cudaStream_t s) {
       out<<<grid, kScanThreads, G::kBytes, s>>>(a, ck, vec, vecbc, st);
     };
     // the tiles of other widths cost a condition per access
-    if (vec && vecbc && a.N == G::NP && (a.H / a.G) % G::CH == 0 && G::LPC <= 4)
-      run(std::true_type{});
-    else
-      run(std::false_type{});
+    bool whole = false;
+    if constexpr (G::LPC <= 4) {
+      whole = vec && vecbc && a.N == G::NP && (a.H / a.G) % G::CH == 0;
+      if (whole) run(std::true_type{});
+    }
+    if (!whole) run(std::false_type{});
   });
   return cudaGetLastError();
 }

@@ -22,6 +22,11 @@
 
 namespace {
 using namespace s4sel;
+#ifndef S4_EB
+#define S4_EB 4
+#define S4_TBK 3
+#define S4_KC 12
+#endif
 
 template <int LPC_, int SPT_>
 struct Geo {
@@ -32,12 +37,27 @@ struct Geo {
   static constexpr int OWN = TC / 4 * kOwn<LPC>;         // tokens of a tile that a lane stages and finishes
   // shared memory in floats: cells [TC][WARPS * SLOTS][2][4] | B, C [TC][NP] | states at blocks | sums of dB, dC
   static constexpr int B0 = TC * WARPS * SLOTS * 8, C0 = B0 + TC * NP, S0 = C0 + TC * NP;
-  static constexpr int R0 = S0 + TC / TB * kThreads * CPT * SPT, END = R0 + WARPS * TB * 2 * NP;
-  static constexpr int kBytes = 4 * END;
-  // (1): a warp's tile of 4 tokens: steps, inputs, dyp [4][SLOTS][6 of 8] | B, C [4][NP]
-  static constexpr int EB = 4 * SLOTS * 8, EC = EB + 4 * NP, EEND = EC + 4 * NP;
-  static constexpr int kEndsBytes = 4 * EEND * WARPS;
-  static constexpr int VECS = 4 * NP / 32;               // elements of B, of C that a lane stages there
+  // | the tile before: x, dt, z, dy [4][OWN][kThreads] packs of 2 | B, C | its states
+  static constexpr int VECS = TC * NP / kThreads > 0 ? TC * NP / kThreads : 1;  // elements of B, of C a thread stages
+  static constexpr int R0 = S0 + TC / TB * kThreads * CPT * SPT, X0 = R0 + WARPS * TB * 2 * NP;
+  template <typename T>
+  static constexpr int V0() { return X0 + 4 * OWN * kThreads * 2 * (int)sizeof(T) / 4; }
+  template <typename T>
+  static constexpr int N0() { return V0<T>() + 2 * VECS * kThreads * (int)sizeof(T) / 4; }
+  template <typename T>
+  static constexpr int kBytes() { return 4 * (N0<T>() + kThreads * CPT * SPT); }
+  static constexpr int GT = 16 / SPT;                    // tokens whose sums over channels are formed together
+};
+// (1): a warp's tile of TT tokens: steps, inputs, dyp [TT][SLOTS][6 of 8] | B, C [TT][NP]
+template <int LPC_, int SPT_, int TC_>
+struct EndsGeo {
+  static constexpr int LPC = LPC_, SPT = SPT_, NP = LPC * SPT, CPT = 2, SLOTS = 32 / LPC, CH = SLOTS * CPT;
+  static constexpr int TT = LPC == 1 || NP > 64 ? 4 : 8, TC = TC_;  // its tile, and (3)'s
+  static constexpr int OWN = TT / 4 * kOwn<LPC>;
+  // | the next tile's x, dt, z, dy [4][OWN][32] packs of 2 | its B, C
+  static constexpr int B0 = TT * SLOTS * 8, C0 = B0 + TT * NP, X0 = C0 + TT * NP;
+  static constexpr int V0 = X0 + 4 * OWN * 32 * 2, END = V0 + 2 * TT * NP, kBytes = 4 * END * (kThreads / 32);
+  static constexpr int VECS = TT * NP / 32;              // elements of B, of C that a lane stages
 };
 
 struct Work {
@@ -55,23 +75,33 @@ template <typename T>
 struct Cell {
   Pack<T, 2> x, dt, z, dy;
 };
-template <typename T, bool WHOLE>
-__device__ __forceinline__ Cell<T> ld_cell(const s4_selective_bwd_args& a, const T* x, const T* dt, const T* z, const T* dy,
-                                           long long t, int n, bool vec) {
-  Cell<T> c;
-  if (WHOLE) {
-    c.x = ld_whole<T, 2>(x + t * a.x.row);
-    c.dt = ld_whole<T, 2>(dt + t * a.dt.row);
-    c.dy = ld_whole<T, 2>(dy + t * a.dy.row);
-    if (z) c.z = ld_whole<T, 2>(z + t * a.z.row);
-  } else {
-    c.x = ld_pack<T, 2>(x + t * a.x.row, n, vec);
-    c.dt = ld_pack<T, 2>(dt + t * a.dt.row, n, vec);
-    c.dy = ld_pack<T, 2>(dy + t * a.dy.row, n, vec);
-    if (z) c.z = ld_pack<T, 2>(z + t * a.z.row, n, vec);
+// A lane's slots for OWN of them in shared memory, STRIDE lanes apart: [4][OWN][STRIDE].
+template <typename T, int OWN, int STRIDE>
+struct Cells {
+  Pack<T, 2>* s;
+  __device__ __forceinline__ void fetch(int k, const s4_selective_bwd_args& a, const T* x, const T* dt, const T* z,
+                                        const T* dy, long long t) {
+    fetch_whole<T, 2>(s + k * STRIDE, x + t * a.x.row);
+    fetch_whole<T, 2>(s + (OWN + k) * STRIDE, dt + t * a.dt.row);
+    fetch_whole<T, 2>(s + (2 * OWN + k) * STRIDE, dy + t * a.dy.row);
+    if (z) fetch_whole<T, 2>(s + (3 * OWN + k) * STRIDE, z + t * a.z.row);
   }
-  return c;
-}
+  __device__ __forceinline__ void load(int k, const s4_selective_bwd_args& a, const T* x, const T* dt, const T* z,
+                                       const T* dy, long long t, int n, bool vec) {
+    s[k * STRIDE] = ld_pack<T, 2>(x + t * a.x.row, n, vec);
+    s[(OWN + k) * STRIDE] = ld_pack<T, 2>(dt + t * a.dt.row, n, vec);
+    s[(2 * OWN + k) * STRIDE] = ld_pack<T, 2>(dy + t * a.dy.row, n, vec);
+    if (z) s[(3 * OWN + k) * STRIDE] = ld_pack<T, 2>(z + t * a.z.row, n, vec);
+  }
+  __device__ __forceinline__ Cell<T> get(int k, const T* z) const {
+    Cell<T> c;
+    c.x = s[k * STRIDE];
+    c.dt = s[(OWN + k) * STRIDE];
+    c.dy = s[(2 * OWN + k) * STRIDE];
+    if (z) c.z = s[(3 * OWN + k) * STRIDE];
+    return c;
+  }
+};
 // Step sizes, inputs, dyp and dy silu'(z) of a cell.
 template <typename T>
 __device__ __forceinline__ void eval_cell(const Cell<T>& c, bool gate, bool soft, float2 bias, float2& d, float2& x,
@@ -129,22 +159,22 @@ struct Place {
   }
 };
 
-// (1) A warp per channel block and segment, in tiles of 4 tokens read ahead by one.  The gradient
+// (1) A warp per channel block and segment, in tiles of TT tokens read ahead by one.  The gradient
 // at the segment's start is R = sum_t (prod_{j<=t} a_j) C_t dyp_t.
 template <typename T, typename G, bool WHOLE>
-__global__ void __launch_bounds__(kThreads, 4) selective_ends_kernel(s4_selective_bwd_args a, Work w, bool vec, bool vecbc,
+__global__ void __launch_bounds__(kThreads, S4_EB) selective_ends_kernel(s4_selective_bwd_args a, Work w, bool vec, bool vecbc,
                                                                      bool vecn, St st) {
-  constexpr int LPC = G::LPC, SPT = G::SPT, CPT = G::CPT, NP = G::NP, CH = G::CH, TT = 4, OWN = kOwn<LPC>;
+  constexpr int LPC = G::LPC, SPT = G::SPT, CPT = G::CPT, NP = G::NP, CH = G::CH, TT = G::TT, OWN = G::OWN;
   constexpr int V0 = 16 / (int)sizeof(T), VB = V0 < G::VECS ? V0 : G::VECS, NB = G::VECS / VB;
   extern __shared__ __align__(16) float smem[];
-  float* mine = smem + threadIdx.x / 32 * G::EEND;
+  float* mine = smem + threadIdx.x / 32 * G::END;
   float4(*sd)[G::SLOTS][2] = reinterpret_cast<float4(*)[G::SLOTS][2]>(mine);
-  float(*sb)[NP] = reinterpret_cast<float(*)[NP]>(mine + G::EB);
-  float(*sc)[NP] = reinterpret_cast<float(*)[NP]>(mine + G::EC);
+  float(*sb)[NP] = reinterpret_cast<float(*)[NP]>(mine + G::B0);
+  float(*sc)[NP] = reinterpret_cast<float(*)[NP]>(mine + G::C0);
   record_gen(st);
   const int b = blockIdx.y, wl = threadIdx.x & 31, blocks = chan_blocks<CH>(a.H, a.G);
   const Seq q = seq_of(a.lengths, nullptr, b, a.L, 0, st);
-  const long long task = (long long)blockIdx.x * G::WARPS + threadIdx.x / 32;
+  const long long task = (long long)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
   if (task >= (long long)blocks * w.segs) return;
   const int seg = (int)(task / blocks);
   const Chan c = chan_of<CH>((int)(task % blocks), a.H / a.G);
@@ -173,27 +203,31 @@ __global__ void __launch_bounds__(kThreads, 4) selective_ends_kernel(s4_selectiv
       R[j][i] = make_float2(0.f, 0.f);
     }
   }
-  Cell<T> next[OWN];
-  Pack<T, VB> nb[NB], nc[NB];
+  // this lane's slots of the next tile
+  Cells<T, OWN, 32> next{reinterpret_cast<Pack<T, 2>*>(mine + G::X0) + wl};
+  Pack<T, VB>* nextv = reinterpret_cast<Pack<T, VB>*>(mine + G::V0) + wl;
   const auto fetch = [&](int tb) {
-    const bool whole = WHOLE && tb + TT <= live;
+    if (WHOLE && tb + TT <= live) {
 #pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      const int i = (k * 32 + wl) * VB, t = tb + i / NP;
-      if (whole) {
-        nb[k] = ld_whole<T, VB>(B + t * a.B.row + i % NP);
-        nc[k] = ld_whole<T, VB>(C + t * a.C.row + i % NP);
-      } else {
-        const int n = t < live && S4_IN(t, a.L) ? a.N - i % NP : 0;
-        nb[k] = ld_pack<T, VB>(B + t * a.B.row + i % NP, n, vecbc);
-        nc[k] = ld_pack<T, VB>(C + t * a.C.row + i % NP, n, vecbc);
+      for (int k = 0; k < OWN; ++k) next.fetch(k, a, x, dt, z, dy, tb + p.token(k));
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const int i = (k * 32 + wl) * VB, t = tb + i / NP;
+        fetch_whole<T, VB>(nextv + k * 32, B + t * a.B.row + i % NP);
+        fetch_whole<T, VB>(nextv + (NB + k) * 32, C + t * a.C.row + i % NP);
       }
+      return;
     }
 #pragma unroll
     for (int k = 0; k < OWN; ++k) {
-      const int t = tb + own_token<LPC>(lane, k);
-      next[k] = whole ? ld_cell<T, true>(a, x, dt, z, dy, t, 2, true)
-                      : ld_cell<T, false>(a, x, dt, z, dy, t, t < live && S4_IN(t, a.L) ? p.ns : 0, vec);
+      const int t = tb + p.token(k);
+      next.load(k, a, x, dt, z, dy, t, t < live && S4_IN(t, a.L) ? p.ns : 0, vec);
+    }
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int i = (k * 32 + wl) * VB, t = tb + i / NP, n = t < live && S4_IN(t, a.L) ? a.N - i % NP : 0;
+      nextv[k * 32] = ld_pack<T, VB>(B + t * a.B.row + i % NP, n, vecbc);
+      nextv[(NB + k) * 32] = ld_pack<T, VB>(C + t * a.C.row + i % NP, n, vecbc);
     }
   };
   if (t0 < live) fetch(t0);
@@ -215,12 +249,13 @@ __global__ void __launch_bounds__(kThreads, 4) selective_ends_kernel(s4_selectiv
       if (tb >= live) continue;
     }
     if (tb >= live) continue;
+    fetched();
     __syncwarp();  // the tile before has been read
 #pragma unroll
     for (int k = 0; k < OWN; ++k) {
       float2 d, xv, pv, zf;
-      eval_cell<T>(next[k], z != nullptr, a.softplus, bias, d, xv, pv, zf);
-      const int t = own_token<LPC>(lane, k);
+      eval_cell<T>(next.get(k, z), z != nullptr, a.softplus, bias, d, xv, pv, zf);
+      const int t = p.token(k);
       if (tb + t >= live) d = make_float2(0.f, 0.f);  // padding keeps the state
       sum = add2(sum, d);
       const float2 dx = mul2(d, xv);
@@ -232,10 +267,11 @@ __global__ void __launch_bounds__(kThreads, 4) selective_ends_kernel(s4_selectiv
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       const int i = (k * 32 + wl) * VB;
+      const Pack<T, VB> pb = nextv[k * 32], pc = nextv[(NB + k) * 32];
 #pragma unroll
       for (int e = 0; e < VB; ++e) {
-        (&sb[0][0])[i + e] = nb[k].get(e);
-        (&sc[0][0])[i + e] = nc[k].get(e);
+        (&sb[0][0])[i + e] = pb.get(e);
+        (&sc[0][0])[i + e] = pc.get(e);
       }
     }
     __syncwarp();
@@ -360,7 +396,7 @@ __device__ __forceinline__ float softplus_slope(float d) {
 
 // (3) A CTA per HB channels and segment.
 template <typename T, typename G, bool WHOLE>
-__global__ void __launch_bounds__(kThreads, 3) selective_tiles_kernel(s4_selective_bwd_args a, Work w, bool vec, bool vecbc,
+__global__ void __launch_bounds__(kThreads, S4_TBK) selective_tiles_kernel(s4_selective_bwd_args a, Work w, bool vec, bool vecbc,
                                                                       bool vecn, St st) {
   constexpr int LPC = G::LPC, SPT = G::SPT, CPT = G::CPT, NP = G::NP, CH = G::CH, TC = G::TC, TB = G::TB, OWN = G::OWN;
   using Sum = SumSlots<LPC>;
@@ -403,6 +439,55 @@ __global__ void __launch_bounds__(kThreads, 3) selective_tiles_kernel(s4_selecti
       dA[j][i] = make_float2(0.f, 0.f);
     }
   }
+  // this thread's slots of the tile that comes next, the one before in time
+  constexpr int V0 = 16 / (int)sizeof(T), VB = V0 < G::VECS ? V0 : G::VECS, NB = G::VECS / VB;
+  Cells<T, OWN, kThreads> next{reinterpret_cast<Pack<T, 2>*>(smem + G::X0) + threadIdx.x};
+  Pack<T, VB>* nextv = reinterpret_cast<Pack<T, VB>*>(smem + G::template V0<T>()) + threadIdx.x;
+  float4* nexts = reinterpret_cast<float4*>(smem + G::template N0<T>()) + threadIdx.x;  // [CPT][SPT / 4][kThreads]
+  const auto fetch = [&](int tile) {
+    const int tb = tile * TC, live = min(TC, q.len - tb);
+    if (live <= 0) return;
+    const long long row = ((long long)b * w.tiles + tile) * a.H + h;
+    if (WHOLE && live == TC) {
+#pragma unroll
+      for (int k = 0; k < OWN; ++k) next.fetch(k, a, x, dt, z, dy, tb + p.token(k));
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const int i = (k * kThreads + threadIdx.x) * VB, t = tb + i / NP;
+        if (i >= TC * NP) continue;
+        fetch_whole<T, VB>(nextv + k * kThreads, B + t * a.B.row + i % NP);
+        fetch_whole<T, VB>(nextv + (NB + k) * kThreads, C + t * a.C.row + i % NP);
+      }
+#pragma unroll
+      for (int j = 0; j < CPT; ++j)
+#pragma unroll
+        for (int i = 0; i < SPT / 4; ++i)
+          fetch_whole<float, 4>(reinterpret_cast<Pack<float, 4>*>(nexts + (j * SPT / 4 + i) * kThreads),
+                                w.s_tile + (row + j) * a.N + n0 + 4 * i);
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < OWN; ++k) {
+      const int t = p.token(k);
+      next.load(k, a, x, dt, z, dy, tb + t, t < live && S4_IN(tb + t, a.L) ? p.ns : 0, vec);
+    }
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int i = (k * kThreads + threadIdx.x) * VB, t = i / NP;
+      const int n = i < TC * NP && t < live && S4_IN(tb + t, a.L) ? a.N - i % NP : 0;
+      nextv[k * kThreads] = ld_pack<T, VB>(B + (long long)(tb + t) * a.B.row + i % NP, n, vecbc);
+      nextv[(NB + k) * kThreads] = ld_pack<T, VB>(C + (long long)(tb + t) * a.C.row + i % NP, n, vecbc);
+    }
+#pragma unroll
+    for (int j = 0; j < CPT; ++j) {
+      float f[SPT];
+      ld_f<float, SPT>(w.s_tile + (row + j) * a.N + n0, j < nh ? nn : 0, vecn, f);
+#pragma unroll
+      for (int i = 0; i < SPT / 4; ++i)
+        nexts[(j * SPT / 4 + i) * kThreads] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+    }
+  };
+  fetch(last - 1);
   for (int tile = last - 1; tile >= first; --tile) {
     const int tb = tile * TC, live = min(TC, q.len - tb);  // <= 0: a tile of padding
     float* bc = w.part_bc + (((long long)block * a.batch + b) * a.L + tb) * 2 * NP;
@@ -417,29 +502,33 @@ __global__ void __launch_bounds__(kThreads, 3) selective_tiles_kernel(s4_selecti
         if (dzo) st_f<T, 2>(dzo + t * a.dz.row, p.ns, vec, zero);
       }
       for (int i = threadIdx.x; i < min(TC, a.L - tb) * 2 * NP; i += kThreads) bc[i] = 0.f;
+      if (tile > first) fetch(tile - 1);
       continue;
     }
-    __syncthreads();  // the tile after this one is done with shared memory
     const bool whole = WHOLE && live == TC;
-#pragma unroll 4
+    fetched();
+    __syncthreads();  // the tile after this one is done with shared memory
+#pragma unroll
     for (int k = 0; k < OWN; ++k) {
       const int t = p.token(k);
-      const bool on = t < live;
-      const Cell<T> cell = whole ? ld_cell<T, true>(a, x, dt, z, dy, tb + t, 2, true)
-                                 : ld_cell<T, false>(a, x, dt, z, dy, tb + t, on && S4_IN(tb + t, a.L) ? p.ns : 0, vec);
       float2 d, xv, pv, zf;
-      eval_cell<T>(cell, z != nullptr, a.softplus, bias, d, xv, pv, zf);
-      if (!on) d = make_float2(0.f, 0.f);
+      eval_cell<T>(next.get(k, z), z != nullptr, a.softplus, bias, d, xv, pv, zf);
+      if (t >= live) d = make_float2(0.f, 0.f);
       if (LPC <= 4 || lane < 4) {
         cells[t][cs][0] = make_float4(d.x, d.y, xv.x, xv.y);
         cells[t][cs][1] = make_float4(pv.x, pv.y, zf.x, zf.y);
       }
     }
-    for (int i = threadIdx.x; i < TC * NP; i += kThreads) {
-      const int t = i / NP, n = i % NP;
-      const bool on = t < live && n < a.N && S4_IN(tb + t, a.L);
-      (&sb[0][0])[i] = on ? to_f(B[(tb + t) * a.B.row + n]) : 0.f;
-      (&sc[0][0])[i] = on ? to_f(C[(tb + t) * a.C.row + n]) : 0.f;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int i = (k * kThreads + threadIdx.x) * VB;
+      if (i >= TC * NP) continue;
+      const Pack<T, VB> pb = nextv[k * kThreads], pc = nextv[(NB + k) * kThreads];
+#pragma unroll
+      for (int e = 0; e < VB; ++e) {
+        (&sb[0][0])[i + e] = pb.get(e);
+        (&sc[0][0])[i + e] = pc.get(e);
+      }
     }
     // the state at the tile's start: from the segment's zero start, and what came before it
     {
@@ -448,7 +537,12 @@ __global__ void __launch_bounds__(kThreads, 3) selective_tiles_kernel(s4_selecti
 #pragma unroll
       for (int j = 0; j < CPT; ++j) {
         const int n = j < nh ? nn : 0;
-        ld_states<SPT>(s[j], w.s_tile + (row + j) * a.N + n0, n, vecn);
+#pragma unroll
+        for (int i = 0; i < SPT / 4; ++i) {
+          const float4 v = nexts[(j * SPT / 4 + i) * kThreads];
+          s[j][2 * i] = make_float2(v.x, v.y);
+          s[j][2 * i + 1] = make_float2(v.z, v.w);
+        }
         if (seg > 0) {
           float2 e[SPT / 2];
           ld_states<SPT>(e, w.s_seg + (srow + j) * a.N + n0, n, vecn);
@@ -458,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, 3) selective_tiles_kernel(s4_selecti
             s[j][i] = fma2(ex2(mul2(make_float2(before, before), A[j][i])), e[i], s[j][i]);
         }
       }
+      if (tile > first) fetch(tile - 1);
       __syncthreads();
       // and at the start of each block
 #pragma unroll 1
@@ -524,18 +619,18 @@ __global__ void __launch_bounds__(kThreads, 3) selective_tiles_kernel(s4_selecti
               y[j] = i + e ? fma2(cv[e], now, y[j]) : mul2(cv[e], now);
               rc = j ? fma2(pp[j], now, rc) : mul2(pp[j], now);
             }
-            r[(u & 1) * SPT + 2 * (i + e)] = rc.x;
-            r[(u & 1) * SPT + 2 * (i + e) + 1] = rc.y;
+            r[u % G::GT * SPT + 2 * (i + e)] = rc.x;
+            r[u % G::GT * SPT + 2 * (i + e) + 1] = rc.y;
           }
         }
 #pragma unroll
         for (int j = 0; j < CPT; ++j) vy[j][u] = y[j].x + y[j].y;
-        if (u & 1) {  // two tokens' dC
+        if (u % G::GT == G::GT - 1) {  // a group's dC
           Sum::run(r, wl);
 #pragma unroll
           for (int e = 0; e < Sum::KEEP; ++e) {
             const int v = Sum::kept(wl, e);
-            red[wid][u - 1 + v / SPT][NP + n0 + v % SPT] = r[e];
+            red[wid][u - (G::GT - 1) + v / SPT][NP + n0 + v % SPT] = r[e];
           }
         }
       }
@@ -569,8 +664,8 @@ __global__ void __launch_bounds__(kThreads, 3) selective_tiles_kernel(s4_selecti
               ww[j] = i + e ? fma2(A[j][i + e], q1, ww[j]) : mul2(A[j][i + e], q1);
               dA[j][i + e] = fma2(dd[j], q1, dA[j][i + e]);
             }
-            r[(u & 1) * SPT + 2 * (i + e)] = rb.x;
-            r[(u & 1) * SPT + 2 * (i + e) + 1] = rb.y;
+            r[u % G::GT * SPT + 2 * (i + e)] = rb.x;
+            r[u % G::GT * SPT + 2 * (i + e) + 1] = rb.y;
           }
         }
 #pragma unroll
@@ -578,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 3) selective_tiles_kernel(s4_selecti
           vu[j][u] = uu[j].x + uu[j].y;
           vw[j][u] = ww[j].x + ww[j].y;
         }
-        if (!(u & 1)) {
+        if (u % G::GT == 0) {
           Sum::run(r, wl);
 #pragma unroll
           for (int e = 0; e < Sum::KEEP; ++e) {
@@ -688,18 +783,19 @@ __global__ void __launch_bounds__(256) selective_vectors_kernel(s4_selective_bwd
   out[(row * a.G + g) * a.N + state] = from_f<T>(v);
 }
 
-// The lanes that hold N states, 8 each.
+// The lanes that hold N states: 4 each in (3), 8 each in (1).
 template <typename F>
 auto with_states(int N, F f) {
-  if (N <= 8) return f(Geo<1, 8>{});
-  if (N <= 16) return f(Geo<2, 8>{});
-  if (N <= 32) return f(Geo<4, 8>{});
-  if (N <= 64) return f(Geo<8, 8>{});
-  if (N <= 128) return f(Geo<16, 8>{});
-  return f(Geo<32, 8>{});
+  if (N <= 4) return f(Geo<1, 4>{}, EndsGeo<1, 8, Geo<1, 4>::TC>{});
+  if (N <= 8) return f(Geo<2, 4>{}, EndsGeo<1, 8, Geo<2, 4>::TC>{});
+  if (N <= 16) return f(Geo<4, 4>{}, EndsGeo<2, 8, Geo<4, 4>::TC>{});
+  if (N <= 32) return f(Geo<8, 4>{}, EndsGeo<4, 8, Geo<8, 4>::TC>{});
+  if (N <= 64) return f(Geo<16, 4>{}, EndsGeo<8, 8, Geo<16, 4>::TC>{});
+  if (N <= 128) return f(Geo<32, 4>{}, EndsGeo<16, 8, Geo<32, 4>::TC>{});
+  return f(Geo<32, 8>{}, EndsGeo<32, 8, Geo<32, 8>::TC>{});
 }
 
-constexpr int kCtas = 6;  // per SM that the segments are meant to give: two rounds of (3)
+constexpr int kCtas = S4_KC;  // per SM that the segments are meant to give: two rounds of (3)
 
 // Sizes and the workspace's layout (pointers relative to a null base when ws is null).
 template <typename G>
@@ -728,32 +824,33 @@ Work layout(int batch, int L, int H, int N, int Gr, char* ws, size_t* total) {
   w.part_h = take(bs * H * (N + 2));
   w.part_bc = take((size_t)w.blocks * batch * L * 2 * G::NP);
   // CTAs of one launch
-  if (total) *total = (long long)chan_blocks<G::CH>(H, Gr) * w.segs > INT_MAX ? 0 : at;
+  if (total) *total = (long long)chan_blocks<2>(H, Gr) * w.segs > INT_MAX ? 0 : at;
   return w;
 }
 
 template <typename T>
 cudaError_t bwd_t(const s4_selective_bwd_args& a, St st, cudaStream_t s) {
   const int e = sizeof(T);
-  with_states(a.N, [&](auto geo) {
+  with_states(a.N, [&](auto geo, auto egeo) {
     using G = decltype(geo);
+    using E = decltype(egeo);
     const auto ok = [&](const auto& r) { return vec_ok(r.p, e, 2 * e, r.batch, r.row); };
     const bool vec = ok(a.x) && ok(a.dt) && ok(a.z) && ok(a.dy) && ok(a.dx) && ok(a.ddt) && ok(a.dz) &&
                      (a.G == 1 || (a.H / a.G) % 2 == 0);
-    constexpr int pb = e * (16 / e < G::VECS ? 16 / e : G::VECS);
+    constexpr int pb = e * (16 / e < E::VECS ? 16 / e : E::VECS);
     const bool vecbc = vec_ok(a.B.p, e, pb, a.B.batch, a.B.row) && vec_ok(a.C.p, e, pb, a.C.batch, a.C.row) &&
                        a.B_group * e % pb == 0 && a.C_group * e % pb == 0;
     const bool vecn = a.N % 4 == 0 && vec_ok(a.A, 4, 16) && vec_ok(a.state0, 4, 16);
     const Work w = layout<G>(a.batch, a.L, a.H, a.N, a.G, static_cast<char*>(a.ws), nullptr);
     const auto run = [&](auto whole) {
       constexpr bool W = decltype(whole)::value;
-      const auto ends = selective_ends_kernel<T, G, W>, tiles = selective_tiles_kernel<T, G, W>;
-      cudaFuncSetAttribute(ends, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kEndsBytes);
-      cudaFuncSetAttribute(tiles, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kBytes);
+      const auto ends = selective_ends_kernel<T, E, W>, tiles = selective_tiles_kernel<T, G, W>;
+      cudaFuncSetAttribute(ends, cudaFuncAttributeMaxDynamicSharedMemorySize, E::kBytes);
+      cudaFuncSetAttribute(tiles, cudaFuncAttributeMaxDynamicSharedMemorySize, G::template kBytes<T>());
       {
         s4impl::TimedLaunch tl("selective_bwd", s);
-        const long long tasks = (long long)chan_blocks<G::CH>(a.H, a.G) * w.segs;
-        ends<<<dim3((unsigned)((tasks + G::WARPS - 1) / G::WARPS), a.batch), kThreads, G::kEndsBytes, s>>>(a, w, vec, vecbc,
+        const long long tasks = (long long)chan_blocks<E::CH>(a.H, a.G) * w.segs;
+        ends<<<dim3((unsigned)((tasks + G::WARPS - 1) / G::WARPS), a.batch), kThreads, E::kBytes, s>>>(a, w, vec, vecbc,
                                                                                                        vecn, st);
       }
       {
@@ -762,13 +859,15 @@ cudaError_t bwd_t(const s4_selective_bwd_args& a, St st, cudaStream_t s) {
         selective_joins_kernel<<<dim3((unsigned)((HN + 127) / 128), a.batch), 128, 0, s>>>(a, w);
       }
       s4impl::TimedLaunch tl("selective_bwd", s);
-      tiles<<<dim3((unsigned)(w.blocks * w.segs), a.batch), kThreads, G::kBytes, s>>>(a, w, vec, vecbc, vecn, st);
+      tiles<<<dim3((unsigned)(w.blocks * w.segs), a.batch), kThreads, G::template kBytes<T>(), s>>>(a, w, vec, vecbc, vecn, st);
     };
     // the tiles of other widths cost a condition per access
-    if (vec && vecbc && a.N == G::NP && (a.H / a.G) % G::HB == 0 && G::LPC <= 4)
-      run(std::true_type{});
-    else
-      run(std::false_type{});
+    bool whole = false;
+    if constexpr (G::LPC <= 8 && (int)G::NP == (int)E::NP) {
+      whole = vec && vecbc && a.N == G::NP && (a.H / a.G) % G::HB == 0;
+      if (whole) run(std::true_type{});
+    }
+    if (!whole) run(std::false_type{});
     {
       s4impl::TimedLaunch tl("selective_bwd", s);
       const long long cols = (long long)a.H * (a.N + 2);
@@ -792,7 +891,7 @@ S4_OOB_COUNTER(oob_selective_bwd)
 
 size_t selective_bwd_bytes(int batch, int L, int H, int N, int G) {
   size_t total = 0;
-  with_states(N, [&](auto geo) { layout<decltype(geo)>(batch, L, H, N, G, nullptr, &total); });
+  with_states(N, [&](auto geo, auto) { layout<decltype(geo)>(batch, L, H, N, G, nullptr, &total); });
   return total;
 }
 
