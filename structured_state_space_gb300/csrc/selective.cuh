@@ -83,6 +83,11 @@ __device__ __forceinline__ void fetch_whole(Pack<T, V>* slot, const T* src) {
 }
 __device__ __forceinline__ void fetched() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// Rows of shared memory, one per token, of one VEC-float vector per channel slot: the floats to add
+// to `row` of them so that the LPC tokens and the slots that a warp writes at once (8 lanes of 16
+// bytes, 16 of 8) lie in different banks.
+constexpr int row_pad(int lpc, int row) { return lpc == 1 ? 0 : lpc <= 4 ? (32 / lpc + 32 - row % 32) % 32 : 8; }
+
 // A CTA's channels: blocks of HB within a group.
 struct Chan {
   int g, h0, hend;  // group, first channel, end of the group's channels

@@ -20,10 +20,7 @@ using namespace s4sel;
 // Four CTAs of four warps per SM: 128 registers a thread.  At 20 warps per SM the registers
 // left do not hold enough exponentials in flight (650 us instead of 564 on one sequence of
 // 65536 tokens, 1024 channels, 16 states, bfloat16), at 14 there are too few warps (647 us).
-#ifndef S4_MB
-#define S4_MB 4
-#endif
-constexpr int kScanThreads = 128, kScanCtas = S4_MB;
+constexpr int kScanThreads = 128, kScanCtas = 4;
 
 template <int LPC_, int SPT_>
 struct Geo {
@@ -32,9 +29,10 @@ struct Geo {
   static constexpr int TT = NP <= 64 ? 8 : 4;            // tokens of a tile
   static constexpr int OWN = TT / 4 * kOwn<LPC>;         // tokens of a tile that a lane stages and finishes
   static constexpr int VECS = TT * NP / 32;              // elements of B, of C that a lane stages
-  // Shared memory of a warp in floats: steps and step x of channel pairs [TT][32 / LPC][4] | B | C [TT][NP]
+  // Shared memory of a warp in floats: steps and step x of channel pairs [TT][DROW] | B | C [TT][NP]
   // | the next tile's x, dt, z [3][OWN][32] packs of 2 | its B, C
-  static constexpr int B0 = TT * 32 / LPC * 4, C0 = B0 + TT * NP, X0 = C0 + TT * NP;
+  static constexpr int DROW = 128 / LPC + row_pad(LPC, 128 / LPC);
+  static constexpr int B0 = TT * DROW, C0 = B0 + TT * NP, X0 = C0 + TT * NP;
   static constexpr int V0 = X0 + 3 * OWN * 32 * 2, END = V0 + 2 * TT * NP;
   static constexpr int kBytes = 4 * END * (kScanThreads / 32);
 };
@@ -64,7 +62,7 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas)
   constexpr int V0 = 16 / (int)sizeof(T), VB = V0 < G::VECS ? V0 : G::VECS, NB = G::VECS / VB;
   extern __shared__ __align__(16) float smem[];
   float* mine = smem + threadIdx.x / 32 * G::END;
-  float4(*sd)[32 / LPC] = reinterpret_cast<float4(*)[32 / LPC]>(mine);
+  float4(*sd)[G::DROW / 4] = reinterpret_cast<float4(*)[G::DROW / 4]>(mine);
   float(*sb)[NP] = reinterpret_cast<float(*)[NP]>(mine + G::B0);
   float(*sc)[NP] = reinterpret_cast<float(*)[NP]>(mine + G::C0);
   record_gen(st);

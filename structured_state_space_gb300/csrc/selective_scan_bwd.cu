@@ -24,8 +24,8 @@ namespace {
 using namespace s4sel;
 #ifndef S4_EB
 #define S4_EB 4
-#define S4_TBK 3
-#define S4_KC 12
+#define S4_TBK 4
+#define S4_KC 24
 #endif
 
 template <int LPC_, int SPT_>
@@ -35,11 +35,13 @@ struct Geo {
   static constexpr int WARPS = kThreads / 32, HB = WARPS * CH;  // and of a CTA
   static constexpr int TC = LPC == 1 ? 8 : 16, TB = 4;   // tokens of a tile, of a block in registers
   static constexpr int OWN = TC / 4 * kOwn<LPC>;         // tokens of a tile that a lane stages and finishes
-  // shared memory in floats: cells [TC][WARPS * SLOTS][2][4] | B, C [TC][NP] | states at blocks | sums of dB, dC
-  static constexpr int B0 = TC * WARPS * SLOTS * 8, C0 = B0 + TC * NP, S0 = C0 + TC * NP;
+  // shared memory in floats: (step, x) and (dyp, dy silu') of channel pairs, [TC][ROW] each | B, C [TC][NP] | states at
+  // blocks | sums of dB, dC [WARPS][TB][RROW]
+  static constexpr int ROW = WARPS * SLOTS * 4 + row_pad(LPC, WARPS * SLOTS * 4), RROW = 2 * NP + 16;
+  static constexpr int B0 = 2 * TC * ROW, C0 = B0 + TC * NP, S0 = C0 + TC * NP;
   // | the tile before: x, dt, z, dy [4][OWN][kThreads] packs of 2 | B, C | its states
   static constexpr int VECS = TC * NP / kThreads > 0 ? TC * NP / kThreads : 1;  // elements of B, of C a thread stages
-  static constexpr int R0 = S0 + TC / TB * kThreads * CPT * SPT, X0 = R0 + WARPS * TB * 2 * NP;
+  static constexpr int R0 = S0 + TC / TB * kThreads * CPT * SPT, X0 = R0 + WARPS * TB * RROW;
   template <typename T>
   static constexpr int V0() { return X0 + 4 * OWN * kThreads * 2 * (int)sizeof(T) / 4; }
   template <typename T>
@@ -48,14 +50,16 @@ struct Geo {
   static constexpr int kBytes() { return 4 * (N0<T>() + kThreads * CPT * SPT); }
   static constexpr int GT = 16 / SPT;                    // tokens whose sums over channels are formed together
 };
-// (1): a warp's tile of TT tokens: steps, inputs, dyp [TT][SLOTS][6 of 8] | B, C [TT][NP]
+// (1): a warp's tile of TT tokens: (step, step x) [TT][DROW] and dyp [TT][PROW] of channel pairs | B, C
+// [TT][NP]
 template <int LPC_, int SPT_, int TC_>
 struct EndsGeo {
   static constexpr int LPC = LPC_, SPT = SPT_, NP = LPC * SPT, CPT = 2, SLOTS = 32 / LPC, CH = SLOTS * CPT;
   static constexpr int TT = LPC == 1 || NP > 64 ? 4 : 8, TC = TC_;  // its tile, and (3)'s
   static constexpr int OWN = TT / 4 * kOwn<LPC>;
   // | the next tile's x, dt, z, dy [4][OWN][32] packs of 2 | its B, C
-  static constexpr int B0 = TT * SLOTS * 8, C0 = B0 + TT * NP, X0 = C0 + TT * NP;
+  static constexpr int DROW = SLOTS * 4 + row_pad(LPC, SLOTS * 4), PROW = SLOTS * 2 + row_pad(LPC, SLOTS * 2);
+  static constexpr int P0 = TT * DROW, B0 = P0 + TT * PROW, C0 = B0 + TT * NP, X0 = C0 + TT * NP;
   static constexpr int V0 = X0 + 4 * OWN * 32 * 2, END = V0 + 2 * TT * NP, kBytes = 4 * END * (kThreads / 32);
   static constexpr int VECS = TT * NP / 32;              // elements of B, of C that a lane stages
 };
@@ -168,7 +172,8 @@ __global__ void __launch_bounds__(kThreads, S4_EB) selective_ends_kernel(s4_sele
   constexpr int V0 = 16 / (int)sizeof(T), VB = V0 < G::VECS ? V0 : G::VECS, NB = G::VECS / VB;
   extern __shared__ __align__(16) float smem[];
   float* mine = smem + threadIdx.x / 32 * G::END;
-  float4(*sd)[G::SLOTS][2] = reinterpret_cast<float4(*)[G::SLOTS][2]>(mine);
+  float4(*sd)[G::DROW / 4] = reinterpret_cast<float4(*)[G::DROW / 4]>(mine);
+  float2(*sp)[G::PROW / 2] = reinterpret_cast<float2(*)[G::PROW / 2]>(mine + G::P0);
   float(*sb)[NP] = reinterpret_cast<float(*)[NP]>(mine + G::B0);
   float(*sc)[NP] = reinterpret_cast<float(*)[NP]>(mine + G::C0);
   record_gen(st);
@@ -260,8 +265,8 @@ __global__ void __launch_bounds__(kThreads, S4_EB) selective_ends_kernel(s4_sele
       sum = add2(sum, d);
       const float2 dx = mul2(d, xv);
       if (LPC <= 4 || lane < 4) {
-        sd[t][slot][0] = make_float4(d.x, d.y, dx.x, dx.y);
-        *reinterpret_cast<float2*>(&sd[t][slot][1]) = pv;
+        sd[t][slot] = make_float4(d.x, d.y, dx.x, dx.y);
+        sp[t][slot] = pv;
       }
     }
 #pragma unroll
@@ -278,8 +283,8 @@ __global__ void __launch_bounds__(kThreads, S4_EB) selective_ends_kernel(s4_sele
     if (tb + TT < live) fetch(tb + TT);
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
-      const float4 d = sd[t][slot][0];
-      const float2 pv = *reinterpret_cast<const float2*>(&sd[t][slot][1]);
+      const float4 d = sd[t][slot];
+      const float2 pv = sp[t][slot];
       const float2 dd[CPT] = {make_float2(d.x, d.x), make_float2(d.y, d.y)};
       const float2 xx[CPT] = {make_float2(d.z, d.z), make_float2(d.w, d.w)};
       const float2 pp[CPT] = {make_float2(pv.x, pv.x), make_float2(pv.y, pv.y)};
@@ -380,6 +385,19 @@ struct SumSlots {
     const int slot = wl / LPC;
     return SLOTS == 32 ? slot / 2 : slot * KEEP + k;
   }
+  // The kept sums where at(value) says (neighbouring values are neighbours there, in fours).
+  template <typename At>
+  static __device__ __forceinline__ void put(const float (&r)[16], int wl, At at) {
+    if constexpr (KEEP == 1) {
+      *at(kept(wl, 0)) = r[0];
+    } else if constexpr (KEEP == 2) {
+      *reinterpret_cast<float2*>(at(kept(wl, 0))) = make_float2(r[0], r[1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < KEEP; e += 4)
+        *reinterpret_cast<float4*>(at(kept(wl, e))) = make_float4(r[e], r[e + 1], r[e + 2], r[e + 3]);
+    }
+  }
 };
 
 // (1 - e^-d) / d is the softplus' derivative over the softplus d.  For d < 1/2 a polynomial, the
@@ -401,11 +419,12 @@ __global__ void __launch_bounds__(kThreads, S4_TBK) selective_tiles_kernel(s4_se
   constexpr int LPC = G::LPC, SPT = G::SPT, CPT = G::CPT, NP = G::NP, CH = G::CH, TC = G::TC, TB = G::TB, OWN = G::OWN;
   using Sum = SumSlots<LPC>;
   extern __shared__ __align__(16) float smem[];
-  float4(*cells)[G::WARPS * G::SLOTS][2] = reinterpret_cast<float4(*)[G::WARPS * G::SLOTS][2]>(smem);
+  float4(*steps)[G::ROW / 4] = reinterpret_cast<float4(*)[G::ROW / 4]>(smem);
+  float4(*outs)[G::ROW / 4] = reinterpret_cast<float4(*)[G::ROW / 4]>(smem + TC * G::ROW);
   float(*sb)[NP] = reinterpret_cast<float(*)[NP]>(smem + G::B0);
   float(*sc)[NP] = reinterpret_cast<float(*)[NP]>(smem + G::C0);
   float4* keep = reinterpret_cast<float4*>(smem + G::S0) + threadIdx.x;
-  float(*red)[TB][2 * NP] = reinterpret_cast<float(*)[TB][2 * NP]>(smem + G::R0);
+  float(*red)[TB][G::RROW] = reinterpret_cast<float(*)[TB][G::RROW]>(smem + G::R0);
   const int b = blockIdx.y, seg = blockIdx.x / w.blocks, block = blockIdx.x % w.blocks;
   const int wid = threadIdx.x / 32, wl = threadIdx.x & 31;
   const Chan c = chan_of<G::HB>(block, a.H / a.G);
@@ -515,8 +534,8 @@ __global__ void __launch_bounds__(kThreads, S4_TBK) selective_tiles_kernel(s4_se
       eval_cell<T>(next.get(k, z), z != nullptr, a.softplus, bias, d, xv, pv, zf);
       if (t >= live) d = make_float2(0.f, 0.f);
       if (LPC <= 4 || lane < 4) {
-        cells[t][cs][0] = make_float4(d.x, d.y, xv.x, xv.y);
-        cells[t][cs][1] = make_float4(pv.x, pv.y, zf.x, zf.y);
+        steps[t][cs] = make_float4(d.x, d.y, xv.x, xv.y);
+        outs[t][cs] = make_float4(pv.x, pv.y, zf.x, zf.y);
       }
     }
 #pragma unroll
@@ -564,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, S4_TBK) selective_tiles_kernel(s4_se
 #pragma unroll
         for (int u = 0; u < TB; ++u) {
           const int t = k * TB + u;
-          const float4 d = cells[t][cs][0];
+          const float4 d = steps[t][cs];
           const float2 dd[CPT] = {make_float2(d.x, d.x), make_float2(d.y, d.y)};
           const float2 dx = mul2(make_float2(d.x, d.y), make_float2(d.z, d.w));
           const float2 xx[CPT] = {make_float2(dx.x, dx.x), make_float2(dx.y, dx.y)};
@@ -596,8 +615,8 @@ __global__ void __launch_bounds__(kThreads, S4_TBK) selective_tiles_kernel(s4_se
 #pragma unroll
       for (int u = 0; u < TB; ++u) {
         const int t = k * TB + u;
-        const float4 d = cells[t][cs][0];
-        const float2 pv = *reinterpret_cast<const float2*>(&cells[t][cs][1]);
+        const float4 d = steps[t][cs];
+        const float2 pv = *reinterpret_cast<const float2*>(&outs[t][cs]);
         const float2 dd[CPT] = {make_float2(d.x, d.x), make_float2(d.y, d.y)};
         const float2 dx = mul2(make_float2(d.x, d.y), make_float2(d.z, d.w));
         const float2 xx[CPT] = {make_float2(dx.x, dx.x), make_float2(dx.y, dx.y)};
@@ -627,19 +646,15 @@ __global__ void __launch_bounds__(kThreads, S4_TBK) selective_tiles_kernel(s4_se
         for (int j = 0; j < CPT; ++j) vy[j][u] = y[j].x + y[j].y;
         if (u % G::GT == G::GT - 1) {  // a group's dC
           Sum::run(r, wl);
-#pragma unroll
-          for (int e = 0; e < Sum::KEEP; ++e) {
-            const int v = Sum::kept(wl, e);
-            red[wid][u - (G::GT - 1) + v / SPT][NP + n0 + v % SPT] = r[e];
-          }
+          Sum::put(r, wl, [&](int v) { return &red[wid][u - (G::GT - 1) + v / SPT][NP + n0 + v % SPT]; });
         }
       }
       // backward: the gradients of the states, dB, u, w, dA
 #pragma unroll
       for (int u = TB - 1; u >= 0; --u) {
         const int t = k * TB + u;
-        const float4 d = cells[t][cs][0];
-        const float2 pv = *reinterpret_cast<const float2*>(&cells[t][cs][1]);
+        const float4 d = steps[t][cs];
+        const float2 pv = *reinterpret_cast<const float2*>(&outs[t][cs]);
         const float2 dd[CPT] = {make_float2(d.x, d.x), make_float2(d.y, d.y)};
         const float2 dx = mul2(make_float2(d.x, d.y), make_float2(d.z, d.w));
         const float2 xx[CPT] = {make_float2(dx.x, dx.x), make_float2(dx.y, dx.y)};
@@ -675,11 +690,7 @@ __global__ void __launch_bounds__(kThreads, S4_TBK) selective_tiles_kernel(s4_se
         }
         if (u % G::GT == 0) {
           Sum::run(r, wl);
-#pragma unroll
-          for (int e = 0; e < Sum::KEEP; ++e) {
-            const int v = Sum::kept(wl, e);
-            red[wid][u + v / SPT][n0 + v % SPT] = r[e];
-          }
+          Sum::put(r, wl, [&](int v) { return &red[wid][u + v / SPT][n0 + v % SPT]; });
         }
       }
       // the block's tokens, each finished by the lane that owns it
@@ -692,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, S4_TBK) selective_tiles_kernel(s4_se
 #pragma unroll
       for (int i = 0; i < kOwn<LPC>; ++i) {
         const int t = k * TB + own_token<LPC>(lane, i);
-        const float4 c0 = cells[t][cs][0], c1 = cells[t][cs][1];
+        const float4 c0 = steps[t][cs], c1 = outs[t][cs];
         const float d[2] = {c0.x, c0.y}, xv[2] = {c0.z, c0.w}, pv[2] = {c1.x, c1.y}, zf[2] = {c1.z, c1.w};
         const float Dj[2] = {Dv.x, Dv.y};
         float o1[2], o2[2], o3[2], od[2];
