@@ -139,6 +139,28 @@ __device__ __forceinline__ void st_whole(T* p, const float (&v)[V]) {
   st_f<T, V>(p, V, true, v);
 }
 
+// ---- packs on their way from global to shared memory -----------------------------------------
+// A pack is copied asynchronously into a slot of the thread's own, which the thread alone reads
+// back after fetched(): the next tile's data then waits in no registers.  Packs of less than 4
+// bytes, and those that may not be read whole, go through registers.
+template <typename T, int V>
+__device__ __forceinline__ void fetch_whole(Pack<T, V>* slot, const T* src) {
+  constexpr int BYTES = Pack<T, V>::BYTES;
+  if constexpr (BYTES >= 4) {
+#pragma unroll
+    for (int i = 0; i < BYTES; i += 16)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(s4dev::smem_u32(slot) + i),
+                   "l"(reinterpret_cast<const char*>(src) + i), "n"(BYTES < 16 ? BYTES : 16)
+                   : "memory");
+  } else
+    *slot = ld_whole<T, V>(src);
+}
+// All but the thread's last N commits of copies are done (fetched(): all copies).
+template <int N>
+__device__ __forceinline__ void fetched_but() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void fetched() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // v sigmoid(v) and its derivative.  sigmoid = 1 / (1 + 2^(-v log2 e)) to about 2^-22, more for
 // large negative v by |v| 2^-24 (the exponent's rounding); it tends to 0 and 1 without
 // overflow trouble (2^.. = inf gives 0).

@@ -69,20 +69,6 @@ __device__ __forceinline__ float2 softplus2(float2 v) {
   return fma2(s, p, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
 }
 
-// ---- packs on their way from global to shared memory -----------------------------------------
-// A pack is copied asynchronously into a slot of the thread's own, which the thread alone reads
-// back after fetched(): the next tile's data then waits in no registers.  Packs of less than 4
-// bytes, and those that may not be read whole, go through registers.
-template <typename T, int V>
-__device__ __forceinline__ void fetch_whole(Pack<T, V>* slot, const T* src) {
-  constexpr int BYTES = Pack<T, V>::BYTES;
-  if constexpr (BYTES >= 4)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(s4dev::smem_u32(slot)), "l"(src), "n"(BYTES) : "memory");
-  else
-    *slot = ld_whole<T, V>(src);
-}
-__device__ __forceinline__ void fetched() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 // Rows of shared memory, one per token, of one VEC-float vector per channel slot: the floats to add
 // to `row` of them so that the LPC tokens and the slots that a warp writes at once (8 lanes of 16
 // bytes, 16 of 8) lie in different banks.

@@ -17,7 +17,7 @@ using s4impl::St;
 constexpr int kSegFwd = 16;   // tokens of a thread's segment, forward
 constexpr int kSegBwd = 64;   // and backward
 constexpr int kThreads = 128;
-constexpr int kWarpsBwd = 8;
+constexpr int kWarpsBwd = 8, kVecBwd = 4;
 
 template <typename T, int KW, int V>
 __global__ void __launch_bounds__(kThreads) short_conv_kernel(s4_short_conv_args a, bool vec, St st) {
@@ -102,12 +102,25 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(s4_short_conv_args
 // Backward.  dv_t = dy_t silu'(v_t) with v_t formed again from the window; token t - (KW-1)'s
 // dx is complete once dv_t is known.  A CTA is 8 warps along time and 32 lanes along
 // channels; the filter's gradients are summed in registers, then over the CTA's warps,
-// and leave as one row of partial sums per CTA.
+// and leave as one row of partial sums per CTA.  Inputs arrive by asynchronous copies into slots of
+// the thread's own, kAhead groups of KW tokens ahead: at two CTAs per SM (the window, the filter
+// and its sums take 115 registers; one CTA with 8 taps) that keeps 128 KB or more per SM on their way.
+template <typename T, int KW>
+constexpr int kAhead = sizeof(T) == 4 ? 2 : KW == 4 ? 4 : 5;
 template <typename T, int KW, int V>
-__global__ void __launch_bounds__(32 * kWarpsBwd) short_conv_bwd_kernel(s4_short_conv_bwd_args a, bool vec, float* part,
-                                                                       St st) {
+constexpr int bwd_slot_bytes() { return (kAhead<T, KW> + 1) * 2 * KW * 32 * kWarpsBwd * Pack<T, V>::BYTES; }
+template <int KW, int V>
+constexpr int bwd_red_bytes() { return 4 * kWarpsBwd * (KW + 1) * V * 33; }
+
+template <typename T, int KW, int V>
+__global__ void __launch_bounds__(32 * kWarpsBwd, KW == 4 ? 2 : 1)
+    short_conv_bwd_kernel(s4_short_conv_bwd_args a, bool vec, float* part, St st) {
   record_gen(st);
-  __shared__ float red[kWarpsBwd][(KW + 1) * V][33];
+  extern __shared__ __align__(16) char conv_smem[];
+  float(*red)[(KW + 1) * V][33] = reinterpret_cast<float(*)[(KW + 1) * V][33]>(conv_smem);
+  constexpr int AHEAD = kAhead<T, KW>;
+  // slots [AHEAD + 1][x, dy][KW][threads]; the sums over the CTA come after the last use of them
+  Pack<T, V>* slots = reinterpret_cast<Pack<T, V>*>(conv_smem) + threadIdx.x;
   const int b = blockIdx.z, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const Seq q = seq_of(a.lengths, nullptr, b, a.L, 0, st);
   const int h = (blockIdx.x * 32 + lane) * V, n = min(V, a.H - h);
@@ -147,27 +160,44 @@ __global__ void __launch_bounds__(32 * kWarpsBwd) short_conv_bwd_kernel(s4_short
         ld_f<T, V>(state + (t + a.W - 1) * (long long)a.H, n, vec, win[k]);
     }
     // token t of the loop: dv_t, and dx of token t - (KW - 1)
-    for (int tb = t0; tb < t1 + KW - 1; tb += KW) {
-      Pack<T, V> xi[KW], di[KW];
+    const int tend = min(t1 + KW - 1, q.len);
+    const bool whole = vec && n >= V;
+    const auto slot = [&](int g, int which, int u) -> Pack<T, V>& {
+      return slots[((g % (AHEAD + 1) * 2 + which) * KW + u) * 32 * kWarpsBwd];
+    };
+    const auto fetch = [&](int g) {
 #pragma unroll
       for (int u = 0; u < KW; ++u) {
-        const int t = tb + u;
-        if (t < min(t1 + KW - 1, q.len) && S4_IN(t, a.L)) {
-          xi[u] = ld_pack<T, V>(x + t * a.x.row, n, vec);
-          di[u] = ld_pack<T, V>(dy + t * a.dy.row, n, vec);
+        const int t = t0 + g * KW + u;
+        if (t >= tend || !S4_IN(t, a.L)) continue;
+        if (whole) {
+          fetch_whole<T, V>(&slot(g, 0, u), x + t * a.x.row);
+          fetch_whole<T, V>(&slot(g, 1, u), dy + t * a.dy.row);
+        } else {
+          slot(g, 0, u) = ld_pack<T, V>(x + t * a.x.row, n, vec);
+          slot(g, 1, u) = ld_pack<T, V>(dy + t * a.dy.row, n, vec);
         }
       }
+      fetch_commit();
+    };
+#pragma unroll
+    for (int g = 0; g < AHEAD; ++g) fetch(g);
+    for (int tb = t0; tb < t1 + KW - 1; tb += KW) {
+      const int gr = (tb - t0) / KW;
+      fetch(gr + AHEAD);
+      fetched_but<AHEAD>();
 #pragma unroll
       for (int u = 0; u < KW; ++u) {
         const int t = tb + u;
         if (t >= t1 + KW - 1) break;
         const bool own = t < t1;
         if (t < q.len) {
+          const Pack<T, V> xi = slot(gr, 0, u), di = slot(gr, 1, u);
 #pragma unroll
-          for (int i = 0; i < V; ++i) win[(KW - 1 + u) % KW][i] = xi[u].get(i);
+          for (int i = 0; i < V; ++i) win[(KW - 1 + u) % KW][i] = xi.get(i);
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            float d = di[u].get(i);
+            float d = di.get(i);
             if (a.silu) {
               float v = bias[i];
 #pragma unroll
@@ -212,6 +242,8 @@ __global__ void __launch_bounds__(32 * kWarpsBwd) short_conv_bwd_kernel(s4_short
       }
     }
   }
+  fetched();
+  __syncthreads();  // the slots become the sums
 #pragma unroll
   for (int k = 0; k <= KW; ++k)
 #pragma unroll
@@ -261,7 +293,7 @@ dim3 bwd_grid(int batch, int L, int H) {
 
 template <typename T>
 cudaError_t bwd_t(const s4_short_conv_bwd_args& a, St st, cudaStream_t s) {
-  constexpr int V = 4;
+  constexpr int V = kVecBwd;
   const int e = sizeof(T), bytes = sizeof(Pack<T, V>);
   const bool vec = vec_ok(a.x.p, e, bytes, a.x.batch, a.x.row) && vec_ok(a.dy.p, e, bytes, a.dy.batch, a.dy.row) &&
                    vec_ok(a.dx.p, e, bytes, a.dx.batch, a.dx.row) && vec_ok(a.state0, e, bytes, a.H) &&
@@ -270,10 +302,15 @@ cudaError_t bwd_t(const s4_short_conv_bwd_args& a, St st, cudaStream_t s) {
   const dim3 grid = bwd_grid(a.batch, a.L, a.H);
   {
     s4impl::TimedLaunch tl("short_conv_bwd", s);
+    const auto run = [&](auto kernel, int bytes) {
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      kernel<<<grid, 32 * kWarpsBwd, bytes, s>>>(a, vec, part, st);
+    };
+    const auto most = [](int x, int y) { return x > y ? x : y; };
     if (a.W <= 4)
-      short_conv_bwd_kernel<T, 4, V><<<grid, 32 * kWarpsBwd, 0, s>>>(a, vec, part, st);
+      run(short_conv_bwd_kernel<T, 4, V>, most(bwd_slot_bytes<T, 4, V>(), bwd_red_bytes<4, V>()));
     else
-      short_conv_bwd_kernel<T, 8, V><<<grid, 32 * kWarpsBwd, 0, s>>>(a, vec, part, st);
+      run(short_conv_bwd_kernel<T, 8, V>, most(bwd_slot_bytes<T, 8, V>(), bwd_red_bytes<8, V>()));
   }
   s4impl::TimedLaunch tl("short_conv_bwd", s);
   const long long cols = (long long)(a.W + 1) * a.H;
