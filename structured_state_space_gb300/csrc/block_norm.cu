@@ -40,281 +40,292 @@ __device__ __forceinline__ float group_sum(float v, float (&red)[2][2][32], int&
   return s[0];
 }
 
-// NV packs of V channels per thread, pack i at channel (lane + i * width) V.
-template <typename T, typename R, int V, int NV, bool CTA>
+// A pack of parameters as pairs; `with` where there are none.
+template <int V>
+__device__ __forceinline__ void ld_param(float2 (&v)[V / 2], const float* p, int c, int n, bool vec, float with) {
+  if (p) {
+    to_pairs<float, V>(ld_pack<float, V>(p + c, n, vec), v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) v[i] = make_float2(with, with);
+  }
+}
+__device__ __forceinline__ float both(float2 v) { return v.x + v.y; }
+__device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
+
+// The rows that a group has on their way: with AHEAD, a row's packs are copied into slots of the
+// thread's own (two sets of them) while the row before is worked on; else they are read
+// when they are needed.  [2][NT][threads] packs of T, then [2][NR][threads] of R.
+template <typename T, typename R, int V, int NT, int NR, bool AHEAD>
+struct Rows {
+  Pack<T, V>* st;
+  Pack<R, V>* sr;
+  __device__ __forceinline__ Rows(char* smem)
+      : st(reinterpret_cast<Pack<T, V>*>(smem) + threadIdx.x),
+        sr(reinterpret_cast<Pack<R, V>*>(smem + 2 * NT * Pack<T, V>::BYTES * blockDim.x) + threadIdx.x) {}
+  __device__ __forceinline__ void fetch_t(int stage, int which, const T* p) {
+    fetch_whole<T, V>(st + (stage * NT + which) * blockDim.x, p);
+  }
+  __device__ __forceinline__ void fetch_r(int stage, int which, const R* p) {
+    fetch_whole<R, V>(sr + (stage * NR + which) * blockDim.x, p);
+  }
+  __device__ __forceinline__ void get_t(int stage, int which, const T* p, int n, bool vec, float2 (&v)[V / 2]) const {
+    to_pairs<T, V>(AHEAD ? st[(stage * NT + which) * blockDim.x] : ld_pack<T, V>(p, n, vec), v);
+  }
+  __device__ __forceinline__ void get_r(int stage, int which, const R* p, int n, bool vec, float2 (&v)[V / 2]) const {
+    to_pairs<R, V>(AHEAD ? sr[(stage * NR + which) * blockDim.x] : ld_pack<R, V>(p, n, vec), v);
+  }
+};
+
+template <typename T, typename R, int V, int NT, int NR>
+constexpr int kRowBytes = 2 * (NT * Pack<T, V>::BYTES + NR * Pack<R, V>::BYTES);  // per thread
+
+// NV packs of V channels per thread, pack i at channel (lane + i * width) V.  Groups walk over the
+// rows.  What is absent is neutral: a weight of 1, a residual of 0 (without w_post r1 is 1).
+template <typename T, typename R, int V, int NV, bool CTA, bool AHEAD>
 __global__ void __launch_bounds__(CTA ? kMaxThreads : 128) block_norm_kernel(s4_block_norm_args a, bool vec) {
+  static_assert(!AHEAD || NV == 1, "");
   __shared__ float red[2][2][32];
-  int phase = 0;
+  extern __shared__ __align__(16) char norm_smem[];
+  int phase = 0, stage = 0;
   const int width = CTA ? blockDim.x : 32, lane = CTA ? threadIdx.x : threadIdx.x & 31;
-  const long long row = CTA ? (long long)blockIdx.x : (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (row >= a.rows) return;  // whole groups only
-  const T* o = static_cast<const T*>(a.o) + row * a.o_row;
-  const T* gate = a.gate ? static_cast<const T*>(a.gate) + row * a.gate_row : nullptr;
-  const R* h = a.h ? static_cast<const R*>(a.h) + row * a.h_row : nullptr;
-  float v[NV][V], hv[NV][V];
-  float ss = 0.f;
+  const int per = CTA ? 1 : blockDim.x >> 5;
+  const long long first = (long long)blockIdx.x * per + (CTA ? 0 : threadIdx.x >> 5), step = (long long)gridDim.x * per;
+  const float inv = 1.f / (float)a.H;
+  Rows<T, R, V, 2, 1, AHEAD> rows(norm_smem);
+  const auto fetch = [&](long long row, int stage) {
+    const int c = lane * V;
+    if (row < a.rows && c < a.H && S4_IN(row, a.rows)) {
+      rows.fetch_t(stage, 0, static_cast<const T*>(a.o) + row * a.o_row + c);
+      if (a.gate) rows.fetch_t(stage, 1, static_cast<const T*>(a.gate) + row * a.gate_row + c);
+      if (a.h) rows.fetch_r(stage, 0, static_cast<const R*>(a.h) + row * a.h_row + c);
+    }
+    fetch_commit();
+  };
+  if (AHEAD) fetch(first, 0);
+  for (long long row = first; row < a.rows; row += step, stage ^= 1) {
+    if (AHEAD) {
+      fetch(row + step, stage ^ 1);
+      fetched_but<1>();
+    }
+    float2 v[NV][V / 2], hv[NV][V / 2], ss = two(0.f);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (lane + i * width) * V, n = a.H - c;
+    for (int i = 0; i < NV; ++i) {
+      const int c = (lane + i * width) * V, n = a.H - c;
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[i][j] = hv[i][j] = 0.f;
-    if (n > 0 && S4_IN(c, a.H) && S4_IN(row, a.rows)) {
-      ld_f<T, V>(o + c, n, vec, v[i]);
-      if (h) ld_f<R, V>(h + c, n, vec, hv[i]);
-      if (gate) {
-        float g[V];
-        ld_f<T, V>(gate + c, n, vec, g);
+      for (int j = 0; j < V / 2; ++j) v[i][j] = hv[i][j] = two(0.f);
+      if (n <= 0 || !S4_IN(c, a.H) || !S4_IN(row, a.rows)) continue;
+      rows.get_t(stage, 0, static_cast<const T*>(a.o) + row * a.o_row + c, n, vec, v[i]);
+      if (a.h) rows.get_r(stage, 0, static_cast<const R*>(a.h) + row * a.h_row + c, n, vec, hv[i]);
+      if (a.gate) {
+        float2 g[V / 2];
+        rows.get_t(stage, 1, static_cast<const T*>(a.gate) + row * a.gate_row + c, n, vec, g);
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[i][j] = j < n ? v[i][j] * silu(g[j]) : 0.f;
+        for (int j = 0; j < V / 2; ++j) v[i][j] = mul2(v[i][j], silu(g[j]));
       }
 #pragma unroll
-      for (int j = 0; j < V; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+      for (int j = 0; j < V / 2; ++j) ss = fma2(v[i][j], v[i][j], ss);
     }
-  }
-  float r1 = 1.f;
-  if (a.w_post) r1 = rsqrtf(group_sum<CTA>(ss, red, phase) / (float)a.H + a.eps);
-  ss = 0.f;
+    float r1 = 1.f;
+    if (a.w_post) r1 = rsqrtf(group_sum<CTA>(both(ss), red, phase) * inv + a.eps);
+    ss = two(0.f);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (lane + i * width) * V, n = a.H - c;
-    if (n <= 0) continue;
-    float w[V], sc[V];
-    if (a.w_post) ld_f<float, V>(a.w_post + c, n, vec, w);
-    if (a.scale) ld_f<float, V>(a.scale + c, n, vec, sc);
+    for (int i = 0; i < NV; ++i) {
+      const int c = (lane + i * width) * V, n = a.H - c;
+      if (n <= 0) continue;
+      float2 w[V / 2], sc[V / 2];
+      ld_param<V>(w, a.w_post, c, n, vec, 1.f);
+      ld_param<V>(sc, a.scale, c, n, vec, 1.f);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float p = a.w_post ? v[i][j] * r1 * w[j] : v[i][j];
-      hv[i][j] = a.scale ? fmaf(sc[j], p, hv[i][j]) : hv[i][j] + p;
-      ss = fmaf(hv[i][j], hv[i][j], ss);
+      for (int j = 0; j < V / 2; ++j) {
+        hv[i][j] = fma2(sc[j], mul2(mul2(v[i][j], two(r1)), w[j]), hv[i][j]);
+        ss = fma2(hv[i][j], hv[i][j], ss);
+      }
+      st_pairs<R, V>(static_cast<R*>(a.h_out) + row * a.h_out_row + c, n, vec, hv[i]);
     }
-    st_f<R, V>(static_cast<R*>(a.h_out) + row * a.h_out_row + c, n, vec, hv[i]);
-  }
-  if (!a.w_pre) return;
-  const float r2 = rsqrtf(group_sum<CTA>(ss, red, phase) / (float)a.H + a.eps);
+    if (!a.w_pre) continue;
+    const float r2 = rsqrtf(group_sum<CTA>(both(ss), red, phase) * inv + a.eps);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (lane + i * width) * V, n = a.H - c;
-    if (n <= 0) continue;
-    float w[V];
-    ld_f<float, V>(a.w_pre + c, n, vec, w);
+    for (int i = 0; i < NV; ++i) {
+      const int c = (lane + i * width) * V, n = a.H - c;
+      if (n <= 0) continue;
+      float2 w[V / 2];
+      ld_param<V>(w, a.w_pre, c, n, vec, 1.f);
 #pragma unroll
-    for (int j = 0; j < V; ++j) w[j] *= hv[i][j] * r2;
-    st_f<T, V>(static_cast<T*>(a.y) + row * a.y_row + c, n, vec, w);
+      for (int j = 0; j < V / 2; ++j) w[j] = mul2(mul2(hv[i][j], two(r2)), w[j]);
+      st_pairs<T, V>(static_cast<T*>(a.y) + row * a.y_row + c, n, vec, w);
+    }
   }
 }
 
-// Backward, with unit = v r1, unit2 = h' r2:
-//   dh = dh' + r2 (dy w_pre - unit2 mean(dy w_pre unit2)),  dw_pre = sum_rows dy unit2
-//   dp = scale dh,  dscale = sum_rows dh p,  dw_post = sum_rows dp unit
-//   dv = r1 (dp w_post - unit mean(dp w_post unit)),  do = dv silu(gate),  dgate = dv o silu'(gate)
-// Three rounds of reductions per row: the mean of v^2; with f = dy w_pre, those of h'^2 and f h', which
-// give mean(f unit2) = r2 mean(f h'); and the last mean.  (dh being linear in sums that do not need
+// Backward, with unit = v r1, unit2 = h' r2, f = dy w_pre, q = scale w_post:
+//   dh = dh' + r2 (f - unit2 mean(f unit2)),  dw_pre = sum_rows dy unit2
+//   dv = r1 (q dh - unit mean(q dh unit)),  do = dv silu(gate),  dgate = dv o silu'(gate)
+//   U = sum_rows dh unit,  dw_post = scale U,  dscale = w_post U
+// Three rounds of reductions per row: the mean of v^2; those of h'^2 and f h', which give
+// mean(f unit2) = r2 mean(f h'); and the last mean.  (dh being linear in sums that do not need
 // r2, the third could go with the second, but where the two terms of dv nearly cancel that
-// costs them their last digits.)  A group walks over rows with the three column sums of its channels in registers and leaves
-// them as one row of partial sums.  AHEAD: the next row's reads are copied into slots of the
-// thread's own meanwhile; at two CTAs per SM nothing else would be on its way during the sums
-// (16384 rows of 2048 channels in bfloat16: 306 us without).
-template <typename T, typename R, int V>
-struct RowSlots {  // per thread, [..][blockDim.x]
-  static constexpr int kBytes = 3 * Pack<T, V>::BYTES + 2 * Pack<R, V>::BYTES;
-};
+// costs them their last digits.)  A group walks over rows with the two column sums of its
+// channels in registers and leaves them as one row of partial sums.
 template <typename T, typename R, int V, int NV, bool CTA, bool AHEAD>
 __global__ void __launch_bounds__(CTA ? kMaxThreads : 128)
     block_norm_bwd_kernel(s4_block_norm_bwd_args a, bool vec, float* part) {
   static_assert(!AHEAD || NV == 1, "");
   __shared__ float red[2][2][32];
   extern __shared__ __align__(16) char norm_smem[];
-  int phase = 0;
+  int phase = 0, stage = 0;
   const int width = CTA ? blockDim.x : 32, lane = CTA ? threadIdx.x : threadIdx.x & 31;
   const int per = CTA ? 1 : blockDim.x >> 5;
   const long long first = (long long)blockIdx.x * per + (CTA ? 0 : threadIdx.x >> 5), step = (long long)gridDim.x * per;
   const float inv = 1.f / (float)a.H;
   const bool with_dy = a.dy && a.w_pre;
-  float s_post[NV][V], s_scale[NV][V], s_pre[NV][V];
+  float2 U[NV][V / 2], s_pre[NV][V / 2];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < V; ++j) s_post[i][j] = s_scale[i][j] = s_pre[i][j] = 0.f;
+    for (int j = 0; j < V / 2; ++j) U[i][j] = s_pre[i][j] = two(0.f);
 
-  // slots [2][o, gate, dy][threads] of T, then [2][h, dh'][threads] of R
-  Pack<T, V>* st = reinterpret_cast<Pack<T, V>*>(norm_smem) + threadIdx.x;
-  Pack<R, V>* sr = reinterpret_cast<Pack<R, V>*>(norm_smem + 6 * Pack<T, V>::BYTES * blockDim.x) + threadIdx.x;
-  const int c0 = lane * V, n0 = a.H - c0;
+  Rows<T, R, V, 3, 2, AHEAD> rows(norm_smem);
   const auto fetch = [&](long long row, int stage) {
-    if (row < a.rows && n0 >= V && S4_IN(row, a.rows)) {
-      Pack<T, V>* t = st + stage * 3 * blockDim.x;
-      Pack<R, V>* r = sr + stage * 2 * blockDim.x;
-      fetch_whole<T, V>(t, static_cast<const T*>(a.o) + row * a.o_row + c0);
-      if (a.gate) fetch_whole<T, V>(t + blockDim.x, static_cast<const T*>(a.gate) + row * a.gate_row + c0);
-      if (with_dy) fetch_whole<T, V>(t + 2 * blockDim.x, static_cast<const T*>(a.dy) + row * a.dy_row + c0);
-      if (a.h && with_dy) fetch_whole<R, V>(r, static_cast<const R*>(a.h) + row * a.h_row + c0);
-      if (a.dh_out) fetch_whole<R, V>(r + blockDim.x, static_cast<const R*>(a.dh_out) + row * a.dh_out_row + c0);
+    const int c = lane * V;
+    if (row < a.rows && c < a.H && S4_IN(row, a.rows)) {
+      rows.fetch_t(stage, 0, static_cast<const T*>(a.o) + row * a.o_row + c);
+      if (a.gate) rows.fetch_t(stage, 1, static_cast<const T*>(a.gate) + row * a.gate_row + c);
+      if (with_dy) rows.fetch_t(stage, 2, static_cast<const T*>(a.dy) + row * a.dy_row + c);
+      if (a.h && with_dy) rows.fetch_r(stage, 0, static_cast<const R*>(a.h) + row * a.h_row + c);
+      if (a.dh_out) rows.fetch_r(stage, 1, static_cast<const R*>(a.dh_out) + row * a.dh_out_row + c);
     }
     fetch_commit();
   };
   if (AHEAD) fetch(first, 0);
-  int stage = 0;
   for (long long row = first; row < a.rows; row += step, stage ^= 1) {
     const T* o = static_cast<const T*>(a.o) + row * a.o_row;
     const T* gate = a.gate ? static_cast<const T*>(a.gate) + row * a.gate_row : nullptr;
-    const R* h = a.h ? static_cast<const R*>(a.h) + row * a.h_row : nullptr;
-    const T* dy = with_dy ? static_cast<const T*>(a.dy) + row * a.dy_row : nullptr;
-    const R* dho = a.dh_out ? static_cast<const R*>(a.dh_out) + row * a.dh_out_row : nullptr;
-    Pack<T, V>* t = st + stage * 3 * blockDim.x;
-    Pack<R, V>* r = sr + stage * 2 * blockDim.x;
     if (AHEAD) {
       fetch(row + step, stage ^ 1);
       fetched_but<1>();
     }
-    // array `which` of the row's pack i
-    const auto ld_t = [&](int which, const T* p, int i, float (&v)[V]) {
-      const int c = (lane + i * width) * V, n = a.H - c;
-      if (AHEAD) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = t[which * blockDim.x].get(j);
-      } else {
-        ld_f<T, V>(p + c, n, vec, v);
-      }
-    };
-    const auto ld_r = [&](int which, const R* p, int i, float (&v)[V]) {
-      const int c = (lane + i * width) * V, n = a.H - c;
-      if (AHEAD) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = r[which * blockDim.x].get(j);
-      } else {
-        ld_f<R, V>(p + c, n, vec, v);
-      }
-    };
-    float v[NV][V], hv[NV][V], d[NV][V];
-    float ss = 0.f;
+    float2 v[NV][V / 2], hv[NV][V / 2], d[NV][V / 2], ss = two(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (lane + i * width) * V, n = a.H - c;
 #pragma unroll
-      for (int j = 0; j < V; ++j) v[i][j] = hv[i][j] = d[i][j] = 0.f;
+      for (int j = 0; j < V / 2; ++j) v[i][j] = hv[i][j] = d[i][j] = two(0.f);
       if (n <= 0 || !S4_IN(c, a.H)) continue;
-      ld_t(0, o, i, v[i]);
-      if (h && dy) ld_r(0, h, i, hv[i]);
-      if (dy) ld_t(2, dy, i, d[i]);
+      rows.get_t(stage, 0, o + c, n, vec, v[i]);
+      if (with_dy) {
+        rows.get_t(stage, 2, static_cast<const T*>(a.dy) + row * a.dy_row + c, n, vec, d[i]);
+        if (a.h) rows.get_r(stage, 0, static_cast<const R*>(a.h) + row * a.h_row + c, n, vec, hv[i]);
+      }
       if (gate) {
-        float g[V];
-        ld_t(1, gate, i, g);
+        float2 g[V / 2];
+        rows.get_t(stage, 1, gate + c, n, vec, g);
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[i][j] = j < n ? v[i][j] * silu(g[j]) : 0.f;
+        for (int j = 0; j < V / 2; ++j) v[i][j] = mul2(v[i][j], silu(g[j]));
       }
 #pragma unroll
-      for (int j = 0; j < V; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+      for (int j = 0; j < V / 2; ++j) ss = fma2(v[i][j], v[i][j], ss);
     }
     float r1 = 1.f;
-    if (a.w_post) {
-      float sum[1] = {ss};
-      group_sums<CTA, 1>(sum, red, phase);
-      r1 = rsqrtf(sum[0] * inv + a.eps);
-    }
+    if (a.w_post) r1 = rsqrtf(group_sum<CTA>(both(ss), red, phase) * inv + a.eps);
     // v -> unit; h'
-    float sum[2] = {0.f, 0.f};
+    float r2 = 0.f, m2 = 0.f;
+    if (with_dy) {
+      float2 s0 = two(0.f), s1 = two(0.f);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (lane + i * width) * V, n = a.H - c;
-      if (n <= 0) continue;
-      float w[V], sc[V], wp[V];
-      if (a.w_post) ld_f<float, V>(a.w_post + c, n, vec, w);
-      if (a.scale) ld_f<float, V>(a.scale + c, n, vec, sc);
-      if (dy) ld_f<float, V>(a.w_pre + c, n, vec, wp);
+      for (int i = 0; i < NV; ++i) {
+        const int c = (lane + i * width) * V, n = a.H - c;
+        if (n <= 0) continue;
+        float2 w[V / 2], sc[V / 2], wp[V / 2];
+        ld_param<V>(w, a.w_post, c, n, vec, 1.f);
+        ld_param<V>(sc, a.scale, c, n, vec, 1.f);
+        ld_param<V>(wp, a.w_pre, c, n, vec, 1.f);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        v[i][j] *= r1;
-        const float p = a.w_post ? v[i][j] * w[j] : v[i][j];
-        hv[i][j] = a.scale ? fmaf(sc[j], p, hv[i][j]) : hv[i][j] + p;
-        if (dy) {
-          sum[0] = fmaf(hv[i][j], hv[i][j], sum[0]);
-          sum[1] = fmaf(d[i][j] * wp[j], hv[i][j], sum[1]);
+        for (int j = 0; j < V / 2; ++j) {
+          v[i][j] = mul2(v[i][j], two(r1));
+          hv[i][j] = fma2(sc[j], mul2(v[i][j], w[j]), hv[i][j]);
+          s0 = fma2(hv[i][j], hv[i][j], s0);
+          s1 = fma2(mul2(d[i][j], wp[j]), hv[i][j], s1);
         }
       }
-    }
-    float r2 = 0.f, m2 = 0.f;
-    if (dy) {
+      float sum[2] = {both(s0), both(s1)};
       group_sums<CTA, 2>(sum, red, phase);
       r2 = rsqrtf(sum[0] * inv + a.eps);
       m2 = r2 * sum[1] * inv;
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) v[i][j] = mul2(v[i][j], two(r1));
     }
-    // d -> dh, then dp w_post
-    ss = 0.f;
+    // d -> dh, then q dh
+    ss = two(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (lane + i * width) * V, n = a.H - c;
       if (n <= 0) continue;
-      float e[V], w[V], sc[V], wp[V];
-      if (dho) ld_r(1, dho, i, e);
-      if (dy) ld_f<float, V>(a.w_pre + c, n, vec, wp);
-      if (a.w_post) ld_f<float, V>(a.w_post + c, n, vec, w);
-      if (a.scale) ld_f<float, V>(a.scale + c, n, vec, sc);
+      float2 e[V / 2], w[V / 2], sc[V / 2], wp[V / 2];
+      if (a.dh_out)
+        rows.get_r(stage, 1, static_cast<const R*>(a.dh_out) + row * a.dh_out_row + c, n, vec, e);
+      else
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        float dh = 0.f;
-        if (dy) {
-          const float unit2 = hv[i][j] * r2;
-          s_pre[i][j] = fmaf(d[i][j], unit2, s_pre[i][j]);
-          dh = r2 * (d[i][j] * wp[j] - unit2 * m2);
-        }
-        if (dho) dh += e[j];
-        e[j] = dh;
-        const float p = a.w_post ? v[i][j] * w[j] : v[i][j];
-        s_scale[i][j] = fmaf(dh, p, s_scale[i][j]);
-        const float dp = a.scale ? dh * sc[j] : dh;
-        s_post[i][j] = fmaf(dp, v[i][j], s_post[i][j]);
-        d[i][j] = a.w_post ? dp * w[j] : dp;
-        ss = fmaf(d[i][j], v[i][j], ss);
+        for (int j = 0; j < V / 2; ++j) e[j] = two(0.f);
+      ld_param<V>(w, a.w_post, c, n, vec, 1.f);
+      ld_param<V>(sc, a.scale, c, n, vec, 1.f);
+      ld_param<V>(wp, a.w_pre, c, n, vec, 1.f);
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) {
+        const float2 unit2 = mul2(hv[i][j], two(r2));
+        s_pre[i][j] = fma2(d[i][j], unit2, s_pre[i][j]);
+        e[j] = fma2(two(r2), fma2(unit2, two(-m2), mul2(d[i][j], wp[j])), e[j]);
+        U[i][j] = fma2(e[j], v[i][j], U[i][j]);
+        d[i][j] = mul2(mul2(e[j], sc[j]), w[j]);
+        ss = fma2(d[i][j], v[i][j], ss);
       }
-      if (a.dh) st_f<R, V>(static_cast<R*>(a.dh) + row * a.dh_row + c, n, vec, e);
+      if (a.dh) st_pairs<R, V>(static_cast<R*>(a.dh) + row * a.dh_row + c, n, vec, e);
     }
-    float m1 = 0.f;
-    if (a.w_post) {
-      float s1[1] = {ss};
-      group_sums<CTA, 1>(s1, red, phase);
-      m1 = s1[0] * inv;
-    }
+    const float m1 = a.w_post ? group_sum<CTA>(both(ss), red, phase) * inv : 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (lane + i * width) * V, n = a.H - c;
       if (n <= 0) continue;
 #pragma unroll
-      for (int j = 0; j < V; ++j) d[i][j] = a.w_post ? r1 * (d[i][j] - v[i][j] * m1) : d[i][j];
+      for (int j = 0; j < V / 2; ++j) d[i][j] = mul2(two(r1), fma2(v[i][j], two(-m1), d[i][j]));
       if (gate) {
-        float g[V], ov[V];
-        ld_t(1, gate, i, g);
-        ld_t(0, o, i, ov);
+        float2 g[V / 2], ov[V / 2];
+        rows.get_t(stage, 1, gate + c, n, vec, g);
+        rows.get_t(stage, 0, o + c, n, vec, ov);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float s = sigmoid(g[j]), q = g[j] * s;
-          ov[j] *= d[i][j] * fmaf(q, 1.f - s, s);
-          d[i][j] *= q;
+        for (int j = 0; j < V / 2; ++j) {
+          const float2 s = sigmoid(g[j]), q = mul2(g[j], s);
+          ov[j] = mul2(mul2(ov[j], d[i][j]), fma2(q, fma2(s, two(-1.f), two(1.f)), s));
+          d[i][j] = mul2(d[i][j], q);
         }
-        st_f<T, V>(static_cast<T*>(a.dgate) + row * a.dgate_row + c, n, vec, ov);
+        st_pairs<T, V>(static_cast<T*>(a.dgate) + row * a.dgate_row + c, n, vec, ov);
       }
-      st_f<T, V>(static_cast<T*>(a.do_) + row * a.do_row + c, n, vec, d[i]);
+      st_pairs<T, V>(static_cast<T*>(a.do_) + row * a.do_row + c, n, vec, d[i]);
     }
   }
-  // part[group][3][H]
-  float* out = part + first * 3 * a.H;
+  // part[group][2][H]
+  float* out = part + first * 2 * a.H;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (lane + i * width) * V;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      if (c + j >= a.H) continue;
-      out[c + j] = s_post[i][j];
-      out[a.H + c + j] = s_scale[i][j];
-      out[2 * a.H + c + j] = s_pre[i][j];
-    }
+    if (a.H - c <= 0) continue;
+    st_pairs<float, V>(out + c, a.H - c, a.H % 4 == 0, U[i]);
+    st_pairs<float, V>(out + a.H + c, a.H - c, a.H % 4 == 0, s_pre[i]);
   }
 }
 
-__global__ void __launch_bounds__(256) block_norm_sums_kernel(const float* part, int rows, int H, float* dw_post,
-                                                              float* dscale, float* dw_pre) {
-  column_sums(part, rows, 3ll * H, [=](long long c, float v) {
-    float* out = c < H ? dw_post : c < 2ll * H ? dscale : dw_pre;
-    if (out) out[c % H] = v;
+__global__ void __launch_bounds__(256) block_norm_sums_kernel(const float* part, int rows, s4_block_norm_bwd_args a) {
+  column_sums(part, rows, 2ll * a.H, [=](long long c, float v) {
+    const int h = (int)(c % a.H);
+    if (c >= a.H) {
+      if (a.dw_pre) a.dw_pre[h] = v;
+    } else {
+      if (a.dw_post) a.dw_post[h] = a.scale ? a.scale[h] * v : v;
+      if (a.dscale) a.dscale[h] = a.w_post ? a.w_post[h] * v : v;
+    }
   });
 }
 
@@ -331,13 +342,14 @@ Shape shape_for(int H, int V) {
   while (nv * kMaxThreads < packs) nv *= 2;
   return {true, nv, ((packs + nv - 1) / nv + 31) / 32 * 32};
 }
-// Groups that share the rows of the backward pass (each leaves one row of partial sums).
-constexpr int kBwdCtas = 4;  // CTAs per SM
-int bwd_ctas(long long rows, int H, int V, int sms) {
-  const Shape sh = shape_for(H, V);
-  const long long per = sh.cta ? 1 : sh.threads / 32;
-  const long long need = (rows + per - 1) / per;
-  return (int)(need < (long long)sms * kBwdCtas ? need : (long long)sms * kBwdCtas);
+// CTAs that walk over the rows: what runs at once, by the registers of a thread (in the backward
+// pass each group leaves one row of partial sums).
+constexpr int kFwdRegs = 64, kBwdRegs = 96;
+int ctas_for(long long rows, const Shape& sh, int regs) {
+  const long long per = sh.cta ? 1 : sh.threads / 32, need = (rows + per - 1) / per;
+  const int fit = 65536 / (regs * sh.threads);
+  const long long most = (long long)s4impl::num_sms() * (fit < 1 ? 1 : fit);
+  return (int)(need < most ? need : most);
 }
 
 template <typename T, typename R, int V>
@@ -347,21 +359,26 @@ cudaError_t fwd_t(const s4_block_norm_args& a, cudaStream_t s) {
                    vec_ok(a.h_out, er, br, a.h_out_row) && vec_ok(a.y, et, bt, a.y_row) && vec_ok(a.w_post, 4, 16) &&
                    vec_ok(a.scale, 4, 16) && vec_ok(a.w_pre, 4, 16);
   const Shape sh = shape_for(a.H, V);
-  const long long per = sh.cta ? 1 : sh.threads / 32;
-  const unsigned grid = (unsigned)((a.rows + per - 1) / per);
+  const int grid = ctas_for(a.rows, sh, kFwdRegs);
+  const auto run = [&](auto kernel, int bytes) {
+    if (bytes > 0) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    kernel<<<grid, sh.threads, bytes, s>>>(a, vec);
+  };
   s4impl::TimedLaunch tl("block_norm", s);
+  // rows of whole packs, read ahead; others as they come
+  const int ahead = vec && a.H % V == 0 ? kRowBytes<T, R, V, 2, 1> * sh.threads : 0;
   if (!sh.cta && sh.nv == 1)
-    block_norm_kernel<T, R, V, 1, false><<<grid, sh.threads, 0, s>>>(a, vec);
+    ahead ? run(block_norm_kernel<T, R, V, 1, false, true>, ahead) : run(block_norm_kernel<T, R, V, 1, false, false>, 0);
   else if (!sh.cta)
-    block_norm_kernel<T, R, V, 2, false><<<grid, sh.threads, 0, s>>>(a, vec);
+    run(block_norm_kernel<T, R, V, 2, false, false>, 0);
   else if (sh.nv == 1)
-    block_norm_kernel<T, R, V, 1, true><<<grid, sh.threads, 0, s>>>(a, vec);
+    ahead ? run(block_norm_kernel<T, R, V, 1, true, true>, ahead) : run(block_norm_kernel<T, R, V, 1, true, false>, 0);
   else if (sh.nv == 2)
-    block_norm_kernel<T, R, V, 2, true><<<grid, sh.threads, 0, s>>>(a, vec);
+    run(block_norm_kernel<T, R, V, 2, true, false>, 0);
   else if (sh.nv == 4)
-    block_norm_kernel<T, R, V, 4, true><<<grid, sh.threads, 0, s>>>(a, vec);
+    run(block_norm_kernel<T, R, V, 4, true, false>, 0);
   else if constexpr (V == 4)  // 16384 channels in 32 bits
-    block_norm_kernel<T, R, V, 8, true><<<grid, sh.threads, 0, s>>>(a, vec);
+    run(block_norm_kernel<T, R, V, 8, true, false>, 0);
   return cudaGetLastError();
 }
 
@@ -374,7 +391,7 @@ cudaError_t bwd_t(const s4_block_norm_bwd_args& a, cudaStream_t s) {
                    vec_ok(a.dh, er, br, a.dh_row) && vec_ok(a.w_post, 4, 16) && vec_ok(a.scale, 4, 16) &&
                    vec_ok(a.w_pre, 4, 16);
   const Shape sh = shape_for(a.H, V);
-  const int grid = bwd_ctas(a.rows, a.H, V, s4impl::num_sms());
+  const int grid = ctas_for(a.rows, sh, kBwdRegs);
   float* part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + s4impl::kStatusBytes);
   {
     s4impl::TimedLaunch tl("block_norm_bwd", s);
@@ -383,7 +400,7 @@ cudaError_t bwd_t(const s4_block_norm_bwd_args& a, cudaStream_t s) {
       kernel<<<grid, sh.threads, bytes, s>>>(a, vec, part);
     };
     // rows of whole packs, read ahead; others as they come
-    const int ahead = vec && a.H % V == 0 ? 2 * RowSlots<T, R, V>::kBytes * sh.threads : 0;
+    const int ahead = vec && a.H % V == 0 ? kRowBytes<T, R, V, 3, 2> * sh.threads : 0;
     if (!sh.cta && sh.nv == 1)
       ahead ? run(block_norm_bwd_kernel<T, R, V, 1, false, true>, ahead)
             : run(block_norm_bwd_kernel<T, R, V, 1, false, false>, 0);
@@ -401,8 +418,7 @@ cudaError_t bwd_t(const s4_block_norm_bwd_args& a, cudaStream_t s) {
   }
   if (!a.dw_post && !a.dscale && !a.dw_pre) return cudaGetLastError();
   s4impl::TimedLaunch tl("block_norm_bwd", s);
-  block_norm_sums_kernel<<<(unsigned)((3ll * a.H + 31) / 32), 256, 0, s>>>(
-      part, grid * (sh.cta ? 1 : sh.threads / 32), a.H, a.dw_post, a.dscale, a.dw_pre);
+  block_norm_sums_kernel<<<(unsigned)((2ll * a.H + 31) / 32), 256, 0, s>>>(part, grid * (sh.cta ? 1 : sh.threads / 32), a);
   return cudaGetLastError();
 }
 
@@ -426,10 +442,10 @@ size_t block_norm_bwd_scratch(long long rows, int H) {
   size_t most = 0;
   for (int V : {4, 8}) {
     const Shape sh = shape_for(H, V);
-    const size_t r = (size_t)bwd_ctas(rows, H, V, num_sms()) * (sh.cta ? 1 : sh.threads / 32);
+    const size_t r = (size_t)ctas_for(rows, sh, kBwdRegs) * (sh.cta ? 1 : sh.threads / 32);
     most = r > most ? r : most;
   }
-  return sizeof(float) * 3 * most * (size_t)H;
+  return sizeof(float) * 2 * most * (size_t)H;
 }
 
 cudaError_t launch_block_norm_bwd(const s4_block_norm_bwd_args& a, cudaStream_t s) {

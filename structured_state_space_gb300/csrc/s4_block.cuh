@@ -134,6 +134,22 @@ __device__ __forceinline__ void st_f(T* p, int n, bool vec, const float (&v)[V])
   st_pack<T, V>(p, n, vec, r);
 }
 
+// A pack of an even number of elements as pairs.
+template <typename T, int V>
+__device__ __forceinline__ void to_pairs(const Pack<T, V>& r, float2 (&v)[V / 2]) {
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) v[i] = make_float2(r.get(2 * i), r.get(2 * i + 1));
+}
+template <typename T, int V>
+__device__ __forceinline__ void st_pairs(T* p, int n, bool vec, const float2 (&v)[V / 2]) {
+  float f[V];
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    f[2 * i] = v[i].x;
+    f[2 * i + 1] = v[i].y;
+  }
+  st_f<T, V>(p, n, vec, f);
+}
 template <typename T, int V>
 __device__ __forceinline__ void st_whole(T* p, const float (&v)[V]) {
   st_f<T, V>(p, V, true, v);
@@ -161,18 +177,51 @@ __device__ __forceinline__ void fetched_but() { asm volatile("cp.async.wait_grou
 __device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void fetched() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// ---- packed pairs -----------------------------------------------------------------------
+__device__ __forceinline__ unsigned long long u64(float2 v) { return *reinterpret_cast<unsigned long long*>(&v); }
+__device__ __forceinline__ float2 f2(unsigned long long v) { return *reinterpret_cast<float2*>(&v); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(u64(a)), "l"(u64(b)));
+  return f2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(u64(a)), "l"(u64(b)));
+  return f2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(u64(a)), "l"(u64(b)), "l"(u64(c)));
+  return f2(r);
+}
+
+// 2^v (relative error 2^-22, 0 for results below the normal range)
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float2 ex2(float2 v) { return make_float2(ex2(v.x), ex2(v.y)); }
+constexpr float kLog2e = 1.44269504088896340736f;
 // v sigmoid(v) and its derivative.  sigmoid = 1 / (1 + 2^(-v log2 e)) to about 2^-22, more for
 // large negative v by |v| 2^-24 (the exponent's rounding); it tends to 0 and 1 without
 // overflow trouble (2^.. = inf gives 0).
-__device__ __forceinline__ float sigmoid(float v) {
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.44269504088896340736f));
-  return s4dev::rcp_approx(1.f + e);
+__device__ __forceinline__ float sigmoid(float v) { return s4dev::rcp_approx(1.f + ex2(v * -kLog2e)); }
+__device__ __forceinline__ float2 sigmoid(float2 v) {
+  const float2 e = add2(ex2(mul2(v, make_float2(-kLog2e, -kLog2e))), make_float2(1.f, 1.f));
+  return make_float2(s4dev::rcp_approx(e.x), s4dev::rcp_approx(e.y));
 }
 __device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
+__device__ __forceinline__ float2 silu(float2 v) { return mul2(v, sigmoid(v)); }
+// silu' = s + silu (1 - s)
+__device__ __forceinline__ float2 silu_grad(float2 v) {
+  const float2 s = sigmoid(v), q = mul2(v, s);
+  return fma2(q, fma2(s, make_float2(-1.f, -1.f), make_float2(1.f, 1.f)), s);
+}
 __device__ __forceinline__ float silu_grad(float v) {
   const float s = sigmoid(v);
-  return s * fmaf(v, 1.f - s, 1.f);
+  return fmaf(v * s, 1.f - s, s);
 }
 
 // The status block is optional in these calls (a null one records nothing).

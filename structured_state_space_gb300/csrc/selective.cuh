@@ -14,35 +14,9 @@ using namespace s4blk;
 using s4impl::St;
 
 constexpr int kThreads = 128;
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-
-// ---- packed pairs -----------------------------------------------------------------------
-__device__ __forceinline__ unsigned long long u64(float2 v) { return *reinterpret_cast<unsigned long long*>(&v); }
-__device__ __forceinline__ float2 f2(unsigned long long v) { return *reinterpret_cast<float2*>(&v); }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(u64(a)), "l"(u64(b)));
-  return f2(r);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  unsigned long long r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(u64(a)), "l"(u64(b)));
-  return f2(r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(u64(a)), "l"(u64(b)), "l"(u64(c)));
-  return f2(r);
-}
+constexpr float kLn2 = 0.69314718055994530942f;
 
 // ---- functions ----------------------------------------------------------------------------
-// 2^v (relative error 2^-22, 0 for results below the normal range)
-__device__ __forceinline__ float ex2(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-__device__ __forceinline__ float2 ex2(float2 v) { return make_float2(ex2(v.x), ex2(v.y)); }
 // log(1 + e^v) = max(v, 0) + log1p(u), u = e^-|v|: no overflow, and the relative precision of
 // log1p for small u.  log1p(u) = 2 atanh(s) with s = u / (2 + u) <= 1/3; 2 atanh(s) / s is a
 // polynomial in s^2 on [0, 1/9], here its interpolation at the Chebyshev points of degree 4

@@ -117,10 +117,8 @@ __device__ __forceinline__ void eval_cell(const Cell<T>& c, bool gate, bool soft
   zf = make_float2(0.f, 0.f);
   if (gate) {
     const float2 z = make_float2(c.z.get(0), c.z.get(1));
-    const float2 s = make_float2(sigmoid(z.x), sigmoid(z.y));
-    // silu = z s, silu' = s + silu (1 - s)
-    const float2 q = mul2(z, s);
-    zf = mul2(p, make_float2(fmaf(q.x, 1.f - s.x, s.x), fmaf(q.y, 1.f - s.y, s.y)));
+    const float2 s = sigmoid(z), q = mul2(z, s);  // silu = q, silu' = s + q (1 - s)
+    zf = mul2(p, fma2(q, fma2(s, make_float2(-1.f, -1.f), make_float2(1.f, 1.f)), s));
     p = mul2(p, q);
   }
 }

@@ -4,16 +4,15 @@
 //   v_t = bias + sum_{k<W} w[k] x[t-W+1+k],  y = v sigmoid(v)
 //
 // About 2 W + 5 operations on 4 bytes (16-bit types) moved: the bound is memory.  A thread
-// owns V neighbouring channels (one access of 16 bytes) and walks a segment of the
-// sequence with the last taps in registers, so that each input is read from memory once
-// and W - 1 more times per segment from cache.
+// owns V neighbouring channels and walks a segment of the sequence with the last taps in
+// registers, so that each input is read from memory once and W - 1 more times per segment
+// from cache.  Channels go through packed fp32 operations in pairs.
 #include "s4_block.cuh"
 
 namespace {
 using namespace s4blk;
 using s4impl::St;
 
-// Taps are kept as KW = 4 or 8 (the first KW - W have weight 0 and are not read).
 constexpr int kSegFwd = 16;   // tokens of a thread's segment, forward
 constexpr int kSegBwd = 64;   // and backward
 constexpr int kThreads = 128;
@@ -28,58 +27,71 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(s4_short_conv_args
   const long long gid = (long long)blockIdx.x * kThreads + threadIdx.x;
   if (gid >= (long long)ncv * nseg) return;
   const int seg = (int)(gid / ncv), h = (int)(gid % ncv) * V, n = min(V, a.H - h);
-  const int t0 = seg * kSegFwd, t1 = min(a.L, t0 + kSegFwd), pad = KW - a.W;
+  const int t0 = seg * kSegFwd, t1 = min(a.L, t0 + kSegFwd), live = min(t1, q.len);
   const T* x = static_cast<const T*>(a.x.p) + b * a.x.batch + h;
   T* y = static_cast<T*>(a.y.p) + b * a.y.batch + h;
   const long long srow = a.H, sslot = (long long)(a.W - 1) * a.H;
   const T* state = a.state ? static_cast<const T*>(a.state) + (q.slot < 0 ? 0 : q.slot) * sslot + h : nullptr;
+  const bool whole = vec && n >= V;
 
-  float w[KW][V], bias[V], win[KW][V];
+  // the segment's first inputs, on their way before the filter is read
+  Pack<T, V> in[KW];
+  const auto fetch = [&](int t) {
+    if (whole && t + KW <= live) {
+#pragma unroll
+      for (int u = 0; u < KW; ++u) in[u] = ld_whole<T, V>(x + (t + u) * a.x.row);
+      return;
+    }
+#pragma unroll
+    for (int u = 0; u < KW; ++u)
+      in[u] = ld_pack<T, V>(x + (t + u) * a.x.row, t + u < live && S4_IN(t + u, a.L) ? n : 0, vec);
+  };
+  if (t0 < live) fetch(t0);
+  float2 w[KW][V / 2], bias[V / 2], win[KW][V / 2];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const bool in = i < n && S4_IN(h + i, a.H);
-    bias[i] = a.bias && in ? a.bias[h + i] : 0.f;
+    const bool on = i < n && S4_IN(h + i, a.H);
+    (i % 2 ? bias[i / 2].y : bias[i / 2].x) = a.bias && on ? a.bias[h + i] : 0.f;
 #pragma unroll
-    for (int k = 0; k < KW; ++k) w[k][i] = in && k >= pad ? a.w[(long long)(h + i) * a.W + k - pad] : 0.f;
+    for (int k = 0; k < KW; ++k)
+      (i % 2 ? w[k][i / 2].y : w[k][i / 2].x) = on ? a.w[(long long)(h + i) * KW + k] : 0.f;
   }
   // the inputs before the segment: of the sequence, of the state, or zeros
 #pragma unroll
   for (int k = 0; k < KW - 1; ++k) {
     const int t = t0 - (KW - 1) + k;
-#pragma unroll
-    for (int i = 0; i < V; ++i) win[k][i] = 0.f;
-    if (t >= 0 && t < q.len) {
-      ld_f<T, V>(x + t * a.x.row, n, vec, win[k]);
-    } else if (t < 0 && t >= -(a.W - 1) && state && q.slot >= 0) {
-      ld_f<T, V>(state + (t + a.W - 1) * srow, n, vec, win[k]);
-    }
+    Pack<T, V> r;
+    r.zero();
+    if (t >= 0 && t < q.len)
+      r = ld_pack<T, V>(x + t * a.x.row, n, vec);
+    else if (t < 0 && t >= -(a.W - 1) && state && q.slot >= 0)
+      r = ld_pack<T, V>(state + (t + a.W - 1) * srow, n, vec);
+    to_pairs<T, V>(r, win[k]);
   }
-  for (int t = t0; t < t1; t += KW) {
-    Pack<T, V> in[KW];
+  for (int t = t0; t < live; t += KW) {
+    Pack<T, V> now[KW];
 #pragma unroll
-    for (int u = 0; u < KW; ++u)
-      if (t + u < min(t1, q.len) && S4_IN(t + u, a.L)) in[u] = ld_pack<T, V>(x + (t + u) * a.x.row, n, vec);
+    for (int u = 0; u < KW; ++u) now[u] = in[u];
+    if (t + KW < live) fetch(t + KW);
 #pragma unroll
     for (int u = 0; u < KW; ++u) {
-      if (t + u >= t1) break;
-      float out[V];
-      if (t + u < q.len) {
-        // the window is a ring: the input of token t + u replaces that of t + u - KW
+      if (t + u >= live) break;
+      // the window is a ring: the input of token t + u replaces that of t + u - KW
+      to_pairs<T, V>(now[u], win[(KW - 1 + u) % KW]);
+      float2 out[V / 2];
 #pragma unroll
-        for (int i = 0; i < V; ++i) win[(KW - 1 + u) % KW][i] = in[u].get(i);
+      for (int i = 0; i < V / 2; ++i) {
+        float2 v = bias[i];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          float v = bias[i];
-#pragma unroll
-          for (int k = 0; k < KW; ++k) v = fmaf(w[k][i], win[(k + u) % KW][i], v);
-          out[i] = a.silu ? silu(v) : v;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) out[i] = 0.f;
+        for (int k = 0; k < KW; ++k) v = fma2(w[k][i], win[(k + u) % KW][i], v);
+        out[i] = a.silu ? silu(v) : v;
       }
-      if (S4_IN(t + u, a.L)) st_f<T, V>(y + (t + u) * a.y.row, n, vec, out);
+      if (S4_IN(t + u, a.L)) st_pairs<T, V>(y + (t + u) * a.y.row, n, vec, out);
     }
+  }
+  for (int t = max(t0, live); t < t1; ++t) {  // padding
+    const float zero[V] = {};
+    st_f<T, V>(y + t * a.y.row, n, vec, zero);
   }
   // The state after the last real token, row j being input len - (W-1) + j.  The thread
   // that read the channels' old state writes the new one (in place too: rows are taken
@@ -103,17 +115,23 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(s4_short_conv_args
 // dx is complete once dv_t is known.  A CTA is 8 warps along time and 32 lanes along
 // channels; the filter's gradients are summed in registers, then over the CTA's warps,
 // and leave as one row of partial sums per CTA.  Inputs arrive by asynchronous copies into slots of
-// the thread's own, kAhead groups of KW tokens ahead: at two CTAs per SM (the window, the filter
-// and its sums take 115 registers; one CTA with 8 taps) that keeps 128 KB or more per SM on their way.
+// the thread's own, kAhead groups of KW tokens ahead: with up to 4 taps two CTAs run per SM (the
+// window, the filter and its sums take 128 registers), one with more, and 80 KB or more per SM
+// are on their way.
 template <typename T, int KW>
-constexpr int kAhead = sizeof(T) == 4 ? 2 : KW == 4 ? 4 : 5;
+constexpr int ahead_of() {
+  const int group = 2 * KW * 32 * kWarpsBwd * kVecBwd * (int)sizeof(T), fit = (80 << 10) / group - 1;
+  return fit < 2 ? 2 : fit > 5 ? 5 : fit;
+}
+template <typename T, int KW>
+constexpr int kAhead = ahead_of<T, KW>();
 template <typename T, int KW, int V>
 constexpr int bwd_slot_bytes() { return (kAhead<T, KW> + 1) * 2 * KW * 32 * kWarpsBwd * Pack<T, V>::BYTES; }
 template <int KW, int V>
 constexpr int bwd_red_bytes() { return 4 * kWarpsBwd * (KW + 1) * V * 33; }
 
 template <typename T, int KW, int V>
-__global__ void __launch_bounds__(32 * kWarpsBwd, KW == 4 ? 2 : 1)
+__global__ void __launch_bounds__(32 * kWarpsBwd, KW <= 4 ? 2 : 1)
     short_conv_bwd_kernel(s4_short_conv_bwd_args a, bool vec, float* part, St st) {
   record_gen(st);
   extern __shared__ __align__(16) char conv_smem[];
@@ -124,12 +142,12 @@ __global__ void __launch_bounds__(32 * kWarpsBwd, KW == 4 ? 2 : 1)
   const int b = blockIdx.z, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const Seq q = seq_of(a.lengths, nullptr, b, a.L, 0, st);
   const int h = (blockIdx.x * 32 + lane) * V, n = min(V, a.H - h);
-  const int seg = blockIdx.y * kWarpsBwd + wid, t0 = seg * kSegBwd, pad = KW - a.W;
-  float acc[KW + 1][V];
+  const int seg = blockIdx.y * kWarpsBwd + wid, t0 = seg * kSegBwd;
+  float2 acc[KW + 1][V / 2];
 #pragma unroll
   for (int k = 0; k <= KW; ++k)
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[k][i] = 0.f;
+    for (int i = 0; i < V / 2; ++i) acc[k][i] = make_float2(0.f, 0.f);
 
   if (n > 0 && t0 < a.L) {
     const int t1 = min(a.L, t0 + kSegBwd);
@@ -140,25 +158,61 @@ __global__ void __launch_bounds__(32 * kWarpsBwd, KW == 4 ? 2 : 1)
     const T* state = a.state0 ? static_cast<const T*>(a.state0) + sb : nullptr;
     const T* dst = a.dstate ? static_cast<const T*>(a.dstate) + sb : nullptr;
     T* dst0 = a.dstate0 ? static_cast<T*>(a.dstate0) + sb : nullptr;
-    float w[KW][V], bias[V], win[KW][V], dv[KW][V];
+    float2 w[KW][V / 2], bias[V / 2], win[KW][V / 2], dv[KW][V / 2];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      bias[i] = a.bias && i < n ? a.bias[h + i] : 0.f;
+      (i % 2 ? bias[i / 2].y : bias[i / 2].x) = a.bias && i < n ? a.bias[h + i] : 0.f;
 #pragma unroll
-      for (int k = 0; k < KW; ++k) w[k][i] = i < n && k >= pad ? a.w[(long long)(h + i) * a.W + k - pad] : 0.f;
+      for (int k = 0; k < KW; ++k)
+        (i % 2 ? w[k][i / 2].y : w[k][i / 2].x) = i < n ? a.w[(long long)(h + i) * KW + k] : 0.f;
     }
 #pragma unroll
-    for (int k = 0; k < KW; ++k)
-#pragma unroll
-      for (int i = 0; i < V; ++i) win[k][i] = dv[k][i] = 0.f;
-#pragma unroll
-    for (int k = 0; k < KW - 1; ++k) {
+    for (int k = 0; k < KW; ++k) {
       const int t = t0 - (KW - 1) + k;
-      if (t >= 0 && t < q.len)
-        ld_f<T, V>(x + t * a.x.row, n, vec, win[k]);
-      else if (t < 0 && t >= -(a.W - 1) && state)
-        ld_f<T, V>(state + (t + a.W - 1) * (long long)a.H, n, vec, win[k]);
+      Pack<T, V> r;
+      r.zero();
+      if (k < KW - 1 && t >= 0 && t < q.len)
+        r = ld_pack<T, V>(x + t * a.x.row, n, vec);
+      else if (k < KW - 1 && t < 0 && t >= -(a.W - 1) && state)
+        r = ld_pack<T, V>(state + (t + a.W - 1) * (long long)a.H, n, vec);
+      to_pairs<T, V>(r, win[k]);
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) dv[k][i] = make_float2(0.f, 0.f);
     }
+    // dv of the token whose input is `xi`, into the ring's place u
+    const auto gradient = [&](int u, const Pack<T, V>& xi, const Pack<T, V>& di) {
+      to_pairs<T, V>(xi, win[(KW - 1 + u) % KW]);
+      float2 d[V / 2];
+      to_pairs<T, V>(di, d);
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        if (a.silu) {
+          float2 v = bias[i];
+#pragma unroll
+          for (int k = 0; k < KW; ++k) v = fma2(w[k][i], win[(k + u) % KW][i], v);
+          d[i] = mul2(d[i], silu_grad(v));
+        }
+        dv[(KW - 1 + u) % KW][i] = d[i];
+      }
+    };
+    const auto add_filter = [&](int u) {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        const float2 d = dv[(KW - 1 + u) % KW][i];
+#pragma unroll
+        for (int k = 0; k < KW; ++k) acc[k][i] = fma2(d, win[(k + u) % KW][i], acc[k][i]);
+        acc[KW][i] = add2(acc[KW][i], d);
+      }
+    };
+    // dx of the ring's oldest token (entry (k + u) % KW is k tokens after it)
+    const auto input = [&](int u, float2 (&g)[V / 2]) {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        g[i] = mul2(w[KW - 1][i], dv[u % KW][i]);
+#pragma unroll
+        for (int k = 1; k < KW; ++k) g[i] = fma2(w[KW - 1 - k][i], dv[(k + u) % KW][i], g[i]);
+      }
+    };
     // token t of the loop: dv_t, and dx of token t - (KW - 1)
     const int tend = min(t1 + KW - 1, q.len);
     const bool whole = vec && n >= V;
@@ -186,59 +240,49 @@ __global__ void __launch_bounds__(32 * kWarpsBwd, KW == 4 ? 2 : 1)
       const int gr = (tb - t0) / KW;
       fetch(gr + AHEAD);
       fetched_but<AHEAD>();
+      // a group inside the segment, of real tokens, away from the state on return
+      if (whole && tb > t0 && tb + KW <= min(t1, q.len) && (!dst || tb < q.len - (a.W - 1))) {
+#pragma unroll
+        for (int u = 0; u < KW; ++u) {
+          gradient(u, slot(gr, 0, u), slot(gr, 1, u));
+          add_filter(u);
+          float2 g[V / 2];
+          input(u, g);
+          st_pairs<T, V>(dx + (tb + u - (KW - 1)) * a.dx.row, V, true, g);
+        }
+        continue;
+      }
 #pragma unroll
       for (int u = 0; u < KW; ++u) {
         const int t = tb + u;
         if (t >= t1 + KW - 1) break;
-        const bool own = t < t1;
         if (t < q.len) {
-          const Pack<T, V> xi = slot(gr, 0, u), di = slot(gr, 1, u);
-#pragma unroll
-          for (int i = 0; i < V; ++i) win[(KW - 1 + u) % KW][i] = xi.get(i);
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            float d = di.get(i);
-            if (a.silu) {
-              float v = bias[i];
-#pragma unroll
-              for (int k = 0; k < KW; ++k) v = fmaf(w[k][i], win[(k + u) % KW][i], v);
-              d *= silu_grad(v);
-            }
-            dv[(KW - 1 + u) % KW][i] = d;
-            if (own) {
-#pragma unroll
-              for (int k = 0; k < KW; ++k) acc[k][i] = fmaf(d, win[(k + u) % KW][i], acc[k][i]);
-              acc[KW][i] += d;
-            }
-          }
+          gradient(u, slot(gr, 0, u), slot(gr, 1, u));
+          if (t < t1) add_filter(u);
         } else {
 #pragma unroll
-          for (int i = 0; i < V; ++i) dv[(KW - 1 + u) % KW][i] = 0.f;
+          for (int i = 0; i < V / 2; ++i) dv[(KW - 1 + u) % KW][i] = make_float2(0.f, 0.f);
         }
-        // dv of tokens t - (KW-1) .. t in ring order: entry (k + u) % KW is token t - (KW-1) + k
         const int tx = t - (KW - 1);
         const bool before = tx < 0;  // an input of the state on entry
         if (before ? (seg != 0 || tx < -(a.W - 1) || !dst0) : tx < t0) continue;
-        float g[V];
+        float2 g[V / 2];
 #pragma unroll
-        for (int i = 0; i < V; ++i) g[i] = 0.f;
+        for (int i = 0; i < V / 2; ++i) g[i] = make_float2(0.f, 0.f);
         if (tx < q.len) {
-#pragma unroll
-          for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int k = 0; k < KW; ++k) g[i] = fmaf(w[KW - 1 - k][i], dv[(k + u) % KW][i], g[i]);
+          input(u, g);
           const int j = tx - q.len + a.W - 1;  // its row of the state on return
           if (dst && j >= 0) {
-            float e[V];
-            ld_f<T, V>(dst + j * (long long)a.H, n, vec, e);
+            float2 e[V / 2];
+            to_pairs<T, V>(ld_pack<T, V>(dst + j * (long long)a.H, n, vec), e);
 #pragma unroll
-            for (int i = 0; i < V; ++i) g[i] += e[i];
+            for (int i = 0; i < V / 2; ++i) g[i] = add2(g[i], e[i]);
           }
         }
         if (before)
-          st_f<T, V>(dst0 + (tx + a.W - 1) * (long long)a.H, n, vec, g);
+          st_pairs<T, V>(dst0 + (tx + a.W - 1) * (long long)a.H, n, vec, g);
         else if (S4_IN(tx, a.L))
-          st_f<T, V>(dx + tx * a.dx.row, n, vec, g);
+          st_pairs<T, V>(dx + tx * a.dx.row, n, vec, g);
       }
     }
   }
@@ -247,17 +291,17 @@ __global__ void __launch_bounds__(32 * kWarpsBwd, KW == 4 ? 2 : 1)
 #pragma unroll
   for (int k = 0; k <= KW; ++k)
 #pragma unroll
-    for (int i = 0; i < V; ++i) red[wid][k * V + i][lane] = acc[k][i];
+    for (int i = 0; i < V; ++i) red[wid][k * V + i][lane] = i % 2 ? acc[k][i / 2].y : acc[k][i / 2].x;
   __syncthreads();
   // partial sums of this CTA: part[row][k][h], k < W the taps, k = W the bias
   float* out = part + ((long long)b * gridDim.y + blockIdx.y) * (a.W + 1) * a.H;
   for (int c = threadIdx.x; c < (KW + 1) * 32 * V; c += 32 * kWarpsBwd) {
     const int k = c / (32 * V), hl = c % (32 * V), hh = blockIdx.x * 32 * V + hl;
-    if (k < pad || hh >= a.H) continue;
+    if (hh >= a.H) continue;
     float t = 0.f;
 #pragma unroll
     for (int v = 0; v < kWarpsBwd; ++v) t += red[v][k * V + hl % V][hl / V];
-    out[(long long)(k - pad) * a.H + hh] = t;
+    out[(long long)k * a.H + hh] = t;
   }
 }
 
@@ -272,6 +316,20 @@ __global__ void __launch_bounds__(256) short_conv_sums_kernel(const float* part,
   });
 }
 
+// A filter's taps are compiled in: what a longer window would multiply by 0 may be infinite.
+template <typename F>
+void with_taps(int W, F f) {
+  switch (W) {
+    case 2: return f(std::integral_constant<int, 2>{});
+    case 3: return f(std::integral_constant<int, 3>{});
+    case 4: return f(std::integral_constant<int, 4>{});
+    case 5: return f(std::integral_constant<int, 5>{});
+    case 6: return f(std::integral_constant<int, 6>{});
+    case 7: return f(std::integral_constant<int, 7>{});
+    default: return f(std::integral_constant<int, 8>{});
+  }
+}
+
 template <typename T, int V>
 cudaError_t fwd_t(const s4_short_conv_args& a, St st, cudaStream_t s) {
   const int e = sizeof(T), bytes = sizeof(Pack<T, V>);
@@ -280,10 +338,7 @@ cudaError_t fwd_t(const s4_short_conv_args& a, St st, cudaStream_t s) {
   const long long n = (long long)((a.H + V - 1) / V) * ((a.L + kSegFwd - 1) / kSegFwd);
   const dim3 grid((unsigned)((n + kThreads - 1) / kThreads), a.batch);
   s4impl::TimedLaunch tl("short_conv", s);
-  if (a.W <= 4)
-    short_conv_kernel<T, 4, V><<<grid, kThreads, 0, s>>>(a, vec, st);
-  else
-    short_conv_kernel<T, 8, V><<<grid, kThreads, 0, s>>>(a, vec, st);
+  with_taps(a.W, [&](auto taps) { short_conv_kernel<T, decltype(taps)::value, V><<<grid, kThreads, 0, s>>>(a, vec, st); });
   return cudaGetLastError();
 }
 
@@ -302,15 +357,13 @@ cudaError_t bwd_t(const s4_short_conv_bwd_args& a, St st, cudaStream_t s) {
   const dim3 grid = bwd_grid(a.batch, a.L, a.H);
   {
     s4impl::TimedLaunch tl("short_conv_bwd", s);
-    const auto run = [&](auto kernel, int bytes) {
+    with_taps(a.W, [&](auto taps) {
+      constexpr int KW = decltype(taps)::value, slots = bwd_slot_bytes<T, KW, V>(), sums = bwd_red_bytes<KW, V>();
+      constexpr int bytes = slots > sums ? slots : sums;
+      const auto kernel = short_conv_bwd_kernel<T, KW, V>;
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
       kernel<<<grid, 32 * kWarpsBwd, bytes, s>>>(a, vec, part, st);
-    };
-    const auto most = [](int x, int y) { return x > y ? x : y; };
-    if (a.W <= 4)
-      run(short_conv_bwd_kernel<T, 4, V>, most(bwd_slot_bytes<T, 4, V>(), bwd_red_bytes<4, V>()));
-    else
-      run(short_conv_bwd_kernel<T, 8, V>, most(bwd_slot_bytes<T, 8, V>(), bwd_red_bytes<8, V>()));
+    });
   }
   s4impl::TimedLaunch tl("short_conv_bwd", s);
   const long long cols = (long long)(a.W + 1) * a.H;
@@ -329,8 +382,8 @@ S4_OOB_COUNTER(oob_short_conv)
 
 cudaError_t launch_short_conv(const s4_short_conv_args& a, St st, cudaStream_t s) {
   if (a.dtype == S4_F32) return fwd_t<float, 4>(a, st, s);
-  if (a.dtype == S4_BF16) return fwd_t<__nv_bfloat16, 8>(a, st, s);
-  return fwd_t<__half, 8>(a, st, s);
+  if (a.dtype == S4_BF16) return fwd_t<__nv_bfloat16, 4>(a, st, s);
+  return fwd_t<__half, 4>(a, st, s);
 }
 
 size_t short_conv_bwd_scratch(int batch, int L, int H, int W) {

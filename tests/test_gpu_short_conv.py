@@ -152,6 +152,21 @@ def test_padding_does_not_reach_the_gradients():
     assert (again["dx"][1] == 0).all() and (again["dx"][2, 7:] == 0).all()
 
 
+@pytest.mark.parametrize("W", [2, 3, 4, 5, 7])
+def test_an_infinity_reaches_only_its_taps(W):
+    r = Inputs(W)
+    x, w, dy = r.normal(1, 40, 8), r.normal(8, W), r.normal(1, 40, 8)
+    x[0, 11] = float("inf")
+    y = s4.s4_short_conv_fwd(x, w, silu=False)
+    bad = ~torch.isfinite(y[0]).any(1)
+    assert torch.nonzero(bad).flatten().tolist() == list(range(11, 11 + W))
+    dy[0, 20] = float("inf")
+    x[0, 11] = 0
+    g = s4.s4_short_conv_bwd(x, w, None, dy, silu=False)
+    bad = ~torch.isfinite(g["dx"][0]).any(1)
+    assert torch.nonzero(bad).flatten().tolist() == list(range(20 - W + 1, 21))
+
+
 def test_other_stream_and_graph_and_determinism():
     r = Inputs(10)
     x, w, b, dy = r.normal(2, 300, 64, dtype=torch.bfloat16), r.normal(64, 4), r.normal(64), \
