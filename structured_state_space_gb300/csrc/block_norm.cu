@@ -56,24 +56,26 @@ __device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
 // The rows that a group has on their way: with AHEAD, a row's packs are copied into slots of the
 // thread's own (two sets of them) while the row before is worked on; else they are read
 // when they are needed.  [2][NT][threads] packs of T, then [2][NR][threads] of R.
-template <typename T, typename R, int V, int NT, int NR, bool AHEAD>
+template <typename T, typename R, int V, int NV, int NT, int NR, bool AHEAD>
 struct Rows {
   Pack<T, V>* st;
   Pack<R, V>* sr;
   __device__ __forceinline__ Rows(char* smem)
       : st(reinterpret_cast<Pack<T, V>*>(smem) + threadIdx.x),
-        sr(reinterpret_cast<Pack<R, V>*>(smem + 2 * NT * Pack<T, V>::BYTES * blockDim.x) + threadIdx.x) {}
-  __device__ __forceinline__ void fetch_t(int stage, int which, const T* p) {
-    fetch_whole<T, V>(st + (stage * NT + which) * blockDim.x, p);
+        sr(reinterpret_cast<Pack<R, V>*>(smem + 2 * NT * NV * Pack<T, V>::BYTES * blockDim.x) + threadIdx.x) {}
+  __device__ __forceinline__ void fetch_t(int stage, int which, int i, const T* p) {
+    fetch_whole<T, V>(st + ((stage * NT + which) * NV + i) * blockDim.x, p);
   }
-  __device__ __forceinline__ void fetch_r(int stage, int which, const R* p) {
-    fetch_whole<R, V>(sr + (stage * NR + which) * blockDim.x, p);
+  __device__ __forceinline__ void fetch_r(int stage, int which, int i, const R* p) {
+    fetch_whole<R, V>(sr + ((stage * NR + which) * NV + i) * blockDim.x, p);
   }
-  __device__ __forceinline__ void get_t(int stage, int which, const T* p, int n, bool vec, float2 (&v)[V / 2]) const {
-    to_pairs<T, V>(AHEAD ? st[(stage * NT + which) * blockDim.x] : ld_pack<T, V>(p, n, vec), v);
+  __device__ __forceinline__ void get_t(int stage, int which, int i, const T* p, int n, bool vec,
+                                        float2 (&v)[V / 2]) const {
+    to_pairs<T, V>(AHEAD ? st[((stage * NT + which) * NV + i) * blockDim.x] : ld_pack<T, V>(p, n, vec), v);
   }
-  __device__ __forceinline__ void get_r(int stage, int which, const R* p, int n, bool vec, float2 (&v)[V / 2]) const {
-    to_pairs<R, V>(AHEAD ? sr[(stage * NR + which) * blockDim.x] : ld_pack<R, V>(p, n, vec), v);
+  __device__ __forceinline__ void get_r(int stage, int which, int i, const R* p, int n, bool vec,
+                                        float2 (&v)[V / 2]) const {
+    to_pairs<R, V>(AHEAD ? sr[((stage * NR + which) * NV + i) * blockDim.x] : ld_pack<R, V>(p, n, vec), v);
   }
 };
 
@@ -82,9 +84,9 @@ constexpr int kRowBytes = 2 * (NT * Pack<T, V>::BYTES + NR * Pack<R, V>::BYTES);
 
 // NV packs of V channels per thread, pack i at channel (lane + i * width) V.  Groups walk over the
 // rows.  What is absent is neutral: a weight of 1, a residual of 0 (without w_post r1 is 1).
-template <typename T, typename R, int V, int NV, bool CTA, bool AHEAD>
-__global__ void __launch_bounds__(CTA ? kMaxThreads : 128) block_norm_kernel(s4_block_norm_args a, bool vec) {
-  static_assert(!AHEAD || NV == 1, "");
+template <typename T, typename R, int V, int NV, int MAX, bool AHEAD>
+__global__ void __launch_bounds__(MAX, NV == 1 ? 1024 / MAX : 1) block_norm_kernel(s4_block_norm_args a, bool vec) {
+  constexpr bool CTA = MAX > 128;  // a row per CTA, or per warp
   __shared__ float red[2][2][32];
   extern __shared__ __align__(16) char norm_smem[];
   int phase = 0, stage = 0;
@@ -92,13 +94,15 @@ __global__ void __launch_bounds__(CTA ? kMaxThreads : 128) block_norm_kernel(s4_
   const int per = CTA ? 1 : blockDim.x >> 5;
   const long long first = (long long)blockIdx.x * per + (CTA ? 0 : threadIdx.x >> 5), step = (long long)gridDim.x * per;
   const float inv = 1.f / (float)a.H;
-  Rows<T, R, V, 2, 1, AHEAD> rows(norm_smem);
+  Rows<T, R, V, NV, 2, 1, AHEAD> rows(norm_smem);
   const auto fetch = [&](long long row, int stage) {
-    const int c = lane * V;
-    if (row < a.rows && c < a.H && S4_IN(row, a.rows)) {
-      rows.fetch_t(stage, 0, static_cast<const T*>(a.o) + row * a.o_row + c);
-      if (a.gate) rows.fetch_t(stage, 1, static_cast<const T*>(a.gate) + row * a.gate_row + c);
-      if (a.h) rows.fetch_r(stage, 0, static_cast<const R*>(a.h) + row * a.h_row + c);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (lane + i * width) * V;
+      if (row >= a.rows || c >= a.H || !S4_IN(row, a.rows)) continue;
+      rows.fetch_t(stage, 0, i, static_cast<const T*>(a.o) + row * a.o_row + c);
+      if (a.gate) rows.fetch_t(stage, 1, i, static_cast<const T*>(a.gate) + row * a.gate_row + c);
+      if (a.h) rows.fetch_r(stage, 0, i, static_cast<const R*>(a.h) + row * a.h_row + c);
     }
     fetch_commit();
   };
@@ -115,11 +119,11 @@ __global__ void __launch_bounds__(CTA ? kMaxThreads : 128) block_norm_kernel(s4_
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) v[i][j] = hv[i][j] = two(0.f);
       if (n <= 0 || !S4_IN(c, a.H) || !S4_IN(row, a.rows)) continue;
-      rows.get_t(stage, 0, static_cast<const T*>(a.o) + row * a.o_row + c, n, vec, v[i]);
-      if (a.h) rows.get_r(stage, 0, static_cast<const R*>(a.h) + row * a.h_row + c, n, vec, hv[i]);
+      rows.get_t(stage, 0, i, static_cast<const T*>(a.o) + row * a.o_row + c, n, vec, v[i]);
+      if (a.h) rows.get_r(stage, 0, i, static_cast<const R*>(a.h) + row * a.h_row + c, n, vec, hv[i]);
       if (a.gate) {
         float2 g[V / 2];
-        rows.get_t(stage, 1, static_cast<const T*>(a.gate) + row * a.gate_row + c, n, vec, g);
+        rows.get_t(stage, 1, i, static_cast<const T*>(a.gate) + row * a.gate_row + c, n, vec, g);
 #pragma unroll
         for (int j = 0; j < V / 2; ++j) v[i][j] = mul2(v[i][j], silu(g[j]));
       }
@@ -167,10 +171,10 @@ __global__ void __launch_bounds__(CTA ? kMaxThreads : 128) block_norm_kernel(s4_
 // r2, the third could go with the second, but where the two terms of dv nearly cancel that
 // costs them their last digits.)  A group walks over rows with the two column sums of its
 // channels in registers and leaves them as one row of partial sums.
-template <typename T, typename R, int V, int NV, bool CTA, bool AHEAD>
-__global__ void __launch_bounds__(CTA ? kMaxThreads : 128)
+template <typename T, typename R, int V, int NV, int MAX, bool AHEAD>
+__global__ void __launch_bounds__(MAX, NV == 1 ? 512 / MAX : 1)
     block_norm_bwd_kernel(s4_block_norm_bwd_args a, bool vec, float* part) {
-  static_assert(!AHEAD || NV == 1, "");
+  constexpr bool CTA = MAX > 128;  // a row per CTA, or per warp
   __shared__ float red[2][2][32];
   extern __shared__ __align__(16) char norm_smem[];
   int phase = 0, stage = 0;
@@ -185,15 +189,17 @@ __global__ void __launch_bounds__(CTA ? kMaxThreads : 128)
 #pragma unroll
     for (int j = 0; j < V / 2; ++j) U[i][j] = s_pre[i][j] = two(0.f);
 
-  Rows<T, R, V, 3, 2, AHEAD> rows(norm_smem);
+  Rows<T, R, V, NV, 3, 2, AHEAD> rows(norm_smem);
   const auto fetch = [&](long long row, int stage) {
-    const int c = lane * V;
-    if (row < a.rows && c < a.H && S4_IN(row, a.rows)) {
-      rows.fetch_t(stage, 0, static_cast<const T*>(a.o) + row * a.o_row + c);
-      if (a.gate) rows.fetch_t(stage, 1, static_cast<const T*>(a.gate) + row * a.gate_row + c);
-      if (with_dy) rows.fetch_t(stage, 2, static_cast<const T*>(a.dy) + row * a.dy_row + c);
-      if (a.h && with_dy) rows.fetch_r(stage, 0, static_cast<const R*>(a.h) + row * a.h_row + c);
-      if (a.dh_out) rows.fetch_r(stage, 1, static_cast<const R*>(a.dh_out) + row * a.dh_out_row + c);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (lane + i * width) * V;
+      if (row >= a.rows || c >= a.H || !S4_IN(row, a.rows)) continue;
+      rows.fetch_t(stage, 0, i, static_cast<const T*>(a.o) + row * a.o_row + c);
+      if (a.gate) rows.fetch_t(stage, 1, i, static_cast<const T*>(a.gate) + row * a.gate_row + c);
+      if (with_dy) rows.fetch_t(stage, 2, i, static_cast<const T*>(a.dy) + row * a.dy_row + c);
+      if (a.h && with_dy) rows.fetch_r(stage, 0, i, static_cast<const R*>(a.h) + row * a.h_row + c);
+      if (a.dh_out) rows.fetch_r(stage, 1, i, static_cast<const R*>(a.dh_out) + row * a.dh_out_row + c);
     }
     fetch_commit();
   };
@@ -212,14 +218,14 @@ __global__ void __launch_bounds__(CTA ? kMaxThreads : 128)
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) v[i][j] = hv[i][j] = d[i][j] = two(0.f);
       if (n <= 0 || !S4_IN(c, a.H)) continue;
-      rows.get_t(stage, 0, o + c, n, vec, v[i]);
+      rows.get_t(stage, 0, i, o + c, n, vec, v[i]);
       if (with_dy) {
-        rows.get_t(stage, 2, static_cast<const T*>(a.dy) + row * a.dy_row + c, n, vec, d[i]);
-        if (a.h) rows.get_r(stage, 0, static_cast<const R*>(a.h) + row * a.h_row + c, n, vec, hv[i]);
+        rows.get_t(stage, 2, i, static_cast<const T*>(a.dy) + row * a.dy_row + c, n, vec, d[i]);
+        if (a.h) rows.get_r(stage, 0, i, static_cast<const R*>(a.h) + row * a.h_row + c, n, vec, hv[i]);
       }
       if (gate) {
         float2 g[V / 2];
-        rows.get_t(stage, 1, gate + c, n, vec, g);
+        rows.get_t(stage, 1, i, gate + c, n, vec, g);
 #pragma unroll
         for (int j = 0; j < V / 2; ++j) v[i][j] = mul2(v[i][j], silu(g[j]));
       }
@@ -266,7 +272,7 @@ __global__ void __launch_bounds__(CTA ? kMaxThreads : 128)
       if (n <= 0) continue;
       float2 e[V / 2], w[V / 2], sc[V / 2], wp[V / 2];
       if (a.dh_out)
-        rows.get_r(stage, 1, static_cast<const R*>(a.dh_out) + row * a.dh_out_row + c, n, vec, e);
+        rows.get_r(stage, 1, i, static_cast<const R*>(a.dh_out) + row * a.dh_out_row + c, n, vec, e);
       else
 #pragma unroll
         for (int j = 0; j < V / 2; ++j) e[j] = two(0.f);
@@ -293,8 +299,8 @@ __global__ void __launch_bounds__(CTA ? kMaxThreads : 128)
       for (int j = 0; j < V / 2; ++j) d[i][j] = mul2(two(r1), fma2(v[i][j], two(-m1), d[i][j]));
       if (gate) {
         float2 g[V / 2], ov[V / 2];
-        rows.get_t(stage, 1, gate + c, n, vec, g);
-        rows.get_t(stage, 0, o + c, n, vec, ov);
+        rows.get_t(stage, 1, i, gate + c, n, vec, g);
+        rows.get_t(stage, 0, i, o + c, n, vec, ov);
 #pragma unroll
         for (int j = 0; j < V / 2; ++j) {
           const float2 s = sigmoid(g[j]), q = mul2(g[j], s);
@@ -342,79 +348,99 @@ Shape shape_for(int H, int V) {
   while (nv * kMaxThreads < packs) nv *= 2;
   return {true, nv, ((packs + nv - 1) / nv + 31) / 32 * 32};
 }
-// CTAs that walk over the rows: what runs at once, by the registers of a thread (in the backward
-// pass each group leaves one row of partial sums).
-constexpr int kFwdRegs = 64, kBwdRegs = 96;
-int ctas_for(long long rows, const Shape& sh, int regs) {
+// CTAs that walk over rows read ahead: as many as run at once (asked once per device, kernel and
+// CTA size; a grid of 1.5 rounds took 142 us instead of 102 forward on 16001 rows of 2560 channels).
+// Rows that are not read ahead have a group each in the forward pass.  In the backward pass each
+// group leaves one row of partial sums, of kMostThreads threads per SM at most.
+constexpr int kMaxAhead = 200 * 1024, kMostThreads = 1024;
+int most_ctas(long long rows, const Shape& sh, int per_sm) {
   const long long per = sh.cta ? 1 : sh.threads / 32, need = (rows + per - 1) / per;
-  const int fit = 65536 / (regs * sh.threads);
+  const int fit = kMostThreads / sh.threads < per_sm ? kMostThreads / sh.threads : per_sm;
   const long long most = (long long)s4impl::num_sms() * (fit < 1 ? 1 : fit);
   return (int)(need < most ? need : most);
+}
+template <auto Kernel>
+int ctas_for(long long rows, const Shape& sh, int bytes) {
+  static std::atomic<int> known[64][kMaxThreads / 32 + 1];
+  allow_shared<Kernel>(kMaxAhead);
+  std::atomic<int>& k = known[device()][sh.threads / 32];
+  int per_sm = k.load(std::memory_order_relaxed);
+  if (per_sm == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, Kernel, sh.threads, bytes) != cudaSuccess || per_sm < 1)
+      per_sm = 1;
+    k.store(per_sm, std::memory_order_relaxed);
+  }
+  return most_ctas(rows, sh, per_sm);
+}
+
+// f(kernel shape as constants: packs per thread, largest CTA)
+template <int V, typename F>
+void with_shape(const Shape& sh, F f) {
+  if (!sh.cta) {
+    if (sh.nv == 1) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 128>{});
+    return f(std::integral_constant<int, 2>{}, std::integral_constant<int, 128>{});
+  }
+  if (sh.nv == 1 && sh.threads <= 256) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 256>{});
+  if (sh.nv == 1) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, kMaxThreads>{});
+  if (sh.nv == 2) return f(std::integral_constant<int, 2>{}, std::integral_constant<int, kMaxThreads>{});
+  if (sh.nv == 4) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, kMaxThreads>{});
+  if constexpr (V == 4)  // 16384 channels in 32 bits
+    return f(std::integral_constant<int, 8>{}, std::integral_constant<int, kMaxThreads>{});
 }
 
 template <typename T, typename R, int V>
 cudaError_t fwd_t(const s4_block_norm_args& a, cudaStream_t s) {
   const int et = sizeof(T), er = sizeof(R), bt = sizeof(Pack<T, V>), br = sizeof(Pack<R, V>);
-  const bool vec = vec_ok(a.o, et, bt, a.o_row) && vec_ok(a.gate, et, bt, a.gate_row) && vec_ok(a.h, er, br, a.h_row) &&
-                   vec_ok(a.h_out, er, br, a.h_out_row) && vec_ok(a.y, et, bt, a.y_row) && vec_ok(a.w_post, 4, 16) &&
-                   vec_ok(a.scale, 4, 16) && vec_ok(a.w_pre, 4, 16);
+  const bool vec = vec_ok(a.o, et, bt, a.o_row) && vec_ok(a.gate, et, bt, a.gate_row) &&
+                   vec_ok(a.h, er, br < 16 ? br : 16, a.h_row) && vec_ok(a.h_out, er, br < 16 ? br : 16, a.h_out_row) &&
+                   vec_ok(a.y, et, bt, a.y_row) && vec_ok(a.w_post, 4, 16) && vec_ok(a.scale, 4, 16) &&
+                   vec_ok(a.w_pre, 4, 16);
   const Shape sh = shape_for(a.H, V);
-  const int grid = ctas_for(a.rows, sh, kFwdRegs);
-  const auto run = [&](auto kernel, int bytes) {
-    if (bytes > 0) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    kernel<<<grid, sh.threads, bytes, s>>>(a, vec);
-  };
   s4impl::TimedLaunch tl("block_norm", s);
-  // rows of whole packs, read ahead; others as they come
-  const int ahead = vec && a.H % V == 0 ? kRowBytes<T, R, V, 2, 1> * sh.threads : 0;
-  if (!sh.cta && sh.nv == 1)
-    ahead ? run(block_norm_kernel<T, R, V, 1, false, true>, ahead) : run(block_norm_kernel<T, R, V, 1, false, false>, 0);
-  else if (!sh.cta)
-    run(block_norm_kernel<T, R, V, 2, false, false>, 0);
-  else if (sh.nv == 1)
-    ahead ? run(block_norm_kernel<T, R, V, 1, true, true>, ahead) : run(block_norm_kernel<T, R, V, 1, true, false>, 0);
-  else if (sh.nv == 2)
-    run(block_norm_kernel<T, R, V, 2, true, false>, 0);
-  else if (sh.nv == 4)
-    run(block_norm_kernel<T, R, V, 4, true, false>, 0);
-  else if constexpr (V == 4)  // 16384 channels in 32 bits
-    run(block_norm_kernel<T, R, V, 8, true, false>, 0);
+  with_shape<V>(sh, [&](auto nv, auto max) {
+    constexpr int NV = decltype(nv)::value, MAX = decltype(max)::value;
+    if constexpr (NV <= 2) {
+      const int bytes = NV * kRowBytes<T, R, V, 2, 1> * sh.threads;
+      if (vec && a.H % V == 0 && bytes <= kMaxAhead) {
+        constexpr auto kernel = block_norm_kernel<T, R, V, NV, MAX, true>;
+        kernel<<<ctas_for<kernel>(a.rows, sh, bytes), sh.threads, bytes, s>>>(a, vec);
+        return;
+      }
+    }
+    const long long per = sh.cta ? 1 : sh.threads / 32;
+    block_norm_kernel<T, R, V, NV, MAX, false><<<(unsigned)((a.rows + per - 1) / per), sh.threads, 0, s>>>(a, vec);
+  });
   return cudaGetLastError();
 }
 
 template <typename T, typename R, int V>
 cudaError_t bwd_t(const s4_block_norm_bwd_args& a, cudaStream_t s) {
-  const int et = sizeof(T), er = sizeof(R), bt = sizeof(Pack<T, V>), br = sizeof(Pack<R, V>);
+  const int et = sizeof(T), er = sizeof(R), bt = sizeof(Pack<T, V>), br = sizeof(Pack<R, V>) < 16 ? sizeof(Pack<R, V>) : 16;
   const bool vec = vec_ok(a.o, et, bt, a.o_row) && vec_ok(a.gate, et, bt, a.gate_row) && vec_ok(a.h, er, br, a.h_row) &&
                    vec_ok(a.dy, et, bt, a.dy_row) && vec_ok(a.dh_out, er, br, a.dh_out_row) &&
                    vec_ok(a.do_, et, bt, a.do_row) && vec_ok(a.dgate, et, bt, a.dgate_row) &&
                    vec_ok(a.dh, er, br, a.dh_row) && vec_ok(a.w_post, 4, 16) && vec_ok(a.scale, 4, 16) &&
                    vec_ok(a.w_pre, 4, 16);
   const Shape sh = shape_for(a.H, V);
-  const int grid = ctas_for(a.rows, sh, kBwdRegs);
+  int grid = 0;
   float* part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + s4impl::kStatusBytes);
   {
     s4impl::TimedLaunch tl("block_norm_bwd", s);
-    const auto run = [&](auto kernel, int bytes) {
-      if (bytes > 0) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-      kernel<<<grid, sh.threads, bytes, s>>>(a, vec, part);
-    };
-    // rows of whole packs, read ahead; others as they come
-    const int ahead = vec && a.H % V == 0 ? kRowBytes<T, R, V, 3, 2> * sh.threads : 0;
-    if (!sh.cta && sh.nv == 1)
-      ahead ? run(block_norm_bwd_kernel<T, R, V, 1, false, true>, ahead)
-            : run(block_norm_bwd_kernel<T, R, V, 1, false, false>, 0);
-    else if (!sh.cta)
-      run(block_norm_bwd_kernel<T, R, V, 2, false, false>, 0);
-    else if (sh.nv == 1)
-      ahead ? run(block_norm_bwd_kernel<T, R, V, 1, true, true>, ahead)
-            : run(block_norm_bwd_kernel<T, R, V, 1, true, false>, 0);
-    else if (sh.nv == 2)
-      run(block_norm_bwd_kernel<T, R, V, 2, true, false>, 0);
-    else if (sh.nv == 4)
-      run(block_norm_bwd_kernel<T, R, V, 4, true, false>, 0);
-    else if constexpr (V == 4)  // 16384 channels in 32 bits
-      run(block_norm_bwd_kernel<T, R, V, 8, true, false>, 0);
+    with_shape<V>(sh, [&](auto nv, auto max) {
+      constexpr int NV = decltype(nv)::value, MAX = decltype(max)::value;
+      if constexpr (NV <= 2) {
+        const int bytes = NV * kRowBytes<T, R, V, 3, 2> * sh.threads;
+        if (vec && a.H % V == 0 && bytes <= kMaxAhead) {
+          constexpr auto kernel = block_norm_bwd_kernel<T, R, V, NV, MAX, true>;
+          grid = ctas_for<kernel>(a.rows, sh, bytes);
+          kernel<<<grid, sh.threads, bytes, s>>>(a, vec, part);
+          return;
+        }
+      }
+      constexpr auto kernel = block_norm_bwd_kernel<T, R, V, NV, MAX, false>;
+      grid = ctas_for<kernel>(a.rows, sh, 0);
+      kernel<<<grid, sh.threads, 0, s>>>(a, vec, part);
+    });
   }
   if (!a.dw_post && !a.dscale && !a.dw_pre) return cudaGetLastError();
   s4impl::TimedLaunch tl("block_norm_bwd", s);
@@ -442,7 +468,7 @@ size_t block_norm_bwd_scratch(long long rows, int H) {
   size_t most = 0;
   for (int V : {4, 8}) {
     const Shape sh = shape_for(H, V);
-    const size_t r = (size_t)ctas_for(rows, sh, kBwdRegs) * (sh.cta ? 1 : sh.threads / 32);
+    const size_t r = (size_t)most_ctas(rows, sh, 16) * (sh.cta ? 1 : sh.threads / 32);
     most = r > most ? r : most;
   }
   return sizeof(float) * 2 * most * (size_t)H;

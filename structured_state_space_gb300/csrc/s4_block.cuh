@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "s4_block.h"
@@ -284,6 +285,20 @@ __device__ __forceinline__ void column_sums(const float* part, int rows, long lo
 }
 
 // ---- host side ----------------------------------------------------------------------
+// The current device (0 .. 63).
+inline int device() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 ? dev : 0;
+}
+// Lets a kernel have `bytes` of shared memory, once per device.
+template <auto Kernel>
+void allow_shared(int bytes) {
+  static std::atomic<unsigned long long> done{0};
+  const unsigned long long bit = 1ull << device();
+  if (bytes <= 48 * 1024 || (done.load(std::memory_order_relaxed) & bit)) return;
+  if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess)
+    done.fetch_or(bit, std::memory_order_relaxed);
+}
 // Whether an array's accesses of `bytes` bytes are aligned: its address and its strides
 // (in elements of `e` bytes).
 inline bool vec_ok(const void* p, int e, int bytes, long long s0 = 0, long long s1 = 0) {

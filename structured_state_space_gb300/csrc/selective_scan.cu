@@ -415,11 +415,9 @@ cudaError_t scan_t(const s4_selective_args& a, St st, cudaStream_t s) {
     const long long blocks = chan_blocks<G::CH>(a.H, a.G);
     const auto run = [&](auto whole) {
       constexpr bool W = decltype(whole)::value;
-      const auto ends = selective_scan_kernel<T, G, 0, W>, out = selective_scan_kernel<T, G, 1, W>;
-      if (G::kBytes > 48 * 1024) {
-        cudaFuncSetAttribute(ends, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kBytes);
-        cudaFuncSetAttribute(out, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kBytes);
-      }
+      constexpr auto ends = selective_scan_kernel<T, G, 0, W>, out = selective_scan_kernel<T, G, 1, W>;
+      allow_shared<ends>(G::kBytes);
+      allow_shared<out>(G::kBytes);
       if (ck.count > 1) {
         {
           s4impl::TimedLaunch tl("selective_scan", s);

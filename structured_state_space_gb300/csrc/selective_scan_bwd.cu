@@ -853,9 +853,10 @@ cudaError_t bwd_t(const s4_selective_bwd_args& a, St st, cudaStream_t s) {
     const Work w = layout<G>(a.batch, a.L, a.H, a.N, a.G, static_cast<char*>(a.ws), nullptr);
     const auto run = [&](auto whole) {
       constexpr bool W = decltype(whole)::value;
-      const auto ends = selective_ends_kernel<T, E, W>, tiles = selective_tiles_kernel<T, G, W>;
-      cudaFuncSetAttribute(ends, cudaFuncAttributeMaxDynamicSharedMemorySize, E::kBytes);
-      cudaFuncSetAttribute(tiles, cudaFuncAttributeMaxDynamicSharedMemorySize, G::template kBytes<T>());
+      constexpr auto ends = selective_ends_kernel<T, E, W>;
+      constexpr auto tiles = selective_tiles_kernel<T, G, W>;
+      allow_shared<ends>(E::kBytes);
+      allow_shared<tiles>(G::template kBytes<T>());
       {
         s4impl::TimedLaunch tl("selective_bwd", s);
         const long long tasks = (long long)chan_blocks<E::CH>(a.H, a.G) * w.segs;

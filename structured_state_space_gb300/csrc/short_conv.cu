@@ -360,8 +360,8 @@ cudaError_t bwd_t(const s4_short_conv_bwd_args& a, St st, cudaStream_t s) {
     with_taps(a.W, [&](auto taps) {
       constexpr int KW = decltype(taps)::value, slots = bwd_slot_bytes<T, KW, V>(), sums = bwd_red_bytes<KW, V>();
       constexpr int bytes = slots > sums ? slots : sums;
-      const auto kernel = short_conv_bwd_kernel<T, KW, V>;
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      constexpr auto kernel = short_conv_bwd_kernel<T, KW, V>;
+      allow_shared<kernel>(bytes);
       kernel<<<grid, 32 * kWarpsBwd, bytes, s>>>(a, vec, part, st);
     });
   }
