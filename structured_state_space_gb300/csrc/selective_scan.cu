@@ -20,7 +20,7 @@ using namespace s4sel;
 // Four CTAs of four warps per SM: 128 registers a thread.  At 20 warps per SM the registers
 // left do not hold enough exponentials in flight (650 us instead of 564 on one sequence of
 // 65536 tokens, 1024 channels, 16 states, bfloat16), at 14 there are too few warps (647 us).
-constexpr int kScanThreads = 128, kScanCtas = 4;
+constexpr int kScanThreads = 128, kScanCtas = 4, kStepThreads = 128;
 
 template <int LPC_, int SPT_>
 struct Geo {
@@ -296,49 +296,66 @@ __global__ void __launch_bounds__(128) selective_join_kernel(s4_selective_args a
 }
 
 // One token per sequence: the state is read, advanced and written once (8 bytes per channel and
-// state, which bound it).
-template <typename T, int LPC, int SPT>
-__global__ void __launch_bounds__(256) selective_step_kernel(s4_selective_args a, bool vec, St st) {
-  constexpr int HB = 256 / LPC;
+// state, which bound it).  A thread takes 8 states of a channel and has all its reads under way
+// before the first is used.  WHOLE: aligned, and every thread's channel and states exist (a
+// call is then half of the instructions).  Two and four channels per thread were no faster (24.0
+// us instead of 23.3 on 256 sequences of 2048 channels and 16 states, 31.5 with four).
+template <typename T, int LPC, int SPT, bool WHOLE>
+__global__ void __launch_bounds__(kStepThreads) selective_step_kernel(s4_selective_args a, bool vec, bool vecbc, St st) {
+  constexpr int HB = kStepThreads / LPC;
   record_gen(st);
   const int b = blockIdx.y;
   const Chan c = chan_of<HB>(blockIdx.x, a.H / a.G);
   const Seq q = seq_of(a.lengths, a.index, b, 1, a.slots, st);
-  const int lane = threadIdx.x % LPC, h = c.h0 + threadIdx.x / LPC, n0 = lane * SPT, n = a.N - n0;
-  float acc = 0.f, xv = 0.f, zv = 0.f;
-  if (h < c.hend && q.slot >= 0) {
-    const long long at = (q.slot * a.H + h) * a.N + n0;
-    float s[SPT];
-#pragma unroll
-    for (int i = 0; i < SPT; ++i) s[i] = 0.f;
-    if (n > 0 && a.state && S4_IN(q.slot, a.slots))
-      ld_f<float, SPT>(a.state + at, n, vec, s);
-    if (q.len > 0) {
-      float A[SPT], Bv[SPT], Cv[SPT];
-      xv = to_f(static_cast<const T*>(a.x.p)[b * a.x.batch + h]);
-      float d = to_f(static_cast<const T*>(a.dt.p)[b * a.dt.batch + h]);
-      if (a.z.p) zv = to_f(static_cast<const T*>(a.z.p)[b * a.z.batch + h]);
-      if (a.dt_bias) d += a.dt_bias[h];
-      if (a.softplus) d = softplus(d);
-      if (n > 0) {
-        ld_f<float, SPT>(a.A + (long long)h * a.N + n0, n, vec, A);
-        ld_f<T, SPT>(static_cast<const T*>(a.B.p) + b * a.B.batch + c.g * a.B_group + n0, n, false, Bv);
-        ld_f<T, SPT>(static_cast<const T*>(a.C.p) + b * a.C.batch + c.g * a.C_group + n0, n, false, Cv);
-#pragma unroll
-        for (int i = 0; i < SPT; ++i) {
-          s[i] = fmaf(ex2(d * A[i] * kLog2e), s[i], d * xv * Bv[i]);
-          acc = fmaf(Cv[i], s[i], acc);
-        }
-      }
-    }
-    if (n > 0 && a.state_out && S4_IN(q.slot, a.slots)) st_f<float, SPT>(a.state_out + at, n, vec, s);
+  const int lane = threadIdx.x % LPC, h = c.h0 + threadIdx.x / LPC, n0 = lane * SPT, n = WHOLE ? SPT : a.N - n0;
+  const bool in = WHOLE || h < c.hend, on = q.len > 0;  // `on`: the token advances the state
+  const bool put = in && (WHOLE || n > 0) && a.state_out && q.slot >= 0 && S4_IN(q.slot, a.slots);
+  T* y = static_cast<T*>(a.y.p) + b * a.y.batch;
+  if (WHOLE && !on && !put) {  // a row that is not in use
+    if (lane == 0) y[h] = from_f<T>(0.f);
+    return;
   }
+  const long long at = (q.slot * a.H + h) * a.N + n0;
+  Pack<float, SPT> ps, pA;
+  Pack<T, SPT> pb, pc;
+  ps.zero();
+  if (in && q.slot >= 0 && a.state && S4_IN(q.slot, a.slots))
+    ps = ld_pack<float, SPT>(a.state + at, n, WHOLE || vec);
+  pA = ld_pack<float, SPT>(a.A + (long long)h * a.N + n0, in ? n : 0, WHOLE || vec);
+  float xv = 0.f, d = 0.f, zv = 0.f;
+  if (in && on && S4_IN(h, a.H)) {
+    xv = to_f(static_cast<const T*>(a.x.p)[b * a.x.batch + h]);
+    d = to_f(static_cast<const T*>(a.dt.p)[b * a.dt.batch + h]);
+    if (a.z.p) zv = to_f(static_cast<const T*>(a.z.p)[b * a.z.batch + h]);
+  }
+  pb = ld_pack<T, SPT>(static_cast<const T*>(a.B.p) + b * a.B.batch + c.g * a.B_group + n0, on ? n : 0, WHOLE || vecbc);
+  pc = ld_pack<T, SPT>(static_cast<const T*>(a.C.p) + b * a.C.batch + c.g * a.C_group + n0, on ? n : 0, WHOLE || vecbc);
+  if (a.dt_bias && in) d += a.dt_bias[h];
+  const float skip = a.D && in ? a.D[h] : 0.f;
+
+  float2 s[SPT / 2], acc = make_float2(0.f, 0.f);
+  to_pairs<float, SPT>(ps, s);
+  if (on) {
+    float2 A[SPT / 2], Bv[SPT / 2], Cv[SPT / 2];
+    to_pairs<float, SPT>(pA, A);
+    to_pairs<T, SPT>(pb, Bv);
+    to_pairs<T, SPT>(pc, Cv);
+    if (a.softplus) d = softplus(d);
+    const float2 dl = make_float2(d * kLog2e, d * kLog2e), dx = make_float2(d * xv, d * xv);
 #pragma unroll
-  for (int o = LPC / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-  if (lane == 0 && h < c.hend) {
-    if (a.D && q.len > 0) acc = fmaf(a.D[h], xv, acc);
-    if (a.z.p) acc *= silu(zv);
-    static_cast<T*>(a.y.p)[b * a.y.batch + h] = from_f<T>(q.len > 0 ? acc : 0.f);
+    for (int i = 0; i < SPT / 2; ++i) {
+      s[i] = fma2(ex2(mul2(dl, A[i])), s[i], mul2(dx, Bv[i]));
+      acc = fma2(Cv[i], s[i], acc);
+    }
+  }
+  if (put) st_pairs<float, SPT>(a.state_out + at, n, WHOLE || vec, s);
+  float v = acc.x + acc.y;
+#pragma unroll
+  for (int o = LPC / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (lane == 0 && in) {
+    v = fmaf(skip, xv, v);
+    if (a.z.p) v *= silu(zv);
+    y[h] = from_f<T>(on ? v : 0.f);
   }
 }
 
@@ -369,31 +386,21 @@ auto with_states(int N, F f) {
   if (N <= 128) return f(Geo<16, 8>{});
   return f(Geo<32, 8>{});
 }
-// The same for one token, 4 each.
-template <int LPC_, int SPT_>
-struct StepGeo {
-  static constexpr int LPC = LPC_, SPT = SPT_;
-};
-template <typename F>
-void with_step_states(int N, F f) {
-  if (N <= 4) return f(StepGeo<1, 4>{});
-  if (N <= 8) return f(StepGeo<2, 4>{});
-  if (N <= 16) return f(StepGeo<4, 4>{});
-  if (N <= 32) return f(StepGeo<8, 4>{});
-  if (N <= 64) return f(StepGeo<16, 4>{});
-  if (N <= 128) return f(StepGeo<32, 4>{});
-  return f(StepGeo<32, 8>{});
-}
-
 template <typename T>
 cudaError_t step_t(const s4_selective_args& a, St st, cudaStream_t s) {
-  const bool vec = a.N % 4 == 0 && vec_ok(a.state, 4, 16) && vec_ok(a.state_out, 4, 16) && vec_ok(a.A, 4, 16);
+  const int e = sizeof(T);
   s4impl::TimedLaunch tl("selective_step", s);
-  with_step_states(a.N, [&](auto geo) {
+  with_states(a.N, [&](auto geo) {
     using G = decltype(geo);
-    constexpr int HB = 256 / G::LPC;
-    const dim3 grid(a.G * ((a.H / a.G + HB - 1) / HB), a.batch);
-    selective_step_kernel<T, G::LPC, G::SPT><<<grid, 256, 0, s>>>(a, vec, st);
+    constexpr int LPC = G::LPC, SPT = G::SPT, HB = kStepThreads / LPC, pb = e * SPT < 16 ? e * SPT : 16;
+    const bool vec = a.N % 4 == 0 && vec_ok(a.state, 4, 16) && vec_ok(a.state_out, 4, 16) && vec_ok(a.A, 4, 16);
+    const bool vecbc = vec_ok(a.B.p, e, pb, a.B.batch) && vec_ok(a.C.p, e, pb, a.C.batch) && a.B_group * e % pb == 0 &&
+                       a.C_group * e % pb == 0;
+    const dim3 grid(chan_blocks<HB>(a.H, a.G), a.batch);
+    if (vec && vecbc && a.N == G::NP && (a.H / a.G) % HB == 0)
+      selective_step_kernel<T, LPC, SPT, true><<<grid, kStepThreads, 0, s>>>(a, vec, vecbc, st);
+    else
+      selective_step_kernel<T, LPC, SPT, false><<<grid, kStepThreads, 0, s>>>(a, vec, vecbc, st);
   });
   return cudaGetLastError();
 }

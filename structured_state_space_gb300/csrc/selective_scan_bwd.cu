@@ -10,23 +10,18 @@
 // shared memory and the shuffles deliver to registers bound it, about 20 clocks of an SM quarter
 // each for 32 (token, channel, state).
 //
-// Three kernels.  (1) per segment of tokens, walking forward: the state at each tile's start, from
+// Four kernels.  (1) per segment of tokens, walking forward: the state at each tile's start, from
 // a zero start, and the gradient at the segment's start from a zero end; (2) joins the
 // segments; (3) per segment, walking backward tile by tile with the gradient in registers:
 // the states at every block of TB tokens, then block by block the states again, in registers,
 // and the gradients.  Channels and tokens are summed in a fixed order: over a thread's channels,
-// its warp, its CTA, then as partial sums, which (4) adds up.
+// its warp, its CTA, then as partial sums, which (4) adds up.  With one segment there is no (2).
 #include <limits.h>
 
 #include "selective.cuh"
 
 namespace {
 using namespace s4sel;
-#ifndef S4_EB
-#define S4_EB 4
-#define S4_TBK 4
-#define S4_KC 24
-#endif
 
 template <int LPC_, int SPT_>
 struct Geo {
@@ -164,7 +159,7 @@ struct Place {
 // (1) A warp per channel block and segment, in tiles of TT tokens read ahead by one.  The gradient
 // at the segment's start is R = sum_t (prod_{j<=t} a_j) C_t dyp_t.
 template <typename T, typename G, bool WHOLE>
-__global__ void __launch_bounds__(kThreads, S4_EB) selective_ends_kernel(s4_selective_bwd_args a, Work w, bool vec, bool vecbc,
+__global__ void __launch_bounds__(kThreads, 4) selective_ends_kernel(s4_selective_bwd_args a, Work w, bool vec, bool vecbc,
                                                                      bool vecn, St st) {
   constexpr int LPC = G::LPC, SPT = G::SPT, CPT = G::CPT, NP = G::NP, CH = G::CH, TT = G::TT, OWN = G::OWN;
   constexpr int V0 = 16 / (int)sizeof(T), VB = V0 < G::VECS ? V0 : G::VECS, NB = G::VECS / VB;
@@ -352,7 +347,6 @@ __global__ void __launch_bounds__(128) selective_joins_kernel(s4_selective_bwd_a
       g = fmaf(ex2(dg[e] * A), g, gv[e]);
     }
   }
-  if (a.dstate0) a.dstate0[(long long)b * HN + i] = g;
 }
 
 // 16 values per lane summed over the warp's channel slots: halves are exchanged over the lanes'
@@ -412,7 +406,7 @@ __device__ __forceinline__ float softplus_slope(float d) {
 
 // (3) A CTA per HB channels and segment.
 template <typename T, typename G, bool WHOLE>
-__global__ void __launch_bounds__(kThreads, S4_TBK) selective_tiles_kernel(s4_selective_bwd_args a, Work w, bool vec, bool vecbc,
+__global__ void __launch_bounds__(kThreads, 4) selective_tiles_kernel(s4_selective_bwd_args a, Work w, bool vec, bool vecbc,
                                                                       bool vecn, St st) {
   constexpr int LPC = G::LPC, SPT = G::SPT, CPT = G::CPT, NP = G::NP, CH = G::CH, TC = G::TC, TB = G::TB, OWN = G::OWN;
   using Sum = SumSlots<LPC>;
@@ -449,7 +443,10 @@ __global__ void __launch_bounds__(kThreads, S4_TBK) selective_tiles_kernel(s4_se
   for (int j = 0; j < CPT; ++j) {
     const int n = j < nh ? nn : 0;
     ld_states<SPT>(A[j], a.A + (long long)(h + j) * a.N + n0, n, vecn);
-    ld_states<SPT>(g[j], w.g_seg + (srow + j) * a.N + n0, n, vecn);
+    if (w.segs > 1)
+      ld_states<SPT>(g[j], w.g_seg + (srow + j) * a.N + n0, n, vecn);
+    else
+      ld_states<SPT>(g[j], a.dstate + ((long long)b * a.H + h + j) * a.N + n0, a.dstate ? n : 0, vecn);
 #pragma unroll
     for (int i = 0; i < SPT / 2; ++i) {
       A[j][i] = mul2(A[j][i], make_float2(kLog2e, kLog2e));
@@ -755,6 +752,7 @@ __global__ void __launch_bounds__(kThreads, S4_TBK) selective_tiles_kernel(s4_se
   for (int j = 0; j < CPT; ++j) {
     if (j >= nh) continue;
     st_states<SPT>(ph + (long long)(h + j) * a.N + n0, nn, vecn, dA[j]);
+    if (seg == 0 && a.dstate0) st_states<SPT>(a.dstate0 + ((long long)b * a.H + h + j) * a.N + n0, nn, vecn, g[j]);
     if (lane == 0) {
       ph[(long long)a.H * a.N + h + j] = j ? dD.y : dD.x;
       ph[(long long)a.H * (a.N + 1) + h + j] = j ? db.y : db.x;
@@ -762,31 +760,32 @@ __global__ void __launch_bounds__(kThreads, S4_TBK) selective_tiles_kernel(s4_se
   }
 }
 
-// (4) The partial sums: over segments and sequences ...
-__global__ void __launch_bounds__(256) selective_sums_kernel(const float* part, int rows, int H, int N, float* dA, float* dD,
-                                                             float* db) {
-  column_sums(part, rows, (long long)H * (N + 2), [=](long long c, float v) {
-    const long long HN = (long long)H * N;
-    if (c < HN)
-      dA[c] = v;
-    else if (c < HN + H) {
-      if (dD) dD[c - HN] = v;
-    } else if (db) {
-      db[c - HN - H] = v;
-    }
-  });
-}
-// ... and dB, dC over a group's channel blocks.
+// (4) The partial sums, in one launch: those over segments and sequences by the first CTAs, dB and dC
+// over a group's channel blocks by the others.
 template <typename T>
-__global__ void __launch_bounds__(256) selective_vectors_kernel(s4_selective_bwd_args a, Work w, int NP, int per) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, rows = (long long)a.batch * a.L;
-  const int cols = a.G * 2 * NP;
-  if (i >= rows * cols) return;
-  const long long row = i / cols;
-  const int g = (int)(i % cols) / (2 * NP), n = (int)(i % (2 * NP));
+__global__ void __launch_bounds__(256) selective_sums_kernel(s4_selective_bwd_args a, Work w, int NP, int param_ctas) {
+  const long long HN = (long long)a.H * a.N, cols = HN + 2ll * a.H;
+  if (blockIdx.x < param_ctas) {
+    column_sums(w.part_h, a.batch * w.segs, cols, [=](long long c, float v) {
+      if (c < HN)
+        a.dA[c] = v;
+      else if (c < HN + a.H) {
+        if (a.dD) a.dD[c - HN] = v;
+      } else if (a.ddt_bias) {
+        a.ddt_bias[c - HN - a.H] = v;
+      }
+    });
+    return;
+  }
+  const long long i = (long long)(blockIdx.x - param_ctas) * 256 + threadIdx.x, rows = (long long)a.batch * a.L;
+  const int per_row = a.G * 2 * NP, per = w.blocks / a.G;
+  if (i >= rows * per_row) return;
+  const long long row = i / per_row;
+  const int g = (int)(i % per_row) / (2 * NP), n = (int)(i % (2 * NP)), state = n % NP;
+  const float* p = w.part_bc + ((long long)g * per * rows + row) * 2 * NP + n;
   float v = 0.f;
-  for (int k = 0; k < per; ++k) v += w.part_bc[((long long)(g * per + k) * rows + row) * 2 * NP + n];
-  const int state = n % NP;
+#pragma unroll 4
+  for (int k = 0; k < per; ++k) v += p[(long long)k * rows * 2 * NP];
   if (state >= a.N) return;
   T* out = static_cast<T*>(n < NP ? a.dB : a.dC);
   out[(row * a.G + g) * a.N + state] = from_f<T>(v);
@@ -804,7 +803,10 @@ auto with_states(int N, F f) {
   return f(Geo<32, 8>{}, EndsGeo<32, 8, Geo<32, 8>::TC>{});
 }
 
-constexpr int kCtas = S4_KC;  // per SM that the segments are meant to give: two rounds of (3)
+// CTAs per SM that the segments are meant to give: six rounds of (3).  4 sequences of 4096 tokens, 2048
+// channels and 16 states took 920 us with four rounds, 900 with six; 2 of 333 tokens, 256
+// channels and 64 states 127 us with segments of four tiles or more, 65 with one.
+constexpr int kCtas = 24;
 
 // Sizes and the workspace's layout (pointers relative to a null base when ws is null).
 template <typename G>
@@ -814,8 +816,7 @@ Work layout(int batch, int L, int H, int N, int Gr, char* ws, size_t* total) {
   w.blocks = chan_blocks<G::HB>(H, Gr);
   const long long ctas = (long long)batch * w.blocks, want = (long long)s4impl::num_sms() * kCtas;
   long long segs = (want + ctas - 1) / ctas;
-  if (segs > w.tiles / 4) segs = w.tiles / 4;
-  if (segs < 1) segs = 1;
+  if (segs > w.tiles) segs = w.tiles;
   w.seg_tiles = (int)((w.tiles + segs - 1) / segs);
   w.segs = (w.tiles + w.seg_tiles - 1) / w.seg_tiles;
   const size_t HN = (size_t)H * N, bt = (size_t)batch * w.tiles, bs = (size_t)batch * w.segs;
@@ -849,7 +850,8 @@ cudaError_t bwd_t(const s4_selective_bwd_args& a, St st, cudaStream_t s) {
     constexpr int pb = e * (16 / e < E::VECS ? 16 / e : E::VECS);
     const bool vecbc = vec_ok(a.B.p, e, pb, a.B.batch, a.B.row) && vec_ok(a.C.p, e, pb, a.C.batch, a.C.row) &&
                        a.B_group * e % pb == 0 && a.C_group * e % pb == 0;
-    const bool vecn = a.N % 4 == 0 && vec_ok(a.A, 4, 16) && vec_ok(a.state0, 4, 16);
+    const bool vecn = a.N % 4 == 0 && vec_ok(a.A, 4, 16) && vec_ok(a.state0, 4, 16) && vec_ok(a.dstate, 4, 16) &&
+                      vec_ok(a.dstate0, 4, 16);
     const Work w = layout<G>(a.batch, a.L, a.H, a.N, a.G, static_cast<char*>(a.ws), nullptr);
     const auto run = [&](auto whole) {
       constexpr bool W = decltype(whole)::value;
@@ -863,7 +865,7 @@ cudaError_t bwd_t(const s4_selective_bwd_args& a, St st, cudaStream_t s) {
         ends<<<dim3((unsigned)((tasks + G::WARPS - 1) / G::WARPS), a.batch), kThreads, E::kBytes, s>>>(a, w, vec, vecbc,
                                                                                                        vecn, st);
       }
-      {
+      if (w.segs > 1) {
         s4impl::TimedLaunch tl("selective_bwd", s);
         const long long HN = (long long)a.H * a.N;
         selective_joins_kernel<<<dim3((unsigned)((HN + 127) / 128), a.batch), 128, 0, s>>>(a, w);
@@ -878,15 +880,10 @@ cudaError_t bwd_t(const s4_selective_bwd_args& a, St st, cudaStream_t s) {
       if (whole) run(std::true_type{});
     }
     if (!whole) run(std::false_type{});
-    {
-      s4impl::TimedLaunch tl("selective_bwd", s);
-      const long long cols = (long long)a.H * (a.N + 2);
-      selective_sums_kernel<<<(unsigned)((cols + 31) / 32), 256, 0, s>>>(w.part_h, a.batch * w.segs, a.H, a.N, a.dA, a.dD,
-                                                                        a.ddt_bias);
-    }
     s4impl::TimedLaunch tl("selective_bwd", s);
+    const int param_ctas = (int)(((long long)a.H * (a.N + 2) + 31) / 32);
     const long long n = (long long)a.batch * a.L * a.G * 2 * G::NP;
-    selective_vectors_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a, w, G::NP, w.blocks / a.G);
+    selective_sums_kernel<T><<<(unsigned)(param_ctas + (n + 255) / 256), 256, 0, s>>>(a, w, G::NP, param_ctas);
   });
   return cudaGetLastError();
 }
