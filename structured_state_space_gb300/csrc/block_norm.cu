@@ -17,26 +17,31 @@ constexpr int kMaxThreads = 512;  // of the CTA that holds a row
 
 // K sums over the group that holds a row: a warp, or the CTA's warps.  `red` has a slot per warp;
 // two sets of them alternate so that one barrier per round is enough.
-template <bool CTA, int K>
+template <int MAX, int K>
 __device__ __forceinline__ void group_sums(float (&v)[K], float (&red)[2][2][32], int& phase) {
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
-  if constexpr (CTA) {
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  if constexpr (MAX > 128) {
+    constexpr int MOST = MAX / 32;  // warps, a power of two
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5, from = lane & (MOST - 1);
     if (lane == 0) {
 #pragma unroll
       for (int k = 0; k < K; ++k) red[phase][k][wid] = v[k];
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = warp_sum(lane < nw ? red[phase][k][lane] : 0.f);
+    for (int k = 0; k < K; ++k) {
+      v[k] = from < nw ? red[phase][k][from] : 0.f;
+#pragma unroll
+      for (int o = MOST / 2; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    }
     phase ^= 1;
   }
 }
-template <bool CTA>
+template <int MAX>
 __device__ __forceinline__ float group_sum(float v, float (&red)[2][2][32], int& phase) {
   float s[1] = {v};
-  group_sums<CTA, 1>(s, red, phase);
+  group_sums<MAX, 1>(s, red, phase);
   return s[0];
 }
 
@@ -131,7 +136,7 @@ __global__ void __launch_bounds__(MAX, NV == 1 ? 1024 / MAX : 1) block_norm_kern
       for (int j = 0; j < V / 2; ++j) ss = fma2(v[i][j], v[i][j], ss);
     }
     float r1 = 1.f;
-    if (a.w_post) r1 = rsqrtf(group_sum<CTA>(both(ss), red, phase) * inv + a.eps);
+    if (a.w_post) r1 = rsqrtf(group_sum<MAX>(both(ss), red, phase) * inv + a.eps);
     ss = two(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -148,7 +153,7 @@ __global__ void __launch_bounds__(MAX, NV == 1 ? 1024 / MAX : 1) block_norm_kern
       st_pairs<R, V>(static_cast<R*>(a.h_out) + row * a.h_out_row + c, n, vec, hv[i]);
     }
     if (!a.w_pre) continue;
-    const float r2 = rsqrtf(group_sum<CTA>(both(ss), red, phase) * inv + a.eps);
+    const float r2 = rsqrtf(group_sum<MAX>(both(ss), red, phase) * inv + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (lane + i * width) * V, n = a.H - c;
@@ -204,6 +209,18 @@ __global__ void __launch_bounds__(MAX, NV == 1 ? 512 / MAX : 1)
     fetch_commit();
   };
   if (AHEAD) fetch(first, 0);
+  // q and w_pre: with one pack per thread they stay in registers
+  float2 q[V / 2], wp[V / 2];
+  const auto ld_params = [&](int i) {
+    const int c = (lane + i * width) * V, n = a.H - c;
+    float2 w[V / 2];
+    ld_param<V>(w, a.w_post, c, n, vec, 1.f);
+    ld_param<V>(q, a.scale, c, n, vec, 1.f);
+    ld_param<V>(wp, a.w_pre, c, n, vec, 1.f);
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) q[j] = mul2(q[j], w[j]);
+  };
+  if (NV == 1) ld_params(0);
   for (long long row = first; row < a.rows; row += step, stage ^= 1) {
     const T* o = static_cast<const T*>(a.o) + row * a.o_row;
     const T* gate = a.gate ? static_cast<const T*>(a.gate) + row * a.gate_row : nullptr;
@@ -233,7 +250,7 @@ __global__ void __launch_bounds__(MAX, NV == 1 ? 512 / MAX : 1)
       for (int j = 0; j < V / 2; ++j) ss = fma2(v[i][j], v[i][j], ss);
     }
     float r1 = 1.f;
-    if (a.w_post) r1 = rsqrtf(group_sum<CTA>(both(ss), red, phase) * inv + a.eps);
+    if (a.w_post) r1 = rsqrtf(group_sum<MAX>(both(ss), red, phase) * inv + a.eps);
     // v -> unit; h'
     float r2 = 0.f, m2 = 0.f;
     if (with_dy) {
@@ -242,20 +259,17 @@ __global__ void __launch_bounds__(MAX, NV == 1 ? 512 / MAX : 1)
       for (int i = 0; i < NV; ++i) {
         const int c = (lane + i * width) * V, n = a.H - c;
         if (n <= 0) continue;
-        float2 w[V / 2], sc[V / 2], wp[V / 2];
-        ld_param<V>(w, a.w_post, c, n, vec, 1.f);
-        ld_param<V>(sc, a.scale, c, n, vec, 1.f);
-        ld_param<V>(wp, a.w_pre, c, n, vec, 1.f);
+        if (NV > 1) ld_params(i);
 #pragma unroll
         for (int j = 0; j < V / 2; ++j) {
           v[i][j] = mul2(v[i][j], two(r1));
-          hv[i][j] = fma2(sc[j], mul2(v[i][j], w[j]), hv[i][j]);
+          hv[i][j] = fma2(q[j], v[i][j], hv[i][j]);
           s0 = fma2(hv[i][j], hv[i][j], s0);
           s1 = fma2(mul2(d[i][j], wp[j]), hv[i][j], s1);
         }
       }
       float sum[2] = {both(s0), both(s1)};
-      group_sums<CTA, 2>(sum, red, phase);
+      group_sums<MAX, 2>(sum, red, phase);
       r2 = rsqrtf(sum[0] * inv + a.eps);
       m2 = r2 * sum[1] * inv;
     } else {
@@ -270,27 +284,25 @@ __global__ void __launch_bounds__(MAX, NV == 1 ? 512 / MAX : 1)
     for (int i = 0; i < NV; ++i) {
       const int c = (lane + i * width) * V, n = a.H - c;
       if (n <= 0) continue;
-      float2 e[V / 2], w[V / 2], sc[V / 2], wp[V / 2];
+      float2 e[V / 2];
+      if (NV > 1) ld_params(i);
       if (a.dh_out)
         rows.get_r(stage, 1, i, static_cast<const R*>(a.dh_out) + row * a.dh_out_row + c, n, vec, e);
       else
 #pragma unroll
         for (int j = 0; j < V / 2; ++j) e[j] = two(0.f);
-      ld_param<V>(w, a.w_post, c, n, vec, 1.f);
-      ld_param<V>(sc, a.scale, c, n, vec, 1.f);
-      ld_param<V>(wp, a.w_pre, c, n, vec, 1.f);
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) {
         const float2 unit2 = mul2(hv[i][j], two(r2));
         s_pre[i][j] = fma2(d[i][j], unit2, s_pre[i][j]);
         e[j] = fma2(two(r2), fma2(unit2, two(-m2), mul2(d[i][j], wp[j])), e[j]);
         U[i][j] = fma2(e[j], v[i][j], U[i][j]);
-        d[i][j] = mul2(mul2(e[j], sc[j]), w[j]);
+        d[i][j] = mul2(e[j], q[j]);
         ss = fma2(d[i][j], v[i][j], ss);
       }
       if (a.dh) st_pairs<R, V>(static_cast<R*>(a.dh) + row * a.dh_row + c, n, vec, e);
     }
-    const float m1 = a.w_post ? group_sum<CTA>(both(ss), red, phase) * inv : 0.f;
+    const float m1 = a.w_post ? group_sum<MAX>(both(ss), red, phase) * inv : 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (lane + i * width) * V, n = a.H - c;
@@ -303,9 +315,9 @@ __global__ void __launch_bounds__(MAX, NV == 1 ? 512 / MAX : 1)
         rows.get_t(stage, 0, i, o + c, n, vec, ov);
 #pragma unroll
         for (int j = 0; j < V / 2; ++j) {
-          const float2 s = sigmoid(g[j]), q = mul2(g[j], s);
-          ov[j] = mul2(mul2(ov[j], d[i][j]), fma2(q, fma2(s, two(-1.f), two(1.f)), s));
-          d[i][j] = mul2(d[i][j], q);
+          const float2 s = sigmoid(g[j]), act = mul2(g[j], s);
+          ov[j] = mul2(mul2(ov[j], d[i][j]), fma2(act, fma2(s, two(-1.f), two(1.f)), s));
+          d[i][j] = mul2(d[i][j], act);
         }
         st_pairs<T, V>(static_cast<T*>(a.dgate) + row * a.dgate_row + c, n, vec, ov);
       }

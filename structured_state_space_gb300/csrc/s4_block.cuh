@@ -126,12 +126,28 @@ __device__ __forceinline__ void ld_f(const T* p, int n, bool vec, float (&v)[V])
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] = r.get(i);
 }
+// Two values rounded into one word.
+template <typename T>
+__device__ __forceinline__ unsigned two_of(float lo, float hi) {
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const unsigned*>(&r);
+  } else {
+    const __half2 r = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const unsigned*>(&r);
+  }
+}
 template <typename T, int V>
 __device__ __forceinline__ void st_f(T* p, int n, bool vec, const float (&v)[V]) {
   Pack<T, V> r;
-  r.zero();
+  if constexpr (sizeof(T) == 2 && V % 2 == 0) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) r.put(i, from_f<T>(v[i]));
+    for (int i = 0; i < V / 2; ++i) r.w[i] = two_of<T>(v[2 * i], v[2 * i + 1]);
+  } else {
+    r.zero();
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.put(i, from_f<T>(v[i]));
+  }
   st_pack<T, V>(p, n, vec, r);
 }
 
