@@ -84,32 +84,6 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas)
   const T* C = static_cast<const T*>(a.C.p) + b * a.C.batch + c.g * a.C_group;
   T* y = MODE ? static_cast<T*>(a.y.p) + b * a.y.batch + h : nullptr;
 
-  float2 A[CPT][SPT / 2], s[CPT][SPT / 2];  // pairs of neighbouring states
-  float bias[CPT], skip[CPT];
-  float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int j = 0; j < CPT; ++j) {
-    const int hs = h + j;
-    const bool on = j < nh;
-    bias[j] = a.dt_bias && on ? a.dt_bias[hs] : 0.f;
-    skip[j] = MODE && a.D && on ? a.D[hs] : 0.f;
-#pragma unroll
-    for (int i = 0; i < SPT; ++i) {
-      const int n = n0 + i;
-      const bool in = on && n < a.N;
-      float v = 0.f;
-      if (MODE == 1 && in && (t0 < q.len || chunk == 0)) {
-        if (ck.count > 1)
-          v = ck.start[(((long long)b * ck.count + chunk) * a.H + hs) * a.N + n];
-        else if (a.state && q.slot >= 0)
-          v = a.state[(q.slot * a.H + hs) * a.N + n];
-      }
-      const float Av = in ? a.A[(long long)hs * a.N + n] * kLog2e : 0.f;
-      (i % 2 ? A[j][i / 2].y : A[j][i / 2].x) = Av;
-      (i % 2 ? s[j][i / 2].y : s[j][i / 2].x) = v;
-    }
-  }
-
   // the k-th token of a tile that this lane owns
   const auto token = [&](int k) { return k / kOwn<LPC> * 4 + own_token<LPC>(lane, k % kOwn<LPC>); };
   // this lane's slots of the next tile
@@ -147,7 +121,33 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas)
       if (MODE == 1) nextv[(NB + k) * 32] = ld_pack<T, VB>(C + t * a.C.row + i % NP, n, vecbc);
     }
   };
-  if (t0 < live) fetch(t0);
+  if (t0 < live) fetch(t0);  // before the reads below, which take as long
+  float2 A[CPT][SPT / 2], s[CPT][SPT / 2];  // pairs of neighbouring states
+  float bias[CPT], skip[CPT];
+  float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int j = 0; j < CPT; ++j) {
+    const int hs = h + j;
+    const bool on = j < nh;
+    bias[j] = a.dt_bias && on ? a.dt_bias[hs] : 0.f;
+    skip[j] = MODE && a.D && on ? a.D[hs] : 0.f;
+#pragma unroll
+    for (int i = 0; i < SPT; ++i) {
+      const int n = n0 + i;
+      const bool in = on && n < a.N;
+      float v = 0.f;
+      if (MODE == 1 && in && (t0 < q.len || chunk == 0)) {
+        if (ck.count > 1)
+          v = ck.start[(((long long)b * ck.count + chunk) * a.H + hs) * a.N + n];
+        else if (a.state && q.slot >= 0)
+          v = a.state[(q.slot * a.H + hs) * a.N + n];
+      }
+      const float Av = in ? a.A[(long long)hs * a.N + n] * kLog2e : 0.f;
+      (i % 2 ? A[j][i / 2].y : A[j][i / 2].x) = Av;
+      (i % 2 ? s[j][i / 2].y : s[j][i / 2].x) = v;
+    }
+  }
+
   for (int tb = t0; tb < live; tb += TT) {
     const bool whole = tb + TT <= live;
     Pack<T, CPT> px[OWN], pz[OWN];

@@ -185,22 +185,6 @@ __global__ void __launch_bounds__(kThreads, 4) selective_ends_kernel(s4_selectiv
   const T* B = static_cast<const T*>(a.B.p) + b * a.B.batch + c.g * a.B_group;
   const T* C = static_cast<const T*>(a.C.p) + b * a.C.batch + c.g * a.C_group;
   const int t0 = seg * w.seg_tiles * G::TC, t1 = min(a.L, t0 + w.seg_tiles * G::TC), live = min(t1, q.len);
-  float2 A[CPT][SPT / 2], s[CPT][SPT / 2], P[CPT][SPT / 2], R[CPT][SPT / 2], sum = make_float2(0.f, 0.f);
-  const float2 bias = make_float2(a.dt_bias && nh > 0 ? a.dt_bias[h] : 0.f, a.dt_bias && nh > 1 ? a.dt_bias[h + 1] : 0.f);
-#pragma unroll
-  for (int j = 0; j < CPT; ++j) {
-    const int n = j < nh ? nn : 0;
-    ld_states<SPT>(A[j], a.A + (long long)(h + j) * a.N + n0, n, vecn);
-    if (seg == 0 && a.state0)
-      ld_states<SPT>(s[j], a.state0 + ((long long)b * a.H + h + j) * a.N + n0, n, vecn);
-#pragma unroll
-    for (int i = 0; i < SPT / 2; ++i) {
-      A[j][i] = mul2(A[j][i], make_float2(kLog2e, kLog2e));
-      if (!(seg == 0 && a.state0)) s[j][i] = make_float2(0.f, 0.f);
-      P[j][i] = make_float2(1.f, 1.f);
-      R[j][i] = make_float2(0.f, 0.f);
-    }
-  }
   // this lane's slots of the next tile
   Cells<T, OWN, 32> next{reinterpret_cast<Pack<T, 2>*>(mine + G::X0) + wl};
   Pack<T, VB>* nextv = reinterpret_cast<Pack<T, VB>*>(mine + G::V0) + wl;
@@ -228,7 +212,23 @@ __global__ void __launch_bounds__(kThreads, 4) selective_ends_kernel(s4_selectiv
       nextv[(NB + k) * 32] = ld_pack<T, VB>(C + t * a.C.row + i % NP, n, vecbc);
     }
   };
-  if (t0 < live) fetch(t0);
+  if (t0 < live) fetch(t0);  // before the reads below, which take as long
+  float2 A[CPT][SPT / 2], s[CPT][SPT / 2], P[CPT][SPT / 2], R[CPT][SPT / 2], sum = make_float2(0.f, 0.f);
+  const float2 bias = make_float2(a.dt_bias && nh > 0 ? a.dt_bias[h] : 0.f, a.dt_bias && nh > 1 ? a.dt_bias[h + 1] : 0.f);
+#pragma unroll
+  for (int j = 0; j < CPT; ++j) {
+    const int n = j < nh ? nn : 0;
+    ld_states<SPT>(A[j], a.A + (long long)(h + j) * a.N + n0, n, vecn);
+    if (seg == 0 && a.state0)
+      ld_states<SPT>(s[j], a.state0 + ((long long)b * a.H + h + j) * a.N + n0, n, vecn);
+#pragma unroll
+    for (int i = 0; i < SPT / 2; ++i) {
+      A[j][i] = mul2(A[j][i], make_float2(kLog2e, kLog2e));
+      if (!(seg == 0 && a.state0)) s[j][i] = make_float2(0.f, 0.f);
+      P[j][i] = make_float2(1.f, 1.f);
+      R[j][i] = make_float2(0.f, 0.f);
+    }
+  }
   for (int tb = t0; tb < t1; tb += TT) {
     if (tb % G::TC == 0) {  // a tile of (3) starts
       const long long row = ((long long)b * w.tiles + tb / G::TC) * a.H + h;
@@ -434,25 +434,6 @@ __global__ void __launch_bounds__(kThreads, 4) selective_tiles_kernel(s4_selecti
   T* dzo = z ? static_cast<T*>(a.dz.p) + b * a.dz.batch + h : nullptr;
   const int first = seg * w.seg_tiles, last = min(w.tiles, first + w.seg_tiles);
 
-  float2 A[CPT][SPT / 2], g[CPT][SPT / 2], dA[CPT][SPT / 2];
-  float2 dD = make_float2(0.f, 0.f), db = dD;
-  const float2 bias = make_float2(a.dt_bias && nh > 0 ? a.dt_bias[h] : 0.f, a.dt_bias && nh > 1 ? a.dt_bias[h + 1] : 0.f);
-  const float2 Dv = make_float2(a.D && nh > 0 ? a.D[h] : 0.f, a.D && nh > 1 ? a.D[h + 1] : 0.f);
-  const long long srow = ((long long)b * w.segs + seg) * a.H + h;
-#pragma unroll
-  for (int j = 0; j < CPT; ++j) {
-    const int n = j < nh ? nn : 0;
-    ld_states<SPT>(A[j], a.A + (long long)(h + j) * a.N + n0, n, vecn);
-    if (w.segs > 1)
-      ld_states<SPT>(g[j], w.g_seg + (srow + j) * a.N + n0, n, vecn);
-    else
-      ld_states<SPT>(g[j], a.dstate + ((long long)b * a.H + h + j) * a.N + n0, a.dstate ? n : 0, vecn);
-#pragma unroll
-    for (int i = 0; i < SPT / 2; ++i) {
-      A[j][i] = mul2(A[j][i], make_float2(kLog2e, kLog2e));
-      dA[j][i] = make_float2(0.f, 0.f);
-    }
-  }
   // this thread's slots of the tile that comes next, the one before in time
   constexpr int V0 = 16 / (int)sizeof(T), VB = V0 < G::VECS ? V0 : G::VECS, NB = G::VECS / VB;
   Cells<T, OWN, kThreads> next{reinterpret_cast<Pack<T, 2>*>(smem + G::X0) + threadIdx.x};
@@ -501,7 +482,26 @@ __global__ void __launch_bounds__(kThreads, 4) selective_tiles_kernel(s4_selecti
         nexts[(j * SPT / 4 + i) * kThreads] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
     }
   };
-  fetch(last - 1);
+  fetch(last - 1);  // before the reads below, which take as long
+  float2 A[CPT][SPT / 2], g[CPT][SPT / 2], dA[CPT][SPT / 2];
+  float2 dD = make_float2(0.f, 0.f), db = dD;
+  const float2 bias = make_float2(a.dt_bias && nh > 0 ? a.dt_bias[h] : 0.f, a.dt_bias && nh > 1 ? a.dt_bias[h + 1] : 0.f);
+  const float2 Dv = make_float2(a.D && nh > 0 ? a.D[h] : 0.f, a.D && nh > 1 ? a.D[h + 1] : 0.f);
+  const long long srow = ((long long)b * w.segs + seg) * a.H + h;
+#pragma unroll
+  for (int j = 0; j < CPT; ++j) {
+    const int n = j < nh ? nn : 0;
+    ld_states<SPT>(A[j], a.A + (long long)(h + j) * a.N + n0, n, vecn);
+    if (w.segs > 1)
+      ld_states<SPT>(g[j], w.g_seg + (srow + j) * a.N + n0, n, vecn);
+    else
+      ld_states<SPT>(g[j], a.dstate + ((long long)b * a.H + h + j) * a.N + n0, a.dstate ? n : 0, vecn);
+#pragma unroll
+    for (int i = 0; i < SPT / 2; ++i) {
+      A[j][i] = mul2(A[j][i], make_float2(kLog2e, kLog2e));
+      dA[j][i] = make_float2(0.f, 0.f);
+    }
+  }
   for (int tile = last - 1; tile >= first; --tile) {
     const int tb = tile * TC, live = min(TC, q.len - tb);  // <= 0: a tile of padding
     float* bc = w.part_bc + (((long long)block * a.batch + b) * a.L + tb) * 2 * NP;
