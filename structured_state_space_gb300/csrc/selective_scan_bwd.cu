@@ -31,12 +31,12 @@ struct Geo {
   static constexpr int TC = LPC == 1 ? 8 : 16, TB = 4;   // tokens of a tile, of a block in registers
   static constexpr int OWN = TC / 4 * kOwn<LPC>;         // tokens of a tile that a lane stages and finishes
   // shared memory in floats: (step, x) and (dyp, dy silu') of channel pairs, [TC][ROW] each | B, C [TC][NP] | states at
-  // blocks | sums of dB, dC [WARPS][TB][RROW]
+  // blocks | sums of dB, dC [2][WARPS][TB][RROW]
   static constexpr int ROW = WARPS * SLOTS * 4 + row_pad(LPC, WARPS * SLOTS * 4), RROW = 2 * NP + 16;
   static constexpr int B0 = 2 * TC * ROW, C0 = B0 + TC * NP, S0 = C0 + TC * NP;
   // | the tile before: x, dt, z, dy [4][OWN][kThreads] packs of 2 | B, C | its states
   static constexpr int VECS = TC * NP / kThreads > 0 ? TC * NP / kThreads : 1;  // elements of B, of C a thread stages
-  static constexpr int R0 = S0 + TC / TB * kThreads * CPT * SPT, X0 = R0 + WARPS * TB * RROW;
+  static constexpr int R0 = S0 + TC / TB * kThreads * CPT * SPT, X0 = R0 + 2 * WARPS * TB * RROW;
   template <typename T>
   static constexpr int V0() { return X0 + 4 * OWN * kThreads * 2 * (int)sizeof(T) / 4; }
   template <typename T>
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 4) selective_tiles_kernel(s4_selecti
   float(*sb)[NP] = reinterpret_cast<float(*)[NP]>(smem + G::B0);
   float(*sc)[NP] = reinterpret_cast<float(*)[NP]>(smem + G::C0);
   float4* keep = reinterpret_cast<float4*>(smem + G::S0) + threadIdx.x;
-  float(*red)[TB][G::RROW] = reinterpret_cast<float(*)[TB][G::RROW]>(smem + G::R0);
+  float(*reds)[TB][G::RROW] = reinterpret_cast<float(*)[TB][G::RROW]>(smem + G::R0);  // blocks take them in turn
   const int b = blockIdx.y, seg = blockIdx.x / w.blocks, block = blockIdx.x % w.blocks;
   const int wid = threadIdx.x / 32, wl = threadIdx.x & 31;
   const Chan c = chan_of<G::HB>(block, a.H / a.G);
@@ -598,6 +598,7 @@ __global__ void __launch_bounds__(kThreads, 4) selective_tiles_kernel(s4_selecti
 #pragma unroll 1
     for (int k = TC / TB - 1; k >= 0; --k) {
       float2 s[TB][CPT][SPT / 2];  // before each token
+      float(*red)[TB][G::RROW] = reds + (k & 1) * G::WARPS;
       float vy[CPT][TB], vu[CPT][TB], vw[CPT][TB];
 #pragma unroll
       for (int i = 0; i < SPT / 2; ++i) {
@@ -735,7 +736,6 @@ __global__ void __launch_bounds__(kThreads, 4) selective_tiles_kernel(s4_selecti
         const int t = k * TB + u;
         if (tb + t < a.L && S4_IN(tb + t, a.L)) bc[t * 2 * NP + n] = v;
       }
-      __syncthreads();
     }
   }
   // the segment's part of dA, dD, ddt_bias (lanes that own no tokens hold the sums of none)
