@@ -273,6 +273,8 @@ s4_status s4_hippo_dplr(int kind, int N, double theta, const double* B, const do
  *    zeros, touches no state, and is recorded as S4_ERR_INVALID_INDEX in the
  *    status block of `ws` (read with s4_get_status).
  *  - Results are the same on every run: no sum goes through atomics.
+ *  - Outputs do not overlap inputs or each other, except where a comment below allows one array
+ *    for both (state and state_out, h and h_out).
  *  - Sizes: 1 <= batch <= 65535, 1 <= L <= 2^24, 1 <= H <= 65536,
  *    2 <= W <= 8, 1 <= N <= 256; offsets are 64 bits wide.
  * ====================================================================== */

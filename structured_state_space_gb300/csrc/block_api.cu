@@ -42,6 +42,7 @@ s4_status s4_short_conv_fwd(const s4_short_conv_args* a, void* stream) {
       !aligned(a->lengths, 4) || !aligned(a->index, 4) || !aligned(a->state, e) || !aligned(a->state_out, e))
     return S4_ERR_INVALID_ARG;
   if ((a->state || a->state_out) && (a->slots < 1 || (!a->index && a->slots < a->batch))) return S4_ERR_INVALID_ARG;
+  if (a->y.p == a->x.p && a->L > 1) return S4_ERR_INVALID_ARG;  // an output's neighbours still need its input
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   s4impl::St st{nullptr, 0u};
   if (a->ws) {
@@ -66,7 +67,7 @@ s4_status s4_short_conv_bwd(const s4_short_conv_bwd_args* a, void* stream) {
       !aligned(a->w, 4) || !aligned(a->dw, 4) || !aligned(a->bias, 4) || !aligned(a->dbias, 4) ||
       !aligned(a->lengths, 4) || !aligned(a->state0, e) || !aligned(a->dstate, e) || !aligned(a->dstate0, e))
     return S4_ERR_INVALID_ARG;
-  if (a->dstate0 && a->dstate0 == a->dstate) return S4_ERR_INVALID_ARG;
+  if ((a->dstate0 && a->dstate0 == a->dstate) || a->dx.p == a->x.p || a->dx.p == a->dy.p) return S4_ERR_INVALID_ARG;
   const s4_status w = ws_ok(a->ws, a->ws_bytes, s4_short_conv_bwd_workspace_bytes(a->batch, a->L, a->H, a->W));
   if (w != S4_OK) return w;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

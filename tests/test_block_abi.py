@@ -41,7 +41,7 @@ def call(lib, name, fmt, *values):
 
 
 def conv(**kw):
-    v = dict(x=(A, 8, 8), y=(A, 8, 8), w=A, bias=A, lengths=0, index=0, state=A, out=A, ws=A, nws=256, batch=1, L=1, H=8,
+    v = dict(x=(A, 8, 8), y=(2 * A, 8, 8), w=A, bias=A, lengths=0, index=0, state=A, out=A, ws=A, nws=256, batch=1, L=1, H=8,
              W=4, slots=1, dtype=1, silu=1) | kw
     return *v["x"], *v["y"], *(v[k] for k in ("w", "bias", "lengths", "index", "state", "out", "ws", "nws", "batch", "L",
                                               "H", "W", "slots", "dtype", "silu"))
@@ -51,7 +51,7 @@ def conv(**kw):
     ({"x": (0, 8, 8)}, 1), ({"y": (0, 8, 8)}, 1), ({"x": (A + 1, 8, 8)}, 1), ({"x": (A, -8, 8)}, 1), ({"w": 0}, 1),
     ({"w": A + 2}, 1), ({"batch": 0}, 1), ({"batch": 65536}, 1), ({"L": 0}, 1), ({"L": (1 << 24) + 1}, 1), ({"H": 0}, 1),
     ({"H": 65537}, 1), ({"W": 1}, 1), ({"W": 9}, 1), ({"dtype": 3}, 1), ({"slots": 0}, 1), ({"batch": 2}, 1),
-    ({"state": A + 1}, 1), ({"index": A + 2}, 1), ({"nws": 255}, 2), ({"ws": A + 64}, 2)])
+    ({"state": A + 1}, 1), ({"index": A + 2}, 1), ({"L": 2, "y": (A, 8, 8)}, 1), ({"nws": 255}, 2), ({"ws": A + 64}, 2)])
 def test_short_conv_refuses(lib, kw, code):
     assert call(lib, "s4_short_conv_fwd", block._CONV, *conv(**kw)) == code
 
