@@ -6,9 +6,9 @@
 //   dx = d u + D dyp,  draw = (x u + sum_n A w) softplus',  dA = sum d w,  dz = dy ypre silu'(z)
 //
 // Per (token, channel, state) 22 multiplications and additions, four exponentials and the sums of dB
-// and dC over channels; per (token, channel) 14 bytes in 16 bits.  The arithmetic and what
-// shared memory and the shuffles deliver to registers bound it, about 20 clocks of an SM quarter
-// each for 32 (token, channel, state).
+// and dC over channels; per (token, channel) 14 bytes in 16 bits.  Instructions bound it, about 44
+// clocks of an SM quarter for 32 (token, channel, state), and close behind what shared memory and the
+// shuffles deliver to registers.
 //
 // Four kernels.  (1) per segment of tokens, walking forward: the state at each tile's start, from
 // a zero start, and the gradient at the segment's start from a zero end; (2) joins the
@@ -16,6 +16,9 @@
 // the states at every block of TB tokens, then block by block the states again, in registers,
 // and the gradients.  Channels and tokens are summed in a fixed order: over a thread's channels,
 // its warp, its CTA, then as partial sums, which (4) adds up.  With one segment there is no (2).
+//
+// Measured: 899 us on 4 sequences of 4096 tokens, 2048 channels and 16 states in bfloat16: (1) 200, (2) 20,
+// (3) 650, (4) 28.
 #include <limits.h>
 
 #include "selective.cuh"
