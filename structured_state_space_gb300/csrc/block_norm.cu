@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(MAX, NV == 1 ? 512 / MAX : 1)
 }
 
 __global__ void __launch_bounds__(256) block_norm_sums_kernel(const float* part, int rows, s4_block_norm_bwd_args a) {
-  column_sums(part, rows, 2ll * a.H, [=](long long c, float v) {
+  column_sums(part, rows, 2ll * a.H, 2ll * a.H, [=](long long c, float v) {
     const int h = (int)(c % a.H);
     if (c >= a.H) {
       if (a.dw_pre) a.dw_pre[h] = v;

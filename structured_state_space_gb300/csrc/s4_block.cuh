@@ -272,10 +272,10 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// part[row][col] summed over the rows, columns in chunks of 32 per CTA, 8 row groups of
-// one warp each; put(col, sum).
+// part[row][col], rows `pitch` floats apart, summed over the rows, columns in chunks of 32 per
+// CTA, 8 row groups of one warp each; put(col, sum).
 template <typename Put>
-__device__ __forceinline__ void column_sums(const float* part, int rows, long long cols, Put put) {
+__device__ __forceinline__ void column_sums(const float* part, int rows, long long cols, long long pitch, Put put) {
   __shared__ float s[8][33];
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const long long c = (long long)blockIdx.x * 32 + lane;
@@ -283,12 +283,12 @@ __device__ __forceinline__ void column_sums(const float* part, int rows, long lo
   if (c < cols) {
     int r = wid;
     for (; r + 24 < rows; r += 32) {
-      a0 += part[r * cols + c];
-      a1 += part[(r + 8) * cols + c];
-      a2 += part[(r + 16) * cols + c];
-      a3 += part[(r + 24) * cols + c];
+      a0 += part[r * pitch + c];
+      a1 += part[(r + 8) * pitch + c];
+      a2 += part[(r + 16) * pitch + c];
+      a3 += part[(r + 24) * pitch + c];
     }
-    for (; r < rows; r += 8) a0 += part[r * cols + c];
+    for (; r < rows; r += 8) a0 += part[r * pitch + c];
   }
   s[wid][lane] = (a0 + a1) + (a2 + a3);
   __syncthreads();

@@ -68,7 +68,8 @@ struct Work {
   float *s_tile, *d_before;    // [batch][tiles][H][N], [batch][tiles][H]: state and step sum at a tile's start
   float *s_seg, *g_seg;        // [batch][segs][H][N]: a segment's ends from zero, then its corrections
   float *d_seg;                // [batch][segs][H]
-  float *part_h;               // [batch * segs][H][N + 2]: dA, dD, ddt_bias
+  float *part_h;               // [batch * segs][pitch_h]: dA [H][N], dD [H], ddt_bias [H]
+  long long pitch_h;           // H (N + 2) rounded up to whole words of 16 bytes, which dA is stored in
   float *part_bc;              // [blocks][batch][L][2 NP]
 };
 
@@ -742,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 4) selective_tiles_kernel(s4_selecti
     }
   }
   // the segment's part of dA, dD, ddt_bias (lanes that own no tokens hold the sums of none)
-  float* ph = w.part_h + ((long long)b * w.segs + seg) * a.H * (a.N + 2);
+  float* ph = w.part_h + ((long long)b * w.segs + seg) * w.pitch_h;
   if (LPC > 4 && lane >= 4) dD = db = make_float2(0.f, 0.f);
 #pragma unroll
   for (int o = 1; o < (LPC < 4 ? LPC : 4); o <<= 1) {
@@ -769,7 +770,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) selective_sums_kernel(s4_selective_bwd_args a, Work w, int NP, int param_ctas) {
   const long long HN = (long long)a.H * a.N, cols = HN + 2ll * a.H;
   if (blockIdx.x < param_ctas) {
-    column_sums(w.part_h, a.batch * w.segs, cols, [=](long long c, float v) {
+    column_sums(w.part_h, a.batch * w.segs, cols, w.pitch_h, [=](long long c, float v) {
       if (c < HN)
         a.dA[c] = v;
       else if (c < HN + a.H) {
@@ -834,7 +835,8 @@ Work layout(int batch, int L, int H, int N, int Gr, char* ws, size_t* total) {
   w.s_seg = take(bs * HN);
   w.g_seg = take(bs * HN);
   w.d_seg = take(bs * H);
-  w.part_h = take(bs * H * (N + 2));
+  w.pitch_h = ((long long)H * (N + 2) + 3) / 4 * 4;
+  w.part_h = take(bs * w.pitch_h);
   w.part_bc = take((size_t)w.blocks * batch * L * 2 * G::NP);
   // CTAs of one launch
   if (total) *total = (long long)chan_blocks<2>(H, Gr) * w.segs > INT_MAX ? 0 : at;

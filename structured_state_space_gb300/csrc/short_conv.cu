@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(32 * kWarpsBwd, KW <= 4 ? 2 : 1)
 
 __global__ void __launch_bounds__(256) short_conv_sums_kernel(const float* part, int rows, int H, int W, float* dw,
                                                               float* dbias) {
-  column_sums(part, rows, (long long)(W + 1) * H, [=](long long c, float v) {
+  column_sums(part, rows, (long long)(W + 1) * H, (long long)(W + 1) * H, [=](long long c, float v) {
     const long long k = c / H, h = c % H;
     if (k < W)
       dw[h * W + k] = v;
