@@ -295,7 +295,7 @@ typedef struct {
  * channel, and SiLU:  v_t = bias + sum_{k<W} w[k] x[t-W+1+k],  y = v sigmoid(v)
  * (silu = 0: y = v).  The W-1 inputs before the first token are the state (oldest
  * first); the state after the call is the last W-1 inputs.  L = 1 is the
- * single-token form.
+ * single-token form, in which y may be x (with the same batch stride).
  */
 typedef struct {
     s4_rows x;                /* [batch][L][H] */

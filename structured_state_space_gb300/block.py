@@ -166,7 +166,7 @@ def s4_short_conv_fwd(x, w, bias=None, *, silu=True, lengths=None, state=None, s
 
 
 def s4_short_conv_step(x, w, bias, state, *, silu=True, state_out=None, index=None, y=None, ws=None, stream=None):
-    """One token per sequence: x [batch, H] -> y [batch, H].  The state is updated in place, or
+    """One token per sequence: x [batch, H] -> y [batch, H] (y may be x).  The state is updated in place, or
     written to state_out (the old one then stays, as for tokens that may be rejected)."""
     if stream is not None:
         return _on(stream, s4_short_conv_step, x, w, bias, state, silu=silu, state_out=state_out, index=index, y=y, ws=ws)

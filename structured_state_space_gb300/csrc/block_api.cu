@@ -42,7 +42,8 @@ s4_status s4_short_conv_fwd(const s4_short_conv_args* a, void* stream) {
       !aligned(a->lengths, 4) || !aligned(a->index, 4) || !aligned(a->state, e) || !aligned(a->state_out, e))
     return S4_ERR_INVALID_ARG;
   if ((a->state || a->state_out) && (a->slots < 1 || (!a->index && a->slots < a->batch))) return S4_ERR_INVALID_ARG;
-  if (a->y.p == a->x.p && a->L > 1) return S4_ERR_INVALID_ARG;  // an output's neighbours still need its input
+  // in place: only single tokens (else an output's neighbours still need its input), each at its own address
+  if (a->y.p == a->x.p && (a->L > 1 || (a->batch > 1 && a->y.batch != a->x.batch))) return S4_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   s4impl::St st{nullptr, 0u};
   if (a->ws) {

@@ -98,7 +98,8 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(s4_short_conv_args
   }
   // The state after the last real token, row j being input len - (W-1) + j.  The thread
   // that read the channels' old state writes the new one (in place too: rows are taken
-  // from rows at or after them, in ascending order).
+  // from rows at or after them, in ascending order).  A single token is taken from its
+  // register: y may be x there, and has been written.
   if (seg == 0 && a.state_out && q.slot >= 0) {
     T* so = static_cast<T*>(a.state_out) + q.slot * sslot + h;
     for (int j = 0; j < a.W - 1; ++j) {
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(s4_short_conv_args
       Pack<T, V> r;
       r.zero();
       if (t >= 0)
-        r = ld_pack<T, V>(x + t * a.x.row, n, vec);
+        r = a.L == 1 ? in[0] : ld_pack<T, V>(x + t * a.x.row, n, vec);
       else if (state)
         r = ld_pack<T, V>(state + (t + a.W - 1) * srow, n, vec);
       if (S4_IN(q.slot, a.slots)) st_pack<T, V>(so + j * srow, n, vec, r);
