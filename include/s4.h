@@ -261,7 +261,8 @@ s4_status s4_hippo_dplr(int kind, int N, double theta, const double* B, const do
  *  - `lengths` [batch] (device, may be NULL): the sequences' real lengths, 0
  *    to L.  Tokens from there on are padding: what they hold (infinities and
  *    NaN too) is not used, their outputs and gradients are zeros, and the state
- *    stays as after the last real token.
+ *    stays as after the last real token.  What a real token's infinity reaches is
+ *    infinite or NaN, not always the one that the formula gives.
  *  - `state`, `state_out` (may be NULL): the state on entry (NULL: zeros) and
  *    where the state after the last real token goes (NULL: nowhere); they may
  *    be the same array (in place).  `index` [batch] (device, may be NULL):

@@ -649,6 +649,17 @@ __global__ void __launch_bounds__(kThreads, 4) selective_tiles_kernel(s4_selecti
           Sum::put(r, wl, [&](int v) { return &red[wid][u - (G::GT - 1) + v / SPT][NP + n0 + v % SPT]; });
         }
       }
+      // Padding adds nothing to dA, whatever state it holds back (an infinite one: 0 inf).  With 4 states
+      // per thread those states are cleared (skipping each product costs 2 % on 4 x 4096 x 2048 with 16
+      // states); with 8, where this spills more, the products are skipped (clearing costs 5 %).
+      constexpr bool CLEAR = SPT == 4;
+      if (CLEAR && !whole && (k + 1) * TB > live) {
+#pragma unroll
+        for (int u = 0; u < TB; ++u)
+#pragma unroll
+          for (int i = 0; i < SPT / 2; ++i)
+            if (k * TB + u >= live) s[u][0][i] = s[u][1][i] = make_float2(0.f, 0.f);
+      }
       // backward: the gradients of the states, dB, u, w, dA
 #pragma unroll
       for (int u = TB - 1; u >= 0; --u) {
@@ -677,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 4) selective_tiles_kernel(s4_selecti
               g[j][i + e] = mul2(gv, ex2(mul2(dd[j], A[j][i + e])));
               const float2 q1 = mul2(g[j][i + e], s[u][j][i + e]);
               ww[j] = i + e ? fma2(A[j][i + e], q1, ww[j]) : mul2(A[j][i + e], q1);
-              dA[j][i + e] = fma2(dd[j], q1, dA[j][i + e]);
+              if (CLEAR || whole || t < live) dA[j][i + e] = fma2(dd[j], q1, dA[j][i + e]);
             }
             r[u % G::GT * SPT + 2 * (i + e)] = rb.x;
             r[u % G::GT * SPT + 2 * (i + e) + 1] = rb.y;
@@ -712,8 +723,8 @@ __global__ void __launch_bounds__(kThreads, 4) selective_tiles_kernel(s4_selecti
           o1[j] = fmaf(d[j], vu[j][i], Dj[j] * pv[j]);
           o2[j] = fmaf(xv[j], vu[j][i], kLn2 * vw[j][i]);
           if (a.softplus) o2[j] *= softplus_slope(d[j]);
-          if (t >= live) o2[j] = 0.f;
           o3[j] = zf[j] * fmaf(Dj[j], xv[j], vy[j][i]);
+          if (t >= live) o1[j] = o2[j] = o3[j] = 0.f;
           od[j] = pv[j] * xv[j];
         }
         dD = add2(dD, make_float2(od[0], od[1]));
@@ -738,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 4) selective_tiles_kernel(s4_selecti
 #pragma unroll
         for (int e = 0; e < G::WARPS; ++e) v += red[e][u][n];
         const int t = k * TB + u;
-        if (tb + t < a.L && S4_IN(tb + t, a.L)) bc[t * 2 * NP + n] = v;
+        if (tb + t < a.L && S4_IN(tb + t, a.L)) bc[t * 2 * NP + n] = t < live ? v : 0.f;
       }
     }
   }
