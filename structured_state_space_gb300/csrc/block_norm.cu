@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(MAX, NV == 1 ? 1024 / MAX : 1) block_norm_kern
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (lane + i * width) * V;
-      if (row >= a.rows || c >= a.H || !S4_IN(row, a.rows)) continue;
+      if (row >= a.rows || c >= a.H) continue;
       rows.fetch_t(stage, 0, i, static_cast<const T*>(a.o) + row * a.o_row + c);
       if (a.gate) rows.fetch_t(stage, 1, i, static_cast<const T*>(a.gate) + row * a.gate_row + c);
       if (a.h) rows.fetch_r(stage, 0, i, static_cast<const R*>(a.h) + row * a.h_row + c);
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(MAX, NV == 1 ? 1024 / MAX : 1) block_norm_kern
       const int c = (lane + i * width) * V, n = a.H - c;
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) v[i][j] = hv[i][j] = two(0.f);
-      if (n <= 0 || !S4_IN(c, a.H) || !S4_IN(row, a.rows)) continue;
+      if (n <= 0) continue;
       rows.get_t(stage, 0, i, static_cast<const T*>(a.o) + row * a.o_row + c, n, vec, v[i]);
       if (a.h) rows.get_r(stage, 0, i, static_cast<const R*>(a.h) + row * a.h_row + c, n, vec, hv[i]);
       if (a.gate) {
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(MAX, NV == 1 ? 512 / MAX : 1)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (lane + i * width) * V;
-      if (row >= a.rows || c >= a.H || !S4_IN(row, a.rows)) continue;
+      if (row >= a.rows || c >= a.H) continue;
       rows.fetch_t(stage, 0, i, static_cast<const T*>(a.o) + row * a.o_row + c);
       if (a.gate) rows.fetch_t(stage, 1, i, static_cast<const T*>(a.gate) + row * a.gate_row + c);
       if (with_dy) rows.fetch_t(stage, 2, i, static_cast<const T*>(a.dy) + row * a.dy_row + c);
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(MAX, NV == 1 ? 512 / MAX : 1)
       const int c = (lane + i * width) * V, n = a.H - c;
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) v[i][j] = hv[i][j] = d[i][j] = two(0.f);
-      if (n <= 0 || !S4_IN(c, a.H)) continue;
+      if (n <= 0) continue;
       rows.get_t(stage, 0, i, o + c, n, vec, v[i]);
       if (with_dy) {
         rows.get_t(stage, 2, i, static_cast<const T*>(a.dy) + row * a.dy_row + c, n, vec, d[i]);
@@ -342,10 +342,10 @@ __global__ void __launch_bounds__(256) block_norm_sums_kernel(const float* part,
   column_sums(part, rows, 2ll * a.H, 2ll * a.H, [=](long long c, float v) {
     const int h = (int)(c % a.H);
     if (c >= a.H) {
-      if (a.dw_pre) a.dw_pre[h] = v;
+      if (a.dw_pre) wr(a.dw_pre + h, v);
     } else {
-      if (a.dw_post) a.dw_post[h] = a.scale ? a.scale[h] * v : v;
-      if (a.dscale) a.dscale[h] = a.w_post ? a.w_post[h] * v : v;
+      if (a.dw_post) wr(a.dw_post + h, a.scale ? rd(a.scale + h) * v : v);
+      if (a.dscale) wr(a.dscale + h, a.w_post ? rd(a.w_post + h) * v : v);
     }
   });
 }
@@ -411,6 +411,16 @@ cudaError_t fwd_t(const s4_block_norm_args& a, cudaStream_t s) {
                    vec_ok(a.y, et, bt, a.y_row) && vec_ok(a.w_post, 4, 16) && vec_ok(a.scale, 4, 16) &&
                    vec_ok(a.w_pre, 4, 16);
   const Shape sh = shape_for(a.H, V);
+#ifdef S4_BOUNDS_CHECK
+  s4impl::Extents x{};
+  x.add(a.o, et, true, false, a.H, a.rows, a.o_row);
+  x.add(a.gate, et, true, false, a.H, a.rows, a.gate_row);
+  x.add(a.h, er, true, false, a.H, a.rows, a.h_row);
+  x.add(a.h_out, er, false, true, a.H, a.rows, a.h_out_row);
+  x.add(a.y, et, false, true, a.H, a.rows, a.y_row);
+  for (const float* p : {a.w_post, a.scale, a.w_pre}) x.in(p, 4, a.H);
+  if (const cudaError_t err = set_extents(x, s); err != cudaSuccess) return err;
+#endif
   s4impl::TimedLaunch tl("block_norm", s);
   with_shape<V>(sh, [&](auto nv, auto max) {
     constexpr int NV = decltype(nv)::value, MAX = decltype(max)::value;
@@ -439,6 +449,21 @@ cudaError_t bwd_t(const s4_block_norm_bwd_args& a, cudaStream_t s) {
   const Shape sh = shape_for(a.H, V);
   int grid = 0;
   float* part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + s4impl::kStatusBytes);
+#ifdef S4_BOUNDS_CHECK
+  s4impl::Extents x{};
+  x.add(a.o, et, true, false, a.H, a.rows, a.o_row);
+  x.add(a.gate, et, true, false, a.H, a.rows, a.gate_row);
+  x.add(a.h, er, true, false, a.H, a.rows, a.h_row);
+  x.add(a.dy, et, true, false, a.H, a.rows, a.dy_row);
+  x.add(a.dh_out, er, true, false, a.H, a.rows, a.dh_out_row);
+  x.add(a.do_, et, false, true, a.H, a.rows, a.do_row);
+  x.add(a.dgate, et, false, true, a.H, a.rows, a.dgate_row);
+  x.add(a.dh, er, false, true, a.H, a.rows, a.dh_row);
+  for (const float* p : {a.w_post, a.scale, a.w_pre}) x.in(p, 4, a.H);
+  for (const float* p : {a.dw_post, a.dscale, a.dw_pre}) x.out(p, 4, a.H);
+  x.scratch(part, 4, a.H, (long long)(s4impl::block_norm_bwd_scratch(a.rows, a.H) / (4ull * a.H)));
+  if (const cudaError_t err = set_extents(x, s); err != cudaSuccess) return err;
+#endif
   {
     s4impl::TimedLaunch tl("block_norm_bwd", s);
     with_shape<V>(sh, [&](auto nv, auto max) {

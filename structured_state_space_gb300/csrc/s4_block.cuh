@@ -11,10 +11,37 @@
 
 #include "s4_block.h"
 #include "s4_dev.cuh"
+#include "s4_extents.h"
 
 namespace s4blk {
 
 using s4impl::St;
+
+// ---- accesses to global memory ------------------------------------------------------------------
+// touch(): whether an access may be made.  In the bounds-checked build each one is compared with the
+// extents of the call's arrays and its address with the access's width; one that does not fit is
+// counted and left out (a load gives zero).
+#ifdef S4_BOUNDS_CHECK
+static __device__ s4impl::Extents g_extents;
+static __device__ __noinline__ bool touch(const void* p, int bytes, int align, bool write) {
+  const bool ok = s4impl::access_ok(g_extents.list, g_extents.n, reinterpret_cast<unsigned long long>(p), bytes, align, write);
+  if (!ok) s4dev::s4_oob_hit();
+  return ok;
+}
+inline cudaError_t set_extents(const s4impl::Extents& x, cudaStream_t s) {
+  return cudaMemcpyToSymbolAsync(g_extents, &x, sizeof(x), 0, cudaMemcpyHostToDevice, s);
+}
+#else
+__device__ __forceinline__ constexpr bool touch(const void*, int, int, bool) { return true; }
+#endif
+template <typename T>
+__device__ __forceinline__ T rd(const T* p) {
+  return touch(p, sizeof(T), sizeof(T), false) ? *p : T{};
+}
+template <typename T>
+__device__ __forceinline__ void wr(T* p, T v) {
+  if (touch(p, sizeof(T), sizeof(T), true)) *p = v;
+}
 
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -74,6 +101,10 @@ __device__ __forceinline__ Pack<T, V> ld_pack(const T* p, int n, bool vec) {
   Pack<T, V> r;
   using P = Pack<T, V>;
   if (vec && n >= V) {
+    if (!touch(p, P::BYTES, P::BYTES < 16 ? P::BYTES : 16, false)) {
+      r.zero();
+      return r;
+    }
     if constexpr (P::BYTES >= 16) {
 #pragma unroll
       for (int i = 0; i < P::BYTES / 16; ++i)
@@ -87,7 +118,7 @@ __device__ __forceinline__ Pack<T, V> ld_pack(const T* p, int n, bool vec) {
     r.zero();
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (i < n) r.put(i, p[i]);
+      if (i < n) r.put(i, rd(p + i));
   }
   return r;
 }
@@ -100,6 +131,7 @@ template <typename T, int V>
 __device__ __forceinline__ void st_pack(T* p, int n, bool vec, const Pack<T, V>& r) {
   using P = Pack<T, V>;
   if (vec && n >= V) {
+    if (!touch(p, P::BYTES, P::BYTES < 16 ? P::BYTES : 16, true)) return;
     if constexpr (P::BYTES >= 16) {
 #pragma unroll
       for (int i = 0; i < P::BYTES / 16; ++i)
@@ -114,9 +146,9 @@ __device__ __forceinline__ void st_pack(T* p, int n, bool vec, const Pack<T, V>&
     for (int i = 0; i < V; ++i) {
       if (i >= n) continue;
       if constexpr (sizeof(T) == 4)
-        reinterpret_cast<unsigned*>(p)[i] = r.w[i];
+        wr(reinterpret_cast<unsigned*>(p) + i, r.w[i]);
       else
-        reinterpret_cast<unsigned short*>(p)[i] = (unsigned short)(r.w[i / P::PER] >> (16 * (i % P::PER)));
+        wr(reinterpret_cast<unsigned short*>(p) + i, (unsigned short)(r.w[i / P::PER] >> (16 * (i % P::PER))));
     }
   }
 }
@@ -179,6 +211,10 @@ __device__ __forceinline__ void st_whole(T* p, const float (&v)[V]) {
 template <typename T, int V>
 __device__ __forceinline__ void fetch_whole(Pack<T, V>* slot, const T* src) {
   constexpr int BYTES = Pack<T, V>::BYTES;
+  if (!touch(src, BYTES, BYTES < 16 ? BYTES : 16, false)) {
+    slot->zero();
+    return;
+  }
   if constexpr (BYTES >= 4) {
 #pragma unroll
     for (int i = 0; i < BYTES; i += 16)
@@ -254,8 +290,8 @@ struct Seq {
 };
 __device__ __forceinline__ Seq seq_of(const int* lengths, const int* index, int b, int L, int slots, St st) {
   Seq q;
-  q.slot = index ? index[b] : b;
-  q.len = lengths ? lengths[b] : L;
+  q.slot = index ? rd(index + b) : b;
+  q.len = lengths ? rd(lengths + b) : L;
   const bool bad = q.len < 0 || q.len > L || (index && slots > 0 && q.slot >= slots);
   if (bad && st.w && threadIdx.x == 0) s4dev::st_flag(st, s4impl::ST_BAD_INDEX);
   if (bad || q.slot < 0) {
@@ -283,12 +319,12 @@ __device__ __forceinline__ void column_sums(const float* part, int rows, long lo
   if (c < cols) {
     int r = wid;
     for (; r + 24 < rows; r += 32) {
-      a0 += part[r * pitch + c];
-      a1 += part[(r + 8) * pitch + c];
-      a2 += part[(r + 16) * pitch + c];
-      a3 += part[(r + 24) * pitch + c];
+      a0 += rd(part + r * pitch + c);
+      a1 += rd(part + (r + 8) * pitch + c);
+      a2 += rd(part + (r + 16) * pitch + c);
+      a3 += rd(part + (r + 24) * pitch + c);
     }
-    for (; r < rows; r += 8) a0 += part[r * pitch + c];
+    for (; r < rows; r += 8) a0 += rd(part + r * pitch + c);
   }
   s[wid][lane] = (a0 + a1) + (a2 + a3);
   __syncthreads();

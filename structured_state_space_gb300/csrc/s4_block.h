@@ -24,6 +24,13 @@ inline bool dtype_ok(int dtype) { return dtype == S4_F32 || dtype == S4_BF16 || 
 // Device bytes of the workspace's status block, before its other sections.
 constexpr size_t kStatusBytes = 256;
 inline size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
+// Bytes between two sections of a workspace: none, but in the bounds-checked build, where an access
+// beyond a section's end is not to land in the next.
+#ifdef S4_BOUNDS_CHECK
+constexpr size_t kGap = 4096;
+#else
+constexpr size_t kGap = 0;
+#endif
 
 cudaError_t launch_short_conv(const s4_short_conv_args& a, St st, cudaStream_t s);
 size_t short_conv_bwd_scratch(int batch, int L, int H, int W);

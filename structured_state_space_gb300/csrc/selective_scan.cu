@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas)
     }
 #pragma unroll
     for (int k = 0; k < OWN; ++k) {
-      const int t = tb + token(k), n = t < live && S4_IN(t, a.L) ? ns : 0;
+      const int t = tb + token(k), n = t < live ? ns : 0;
       next[k * 32] = ld_pack<T, CPT>(x + t * a.x.row, n, vec);
       next[(OWN + k) * 32] = ld_pack<T, CPT>(dt + t * a.dt.row, n, vec);
       if (z) next[(2 * OWN + k) * 32] = ld_pack<T, CPT>(z + t * a.z.row, n, vec);
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas)
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       const int i = (k * 32 + wl) * VB, t = tb + i / NP;
-      const int n = t < live && S4_IN(t, a.L) ? a.N - i % NP : 0;
+      const int n = t < live ? a.N - i % NP : 0;
       nextv[k * 32] = ld_pack<T, VB>(B + t * a.B.row + i % NP, n, vecbc);
       if (MODE == 1) nextv[(NB + k) * 32] = ld_pack<T, VB>(C + t * a.C.row + i % NP, n, vecbc);
     }
@@ -133,8 +133,8 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas)
   for (int j = 0; j < CPT; ++j) {
     const int hs = h + j;
     const bool on = j < nh;
-    bias[j] = a.dt_bias && on ? a.dt_bias[hs] : 0.f;
-    skip[j] = MODE && a.D && on ? a.D[hs] : 0.f;
+    bias[j] = a.dt_bias && on ? rd(a.dt_bias + hs) : 0.f;
+    skip[j] = MODE && a.D && on ? rd(a.D + hs) : 0.f;
 #pragma unroll
     for (int i = 0; i < SPT; ++i) {
       const int n = n0 + i;
@@ -142,11 +142,11 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas)
       float v = 0.f;
       if (MODE == 1 && in && (t0 < q.len || chunk == 0)) {
         if (ck.count > 1)
-          v = ck.start[(((long long)b * ck.count + chunk) * a.H + hs) * a.N + n];
+          v = rd(ck.start + (((long long)b * ck.count + chunk) * a.H + hs) * a.N + n);
         else if (a.state && q.slot >= 0)
-          v = a.state[(q.slot * a.H + hs) * a.N + n];
+          v = rd(a.state + (q.slot * a.H + hs) * a.N + n);
       }
-      const float Av = in ? a.A[(long long)hs * a.N + n] * kLog2e : 0.f;
+      const float Av = in ? rd(a.A + (long long)hs * a.N + n) * kLog2e : 0.f;
       (i % 2 ? A[j][i / 2].y : A[j][i / 2].x) = Av;
       (i % 2 ? s[j][i / 2].y : s[j][i / 2].x) = v;
     }
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas)
           }
           if (WHOLE && whole) {
             if (LPC <= 4 || lane < 4) st_whole<T, CPT>(y + t * a.y.row, out);
-          } else if (t < live && ns > 0 && S4_IN(t, a.L)) {
+          } else if (t < live && ns > 0) {
             st_f<T, CPT>(y + t * a.y.row, ns, vec, out);
           }
         }
@@ -248,8 +248,7 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas)
   float* out = nullptr;
   if (MODE == 0)
     out = ck.start + ((long long)b * ck.count + chunk) * a.H * a.N;
-  else if (a.state_out && q.slot >= 0 && ((t0 < q.len && q.len <= t1) || (q.len == 0 && chunk == 0)) &&
-           S4_IN(q.slot, a.slots))
+  else if (a.state_out && q.slot >= 0 && ((t0 < q.len && q.len <= t1) || (q.len == 0 && chunk == 0)))
     out = a.state_out + q.slot * a.H * a.N;
   if (MODE == 0) {  // the tokens are spread over up to four lanes
 #pragma unroll
@@ -265,8 +264,8 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas)
       if (j >= nh) continue;
 #pragma unroll
       for (int i = 0; i < SPT; ++i)
-        if (n0 + i < a.N) out[(long long)hs * a.N + n0 + i] = i % 2 ? s[j][i / 2].y : s[j][i / 2].x;
-      if (MODE == 0 && lane == 0) ck.total[((long long)b * ck.count + chunk) * a.H + hs] = j ? sum.y : sum.x;
+        if (n0 + i < a.N) wr(out + (long long)hs * a.N + n0 + i, i % 2 ? s[j][i / 2].y : s[j][i / 2].x);
+      if (MODE == 0 && lane == 0) wr(ck.total + ((long long)b * ck.count + chunk) * a.H + hs, j ? sum.y : sum.x);
     }
   }
 }
@@ -278,22 +277,22 @@ __global__ void __launch_bounds__(128) selective_join_kernel(s4_selective_args a
   const Seq q = seq_of(a.lengths, a.index, b, a.L, a.slots, st);
   const long long i = (long long)blockIdx.x * 128 + threadIdx.x, HN = (long long)a.H * a.N;
   if (i >= HN) return;
-  const float A = a.A[i] * kLog2e;
+  const float A = rd(a.A + i) * kLog2e;
   float* p = ck.start + (long long)b * ck.count * HN + i;
   const float* tot = ck.total + (long long)b * ck.count * a.H + i / a.N;
   const int used = q.len ? (q.len + ck.len - 1) / ck.len : 1;  // chunks with real tokens
-  float s = a.state && q.slot >= 0 ? a.state[q.slot * HN + i] : 0.f;
+  float s = a.state && q.slot >= 0 ? rd(a.state + q.slot * HN + i) : 0.f;
   for (int c0 = 0; c0 < used; c0 += 8) {
     float end[8], d[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const bool more = c0 + k + 1 < used;
-      end[k] = more ? p[(c0 + k) * HN] : 0.f;
-      d[k] = more ? tot[(long long)(c0 + k) * a.H] : 0.f;
+      end[k] = more ? rd(p + (c0 + k) * HN) : 0.f;
+      d[k] = more ? rd(tot + (long long)(c0 + k) * a.H) : 0.f;
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      if (c0 + k < used) p[(c0 + k) * HN] = s;
+      if (c0 + k < used) wr(p + (c0 + k) * HN, s);
       s = fmaf(ex2(d[k] * A), s, end[k]);
     }
   }
@@ -313,29 +312,29 @@ __global__ void __launch_bounds__(kStepThreads) selective_step_kernel(s4_selecti
   const Seq q = seq_of(a.lengths, a.index, b, 1, a.slots, st);
   const int lane = threadIdx.x % LPC, h = c.h0 + threadIdx.x / LPC, n0 = lane * SPT, n = WHOLE ? SPT : a.N - n0;
   const bool in = WHOLE || h < c.hend, on = q.len > 0;  // `on`: the token advances the state
-  const bool put = in && (WHOLE || n > 0) && a.state_out && q.slot >= 0 && S4_IN(q.slot, a.slots);
+  const bool put = in && (WHOLE || n > 0) && a.state_out && q.slot >= 0;
   T* y = static_cast<T*>(a.y.p) + b * a.y.batch;
   if (WHOLE && !on && !put) {  // a row that is not in use
-    if (lane == 0) y[h] = from_f<T>(0.f);
+    if (lane == 0) wr(y + h, from_f<T>(0.f));
     return;
   }
   const long long at = (q.slot * a.H + h) * a.N + n0;
   Pack<float, SPT> ps, pA;
   Pack<T, SPT> pb, pc;
   ps.zero();
-  if (in && q.slot >= 0 && a.state && S4_IN(q.slot, a.slots))
+  if (in && q.slot >= 0 && a.state)
     ps = ld_pack<float, SPT>(a.state + at, n, WHOLE || vec);
   pA = ld_pack<float, SPT>(a.A + (long long)h * a.N + n0, in ? n : 0, WHOLE || vec);
   float xv = 0.f, d = 0.f, zv = 0.f;
-  if (in && on && S4_IN(h, a.H)) {
-    xv = to_f(static_cast<const T*>(a.x.p)[b * a.x.batch + h]);
-    d = to_f(static_cast<const T*>(a.dt.p)[b * a.dt.batch + h]);
-    if (a.z.p) zv = to_f(static_cast<const T*>(a.z.p)[b * a.z.batch + h]);
+  if (in && on) {
+    xv = to_f(rd(static_cast<const T*>(a.x.p) + b * a.x.batch + h));
+    d = to_f(rd(static_cast<const T*>(a.dt.p) + b * a.dt.batch + h));
+    if (a.z.p) zv = to_f(rd(static_cast<const T*>(a.z.p) + b * a.z.batch + h));
   }
   pb = ld_pack<T, SPT>(static_cast<const T*>(a.B.p) + b * a.B.batch + c.g * a.B_group + n0, on ? n : 0, WHOLE || vecbc);
   pc = ld_pack<T, SPT>(static_cast<const T*>(a.C.p) + b * a.C.batch + c.g * a.C_group + n0, on ? n : 0, WHOLE || vecbc);
-  if (a.dt_bias && in) d += a.dt_bias[h];
-  const float skip = a.D && in ? a.D[h] : 0.f;
+  if (a.dt_bias && in) d += rd(a.dt_bias + h);
+  const float skip = a.D && in ? rd(a.D + h) : 0.f;
 
   float2 s[SPT / 2], acc = make_float2(0.f, 0.f);
   to_pairs<float, SPT>(ps, s);
@@ -359,7 +358,7 @@ __global__ void __launch_bounds__(kStepThreads) selective_step_kernel(s4_selecti
   if (lane == 0 && in) {
     v = fmaf(skip, xv, v);
     if (a.z.p) v *= silu(zv);
-    y[h] = from_f<T>(on ? v : 0.f);
+    wr(y + h, from_f<T>(on ? v : 0.f));
   }
 }
 
@@ -390,9 +389,31 @@ auto with_states(int N, F f) {
   if (N <= 128) return f(Geo<16, 8>{});
   return f(Geo<32, 8>{});
 }
+#ifdef S4_BOUNDS_CHECK
+cudaError_t extents(const s4_selective_args& a, const Chunks& ck, int e, cudaStream_t s) {
+  s4impl::Extents x{};
+  for (const s4_rows* r : {&a.x, &a.dt, &a.z}) x.in_rows(*r, e, a.batch, a.L, a.H);
+  x.add(a.B.p, e, true, false, a.N, a.batch, a.B.batch, a.L, a.B.row, a.G, a.B_group);
+  x.add(a.C.p, e, true, false, a.N, a.batch, a.C.batch, a.L, a.C.row, a.G, a.C_group);
+  x.out_rows(a.y, e, a.batch, a.L, a.H);
+  x.in(a.A, 4, a.N, a.H);
+  for (const float* p : {a.D, a.dt_bias}) x.in(p, 4, a.H);
+  for (const int* p : {a.lengths, a.index}) x.in(p, 4, a.batch);
+  x.in(a.state, 4, a.N, (long long)a.slots * a.H);
+  x.out(a.state_out, 4, a.N, (long long)a.slots * a.H);
+  if (ck.count > 1) {
+    x.scratch(ck.start, 4, a.N, (long long)a.batch * ck.count * a.H);
+    x.scratch(ck.total, 4, a.H, (long long)a.batch * ck.count);
+  }
+  return set_extents(x, s);
+}
+#endif
 template <typename T>
 cudaError_t step_t(const s4_selective_args& a, St st, cudaStream_t s) {
   const int e = sizeof(T);
+#ifdef S4_BOUNDS_CHECK
+  if (const cudaError_t err = extents(a, Chunks{1, 1, nullptr, nullptr}, e, s); err != cudaSuccess) return err;
+#endif
   s4impl::TimedLaunch tl("selective_step", s);
   with_states(a.N, [&](auto geo) {
     using G = decltype(geo);
@@ -422,7 +443,10 @@ cudaError_t scan_t(const s4_selective_args& a, St st, cudaStream_t s) {
                        a.B_group * e % pb == 0 && a.C_group * e % pb == 0;
     Chunks ck = plan(a.batch, a.L, a.H, a.N, a.G, G::CH);
     ck.start = reinterpret_cast<float*>(static_cast<char*>(a.ws) + s4impl::kStatusBytes);
-    ck.total = ck.start + (long long)a.batch * ck.count * a.H * a.N;
+    ck.total = ck.start + (long long)a.batch * ck.count * a.H * a.N + s4impl::kGap / 4;
+#ifdef S4_BOUNDS_CHECK
+    if (extents(a, ck, e, s) != cudaSuccess) return;
+#endif
     const long long blocks = chan_blocks<G::CH>(a.H, a.G);
     const auto run = [&](auto whole) {
       constexpr bool W = decltype(whole)::value;
@@ -466,7 +490,7 @@ size_t selective_scratch(int batch, int L, int H, int N, int G) {
   if (L == 1) return 0;
   return with_states(N, [&](auto geo) -> size_t {
     const Chunks ck = plan(batch, L, H, N, G, decltype(geo)::CH);
-    return ck.count == 1 ? 0 : sizeof(float) * (size_t)batch * ck.count * H * (N + 1);
+    return ck.count == 1 ? 0 : sizeof(float) * (size_t)batch * ck.count * H * (N + 1) + s4impl::kGap;
   });
 }
 

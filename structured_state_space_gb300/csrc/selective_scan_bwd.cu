@@ -207,18 +207,18 @@ __global__ void __launch_bounds__(kThreads, 4) selective_ends_kernel(s4_selectiv
 #pragma unroll
     for (int k = 0; k < OWN; ++k) {
       const int t = tb + p.token(k);
-      next.load(k, a, x, dt, z, dy, t, t < live && S4_IN(t, a.L) ? p.ns : 0, vec);
+      next.load(k, a, x, dt, z, dy, t, t < live ? p.ns : 0, vec);
     }
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
-      const int i = (k * 32 + wl) * VB, t = tb + i / NP, n = t < live && S4_IN(t, a.L) ? a.N - i % NP : 0;
+      const int i = (k * 32 + wl) * VB, t = tb + i / NP, n = t < live ? a.N - i % NP : 0;
       nextv[k * 32] = ld_pack<T, VB>(B + t * a.B.row + i % NP, n, vecbc);
       nextv[(NB + k) * 32] = ld_pack<T, VB>(C + t * a.C.row + i % NP, n, vecbc);
     }
   };
   if (t0 < live) fetch(t0);  // before the reads below, which take as long
   float2 A[CPT][SPT / 2], s[CPT][SPT / 2], P[CPT][SPT / 2], R[CPT][SPT / 2], sum = make_float2(0.f, 0.f);
-  const float2 bias = make_float2(a.dt_bias && nh > 0 ? a.dt_bias[h] : 0.f, a.dt_bias && nh > 1 ? a.dt_bias[h + 1] : 0.f);
+  const float2 bias = make_float2(a.dt_bias && nh > 0 ? rd(a.dt_bias + h) : 0.f, a.dt_bias && nh > 1 ? rd(a.dt_bias + h + 1) : 0.f);
 #pragma unroll
   for (int j = 0; j < CPT; ++j) {
     const int n = j < nh ? nn : 0;
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 4) selective_ends_kernel(s4_selectiv
       for (int j = 0; j < CPT; ++j) {
         if (j >= nh) continue;
         st_states<SPT>(w.s_tile + (row + j) * a.N + n0, nn, vecn, s[j]);
-        if (lane == 0) w.d_before[row + j] = j ? all.y : all.x;
+        if (lane == 0) wr(w.d_before + row + j, j ? all.y : all.x);
       }
       if (tb >= live) continue;
     }
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 4) selective_ends_kernel(s4_selectiv
     if (j >= nh) continue;
     st_states<SPT>(w.s_seg + (row + j) * a.N + n0, nn, vecn, s[j]);
     st_states<SPT>(w.g_seg + (row + j) * a.N + n0, nn, vecn, R[j]);
-    if (lane == 0) w.d_seg[row + j] = j ? sum.y : sum.x;
+    if (lane == 0) wr(w.d_seg + row + j, j ? sum.y : sum.x);
   }
 }
 
@@ -325,28 +325,28 @@ __global__ void __launch_bounds__(128) selective_joins_kernel(s4_selective_bwd_a
   const int b = blockIdx.y;
   const long long i = (long long)blockIdx.x * 128 + threadIdx.x, HN = (long long)a.H * a.N;
   if (i >= HN) return;
-  const float A = a.A[i] * kLog2e;
+  const float A = rd(a.A + i) * kLog2e;
   float* sp = w.s_seg + (long long)b * w.segs * HN + i;
   float* gp = w.g_seg + (long long)b * w.segs * HN + i;
   const float* dp = w.d_seg + (long long)b * w.segs * a.H + i / a.N;
-  float s = 0.f, g = a.dstate ? a.dstate[(long long)b * HN + i] : 0.f;
+  float s = 0.f, g = a.dstate ? rd(a.dstate + (long long)b * HN + i) : 0.f;
   for (int k0 = 0; k0 < w.segs; k0 += 8) {
     float sv[8], gv[8], ds[8], dg[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int k = k0 + e, r = w.segs - 1 - k;
       const bool in = k < w.segs;
-      sv[e] = in ? sp[k * HN] : 0.f;
-      gv[e] = in ? gp[r * HN] : 0.f;
-      ds[e] = in ? dp[(long long)k * a.H] : 0.f;
-      dg[e] = in ? dp[(long long)r * a.H] : 0.f;
+      sv[e] = in ? rd(sp + k * HN) : 0.f;
+      gv[e] = in ? rd(gp + r * HN) : 0.f;
+      ds[e] = in ? rd(dp + (long long)k * a.H) : 0.f;
+      dg[e] = in ? rd(dp + (long long)r * a.H) : 0.f;
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int k = k0 + e, r = w.segs - 1 - k;
       if (k >= w.segs) break;
-      sp[k * HN] = s;
-      gp[r * HN] = g;
+      wr(sp + k * HN, s);
+      wr(gp + r * HN, g);
       s = fmaf(ex2(ds[e] * A), s, sv[e]);
       g = fmaf(ex2(dg[e] * A), g, gv[e]);
     }
@@ -468,12 +468,12 @@ __global__ void __launch_bounds__(kThreads, 4) selective_tiles_kernel(s4_selecti
 #pragma unroll
     for (int k = 0; k < OWN; ++k) {
       const int t = p.token(k);
-      next.load(k, a, x, dt, z, dy, tb + t, t < live && S4_IN(tb + t, a.L) ? p.ns : 0, vec);
+      next.load(k, a, x, dt, z, dy, tb + t, t < live ? p.ns : 0, vec);
     }
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       const int i = (k * kThreads + threadIdx.x) * VB, t = i / NP;
-      const int n = i < TC * NP && t < live && S4_IN(tb + t, a.L) ? a.N - i % NP : 0;
+      const int n = i < TC * NP && t < live ? a.N - i % NP : 0;
       nextv[k * kThreads] = ld_pack<T, VB>(B + (long long)(tb + t) * a.B.row + i % NP, n, vecbc);
       nextv[(NB + k) * kThreads] = ld_pack<T, VB>(C + (long long)(tb + t) * a.C.row + i % NP, n, vecbc);
     }
@@ -489,8 +489,8 @@ __global__ void __launch_bounds__(kThreads, 4) selective_tiles_kernel(s4_selecti
   fetch(last - 1);  // before the reads below, which take as long
   float2 A[CPT][SPT / 2], g[CPT][SPT / 2], dA[CPT][SPT / 2];
   float2 dD = make_float2(0.f, 0.f), db = dD;
-  const float2 bias = make_float2(a.dt_bias && nh > 0 ? a.dt_bias[h] : 0.f, a.dt_bias && nh > 1 ? a.dt_bias[h + 1] : 0.f);
-  const float2 Dv = make_float2(a.D && nh > 0 ? a.D[h] : 0.f, a.D && nh > 1 ? a.D[h + 1] : 0.f);
+  const float2 bias = make_float2(a.dt_bias && nh > 0 ? rd(a.dt_bias + h) : 0.f, a.dt_bias && nh > 1 ? rd(a.dt_bias + h + 1) : 0.f);
+  const float2 Dv = make_float2(a.D && nh > 0 ? rd(a.D + h) : 0.f, a.D && nh > 1 ? rd(a.D + h + 1) : 0.f);
   const long long srow = ((long long)b * w.segs + seg) * a.H + h;
 #pragma unroll
   for (int j = 0; j < CPT; ++j) {
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 4) selective_tiles_kernel(s4_selecti
         st_f<T, 2>(dto + t * a.ddt.row, p.ns, vec, zero);
         if (dzo) st_f<T, 2>(dzo + t * a.dz.row, p.ns, vec, zero);
       }
-      for (int i = threadIdx.x; i < min(TC, a.L - tb) * 2 * NP; i += kThreads) bc[i] = 0.f;
+      for (int i = threadIdx.x; i < min(TC, a.L - tb) * 2 * NP; i += kThreads) wr(bc + i, 0.f);
       if (tile > first) fetch(tile - 1);
       continue;
     }
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 4) selective_tiles_kernel(s4_selecti
         if (seg > 0) {
           float2 e[SPT / 2];
           ld_states<SPT>(e, w.s_seg + (srow + j) * a.N + n0, n, vecn);
-          const float before = j < nh ? w.d_before[row + j] : 0.f;
+          const float before = j < nh ? rd(w.d_before + row + j) : 0.f;
 #pragma unroll
           for (int i = 0; i < SPT / 2; ++i)
             s[j][i] = fma2(ex2(mul2(make_float2(before, before), A[j][i])), e[i], s[j][i]);
@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 4) selective_tiles_kernel(s4_selecti
             st_whole<T, 2>(dto + tt * a.ddt.row, o2);
             if (dzo) st_whole<T, 2>(dzo + tt * a.dz.row, o3);
           }
-        } else if (tt < a.L && p.ns > 0 && S4_IN(tt, a.L)) {
+        } else if (tt < a.L && p.ns > 0) {
           st_f<T, 2>(dxo + tt * a.dx.row, p.ns, vec, o1);
           st_f<T, 2>(dto + tt * a.ddt.row, p.ns, vec, o2);
           if (dzo) st_f<T, 2>(dzo + tt * a.dz.row, p.ns, vec, o3);
@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 4) selective_tiles_kernel(s4_selecti
 #pragma unroll
         for (int e = 0; e < G::WARPS; ++e) v += red[e][u][n];
         const int t = k * TB + u;
-        if (tb + t < a.L && S4_IN(tb + t, a.L)) bc[t * 2 * NP + n] = t < live ? v : 0.f;
+        if (tb + t < a.L) wr(bc + t * 2 * NP + n, t < live ? v : 0.f);
       }
     }
   }
@@ -769,8 +769,8 @@ __global__ void __launch_bounds__(kThreads, 4) selective_tiles_kernel(s4_selecti
     st_states<SPT>(ph + (long long)(h + j) * a.N + n0, nn, vecn, dA[j]);
     if (seg == 0 && a.dstate0) st_states<SPT>(a.dstate0 + ((long long)b * a.H + h + j) * a.N + n0, nn, vecn, g[j]);
     if (lane == 0) {
-      ph[(long long)a.H * a.N + h + j] = j ? dD.y : dD.x;
-      ph[(long long)a.H * (a.N + 1) + h + j] = j ? db.y : db.x;
+      wr(ph + (long long)a.H * a.N + h + j, j ? dD.y : dD.x);
+      wr(ph + (long long)a.H * (a.N + 1) + h + j, j ? db.y : db.x);
     }
   }
 }
@@ -783,11 +783,11 @@ __global__ void __launch_bounds__(256) selective_sums_kernel(s4_selective_bwd_ar
   if (blockIdx.x < param_ctas) {
     column_sums(w.part_h, a.batch * w.segs, cols, w.pitch_h, [=](long long c, float v) {
       if (c < HN)
-        a.dA[c] = v;
+        wr(a.dA + c, v);
       else if (c < HN + a.H) {
-        if (a.dD) a.dD[c - HN] = v;
+        if (a.dD) wr(a.dD + c - HN, v);
       } else if (a.ddt_bias) {
-        a.ddt_bias[c - HN - a.H] = v;
+        wr(a.ddt_bias + c - HN - a.H, v);
       }
     });
     return;
@@ -800,10 +800,10 @@ __global__ void __launch_bounds__(256) selective_sums_kernel(s4_selective_bwd_ar
   const float* p = w.part_bc + ((long long)g * per * rows + row) * 2 * NP + n;
   float v = 0.f;
 #pragma unroll 4
-  for (int k = 0; k < per; ++k) v += p[(long long)k * rows * 2 * NP];
+  for (int k = 0; k < per; ++k) v += rd(p + (long long)k * rows * 2 * NP);
   if (state >= a.N) return;
   T* out = static_cast<T*>(n < NP ? a.dB : a.dC);
-  out[(row * a.G + g) * a.N + state] = from_f<T>(v);
+  wr(out + (row * a.G + g) * a.N + state, from_f<T>(v));
 }
 
 // The lanes that hold N states: 4 each in (3), 8 each in (1).
@@ -838,7 +838,7 @@ Work layout(int batch, int L, int H, int N, int Gr, char* ws, size_t* total) {
   size_t at = s4impl::kStatusBytes;
   auto take = [&](size_t n) {
     float* p = reinterpret_cast<float*>(ws + at);
-    at += s4impl::align256(4 * n);
+    at += s4impl::align256(4 * n) + s4impl::kGap;
     return p;
   };
   w.s_tile = take(bt * HN);
@@ -853,6 +853,32 @@ Work layout(int batch, int L, int H, int N, int Gr, char* ws, size_t* total) {
   if (total) *total = (long long)chan_blocks<2>(H, Gr) * w.segs > INT_MAX ? 0 : at;
   return w;
 }
+
+#ifdef S4_BOUNDS_CHECK
+cudaError_t extents(const s4_selective_bwd_args& a, const Work& w, int NP, int e, cudaStream_t s) {
+  s4impl::Extents x{};
+  const long long b = a.batch, H = a.H, N = a.N;
+  for (const s4_rows* r : {&a.x, &a.dt, &a.z, &a.dy}) x.in_rows(*r, e, a.batch, a.L, H);
+  x.add(a.B.p, e, true, false, N, b, a.B.batch, a.L, a.B.row, a.G, a.B_group);
+  x.add(a.C.p, e, true, false, N, b, a.C.batch, a.L, a.C.row, a.G, a.C_group);
+  for (const s4_rows_out* r : {&a.dx, &a.ddt, &a.dz}) x.out_rows(*r, e, a.batch, a.L, H);
+  for (const void* p : {a.dB, a.dC}) x.out(p, e, N, b * a.L * a.G);
+  x.in(a.A, 4, N, H);
+  for (const float* p : {a.D, a.dt_bias}) x.in(p, 4, H);
+  x.in(a.lengths, 4, b);
+  for (const float* p : {a.state0, a.dstate}) x.in(p, 4, N, b * H);
+  x.out(a.dstate0, 4, N, b * H);
+  x.out(a.dA, 4, N, H);
+  for (const float* p : {a.dD, a.ddt_bias}) x.out(p, 4, H);
+  x.scratch(w.s_tile, 4, N, b * w.tiles * H);
+  x.scratch(w.d_before, 4, H, b * w.tiles);
+  for (const float* p : {w.s_seg, w.g_seg}) x.scratch(p, 4, N, b * w.segs * H);
+  x.scratch(w.d_seg, 4, H, b * w.segs);
+  x.add(w.part_h, 4, true, true, H * (N + 2), b * w.segs, w.pitch_h);
+  x.scratch(w.part_bc, 4, 2 * NP, (long long)w.blocks * b * a.L);
+  return set_extents(x, s);
+}
+#endif
 
 template <typename T>
 cudaError_t bwd_t(const s4_selective_bwd_args& a, St st, cudaStream_t s) {
@@ -869,6 +895,9 @@ cudaError_t bwd_t(const s4_selective_bwd_args& a, St st, cudaStream_t s) {
     const bool vecn = a.N % 4 == 0 && vec_ok(a.A, 4, 16) && vec_ok(a.state0, 4, 16) && vec_ok(a.dstate, 4, 16) &&
                       vec_ok(a.dstate0, 4, 16);
     const Work w = layout<G>(a.batch, a.L, a.H, a.N, a.G, static_cast<char*>(a.ws), nullptr);
+#ifdef S4_BOUNDS_CHECK
+    if (extents(a, w, G::NP, e, s) != cudaSuccess) return;
+#endif
     const auto run = [&](auto whole) {
       constexpr bool W = decltype(whole)::value;
       constexpr auto ends = selective_ends_kernel<T, E, W>;

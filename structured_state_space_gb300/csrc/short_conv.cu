@@ -47,17 +47,17 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(s4_short_conv_args
     }
 #pragma unroll
     for (int u = 0; u < KW; ++u)
-      in[u] = ld_pack<T, V>(x + (t + u) * a.x.row, t + u < live && S4_IN(t + u, a.L) ? n : 0, vec);
+      in[u] = ld_pack<T, V>(x + (t + u) * a.x.row, t + u < live ? n : 0, vec);
   };
   if (t0 < live) fetch(t0);
   float2 w[KW][V / 2], bias[V / 2], win[KW][V / 2];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const bool on = i < n && S4_IN(h + i, a.H);
-    (i % 2 ? bias[i / 2].y : bias[i / 2].x) = a.bias && on ? a.bias[h + i] : 0.f;
+    const bool on = i < n;
+    (i % 2 ? bias[i / 2].y : bias[i / 2].x) = a.bias && on ? rd(a.bias + h + i) : 0.f;
 #pragma unroll
     for (int k = 0; k < KW; ++k)
-      (i % 2 ? w[k][i / 2].y : w[k][i / 2].x) = on ? a.w[(long long)(h + i) * KW + k] : 0.f;
+      (i % 2 ? w[k][i / 2].y : w[k][i / 2].x) = on ? rd(a.w + (long long)(h + i) * KW + k) : 0.f;
   }
   // the inputs before the segment: of the sequence, of the state, or zeros
 #pragma unroll
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(s4_short_conv_args
         for (int k = 0; k < KW; ++k) v = fma2(w[k][i], win[(k + u) % KW][i], v);
         out[i] = a.silu ? silu(v) : v;
       }
-      if (S4_IN(t + u, a.L)) st_pairs<T, V>(y + (t + u) * a.y.row, n, vec, out);
+      st_pairs<T, V>(y + (t + u) * a.y.row, n, vec, out);
     }
   }
   for (int t = max(t0, live); t < t1; ++t) {  // padding
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(s4_short_conv_args
         r = a.L == 1 ? in[0] : ld_pack<T, V>(x + t * a.x.row, n, vec);
       else if (state)
         r = ld_pack<T, V>(state + (t + a.W - 1) * srow, n, vec);
-      if (S4_IN(q.slot, a.slots)) st_pack<T, V>(so + j * srow, n, vec, r);
+      st_pack<T, V>(so + j * srow, n, vec, r);
     }
   }
 }
@@ -165,10 +165,10 @@ __global__ void __launch_bounds__(32 * kWarpsBwd, KW <= 4 ? 2 : 1)
     float2 w[KW][V / 2], bias[V / 2], win[KW][V / 2], dv[KW][V / 2];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      (i % 2 ? bias[i / 2].y : bias[i / 2].x) = a.bias && i < n ? a.bias[h + i] : 0.f;
+      (i % 2 ? bias[i / 2].y : bias[i / 2].x) = a.bias && i < n ? rd(a.bias + h + i) : 0.f;
 #pragma unroll
       for (int k = 0; k < KW; ++k)
-        (i % 2 ? w[k][i / 2].y : w[k][i / 2].x) = i < n ? a.w[(long long)(h + i) * KW + k] : 0.f;
+        (i % 2 ? w[k][i / 2].y : w[k][i / 2].x) = i < n ? rd(a.w + (long long)(h + i) * KW + k) : 0.f;
     }
 #pragma unroll
     for (int k = 0; k < KW; ++k) {
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(32 * kWarpsBwd, KW <= 4 ? 2 : 1)
 #pragma unroll
       for (int u = 0; u < KW; ++u) {
         const int t = t0 + g * KW + u;
-        if (t >= tend || !S4_IN(t, a.L)) continue;
+        if (t >= tend) continue;
         if (whole) {
           fetch_whole<T, V>(&slot(g, 0, u), x + t * a.x.row);
           fetch_whole<T, V>(&slot(g, 1, u), dy + t * a.dy.row);
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(32 * kWarpsBwd, KW <= 4 ? 2 : 1)
         }
         if (before)
           st_pairs<T, V>(dst0 + (tx + a.W - 1) * (long long)a.H, n, vec, g);
-        else if (S4_IN(tx, a.L))
+        else
           st_pairs<T, V>(dx + tx * a.dx.row, n, vec, g);
       }
     }
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(32 * kWarpsBwd, KW <= 4 ? 2 : 1)
     float t = 0.f;
 #pragma unroll
     for (int v = 0; v < kWarpsBwd; ++v) t += red[v][k * V + hl % V][hl / V];
-    out[(long long)k * a.H + hh] = t;
+    wr(out + (long long)k * a.H + hh, t);
   }
 }
 
@@ -315,9 +315,9 @@ __global__ void __launch_bounds__(256) short_conv_sums_kernel(const float* part,
   column_sums(part, rows, (long long)(W + 1) * H, (long long)(W + 1) * H, [=](long long c, float v) {
     const long long k = c / H, h = c % H;
     if (k < W)
-      dw[h * W + k] = v;
+      wr(dw + h * W + k, v);
     else if (dbias)
-      dbias[h] = v;
+      wr(dbias + h, v);
   });
 }
 
@@ -342,6 +342,18 @@ cudaError_t fwd_t(const s4_short_conv_args& a, St st, cudaStream_t s) {
                    vec_ok(a.state, e, bytes, a.H) && vec_ok(a.state_out, e, bytes, a.H);
   const long long n = (long long)((a.H + V - 1) / V) * ((a.L + kSegFwd - 1) / kSegFwd);
   const dim3 grid((unsigned)((n + kThreads - 1) / kThreads), a.batch);
+#ifdef S4_BOUNDS_CHECK
+  s4impl::Extents x{};
+  x.in_rows(a.x, e, a.batch, a.L, a.H);
+  x.out_rows(a.y, e, a.batch, a.L, a.H);
+  x.in(a.w, 4, a.W, a.H);
+  x.in(a.bias, 4, a.H);
+  x.in(a.lengths, 4, a.batch);
+  x.in(a.index, 4, a.batch);
+  x.in(a.state, e, a.H, (long long)a.slots * (a.W - 1));
+  x.out(a.state_out, e, a.H, (long long)a.slots * (a.W - 1));
+  if (const cudaError_t err = set_extents(x, s); err != cudaSuccess) return err;
+#endif
   s4impl::TimedLaunch tl("short_conv", s);
   with_taps(a.W, [&](auto taps) { short_conv_kernel<T, decltype(taps)::value, V><<<grid, kThreads, 0, s>>>(a, vec, st); });
   return cudaGetLastError();
@@ -360,6 +372,21 @@ cudaError_t bwd_t(const s4_short_conv_bwd_args& a, St st, cudaStream_t s) {
                    vec_ok(a.dstate, e, bytes, a.H) && vec_ok(a.dstate0, e, bytes, a.H);
   float* part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + s4impl::kStatusBytes);
   const dim3 grid = bwd_grid(a.batch, a.L, a.H);
+#ifdef S4_BOUNDS_CHECK
+  s4impl::Extents x{};
+  x.in_rows(a.x, e, a.batch, a.L, a.H);
+  x.in_rows(a.dy, e, a.batch, a.L, a.H);
+  x.out_rows(a.dx, e, a.batch, a.L, a.H);
+  x.in(a.w, 4, a.W, a.H);
+  x.in(a.bias, 4, a.H);
+  x.in(a.lengths, 4, a.batch);
+  for (const void* p : {a.state0, a.dstate}) x.in(p, e, a.H, (long long)a.batch * (a.W - 1));
+  x.out(a.dstate0, e, a.H, (long long)a.batch * (a.W - 1));
+  x.out(a.dw, 4, a.W, a.H);
+  x.out(a.dbias, 4, a.H);
+  x.scratch(part, 4, a.H, (long long)grid.y * grid.z * (a.W + 1));
+  if (const cudaError_t err = set_extents(x, s); err != cudaSuccess) return err;
+#endif
   {
     s4impl::TimedLaunch tl("short_conv_bwd", s);
     with_taps(a.W, [&](auto taps) {
