@@ -15,7 +15,7 @@ Entry points (same names as the C ABI):
     s4_recurrent_fwd(Lambda, P, Q, B, C, dt, D, u, x)  -> (y, x)   (recurrent mode)
     s4_workspace_bytes(H, N, r, L, batch)
     s4_get_status(ws), s4_status_str(code)
-and the selective block's operators (block.py, imported on first use):
+and the selective block's operators (block.py, loaded at the first call):
     s4_short_conv_fwd / _step / _bwd                   short causal convolution with SiLU
     s4_selective_scan_fwd / _bwd, s4_selective_step    selective state-space scan, prompts and single tokens
     s4_block_norm_fwd / _bwd                           norms around a block, gate, residual scale and sum
@@ -61,19 +61,27 @@ class S4Error(RuntimeError):
         super().__init__(f"{where}: {self.name} ({s4_status_str(self.code)})")
 
 
-# The selective block's operators, defined in block.py (which needs torch, loaded on first use).
+# The selective block's operators, defined in block.py, which needs torch and is loaded at the first call of one
+# of them; they then take the places of these.
 _BLOCK = ["s4_short_conv_fwd", "s4_short_conv_step", "s4_short_conv_bwd", "s4_selective_scan_fwd", "s4_selective_step",
           "s4_selective_scan_bwd", "s4_block_norm_fwd", "s4_block_norm_bwd"]
 __all__ += _BLOCK
 
 
-def __getattr__(name):
-    if name in _BLOCK:
-        from . import block
-        for n in _BLOCK:
-            globals()[n] = getattr(block, n)
-        return globals()[name]
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+def _at_first_call(name):
+    def operator(*args, **kw):
+        if globals()[name] is operator:
+            from . import block
+            globals().update((n, getattr(block, n)) for n in _BLOCK)
+        return globals()[name](*args, **kw)
+    operator.__name__ = operator.__qualname__ = name
+    operator.__doc__ = f"See block.{name}."
+    return operator
+
+
+for _name in _BLOCK:
+    globals()[_name] = _at_first_call(_name)
+del _name
 
 
 _lib = None
