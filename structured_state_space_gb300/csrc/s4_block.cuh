@@ -272,10 +272,6 @@ __device__ __forceinline__ float2 silu_grad(float2 v) {
   const float2 s = sigmoid(v), q = mul2(v, s);
   return fma2(q, fma2(s, make_float2(-1.f, -1.f), make_float2(1.f, 1.f)), s);
 }
-__device__ __forceinline__ float silu_grad(float v) {
-  const float s = sigmoid(v);
-  return fmaf(v * s, 1.f - s, s);
-}
 
 // The status block is optional in these calls (a null one records nothing).
 __device__ __forceinline__ void record_gen(St st) {

@@ -16,9 +16,7 @@ constexpr unsigned ST_BAD_INDEX = 64u;
 // The status of a call on `s` (defined in s4_api.cu).
 bool call_status(void* ws, cudaStream_t s, St* st, bool* chain);
 
-// Channels that one access of 16 bytes covers, per type.
 inline int dtype_bytes(int dtype) { return dtype == S4_F32 ? 4 : 2; }
-inline int dtype_vec(int dtype) { return 16 / dtype_bytes(dtype); }
 inline bool dtype_ok(int dtype) { return dtype == S4_F32 || dtype == S4_BF16 || dtype == S4_F16; }
 
 // Device bytes of the workspace's status block, before its other sections.

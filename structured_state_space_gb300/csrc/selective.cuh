@@ -66,15 +66,6 @@ __device__ __forceinline__ Chan chan_of(int block, int Hg) {
   return c;
 }
 
-// [TT][NP] of B or C in fp32, tokens from t0 (those from `len` on, and padded states, as zeros).
-template <typename T, int TT, int NP>
-__device__ __forceinline__ void stage_vectors(float* s, const T* p, long long row, int t0, int len, int N) {
-  for (int i = threadIdx.x; i < TT * NP; i += kThreads) {
-    const int t = i / NP, n = i % NP;
-    s[i] = t0 + t < len && n < N ? to_f(p[(t0 + t) * row + n]) : 0.f;
-  }
-}
-
 // Four tokens' values v[0..3] of a channel, summed over its LPC lanes.  With LPC >= 4 the lane
 // comes to hold the sum of token (lane & 3), after 3 exchanges rather than 8; with fewer lanes
 // each holds 4 / LPC tokens (v[0] .. for tokens own, own + LPC ...).
