@@ -401,7 +401,8 @@ s4_status s4_selective_scan_bwd(const s4_selective_bwd_args* a, void* stream);
  *     h_out = h + scale p,  y = h_out rsqrt(mean h_out^2 + eps) w_pre
  * where gate, w_post (then p = v), scale (1), h (0) and w_pre (then no y) may each be
  * absent.  h and h_out are fp32 (res_f32 = 1) or of the activations' type; y is
- * formed from h_out before its rounding.  h_out may be h.  1 <= H <= 16384.
+ * formed from h_out before its rounding.  h_out may be h (with the same row stride).
+ * 1 <= H <= 16384.
  */
 typedef struct {
     const void *o, *gate, *h;       /* [rows][H], row strides below in elements */

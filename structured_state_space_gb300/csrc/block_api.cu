@@ -141,6 +141,8 @@ s4_status s4_block_norm_fwd(const s4_block_norm_args* a, void* stream) {
       !aligned(a->h_out, er) || !aligned(a->y, e) || !aligned(a->w_post, 4) || !aligned(a->scale, 4) ||
       !aligned(a->w_pre, 4) || a->o_row < 0 || a->gate_row < 0 || a->h_row < 0 || a->h_out_row < 0 || a->y_row < 0)
     return S4_ERR_INVALID_ARG;
+  // in place: each row at its own address (else a row would replace another that is still needed)
+  if (a->h_out == a->h && a->rows > 1 && a->h_out_row != a->h_row) return S4_ERR_INVALID_ARG;
   return cuda_status(s4impl::launch_block_norm(*a, static_cast<cudaStream_t>(stream)));
 }
 
