@@ -8,8 +8,9 @@
 // registers of one warp or one CTA from its read to its results, so every array is
 // passed over once; both sums of squares are reductions over the group.
 //
-// Measured: forward 100 us on 16001 rows of 2560 channels in float16 (5.7 TB/s), backward 132 us on 16384
-// rows of 2048 in bfloat16 (5.6 TB/s); the residual in fp32.
+// Measured: forward 100 us on 16001 rows of 2560 channels in float16 (5.7 TB/s), 135 in fp32 (6.1); backward 132
+// us on 16384 rows of 2048 in bfloat16 (5.6 TB/s), 191 in fp32 (5.6); the residual in fp32.  The gradients
+// of more than 8192 channels (4 packs of 8 a thread, 8 of 4 in fp32) spill 860 to 970 bytes of registers a thread.
 #include "s4_block.cuh"
 
 namespace {

@@ -17,8 +17,9 @@
 // and the gradients.  Channels and tokens are summed in a fixed order: over a thread's channels,
 // its warp, its CTA, then as partial sums, which (4) adds up.  With one segment there is no (2).
 //
-// Measured: 899 us on 4 sequences of 4096 tokens, 2048 channels and 16 states in bfloat16: (1) 200, (2) 20,
-// (3) 650, (4) 28.
+// Measured: 897 us on 4 sequences of 4096 tokens, 2048 channels and 16 states in bfloat16: (1) 200, (2) 20,
+// (3) 650, (4) 28.  The instances spill some registers: (3) 20 bytes of stores a thread with 16 states in 16 bits,
+// up to 48 with other numbers, and 590 to 720 with more than 128 states.
 #include <limits.h>
 
 #include "selective.cuh"
@@ -918,7 +919,10 @@ cudaError_t bwd_t(const s4_selective_bwd_args& a, St st, cudaStream_t s) {
       s4impl::TimedLaunch tl("selective_bwd", s);
       tiles<<<dim3((unsigned)(w.blocks * w.segs), a.batch), kThreads, G::template kBytes<T>(), s>>>(a, w, vec, vecbc, vecn, st);
     };
-    // the tiles of other widths cost a condition per access
+    // Whole tiles spare a condition per access and overlap the next tile's copies: 4 sequences of 2048 tokens and 1024
+    // channels (bfloat16) take 266, 302 and 548 us instead of 485, 486 and 793 with 8, 16 and 32 states.  They are
+    // compiled for these numbers only; with 64, 128 and 256 states the same takes 1.71, 4.85 and 15.9 ms and
+    // would take 1.26, 3.61 and 11.1.
     bool whole = false;
     if constexpr (G::LPC <= 8 && (int)G::NP == (int)E::NP) {
       whole = vec && vecbc && a.N == G::NP && (a.H / a.G) % G::HB == 0;
