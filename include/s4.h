@@ -435,6 +435,173 @@ typedef struct {
 size_t s4_block_norm_bwd_workspace_bytes(long long rows, int H);
 s4_status s4_block_norm_bwd(const s4_block_norm_bwd_args* a, void* stream);
 
+/* ======================================================================
+ * Linear attention with a decay for each head, rotary positions, layer norm and
+ * the loss over a vocabulary: what a model needs around a mixer whose state is a
+ * matrix per head, with backward passes, for prompts and for single tokens.
+ *
+ * Conventions as for the selective block, and
+ *  - Arrays of heads are [batch][L][heads][width], given as s4_heads: the address of
+ *    element (0, 0, 0, 0) and the strides of the batch, the tokens and the heads
+ *    in elements; a head's channels are contiguous.  A slice of a projection's
+ *    output is passed as it lies.
+ *  - Sums, states, norms and the statistics of the softmax are fp32, outputs are
+ *    rounded once.  Products run on the tensor cores with operands of 16 bits: bfloat16
+ *    inputs as they are; float16 and fp32 inputs, and what must not lose
+ *    digits on the way (the keys that enter an fp32 state), as sums of two or three
+ *    bfloat16 terms.  With bfloat16 inputs the weights between the two products of a
+ *    pass, and the state where it is multiplied, are rounded to bfloat16 on the way.
+ * ====================================================================== */
+typedef struct {
+    const void* p;
+    long long batch, row, head;
+} s4_heads;
+typedef struct {
+    void* p;
+    long long batch, row, head;
+} s4_heads_out;
+
+/*
+ * s4_linear_attention_fwd -- per sequence and head h, with the state S [K][V] (fp32) and
+ * key and value of the head's group h / (H / G):
+ *     S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,    o_t = scale S_t^T q_t.
+ * L = 1 is the single-token form.  Stable for log_decay <= 0 (not checked); -infinity
+ * leaves each token with itself.  1 <= K, V <= 256, 1 <= H <= 4096, G divides H.
+ */
+typedef struct {
+    s4_heads q;               /* [batch][L][H][K] */
+    s4_heads k;               /* [batch][L][G][K] */
+    s4_heads v;               /* [batch][L][G][V] */
+    s4_heads_out o;           /* [batch][L][H][V] */
+    const float* log_decay;   /* [H] */
+    const int *lengths, *index;
+    const float* state;       /* [slots][H][K][V] or NULL */
+    float* state_out;
+    void* ws;                 /* s4_linear_attention_workspace_bytes */
+    size_t ws_bytes;
+    float scale;
+    int batch, L, H, G, K, V, slots, dtype;
+} s4_linear_attention_args;
+s4_status s4_linear_attention_fwd(const s4_linear_attention_args* a, void* stream);
+
+/* Bytes of scratch of s4_linear_attention_fwd; 0 if the sizes are out of range.  Where it
+ * is 256 (the status block alone; always for L = 1) ws may be NULL. */
+size_t s4_linear_attention_workspace_bytes(int batch, int L, int H, int G, int K, int V);
+
+/*
+ * s4_linear_attention_bwd -- gradients of s4_linear_attention_fwd from dout (the gradient of o):
+ * with w_ij = scale exp(log_decay (i - j)), R_t = scale q_t dout_t^T + exp(log_decay) R_{t+1},
+ *     dq_i = sum_{j<=i} w_ij (dout_i . v_j) k_j          (and the state on entry's part)
+ *     dk_j = sum_{i>=j} w_ij (v_j . dout_i) q_i = R_j v_j,    dv_j = R_j^T k_j
+ * (dk, dv summed over a group's heads).  The decay is a constant of the head and has no
+ * gradient.  state0, dstate, dstate0 [batch][H][K][V] fp32 as for s4_selective_scan_bwd.
+ */
+typedef struct {
+    s4_heads q, k, v, dout;
+    s4_heads_out dq, dk, dv;
+    const float* log_decay;
+    const int* lengths;
+    const float *state0, *dstate;
+    float* dstate0;           /* not the array dstate */
+    void* ws;                 /* s4_linear_attention_bwd_workspace_bytes */
+    size_t ws_bytes;
+    float scale;              /* not 0 */
+    int batch, L, H, G, K, V, dtype;
+} s4_linear_attention_bwd_args;
+size_t s4_linear_attention_bwd_workspace_bytes(int batch, int L, int H, int G, int K, int V);
+s4_status s4_linear_attention_bwd(const s4_linear_attention_bwd_args* a, void* stream);
+
+/*
+ * s4_rotary -- turns the first 2 R channels of each head by its token's position: pair i, which is
+ * (x[i], x[R + i]), or (x[2i], x[2i + 1]) with pairs = 1, as a complex number times
+ * amplitude exp(+-1i position freqs[i]) (inverse = 1: minus, the gradients' rotation); the other
+ * D - 2 R channels are copied.  freqs are angles in radians (fp64, |freq| < 2^10, finite); the angle
+ * is reduced exactly, to 2^-32 turns, at any position of 32 bits.  q and k (k.p may be NULL) in
+ * one call; an output may be its input, at the same strides.  1 <= D <= 256, 2 <= 2 R <= D.
+ */
+typedef struct {
+    s4_heads q;               /* [batch][L][H][D] */
+    s4_heads k;               /* [batch][L][G][D] or none */
+    s4_heads_out q_out, k_out;
+    const double* freqs;      /* [R] */
+    const int* positions;     /* [batch][L], or NULL: a token's place in its sequence */
+    long long positions_batch;/* stride of the batch (0: one row for all); tokens are contiguous */
+    float amplitude;
+    int batch, L, H, G, D, R, pairs, inverse, dtype;
+} s4_rotary_args;
+s4_status s4_rotary(const s4_rotary_args* a, void* stream);
+
+/*
+ * s4_layer_norm_fwd -- y = (x - mean) rsqrt(mean (x - mean)^2 + eps) w + b over each row's H channels;
+ * w and b may be absent (1 and 0).  y may be x (with the same row stride).  1 <= H <= 16384.
+ */
+typedef struct {
+    const void* x;            /* [rows][H], row strides below in elements */
+    void* y;
+    const float *w, *b;       /* [H] or NULL */
+    long long x_row, y_row, rows;
+    float eps;
+    int H, dtype;
+} s4_layer_norm_args;
+s4_status s4_layer_norm_fwd(const s4_layer_norm_args* a, void* stream);
+
+/*
+ * s4_layer_norm_bwd -- gradients of s4_layer_norm_fwd from dy: with u = (x - mean) r and d = dy w,
+ *     dx = r (d - mean d - u mean(d u)),  dw = sum_rows dy u,  db = sum_rows dy.
+ */
+typedef struct {
+    const void *x, *dy;
+    void* dx;
+    const float* w;           /* [H] or NULL */
+    float *dw, *db;           /* [H]; each may be NULL */
+    void* ws;                 /* s4_layer_norm_bwd_workspace_bytes */
+    size_t ws_bytes;
+    long long x_row, dy_row, dx_row, rows;
+    float eps;
+    int H, dtype;
+} s4_layer_norm_bwd_args;
+size_t s4_layer_norm_bwd_workspace_bytes(long long rows, int H);
+s4_status s4_layer_norm_bwd(const s4_layer_norm_bwd_args* a, void* stream);
+
+/*
+ * s4_vocab_loss_fwd -- softmax cross entropy of hidden states h [rows][H] against a vocabulary's
+ * weights w [V][H], without keeping the logits:
+ *     x = w h,  lse = log sum_v exp(x_v),  loss = lse - x_target.
+ * A row whose target is negative has a loss of 0 (its lse is formed all the same); a target
+ * >= V is recorded as S4_ERR_INVALID_INDEX and counts as a negative one.
+ * 1 <= rows <= 2^22, 1 <= H <= 16384, 1 <= V <= 2^22.
+ */
+typedef struct {
+    const void *h, *w;        /* row strides below in elements */
+    const void* targets;      /* [rows] int32, or int64 with wide_targets = 1 */
+    float *loss, *lse;        /* [rows] */
+    void* ws;                 /* s4_vocab_loss_workspace_bytes */
+    size_t ws_bytes;
+    long long h_row, w_row, rows;
+    int H, V, wide_targets, dtype;
+} s4_vocab_loss_args;
+/* The sizes, strides, addresses and type of `a` count, its ws and ws_bytes do not. */
+size_t s4_vocab_loss_workspace_bytes(const s4_vocab_loss_args* a);
+s4_status s4_vocab_loss_fwd(const s4_vocab_loss_args* a, void* stream);
+
+/*
+ * s4_vocab_loss_bwd -- gradients of sum_rows dloss loss from the forward's inputs and its lse:
+ *     g_v = dloss (exp(x_v - lse) - [v = target])  (0 for rows without a target),
+ *     dh = sum_v g_v w_v,   dw_v = sum_rows g_v h.
+ * The logits are formed again, a piece of the vocabulary at a time.
+ */
+typedef struct {
+    const void *h, *w, *targets;
+    const float *lse, *dloss; /* [rows] */
+    void *dh, *dw;            /* [rows][H] and [V][H], dense, of the inputs' type */
+    void* ws;                 /* s4_vocab_loss_bwd_workspace_bytes */
+    size_t ws_bytes;
+    long long h_row, w_row, rows;
+    int H, V, wide_targets, dtype;
+} s4_vocab_loss_bwd_args;
+size_t s4_vocab_loss_bwd_workspace_bytes(const s4_vocab_loss_bwd_args* a);
+s4_status s4_vocab_loss_bwd(const s4_vocab_loss_bwd_args* a, void* stream);
+
 /* Synchronises `stream`, then returns the device-detected status recorded in
  * `ws` by the last entry point that used it (S4_OK if none), or
  * S4_ERR_CUDA if the synchronisation or the read fails. */

@@ -19,6 +19,11 @@ and the selective block's operators (block.py, loaded at the first call):
     s4_short_conv_fwd / _step / _bwd                   short causal convolution with SiLU
     s4_selective_scan_fwd / _bwd, s4_selective_step    selective state-space scan, prompts and single tokens
     s4_block_norm_fwd / _bwd                           norms around a block, gate, residual scale and sum
+and those of the linear-attention block (sequence.py, likewise):
+    s4_linear_attention_fwd / _step / _bwd             linear attention with a decay for each head
+    s4_rotary_freqs, s4_rotary_fwd / _bwd              rotary positions of queries and keys
+    s4_layer_norm_fwd / _bwd                           layer norm
+    s4_vocab_loss_fwd / _bwd                           softmax cross entropy over a vocabulary
 """
 from __future__ import annotations
 
@@ -49,6 +54,10 @@ ABI_FUNCTIONS = [
     "s4_selective_scan_fwd", "s4_selective_scan_workspace_bytes",
     "s4_selective_scan_bwd", "s4_selective_scan_bwd_workspace_bytes",
     "s4_block_norm_fwd", "s4_block_norm_bwd", "s4_block_norm_bwd_workspace_bytes",
+    "s4_linear_attention_fwd", "s4_linear_attention_workspace_bytes",
+    "s4_linear_attention_bwd", "s4_linear_attention_bwd_workspace_bytes", "s4_rotary",
+    "s4_layer_norm_fwd", "s4_layer_norm_bwd", "s4_layer_norm_bwd_workspace_bytes",
+    "s4_vocab_loss_fwd", "s4_vocab_loss_workspace_bytes", "s4_vocab_loss_bwd", "s4_vocab_loss_bwd_workspace_bytes",
 ]
 
 HIPPO_KINDS = {"legs": 0, "legt": 1, "lagt": 2}
@@ -61,26 +70,32 @@ class S4Error(RuntimeError):
         super().__init__(f"{where}: {self.name} ({s4_status_str(self.code)})")
 
 
-# The selective block's operators, defined in block.py, which needs torch and is loaded at the first call of one
-# of them; they then take the places of these.
+# The selective block's operators, defined in block.py, and those of the linear-attention block, in sequence.py; both
+# need torch and are loaded at the first call of one of theirs, which then take the places of these.
 _BLOCK = ["s4_short_conv_fwd", "s4_short_conv_step", "s4_short_conv_bwd", "s4_selective_scan_fwd", "s4_selective_step",
           "s4_selective_scan_bwd", "s4_block_norm_fwd", "s4_block_norm_bwd"]
-__all__ += _BLOCK
+_SEQUENCE = ["s4_linear_attention_fwd", "s4_linear_attention_step", "s4_linear_attention_bwd", "s4_rotary_freqs",
+             "s4_rotary_fwd", "s4_rotary_bwd", "s4_layer_norm_fwd", "s4_layer_norm_bwd", "s4_vocab_loss_fwd",
+             "s4_vocab_loss_bwd"]
+__all__ += _BLOCK + _SEQUENCE
 
 
-def _at_first_call(name):
+def _at_first_call(name, module, names):
     def operator(*args, **kw):
         if globals()[name] is operator:
-            from . import block
-            globals().update((n, getattr(block, n)) for n in _BLOCK)
+            import importlib
+            loaded = importlib.import_module("." + module, __name__)
+            globals().update((n, getattr(loaded, n)) for n in names)
         return globals()[name](*args, **kw)
     operator.__name__ = operator.__qualname__ = name
-    operator.__doc__ = f"See block.{name}."
+    operator.__doc__ = f"See {module}.{name}."
     return operator
 
 
 for _name in _BLOCK:
-    globals()[_name] = _at_first_call(_name)
+    globals()[_name] = _at_first_call(_name, "block", _BLOCK)
+for _name in _SEQUENCE:
+    globals()[_name] = _at_first_call(_name, "sequence", _SEQUENCE)
 del _name
 
 

@@ -1,0 +1,661 @@
+// Linear attention with a decay for each head, forward and backward.  Every pass of it is one walk
+//
+//   out_i = scale (sum_{j<=i} e^{g (i-j)} (a_i . b_j) c_j + e^{g i} M^T a_i),   M' = e^{g n} M + sum_j e^{g (n-j)} b_j c_j^T
+//
+// over the tokens of a sequence in one direction, M being the state that the first of them sees (already
+// decayed once): forward (a, b, c) = (q, k, v); the gradients of q (dout, v, k), and from the
+// end, with the state's gradient as M, those of k (v, dout, q) and v (k, q, dout).
+#include "s4_block.cuh"
+#include "s4_sequence.h"
+
+namespace {
+using namespace s4blk;
+
+// One of a walk's inputs: [batch][L][heads][width], head h of the walk reads head h / per.
+struct In {
+  const void* p;
+  long long batch, row, head;
+  int per;
+};
+struct Walk {
+  In a, b, c;
+  void* out;                  // of the activations' type, or fp32 (out_f32)
+  long long out_batch, out_row, out_head;
+  const float* log_decay;
+  const int *lengths, *index;
+  const float* init;          // [slots][heads][...] state on entry, element (r, c) at r init_r + c init_c
+  float* last;                // where the state on return goes, laid out the same
+  float* local;               // [batch][heads][segs][da][dc], with several segments: what each starts from
+  long long init_r, init_c;
+  float scale, init_scale, last_scale;
+  int batch, L, H, da, dc, slots, segs, seg;
+  bool reverse, out_f32, vec;
+};
+
+constexpr int kThreads = 128, kCols = 64;  // per CTA: 4 warps, columns of c
+
+__device__ __forceinline__ float decay_of(const float* log_decay, int h) {
+  const float g = rd(log_decay + h);
+  return g < -1e30f ? -1e30f : g;  // -infinity times no tokens is no decay
+}
+__device__ __forceinline__ float power(float g, int n) { return ex2(g * kLog2e * (float)n); }
+
+// ---- matrix products of 16x8x16 bfloat16 tiles ------------------------------------------------------
+__device__ __forceinline__ void ldsm(unsigned (&r)[4], const __nv_bfloat16* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(s4dev::smem_u32(p)));
+}
+__device__ __forceinline__ void ldsm_t(unsigned (&r)[4], const __nv_bfloat16* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(s4dev::smem_u32(p)));
+}
+__device__ __forceinline__ void mma(float (&d)[4], const unsigned (&a)[4], unsigned b0, unsigned b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two values as NP words of two bfloat16 terms each: a term is what the ones before leave of the
+// value, rounded (8 bits each).
+template <int NP>
+__device__ __forceinline__ void split(float x, float y, unsigned (&w)[NP]) {
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    w[p] = two_of<__nv_bfloat16>(x, y);
+    x -= __uint_as_float(w[p] << 16);
+    y -= __uint_as_float(w[p] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ float lo_of(unsigned w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_of(unsigned w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Terms of an input: a bfloat16 is itself, a float16 two bfloat16, a float three.
+template <typename T>
+constexpr int kTerms = std::is_same_v<T, float> ? 3 : std::is_same_v<T, __half> ? 2 : 1;
+
+template <typename T, int D, int C>
+constexpr int kWalkBytes = 2 * kTerms<T> * (2 * C * (D + 8) + (C + D) * (kCols + 8));
+
+// Rows [i0, i0 + n) of the walk, columns [c0, c0 + W) of `width`, as terms in shared memory [terms][C][W + 8].
+template <typename T, int W, int C>
+__device__ __forceinline__ void load_rows(__nv_bfloat16* s, const T* p, long long row, int first, int step, int n, int width,
+                                          bool vec) {
+  constexpr int NP = kTerms<T>, PACKS = W / 8;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < C * PACKS; i += kThreads) {
+    const int r = i / PACKS, c = (i % PACKS) * 8;
+    Pack<T, 8> v;
+    const int have = r < n ? width - c : 0;
+    if (have > 0)
+      v = ld_pack<T, 8>(p + (long long)(first + step * r) * row + c, have < 8 ? have : 8, vec);
+    else
+      v.zero();
+    __nv_bfloat16* at = s + r * (W + 8) + c;
+    if constexpr (NP == 1) {
+      *reinterpret_cast<uint4*>(at) = *reinterpret_cast<const uint4*>(v.w);
+    } else {
+      unsigned w[4][NP];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) split<NP>(v.get(2 * j), v.get(2 * j + 1), w[j]);
+#pragma unroll
+      for (int t = 0; t < NP; ++t)
+        *reinterpret_cast<uint4*>(at + t * C * (W + 8)) = make_uint4(w[0][t], w[1][t], w[2][t], w[3][t]);
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ const T* at_head(const In& x, int b, int h) {
+  return static_cast<const T*>(x.p) + b * x.batch + (long long)(h / x.per) * x.head;
+}
+
+// The walk of one sequence, head and 64 columns of c, over one segment of the sequence, in chunks of C
+// tokens: the sums over a chunk's own tokens are products of its tiles, those over earlier tokens go
+// through M, in registers (warp w has rows w D/4 on).  D: da rounded up.  STATE: only M, from zero, for
+// the segments after it.
+template <typename T, int D, int C, bool STATE>
+__global__ void __launch_bounds__(kThreads) walk_kernel(Walk w, St st) {
+  constexpr int NP = kTerms<T>, NK = NP == 1 ? 2 : NP;  // terms of inputs, of scaled keys
+  constexpr int RW = C / 16, CW = 4 / RW, NT = kCols / 8 / CW;  // warps along tokens and columns, column tiles each
+  constexpr int MT = D / 64;                                    // tiles of 16 rows of M per warp
+  constexpr int PA = D + 8, PC = kCols + 8, SA = C * PA, SC = C * PC, SM = D * PC;
+  extern __shared__ __align__(16) char walk_smem[];
+  __nv_bfloat16* sa = reinterpret_cast<__nv_bfloat16*>(walk_smem);
+  __nv_bfloat16 *sb = sa + NP * SA, *sc = sb + NP * SA, *sm = sc + NP * SC;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, g4 = lane >> 2, t4 = lane & 3;
+  const int nc = (w.dc + kCols - 1) / kCols;
+  const int c0 = (int)(blockIdx.x % nc) * kCols, h = (int)(blockIdx.x / nc) % w.H, b = (int)(blockIdx.x / nc) / w.H;
+  const int seg = blockIdx.y, cols = w.dc - c0 < kCols ? w.dc - c0 : kCols;
+  record_gen(st);
+  const Seq q = seq_of(w.lengths, w.index, b, w.L, w.slots, st);
+  const int begin = seg * w.seg, end = begin + w.seg < q.len ? begin + w.seg : q.len;
+  const float g = decay_of(w.log_decay, h);
+  const T *pa = at_head<T>(w.a, b, h), *pb = at_head<T>(w.b, b, h), *pc = at_head<T>(w.c, b, h) + c0;
+
+  if (STATE && begin + w.seg >= q.len) return;  // no tokens behind this segment
+  if (!STATE) {
+    // padding, in the order of memory
+    const int from = q.len > begin ? q.len : begin, to = begin + w.seg < w.L ? begin + w.seg : w.L;
+    for (long long i = threadIdx.x; i < (long long)(to - from) * cols; i += kThreads) {
+      const long long at = b * w.out_batch + (from + i / cols) * w.out_row + h * w.out_head + c0 + i % cols;
+      if (w.out_f32)
+        wr(static_cast<float*>(w.out) + at, 0.f);
+      else
+        wr(static_cast<T*>(w.out) + at, from_f<T>(0.f));
+    }
+  }
+  const long long cells = (long long)w.da * w.dc;
+  const float* init = w.init && q.slot >= 0 ? w.init + (q.slot * w.H + h) * cells : nullptr;
+  float* last = w.last && q.slot >= 0 ? w.last + (q.slot * w.H + h) * cells : nullptr;
+  if (!STATE && q.len == 0) {
+    if (last && seg == 0)
+      for (int i = threadIdx.x; i < w.da * cols; i += kThreads) {
+        const long long at = (i / cols) * w.init_r + (c0 + i % cols) * w.init_c;
+        wr(last + at, init ? rd(init + at) : 0.f);
+      }
+    return;
+  }
+  if (begin >= q.len) return;
+
+  // M: element (row, col) of tile (i, j): rows m0 + 16 i + g4 (+8), columns 8 j + 2 t4 (+1)
+  const int m0 = wid * (D / 4);
+  float m[MT][8][4];
+  const auto each = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = m0 + 16 * i + g4 + (e >> 1) * 8, c = 8 * j + 2 * t4 + (e & 1);
+          f(m[i][j][e], r, c, r < w.da && c < cols);
+        }
+  };
+  float* local = w.local + (((long long)b * w.H + h) * w.segs + seg) * cells + c0;
+  if (STATE || (w.segs == 1 && !init)) {
+    each([&](float& v, int, int, bool) { v = 0.f; });
+  } else if (w.segs == 1) {
+    const float by = w.init_scale * (w.reverse ? 1.f : power(g, 1));
+    each([&](float& v, int r, int c, bool in) { v = in ? by * rd(init + r * w.init_r + (c0 + c) * w.init_c) : 0.f; });
+  } else {
+    // not from `init`, which may be where the last segment's CTA has put the state on return
+    each([&](float& v, int r, int c, bool in) { v = in ? rd(local + (long long)r * w.dc + c) : 0.f; });
+  }
+
+  for (int i0 = begin; i0 < end; i0 += C) {
+    const int n = end - i0 < C ? end - i0 : C, first = w.reverse ? q.len - 1 - i0 : i0, step = w.reverse ? -1 : 1;
+    const bool at_end = i0 + n >= q.len;
+    __syncthreads();
+    if (!STATE) {
+      load_rows<T, D, C>(sa, pa, w.a.row, first, step, n, w.da, w.vec);
+      // the state that this chunk sees
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            unsigned t[NP];
+            split<NP>(m[i][j][2 * half], m[i][j][2 * half + 1], t);
+            __nv_bfloat16* at = sm + (m0 + 16 * i + g4 + 8 * half) * PC + 8 * j + 2 * t4;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) *reinterpret_cast<unsigned*>(at + p * SM) = t[p];
+          }
+    }
+    load_rows<T, D, C>(sb, pb, w.b.row, first, step, n, w.da, w.vec);
+    load_rows<T, kCols, C>(sc, pc, w.c.row, first, step, n, cols, w.vec);
+    __syncthreads();
+
+    if (!STATE) {
+      const int r0 = (wid % RW) * 16, n0 = (wid / RW) * (NT * 8);
+      if (r0 < n) {
+        float o[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+#pragma unroll
+        for (int k = 0; k < D; k += 16) {
+          unsigned fa[NP][4];
+#pragma unroll
+          for (int p = 0; p < NP; ++p) ldsm(fa[p], sa + p * SA + (r0 + (lane & 15)) * PA + k + (lane >> 4) * 8);
+#pragma unroll
+          for (int j = 0; j < NT; j += 2) {
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+              unsigned fb[4];
+              ldsm_t(fb, sm + p * SM + (k + (lane & 15)) * PC + n0 + 8 * j + (lane >> 4) * 8);
+#pragma unroll
+              for (int u = 0; u + p < NP; ++u) {
+                mma(o[j], fa[u], fb[0], fb[1]);
+                mma(o[j + 1], fa[u], fb[2], fb[3]);
+              }
+            }
+          }
+        }
+        const int i_lo = r0 + g4, i_hi = i_lo + 8;
+        const float d_lo = power(g, i_lo), d_hi = power(g, i_hi);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) o[j][0] *= d_lo, o[j][1] *= d_lo, o[j][2] *= d_hi, o[j][3] *= d_hi;
+        for (int j0 = 0; j0 <= r0; j0 += 16) {
+          float s[2][4] = {};
+#pragma unroll
+          for (int k = 0; k < D; k += 16) {
+            unsigned fa[NP][4];
+#pragma unroll
+            for (int p = 0; p < NP; ++p) ldsm(fa[p], sa + p * SA + (r0 + (lane & 15)) * PA + k + (lane >> 4) * 8);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+              unsigned fb[4];
+              ldsm(fb, sb + p * SA + (j0 + (lane & 7) + (lane >> 4) * 8) * PA + k + (lane >> 3 & 1) * 8);
+#pragma unroll
+              for (int u = 0; u + p < NP; ++u) {
+                mma(s[0], fa[u], fb[0], fb[1]);
+                mma(s[1], fa[u], fb[2], fb[3]);
+              }
+            }
+          }
+          // the decayed weights as the left operand of the next product
+          unsigned fp[NP][4];
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int lag = i_lo + 8 * half - (j0 + 8 * x + 2 * t4);
+              const float u = lag >= 0 ? s[x][2 * half] * power(g, lag) : 0.f;
+              const float v = lag >= 1 ? s[x][2 * half + 1] * power(g, lag - 1) : 0.f;
+              unsigned t[NP];
+              split<NP>(u, v, t);
+#pragma unroll
+              for (int p = 0; p < NP; ++p) fp[p][2 * x + half] = t[p];
+            }
+#pragma unroll
+          for (int j = 0; j < NT; j += 2)
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+              unsigned fb[4];
+              ldsm_t(fb, sc + p * SC + (j0 + (lane & 15)) * PC + n0 + 8 * j + (lane >> 4) * 8);
+#pragma unroll
+              for (int u = 0; u + p < NP; ++u) {
+                mma(o[j], fp[u], fb[0], fb[1]);
+                mma(o[j + 1], fp[u], fb[2], fb[3]);
+              }
+            }
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int i = r0 + g4 + 8 * half;
+          if (i >= n) continue;
+          const long long at = b * w.out_batch + (long long)(first + step * i) * w.out_row + h * w.out_head + c0;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const int c = n0 + 8 * j + 2 * t4;
+            const float v[2] = {w.scale * o[j][2 * half], w.scale * o[j][2 * half + 1]};
+            if (c >= cols) continue;
+            if (w.out_f32)
+              st_f<float, 2>(static_cast<float*>(w.out) + at + c, cols - c, w.vec, v);
+            else
+              st_f<T, 2>(static_cast<T*>(w.out) + at + c, cols - c, w.vec, v);
+          }
+        }
+      }
+      if (at_end ? !last : i0 + n >= end) break;  // nothing needs the state any more
+    }
+
+    // M' = e^{g n} M + sum_j e^{g (n - j)} b_j c_j^T; what is kept as the forward pass's state has decayed once less
+    const int less = !STATE && at_end && !w.reverse ? 1 : 0;
+    const float by = expm1f(g * (float)(n - less));
+    each([&](float& v, int, int, bool) { v = fmaf(v, by, v); });
+#pragma unroll 1
+    for (int k = 0; k < C; k += 16) {
+      float f[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int j = k + 2 * t4 + (x & 1) + (x >> 1) * 8;
+        f[x] = power(g, n - less - j < 0 ? 0 : n - less - j);  // (rows from n on are zeros)
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        unsigned fa[NK][4];
+        unsigned raw[NP][4];
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+          ldsm_t(raw[p], sb + p * SA + (k + (lane & 7) + (lane >> 4) * 8) * PA + m0 + 16 * i + (lane >> 3 & 1) * 8);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          float u = 0.f, v = 0.f;
+#pragma unroll
+          for (int p = NP - 1; p >= 0; --p) u += lo_of(raw[p][x]), v += hi_of(raw[p][x]);
+          unsigned t[NK];
+          split<NK>(u * f[(x >> 1) * 2], v * f[(x >> 1) * 2 + 1], t);
+#pragma unroll
+          for (int p = 0; p < NK; ++p) fa[p][x] = t[p];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j += 2)
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            unsigned fb[4];
+            ldsm_t(fb, sc + p * SC + (k + (lane & 15)) * PC + 8 * j + (lane >> 4) * 8);
+#pragma unroll
+            for (int u = 0; u + p < NK; ++u) {
+              mma(m[i][j], fa[u], fb[0], fb[1]);
+              mma(m[i][j + 1], fa[u], fb[2], fb[3]);
+            }
+          }
+      }
+    }
+  }
+  if (STATE) {
+    float* to = local + cells;  // the next segment's
+    each([&](float& v, int r, int c, bool in) {
+      if (in) wr(to + (long long)r * w.dc + c, v);
+    });
+  } else if (last && end == q.len) {
+    each([&](float& v, int r, int c, bool in) {
+      if (in) wr(last + r * w.init_r + (c0 + c) * w.init_c, w.last_scale * v);
+    });
+  }
+}
+
+// What each segment starts from, in their order: slot 0 the state on entry, slot s + 1, which holds what segment s
+// adds, that and what comes before.
+__global__ void __launch_bounds__(256) join_kernel(Walk w, St st) {
+  const long long cells = (long long)w.da * w.dc, i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int h = blockIdx.y % w.H, b = blockIdx.y / w.H;
+  if (i >= cells) return;
+  const Seq q = seq_of(w.lengths, w.index, b, w.L, w.slots, st);
+  const float g = decay_of(w.log_decay, h), by = expm1f(g * (float)w.seg);
+  float v = 0.f;
+  if (w.init && q.slot >= 0)
+    v = w.init_scale * (w.reverse ? 1.f : power(g, 1)) *
+        rd(w.init + (q.slot * w.H + h) * cells + (i / w.dc) * w.init_r + (i % w.dc) * w.init_c);
+  float* p = w.local + ((long long)b * w.H + h) * w.segs * cells + i;
+  wr(p, v);
+  for (int s = 1; s * w.seg < q.len; ++s) {
+    p += cells;
+    v = fmaf(v, by, v) + rd(p);
+    wr(p, v);
+  }
+}
+
+// Gradients of shared heads: part [batch][L][H][d], summed over each group's heads in their order.
+template <typename T>
+__global__ void __launch_bounds__(256) group_sum_kernel(const float* part, T* out, long long batch_stride, long long row,
+                                                        long long head, int batch, int L, int H, int G, int d) {
+  const long long n = (long long)batch * L * G * d, each = H / G;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+    const int c = (int)(i % d), gr = (int)(i / d % G);
+    const long long token = i / d / G;
+    const float* p = part + (token * H + gr * each) * d + c;
+    float v = 0.f;
+    for (int j = 0; j < each; ++j) v += rd(p + (long long)j * d);
+    wr(out + (token / L) * batch_stride + (token % L) * row + gr * head + c, from_f<T>(v));
+  }
+}
+
+// ---- one token -----------------------------------------------------------------------------------
+// The state is read and written once, everything else is small: the bound is memory.  A CTA has some
+// columns of one head's state, a thread V neighbouring ones of every RG-th row; the sums over rows
+// meet in shared memory.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) step_kernel(s4_linear_attention_args a, int lanes, int blocks, St st) {
+  __shared__ float sums[256][V];
+  __shared__ float sq[256], sk[256];
+  const int cb = blockIdx.x % blocks, h = (int)(blockIdx.x / blocks) % a.H, b = (int)(blockIdx.x / blocks) / a.H;
+  record_gen(st);
+  const Seq q = seq_of(a.lengths, a.index, b, 1, a.slots, st);
+  const int lane = threadIdx.x % lanes, rg = threadIdx.x / lanes, RG = 256 / lanes, c = (cb * lanes + lane) * V;
+  T* o = static_cast<T*>(a.o.p) + b * a.o.batch + h * a.o.head;
+  const long long at = (q.slot < 0 ? 0 : q.slot * a.H + h) * a.K * a.V;
+  const float* s = a.state && q.slot >= 0 ? a.state + at : nullptr;
+  float* to = a.state_out && q.slot >= 0 ? a.state_out + at : nullptr;
+  if (q.len == 0) {
+    if (c < a.V) {
+      if (rg == 0)
+        for (int j = 0; j < V; ++j) wr(o + c + j, from_f<T>(0.f));
+      if (to && (to != s))
+        for (int r = rg; r < a.K; r += RG) {
+          float v[V] = {};
+          if (s) ld_f<float, V>(s + (long long)r * a.V + c, V, true, v);
+          st_f<float, V>(to + (long long)r * a.V + c, V, true, v);
+        }
+    }
+    return;
+  }
+  const int kv = h / (a.H / a.G);
+  const T* pq = static_cast<const T*>(a.q.p) + b * a.q.batch + h * a.q.head;
+  const T* pk = static_cast<const T*>(a.k.p) + b * a.k.batch + kv * a.k.head;
+  if (threadIdx.x < a.K) {
+    sq[threadIdx.x] = to_f(rd(pq + threadIdx.x)) * a.scale;
+    sk[threadIdx.x] = to_f(rd(pk + threadIdx.x));
+  }
+  const float by = expm1f(decay_of(a.log_decay, h));
+  float v[V], sum[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    sum[j] = 0.f;
+    v[j] = c < a.V ? to_f(rd(static_cast<const T*>(a.v.p) + b * a.v.batch + kv * a.v.head + c + j)) : 0.f;
+  }
+  __syncthreads();
+  if (c < a.V) {
+#pragma unroll 8
+    for (int r = rg; r < a.K; r += RG) {
+      float x[V] = {};
+      if (s) ld_f<float, V>(s + (long long)r * a.V + c, V, true, x);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        x[j] = fmaf(sk[r], v[j], fmaf(x[j], by, x[j]));
+        sum[j] = fmaf(sq[r], x[j], sum[j]);
+      }
+      if (to) st_f<float, V>(to + (long long)r * a.V + c, V, true, x);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) sums[threadIdx.x][j] = sum[j];
+  __syncthreads();
+  if (rg != 0 || c >= a.V) return;
+  for (int r = 1; r < RG; ++r)
+#pragma unroll
+    for (int j = 0; j < V; ++j) sum[j] += sums[r * lanes + lane][j];
+#pragma unroll
+  for (int j = 0; j < V; ++j) wr(o + c + j, from_f<T>(sum[j]));
+}
+
+template <typename T>
+cudaError_t step_t(const s4_linear_attention_args& a, St st, cudaStream_t s) {
+  const bool wide = a.V % 4 == 0 && vec_ok(a.state, 4, 16) && vec_ok(a.state_out, 4, 16);
+  const int V = wide ? 4 : 1, packs = a.V / V;
+  // Columns are shared out until every SM has a few CTAs, in blocks of whole sectors at least.
+  int lanes = 1;
+  while (lanes < packs && lanes < 64) lanes *= 2;
+  const long long heads = (long long)a.batch * a.H;
+  while (lanes * V > 8 && heads * ((packs + lanes - 1) / lanes) < 4ll * s4impl::num_sms()) lanes /= 2;
+  const int blocks = (packs + lanes - 1) / lanes;
+  s4impl::TimedLaunch tl("linear_attention", s);
+  if (wide)
+    step_kernel<T, 4><<<(unsigned)(heads * blocks), 256, 0, s>>>(a, lanes, blocks, st);
+  else
+    step_kernel<T, 1><<<(unsigned)(heads * blocks), 256, 0, s>>>(a, lanes, blocks, st);
+  return cudaGetLastError();
+}
+
+// ---- host side -----------------------------------------------------------------------------------
+// Segments of a sequence: as many as give each SM three CTAs, of 256 tokens or more.
+int segments(long long walks, int L) {
+  const long long want = (3ll * s4impl::num_sms() + walks - 1) / walks, most = (L + 255) / 256;
+  const long long n = want < most ? want : most;
+  return (int)(n < 1 ? 1 : n);
+}
+int segment_tokens(int L, int segs) { return ((L + segs - 1) / segs + 63) / 64 * 64; }
+size_t local_bytes(int batch, int L, int H, int da, int dc) {
+  const int segs = segments((long long)batch * H * ((dc + kCols - 1) / kCols), L);
+  return s4impl::align256(segs == 1 ? 0 : sizeof(float) * (size_t)batch * H * segs * da * dc);
+}
+
+template <typename T, int D>
+cudaError_t walk_d(const Walk& w, St st, cudaStream_t s) {
+  constexpr int C = kTerms<T> == 3 ? 32 : 64, bytes = kWalkBytes<T, D, C>;
+  const unsigned walks = (unsigned)((long long)w.batch * w.H * ((w.dc + kCols - 1) / kCols));
+  constexpr auto kernel = walk_kernel<T, D, C, false>;
+  allow_shared<kernel>(bytes);
+  if (w.segs > 1) {
+    constexpr auto state = walk_kernel<T, D, C, true>;
+    allow_shared<state>(bytes);
+    {
+      s4impl::TimedLaunch tl("linear_attention", s);
+      state<<<dim3(walks, w.segs - 1), kThreads, bytes, s>>>(w, st);
+    }
+    s4impl::TimedLaunch tl("linear_attention", s);
+    join_kernel<<<dim3((unsigned)((w.da * w.dc + 255) / 256), w.batch * w.H), 256, 0, s>>>(w, st);
+  }
+  s4impl::TimedLaunch tl("linear_attention", s);
+  kernel<<<dim3(walks, w.segs), kThreads, bytes, s>>>(w, st);
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t walk_t(Walk w, St st, cudaStream_t s) {
+  w.segs = segments((long long)w.batch * w.H * ((w.dc + kCols - 1) / kCols), w.L);
+  w.seg = segment_tokens(w.L, w.segs);
+  w.segs = (w.L + w.seg - 1) / w.seg;
+  const int e = sizeof(T), eo = w.out_f32 ? 4 : e;
+  const auto ok = [&](const In& x) { return vec_ok(x.p, e, 16, x.batch, x.row) && vec_ok(x.p, e, 16, x.head); };
+  w.vec = ok(w.a) && ok(w.b) && ok(w.c) && vec_ok(w.out, eo, 2 * eo, w.out_batch, w.out_row) &&
+          vec_ok(w.out, eo, 2 * eo, w.out_head);
+#ifdef S4_BOUNDS_CHECK
+  s4impl::Extents x{};
+  const auto add = [&](const In& i, int d) {
+    x.add(i.p, e, true, false, d, w.batch, i.batch, w.L, i.row, (w.H + i.per - 1) / i.per, i.head);
+  };
+  add(w.a, w.da), add(w.b, w.da), add(w.c, w.dc);
+  x.add(w.out, eo, false, true, w.dc, w.batch, w.out_batch, w.L, w.out_row, w.H, w.out_head);
+  x.in(w.log_decay, 4, w.H);
+  x.in(w.lengths, 4, w.batch);
+  x.in(w.index, 4, w.batch);
+  x.in(w.init, 4, (long long)w.H * w.da * w.dc, w.slots);
+  x.out(w.last, 4, (long long)w.H * w.da * w.dc, w.slots);
+  if (w.segs > 1) x.scratch(w.local, 4, (long long)w.batch * w.H * w.segs * w.da * w.dc);
+  if (const cudaError_t err = set_extents(x, s); err != cudaSuccess) return err;
+#endif
+  if (w.da <= 64) return walk_d<T, 64>(w, st, s);
+  return w.da <= 128 ? walk_d<T, 128>(w, st, s) : walk_d<T, 256>(w, st, s);
+}
+
+In in_of(const s4_heads& r, int per) { return {r.p, r.batch, r.row, r.head, per}; }
+
+template <typename T>
+cudaError_t fwd_t(const s4_linear_attention_args& a, St st, cudaStream_t s) {
+  if (a.L == 1) {
+#ifdef S4_BOUNDS_CHECK
+    s4impl::Extents x{};
+    const int e = sizeof(T);
+    x.add(a.q.p, e, true, false, a.K, a.batch, a.q.batch, a.H, a.q.head);
+    x.add(a.k.p, e, true, false, a.K, a.batch, a.k.batch, a.G, a.k.head);
+    x.add(a.v.p, e, true, false, a.V, a.batch, a.v.batch, a.G, a.v.head);
+    x.add(a.o.p, e, false, true, a.V, a.batch, a.o.batch, a.H, a.o.head);
+    x.in(a.log_decay, 4, a.H);
+    x.in(a.lengths, 4, a.batch);
+    x.in(a.index, 4, a.batch);
+    x.in(a.state, 4, (long long)a.H * a.K * a.V, a.slots);
+    x.out(a.state_out, 4, (long long)a.H * a.K * a.V, a.slots);
+    if (const cudaError_t err = set_extents(x, s); err != cudaSuccess) return err;
+#endif
+    return step_t<T>(a, st, s);
+  }
+  Walk w{};
+  w.a = in_of(a.q, 1), w.b = in_of(a.k, a.H / a.G), w.c = in_of(a.v, a.H / a.G);
+  w.out = a.o.p, w.out_batch = a.o.batch, w.out_row = a.o.row, w.out_head = a.o.head;
+  w.log_decay = a.log_decay, w.lengths = a.lengths, w.index = a.index;
+  w.init = a.state, w.last = a.state_out, w.init_r = a.V, w.init_c = 1;
+  w.local = reinterpret_cast<float*>(static_cast<char*>(a.ws) + s4impl::kStatusBytes);
+  w.scale = a.scale, w.init_scale = w.last_scale = 1.f;
+  w.batch = a.batch, w.L = a.L, w.H = a.H, w.da = a.K, w.dc = a.V, w.slots = a.slots;
+  return walk_t<T>(w, st, s);
+}
+
+template <typename T>
+cudaError_t bwd_t(const s4_linear_attention_bwd_args& a, St st, cudaStream_t s) {
+  const int each = a.H / a.G;
+  char* at = static_cast<char*>(a.ws) + s4impl::kStatusBytes;
+  Walk w{};
+  w.log_decay = a.log_decay, w.lengths = a.lengths;
+  w.scale = a.scale;
+  w.batch = a.batch, w.L = a.L, w.H = a.H, w.slots = a.batch;
+  // dq: forward over (dout, v, k), the state transposed
+  w.a = in_of(a.dout, 1), w.b = in_of(a.v, each), w.c = in_of(a.k, each);
+  w.out = a.dq.p, w.out_batch = a.dq.batch, w.out_row = a.dq.row, w.out_head = a.dq.head;
+  w.da = a.V, w.dc = a.K, w.init = a.state0, w.init_r = 1, w.init_c = a.V, w.init_scale = 1.f;
+  w.local = reinterpret_cast<float*>(at);
+  cudaError_t err = walk_t<T>(w, st, s);
+  if (err != cudaSuccess) return err;
+  at += local_bytes(a.batch, a.L, a.H, a.V, a.K);
+  w.reverse = true;
+  w.init_scale = 1.f / a.scale;
+  for (const bool key : {true, false}) {
+    const int d = key ? a.K : a.V;
+    const s4_heads_out& out = key ? a.dk : a.dv;
+    float* part = nullptr;
+    w.local = reinterpret_cast<float*>(at);
+    at += local_bytes(a.batch, a.L, a.H, key ? a.V : a.K, d);
+    if (each > 1) {
+      part = reinterpret_cast<float*>(at);
+      at += s4impl::align256(sizeof(float) * (size_t)a.batch * a.L * a.H * d);
+      w.out = part, w.out_f32 = true, w.out_head = d, w.out_row = (long long)a.H * d, w.out_batch = w.out_row * a.L;
+    } else {
+      w.out = out.p, w.out_batch = out.batch, w.out_row = out.row, w.out_head = out.head;
+    }
+    if (key) {  // dk: (v, dout, q), transposed
+      w.a = in_of(a.v, each), w.b = in_of(a.dout, 1), w.c = in_of(a.q, 1);
+      w.init = a.dstate, w.init_r = 1, w.init_c = a.V;
+    } else {  // dv: (k, q, dout); it leaves the state's gradient
+      w.a = in_of(a.k, each), w.b = in_of(a.q, 1), w.c = in_of(a.dout, 1);
+      w.da = a.K, w.dc = a.V, w.init_r = a.V, w.init_c = 1;
+      w.last = a.dstate0, w.last_scale = a.scale;
+    }
+    err = walk_t<T>(w, st, s);
+    if (err != cudaSuccess) return err;
+    if (part) {
+#ifdef S4_BOUNDS_CHECK
+      s4impl::Extents x{};
+      x.in(part, 4, (long long)a.batch * a.L * a.H * d);
+      x.add(out.p, sizeof(T), false, true, d, a.batch, out.batch, a.L, out.row, a.G, out.head);
+      if (const cudaError_t e = set_extents(x, s); e != cudaSuccess) return e;
+#endif
+      const long long n = ((long long)a.batch * a.L * a.G * d + 255) / 256, most = 16ll * s4impl::num_sms();
+      s4impl::TimedLaunch tl("linear_attention", s);
+      group_sum_kernel<T><<<(unsigned)(n < most ? n : most), 256, 0, s>>>(part, static_cast<T*>(out.p), out.batch, out.row,
+                                                                        out.head, a.batch, a.L, a.H, a.G, d);
+      err = cudaGetLastError();
+      if (err != cudaSuccess) return err;
+    }
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+namespace s4impl {
+
+#ifdef S4_BOUNDS_CHECK
+S4_OOB_COUNTER(oob_linear_attention)
+#endif
+
+size_t linear_attention_scratch(int batch, int L, int H, int K, int V) {
+  return L == 1 ? 0 : local_bytes(batch, L, H, K, V);
+}
+
+cudaError_t launch_linear_attention(const s4_linear_attention_args& a, St st, cudaStream_t s) {
+  if (a.dtype == S4_F32) return fwd_t<float>(a, st, s);
+  return a.dtype == S4_BF16 ? fwd_t<__nv_bfloat16>(a, st, s) : fwd_t<__half>(a, st, s);
+}
+
+size_t linear_attention_bwd_scratch(int batch, int L, int H, int G, int K, int V) {
+  const size_t part = H == G ? 0 : align256(sizeof(float) * (size_t)batch * L * H * K) + align256(sizeof(float) * (size_t)batch * L * H * V);
+  return 2 * local_bytes(batch, L, H, V, K) + local_bytes(batch, L, H, K, V) + part;
+}
+
+cudaError_t launch_linear_attention_bwd(const s4_linear_attention_bwd_args& a, St st, cudaStream_t s) {
+  if (a.dtype == S4_F32) return bwd_t<float>(a, st, s);
+  return a.dtype == S4_BF16 ? bwd_t<__nv_bfloat16>(a, st, s) : bwd_t<__half>(a, st, s);
+}
+
+}  // namespace s4impl

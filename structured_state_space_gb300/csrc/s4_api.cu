@@ -11,6 +11,7 @@
 
 #include "s4.h"
 #include "s4_block.h"
+#include "s4_sequence.h"
 #include "s4_dev.cuh"
 #include "s4_internal.h"
 
@@ -280,7 +281,8 @@ long long s4_bounds_violations(void) {
   const unsigned long long c[] = {s4impl::oob_rows(), s4impl::oob_cluster(), s4impl::oob_fourstep(),
                                   s4impl::oob_cauchy(), s4impl::oob_recurrent(), s4impl::oob_bordered(),
                                   s4impl::oob_short_conv(), s4impl::oob_selective(), s4impl::oob_selective_bwd(),
-                                  s4impl::oob_block_norm()};
+                                  s4impl::oob_block_norm(), s4impl::oob_linear_attention(), s4impl::oob_rotary(),
+                                  s4impl::oob_layer_norm(), s4impl::oob_vocab_loss()};
   unsigned long long t = 0;
   for (unsigned long long v : c) {
     if (v == ~0ull) return -2;
