@@ -21,8 +21,8 @@ OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(LIBDIR, "libs4.so")
 SOURCES = ["s4_api.cu", "cauchy.cu", "fft_rows.cu", "fft_cluster.cu", "fft_fourstep.cu", "s4_noalloc.cu", "recurrent.cu", "bordered.cu",
            "hippo.cpp", "block_api.cu", "short_conv.cu", "selective_scan.cu",
-           "selective_scan_bwd.cu", "block_norm.cu", "sequence_api.cu", "linear_attention.cu", "rotary.cu", "layer_norm.cu",
-           "vocab_loss.cu"]
+           "selective_scan_bwd.cu", "block_norm.cu", "sequence_api.cu", "linear_attention.cu", "linear_attention_tiles.cu",
+           "rotary.cu", "layer_norm.cu", "vocab_loss.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 GENDIR = os.path.join(OBJDIR, "gen")

@@ -5,40 +5,14 @@
 // over the tokens of a sequence in one direction, M being the state that the first of them sees (already
 // decayed once): forward (a, b, c) = (q, k, v); the gradients of q (dout, v, k), and from the
 // end, with the state's gradient as M, those of k (v, dout, q) and v (k, q, dout).
-#include "s4_block.cuh"
-#include "s4_sequence.h"
+#include "linear_attention.cuh"
 
 namespace {
 using namespace s4blk;
-
-// One of a walk's inputs: [batch][L][heads][width], head h of the walk reads head h / per.
-struct In {
-  const void* p;
-  long long batch, row, head;
-  int per;
-};
-struct Walk {
-  In a, b, c;
-  void* out;                  // of the activations' type, or fp32 (out_f32)
-  long long out_batch, out_row, out_head;
-  const float* log_decay;
-  const int *lengths, *index;
-  const float* init;          // [slots][heads][...] state on entry, element (r, c) at r init_r + c init_c
-  float* last;                // where the state on return goes, laid out the same
-  float* local;               // [batch][heads][segs][da][dc], with several segments: what each starts from
-  long long init_r, init_c;
-  float scale, init_scale, last_scale;
-  int batch, L, H, da, dc, slots, segs, seg;
-  bool reverse, out_f32, vec;
-};
+using s4impl::In;
+using s4impl::Walk;
 
 constexpr int kThreads = 128, kCols = 64;  // per CTA: 4 warps, columns of c
-
-__device__ __forceinline__ float decay_of(const float* log_decay, int h) {
-  const float g = rd(log_decay + h);
-  return g < -1e30f ? -1e30f : g;  // -infinity times no tokens is no decay
-}
-__device__ __forceinline__ float power(float g, int n) { return ex2(g * kLog2e * (float)n); }
 
 // ---- matrix products of 16x8x16 bfloat16 tiles ------------------------------------------------------
 __device__ __forceinline__ void ldsm(unsigned (&r)[4], const __nv_bfloat16* p) {
@@ -103,11 +77,6 @@ __device__ __forceinline__ void load_rows(__nv_bfloat16* s, const T* p, long lon
         *reinterpret_cast<uint4*>(at + t * C * (W + 8)) = make_uint4(w[0][t], w[1][t], w[2][t], w[3][t]);
     }
   }
-}
-
-template <typename T>
-__device__ __forceinline__ const T* at_head(const In& x, int b, int h) {
-  return static_cast<const T*>(x.p) + b * x.batch + (long long)(h / x.per) * x.head;
 }
 
 // The walk of one sequence, head and 64 columns of c, over one segment of the sequence, in chunks of C
@@ -365,15 +334,19 @@ __global__ void __launch_bounds__(256) join_kernel(Walk w, St st) {
   if (i >= cells) return;
   const Seq q = seq_of(w.lengths, w.index, b, w.L, w.slots, st);
   const float g = decay_of(w.log_decay, h), by = expm1f(g * (float)w.seg);
+  // counted from the sequence's start, the first segment of a walk from its end is the one that may not be full
+  const int part = w.reverse && w.from_start ? q.len - (q.len - 1) / w.seg * w.seg : w.seg;
+  const float by_first = expm1f(g * (float)part);
   float v = 0.f;
   if (w.init && q.slot >= 0)
     v = w.init_scale * (w.reverse ? 1.f : power(g, 1)) *
-        rd(w.init + (q.slot * w.H + h) * cells + (i / w.dc) * w.init_r + (i % w.dc) * w.init_c);
+        rd(w.init + (q.slot * w.H + h) * cells + (w.from_start ? i % w.da : i / w.dc) * w.init_r +
+           (w.from_start ? i / w.da : i % w.dc) * w.init_c);
   float* p = w.local + ((long long)b * w.H + h) * w.segs * cells + i;
   wr(p, v);
   for (int s = 1; s * w.seg < q.len; ++s) {
     p += cells;
-    v = fmaf(v, by, v) + rd(p);
+    v = fmaf(v, s == 1 ? by_first : by, v) + rd(p);
     wr(p, v);
   }
 }
@@ -488,7 +461,11 @@ int segments(long long walks, int L) {
 }
 int segment_tokens(int L, int segs) { return ((L + segs - 1) / segs + 63) / 64 * 64; }
 size_t local_bytes(int batch, int L, int H, int da, int dc) {
-  const int segs = segments((long long)batch * H * ((dc + kCols - 1) / kCols), L);
+  int segs = segments((long long)batch * H * ((dc + kCols - 1) / kCols), L);
+  for (int passes = 1; passes <= 3; ++passes) {  // whichever kernels the strides allow
+    const int n = da <= 128 && dc <= 128 ? s4impl::tile_segments((long long)batch * H, L, passes) : 1;
+    segs = n > segs ? n : segs;
+  }
   return s4impl::align256(segs == 1 ? 0 : sizeof(float) * (size_t)batch * H * segs * da * dc);
 }
 
@@ -505,8 +482,7 @@ cudaError_t walk_d(const Walk& w, St st, cudaStream_t s) {
       s4impl::TimedLaunch tl("linear_attention", s);
       state<<<dim3(walks, w.segs - 1), kThreads, bytes, s>>>(w, st);
     }
-    s4impl::TimedLaunch tl("linear_attention", s);
-    join_kernel<<<dim3((unsigned)((w.da * w.dc + 255) / 256), w.batch * w.H), 256, 0, s>>>(w, st);
+    if (const cudaError_t err = s4impl::launch_join(w, st, s); err != cudaSuccess) return err;
   }
   s4impl::TimedLaunch tl("linear_attention", s);
   kernel<<<dim3(walks, w.segs), kThreads, bytes, s>>>(w, st);
@@ -514,6 +490,8 @@ cudaError_t walk_d(const Walk& w, St st, cudaStream_t s) {
 }
 template <typename T>
 cudaError_t walk_t(Walk w, St st, cudaStream_t s) {
+  constexpr int code = std::is_same_v<T, float> ? S4_F32 : std::is_same_v<T, __half> ? S4_F16 : S4_BF16;
+  if (s4impl::tiles_take(w, code)) return s4impl::launch_tiles(&w, 1, code, st, s);
   w.segs = segments((long long)w.batch * w.H * ((w.dc + kCols - 1) / kCols), w.L);
   w.seg = segment_tokens(w.L, w.segs);
   w.segs = (w.L + w.seg - 1) / w.seg;
@@ -574,61 +552,66 @@ cudaError_t fwd_t(const s4_linear_attention_args& a, St st, cudaStream_t s) {
 
 template <typename T>
 cudaError_t bwd_t(const s4_linear_attention_bwd_args& a, St st, cudaStream_t s) {
+  constexpr int code = std::is_same_v<T, float> ? S4_F32 : std::is_same_v<T, __half> ? S4_F16 : S4_BF16;
   const int each = a.H / a.G;
   char* at = static_cast<char*>(a.ws) + s4impl::kStatusBytes;
-  Walk w{};
-  w.log_decay = a.log_decay, w.lengths = a.lengths;
-  w.scale = a.scale;
-  w.batch = a.batch, w.L = a.L, w.H = a.H, w.slots = a.batch;
+  const auto take = [&](size_t bytes) {
+    float* p = reinterpret_cast<float*>(at);
+    at += bytes;
+    return p;
+  };
+  Walk w[3]{};
+  for (Walk& x : w) {
+    x.log_decay = a.log_decay, x.lengths = a.lengths;
+    x.scale = a.scale, x.last_scale = a.scale;
+    x.batch = a.batch, x.L = a.L, x.H = a.H, x.slots = a.batch;
+  }
   // dq: forward over (dout, v, k), the state transposed
-  w.a = in_of(a.dout, 1), w.b = in_of(a.v, each), w.c = in_of(a.k, each);
-  w.out = a.dq.p, w.out_batch = a.dq.batch, w.out_row = a.dq.row, w.out_head = a.dq.head;
-  w.da = a.V, w.dc = a.K, w.init = a.state0, w.init_r = 1, w.init_c = a.V, w.init_scale = 1.f;
-  w.local = reinterpret_cast<float*>(at);
-  cudaError_t err = walk_t<T>(w, st, s);
-  if (err != cudaSuccess) return err;
-  at += local_bytes(a.batch, a.L, a.H, a.V, a.K);
-  w.reverse = true;
-  w.init_scale = 1.f / a.scale;
-  for (const bool key : {true, false}) {
-    const int d = key ? a.K : a.V;
-    const s4_heads_out& out = key ? a.dk : a.dv;
-    float* part = nullptr;
-    w.local = reinterpret_cast<float*>(at);
-    at += local_bytes(a.batch, a.L, a.H, key ? a.V : a.K, d);
+  w[0].a = in_of(a.dout, 1), w[0].b = in_of(a.v, each), w[0].c = in_of(a.k, each);
+  w[0].out = a.dq.p, w[0].out_batch = a.dq.batch, w[0].out_row = a.dq.row, w[0].out_head = a.dq.head;
+  w[0].da = a.V, w[0].dc = a.K, w[0].init = a.state0, w[0].init_r = 1, w[0].init_c = a.V, w[0].init_scale = 1.f;
+  // dk: from the end over (v, dout, q), transposed
+  w[1].a = in_of(a.v, each), w[1].b = in_of(a.dout, 1), w[1].c = in_of(a.q, 1);
+  w[1].da = a.V, w[1].dc = a.K, w[1].init = a.dstate, w[1].init_r = 1, w[1].init_c = a.V;
+  // dv: from the end over (k, q, dout); it leaves the state's gradient
+  w[2].a = in_of(a.k, each), w[2].b = in_of(a.q, 1), w[2].c = in_of(a.dout, 1);
+  w[2].da = a.K, w[2].dc = a.V, w[2].init = a.dstate, w[2].init_r = a.V, w[2].init_c = 1, w[2].last = a.dstate0;
+  float* part[3]{};
+  for (int i = 0; i < 3; ++i) {
+    w[i].local = take(local_bytes(a.batch, a.L, a.H, w[i].da, w[i].dc));
+    if (i == 0) continue;
+    const s4_heads_out& out = i == 1 ? a.dk : a.dv;
+    const int d = w[i].dc;
+    w[i].reverse = true, w[i].init_scale = 1.f / a.scale;
     if (each > 1) {
-      part = reinterpret_cast<float*>(at);
-      at += s4impl::align256(sizeof(float) * (size_t)a.batch * a.L * a.H * d);
-      w.out = part, w.out_f32 = true, w.out_head = d, w.out_row = (long long)a.H * d, w.out_batch = w.out_row * a.L;
+      w[i].out = part[i] = take(s4impl::align256(sizeof(float) * (size_t)a.batch * a.L * a.H * d));
+      w[i].out_f32 = true, w[i].out_head = d, w[i].out_row = (long long)a.H * d, w[i].out_batch = w[i].out_row * a.L;
     } else {
-      w.out = out.p, w.out_batch = out.batch, w.out_row = out.row, w.out_head = out.head;
-    }
-    if (key) {  // dk: (v, dout, q), transposed
-      w.a = in_of(a.v, each), w.b = in_of(a.dout, 1), w.c = in_of(a.q, 1);
-      w.init = a.dstate, w.init_r = 1, w.init_c = a.V;
-    } else {  // dv: (k, q, dout); it leaves the state's gradient
-      w.a = in_of(a.k, each), w.b = in_of(a.q, 1), w.c = in_of(a.dout, 1);
-      w.da = a.K, w.dc = a.V, w.init_r = a.V, w.init_c = 1;
-      w.last = a.dstate0, w.last_scale = a.scale;
-    }
-    err = walk_t<T>(w, st, s);
-    if (err != cudaSuccess) return err;
-    if (part) {
-#ifdef S4_BOUNDS_CHECK
-      s4impl::Extents x{};
-      x.in(part, 4, (long long)a.batch * a.L * a.H * d);
-      x.add(out.p, sizeof(T), false, true, d, a.batch, out.batch, a.L, out.row, a.G, out.head);
-      if (const cudaError_t e = set_extents(x, s); e != cudaSuccess) return e;
-#endif
-      const long long n = ((long long)a.batch * a.L * a.G * d + 255) / 256, most = 16ll * s4impl::num_sms();
-      s4impl::TimedLaunch tl("linear_attention", s);
-      group_sum_kernel<T><<<(unsigned)(n < most ? n : most), 256, 0, s>>>(part, static_cast<T*>(out.p), out.batch, out.row,
-                                                                        out.head, a.batch, a.L, a.H, a.G, d);
-      err = cudaGetLastError();
-      if (err != cudaSuccess) return err;
+      w[i].out = out.p, w[i].out_batch = out.batch, w[i].out_row = out.row, w[i].out_head = out.head;
     }
   }
-  return cudaSuccess;
+  cudaError_t err = cudaSuccess;
+  if (s4impl::tiles_take(w[0], code) && s4impl::tiles_take(w[1], code) && s4impl::tiles_take(w[2], code) &&
+      (a.K <= 64) == (a.V <= 64))
+    err = s4impl::launch_tiles(w, 3, code, st, s);
+  else
+    for (int i = 0; i < 3 && err == cudaSuccess; ++i) err = walk_t<T>(w[i], st, s);
+  for (int i = 1; i < 3 && err == cudaSuccess && each > 1; ++i) {
+    const s4_heads_out& out = i == 1 ? a.dk : a.dv;
+    const int d = w[i].dc;
+#ifdef S4_BOUNDS_CHECK
+    s4impl::Extents x{};
+    x.in(part[i], 4, (long long)a.batch * a.L * a.H * d);
+    x.add(out.p, sizeof(T), false, true, d, a.batch, out.batch, a.L, out.row, a.G, out.head);
+    if (const cudaError_t e = set_extents(x, s); e != cudaSuccess) return e;
+#endif
+    const long long n = ((long long)a.batch * a.L * a.G * d + 255) / 256, most = 16ll * s4impl::num_sms();
+    s4impl::TimedLaunch tl("linear_attention", s);
+    group_sum_kernel<T><<<(unsigned)(n < most ? n : most), 256, 0, s>>>(part[i], static_cast<T*>(out.p), out.batch, out.row,
+                                                                      out.head, a.batch, a.L, a.H, a.G, d);
+    err = cudaGetLastError();
+  }
+  return err;
 }
 
 }  // namespace
@@ -641,6 +624,12 @@ S4_OOB_COUNTER(oob_linear_attention)
 
 size_t linear_attention_scratch(int batch, int L, int H, int K, int V) {
   return L == 1 ? 0 : local_bytes(batch, L, H, K, V);
+}
+
+cudaError_t launch_join(const Walk& w, St st, cudaStream_t s) {
+  s4impl::TimedLaunch tl("linear_attention", s);
+  join_kernel<<<dim3((unsigned)((w.da * w.dc + 255) / 256), w.batch * w.H), 256, 0, s>>>(w, st);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_linear_attention(const s4_linear_attention_args& a, St st, cudaStream_t s) {

@@ -282,7 +282,7 @@ long long s4_bounds_violations(void) {
                                   s4impl::oob_cauchy(), s4impl::oob_recurrent(), s4impl::oob_bordered(),
                                   s4impl::oob_short_conv(), s4impl::oob_selective(), s4impl::oob_selective_bwd(),
                                   s4impl::oob_block_norm(), s4impl::oob_linear_attention(), s4impl::oob_rotary(),
-                                  s4impl::oob_layer_norm(), s4impl::oob_vocab_loss()};
+                                  s4impl::oob_layer_norm(), s4impl::oob_vocab_loss(), s4impl::oob_linear_attention_tiles()};
   unsigned long long t = 0;
   for (unsigned long long v : c) {
     if (v == ~0ull) return -2;

@@ -20,6 +20,7 @@ cudaError_t launch_vocab_loss_bwd(const s4_vocab_loss_bwd_args& a, St st, cudaSt
 
 #ifdef S4_BOUNDS_CHECK
 unsigned long long oob_linear_attention();
+unsigned long long oob_linear_attention_tiles();
 unsigned long long oob_rotary();
 unsigned long long oob_layer_norm();
 unsigned long long oob_vocab_loss();

@@ -55,13 +55,25 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
-      "[%32];"
+      "[%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
         "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
         "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
         "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(at));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+      : "r"(at)
+      : "memory");
+}
+// Twice as much, on its way at once.
+__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t at2, uint32_t (&r)[32], uint32_t (&q)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]), "=r"(q[7]), "=r"(q[8]), "=r"(q[9]), "=r"(q[10]), "=r"(q[11]), "=r"(q[12]), "=r"(q[13]), "=r"(q[14]), "=r"(q[15]), "=r"(q[16]), "=r"(q[17]), "=r"(q[18]), "=r"(q[19]), "=r"(q[20]), "=r"(q[21]), "=r"(q[22]), "=r"(q[23]), "=r"(q[24]), "=r"(q[25]), "=r"(q[26]), "=r"(q[27]), "=r"(q[28]), "=r"(q[29]), "=r"(q[30]), "=r"(q[31])
+      : "r"(at), "r"(at2)
+      : "memory");
 }
 __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, int z, unsigned long long* bar) {
   asm volatile(
@@ -112,8 +124,8 @@ __global__ void __launch_bounds__(256, 1)
   __shared__ unsigned long long full[S::STAGES], empty[S::STAGES], ready[2], taken[2], idle;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int failed;
-  char* smem = reinterpret_cast<char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  char* smem = raw + (-s4dev::smem_u32(raw) & 1023);  // (still a shared-memory address to the compiler)
+  const int wid = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (uniform)
   if (st.w) s4dev::st_record_gen(st);
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::STAGES; ++i) s4dev::mbar_init(&full[i], 1), s4dev::mbar_init(&empty[i], 1);
@@ -135,6 +147,9 @@ __global__ void __launch_bounds__(256, 1)
     }
     failed = 1;
     return false;
+  };
+  const auto wait_warp = [&](unsigned long long* bar, unsigned parity) {
+    return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
   };
   struct Tile {
     int m, n, from, to, split;
@@ -186,31 +201,38 @@ __global__ void __launch_bounds__(256, 1)
         if (rounds > 0) s4dev::mbar_wait(&full[i], (unsigned)(rounds - 1) & 1);
       }
     }
-  } else if (wid == 1 && elected()) {
+  } else if (wid == 1) {
+    // the warp stays together, so that the descriptors are uniform; one lane issues
+    const bool one = elected();
     int stage = 0, buf = 0;
     unsigned phase = 0, buf_phase = 0;
-    for (int t = blockIdx.x; t < tiles && !failed; t += gridDim.x) {
+    bool ok = true;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
       const Tile at = tile_of(t);
-      if (!wait(&taken[buf], buf_phase ^ 1)) break;
+      ok = wait_warp(&taken[buf], buf_phase ^ 1);
       fence_after();
       const uint32_t d = tmem + buf * BN;
-      const int steps = p.pairs * (at.to - at.from);
+      const int steps = ok ? p.pairs * (at.to - at.from) : 0;
       for (int i = 0; i < steps; ++i) {
-        if (!wait(&full[stage], phase)) break;
+        ok = wait_warp(&full[stage], phase);
+        if (!ok) break;
         fence_after();
-        const uint32_t a = s4dev::smem_u32(smem + stage * S::STAGE), b = a + S::A;
-        const uint64_t da = tile_desc(a, A_MN ? 8192 : 16), db = tile_desc(b, B_MN ? 8192 : 16);
+        if (one) {
+          const uint32_t a = s4dev::smem_u32(smem + stage * S::STAGE), b = a + S::A;
+          const uint64_t da = tile_desc(a, A_MN ? 8192 : 16), db = tile_desc(b, B_MN ? 8192 : 16);
 #pragma unroll
-        for (int k = 0; k < kBK / 16; ++k)
-          mma_f16(d, da + k * (A_MN ? 2048 >> 4 : 32 >> 4), db + k * (B_MN ? 2048 >> 4 : 32 >> 4), p.what, i + k > 0);
-        mma_commit(&empty[stage]);
+          for (int k = 0; k < kBK / 16; ++k)
+            mma_f16(d, da + k * (A_MN ? 2048 >> 4 : 32 >> 4), db + k * (B_MN ? 2048 >> 4 : 32 >> 4), p.what, i + k > 0);
+          mma_commit(&empty[stage]);
+        }
+        __syncwarp();
         if (++stage == S::STAGES) stage = 0, phase ^= 1;
       }
-      if (failed) break;
-      mma_commit(&ready[buf]);
+      if (ok && one) mma_commit(&ready[buf]);
+      __syncwarp();
       if (++buf == 2) buf = 0, buf_phase ^= 1;
     }
-    if (failed) {
+    if (!ok && one) {
       mma_commit(&idle);
       s4dev::mbar_wait(&idle, 0);
     }
@@ -219,7 +241,7 @@ __global__ void __launch_bounds__(256, 1)
     unsigned buf_phase = 0;
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
       const Tile at = tile_of(t);
-      if (!__all_sync(0xffffffffu, wait(&ready[buf], buf_phase))) break;
+      if (!wait_warp(&ready[buf], buf_phase)) break;
       fence_after();
       if (at.from < at.to)  // (a last piece may have fewer chunks than splits)
         ep(at.m * 128 + (wid & 3) * 32 + lane, at.n, at.split, tmem + ((uint32_t)(wid & 3) * 32 << 16) + buf * BN);
@@ -238,20 +260,24 @@ __global__ void __launch_bounds__(256, 1)
 }
 
 // ---- host side -------------------------------------------------------------------------------------
+// The driver's cuTensorMapEncodeTiled (null where it has none), asked for once.
+inline void* map_encoder() {
+  static void* const f = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r);
+    return e == cudaSuccess && r == cudaDriverEntryPointSuccess ? p : nullptr;
+  }();
+  return f;
+}
+
 // A 16-bit array [planes][rows][width] as boxes of 64 x `box_rows`; false where a map cannot have it.
 inline bool make_map(CUtensorMap* map, const void* p, bool bf16, long long width, long long rows, int planes, long long row,
                      long long plane, int box_rows) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  static const Encode encode = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<Encode>(f);
-  }();
+  const Encode encode = reinterpret_cast<Encode>(map_encoder());
   if (!encode) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, (cuuint64_t)planes};
   const cuuint64_t strides[2] = {(cuuint64_t)row * 2, (cuuint64_t)plane * 2};

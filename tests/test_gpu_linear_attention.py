@@ -149,10 +149,13 @@ def test_slices_of_a_projection(dt):
         q, k, v = wide_[..., left:].split([H * K, G * K, G * V], -1)
         q, k, v = q.unflatten(-1, (H, K)), k.unflatten(-1, (G, K)), v.unflatten(-1, (G, V))
         got = s4.s4_linear_attention_fwd(q, k, v, g)
-        assert torch.equal(got, s4.s4_linear_attention_fwd(q.contiguous(), k.contiguous(), v.contiguous(), g))
+        # rows that are not aligned to 16 bytes may go through another kernel: both are off from the definition by OUT at
+        # most, so from each other by twice that
+        far = 2 * OUT[got.dtype] if left else 0.0
+        close(got, to64(s4.s4_linear_attention_fwd(q.contiguous(), k.contiguous(), v.contiguous(), g)), "rows apart", far)
         # heads outermost
         t = [x.transpose(1, 2).contiguous().transpose(1, 2) for x in (q, k, v)]
-        assert torch.equal(got, s4.s4_linear_attention_fwd(*t, g))
+        close(got, to64(s4.s4_linear_attention_fwd(*t, g)), "heads outermost", far)
         # a broadcast key
         one = k[:, :, :1].expand(-1, -1, G, -1)
         assert torch.equal(s4.s4_linear_attention_fwd(q, one, v, g), s4.s4_linear_attention_fwd(q, one.contiguous(), v, g))
