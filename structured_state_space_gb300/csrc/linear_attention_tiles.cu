@@ -22,11 +22,12 @@ using s4impl::Walk;
 constexpr int kC = 128, kPasses = 3, kThreads = 384;
 
 struct Maps {
-  CUtensorMap a, b, c;
+  CUtensorMap a, b, c, out;  // (out: bfloat16 outputs whose strides a map can have)
 };
 struct Passes {
   Maps maps[kPasses];
   Walk w[kPasses];
+  bool by_map[kPasses];  // whether whole chunks of outputs go by their map
   int limit;
 };
 
@@ -34,9 +35,11 @@ template <int DK, int DV, int NK, bool STATE>
 struct Room {
   static constexpr int TA = kC * DK * 2, TC = kC * DV * 2, TM = DK * DV * 2;  // bytes of a tile
   static constexpr int SA = STATE ? 0 : DK == 64 ? 2 : 1, SB = DK == 64 || STATE ? 2 : 1;
-  static constexpr int SC = DK == 128 && DV == 128 && NK == 3 && !STATE ? 1 : 2;
+  static constexpr int SC = DK == 128 && DV == 128 && !STATE ? 1 : 2;
   static constexpr int A = 0, B = A + SA * TA, C = B + SB * TA, K = C + SC * TC, M = K + NK * TA;
-  static constexpr int BYTES = M + (STATE ? 0 : TM) + 1024;
+  // outputs go through shared memory where it has room for them
+  static constexpr bool STAGED = !STATE && M + TM + TC <= 224 * 1024;
+  static constexpr int O = M + (STATE ? 0 : TM), BYTES = O + (STAGED ? TC : 0) + 1024;
   // columns of tensor memory
   static constexpr int S = 0, O1 = 128, O2 = O1 + DV, D = O2 + DV, COLS = 512;
 };
@@ -94,6 +97,25 @@ __device__ __forceinline__ void put_row(void* out, long long at, int have, bool 
     else
       wr(static_cast<__nv_bfloat16*>(out) + at + x, from_f<__nv_bfloat16>(v));
   }
+}
+
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void* src, int x, int head, int t, int b) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(map),
+               "r"(s4dev::smem_u32(src)), "r"(x), "r"(head), "r"(t), "r"(b)
+               : "memory");
+}
+// Whether all of the first warpgroup's threads say so.
+__device__ __forceinline__ bool all_of(bool v) {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.and.pred q, 1, 128, p;\n selp.b32 %0, 1, 0, q;\n}"
+               : "=r"(r)
+               : "r"((uint32_t)v)
+               : "memory");
+  return r != 0;
+}
+// An arrival that orders no earlier writes (stores to global memory, on which it would wait).
+__device__ __forceinline__ void arrive_relaxed(unsigned long long* bar) {
+  asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(s4dev::smem_u32(bar)) : "memory");
 }
 
 // What all of a CTA's threads know of its walk.
@@ -170,8 +192,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   const int limit = ps.limit;
   const auto wait = [&](unsigned long long* bar, unsigned parity) {
     for (int it = 0; it < limit; it += 256) {
-      if (failed) return false;
       if (s4dev::mbar_wait(bar, parity & 1, limit - it < 256 ? limit - it : 256)) return true;
+      if (failed) return false;
     }
     failed = 1;
     return false;
@@ -295,16 +317,27 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       const int i = wid * 32 + lane;
       const uint32_t lanes = tmem + ((uint32_t)wid * 32 << 16);
       const float scale = w.scale;
-      const bool f32 = w.out_f32, vec = w.vec;
+      const bool f32 = w.out_f32, vec = w.vec, by_map = ps.by_map[blockIdx.z];
       const int dc = w.dc, chunks = sp.chunks;
       const long long row = w.out_row;
       const long long base = b * w.out_batch + h * w.out_head + i * row;
+      // The decays of 32 columns, the same for every chunk: from the thread's own row (with words that blank later tokens),
+      // and from the column of a block that is nearest to the rows behind it.
+      float2 own[16], off[16];
+      uint32_t mask[16];
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const int lag = REV ? 2 * x - lane : lane - 2 * x, next = REV ? lag + 1 : lag - 1;
+        own[x] = make_float2(tab[lag & 31], tab[next & 31]);
+        off[x] = make_float2(tab[REV ? 2 * x : 31 - 2 * x], tab[REV ? 2 * x + 1 : 30 - 2 * x]);
+        mask[x] = (lag >= 0 ? 0xffffu : 0u) | (next >= 0 ? 0xffff0000u : 0u);
+      }
       for (int k = 0; k < chunks; ++k) {
         const int t = start_of(k), n = sp.end - t < kC ? sp.end - t : kC;
-        if (!wait_warp(&s_ready, k)) break;
+        bool ok = wait_warp(&s_ready, k);
         fence_after();
 #pragma unroll 1
-        for (int jb = 0; jb < 4; ++jb) {
+        for (int jb = 0; jb < 4 && ok; ++jb) {
           uint32_t p[16];
           if (REV ? jb < wid : jb > wid) {
 #pragma unroll
@@ -315,23 +348,17 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
             if (jb == wid) {
 #pragma unroll
               for (int x = 0; x < 16; ++x) {
-                const int lag = REV ? 2 * x - lane : lane - 2 * x, next = REV ? lag + 1 : lag - 1;
-                p[x] = two_of<__nv_bfloat16>(lag >= 0 ? __uint_as_float(s[2 * x]) * tab[lag & 31] : 0.f,
-                                             next >= 0 ? __uint_as_float(s[2 * x + 1]) * tab[next & 31] : 0.f);
+                const float2 z = mul2(make_float2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])), own[x]);
+                p[x] = two_of<__nv_bfloat16>(z.x, z.y) & mask[x];
               }
             } else {
-              // lag = (distance to the block's nearest column) + (that column to j)
               const float f = power(g, REV ? 32 * jb - i : i - 32 * jb - 31);
               const float2 far = make_float2(f, f);
 #pragma unroll
-              for (int x = 0; x < 32; x += 4) {
-                const float4 q = *reinterpret_cast<const float4*>(tab + (REV ? x : 28 - x));
-                const float2 lo = REV ? make_float2(q.x, q.y) : make_float2(q.w, q.z);
-                const float2 hi = REV ? make_float2(q.z, q.w) : make_float2(q.y, q.x);
-                const float2 u = mul2(make_float2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), mul2(far, lo));
-                const float2 v = mul2(make_float2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), mul2(far, hi));
-                p[x / 2] = two_of<__nv_bfloat16>(u.x, u.y);
-                p[x / 2 + 1] = two_of<__nv_bfloat16>(v.x, v.y);
+              for (int x = 0; x < 16; ++x) {
+                const float2 z =
+                    mul2(mul2(make_float2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])), off[x]), far);
+                p[x] = two_of<__nv_bfloat16>(z.x, z.y);
               }
             }
             if (REV && 32 * jb + 32 > n) {
@@ -349,7 +376,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         fence_before();
         __syncwarp();
         if (lane == 0) arrive(&p_ready);
-        if (!wait_warp(&o_ready, k)) break;
+        ok = ok && wait_warp(&o_ready, k);
+        const bool staged = R::STAGED && by_map && n == kC;
+        // (the chunk before has been read from the staging rows)
+        if (staged && threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        if (!all_of(ok)) break;  // all four warps or none: they meet again below
         fence_after();
         const float e = power(g, REV ? n - 1 - i : i) * scale;
         const float2 ee = make_float2(e, e), sc = make_float2(scale, scale);
@@ -358,18 +389,37 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         for (int c = 0; c < DV; c += 32) {
           uint32_t u[32], v[32];
           tmem_ld32(lanes + R::O1 + c, lanes + R::O2 + c, u, v);
+          if (c + 32 == DV) {
+            fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_relaxed(&o_free);
+          }
           if (i >= n || c >= dc) continue;
           float2 f[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x)
             f[x] = fma2(make_float2(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1])), ee,
                         mul2(make_float2(__uint_as_float(u[2 * x]), __uint_as_float(u[2 * x + 1])), sc));
-          put_row(w.out, at + c, dc - c, f32, vec, f);
+          if (staged) {
+#pragma unroll
+            for (int x = 0; x < 16; x += 4)
+              *reinterpret_cast<uint4*>(smem + R::O + c / 64 * 16384 + i * 128 + ((c % 64 / 8 + x / 4) ^ (i & 7)) * 16) =
+                  make_uint4(two_of<__nv_bfloat16>(f[x].x, f[x].y), two_of<__nv_bfloat16>(f[x + 1].x, f[x + 1].y),
+                             two_of<__nv_bfloat16>(f[x + 2].x, f[x + 2].y), two_of<__nv_bfloat16>(f[x + 3].x, f[x + 3].y));
+          } else {
+            put_row(w.out, at + c, dc - c, f32, vec, f);
+          }
         }
-        fence_before();
-        __syncwarp();
-        if (lane == 0) arrive(&o_free);
+        if (staged) {
+          s4dev::fence_proxy_async();
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          if (threadIdx.x == 0) {
+            for (int c = 0; c < dc; c += 64) tma_store_4d(&maps.out, smem + R::O + c / 64 * 16384, c, h, t, b);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        }
       }
+      if (R::STAGED && threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     };
     if (w.reverse)
       rows(std::true_type{});
@@ -388,10 +438,19 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       const float by = w.segs > 1 ? 1.f : w.init_scale * (rev ? 1.f : power(g, 1));
       const float* from = STATE || !row ? nullptr : w.segs > 1 ? local + r : init ? init + r * w.init_r : nullptr;
       const long long step = w.segs > 1 ? w.da : w.init_c;
+      if (from && step == 1 && dc % 4 == 0 && (uintptr_t)from % 16 == 0) {
 #pragma unroll
-      for (int c = 0; c < DV / 2; ++c)
-        m[c] = make_float2(from && 2 * c < dc ? by * rd(from + 2 * c * step) : 0.f,
-                           from && 2 * c + 1 < dc ? by * rd(from + (2 * c + 1) * step) : 0.f);
+        for (int c = 0; c < DV / 2; c += 2) {
+          float v[4] = {};
+          if (2 * c < dc) ld_f<float, 4>(from + 2 * c, 4, true, v);
+          m[c] = make_float2(by * v[0], by * v[1]), m[c + 1] = make_float2(by * v[2], by * v[3]);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < DV / 2; ++c)
+          m[c] = make_float2(from && 2 * c < dc ? by * rd(from + 2 * c * step) : 0.f,
+                             from && 2 * c + 1 < dc ? by * rd(from + (2 * c + 1) * step) : 0.f);
+      }
     }
     // the state as the right operand of A M: rows of 128 bytes, swizzled
     const auto put = [&] {
@@ -483,10 +542,18 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     if (row && to && !failed) {
       const long long step = STATE ? w.da : w.init_c;
       const float by = STATE ? 1.f : w.last_scale;
+      if (step == 1 && dc % 4 == 0 && (uintptr_t)to % 16 == 0) {
 #pragma unroll
-      for (int c = 0; c < DV / 2; ++c) {
-        if (2 * c < dc) wr(to + 2 * c * step, by * m[c].x);
-        if (2 * c + 1 < dc) wr(to + (2 * c + 1) * step, by * m[c].y);
+        for (int c = 0; c < DV / 2; c += 2) {
+          const float v[4] = {by * m[c].x, by * m[c].y, by * m[c + 1].x, by * m[c + 1].y};
+          if (2 * c < dc) st_f<float, 4>(to + 2 * c, 4, true, v);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < DV / 2; ++c) {
+          if (2 * c < dc) wr(to + 2 * c * step, by * m[c].x);
+          if (2 * c + 1 < dc) wr(to + (2 * c + 1) * step, by * m[c].y);
+        }
       }
     }
   }
@@ -499,6 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
 }
 
 // ---- host side -----------------------------------------------------------------------------------------
+bool stride_ok(long long v, int n) { return n == 1 || (v > 0 && v % 8 == 0 && v < (1ll << 38)); }
 bool make_map(CUtensorMap* map, const In& x, int width, int heads, int L, int batch) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -548,8 +616,8 @@ S4_OOB_COUNTER(oob_linear_attention_tiles)
 bool tiles_take(const Walk& w, int dtype) {
   if (dtype != S4_BF16 || w.da > 128 || w.dc > 128) return false;
   const auto ok = [&](const In& x) {
-    const auto stride = [](long long v, int n) { return n == 1 || (v > 0 && v % 8 == 0 && v < (1ll << 38)); };
-    return (uintptr_t)x.p % 16 == 0 && (x.head == 0 || stride(x.head, w.H / x.per)) && stride(x.row, w.L) && stride(x.batch, w.batch);
+    return (uintptr_t)x.p % 16 == 0 && (x.head == 0 || stride_ok(x.head, w.H / x.per)) && stride_ok(x.row, w.L) &&
+           stride_ok(x.batch, w.batch);
   };
   return ok(w.a) && ok(w.b) && ok(w.c);
 }
@@ -598,6 +666,9 @@ cudaError_t launch_tiles(const Walk* w, int passes, int dtype, St st, cudaStream
     if (!make_map(&m.a, p.a, p.da, p.H / p.a.per, p.L, p.batch) || !make_map(&m.b, p.b, p.da, p.H / p.b.per, p.L, p.batch) ||
         !make_map(&m.c, p.c, p.dc, p.H / p.c.per, p.L, p.batch))
       return cudaErrorInvalidValue;
+    const In out{p.out, p.out_batch, p.out_row, p.out_head, 1};
+    ps.by_map[i] = !p.out_f32 && (uintptr_t)p.out % 16 == 0 && stride_ok(p.out_head, p.H) && stride_ok(p.out_row, p.L) &&
+                   stride_ok(p.out_batch, p.batch) && make_map(&m.out, out, p.dc, p.H, p.L, p.batch);
 #ifdef S4_BOUNDS_CHECK
     x.add(p.out, e, false, true, p.dc, p.batch, p.out_batch, p.L, p.out_row, p.H, p.out_head);
     x.in(p.init, 4, (long long)p.H * p.da * p.dc, p.slots);

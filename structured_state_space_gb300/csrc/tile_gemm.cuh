@@ -142,8 +142,8 @@ __global__ void __launch_bounds__(256, 1)
   const int tiles = p.tiles_m * p.tiles_n * p.splits;
   const auto wait = [&](unsigned long long* bar, unsigned parity) {
     for (int it = 0; it < p.limit; it += 256) {
-      if (failed) return false;
       if (s4dev::mbar_wait(bar, parity, p.limit - it < 256 ? p.limit - it : 256)) return true;
+      if (failed) return false;
     }
     failed = 1;
     return false;
