@@ -19,7 +19,7 @@ using namespace s4mma;
 using s4impl::In;
 using s4impl::Walk;
 
-constexpr int kC = 128, kPasses = 3, kThreads = 384;
+constexpr int kC = 128, kSlot = 32, kPasses = 3, kThreads = 512;
 
 struct Maps {
   CUtensorMap a, b, c, out;  // (out: bfloat16 outputs whose strides a map can have)
@@ -34,9 +34,11 @@ struct Passes {
 template <int DK, int DV, int NK, bool STATE>
 struct Room {
   static constexpr int TA = kC * DK * 2, TC = kC * DV * 2, TM = DK * DV * 2;  // bytes of a tile
-  static constexpr int SA = STATE ? 0 : DK == 64 ? 2 : 1, SB = DK == 64 || STATE ? 2 : 1;
+  static constexpr int SA = STATE ? 0 : DK == 64 || (DV == 128 && NK == 2) ? 2 : 1, SB = DK == 64 || STATE ? 2 : 1;
   static constexpr int SC = DK == 128 && DV == 128 && !STATE ? 1 : 2;
-  static constexpr int A = 0, B = A + SA * TA, C = B + SB * TA, K = C + SC * TC, M = K + NK * TA;
+  // scaled keys in slots of 32 tokens
+  static constexpr int TK = kSlot * DK * 2, SK = DK == 128 && DV == 128 && !STATE ? 2 : 4;
+  static constexpr int A = 0, B = A + SA * TA, C = B + SB * TA, K = C + SC * TC, M = K + SK * NK * TK;
   // outputs go through shared memory where it has room for them
   static constexpr bool STAGED = !STATE && M + TM + TC <= 224 * 1024;
   static constexpr int O = M + (STATE ? 0 : TM), BYTES = O + (STAGED ? TC : 0) + 1024;
@@ -44,10 +46,11 @@ struct Room {
   static constexpr int S = 0, O1 = 128, O2 = O1 + DV, D = O2 + DV, COLS = 512;
 };
 
-__device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t what, bool add) {
+__device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t what, bool add, uint32_t one) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(what), "r"((uint32_t)add)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(what), "r"((uint32_t)add), "r"(one)
       : "memory");
 }
 // 16 columns of the warp's lanes.
@@ -133,8 +136,9 @@ __device__ __forceinline__ Span span_of(const Walk& w, int seg, int len) {
   return p;
 }
 
-// 384 threads: warps 0 to 3 form P and put out O, warps 4 to 7 scale the keys and hold the state (with more registers: 232
-// a thread of the 3 x 168 that the three warpgroups start with), warp 8 brings the tiles, warp 9 issues the products.  Every wait is bounded; where one gives up the CTA records a stall,
+// 512 threads: warps 0 to 3 form P and put out O, warps 4 to 7 hold the state (with more registers: 208 a thread of the
+// 4 x 128 that the four warpgroups start with), warp 8 brings the tiles, warp 9 issues the products, warps 12 to
+// 15 scale the keys.  Every wait is bounded; where one gives up the CTA records a stall,
 // waits for its copies and products in flight, frees its tensor memory and leaves.
 template <int DK, int DV, int NK, bool STATE>
 __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constant__ Passes ps, s4impl::St st) {
@@ -143,7 +147,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   const Maps& maps = ps.maps[blockIdx.z];
   extern __shared__ char raw[];
   __shared__ unsigned long long full_a[2], full_b[2], full_c[2], empty_a[2], empty_b[2], empty_c[2];
-  __shared__ unsigned long long s_ready, p_ready, keys_ready, d_ready, m_ready, m_free, o_ready, o_free, idle;
+  __shared__ unsigned long long keys_ready[4], keys_free[4];
+  __shared__ unsigned long long s_ready, p_ready, c_clean, d_ready, d_free, m_ready, m_free, o_ready, o_free, idle;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int failed;
   __shared__ __align__(16) float tab[32];
@@ -177,8 +182,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       s4dev::mbar_init(&full_a[i], 1), s4dev::mbar_init(&full_b[i], 1), s4dev::mbar_init(&full_c[i], 1);
       s4dev::mbar_init(&empty_a[i], 1), s4dev::mbar_init(&empty_b[i], STATE ? 4 : 5), s4dev::mbar_init(&empty_c[i], 1);
     }
-    s4dev::mbar_init(&s_ready, 1), s4dev::mbar_init(&p_ready, 4), s4dev::mbar_init(&keys_ready, 4);
-    s4dev::mbar_init(&d_ready, 1), s4dev::mbar_init(&m_ready, 4), s4dev::mbar_init(&m_free, 1);
+    for (int i = 0; i < 4; ++i) s4dev::mbar_init(&keys_ready[i], 4), s4dev::mbar_init(&keys_free[i], 1);
+    s4dev::mbar_init(&s_ready, 1), s4dev::mbar_init(&p_ready, 4), s4dev::mbar_init(&c_clean, 4);
+    s4dev::mbar_init(&d_ready, 1), s4dev::mbar_init(&d_free, 4), s4dev::mbar_init(&m_ready, 4), s4dev::mbar_init(&m_free, 1);
     s4dev::mbar_init(&o_ready, 1), s4dev::mbar_init(&o_free, 4), s4dev::mbar_init(&idle, 1);
     failed = 0;
     s4dev::fence_mbar_init();
@@ -188,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = tmem_slot;
+  constexpr uint32_t tmem = 0;  // where an allocation of all the columns begins
   const int limit = ps.limit;
   const auto wait = [&](unsigned long long* bar, unsigned parity) {
     for (int it = 0; it < limit; it += 256) {
@@ -201,12 +207,17 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   const auto wait_warp = [&](unsigned long long* bar, unsigned parity) {
     return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
   };
+  // two barriers, tested at once
+  const auto wait_both = [&](unsigned long long* x, unsigned px, unsigned long long* y, unsigned py) {
+    const bool a = s4dev::mbar_wait(x, px & 1, 1), b = s4dev::mbar_wait(y, py & 1, 1);
+    return __all_sync(0xffffffffu, (a || wait(x, px)) && (b || wait(y, py))) != 0;
+  };
   // chunk k of the walk begins at token `start`
   const auto start_of = [&](int k) { return sp.begin + kC * (w.reverse ? sp.chunks - 1 - k : k); };
   const auto updates = [&](int k) { return STATE || k + 1 < sp.chunks || (sp.last && last != nullptr); };
 
-  if (wid >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+  if (wid >= 8 && wid < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (wid == 8 && elected()) {
     int na = 0, nb = 0, nc = 0;  // tiles asked for
     for (int k = 0; k < sp.chunks; ++k) {
@@ -248,66 +259,69 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     constexpr uint32_t kS = instruction(true, false, false, 128, 128), kAM = instruction(true, false, true, 128, DV),
                        kD = instruction(true, true, true, 128, DV), kPC = instruction(true, false, true, 128, DV);
     const uint32_t base = s4dev::smem_u32(smem);
-    const bool one = elected();
+    const uint32_t one = elected();
+    int slots = 0, blanked = 0;  // of keys used, chunks that were not full
     for (int k = 0; k < sp.chunks; ++k) {
       const int sb = k % R::SB, sc = k % R::SC;
       const uint64_t dc = tile_desc(base + R::C + sc * R::TC, 16384);
       const uint64_t da = tile_desc(base + R::A + (STATE ? 0 : (k % (R::SA ? R::SA : 1)) * R::TA), 16);
       if constexpr (!STATE) {
-        if (!wait_warp(&full_b[sb], k / R::SB) || !wait_warp(&full_a[k % R::SA], k / R::SA)) break;
+        if (!wait_both(&full_b[sb], k / R::SB, &full_a[k % R::SA], k / R::SA)) break;
         fence_after();
-        if (one) {
-          // S: over the width, 64 at a time
-          const uint64_t db = tile_desc(base + R::B + sb * R::TA, 16);
+        // S: over the width, 64 at a time
+        const uint64_t db = tile_desc(base + R::B + sb * R::TA, 16);
 #pragma unroll
-          for (int i = 0; i < DK / 16; ++i) {
-            const uint32_t at = (i / 4 * 16384 + i % 4 * 32) >> 4;
-            mma_f16(tmem + R::S, da + at, db + at, kS, i > 0);
-          }
-          mma_commit(&s_ready);
-          mma_commit(&empty_b[sb]);
+        for (int i = 0; i < DK / 16; ++i) {
+          const uint32_t at = (i / 4 * 16384 + i % 4 * 32) >> 4;
+          mma_f16(R::S, da + at, db + at, kS, i > 0, one);
         }
+        mma_commit(&s_ready, one);
+        mma_commit(&empty_b[sb], one);
       }
       const bool up = updates(k);
-      // scaled keys (and the last rows of C, where a chunk is not full) are in place
-      if (!wait_warp(&keys_ready, k)) break;
-      if (!wait_warp(&full_c[sc], k / R::SC)) break;
-      fence_after();
-      if (one && up) {
+      // where a chunk is not full, C's last rows have been blanked
+      if (sp.end - start_of(k) < kC && !wait_warp(&c_clean, blanked++)) break;
+      if (!(up ? wait_both(&full_c[sc], k / R::SC, &d_free, k + 1) : wait_warp(&full_c[sc], k / R::SC))) break;
+      if (up) {
+        bool ok = true;
+        for (int j = 0; j < kC / kSlot; ++j, ++slots) {
+          const int sk = slots % R::SK;
+          ok = wait_warp(&keys_ready[sk], slots / R::SK);
+          if (!ok) break;
+          fence_after();
 #pragma unroll
-        for (int p = 0; p < NK; ++p) {
-          // widths of 64: 64 rows of the state, and the same once more
-          const uint64_t dk = tile_desc(base + R::K + p * R::TA, DK == 64 ? 0 : 16384);
+          for (int p = 0; p < NK; ++p) {
+            // widths of 64: 64 rows of the state, and the same once more
+            const uint64_t dk = tile_desc(base + R::K + (sk * NK + p) * R::TK, DK == 64 ? 0 : kSlot * 128);
 #pragma unroll
-          for (int i = 0; i < kC / 16; ++i) mma_f16(tmem + R::D, dk + i * (2048 >> 4), dc + i * (2048 >> 4), kD, p + i > 0);
+            for (int i = 0; i < kSlot / 16; ++i)
+              mma_f16(R::D, dk + i * (2048 >> 4), dc + (j * (kSlot / 16) + i) * (2048 >> 4), kD, j + p + i > 0, one);
+          }
+          mma_commit(&keys_free[sk], one);
         }
-        mma_commit(&d_ready);
-        if (STATE) mma_commit(&empty_c[sc]);
+        if (!ok) break;
+        mma_commit(&d_ready, one);
+        if (STATE) mma_commit(&empty_c[sc], one);
       }
       if constexpr (!STATE) {
-        if (!wait_warp(&m_ready, k) || !wait_warp(&o_free, k + 1)) break;
+        if (!wait_both(&m_ready, k, &o_free, k + 1)) break;
         fence_after();
-        if (one) {
-          const uint64_t dm = tile_desc(base + R::M, DK * 128);
+        const uint64_t dm = tile_desc(base + R::M, DK * 128);
 #pragma unroll
-          for (int i = 0; i < DK / 16; ++i)
-            mma_f16(tmem + R::O2, da + ((i / 4 * 16384 + i % 4 * 32) >> 4), dm + i * (2048 >> 4), kAM, i > 0);
-          mma_commit(&m_free);
-          mma_commit(&empty_a[k % R::SA]);
-        }
+        for (int i = 0; i < DK / 16; ++i)
+          mma_f16(R::O2, da + ((i / 4 * 16384 + i % 4 * 32) >> 4), dm + i * (2048 >> 4), kAM, i > 0, one);
+        mma_commit(&m_free, one);
+        mma_commit(&empty_a[k % R::SA], one);
         if (!wait_warp(&p_ready, k)) break;
         fence_after();
-        if (one) {
 #pragma unroll
-          for (int i = 0; i < kC / 16; ++i) mma_tmem_a(tmem + R::O1, tmem + R::S + i * 8, dc + i * (2048 >> 4), kPC, i > 0);
-          mma_commit(&o_ready);
-          mma_commit(&empty_c[sc]);
-        }
+        for (int i = 0; i < kC / 16; ++i) mma_tmem_a(R::O1, R::S + i * 8, dc + i * (2048 >> 4), kPC, i > 0, one);
+        mma_commit(&o_ready, one);
+        mma_commit(&empty_c[sc], one);
       }
-      __syncwarp();
     }
-    if (failed && one) {
-      mma_commit(&idle);
+    if (failed) {
+      mma_commit(&idle, one);
       s4dev::mbar_wait(&idle, 0);
     }
     }
@@ -321,15 +335,13 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       const int dc = w.dc, chunks = sp.chunks;
       const long long row = w.out_row;
       const long long base = b * w.out_batch + h * w.out_head + i * row;
-      // The decays of 32 columns, the same for every chunk: from the thread's own row (with words that blank later tokens),
-      // and from the column of a block that is nearest to the rows behind it.
-      float2 own[16], off[16];
+      // The decays within the thread's own 32 columns, the same for every chunk, and words that blank later tokens.
+      float2 own[16];
       uint32_t mask[16];
 #pragma unroll
       for (int x = 0; x < 16; ++x) {
         const int lag = REV ? 2 * x - lane : lane - 2 * x, next = REV ? lag + 1 : lag - 1;
         own[x] = make_float2(tab[lag & 31], tab[next & 31]);
-        off[x] = make_float2(tab[REV ? 2 * x : 31 - 2 * x], tab[REV ? 2 * x + 1 : 30 - 2 * x]);
         mask[x] = (lag >= 0 ? 0xffffu : 0u) | (next >= 0 ? 0xffff0000u : 0u);
       }
       for (int k = 0; k < chunks; ++k) {
@@ -355,10 +367,15 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
               const float f = power(g, REV ? 32 * jb - i : i - 32 * jb - 31);
               const float2 far = make_float2(f, f);
 #pragma unroll
-              for (int x = 0; x < 16; ++x) {
-                const float2 z =
-                    mul2(mul2(make_float2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])), off[x]), far);
-                p[x] = two_of<__nv_bfloat16>(z.x, z.y);
+              for (int x = 0; x < 16; x += 2) {
+                // the block's nearest column to each of its columns
+                const float4 q = *reinterpret_cast<const float4*>(tab + (REV ? 2 * x : 28 - 2 * x));
+                const float2 u = mul2(mul2(make_float2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])),
+                                           REV ? make_float2(q.x, q.y) : make_float2(q.w, q.z)), far);
+                const float2 v = mul2(mul2(make_float2(__uint_as_float(s[2 * x + 2]), __uint_as_float(s[2 * x + 3])),
+                                           REV ? make_float2(q.z, q.w) : make_float2(q.y, q.x)), far);
+                p[x] = two_of<__nv_bfloat16>(u.x, u.y);
+                p[x + 1] = two_of<__nv_bfloat16>(v.x, v.y);
               }
             }
             if (REV && 32 * jb + 32 > n) {
@@ -425,9 +442,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       rows(std::true_type{});
     else
       rows(std::false_type{});
-  } else if (wid >= 4) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-    const int r = (wid - 4) * 32 + lane;  // a row of the state, a token of the keys
+  } else if (wid >= 4 && wid < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int r = (wid - 4) * 32 + lane;  // a row of the state
     const uint32_t lanes = tmem + ((uint32_t)(wid - 4) * 32 << 16);
     const bool row = r < w.da, rev = w.reverse;
     const int dc = w.dc, chunks = sp.chunks;
@@ -467,63 +484,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       __syncwarp();
       if (lane == 0) arrive(&m_ready);
     };
+    if (!STATE) put();
     for (int k = 0; k < chunks; ++k) {
-      const int t = start_of(k), n = sp.end - t < kC ? sp.end - t : kC, sb = k % R::SB, sc = k % R::SC;
-      const bool up = updates(k), at_end = sp.last && k + 1 == chunks;
-      const int less = !STATE && at_end && !rev ? 1 : 0;
-      if (!STATE) {
-        if (k > 0 && !wait_warp(&m_free, k - 1)) break;
-        put();
-      }
-      if (!wait_warp(&full_b[sb], k / R::SB)) break;
-      if (up) {
-        const float f = r < n ? power(g, rev ? r + 1 : n - less - r) : 0.f;
-        const float2 ff = make_float2(f, f);
-        const char* from = smem + R::B + sb * R::TA + r * 128;
-        char* to = smem + R::K + r * 128;
-#pragma unroll 1
-        for (int c = 0; c < DK / 8; c += 4, from += c % 8 ? 0 : 16384, to += c % 8 ? 0 : 16384) {
-          // four packs are on their way at once (the compiler cannot move loads over the stores)
-          uint4 v[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) v[y] = *reinterpret_cast<const uint4*>(from + ((((c & 4) + y) ^ (r & 7)) * 16));
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            if (r >= n) v[y] = make_uint4(0, 0, 0, 0);  // behind the last token: anything, NaN too
-            const unsigned x[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
-            unsigned o[NK][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float2 z = mul2(make_float2(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xffff0000u)), ff);
-#pragma unroll
-              for (int p = 0; p < NK; ++p) {
-                o[p][j] = two_of<__nv_bfloat16>(z.x, z.y);
-                if (p + 1 < NK)
-                  z = fma2(make_float2(__uint_as_float(o[p][j] << 16), __uint_as_float(o[p][j] & 0xffff0000u)),
-                           make_float2(-1.f, -1.f), z);
-              }
-            }
-#pragma unroll
-            for (int p = 0; p < NK; ++p)
-              *reinterpret_cast<uint4*>(to + p * R::TA + (((c & 4) + y) ^ (r & 7)) * 16) =
-                  make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
-          }
-        }
-      }
-      __syncwarp();
-      if (lane == 0) arrive(&empty_b[sb]);
-      if (n < kC) {
-        if (!wait_warp(&full_c[sc], k / R::SC)) break;
-        if (r >= n)
-#pragma unroll 1
-          for (int c = 0; c < DV / 8; ++c)
-            *reinterpret_cast<uint4*>(smem + R::C + sc * R::TC + c / 8 * 16384 + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-      }
-      s4dev::fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) arrive(&keys_ready);
-      if (!up) continue;
-      if (!wait_warp(&d_ready, k)) break;  // (only the last chunk may have no update)
+      if (!updates(k)) break;  // (only the last chunk may have no update)
+      const int t = start_of(k), n = sp.end - t < kC ? sp.end - t : kC;
+      const int less = !STATE && sp.last && k + 1 == chunks && !rev ? 1 : 0;
+      if (!wait_warp(&d_ready, k)) break;
       fence_after();
       const float by = expm1f(g * (float)(n - less));
       const float2 bb = make_float2(by, by);
@@ -537,6 +503,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                               make_float2(__uint_as_float(u[2 * x]), __uint_as_float(u[2 * x + 1])));
       }
       fence_before();
+      __syncwarp();
+      if (lane == 0) arrive(&d_free);
+      if (!STATE && k + 1 < chunks) {
+        if (!wait_warp(&m_free, k)) break;
+        put();
+      }
     }
     float* to = STATE ? local + cells + r : last && sp.last ? last + r * w.init_r : nullptr;  // (STATE: the next segment's)
     if (row && to && !failed) {
@@ -555,6 +527,74 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
           if (2 * c + 1 < dc) wr(to + (2 * c + 1) * step, by * m[c].y);
         }
       }
+    }
+  } else if (wid >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    // The keys of a chunk, scaled: four lanes to a token (odd tokens take the halves of 64 columns in the other
+    // order, so that the lanes' packs lie in different banks).
+    const int r = (wid - 12) * 32 + lane, chunks = sp.chunks;
+    const bool rev = w.reverse;
+    int slots = 0;
+    bool ok = true;
+    for (int k = 0; k < chunks; ++k) {
+      const int t = start_of(k), n = sp.end - t < kC ? sp.end - t : kC, sb = k % R::SB, sc = k % R::SC;
+      const int less = !STATE && sp.last && k + 1 == chunks && !rev ? 1 : 0;
+      if (n < kC) {
+        // first of all: the products wait for it before they free the keys' slots
+        if (!wait_warp(&full_c[sc], k / R::SC)) break;
+        if (r >= n)
+#pragma unroll 1
+          for (int c = 0; c < DV / 8; ++c)
+            *reinterpret_cast<uint4*>(smem + R::C + sc * R::TC + c / 8 * 16384 + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+        s4dev::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) arrive(&c_clean);
+      }
+      if (!wait_warp(&full_b[sb], k / R::SB)) break;
+      if (updates(k)) {
+        const int token = r >> 2, quarter = r & 3;
+#pragma unroll 1
+        for (int j = 0; j < kC; j += kSlot, ++slots) {
+          const int sk = slots % R::SK, at = j + token;
+          ok = wait_warp(&keys_free[sk], slots / R::SK + 1);
+          if (!ok) break;
+          const float f = at < n ? power(g, rev ? at + 1 : n - less - at) : 0.f;
+          const float2 ff = make_float2(f, f);
+          const char* from = smem + R::B + sb * R::TA + at * 128;
+          char* to = smem + R::K + sk * NK * R::TK + token * 128;
+          const int c0 = ((quarter + 4 * (token & 1)) ^ (token & 7)) * 16, c1 = ((quarter + 4 * (~token & 1)) ^ (token & 7)) * 16;
+          uint4 v[DK / 32];
+#pragma unroll
+          for (int y = 0; y < DK / 32; ++y) v[y] = *reinterpret_cast<const uint4*>(from + y / 2 * 16384 + (y & 1 ? c1 : c0));
+#pragma unroll
+          for (int y = 0; y < DK / 32; ++y) {
+            if (at >= n) v[y] = make_uint4(0, 0, 0, 0);  // behind the last token: anything, NaN too
+            const unsigned x[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
+            unsigned o[NK][4];
+#pragma unroll
+            for (int w4 = 0; w4 < 4; ++w4) {
+              float2 z = mul2(make_float2(__uint_as_float(x[w4] << 16), __uint_as_float(x[w4] & 0xffff0000u)), ff);
+#pragma unroll
+              for (int p = 0; p < NK; ++p) {
+                o[p][w4] = two_of<__nv_bfloat16>(z.x, z.y);
+                if (p + 1 < NK)
+                  z = fma2(make_float2(__uint_as_float(o[p][w4] << 16), __uint_as_float(o[p][w4] & 0xffff0000u)),
+                           make_float2(-1.f, -1.f), z);
+              }
+            }
+#pragma unroll
+            for (int p = 0; p < NK; ++p)
+              *reinterpret_cast<uint4*>(to + p * R::TK + y / 2 * (kSlot * 128) + (y & 1 ? c1 : c0)) =
+                  make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
+          }
+          s4dev::fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) arrive(&keys_ready[sk]);
+        }
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) arrive(&empty_b[sb]);
     }
   }
   __syncwarp();

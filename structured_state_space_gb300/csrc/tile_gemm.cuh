@@ -37,16 +37,22 @@ __device__ __forceinline__ void tmem_alloc(uint32_t* slot, int cols) {
 __device__ __forceinline__ void tmem_free(uint32_t at, int cols) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols));
 }
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t what, bool add) {
+// Products and commits are issued by the one lane of a warp that has `one` set.  They are predicated, not under a branch:
+// the warp stays together and its descriptors in uniform registers (under a branch an issue took about twice as long).
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t what, bool add, uint32_t one) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(what), "r"((uint32_t)add)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(what), "r"((uint32_t)add), "r"(one)
       : "memory");
 }
 // Arrives at the barrier when all products issued so far are done.
-__device__ __forceinline__ void mma_commit(unsigned long long* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(s4dev::smem_u32(bar))
-               : "memory");
+__device__ __forceinline__ void mma_commit(unsigned long long* bar, uint32_t one) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(s4dev::smem_u32(bar)),
+      "r"(one)
+      : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -138,7 +144,7 @@ __global__ void __launch_bounds__(256, 1)
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = S::COLS == 512 ? 0 : tmem_slot;  // (all of it begins at 0)
   const int tiles = p.tiles_m * p.tiles_n * p.splits;
   const auto wait = [&](unsigned long long* bar, unsigned parity) {
     for (int it = 0; it < p.limit; it += 256) {
@@ -203,7 +209,7 @@ __global__ void __launch_bounds__(256, 1)
     }
   } else if (wid == 1) {
     // the warp stays together, so that the descriptors are uniform; one lane issues
-    const bool one = elected();
+    const uint32_t one = elected();
     int stage = 0, buf = 0;
     unsigned phase = 0, buf_phase = 0;
     bool ok = true;
@@ -217,23 +223,19 @@ __global__ void __launch_bounds__(256, 1)
         ok = wait_warp(&full[stage], phase);
         if (!ok) break;
         fence_after();
-        if (one) {
-          const uint32_t a = s4dev::smem_u32(smem + stage * S::STAGE), b = a + S::A;
-          const uint64_t da = tile_desc(a, A_MN ? 8192 : 16), db = tile_desc(b, B_MN ? 8192 : 16);
+        const uint32_t a = s4dev::smem_u32(smem) + stage * S::STAGE, b = a + S::A;
+        const uint64_t da = tile_desc(a, A_MN ? 8192 : 16), db = tile_desc(b, B_MN ? 8192 : 16);
 #pragma unroll
-          for (int k = 0; k < kBK / 16; ++k)
-            mma_f16(d, da + k * (A_MN ? 2048 >> 4 : 32 >> 4), db + k * (B_MN ? 2048 >> 4 : 32 >> 4), p.what, i + k > 0);
-          mma_commit(&empty[stage]);
-        }
-        __syncwarp();
+        for (int k = 0; k < kBK / 16; ++k)
+          mma_f16(d, da + k * (A_MN ? 2048 >> 4 : 32 >> 4), db + k * (B_MN ? 2048 >> 4 : 32 >> 4), p.what, i + k > 0, one);
+        mma_commit(&empty[stage], one);
         if (++stage == S::STAGES) stage = 0, phase ^= 1;
       }
-      if (ok && one) mma_commit(&ready[buf]);
-      __syncwarp();
+      if (ok) mma_commit(&ready[buf], one);
       if (++buf == 2) buf = 0, buf_phase ^= 1;
     }
-    if (!ok && one) {
-      mma_commit(&idle);
+    if (!ok) {
+      mma_commit(&idle, one);
       s4dev::mbar_wait(&idle, 0);
     }
   } else if (wid >= 4) {
