@@ -11,6 +11,7 @@ namespace {
 using namespace s4blk;
 using s4impl::In;
 using s4impl::Walk;
+using s4impl::Walks;
 
 constexpr int kThreads = 128, kCols = 64;  // per CTA: 4 warps, columns of c
 
@@ -84,7 +85,8 @@ __device__ __forceinline__ void load_rows(__nv_bfloat16* s, const T* p, long lon
 // through M, in registers (warp w has rows w D/4 on).  D: da rounded up.  STATE: only M, from zero, for
 // the segments after it.
 template <typename T, int D, int C, bool STATE>
-__global__ void __launch_bounds__(kThreads) walk_kernel(Walk w, St st) {
+__global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ Walks ws, St st) {
+  const Walk& w = ws.w[blockIdx.z];
   constexpr int NP = kTerms<T>, NK = NP == 1 ? 2 : NP;  // terms of inputs, of scaled keys
   constexpr int RW = C / 16, CW = 4 / RW, NT = kCols / 8 / CW;  // warps along tokens and columns, column tiles each
   constexpr int MT = D / 64;                                    // tiles of 16 rows of M per warp
@@ -94,6 +96,7 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(Walk w, St st) {
   __nv_bfloat16 *sb = sa + NP * SA, *sc = sb + NP * SA, *sm = sc + NP * SC;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, g4 = lane >> 2, t4 = lane & 3;
   const int nc = (w.dc + kCols - 1) / kCols;
+  if (blockIdx.x >= (unsigned)(w.batch * w.H * nc)) return;  // (the other walks have more columns)
   const int c0 = (int)(blockIdx.x % nc) * kCols, h = (int)(blockIdx.x / nc) % w.H, b = (int)(blockIdx.x / nc) / w.H;
   const int seg = blockIdx.y, cols = w.dc - c0 < kCols ? w.dc - c0 : kCols;
   record_gen(st);
@@ -106,13 +109,7 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(Walk w, St st) {
   if (!STATE) {
     // padding, in the order of memory
     const int from = q.len > begin ? q.len : begin, to = begin + w.seg < w.L ? begin + w.seg : w.L;
-    for (long long i = threadIdx.x; i < (long long)(to - from) * cols; i += kThreads) {
-      const long long at = b * w.out_batch + (from + i / cols) * w.out_row + h * w.out_head + c0 + i % cols;
-      if (w.out_f32)
-        wr(static_cast<float*>(w.out) + at, 0.f);
-      else
-        wr(static_cast<T*>(w.out) + at, from_f<T>(0.f));
-    }
+    blank_rows<T>(w, b, h, c0, cols, from, to);
   }
   const long long cells = (long long)w.da * w.dc;
   const float* init = w.init && q.slot >= 0 ? w.init + (q.slot * w.H + h) * cells : nullptr;
@@ -328,7 +325,8 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(Walk w, St st) {
 
 // What each segment starts from, in their order: slot 0 the state on entry, slot s + 1, which holds what segment s
 // adds, that and what comes before.
-__global__ void __launch_bounds__(256) join_kernel(Walk w, St st) {
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Walks ws, St st) {
+  const Walk& w = ws.w[blockIdx.z];
   const long long cells = (long long)w.da * w.dc, i = (long long)blockIdx.x * 256 + threadIdx.x;
   const int h = blockIdx.y % w.H, b = blockIdx.y / w.H;
   if (i >= cells) return;
@@ -352,17 +350,23 @@ __global__ void __launch_bounds__(256) join_kernel(Walk w, St st) {
 }
 
 // Gradients of shared heads: part [batch][L][H][d], summed over each group's heads in their order.
+struct Shared {
+  const float* part;
+  void* out;
+  long long batch, row, head;
+  int d;
+};
 template <typename T>
-__global__ void __launch_bounds__(256) group_sum_kernel(const float* part, T* out, long long batch_stride, long long row,
-                                                        long long head, int batch, int L, int H, int G, int d) {
-  const long long n = (long long)batch * L * G * d, each = H / G;
+__global__ void __launch_bounds__(256) group_sum_kernel(Shared k, Shared v, int batch, int L, int H, int G) {
+  const Shared& x = blockIdx.y ? v : k;
+  const long long n = (long long)batch * L * G * x.d, each = H / G;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
-    const int c = (int)(i % d), gr = (int)(i / d % G);
-    const long long token = i / d / G;
-    const float* p = part + (token * H + gr * each) * d + c;
+    const int c = (int)(i % x.d), gr = (int)(i / x.d % G);
+    const long long token = i / x.d / G;
+    const float* p = x.part + (token * H + gr * each) * x.d + c;
     float v = 0.f;
-    for (int j = 0; j < each; ++j) v += rd(p + (long long)j * d);
-    wr(out + (token / L) * batch_stride + (token % L) * row + gr * head + c, from_f<T>(v));
+    for (int j = 0; j < each; ++j) v += rd(p + (long long)j * x.d);
+    wr(static_cast<T*>(x.out) + (token / L) * x.batch + (token % L) * x.row + gr * x.head + c, from_f<T>(v));
   }
 }
 
@@ -453,15 +457,15 @@ cudaError_t step_t(const s4_linear_attention_args& a, St st, cudaStream_t s) {
 }
 
 // ---- host side -----------------------------------------------------------------------------------
-// Segments of a sequence: as many as give each SM three CTAs, of 256 tokens or more.
+// Segments of a sequence: as many as give each SM three CTAs, of 64 tokens or more.
 int segments(long long walks, int L) {
-  const long long want = (3ll * s4impl::num_sms() + walks - 1) / walks, most = (L + 255) / 256;
+  const long long want = (3ll * s4impl::num_sms() + walks - 1) / walks, most = (L + 63) / 64;
   const long long n = want < most ? want : most;
   return (int)(n < 1 ? 1 : n);
 }
 int segment_tokens(int L, int segs) { return ((L + segs - 1) / segs + 63) / 64 * 64; }
 size_t local_bytes(int batch, int L, int H, int da, int dc) {
-  int segs = segments((long long)batch * H * ((dc + kCols - 1) / kCols), L);
+  int segs = segments((long long)batch * H, L);
   for (int passes = 1; passes <= 3; ++passes) {  // whichever kernels the strides allow
     const int n = da <= 128 && dc <= 128 ? s4impl::tile_segments((long long)batch * H, L, passes) : 1;
     segs = n > segs ? n : segs;
@@ -470,52 +474,74 @@ size_t local_bytes(int batch, int L, int H, int da, int dc) {
 }
 
 template <typename T, int D>
-cudaError_t walk_d(const Walk& w, St st, cudaStream_t s) {
+cudaError_t walk_d(const Walks& ws, int n, St st, cudaStream_t s) {
   constexpr int C = kTerms<T> == 3 ? 32 : 64, bytes = kWalkBytes<T, D, C>;
-  const unsigned walks = (unsigned)((long long)w.batch * w.H * ((w.dc + kCols - 1) / kCols));
+  unsigned walks = 0;
+  for (int i = 0; i < n; ++i) {
+    const unsigned own = (unsigned)((long long)ws.w[i].batch * ws.w[i].H * ((ws.w[i].dc + kCols - 1) / kCols));
+    walks = own > walks ? own : walks;
+  }
   constexpr auto kernel = walk_kernel<T, D, C, false>;
   allow_shared<kernel>(bytes);
-  if (w.segs > 1) {
+  const int segs = ws.w[0].segs;
+  if (segs > 1) {
     constexpr auto state = walk_kernel<T, D, C, true>;
     allow_shared<state>(bytes);
     {
       s4impl::TimedLaunch tl("linear_attention", s);
-      state<<<dim3(walks, w.segs - 1), kThreads, bytes, s>>>(w, st);
+      state<<<dim3(walks, segs - 1, n), kThreads, bytes, s>>>(ws, st);
     }
-    if (const cudaError_t err = s4impl::launch_join(w, st, s); err != cudaSuccess) return err;
+    if (const cudaError_t err = s4impl::launch_join(ws, n, st, s); err != cudaSuccess) return err;
   }
   s4impl::TimedLaunch tl("linear_attention", s);
-  kernel<<<dim3(walks, w.segs), kThreads, bytes, s>>>(w, st);
+  kernel<<<dim3(walks, segs, n), kThreads, bytes, s>>>(ws, st);
   return cudaGetLastError();
 }
+// n walks over the same sequences and heads, in one launch.
 template <typename T>
-cudaError_t walk_t(Walk w, St st, cudaStream_t s) {
+cudaError_t walk_t(Walks ws, int n, St st, cudaStream_t s) {
   constexpr int code = std::is_same_v<T, float> ? S4_F32 : std::is_same_v<T, __half> ? S4_F16 : S4_BF16;
-  if (s4impl::tiles_take(w, code)) return s4impl::launch_tiles(&w, 1, code, st, s);
-  w.segs = segments((long long)w.batch * w.H * ((w.dc + kCols - 1) / kCols), w.L);
-  w.seg = segment_tokens(w.L, w.segs);
-  w.segs = (w.L + w.seg - 1) / w.seg;
-  const int e = sizeof(T), eo = w.out_f32 ? 4 : e;
-  const auto ok = [&](const In& x) { return vec_ok(x.p, e, 16, x.batch, x.row) && vec_ok(x.p, e, 16, x.head); };
-  w.vec = ok(w.a) && ok(w.b) && ok(w.c) && vec_ok(w.out, eo, 2 * eo, w.out_batch, w.out_row) &&
-          vec_ok(w.out, eo, 2 * eo, w.out_head);
+  bool tiles = true;
+  for (int i = 0; i < n; ++i)
+    tiles = tiles && s4impl::tiles_take(ws.w[i], code) && (ws.w[i].da <= 64) == (ws.w[0].da <= 64) &&
+            (ws.w[i].dc <= 64) == (ws.w[0].dc <= 64);
+  if (tiles) return s4impl::launch_tiles(ws, n, code, st, s);
+  int most = 0, least_cols = ws.w[0].dc;
+  for (int i = 0; i < n; ++i) {
+    most = ws.w[i].da > most ? ws.w[i].da : most;
+    least_cols = ws.w[i].dc < least_cols ? ws.w[i].dc : least_cols;
+  }
+  const int want = segments((long long)n * ws.w[0].batch * ws.w[0].H * ((least_cols + kCols - 1) / kCols), ws.w[0].L);
 #ifdef S4_BOUNDS_CHECK
   s4impl::Extents x{};
-  const auto add = [&](const In& i, int d) {
-    x.add(i.p, e, true, false, d, w.batch, i.batch, w.L, i.row, (w.H + i.per - 1) / i.per, i.head);
-  };
-  add(w.a, w.da), add(w.b, w.da), add(w.c, w.dc);
-  x.add(w.out, eo, false, true, w.dc, w.batch, w.out_batch, w.L, w.out_row, w.H, w.out_head);
-  x.in(w.log_decay, 4, w.H);
-  x.in(w.lengths, 4, w.batch);
-  x.in(w.index, 4, w.batch);
-  x.in(w.init, 4, (long long)w.H * w.da * w.dc, w.slots);
-  x.out(w.last, 4, (long long)w.H * w.da * w.dc, w.slots);
-  if (w.segs > 1) x.scratch(w.local, 4, (long long)w.batch * w.H * w.segs * w.da * w.dc);
+  x.in(ws.w[0].log_decay, 4, ws.w[0].H);
+  x.in(ws.w[0].lengths, 4, ws.w[0].batch);
+  x.in(ws.w[0].index, 4, ws.w[0].batch);
+#endif
+  for (int i = 0; i < n; ++i) {
+    Walk& w = ws.w[i];
+    w.seg = segment_tokens(w.L, want);
+    w.segs = (w.L + w.seg - 1) / w.seg;
+    const int e = sizeof(T), eo = w.out_f32 ? 4 : e;
+    const auto ok = [&](const In& x) { return vec_ok(x.p, e, 16, x.batch, x.row) && vec_ok(x.p, e, 16, x.head); };
+    w.vec = ok(w.a) && ok(w.b) && ok(w.c) && vec_ok(w.out, eo, 2 * eo, w.out_batch, w.out_row) &&
+            vec_ok(w.out, eo, 2 * eo, w.out_head);
+#ifdef S4_BOUNDS_CHECK
+    const auto add = [&](const In& i, int d) {
+      x.add(i.p, e, true, false, d, w.batch, i.batch, w.L, i.row, (w.H + i.per - 1) / i.per, i.head);
+    };
+    add(w.a, w.da), add(w.b, w.da), add(w.c, w.dc);
+    x.add(w.out, eo, false, true, w.dc, w.batch, w.out_batch, w.L, w.out_row, w.H, w.out_head);
+    x.in(w.init, 4, (long long)w.H * w.da * w.dc, w.slots);
+    x.out(w.last, 4, (long long)w.H * w.da * w.dc, w.slots);
+    if (w.segs > 1) x.scratch(w.local, 4, (long long)w.batch * w.H * w.segs * w.da * w.dc);
+#endif
+  }
+#ifdef S4_BOUNDS_CHECK
   if (const cudaError_t err = set_extents(x, s); err != cudaSuccess) return err;
 #endif
-  if (w.da <= 64) return walk_d<T, 64>(w, st, s);
-  return w.da <= 128 ? walk_d<T, 128>(w, st, s) : walk_d<T, 256>(w, st, s);
+  if (most <= 64) return walk_d<T, 64>(ws, n, st, s);
+  return most <= 128 ? walk_d<T, 128>(ws, n, st, s) : walk_d<T, 256>(ws, n, st, s);
 }
 
 In in_of(const s4_heads& r, int per) { return {r.p, r.batch, r.row, r.head, per}; }
@@ -539,7 +565,8 @@ cudaError_t fwd_t(const s4_linear_attention_args& a, St st, cudaStream_t s) {
 #endif
     return step_t<T>(a, st, s);
   }
-  Walk w{};
+  Walks ws{};
+  Walk& w = ws.w[0];
   w.a = in_of(a.q, 1), w.b = in_of(a.k, a.H / a.G), w.c = in_of(a.v, a.H / a.G);
   w.out = a.o.p, w.out_batch = a.o.batch, w.out_row = a.o.row, w.out_head = a.o.head;
   w.log_decay = a.log_decay, w.lengths = a.lengths, w.index = a.index;
@@ -547,12 +574,11 @@ cudaError_t fwd_t(const s4_linear_attention_args& a, St st, cudaStream_t s) {
   w.local = reinterpret_cast<float*>(static_cast<char*>(a.ws) + s4impl::kStatusBytes);
   w.scale = a.scale, w.init_scale = w.last_scale = 1.f;
   w.batch = a.batch, w.L = a.L, w.H = a.H, w.da = a.K, w.dc = a.V, w.slots = a.slots;
-  return walk_t<T>(w, st, s);
+  return walk_t<T>(ws, 1, st, s);
 }
 
 template <typename T>
 cudaError_t bwd_t(const s4_linear_attention_bwd_args& a, St st, cudaStream_t s) {
-  constexpr int code = std::is_same_v<T, float> ? S4_F32 : std::is_same_v<T, __half> ? S4_F16 : S4_BF16;
   const int each = a.H / a.G;
   char* at = static_cast<char*>(a.ws) + s4impl::kStatusBytes;
   const auto take = [&](size_t bytes) {
@@ -560,58 +586,63 @@ cudaError_t bwd_t(const s4_linear_attention_bwd_args& a, St st, cudaStream_t s) 
     at += bytes;
     return p;
   };
-  Walk w[3]{};
-  for (Walk& x : w) {
+  Walks ws{};
+  // dk and dv first: they go through the same tokens in the same order, so what one reads the other finds in the L2
+  Walk &dk = ws.w[0], &dv = ws.w[1], &dq = ws.w[2];
+  for (Walk& x : ws.w) {
     x.log_decay = a.log_decay, x.lengths = a.lengths;
     x.scale = a.scale, x.last_scale = a.scale;
     x.batch = a.batch, x.L = a.L, x.H = a.H, x.slots = a.batch;
   }
-  // dq: forward over (dout, v, k), the state transposed
-  w[0].a = in_of(a.dout, 1), w[0].b = in_of(a.v, each), w[0].c = in_of(a.k, each);
-  w[0].out = a.dq.p, w[0].out_batch = a.dq.batch, w[0].out_row = a.dq.row, w[0].out_head = a.dq.head;
-  w[0].da = a.V, w[0].dc = a.K, w[0].init = a.state0, w[0].init_r = 1, w[0].init_c = a.V, w[0].init_scale = 1.f;
-  // dk: from the end over (v, dout, q), transposed
-  w[1].a = in_of(a.v, each), w[1].b = in_of(a.dout, 1), w[1].c = in_of(a.q, 1);
-  w[1].da = a.V, w[1].dc = a.K, w[1].init = a.dstate, w[1].init_r = 1, w[1].init_c = a.V;
+  // dk: from the end over (v, dout, q), the state transposed
+  dk.a = in_of(a.v, each), dk.b = in_of(a.dout, 1), dk.c = in_of(a.q, 1);
+  dk.da = a.V, dk.dc = a.K, dk.init = a.dstate, dk.init_r = 1, dk.init_c = a.V;
   // dv: from the end over (k, q, dout); it leaves the state's gradient
-  w[2].a = in_of(a.k, each), w[2].b = in_of(a.q, 1), w[2].c = in_of(a.dout, 1);
-  w[2].da = a.K, w[2].dc = a.V, w[2].init = a.dstate, w[2].init_r = a.V, w[2].init_c = 1, w[2].last = a.dstate0;
-  float* part[3]{};
+  dv.a = in_of(a.k, each), dv.b = in_of(a.q, 1), dv.c = in_of(a.dout, 1);
+  dv.da = a.K, dv.dc = a.V, dv.init = a.dstate, dv.init_r = a.V, dv.init_c = 1, dv.last = a.dstate0;
+  // dq: forward over (dout, v, k), the state transposed
+  dq.a = in_of(a.dout, 1), dq.b = in_of(a.v, each), dq.c = in_of(a.k, each);
+  dq.out = a.dq.p, dq.out_batch = a.dq.batch, dq.out_row = a.dq.row, dq.out_head = a.dq.head;
+  dq.da = a.V, dq.dc = a.K, dq.init = a.state0, dq.init_r = 1, dq.init_c = a.V, dq.init_scale = 1.f;
+  Shared shared[2];
   for (int i = 0; i < 3; ++i) {
-    w[i].local = take(local_bytes(a.batch, a.L, a.H, w[i].da, w[i].dc));
-    if (i == 0) continue;
-    const s4_heads_out& out = i == 1 ? a.dk : a.dv;
-    const int d = w[i].dc;
-    w[i].reverse = true, w[i].init_scale = 1.f / a.scale;
+    Walk& w = ws.w[i];
+    w.local = take(local_bytes(a.batch, a.L, a.H, w.da, w.dc));
+    if (i == 2) continue;
+    const s4_heads_out& out = i == 0 ? a.dk : a.dv;
+    const int d = w.dc;
+    w.reverse = true, w.init_scale = 1.f / a.scale;
     if (each > 1) {
-      w[i].out = part[i] = take(s4impl::align256(sizeof(float) * (size_t)a.batch * a.L * a.H * d));
-      w[i].out_f32 = true, w[i].out_head = d, w[i].out_row = (long long)a.H * d, w[i].out_batch = w[i].out_row * a.L;
+      float* part = take(s4impl::align256(sizeof(float) * (size_t)a.batch * a.L * a.H * d));
+      w.out = part, w.out_f32 = true, w.out_head = d, w.out_row = (long long)a.H * d, w.out_batch = w.out_row * a.L;
+      shared[i] = {part, out.p, out.batch, out.row, out.head, d};
     } else {
-      w[i].out = out.p, w[i].out_batch = out.batch, w[i].out_row = out.row, w[i].out_head = out.head;
+      w.out = out.p, w.out_batch = out.batch, w.out_row = out.row, w.out_head = out.head;
     }
   }
-  cudaError_t err = cudaSuccess;
-  if (s4impl::tiles_take(w[0], code) && s4impl::tiles_take(w[1], code) && s4impl::tiles_take(w[2], code) &&
-      (a.K <= 64) == (a.V <= 64))
-    err = s4impl::launch_tiles(w, 3, code, st, s);
-  else
-    for (int i = 0; i < 3 && err == cudaSuccess; ++i) err = walk_t<T>(w[i], st, s);
-  for (int i = 1; i < 3 && err == cudaSuccess && each > 1; ++i) {
-    const s4_heads_out& out = i == 1 ? a.dk : a.dv;
-    const int d = w[i].dc;
-#ifdef S4_BOUNDS_CHECK
-    s4impl::Extents x{};
-    x.in(part[i], 4, (long long)a.batch * a.L * a.H * d);
-    x.add(out.p, sizeof(T), false, true, d, a.batch, out.batch, a.L, out.row, a.G, out.head);
-    if (const cudaError_t e = set_extents(x, s); e != cudaSuccess) return e;
-#endif
-    const long long n = ((long long)a.batch * a.L * a.G * d + 255) / 256, most = 16ll * s4impl::num_sms();
-    s4impl::TimedLaunch tl("linear_attention", s);
-    group_sum_kernel<T><<<(unsigned)(n < most ? n : most), 256, 0, s>>>(part[i], static_cast<T*>(out.p), out.batch, out.row,
-                                                                      out.head, a.batch, a.L, a.H, a.G, d);
-    err = cudaGetLastError();
+  cudaError_t err;
+  if ((a.K <= 64) == (a.V <= 64) || std::is_same_v<T, float> || std::is_same_v<T, __half>) {
+    err = walk_t<T>(ws, 3, st, s);
+  } else {  // two shapes of tiles
+    Walks two = ws, one{};
+    two.w[1] = dq;
+    one.w[0] = dv;
+    err = walk_t<T>(two, 2, st, s);
+    if (err == cudaSuccess) err = walk_t<T>(one, 1, st, s);
   }
-  return err;
+  if (err != cudaSuccess || each == 1) return err;
+#ifdef S4_BOUNDS_CHECK
+  s4impl::Extents x{};
+  for (int i = 0; i < 2; ++i) {
+    x.in(shared[i].part, 4, (long long)a.batch * a.L * a.H * shared[i].d);
+    x.add(shared[i].out, sizeof(T), false, true, shared[i].d, a.batch, shared[i].batch, a.L, shared[i].row, a.G, shared[i].head);
+  }
+  if (const cudaError_t e = set_extents(x, s); e != cudaSuccess) return e;
+#endif
+  const long long n = ((long long)a.batch * a.L * a.G * (a.K > a.V ? a.K : a.V) + 255) / 256, most = 16ll * s4impl::num_sms();
+  s4impl::TimedLaunch tl("linear_attention", s);
+  group_sum_kernel<T><<<dim3((unsigned)(n < most ? n : most), 2), 256, 0, s>>>(shared[0], shared[1], a.batch, a.L, a.H, a.G);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -626,9 +657,10 @@ size_t linear_attention_scratch(int batch, int L, int H, int K, int V) {
   return L == 1 ? 0 : local_bytes(batch, L, H, K, V);
 }
 
-cudaError_t launch_join(const Walk& w, St st, cudaStream_t s) {
+cudaError_t launch_join(const Walks& ws, int n, St st, cudaStream_t s) {
   s4impl::TimedLaunch tl("linear_attention", s);
-  join_kernel<<<dim3((unsigned)((w.da * w.dc + 255) / 256), w.batch * w.H), 256, 0, s>>>(w, st);
+  const Walk& w = ws.w[0];  // (all have as many cells)
+  join_kernel<<<dim3((unsigned)((w.da * w.dc + 255) / 256), w.batch * w.H, n), 256, 0, s>>>(ws, st);
   return cudaGetLastError();
 }
 

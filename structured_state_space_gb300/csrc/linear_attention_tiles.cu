@@ -18,6 +18,7 @@ using namespace s4blk;
 using namespace s4mma;
 using s4impl::In;
 using s4impl::Walk;
+using s4impl::Walks;
 
 constexpr int kC = 128, kSlot = 32, kPasses = 3, kThreads = 512;
 
@@ -26,7 +27,7 @@ struct Maps {
 };
 struct Passes {
   Maps maps[kPasses];
-  Walk w[kPasses];
+  Walks walks;
   bool by_map[kPasses];  // whether whole chunks of outputs go by their map
   int limit;
 };
@@ -34,7 +35,7 @@ struct Passes {
 template <int DK, int DV, int NK, bool STATE>
 struct Room {
   static constexpr int TA = kC * DK * 2, TC = kC * DV * 2, TM = DK * DV * 2;  // bytes of a tile
-  static constexpr int SA = STATE ? 0 : DK == 64 || (DV == 128 && NK == 2) ? 2 : 1, SB = DK == 64 || STATE ? 2 : 1;
+  static constexpr int SA = STATE ? 0 : DK == 64 ? 2 : 1, SB = DK == 64 || STATE || (DV == 128 && NK == 2) ? 2 : 1;
   static constexpr int SC = DK == 128 && DV == 128 && !STATE ? 1 : 2;
   // scaled keys in slots of 32 tokens
   static constexpr int TK = kSlot * DK * 2, SK = DK == 128 && DV == 128 && !STATE ? 2 : 4;
@@ -143,7 +144,7 @@ __device__ __forceinline__ Span span_of(const Walk& w, int seg, int len) {
 template <int DK, int DV, int NK, bool STATE>
 __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constant__ Passes ps, s4impl::St st) {
   using R = Room<DK, DV, NK, STATE>;
-  const Walk& w = ps.w[blockIdx.z];
+  const Walk& w = ps.walks.w[blockIdx.z];
   const Maps& maps = ps.maps[blockIdx.z];
   extern __shared__ char raw[];
   __shared__ unsigned long long full_a[2], full_b[2], full_c[2], empty_a[2], empty_b[2], empty_c[2];
@@ -165,13 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   if (!STATE) {
     // padding, in the order of memory
     const int from = q.len > seg * w.seg ? q.len : seg * w.seg, to = (seg + 1) * w.seg < w.L ? (seg + 1) * w.seg : w.L;
-    for (long long i = threadIdx.x; i < (long long)(to - from) * w.dc; i += kThreads) {
-      const long long at = b * w.out_batch + (from + i / w.dc) * w.out_row + h * w.out_head + i % w.dc;
-      if (w.out_f32)
-        wr(static_cast<float*>(w.out) + at, 0.f);
-      else
-        wr(static_cast<__nv_bfloat16*>(w.out) + at, from_f<__nv_bfloat16>(0.f));
-    }
+    blank_rows<__nv_bfloat16>(w, b, h, 0, w.dc, from, to);
     if (q.len == 0 && last && seg == 0)
       for (int i = threadIdx.x; i < cells; i += kThreads) wr(last + i, init ? rd(init + i) : 0.f);
   }
@@ -624,7 +619,7 @@ bool make_map(CUtensorMap* map, const In& x, int width, int heads, int L, int ba
 
 template <int DK, int DV, int NK>
 cudaError_t launch(const Passes& ps, int passes, St st, cudaStream_t s) {
-  const Walk& w = ps.w[0];
+  const Walk& w = ps.walks.w[0];
   const unsigned walks = (unsigned)(w.batch * w.H);
   if (w.segs > 1) {
     using R = Room<DK, DV, NK, true>;
@@ -634,8 +629,7 @@ cudaError_t launch(const Passes& ps, int passes, St st, cudaStream_t s) {
       s4impl::TimedLaunch tl("linear_attention", s);
       state<<<dim3(walks, w.segs - 1, passes), kThreads, R::BYTES, s>>>(ps, st);
     }
-    for (int i = 0; i < passes; ++i)
-      if (const cudaError_t err = s4impl::launch_join(ps.w[i], st, s); err != cudaSuccess) return err;
+    if (const cudaError_t err = s4impl::launch_join(ps.walks, passes, st, s); err != cudaSuccess) return err;
   }
   using R = Room<DK, DV, NK, false>;
   constexpr auto kernel = tiles_kernel<DK, DV, NK, false>;
@@ -680,10 +674,12 @@ int tile_segments(long long walks, int L, int passes) {
   return best;
 }
 
-cudaError_t launch_tiles(const Walk* w, int passes, int dtype, St st, cudaStream_t s) {
+cudaError_t launch_tiles(const Walks& ws, int passes, int dtype, St st, cudaStream_t s) {
   static_assert(sizeof(Passes) <= 4096, "kernel parameters");
   Passes ps{};
   ps.limit = wait_limit();
+  ps.walks = ws;
+  const Walk* w = ws.w;
   const int segs = tile_segments((long long)w->batch * w->H, w->L, passes);
   const int seg = ((w->L + kC - 1) / kC + segs - 1) / segs * kC;
   bool returned = false;
@@ -694,8 +690,7 @@ cudaError_t launch_tiles(const Walk* w, int passes, int dtype, St st, cudaStream
   x.in(w->index, 4, w->batch);
 #endif
   for (int i = 0; i < passes; ++i) {
-    Walk& p = ps.w[i];
-    p = w[i];
+    Walk& p = ps.walks.w[i];
     for (In* x : {&p.a, &p.b, &p.c})
       if (x->head == 0) x->per = p.H;  // one head broadcast to all (a map has no strides of 0)
     p.seg = seg, p.segs = (p.L + seg - 1) / seg, p.from_start = true;
