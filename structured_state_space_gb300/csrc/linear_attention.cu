@@ -415,16 +415,31 @@ __global__ void __launch_bounds__(256) step_kernel(s4_linear_attention_args a, i
   }
   __syncthreads();
   if (c < a.V) {
-#pragma unroll 8
-    for (int r = rg; r < a.K; r += RG) {
-      float x[V] = {};
-      if (s) ld_f<float, V>(s + (long long)r * a.V + c, V, true, x);
+    // 16 rows are on their way at once
+    constexpr int N = 16;
+    for (int r0 = rg; r0 < a.K; r0 += N * RG) {
+      Pack<float, V> x[N];
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        x[j] = fmaf(sk[r], v[j], fmaf(x[j], by, x[j]));
-        sum[j] = fmaf(sq[r], x[j], sum[j]);
+      for (int i = 0; i < N; ++i) {
+        const int r = r0 + i * RG;
+        if (s && r < a.K)
+          x[i] = ld_whole<float, V>(s + (long long)r * a.V + c);
+        else
+          x[i].zero();
       }
-      if (to) st_f<float, V>(to + (long long)r * a.V + c, V, true, x);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int r = r0 + i * RG;
+        if (r >= a.K) continue;
+        float u[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float old = x[i].get(j);
+          u[j] = fmaf(sk[r], v[j], fmaf(old, by, old));
+          sum[j] = fmaf(sq[r], u[j], sum[j]);
+        }
+        if (to) st_whole<float, V>(to + (long long)r * a.V + c, u);
+      }
     }
   }
 #pragma unroll

@@ -11,8 +11,8 @@ constexpr int kMaxThreads = 512;  // of the CTA that holds a row
 
 // K sums over the group that holds a row: a warp, or the CTA's warps.  `red` has a slot per warp;
 // two sets of them alternate so that one barrier per round is enough.
-template <int MAX, int K>
-__device__ __forceinline__ void group_sums(float (&v)[K], float (&red)[2][2][32], int& phase) {
+template <int MAX, int K, int KR>
+__device__ __forceinline__ void group_sums(float (&v)[K], float (&red)[2][KR][32], int& phase) {
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
   if constexpr (MAX > 128) {
@@ -55,13 +55,13 @@ __device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
 // The rows that a group has on their way: with AHEAD, a row's packs are copied into slots of the
 // thread's own (two sets of them) while the row before is worked on; else they are read
 // when they are needed.  [2][NT][threads] packs of T, then [2][NR][threads] of R.
-template <typename T, typename R, int V, int NV, int NT, int NR, bool AHEAD>
+template <typename T, typename R, int V, int NV, int NT, int NR, bool AHEAD, int SETS = 2>
 struct Rows {
   Pack<T, V>* st;
   Pack<R, V>* sr;
   __device__ __forceinline__ Rows(char* smem)
       : st(reinterpret_cast<Pack<T, V>*>(smem) + threadIdx.x),
-        sr(reinterpret_cast<Pack<R, V>*>(smem + 2 * NT * NV * Pack<T, V>::BYTES * blockDim.x) + threadIdx.x) {}
+        sr(reinterpret_cast<Pack<R, V>*>(smem + SETS * NT * NV * Pack<T, V>::BYTES * blockDim.x) + threadIdx.x) {}
   __device__ __forceinline__ void fetch_t(int stage, int which, int i, const T* p) {
     fetch_whole<T, V>(st + ((stage * NT + which) * NV + i) * blockDim.x, p);
   }
@@ -78,8 +78,8 @@ struct Rows {
   }
 };
 
-template <typename T, typename R, int V, int NT, int NR>
-constexpr int kRowBytes = 2 * (NT * Pack<T, V>::BYTES + NR * Pack<R, V>::BYTES);  // per thread
+template <typename T, typename R, int V, int NT, int NR, int SETS = 2>
+constexpr int kRowBytes = SETS * (NT * Pack<T, V>::BYTES + NR * Pack<R, V>::BYTES);  // per thread
 
 // A row's group: a warp up to 32 packs of channels per pack a thread holds, a CTA beyond.
 struct Shape {

@@ -36,43 +36,46 @@ __device__ __forceinline__ unsigned long long turns_of(double freq) {
 // P pairs as they lie: two packs of P (halves) or one of 2 P elements (interleaved).  P = 1 takes any
 // alignment: single elements.
 template <typename T, int P, bool PAIRS>
-__device__ __forceinline__ void ld_pairs_of(const T* x, int R, int i, float (&a)[P], float (&b)[P]) {
-  if constexpr (PAIRS && P == 1) {
-    a[0] = to_f(rd(x + 2 * i)), b[0] = to_f(rd(x + 2 * i + 1));
-  } else if constexpr (PAIRS) {
-    const Pack<T, 2 * P> v = ld_whole<T, 2 * P>(x + 2 * i);
-#pragma unroll
-    for (int j = 0; j < P; ++j) a[j] = v.get(2 * j), b[j] = v.get(2 * j + 1);
-  } else {
-    const Pack<T, P> u = ld_whole<T, P>(x + i), v = ld_whole<T, P>(x + R + i);
-#pragma unroll
-    for (int j = 0; j < P; ++j) a[j] = u.get(j), b[j] = v.get(j);
+struct Turned {
+  static constexpr bool ONE = PAIRS && P > 1;  // one pack of both
+  Pack<T, ONE ? 2 * P : P> u, v;
+  __device__ __forceinline__ void load(const T* x, int R, int i) {
+    if constexpr (ONE) {
+      u = ld_whole<T, 2 * P>(x + 2 * i);
+    } else {
+      u = ld_whole<T, P>(x + (PAIRS ? 2 * i : i));
+      v = ld_whole<T, P>(x + (PAIRS ? 2 * i + 1 : R + i));
+    }
   }
-}
-template <typename T, int P, bool PAIRS>
-__device__ __forceinline__ void st_pairs_of(T* x, int R, int i, const float (&a)[P], const float (&b)[P]) {
-  if constexpr (PAIRS && P == 1) {
-    wr(x + 2 * i, from_f<T>(a[0])), wr(x + 2 * i + 1, from_f<T>(b[0]));
-  } else if constexpr (PAIRS) {
-    float v[2 * P];
+  __device__ __forceinline__ float a(int j) const { return ONE ? u.get(2 * j) : u.get(j); }
+  __device__ __forceinline__ float b(int j) const { return ONE ? u.get(2 * j + 1) : v.get(j); }
+  __device__ __forceinline__ static void store(T* x, int R, int i, const float (&a)[P], const float (&b)[P]) {
+    if constexpr (ONE) {
+      float w[2 * P];
 #pragma unroll
-    for (int j = 0; j < P; ++j) v[2 * j] = a[j], v[2 * j + 1] = b[j];
-    st_whole<T, 2 * P>(x + 2 * i, v);
-  } else {
-    st_whole<T, P>(x + i, a);
-    st_whole<T, P>(x + R + i, b);
+      for (int j = 0; j < P; ++j) w[2 * j] = a[j], w[2 * j + 1] = b[j];
+      st_whole<T, 2 * P>(x + 2 * i, w);
+    } else {
+      st_whole<T, P>(x + (PAIRS ? 2 * i : i), a);
+      st_whole<T, P>(x + (PAIRS ? 2 * i + 1 : R + i), b);
+    }
   }
-}
+};
 
-// Threads: `units` per token and head lane (packs of P pairs, then packs of W copied channels), `lanes`
-// head lanes per token, tokens.  Tokens in steps of the grid.
+constexpr int kAtOnce = 2;  // heads whose channels a thread has on their way (4 leaves room for fewer threads: 64 us, not 54)
+
+// Threads: `units` per token and head lane (packs of P pairs, and packs of W copied channels), `lanes`
+// head lanes per token, `per` tokens.  Tokens in steps of the grid.
 template <typename T, int P, int W, bool PAIRS>
 __global__ void __launch_bounds__(256) rotary_kernel(s4_rotary_args a, int units, int lanes, int per) {
-  const int u = threadIdx.x % units, rest = threadIdx.x / units, lane = rest % lanes, sub = rest / lanes;
+  // first the threads that turn, then those that copy: a warp has one kind or the other
+  const int turned = a.R / P, heads = a.H + a.G, split = turned * lanes * per;
+  const bool copy = (int)threadIdx.x >= split;
+  const int id = threadIdx.x - (copy ? split : 0), mine = copy ? units - turned : turned;
+  if (mine == 0) return;
+  const int u = id % mine, lane = id / mine % lanes, sub = id / mine / lanes;
   if (sub >= per) return;
-  const int turned = (a.R + P - 1) / P, heads = a.H + a.G;
-  const bool copy = u >= turned;
-  const int at = copy ? 2 * a.R + (u - turned) * W : u * P;
+  const int at = copy ? 2 * a.R + u * W : u * P;
   unsigned long long turn[P];
   if (!copy) {
 #pragma unroll
@@ -81,39 +84,66 @@ __global__ void __launch_bounds__(256) rotary_kernel(s4_rotary_args a, int units
   const long long tokens = (long long)a.batch * a.L;
   for (long long token = (long long)blockIdx.x * per + sub; token < tokens; token += (long long)gridDim.x * per) {
     const long long b = token / a.L, t = token - b * a.L;
-    float c[P], s[P];
-    if (!copy) {
-      const long long pos = a.positions ? (long long)rd(a.positions + b * a.positions_batch + t) : t;
-#pragma unroll
-      for (int j = 0; j < P; ++j) {
-        // the signed fraction of a turn, in half turns
-        const unsigned long long f = (unsigned long long)pos * turn[j];
-        sincospif((float)(int)(f >> 32) * 0x1p-31f, &s[j], &c[j]);
-        s[j] *= a.inverse ? -a.amplitude : a.amplitude;
-        c[j] *= a.amplitude;
-      }
-    }
-#pragma unroll 4
-    for (int h = lane; h < heads; h += lanes) {
+    const auto place = [&](int h, const T*& x, T*& y) {
       const bool query = h < a.H;
       const s4_heads& in = query ? a.q : a.k;
       const s4_heads_out& out = query ? a.q_out : a.k_out;
       const int head = query ? h : h - a.H;
-      const T* x = static_cast<const T*>(in.p) + b * in.batch + t * in.row + head * in.head;
-      T* y = static_cast<T*>(out.p) + b * out.batch + t * out.row + head * out.head;
-      if (copy) {
-        if (x != y) st_pack<T, W>(y + at, W, true, ld_whole<T, W>(x + at));
-        continue;
-      }
-      float p[P], q[P];
-      ld_pairs_of<T, P, PAIRS>(x, a.R, at, p, q);
+      x = static_cast<const T*>(in.p) + b * in.batch + t * in.row + head * in.head;
+      y = static_cast<T*>(out.p) + b * out.batch + t * out.row + head * out.head;
+    };
+    const T* x[kAtOnce];
+    T* y[kAtOnce];
+    if (copy) {
+      for (int h0 = lane; h0 < heads; h0 += kAtOnce * lanes) {
+        Pack<T, W> v[kAtOnce];
 #pragma unroll
-      for (int j = 0; j < P; ++j) {
-        const float v = p[j] * c[j] - q[j] * s[j];
-        q[j] = p[j] * s[j] + q[j] * c[j];
-        p[j] = v;
+        for (int i = 0; i < kAtOnce; ++i)
+          if (h0 + i * lanes < heads) {
+            place(h0 + i * lanes, x[i], y[i]);
+            if (x[i] != y[i]) v[i] = ld_whole<T, W>(x[i] + at);
+          }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+          if (h0 + i * lanes < heads && x[i] != y[i]) st_pack<T, W>(y[i] + at, W, true, v[i]);
       }
-      st_pairs_of<T, P, PAIRS>(y, a.R, at, p, q);
+      continue;
+    }
+    // the first heads' channels are on their way before the sines and cosines are formed
+    Turned<T, P, PAIRS> v[kAtOnce];
+    const auto load = [&](int h0) {
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        if (h0 + i * lanes < heads) {
+          place(h0 + i * lanes, x[i], y[i]);
+          v[i].load(x[i], a.R, at);
+        }
+    };
+    const long long pos = a.positions ? (long long)rd(a.positions + b * a.positions_batch + t) : t;
+    load(lane);
+    float c[P], s[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      // the signed fraction of a turn, in half turns
+      const unsigned long long f = (unsigned long long)pos * turn[j];
+      sincospif((float)(int)(f >> 32) * 0x1p-31f, &s[j], &c[j]);
+      s[j] *= a.inverse ? -a.amplitude : a.amplitude;
+      c[j] *= a.amplitude;
+    }
+    for (int h0 = lane; h0 < heads; h0 += kAtOnce * lanes) {
+      if (h0 != lane) load(h0);
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        if (h0 + i * lanes >= heads) continue;
+        float p[P], q[P];
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          const float e = v[i].a(j), f = v[i].b(j);
+          p[j] = e * c[j] - f * s[j];
+          q[j] = e * s[j] + f * c[j];
+        }
+        Turned<T, P, PAIRS>::store(y[i], a.R, at, p, q);
+      }
     }
   }
 }

@@ -362,8 +362,9 @@ cudaError_t fwd_t(const s4_vocab_loss_args& a, St st, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// Words per piece: gradients of the logits of about 256 MB, in whole tiles.
-constexpr size_t kPieceBytes = 256ull << 20;
+// Words per piece: gradients of the logits of up to 512 MB, in whole tiles (8192 rows of 2048 channels, 50257 words: 4.78 ms
+// with the forward pass; pieces of 256 MB 4.86, of 128 MB 4.99: more, and fuller, rounds of tiles in a piece).
+constexpr size_t kPieceBytes = 512ull << 20;
 long long piece_words(long long rows, int V, int planes) {
   long long n = (long long)(kPieceBytes / (2ull * planes * rows)) / kBN * kBN;
   if (n < kBN) n = kBN;
