@@ -62,8 +62,8 @@ class Model(torch.nn.Module):
         """The norm that follows block i's: the next block's, or the last."""
         return self.blocks[i + 1].w_pre if i + 1 < LAYERS else self.w_last
 
-    def forward(self, tokens):
-        """Logits of whole sequences, differentiable."""
+    def hidden(self, tokens):
+        """What the output's weights are multiplied by, for whole sequences, differentiable."""
         h = self.embed(tokens).float()
         h, y = ops.block_norm(h, w_pre=self.blocks[0].w_pre)
         for i, b in enumerate(self.blocks):
@@ -72,7 +72,11 @@ class Model(torch.nn.Module):
             dt, B, C = b.select(u)
             o = b.out(ops.selective_scan(u, dt, -torch.exp(b.log_A), B, C, b.D, z, b.dt_bias))
             h, y = ops.block_norm(o, gate, h, b.w_post, b.scale, self.join(i))
-        return F.linear(y, self.embed.weight)
+        return y
+
+    def forward(self, tokens):
+        """Logits of whole sequences, differentiable."""
+        return F.linear(self.hidden(tokens), self.embed.weight)
 
     def cache(self, slots, device):
         """Per layer: the convolution's last inputs and the scan's states, one slot per sequence."""
@@ -115,8 +119,9 @@ def train(model, steps, half=4, n=64, lr=3e-3, seed=1):
     losses = []
     for _ in range(steps):
         seq = batch(n, half, "cuda", g)
-        logits = model(seq[:, :-1])
-        loss = F.cross_entropy(logits[:, half:].flatten(0, 1), seq[:, half + 1:].flatten())
+        # the loss of the second half, without the logits
+        y = model.hidden(seq[:, :-1])[:, half:].flatten(0, 1)
+        loss = ops.vocab_loss(y, model.embed.weight, seq[:, half + 1:].flatten()).mean()
         opt.zero_grad()
         loss.backward()
         opt.step()

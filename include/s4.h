@@ -626,10 +626,13 @@ int  s4_timing_read(const char* name, int* launches, double* total_ms);
  * before it gives up and records S4_ERR_TIMEOUT (default 4194304; polls < 0
  * restores the default, 0 makes every such wait give up at once).  Only the
  * staged kernels wait this way: the convolution of rows of 2M = 8192 points
- * and the layer's kernel spectrum for M <= 1024.  A kernel whose wait gave up
+ * and the layer's kernel spectrum for M <= 1024 (and the products of linear
+ * attention and the vocabulary loss: see the end).  A kernel whose wait gave up
  * issues no further copies, reads the data from global memory instead, waits
  * for the copy in flight once more (default limit) before it exits, and
- * writes its output as zeros.  Library-wide and read at launch time; meant
+ * writes its output as zeros.  A product whose wait gave up records the same, waits
+ * for its copies and products in flight (default limit), and leaves what it
+ * had not written yet as it was.  Library-wide and read at launch time; meant
  * for tests of that path, not for concurrent use.  Returns S4_OK. */
 s4_status s4_set_wait_limit(int polls);
 

@@ -1,19 +1,23 @@
-"""The selective block's operators as differentiable functions: torch.autograd nodes whose forward and
-backward are the library's calls (block.py).  Nothing beside the inputs is kept for the backward
-pass.  Activations and parameters as in block.py; sequences start from a state of zeros.  There are
-no second derivatives: gradients taken with create_graph=True raise where they are differentiated.
+"""The library's block operators as differentiable functions: torch.autograd nodes whose forward and
+backward are the library's calls (block.py, sequence.py).  Nothing beside the inputs is kept for the backward
+pass (the vocabulary loss keeps its lse).  Activations and parameters as there; sequences start from a state of zeros.
+There are no second derivatives: gradients taken with create_graph=True raise where they are differentiated.
 
     short_conv(x, w, bias, lengths)                               -> y
     selective_scan(x, dt, A, B, C, D, z, dt_bias, lengths)        -> y
     block_norm(o, gate, h, w_post, scale, w_pre, eps)             -> h_out, y
+    linear_attention(q, k, v, log_decay, scale, lengths)          -> o          (no gradient for log_decay)
+    rotary(q, k, freqs, positions, pairs, amplitude)              -> q, k       (k may be None)
+    layer_norm(x, w, b, eps)                                      -> y
+    vocab_loss(h, w, targets)                                     -> losses     (one per row)
 """
 from __future__ import annotations
 
 import torch
 
-from . import block
+from . import block, sequence
 
-__all__ = ["short_conv", "selective_scan", "block_norm"]
+__all__ = ["short_conv", "selective_scan", "block_norm", "linear_attention", "rotary", "layer_norm", "vocab_loss"]
 
 
 class _Final(torch.autograd.Function):
@@ -24,7 +28,7 @@ class _Final(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, *_):
-        raise RuntimeError("the selective block's operators have no second derivatives")
+        raise RuntimeError("the library's block operators have no second derivatives")
 
 
 def _final(grads, inputs):
@@ -95,3 +99,86 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, lengths=None):
 def block_norm(o, gate=None, h=None, w_post=None, scale=None, w_pre=None, eps=1e-5):
     """(h_out, y); y is None without w_pre."""
     return _BlockNorm.apply(o, gate, h, w_post, scale, w_pre, eps)
+
+
+class _LinearAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, log_decay, scale, lengths):
+        ctx.save_for_backward(q, k, v, log_decay, lengths)
+        ctx.scale = scale
+        return sequence.s4_linear_attention_fwd(q, k, v, log_decay, scale=scale, lengths=lengths)
+
+    @staticmethod
+    def backward(ctx, do):
+        q, k, v, log_decay, lengths = ctx.saved_tensors
+        g = sequence.s4_linear_attention_bwd(q, k, v, log_decay, do.contiguous(), scale=ctx.scale, lengths=lengths)
+        return _final((g["dq"], g["dk"], g["dv"], None, None, None), (q, k, v, do))
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, freqs, positions, pairs, amplitude):
+        ctx.save_for_backward(freqs, positions)
+        ctx.how = pairs, amplitude
+        ctx.set_materialize_grads(False)
+        return sequence.s4_rotary_fwd(q, k, freqs, positions=positions, pairs=pairs, amplitude=amplitude)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        freqs, positions = ctx.saved_tensors
+        pairs, amplitude = ctx.how
+        given = [g.contiguous() for g in (dq, dk) if g is not None]
+        if not given:
+            return (None,) * 6
+        # each alone where one is missing: they may have different numbers of heads
+        back = sequence.s4_rotary_bwd(given[0], given[1] if len(given) == 2 else None, freqs, positions=positions,
+                                      pairs=pairs, amplitude=amplitude)
+        got = iter(back)
+        return _final((None if dq is None else next(got), None if dk is None else next(got), None, None, None, None),
+                      (dq, dk))
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, b, eps):
+        ctx.save_for_backward(x, w, b)
+        ctx.eps = eps
+        return sequence.s4_layer_norm_fwd(x, w, b, eps=eps)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, b = ctx.saved_tensors
+        g = sequence.s4_layer_norm_bwd(x, dy.contiguous(), w, b, eps=ctx.eps)
+        return _final((g["dx"], g.get("dw"), g.get("db"), None), (x, w, dy))
+
+
+class _VocabLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, h, w, targets):
+        loss, lse = sequence.s4_vocab_loss_fwd(h, w, targets)
+        ctx.save_for_backward(h, w, targets, lse)
+        return loss
+
+    @staticmethod
+    def backward(ctx, dloss):
+        h, w, targets, lse = ctx.saved_tensors
+        g = sequence.s4_vocab_loss_bwd(h, w, targets, lse, dloss.contiguous())
+        return _final((g["dh"], g["dw"], None), (h, w, dloss))
+
+
+def linear_attention(q, k, v, log_decay, scale=None, lengths=None):
+    return _LinearAttention.apply(q, k, v, log_decay, scale, lengths)
+
+
+def rotary(q, k, freqs, positions=None, pairs=False, amplitude=1.0):
+    """(q, k), turned; k may be None."""
+    return _Rotary.apply(q, k, freqs, positions, pairs, amplitude)
+
+
+def layer_norm(x, w=None, b=None, eps=1e-5):
+    return _LayerNorm.apply(x, w, b, eps)
+
+
+def vocab_loss(h, w, targets):
+    """One loss per row of h (0 where the target is negative)."""
+    return _VocabLoss.apply(h, w, targets)

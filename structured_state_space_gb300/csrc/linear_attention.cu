@@ -488,6 +488,27 @@ size_t local_bytes(int batch, int L, int H, int da, int dc) {
   return s4impl::align256(segs == 1 ? 0 : sizeof(float) * (size_t)batch * H * segs * da * dc);
 }
 
+#ifdef S4_BOUNDS_CHECK
+cudaError_t set_walk_extents(const Walks& ws, int n, int e, cudaStream_t s) {
+  s4impl::Extents x{};
+  x.in(ws.w[0].log_decay, 4, ws.w[0].H);
+  x.in(ws.w[0].lengths, 4, ws.w[0].batch);
+  x.in(ws.w[0].index, 4, ws.w[0].batch);
+  for (int i = 0; i < n; ++i) {
+    const Walk& w = ws.w[i];
+    const auto add = [&](const In& r, int d) {
+      x.add(r.p, e, true, false, d, w.batch, r.batch, w.L, r.row, (w.H + r.per - 1) / r.per, r.head);
+    };
+    add(w.a, w.da), add(w.b, w.da), add(w.c, w.dc);
+    x.add(w.out, w.out_f32 ? 4 : e, false, true, w.dc, w.batch, w.out_batch, w.L, w.out_row, w.H, w.out_head);
+    x.in(w.init, 4, (long long)w.H * w.da * w.dc, w.slots);
+    x.out(w.last, 4, (long long)w.H * w.da * w.dc, w.slots);
+    if (w.segs > 1) x.scratch(w.local, 4, (long long)w.batch * w.H * w.segs * w.da * w.dc);
+  }
+  return set_extents(x, s);
+}
+#endif
+
 template <typename T, int D>
 cudaError_t walk_d(const Walks& ws, int n, St st, cudaStream_t s) {
   constexpr int C = kTerms<T> == 3 ? 32 : 64, bytes = kWalkBytes<T, D, C>;
@@ -506,7 +527,7 @@ cudaError_t walk_d(const Walks& ws, int n, St st, cudaStream_t s) {
       s4impl::TimedLaunch tl("linear_attention", s);
       state<<<dim3(walks, segs - 1, n), kThreads, bytes, s>>>(ws, st);
     }
-    if (const cudaError_t err = s4impl::launch_join(ws, n, st, s); err != cudaSuccess) return err;
+    if (const cudaError_t err = s4impl::launch_join(ws, n, (int)sizeof(T), st, s); err != cudaSuccess) return err;
   }
   s4impl::TimedLaunch tl("linear_attention", s);
   kernel<<<dim3(walks, segs, n), kThreads, bytes, s>>>(ws, st);
@@ -527,12 +548,6 @@ cudaError_t walk_t(Walks ws, int n, St st, cudaStream_t s) {
     least_cols = ws.w[i].dc < least_cols ? ws.w[i].dc : least_cols;
   }
   const int want = segments((long long)n * ws.w[0].batch * ws.w[0].H * ((least_cols + kCols - 1) / kCols), ws.w[0].L);
-#ifdef S4_BOUNDS_CHECK
-  s4impl::Extents x{};
-  x.in(ws.w[0].log_decay, 4, ws.w[0].H);
-  x.in(ws.w[0].lengths, 4, ws.w[0].batch);
-  x.in(ws.w[0].index, 4, ws.w[0].batch);
-#endif
   for (int i = 0; i < n; ++i) {
     Walk& w = ws.w[i];
     w.seg = segment_tokens(w.L, want);
@@ -541,19 +556,9 @@ cudaError_t walk_t(Walks ws, int n, St st, cudaStream_t s) {
     const auto ok = [&](const In& x) { return vec_ok(x.p, e, 16, x.batch, x.row) && vec_ok(x.p, e, 16, x.head); };
     w.vec = ok(w.a) && ok(w.b) && ok(w.c) && vec_ok(w.out, eo, 2 * eo, w.out_batch, w.out_row) &&
             vec_ok(w.out, eo, 2 * eo, w.out_head);
-#ifdef S4_BOUNDS_CHECK
-    const auto add = [&](const In& i, int d) {
-      x.add(i.p, e, true, false, d, w.batch, i.batch, w.L, i.row, (w.H + i.per - 1) / i.per, i.head);
-    };
-    add(w.a, w.da), add(w.b, w.da), add(w.c, w.dc);
-    x.add(w.out, eo, false, true, w.dc, w.batch, w.out_batch, w.L, w.out_row, w.H, w.out_head);
-    x.in(w.init, 4, (long long)w.H * w.da * w.dc, w.slots);
-    x.out(w.last, 4, (long long)w.H * w.da * w.dc, w.slots);
-    if (w.segs > 1) x.scratch(w.local, 4, (long long)w.batch * w.H * w.segs * w.da * w.dc);
-#endif
   }
 #ifdef S4_BOUNDS_CHECK
-  if (const cudaError_t err = set_extents(x, s); err != cudaSuccess) return err;
+  if (const cudaError_t err = set_walk_extents(ws, n, sizeof(T), s); err != cudaSuccess) return err;
 #endif
   if (most <= 64) return walk_d<T, 64>(ws, n, st, s);
   return most <= 128 ? walk_d<T, 128>(ws, n, st, s) : walk_d<T, 256>(ws, n, st, s);
@@ -672,7 +677,10 @@ size_t linear_attention_scratch(int batch, int L, int H, int K, int V) {
   return L == 1 ? 0 : local_bytes(batch, L, H, K, V);
 }
 
-cudaError_t launch_join(const Walks& ws, int n, St st, cudaStream_t s) {
+cudaError_t launch_join(const Walks& ws, int n, int e, St st, cudaStream_t s) {
+#ifdef S4_BOUNDS_CHECK
+  if (const cudaError_t err = set_walk_extents(ws, n, e, s); err != cudaSuccess) return err;
+#endif
   s4impl::TimedLaunch tl("linear_attention", s);
   const Walk& w = ws.w[0];  // (all have as many cells)
   join_kernel<<<dim3((unsigned)((w.da * w.dc + 255) / 256), w.batch * w.H, n), 256, 0, s>>>(ws, st);

@@ -38,7 +38,7 @@ struct Walks {
 bool tiles_take(const Walk& w, int dtype);
 int tile_segments(long long walks, int L, int passes);
 cudaError_t launch_tiles(const Walks& ws, int passes, int dtype, St st, cudaStream_t s);
-cudaError_t launch_join(const Walks& ws, int n, St st, cudaStream_t s);
+cudaError_t launch_join(const Walks& ws, int n, int e, St st, cudaStream_t s);  // (e: bytes of an element)
 
 }  // namespace s4impl
 

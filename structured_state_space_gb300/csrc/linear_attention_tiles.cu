@@ -629,7 +629,7 @@ cudaError_t launch(const Passes& ps, int passes, St st, cudaStream_t s) {
       s4impl::TimedLaunch tl("linear_attention", s);
       state<<<dim3(walks, w.segs - 1, passes), kThreads, R::BYTES, s>>>(ps, st);
     }
-    if (const cudaError_t err = s4impl::launch_join(ps.walks, passes, st, s); err != cudaSuccess) return err;
+    if (const cudaError_t err = s4impl::launch_join(ps.walks, passes, 2, st, s); err != cudaSuccess) return err;
   }
   using R = Room<DK, DV, NK, false>;
   constexpr auto kernel = tiles_kernel<DK, DV, NK, false>;

@@ -62,15 +62,17 @@ struct Turned {
   }
 };
 
-constexpr int kAtOnce = 2;  // heads whose channels a thread has on their way (4 leaves room for fewer threads: 64 us, not 54)
+// Heads whose channels a thread has on their way, and CTAs per SM: 4 x 4096 tokens of 32 heads of 128 channels in bfloat16 take
+// 50 us (a plain copy 44); with one head or four at once 55 and 64, without the bound on registers 70.
+constexpr int kAtOnce = 2, kPerSm = 4;
 
 // Threads: `units` per token and head lane (packs of P pairs, and packs of W copied channels), `lanes`
 // head lanes per token, `per` tokens.  Tokens in steps of the grid.
-template <typename T, int P, int W, bool PAIRS>
-__global__ void __launch_bounds__(256) rotary_kernel(s4_rotary_args a, int units, int lanes, int per) {
+template <typename T, int P, int W, bool PAIRS, bool COPIES>
+__global__ void __launch_bounds__(256, kPerSm) rotary_kernel(s4_rotary_args a, int units, int lanes, int per) {
   // first the threads that turn, then those that copy: a warp has one kind or the other
-  const int turned = a.R / P, heads = a.H + a.G, split = turned * lanes * per;
-  const bool copy = (int)threadIdx.x >= split;
+  const int turned = COPIES ? a.R / P : units, heads = a.H + a.G, split = turned * lanes * per;
+  const bool copy = COPIES && (int)threadIdx.x >= split;
   const int id = threadIdx.x - (copy ? split : 0), mine = copy ? units - turned : turned;
   if (mine == 0) return;
   const int u = id % mine, lane = id / mine % lanes, sub = id / mine / lanes;
@@ -165,8 +167,11 @@ cudaError_t launch(const s4_rotary_args& a, cudaStream_t s) {
   const int per = 256 / (lanes * units) > 0 ? 256 / (lanes * units) : 1;
   const long long need = (tokens + per - 1) / per, most = (long long)s4impl::num_sms() * 16;
   s4impl::TimedLaunch tl("rotary", s);
-  rotary_kernel<T, P, W, PAIRS><<<(unsigned)(need < most ? need : most), (units * lanes * per + 31) / 32 * 32, 0, s>>>(
-      a, units, lanes, per);
+  const unsigned grid = (unsigned)(need < most ? need : most), threads = (units * lanes * per + 31) / 32 * 32;
+  if (a.D == 2 * a.R)
+    rotary_kernel<T, P, W, PAIRS, false><<<grid, threads, 0, s>>>(a, units, lanes, per);
+  else
+    rotary_kernel<T, P, W, PAIRS, true><<<grid, threads, 0, s>>>(a, units, lanes, per);
   return cudaGetLastError();
 }
 
