@@ -102,7 +102,7 @@ __device__ __forceinline__ bool elected() {
 struct Product {
   int M, N;                 // of the result
   int tiles_m, tiles_n;     // of 128 x BN
-  int chunks;               // of 64 k in all
+  int first, chunks;        // of 64 k: where they begin, how many
   int splits;               // the chunks are shared out among so many partial results
   int pairs;                // plane pairs: nibble p of each list
   uint32_t planes_a, planes_b;
@@ -166,8 +166,8 @@ __global__ void __launch_bounds__(256, 1)
     r.m = t % p.tiles_m;
     r.n = t / p.tiles_m % p.tiles_n;
     r.split = t / p.tiles_m / p.tiles_n;
-    r.from = (int)((long long)p.chunks * r.split / p.splits);
-    r.to = (int)((long long)p.chunks * (r.split + 1) / p.splits);
+    r.from = p.first + (int)((long long)p.chunks * r.split / p.splits);
+    r.to = p.first + (int)((long long)p.chunks * (r.split + 1) / p.splits);
     return r;
   };
 

@@ -227,6 +227,7 @@ __global__ void __launch_bounds__(256) splits_kernel(const float* part, int spli
 }
 
 // ---- host side -----------------------------------------------------------------------------------------
+int chunks_of(long long k) { return (int)((k + kBK - 1) / kBK); }
 unsigned blocks_for(long long n) {
   const long long most = 16ll * s4impl::num_sms(), need = (n + 255) / 256;
   return (unsigned)(need < most ? need : most);
@@ -273,22 +274,23 @@ cudaError_t to_terms(const void* p, long long row, long long rows, int H, int pl
   return cudaGetLastError();
 }
 
-// The plane pairs of a product of operands in `n` terms each, the largest first: those whose sizes are
-// above what the last term leaves out.
+// The plane pairs of a product of operands in `n` terms each: those whose sizes are above what the last term leaves
+// out, the smallest first: the tensor cores cut what an addition shifts out of the accumulator, always
+// towards zero, and while the small pairs are summed it is small.
 void pairs_of(int n, Product* p) {
   p->pairs = 0;
   p->planes_a = p->planes_b = 0;
-  for (int sum = 0; sum < n; ++sum)
+  for (int sum = n - 1; sum >= 0; --sum)
     for (int i = 0; i <= sum; ++i, ++p->pairs) {
       p->planes_a |= (uint32_t)i << (4 * p->pairs);
       p->planes_b |= (uint32_t)(sum - i) << (4 * p->pairs);
     }
 }
 
-// result [M][N] = sum over k of A and B: A [M][k] or, A_MN, [k][M]; B likewise.
+// result [M][N] = sum over k of A and B, in 64 k from chunk `first` on: A [M][k] or, A_MN, [k][M]; B likewise.
 template <bool A_MN, bool B_MN, typename Epilogue>
-cudaError_t multiply(const Operand& a, const Operand& b, long long M, long long N, long long K, int splits, const Epilogue& ep,
-                     St st, cudaStream_t s) {
+cudaError_t multiply(const Operand& a, const Operand& b, long long M, long long N, int first, int chunks, int splits,
+                     const Epilogue& ep, St st, cudaStream_t s) {
   constexpr auto kernel = product_kernel<kBN, A_MN, B_MN, Epilogue>;
   CUtensorMap ma, mb;
   if (!make_map(&ma, a.p, a.bf16, a.H, a.rows, a.planes, a.row, a.plane, A_MN ? kBK : 128) ||
@@ -297,7 +299,7 @@ cudaError_t multiply(const Operand& a, const Operand& b, long long M, long long 
   Product p{};
   p.M = (int)M, p.N = (int)N;
   p.tiles_m = (int)((M + 127) / 128), p.tiles_n = (int)((N + kBN - 1) / kBN);
-  p.chunks = (int)((K + kBK - 1) / kBK);
+  p.first = first, p.chunks = chunks;
   p.splits = splits;
   pairs_of(a.planes, &p);
   p.what = instruction(a.bf16, A_MN, B_MN, 128, kBN);
@@ -355,7 +357,7 @@ cudaError_t fwd_t(const s4_vocab_loss_args& a, St st, cudaStream_t s) {
   if (const cudaError_t e = set_extents(x, s); e != cudaSuccess) return e;
 #endif
   const ToSums ep{part, hit, a.targets, a.wide_targets, a.V, a.rows, st};
-  err = multiply<false, false>(h, w, a.rows, a.V, a.H, 1, ep, st, s);
+  err = multiply<false, false>(h, w, a.rows, a.V, 0, chunks_of(a.H), 1, ep, st, s);
   if (err != cudaSuccess) return err;
   s4impl::TimedLaunch tl("vocab_loss", s);
   join_kernel<<<(unsigned)((a.rows + 7) / 8), 256, 0, s>>>(part, hit, a, tiles_n, st);
@@ -371,25 +373,74 @@ long long piece_words(long long rows, int V, int planes) {
   const long long all = (V + kBN - 1ll) / kBN * kBN, pieces = (all + n - 1) / n;
   return (all / kBN + pieces - 1) / pieces * kBN;  // of nearly equal sizes
 }
-// Shares of a piece's words in dh: where its tiles are fewer than the SMs.
-int dh_splits(long long rows, int H, long long words) {
-  const long long tiles = (rows + 127) / 128 * ((H + kBN - 1) / kBN), chunks = words / kBK;
+// Shares of the sum over k of a product [M][N]: where its tiles are fewer than the SMs.
+int shares(long long M, long long N, long long k) {
+  const long long tiles = (M + 127) / 128 * ((N + kBN - 1) / kBN), chunks = chunks_of(k);
   long long n = s4impl::num_sms() / tiles;
   if (n > chunks / 8) n = chunks / 8;
   return n < 1 ? 1 : (int)n;
+}
+// With fp32 results no accumulator sums up more than 4096 k: what the tensor cores cut off then stays below 3e-6
+// (measured about 1e-8 per addition of 16 k); the parts are added rounded.
+constexpr int kExact = 64;  // chunks
+
+// out (+)= A B: in one product where it can go straight out (`part` is then not used, and nothing may be added later),
+// else as `splits` partial results in part [splits][M][N].
+template <typename T, bool A_MN, bool B_MN>
+cudaError_t sum_products(const Operand& a, const Operand& b, long long M, long long N, long long K, int splits, bool add,
+                         bool direct, T* out, float* part, St st, cudaStream_t s) {
+  const int chunks = chunks_of(K), most = sizeof(T) == 4 ? kExact * splits : chunks;
+  if (direct && chunks <= most) {
+    const ToMatrix<T, false> ep{out, (int)M, (int)N, N % 8 == 0 && vec_ok(out, sizeof(T), 16)};
+    return multiply<A_MN, B_MN>(a, b, M, N, 0, chunks, 1, ep, st, s);
+  }
+  const bool vec = N % 4 == 0 && vec_ok(part, 4, 16);
+  for (int first = 0; first < chunks; first += most, add = true) {
+    const int n = chunks - first < most ? chunks - first : most;
+    const cudaError_t err =
+        add ? multiply<A_MN, B_MN>(a, b, M, N, first, n, splits, ToMatrix<float, true>{part, (int)M, (int)N, vec}, st, s)
+            : multiply<A_MN, B_MN>(a, b, M, N, first, n, splits, ToMatrix<float, false>{part, (int)M, (int)N, vec}, st, s);
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
+}
+template <typename T>
+cudaError_t add_up(const float* part, int splits, long long n, T* out, cudaStream_t s) {
+  s4impl::TimedLaunch tl("vocab_loss", s);
+  splits_kernel<T><<<blocks_for(n / 8 + 1), 256, 0, s>>>(part, splits, n, out, vec_ok(out, sizeof(T), 16));
+  return cudaGetLastError();
+}
+
+// What a backward pass has beside the operands' copies.
+struct Plan {
+  long long words, pieces;
+  int dh_splits, dw_splits;
+  size_t g, dh, dw;  // bytes
+};
+template <typename Args>
+Plan plan_of(const Args& a) {
+  Plan p;
+  const int np = terms_of(a.dtype);
+  p.words = piece_words(a.rows, a.V, np), p.pieces = (a.V + p.words - 1) / p.words;
+  p.dh_splits = shares(a.rows, a.H, p.words), p.dw_splits = shares(p.words, a.H, a.rows);
+  p.g = s4impl::align256(2ull * np * a.rows * p.words);
+  p.dh = p.pieces > 1 || p.dh_splits > 1 || a.dtype == S4_F32 ? s4impl::align256(4ull * p.dh_splits * a.rows * a.H) : 0;
+  p.dw = p.dw_splits > 1 ? s4impl::align256(4ull * p.dw_splits * p.words * a.H) : 0;
+  return p;
 }
 
 template <typename T>
 cudaError_t bwd_t(const s4_vocab_loss_bwd_args& a, St st, cudaStream_t s) {
   constexpr int NP = sizeof(T) == 4 ? 3 : std::is_same_v<T, __half> ? 2 : 1;
-  const long long words = piece_words(a.rows, a.V, NP), pieces = (a.V + words - 1) / words;
-  const int splits = dh_splits(a.rows, a.H, words);
+  const Plan p = plan_of(a);
+  const long long words = p.words;
   char* at = static_cast<char*>(a.ws) + s4impl::kStatusBytes;
   __nv_bfloat16* g = reinterpret_cast<__nv_bfloat16*>(at);
-  at += s4impl::align256(2ull * NP * a.rows * words);
-  float* acc = reinterpret_cast<float*>(at);
-  const bool direct = pieces == 1 && splits == 1;
-  if (!direct) at += s4impl::align256(4ull * splits * a.rows * a.H);
+  at += p.g;
+  float* dh = reinterpret_cast<float*>(at);
+  at += p.dh;
+  float* dw = reinterpret_cast<float*>(at);
+  at += p.dw;
   Operand h, w, lh, lw;
   cudaError_t err = operand<T>(a.h, a.h_row, a.rows, a.H, NP, &at, &h, s);
   if (err != cudaSuccess) return err;
@@ -409,12 +460,12 @@ cudaError_t bwd_t(const s4_vocab_loss_bwd_args& a, St st, cudaStream_t s) {
   x.in(a.lse, 4, a.rows);
   x.in(a.dloss, 4, a.rows);
   x.scratch(g, 2, NP * a.rows * words);
-  if (!direct) x.scratch(acc, 4, splits * a.rows * a.H);
+  if (p.dh) x.scratch(dh, 4, p.dh_splits * a.rows * a.H);
+  if (p.dw) x.scratch(dw, 4, p.dw_splits * words * a.H);
   x.out(a.dh, sizeof(T), a.rows * a.H);
-  x.out(a.dw, sizeof(T), (long long)a.V * a.H);
+  x.add(a.dw, sizeof(T), std::is_same_v<T, float>, true, (long long)a.V * a.H);
   if (const cudaError_t e = set_extents(x, s); e != cudaSuccess) return e;
 #endif
-  const bool vec = a.H % 8 == 0, vec_acc = a.H % 4 == 0;
   const auto rows_from = [](const Operand& o, long long first, long long n) {
     Operand r = o;
     r.p = static_cast<const char*>(o.p) + first * o.row * 2;
@@ -424,28 +475,20 @@ cudaError_t bwd_t(const s4_vocab_loss_bwd_args& a, St st, cudaStream_t s) {
   for (long long first = 0; first < a.V; first += words) {
     const long long n = a.V - first < words ? a.V - first : words;
     const ToGrads<NP> grads{g, a.lse, a.dloss, a.targets, a.wide_targets, a.V, (int)first, a.rows, words, st};
-    err = multiply<false, false>(lh, rows_from(lw, first, n), a.rows, n, a.H, 1, grads, st, s);
+    err = multiply<false, false>(lh, rows_from(lw, first, n), a.rows, n, 0, chunks_of(a.H), 1, grads, st, s);
     if (err != cudaSuccess) return err;
     const Operand gr{g, words, words * a.rows, a.rows, (int)n, NP, true};
-    const Operand ws = rows_from(w, first, n);
-    const ToMatrix<T, false> to_w{static_cast<T*>(a.dw) + first * a.H, (int)n, a.H, vec && vec_ok(a.dw, sizeof(T), 16)};
-    err = multiply<true, true>(gr, h, n, a.H, a.rows, 1, to_w, st, s);
+    // the words' gradients: partial sums where there are shares; in fp32 else straight into dw, piece by piece of the rows
+    T* to_w = static_cast<T*>(a.dw) + first * a.H;
+    float* part_w = p.dw ? dw : std::is_same_v<T, float> ? reinterpret_cast<float*>(to_w) : nullptr;
+    err = sum_products<T, true, true>(gr, h, n, a.H, a.rows, p.dw_splits, false, !p.dw, to_w, part_w, st, s);
+    if (err == cudaSuccess && p.dw) err = add_up<T>(dw, p.dw_splits, n * a.H, to_w, s);
     if (err != cudaSuccess) return err;
-    if (direct)
-      err = multiply<false, true>(gr, ws, a.rows, a.H, n, 1,
-                                  ToMatrix<T, false>{static_cast<T*>(a.dh), (int)a.rows, a.H, vec && vec_ok(a.dh, sizeof(T), 16)},
-                                  st, s);
-    else if (first == 0)
-      err = multiply<false, true>(gr, ws, a.rows, a.H, n, splits, ToMatrix<float, false>{acc, (int)a.rows, a.H, vec_acc}, st, s);
-    else
-      err = multiply<false, true>(gr, ws, a.rows, a.H, n, splits, ToMatrix<float, true>{acc, (int)a.rows, a.H, vec_acc}, st, s);
+    err = sum_products<T, false, true>(gr, rows_from(w, first, n), a.rows, a.H, n, p.dh_splits, first > 0, !p.dh,
+                                       static_cast<T*>(a.dh), dh, st, s);
     if (err != cudaSuccess) return err;
   }
-  if (direct) return cudaSuccess;
-  s4impl::TimedLaunch tl("vocab_loss", s);
-  splits_kernel<T><<<blocks_for(a.rows * a.H / 8 + 1), 256, 0, s>>>(acc, splits, a.rows * a.H, static_cast<T*>(a.dh),
-                                                                   vec_ok(a.dh, sizeof(T), 16));
-  return cudaGetLastError();
+  return p.dh ? add_up<T>(dh, p.dh_splits, a.rows * a.H, static_cast<T*>(a.dh), s) : cudaSuccess;
 }
 
 }  // namespace
@@ -467,10 +510,8 @@ cudaError_t launch_vocab_loss(const s4_vocab_loss_args& a, St st, cudaStream_t s
 }
 
 size_t vocab_loss_bwd_scratch(const s4_vocab_loss_bwd_args& a) {
-  const int np = terms_of(a.dtype);
-  const long long words = piece_words(a.rows, a.V, np);
-  size_t n = align256(2ull * np * a.rows * words) + align256(4ull * dh_splits(a.rows, a.H, words) * a.rows * a.H);
-  n += copies(a, np);
+  const Plan p = plan_of(a);
+  size_t n = p.g + p.dh + p.dw + copies(a, terms_of(a.dtype));
   if (a.dtype == S4_F16) n += copies(a, 1);
   return n;
 }

@@ -130,3 +130,25 @@ def test_pieces_of_the_vocabulary():
     d *= dl.double()[:, None]
     close(g["dh"], to64(d @ w.double()), "dh", 2 * 2.0 ** -8)
     close(g["dw"], to64(d.t() @ h.double()), "dw", 2 * 2.0 ** -8)
+
+
+@pytest.mark.parametrize("rows,H,V", [(16384, 48, 300), (40, 64, 40000), (6000, 130, 700), (300, 1500, 9000)])
+def test_long_sums_in_float32(rows, H, V):
+    """Sums over many rows and many words: the tensor cores cut what they shift out of an accumulator towards zero, so an
+    accumulator that takes up too many products drifts (6e-5 for 16384 rows in one)."""
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    h = torch.randn(rows, H, device="cuda", generator=gen)
+    w = torch.randn(V, H, device="cuda", generator=gen) * 2 * H ** -0.5
+    t = torch.randint(-1, V, (rows,), device="cuda", generator=gen)
+    dl = torch.rand(rows, device="cuda", generator=gen)
+    loss, lse = s4.s4_vocab_loss_fwd(h, w, t)
+    g = s4.s4_vocab_loss_bwd(h, w, t, lse, dl)
+    x = h.double() @ w.double().t()
+    l64 = torch.logsumexp(x, -1)
+    close(lse, to64(l64), "lse")
+    d = torch.exp(x - l64[:, None])
+    at = torch.arange(rows, device="cuda")
+    d[at, t.clamp(min=0)] -= 1
+    d *= torch.where(t >= 0, dl.double(), 0.0)[:, None]
+    close(g["dh"], to64(d @ w.double()), "dh")
+    close(g["dw"], to64(d.t() @ h.double()), "dw")
