@@ -8,8 +8,13 @@
 // keys f_j B enter the fp32 state as NK bfloat16 terms: 2 where the state only makes bfloat16 outputs, 3 where
 // it is returned.
 //
-// Products per chunk at widths 128: S, P C and A M 2^22 operations each, D 2^22 a term; the inputs and the output
-// are 128 KB: at the measured rates 1.2 to 1.4 us and 2.9 us of an SM's share.
+// Per chunk at widths 128: S, P C and A M 2^22 operations each, D 2^22 a term, which takes 1.7 to 2 us of an SM's share of
+// the measured rate; the inputs and the output are 128 KB, 2.9 us of an SM's share of the memory's.  Measured on 4 x 4096
+// tokens of 16 heads of 128: 215 us for the three walks of a backward pass, 3.4 us a chunk on 152 SMs at once; what is
+// above the memory's share are 40 of 192 walks left for a second round, and three walks that read 12 arrays
+// where one would read 7.  65536 tokens of 16 heads of 64 take 275 us, 3.0 us a chunk (64 KB, 1.4 us): there
+// the warp that issues the products is the bound, 40 of them per chunk at 90 cycles or so (a right operand of 64
+// columns does not feed the tensor cores), and a walk over segments reads keys and values twice.
 #include "linear_attention.cuh"
 #include "tile_gemm.cuh"
 
@@ -20,6 +25,10 @@ using s4impl::In;
 using s4impl::Walk;
 using s4impl::Walks;
 
+// Why so: accumulators of 128 lanes want 128 tokens; with 64 the products' tiles are half empty.  One warpgroup for P, O and
+// the keys together took 11.9 thousand cycles a chunk, two 6.4, three 6.6 with keys and state side by side (and half
+// the time where the state is returned); stores to global memory straight from the accumulators' lanes, 32
+// rows an instruction, slowed the keys' shared-memory traffic to a third: outputs go through shared memory.
 constexpr int kC = 128, kSlot = 32, kPasses = 3, kThreads = 512;
 
 struct Maps {
@@ -211,114 +220,100 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   const auto start_of = [&](int k) { return sp.begin + kC * (w.reverse ? sp.chunks - 1 - k : k); };
   const auto updates = [&](int k) { return STATE || k + 1 < sp.chunks || (sp.last && last != nullptr); };
 
+  int na = 0, nb = 0, nc = 0;  // tiles asked for
   if (wid >= 8 && wid < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (wid == 8 && elected()) {
-    int na = 0, nb = 0, nc = 0;  // tiles asked for
-    for (int k = 0; k < sp.chunks; ++k) {
-      const int t = start_of(k), sb = k % R::SB, sc = k % R::SC;
-      if (!wait(&empty_b[sb], k / R::SB + 1)) break;
-      s4dev::mbar_expect_tx(&full_b[sb], R::TA);
-#pragma unroll
-      for (int i = 0; i < DK / 64; ++i)
-        tma_load_4d(smem + R::B + sb * R::TA + i * 16384, &maps.b, 64 * i, h / w.b.per, t, b, &full_b[sb]);
-      ++nb;
-      if constexpr (!STATE) {
-        const int sa = k % R::SA;
-        if (!wait(&empty_a[sa], k / R::SA + 1)) break;
-        s4dev::mbar_expect_tx(&full_a[sa], R::TA);
+      for (int k = 0; k < sp.chunks; ++k) {
+        const int t = start_of(k), sb = k % R::SB, sc = k % R::SC;
+        if (!wait(&empty_b[sb], k / R::SB + 1)) break;
+        s4dev::mbar_expect_tx(&full_b[sb], R::TA);
 #pragma unroll
         for (int i = 0; i < DK / 64; ++i)
-          tma_load_4d(smem + R::A + sa * R::TA + i * 16384, &maps.a, 64 * i, h / w.a.per, t, b, &full_a[sa]);
-        ++na;
-      }
-      if (!wait(&empty_c[sc], k / R::SC + 1)) break;
-      s4dev::mbar_expect_tx(&full_c[sc], R::TC);
+          tma_load_4d(smem + R::B + sb * R::TA + i * 16384, &maps.b, 64 * i, h / w.b.per, t, b, &full_b[sb]);
+        ++nb;
+        if constexpr (!STATE) {
+          const int sa = k % R::SA;
+          if (!wait(&empty_a[sa], k / R::SA + 1)) break;
+          s4dev::mbar_expect_tx(&full_a[sa], R::TA);
 #pragma unroll
-      for (int i = 0; i < DV / 64; ++i)
-        tma_load_4d(smem + R::C + sc * R::TC + i * 16384, &maps.c, 64 * i, h / w.c.per, t, b, &full_c[sc]);
-      ++nc;
-    }
-    if (failed) {
-      // the copies in flight
-      const auto drain = [](unsigned long long* bar, int issued, int stages) {
-        for (int j = issued > stages ? issued - stages : 0; j < issued; ++j)
-          s4dev::mbar_wait(&bar[j % stages], (unsigned)(j / stages) & 1);
-      };
-      drain(full_b, nb, R::SB);
-      if constexpr (!STATE) drain(full_a, na, R::SA);
-      drain(full_c, nc, R::SC);
-    }
-  } else if (wid == 9) {
-    // the warp stays together, so that the descriptors are uniform; one lane issues
-    constexpr uint32_t kS = instruction(true, false, false, 128, 128), kAM = instruction(true, false, true, 128, DV),
-                       kD = instruction(true, true, true, 128, DV), kPC = instruction(true, false, true, 128, DV);
-    const uint32_t base = s4dev::smem_u32(smem);
-    const uint32_t one = elected();
-    int slots = 0, blanked = 0;  // of keys used, chunks that were not full
-    for (int k = 0; k < sp.chunks; ++k) {
-      const int sb = k % R::SB, sc = k % R::SC;
-      const uint64_t dc = tile_desc(base + R::C + sc * R::TC, 16384);
-      const uint64_t da = tile_desc(base + R::A + (STATE ? 0 : (k % (R::SA ? R::SA : 1)) * R::TA), 16);
-      if constexpr (!STATE) {
-        if (!wait_both(&full_b[sb], k / R::SB, &full_a[k % R::SA], k / R::SA)) break;
-        fence_after();
-        // S: over the width, 64 at a time
-        const uint64_t db = tile_desc(base + R::B + sb * R::TA, 16);
-#pragma unroll
-        for (int i = 0; i < DK / 16; ++i) {
-          const uint32_t at = (i / 4 * 16384 + i % 4 * 32) >> 4;
-          mma_f16(R::S, da + at, db + at, kS, i > 0, one);
+          for (int i = 0; i < DK / 64; ++i)
+            tma_load_4d(smem + R::A + sa * R::TA + i * 16384, &maps.a, 64 * i, h / w.a.per, t, b, &full_a[sa]);
+          ++na;
         }
-        mma_commit(&s_ready, one);
-        mma_commit(&empty_b[sb], one);
+        if (!wait(&empty_c[sc], k / R::SC + 1)) break;
+        s4dev::mbar_expect_tx(&full_c[sc], R::TC);
+#pragma unroll
+        for (int i = 0; i < DV / 64; ++i)
+          tma_load_4d(smem + R::C + sc * R::TC + i * 16384, &maps.c, 64 * i, h / w.c.per, t, b, &full_c[sc]);
+        ++nc;
       }
-      const bool up = updates(k);
-      // where a chunk is not full, C's last rows have been blanked
-      if (sp.end - start_of(k) < kC && !wait_warp(&c_clean, blanked++)) break;
-      if (!(up ? wait_both(&full_c[sc], k / R::SC, &d_free, k + 1) : wait_warp(&full_c[sc], k / R::SC))) break;
-      if (up) {
-        bool ok = true;
-        for (int j = 0; j < kC / kSlot; ++j, ++slots) {
-          const int sk = slots % R::SK;
-          ok = wait_warp(&keys_ready[sk], slots / R::SK);
+    } else if (wid == 9) {
+      // the warp stays together, so that the descriptors are uniform; one lane issues
+      constexpr uint32_t kS = instruction(true, false, false, 128, 128), kAM = instruction(true, false, true, 128, DV),
+                         kD = instruction(true, true, true, 128, DV), kPC = instruction(true, false, true, 128, DV);
+      const uint32_t base = s4dev::smem_u32(smem);
+      const uint32_t one = elected();
+      int slots = 0, blanked = 0;  // of keys used, chunks that were not full
+      for (int k = 0; k < sp.chunks; ++k) {
+        const int sb = k % R::SB, sc = k % R::SC;
+        const uint64_t dc = tile_desc(base + R::C + sc * R::TC, 16384);
+        const uint64_t da = tile_desc(base + R::A + (STATE ? 0 : (k % (R::SA ? R::SA : 1)) * R::TA), 16);
+        if constexpr (!STATE) {
+          if (!wait_both(&full_b[sb], k / R::SB, &full_a[k % R::SA], k / R::SA)) break;
+          fence_after();
+          // S: over the width, 64 at a time
+          const uint64_t db = tile_desc(base + R::B + sb * R::TA, 16);
+#pragma unroll
+          for (int i = 0; i < DK / 16; ++i) {
+            const uint32_t at = (i / 4 * 16384 + i % 4 * 32) >> 4;
+            mma_f16(R::S, da + at, db + at, kS, i > 0, one);
+          }
+          mma_commit(&s_ready, one);
+          mma_commit(&empty_b[sb], one);
+        }
+        const bool up = updates(k);
+        // where a chunk is not full, C's last rows have been blanked
+        if (sp.end - start_of(k) < kC && !wait_warp(&c_clean, blanked++)) break;
+        if (!(up ? wait_both(&full_c[sc], k / R::SC, &d_free, k + 1) : wait_warp(&full_c[sc], k / R::SC))) break;
+        if (up) {
+          bool ok = true;
+          for (int j = 0; j < kC / kSlot; ++j, ++slots) {
+            const int sk = slots % R::SK;
+            ok = wait_warp(&keys_ready[sk], slots / R::SK);
+            if (!ok) break;
+            fence_after();
+#pragma unroll
+            for (int p = 0; p < NK; ++p) {
+              // widths of 64: 64 rows of the state, and the same once more
+              const uint64_t dk = tile_desc(base + R::K + (sk * NK + p) * R::TK, DK == 64 ? 0 : kSlot * 128);
+#pragma unroll
+              for (int i = 0; i < kSlot / 16; ++i)
+                mma_f16(R::D, dk + i * (2048 >> 4), dc + (j * (kSlot / 16) + i) * (2048 >> 4), kD, j + p + i > 0, one);
+            }
+            mma_commit(&keys_free[sk], one);
+          }
           if (!ok) break;
+          mma_commit(&d_ready, one);
+          if (STATE) mma_commit(&empty_c[sc], one);
+        }
+        if constexpr (!STATE) {
+          if (!wait_both(&m_ready, k, &o_free, k + 1)) break;
+          fence_after();
+          const uint64_t dm = tile_desc(base + R::M, DK * 128);
+#pragma unroll
+          for (int i = 0; i < DK / 16; ++i)
+            mma_f16(R::O2, da + ((i / 4 * 16384 + i % 4 * 32) >> 4), dm + i * (2048 >> 4), kAM, i > 0, one);
+          mma_commit(&m_free, one);
+          mma_commit(&empty_a[k % R::SA], one);
+          if (!wait_warp(&p_ready, k)) break;
           fence_after();
 #pragma unroll
-          for (int p = 0; p < NK; ++p) {
-            // widths of 64: 64 rows of the state, and the same once more
-            const uint64_t dk = tile_desc(base + R::K + (sk * NK + p) * R::TK, DK == 64 ? 0 : kSlot * 128);
-#pragma unroll
-            for (int i = 0; i < kSlot / 16; ++i)
-              mma_f16(R::D, dk + i * (2048 >> 4), dc + (j * (kSlot / 16) + i) * (2048 >> 4), kD, j + p + i > 0, one);
-          }
-          mma_commit(&keys_free[sk], one);
+          for (int i = 0; i < kC / 16; ++i) mma_tmem_a(R::O1, R::S + i * 8, dc + i * (2048 >> 4), kPC, i > 0, one);
+          mma_commit(&o_ready, one);
+          mma_commit(&empty_c[sc], one);
         }
-        if (!ok) break;
-        mma_commit(&d_ready, one);
-        if (STATE) mma_commit(&empty_c[sc], one);
       }
-      if constexpr (!STATE) {
-        if (!wait_both(&m_ready, k, &o_free, k + 1)) break;
-        fence_after();
-        const uint64_t dm = tile_desc(base + R::M, DK * 128);
-#pragma unroll
-        for (int i = 0; i < DK / 16; ++i)
-          mma_f16(R::O2, da + ((i / 4 * 16384 + i % 4 * 32) >> 4), dm + i * (2048 >> 4), kAM, i > 0, one);
-        mma_commit(&m_free, one);
-        mma_commit(&empty_a[k % R::SA], one);
-        if (!wait_warp(&p_ready, k)) break;
-        fence_after();
-#pragma unroll
-        for (int i = 0; i < kC / 16; ++i) mma_tmem_a(R::O1, R::S + i * 8, dc + i * (2048 >> 4), kPC, i > 0, one);
-        mma_commit(&o_ready, one);
-        mma_commit(&empty_c[sc], one);
-      }
-    }
-    if (failed) {
-      mma_commit(&idle, one);
-      s4dev::mbar_wait(&idle, 0);
-    }
     }
   } else if (wid < 4 && !STATE) {
     const auto rows = [&](auto rev) {
@@ -596,7 +591,24 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   fence_before();
   __syncthreads();
   fence_after();
-  if (threadIdx.x == 0 && failed && st.w) s4dev::st_flag(st, s4dev::ST_STALL);
+  if (failed) {
+    // the copies and products in flight
+    if (threadIdx.x == 0 && st.w) s4dev::st_flag(st, s4dev::ST_STALL);
+    const auto drain = [](unsigned long long* bar, int issued, int stages) {
+      for (int j = issued > stages ? issued - stages : 0; j < issued; ++j)
+        s4dev::mbar_wait(&bar[j % stages], (unsigned)(j / stages) & 1);
+    };
+    drain(full_b, nb, R::SB);
+    if constexpr (!STATE) drain(full_a, na, R::SA);
+    drain(full_c, nc, R::SC);
+    if (wid == 9) {
+      mma_commit(&idle, elected());
+      s4dev::mbar_wait(&idle, 0);
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+  }
   if (wid == 9) tmem_free(tmem, R::COLS);
 }
 

@@ -171,8 +171,9 @@ __global__ void __launch_bounds__(256, 1)
     return r;
   };
 
+  int issued = 0;  // rounds of copies
   if (wid == 0 && elected()) {
-    int stage = 0, issued = 0;
+    int stage = 0;
     unsigned phase = 0;
     for (int t = blockIdx.x; t < tiles && !failed; t += gridDim.x) {
       const Tile at = tile_of(t);
@@ -198,13 +199,6 @@ __global__ void __launch_bounds__(256, 1)
           ++issued;
           if (++stage == S::STAGES) stage = 0, phase ^= 1;
         }
-      }
-    }
-    if (failed) {
-      // the copies in flight: the last round of each stage that has one
-      for (int i = 0; i < S::STAGES; ++i) {
-        const int rounds = (issued + S::STAGES - 1 - i) / S::STAGES;
-        if (rounds > 0) s4dev::mbar_wait(&full[i], (unsigned)(rounds - 1) & 1);
       }
     }
   } else if (wid == 1) {
@@ -234,10 +228,6 @@ __global__ void __launch_bounds__(256, 1)
       if (ok) mma_commit(&ready[buf], one);
       if (++buf == 2) buf = 0, buf_phase ^= 1;
     }
-    if (!ok) {
-      mma_commit(&idle, one);
-      s4dev::mbar_wait(&idle, 0);
-    }
   } else if (wid >= 4) {
     int buf = 0;
     unsigned buf_phase = 0;
@@ -257,7 +247,19 @@ __global__ void __launch_bounds__(256, 1)
   fence_before();
   __syncthreads();
   fence_after();
-  if (threadIdx.x == 0 && failed && st.w) s4dev::st_flag(st, s4dev::ST_STALL);
+  if (failed) {
+    // the copies and products in flight: the last rounds of the stages
+    if (threadIdx.x == 0 && st.w) s4dev::st_flag(st, s4dev::ST_STALL);
+    for (int j = issued > S::STAGES ? issued - S::STAGES : 0; j < issued; ++j)
+      s4dev::mbar_wait(&full[j % S::STAGES], (unsigned)(j / S::STAGES) & 1);
+    if (wid == 1) {
+      mma_commit(&idle, elected());
+      s4dev::mbar_wait(&idle, 0);
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+  }
   if (wid == 1) tmem_free(tmem, S::COLS);
 }
 

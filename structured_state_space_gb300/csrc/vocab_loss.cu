@@ -113,17 +113,17 @@ struct ToGrads {
 };
 
 // The values themselves, [splits][M][N] of T, or added to what is there (fp32).
-template <typename T, bool ADD>
+template <typename T, bool ADD, int BN>
 struct ToMatrix {
   T* out;
   int M, N;
   bool vec;
   __device__ __forceinline__ void operator()(long long row, int n, int split, uint32_t tmem) const {
-    T* to = out + ((long long)split * M + row) * N + n * kBN;
-    const int have = N - n * kBN;
+    T* to = out + ((long long)split * M + row) * N + n * BN;
+    const int have = N - n * BN;
     uint32_t r[32];
 #pragma unroll 1
-    for (int c = 0; c < kBN && c < have; c += 32) {
+    for (int c = 0; c < BN && c < have; c += 32) {
       tmem_ld32(tmem + c, r);
       if (row >= M) continue;
 #pragma unroll
@@ -288,26 +288,26 @@ void pairs_of(int n, Product* p) {
 }
 
 // result [M][N] = sum over k of A and B, in 64 k from chunk `first` on: A [M][k] or, A_MN, [k][M]; B likewise.
-template <bool A_MN, bool B_MN, typename Epilogue>
+template <bool A_MN, bool B_MN, int BN = kBN, typename Epilogue>
 cudaError_t multiply(const Operand& a, const Operand& b, long long M, long long N, int first, int chunks, int splits,
                      const Epilogue& ep, St st, cudaStream_t s) {
-  constexpr auto kernel = product_kernel<kBN, A_MN, B_MN, Epilogue>;
+  constexpr auto kernel = product_kernel<BN, A_MN, B_MN, Epilogue>;
   CUtensorMap ma, mb;
   if (!make_map(&ma, a.p, a.bf16, a.H, a.rows, a.planes, a.row, a.plane, A_MN ? kBK : 128) ||
-      !make_map(&mb, b.p, b.bf16, b.H, b.rows, b.planes, b.row, b.plane, B_MN ? kBK : kBN))
+      !make_map(&mb, b.p, b.bf16, b.H, b.rows, b.planes, b.row, b.plane, B_MN ? kBK : BN))
     return cudaErrorInvalidValue;
   Product p{};
   p.M = (int)M, p.N = (int)N;
-  p.tiles_m = (int)((M + 127) / 128), p.tiles_n = (int)((N + kBN - 1) / kBN);
+  p.tiles_m = (int)((M + 127) / 128), p.tiles_n = (int)((N + BN - 1) / BN);
   p.first = first, p.chunks = chunks;
   p.splits = splits;
   pairs_of(a.planes, &p);
-  p.what = instruction(a.bf16, A_MN, B_MN, 128, kBN);
+  p.what = instruction(a.bf16, A_MN, B_MN, 128, BN);
   p.limit = s4impl::wait_limit();
   const long long tiles = (long long)p.tiles_m * p.tiles_n * splits;
-  allow_shared<kernel>(Shape<kBN>::BYTES);
+  allow_shared<kernel>(Shape<BN>::BYTES);
   s4impl::TimedLaunch tl("vocab_loss", s);
-  kernel<<<(unsigned)(tiles < s4impl::num_sms() ? tiles : s4impl::num_sms()), 256, Shape<kBN>::BYTES, s>>>(ma, mb, p, ep, st);
+  kernel<<<(unsigned)(tiles < s4impl::num_sms() ? tiles : s4impl::num_sms()), 256, Shape<BN>::BYTES, s>>>(ma, mb, p, ep, st);
   return cudaGetLastError();
 }
 
@@ -373,9 +373,12 @@ long long piece_words(long long rows, int V, int planes) {
   const long long all = (V + kBN - 1ll) / kBN * kBN, pieces = (all + n - 1) / n;
   return (all / kBN + pieces - 1) / pieces * kBN;  // of nearly equal sizes
 }
+// Columns of the tiles of a product [M][N] (gradients of 8192 rows of 64 channels and 32000 words in fp32: with 64 columns 2.16
+// ms, with 256 2.35).
+int columns(long long N) { return N <= 64 ? 64 : N <= 128 ? 128 : 256; }
 // Shares of the sum over k of a product [M][N]: where its tiles are fewer than the SMs.
 int shares(long long M, long long N, long long k) {
-  const long long tiles = (M + 127) / 128 * ((N + kBN - 1) / kBN), chunks = chunks_of(k);
+  const long long tiles = (M + 127) / 128 * ((N + columns(N) - 1) / columns(N)), chunks = chunks_of(k);
   long long n = s4impl::num_sms() / tiles;
   if (n > chunks / 8) n = chunks / 8;
   return n < 1 ? 1 : (int)n;
@@ -386,23 +389,33 @@ constexpr int kExact = 64;  // chunks
 
 // out (+)= A B: in one product where it can go straight out (`part` is then not used, and nothing may be added later),
 // else as `splits` partial results in part [splits][M][N].
-template <typename T, bool A_MN, bool B_MN>
-cudaError_t sum_products(const Operand& a, const Operand& b, long long M, long long N, long long K, int splits, bool add,
-                         bool direct, T* out, float* part, St st, cudaStream_t s) {
+template <typename T, bool A_MN, int BN>
+cudaError_t sum_products_n(const Operand& a, const Operand& b, long long M, long long N, long long K, int splits, bool add,
+                           bool direct, T* out, float* part, St st, cudaStream_t s) {
   const int chunks = chunks_of(K), most = sizeof(T) == 4 ? kExact * splits : chunks;
   if (direct && chunks <= most) {
-    const ToMatrix<T, false> ep{out, (int)M, (int)N, N % 8 == 0 && vec_ok(out, sizeof(T), 16)};
-    return multiply<A_MN, B_MN>(a, b, M, N, 0, chunks, 1, ep, st, s);
+    const ToMatrix<T, false, BN> ep{out, (int)M, (int)N, N % 8 == 0 && vec_ok(out, sizeof(T), 16)};
+    return multiply<A_MN, true, BN>(a, b, M, N, 0, chunks, 1, ep, st, s);
   }
   const bool vec = N % 4 == 0 && vec_ok(part, 4, 16);
   for (int first = 0; first < chunks; first += most, add = true) {
     const int n = chunks - first < most ? chunks - first : most;
-    const cudaError_t err =
-        add ? multiply<A_MN, B_MN>(a, b, M, N, first, n, splits, ToMatrix<float, true>{part, (int)M, (int)N, vec}, st, s)
-            : multiply<A_MN, B_MN>(a, b, M, N, first, n, splits, ToMatrix<float, false>{part, (int)M, (int)N, vec}, st, s);
+    const ToMatrix<float, true, BN> more{part, (int)M, (int)N, vec};
+    const ToMatrix<float, false, BN> begin{part, (int)M, (int)N, vec};
+    const cudaError_t err = add ? multiply<A_MN, true, BN>(a, b, M, N, first, n, splits, more, st, s)
+                                : multiply<A_MN, true, BN>(a, b, M, N, first, n, splits, begin, st, s);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;
+}
+template <typename T, bool A_MN>
+cudaError_t sum_products(const Operand& a, const Operand& b, long long M, long long N, long long K, int splits, bool add,
+                         bool direct, T* out, float* part, St st, cudaStream_t s) {
+  switch (columns(N)) {
+    case 64: return sum_products_n<T, A_MN, 64>(a, b, M, N, K, splits, add, direct, out, part, st, s);
+    case 128: return sum_products_n<T, A_MN, 128>(a, b, M, N, K, splits, add, direct, out, part, st, s);
+    default: return sum_products_n<T, A_MN, 256>(a, b, M, N, K, splits, add, direct, out, part, st, s);
+  }
 }
 template <typename T>
 cudaError_t add_up(const float* part, int splits, long long n, T* out, cudaStream_t s) {
@@ -481,10 +494,10 @@ cudaError_t bwd_t(const s4_vocab_loss_bwd_args& a, St st, cudaStream_t s) {
     // the words' gradients: partial sums where there are shares; in fp32 else straight into dw, piece by piece of the rows
     T* to_w = static_cast<T*>(a.dw) + first * a.H;
     float* part_w = p.dw ? dw : std::is_same_v<T, float> ? reinterpret_cast<float*>(to_w) : nullptr;
-    err = sum_products<T, true, true>(gr, h, n, a.H, a.rows, p.dw_splits, false, !p.dw, to_w, part_w, st, s);
+    err = sum_products<T, true>(gr, h, n, a.H, a.rows, p.dw_splits, false, !p.dw, to_w, part_w, st, s);
     if (err == cudaSuccess && p.dw) err = add_up<T>(dw, p.dw_splits, n * a.H, to_w, s);
     if (err != cudaSuccess) return err;
-    err = sum_products<T, false, true>(gr, rows_from(w, first, n), a.rows, a.H, n, p.dh_splits, first > 0, !p.dh,
+    err = sum_products<T, false>(gr, rows_from(w, first, n), a.rows, a.H, n, p.dh_splits, first > 0, !p.dh,
                                        static_cast<T*>(a.dh), dh, st, s);
     if (err != cudaSuccess) return err;
   }
