@@ -5,6 +5,11 @@
 // over the tokens of a sequence in one direction, M being the state that the first of them sees (already
 // decayed once): forward (a, b, c) = (q, k, v); the gradients of q (dout, v, k), and from the
 // end, with the state's gradient as M, those of k (v, dout, q) and v (k, q, dout).
+//
+// Here the walks for all types, widths up to 256 and any strides, on warp-wide products; bfloat16 up to widths of
+// 128 at aligned strides goes to linear_attention_tiles.cu.  What bounds these is the latency of their
+// products and shared memory: 4 x 4096 tokens of 16 heads of 128 in bfloat16 1982 us for the three walks of a backward
+// pass (tiles: 215), 2 x 333 tokens of 6 heads of 48 and 80 in fp32 74 us.
 #include "linear_attention.cuh"
 
 namespace {
@@ -373,7 +378,7 @@ __global__ void __launch_bounds__(256) group_sum_kernel(Shared k, Shared v, int 
 // ---- one token -----------------------------------------------------------------------------------
 // The state is read and written once, everything else is small: the bound is memory.  A CTA has some
 // columns of one head's state, a thread V neighbouring ones of every RG-th row; the sums over rows
-// meet in shared memory.
+// meet in shared memory.  128 sequences of 32 heads of 128 x 128: 81 us (5.8 TB/s), with 8 rows on their way 91.
 template <typename T, int V>
 __global__ void __launch_bounds__(256) step_kernel(s4_linear_attention_args a, int lanes, int blocks, St st) {
   __shared__ float sums[256][V];

@@ -8,6 +8,10 @@
 // and its sum of exponentials, which a second kernel joins: 2 rows V H operations.  Backward: a piece of
 // the vocabulary at a time, the logits are formed again and leave as g in 16-bit terms, which two more
 // products take up: 6 rows V H operations.  The bound is the tensor cores.
+//
+// Measured in bfloat16: 1001 rows of 1024 channels and 32000 words 57 us forward (1.15 PFLOP/s), 8192 rows of 2048 and 50257 words
+// 4.79 ms for losses and gradients (1.41 PFLOP/s; the forward product alone 1.77, of 1.71 that a library's
+// sustains and 1.89 that it reaches in a burst).
 #include "s4_block.cuh"
 #include "s4_sequence.h"
 #include "tile_gemm.cuh"
