@@ -92,7 +92,7 @@ __device__ __forceinline__ void load_rows(__nv_bfloat16* s, const T* p, long lon
 template <typename T, int D, int C, bool STATE>
 __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ Walks ws, St st) {
   const Walk& w = ws.w[blockIdx.z];
-  constexpr int NP = kTerms<T>, NK = NP == 1 ? 2 : NP;  // terms of inputs, of scaled keys
+  constexpr int NP = kTerms<T>, NK = 3;  // terms of inputs, of scaled keys
   constexpr int RW = C / 16, CW = 4 / RW, NT = kCols / 8 / CW;  // warps along tokens and columns, column tiles each
   constexpr int MT = D / 64;                                    // tiles of 16 rows of M per warp
   constexpr int PA = D + 8, PC = kCols + 8, SA = C * PA, SC = C * PC, SM = D * PC;
@@ -274,46 +274,58 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ 
 
     // M' = e^{g n} M + sum_j e^{g (n - j)} b_j c_j^T; what is kept as the forward pass's state has decayed once less
     const int less = !STATE && at_end && !w.reverse ? 1 : 0;
+    // The chunk's part is summed up by itself, the smallest pairs of terms first, and added rounded: the tensor cores cut off
+    // what an addition shifts out, always towards zero, and a state that stayed in their accumulators would
+    // drift over long sequences (1.5e-5 after 56321 tokens in fp32).
     const float by = expm1f(g * (float)(n - less));
-    each([&](float& v, int, int, bool) { v = fmaf(v, by, v); });
-#pragma unroll 1
-    for (int k = 0; k < C; k += 16) {
-      float f[4];
+    float f[C / 16][4];
+#pragma unroll
+    for (int k = 0; k < C / 16; ++k)
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const int j = k + 2 * t4 + (x & 1) + (x >> 1) * 8;
-        f[x] = power(g, n - less - j < 0 ? 0 : n - less - j);  // (rows from n on are zeros)
+        const int j = 16 * k + 2 * t4 + (x & 1) + (x >> 1) * 8;
+        f[k][x] = power(g, n - less - j < 0 ? 0 : n - less - j);  // (rows from n on are zeros)
       }
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
+    for (int i = 0; i < MT; ++i) {
+      float d[8][4];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.f;
+#pragma unroll
+      for (int k = 0; k < C / 16; ++k) {
         unsigned fa[NK][4];
         unsigned raw[NP][4];
 #pragma unroll
         for (int p = 0; p < NP; ++p)
-          ldsm_t(raw[p], sb + p * SA + (k + (lane & 7) + (lane >> 4) * 8) * PA + m0 + 16 * i + (lane >> 3 & 1) * 8);
+          ldsm_t(raw[p], sb + p * SA + (16 * k + (lane & 7) + (lane >> 4) * 8) * PA + m0 + 16 * i + (lane >> 3 & 1) * 8);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           float u = 0.f, v = 0.f;
 #pragma unroll
           for (int p = NP - 1; p >= 0; --p) u += lo_of(raw[p][x]), v += hi_of(raw[p][x]);
           unsigned t[NK];
-          split<NK>(u * f[(x >> 1) * 2], v * f[(x >> 1) * 2 + 1], t);
+          split<NK>(u * f[k][(x >> 1) * 2], v * f[k][(x >> 1) * 2 + 1], t);
 #pragma unroll
           for (int p = 0; p < NK; ++p) fa[p][x] = t[p];
         }
 #pragma unroll
-        for (int j = 0; j < 8; j += 2)
+        for (int j = 0; j < 8; j += 2) {
+          unsigned fb[NP][4];
 #pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            unsigned fb[4];
-            ldsm_t(fb, sc + p * SC + (k + (lane & 15)) * PC + 8 * j + (lane >> 4) * 8);
+          for (int p = 0; p < NP; ++p) ldsm_t(fb[p], sc + p * SC + (16 * k + (lane & 15)) * PC + 8 * j + (lane >> 4) * 8);
 #pragma unroll
-            for (int u = 0; u + p < NK; ++u) {
-              mma(m[i][j], fa[u], fb[0], fb[1]);
-              mma(m[i][j + 1], fa[u], fb[2], fb[3]);
+          for (int sum = NK - 1; sum >= 0; --sum)
+#pragma unroll
+            for (int p = 0; p < NP && p <= sum; ++p) {
+              mma(d[j], fa[sum - p], fb[p][0], fb[p][1]);
+              mma(d[j + 1], fa[sum - p], fb[p][2], fb[p][3]);
             }
-          }
+        }
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m[i][j][e] = fmaf(m[i][j][e], by, m[i][j][e]) + d[j][e];
     }
   }
   if (STATE) {
@@ -604,6 +616,7 @@ cudaError_t fwd_t(const s4_linear_attention_args& a, St st, cudaStream_t s) {
 
 template <typename T>
 cudaError_t bwd_t(const s4_linear_attention_bwd_args& a, St st, cudaStream_t s) {
+  constexpr int code = std::is_same_v<T, float> ? S4_F32 : std::is_same_v<T, __half> ? S4_F16 : S4_BF16;
   const int each = a.H / a.G;
   char* at = static_cast<char*>(a.ws) + s4impl::kStatusBytes;
   const auto take = [&](size_t bytes) {
@@ -645,10 +658,14 @@ cudaError_t bwd_t(const s4_linear_attention_bwd_args& a, St st, cudaStream_t s) 
       w.out = out.p, w.out_batch = out.batch, w.out_row = out.row, w.out_head = out.head;
     }
   }
+  // All in one launch where that does not cost more than the launches that it saves: tiles of one shape, or so few walks that
+  // they leave SMs idle (2 x 333 tokens of 6 heads of 48 and 80 in fp32 74 us; a launch each 215).
+  const auto size = [](int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; };
+  const long long walks = 3ll * a.batch * a.H * ((a.K < a.V ? a.K : a.V) + kCols - 1) / kCols;
   cudaError_t err;
-  if ((a.K <= 64) == (a.V <= 64) || std::is_same_v<T, float> || std::is_same_v<T, __half>) {
+  if (size(a.K) == size(a.V) || (!s4impl::tiles_take(dk, code) && walks * segments(walks, a.L) <= 3ll * s4impl::num_sms())) {
     err = walk_t<T>(ws, 3, st, s);
-  } else {  // two shapes of tiles
+  } else {
     Walks two = ws, one{};
     two.w[1] = dq;
     one.w[0] = dv;

@@ -202,3 +202,30 @@ def test_a_length_or_slot_out_of_range():
                                     ws=ws)
     assert s4.STATUS[s4.s4_get_status(ws)] == "S4_ERR_INVALID_INDEX"
     assert not o[1].any() and o[0].any() and o[2].any()
+
+
+def test_long_sums_in_float32():
+    """A long sequence of slow decay: the state of 40000 tokens, and their gradients, against float64 sums on the GPU."""
+    L, K, V = 40000, 100, 34
+    r, q, k, v, g = make(10, 1, L, 1, 1, K, V, torch.float32)
+    g = torch.tensor([-1e-4], device="cuda")
+    do, out = r.normal(1, L, 1, V), torch.zeros(1, 1, K, V, device="cuda")
+    o = s4.s4_linear_attention_fwd(q, k, v, g, state_out=out)
+    got = s4.s4_linear_attention_bwd(q, k, v, g, do)
+    q, k, v, do = (t[0, :, 0].double() for t in (q, k, v, do))
+    i = torch.arange(L, device="cuda")
+    g64 = g.double().item()
+    close(out[0, 0], to64((k * torch.exp(g64 * (L - 1 - i))[:, None]).t() @ v), "state")
+    # (blocks of rows of the whole matrix of weights)
+    want = {n: torch.zeros_like(t) for n, t in (("dq", q), ("dk", k), ("dv", v), ("o", v))}
+    for a in range(0, L, 4000):
+        rows = slice(a, a + 4000)
+        lag = i[rows, None] - i
+        w = torch.where(lag >= 0, torch.exp(g64 * lag.clamp(min=0)), 0.0) * K ** -0.5
+        want["o"][rows] = ((q[rows] @ k.t()) * w) @ v
+        want["dq"][rows] = ((do[rows] @ v.t()) * w) @ k
+        want["dk"] += ((do[rows] @ v.t()) * w).t() @ q[rows]
+        want["dv"] += ((q[rows] @ k.t()) * w).t() @ do[rows]
+    close(o[0, :, 0], to64(want["o"]), "o")
+    for n in ("dq", "dk", "dv"):
+        close(got[n][0, :, 0], to64(want[n]), n)
