@@ -278,21 +278,19 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ 
     // what an addition shifts out, always towards zero, and a state that stayed in their accumulators would
     // drift over long sequences (1.5e-5 after 56321 tokens in fp32).
     const float by = expm1f(g * (float)(n - less));
-    float f[C / 16][4];
-#pragma unroll
-    for (int k = 0; k < C / 16; ++k)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int j = 16 * k + 2 * t4 + (x & 1) + (x >> 1) * 8;
-        f[k][x] = power(g, n - less - j < 0 ? 0 : n - less - j);  // (rows from n on are zeros)
-      }
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       float d[8][4];
 #pragma unroll
       for (int j = 0; j < 8; ++j) d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.f;
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < C / 16; ++k) {
+        float f[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int j = 16 * k + 2 * t4 + (x & 1) + (x >> 1) * 8;
+          f[x] = power(g, n - less - j < 0 ? 0 : n - less - j);  // (rows from n on are zeros)
+        }
         unsigned fa[NK][4];
         unsigned raw[NP][4];
 #pragma unroll
@@ -304,7 +302,7 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ 
 #pragma unroll
           for (int p = NP - 1; p >= 0; --p) u += lo_of(raw[p][x]), v += hi_of(raw[p][x]);
           unsigned t[NK];
-          split<NK>(u * f[k][(x >> 1) * 2], v * f[k][(x >> 1) * 2 + 1], t);
+          split<NK>(u * f[(x >> 1) * 2], v * f[(x >> 1) * 2 + 1], t);
 #pragma unroll
           for (int p = 0; p < NK; ++p) fa[p][x] = t[p];
         }
