@@ -504,7 +504,7 @@ typedef struct {
     const float* log_decay;
     const int* lengths;
     const float *state0, *dstate;
-    float* dstate0;           /* not the array dstate */
+    float* dstate0;           /* neither the array dstate nor state0 */
     void* ws;                 /* s4_linear_attention_bwd_workspace_bytes */
     size_t ws_bytes;
     float scale;              /* not 0 */

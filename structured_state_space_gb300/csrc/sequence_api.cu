@@ -89,7 +89,7 @@ s4_status s4_linear_attention_bwd(const s4_linear_attention_bwd_args* a, void* s
       if (i->p == r->p) return S4_ERR_INVALID_ARG;
   }
   if (!a->log_decay || !aligned(a->log_decay, 4) || !aligned(a->lengths, 4) || !aligned(a->state0, 4) ||
-      !aligned(a->dstate, 4) || !aligned(a->dstate0, 4) || (a->dstate0 && a->dstate0 == a->dstate))
+      !aligned(a->dstate, 4) || !aligned(a->dstate0, 4) || (a->dstate0 && (a->dstate0 == a->dstate || a->dstate0 == a->state0)))
     return S4_ERR_INVALID_ARG;
   const s4_status w =
       ws_ok(a->ws, a->ws_bytes, s4_linear_attention_bwd_workspace_bytes(a->batch, a->L, a->H, a->G, a->K, a->V));
