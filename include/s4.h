@@ -444,7 +444,8 @@ s4_status s4_block_norm_bwd(const s4_block_norm_bwd_args* a, void* stream);
  *  - Arrays of heads are [batch][L][heads][width], given as s4_heads: the address of
  *    element (0, 0, 0, 0) and the strides of the batch, the tokens and the heads
  *    in elements; a head's channels are contiguous.  A slice of a projection's
- *    output is passed as it lies.
+ *    output is passed as it lies.  Inputs may be broadcast (strides of 0), outputs not: an output's
+ *    stride of 0 in a dimension of more than one is refused.
  *  - Sums, states, norms and the statistics of the softmax are fp32, outputs are
  *    rounded once.  Products run on the tensor cores with operands of 16 bits: bfloat16
  *    inputs as they are; float16 and fp32 inputs, and what must not lose

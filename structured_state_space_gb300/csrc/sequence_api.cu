@@ -21,6 +21,10 @@ template <typename Heads>
 bool heads_ok(const Heads& r, int dtype) {
   return r.p && aligned(r.p, s4impl::dtype_bytes(dtype)) && r.batch >= 0 && r.row >= 0 && r.head >= 0;
 }
+// The same of an output, whose elements lie apart: no stride of 0 in a dimension of more than one.
+bool out_ok(const s4_heads_out& r, int dtype, int batch, int L, int heads) {
+  return heads_ok(r, dtype) && (batch == 1 || r.batch > 0) && (L == 1 || r.row > 0) && (heads == 1 || r.head > 0);
+}
 bool tokens_ok(int batch, int L, int H, int G) {
   return batch >= 1 && batch <= kMaxBatch && L >= 1 && L <= kMaxLen && H >= 1 && H <= kMaxHeads && G >= 1 && G <= H;
 }
@@ -54,9 +58,10 @@ size_t s4_linear_attention_workspace_bytes(int batch, int L, int H, int G, int K
 
 s4_status s4_linear_attention_fwd(const s4_linear_attention_args* a, void* stream) {
   if (!a || !s4impl::dtype_ok(a->dtype) || !attention_ok(a->batch, a->L, a->H, a->G, a->K, a->V)) return S4_ERR_INVALID_ARG;
-  if (!heads_ok(a->q, a->dtype) || !heads_ok(a->k, a->dtype) || !heads_ok(a->v, a->dtype) || !heads_ok(a->o, a->dtype) ||
-      a->o.p == a->q.p || a->o.p == a->k.p || a->o.p == a->v.p || !a->log_decay || !aligned(a->log_decay, 4) ||
-      !aligned(a->lengths, 4) || !aligned(a->index, 4) || !aligned(a->state, 4) || !aligned(a->state_out, 4))
+  if (!heads_ok(a->q, a->dtype) || !heads_ok(a->k, a->dtype) || !heads_ok(a->v, a->dtype) ||
+      !out_ok(a->o, a->dtype, a->batch, a->L, a->H) || a->o.p == a->q.p || a->o.p == a->k.p || a->o.p == a->v.p ||
+      !a->log_decay || !aligned(a->log_decay, 4) || !aligned(a->lengths, 4) || !aligned(a->index, 4) || !aligned(a->state, 4) ||
+      !aligned(a->state_out, 4))
     return S4_ERR_INVALID_ARG;
   if ((a->state || a->state_out) && (a->slots < 1 || (!a->index && a->slots < a->batch))) return S4_ERR_INVALID_ARG;
   const size_t need = s4_linear_attention_workspace_bytes(a->batch, a->L, a->H, a->G, a->K, a->V);
@@ -84,7 +89,7 @@ s4_status s4_linear_attention_bwd(const s4_linear_attention_bwd_args* a, void* s
   for (const s4_heads* r : in)
     if (!heads_ok(*r, a->dtype)) return S4_ERR_INVALID_ARG;
   for (const s4_heads_out* r : out) {
-    if (!heads_ok(*r, a->dtype)) return S4_ERR_INVALID_ARG;
+    if (!out_ok(*r, a->dtype, a->batch, a->L, r == &a->dq ? a->H : a->G)) return S4_ERR_INVALID_ARG;
     for (const s4_heads* i : in)
       if (i->p == r->p) return S4_ERR_INVALID_ARG;
   }
@@ -106,8 +111,8 @@ s4_status s4_rotary(const s4_rotary_args* a, void* stream) {
       2 * a->R > a->D || (a->k.p ? a->G < 1 || a->G > kMaxHeads : a->G != 0) || !a->freqs || !aligned(a->freqs, 8) ||
       !aligned(a->positions, 4) || a->positions_batch < 0)
     return S4_ERR_INVALID_ARG;
-  if (!heads_ok(a->q, a->dtype) || !heads_ok(a->q_out, a->dtype) || !a->k.p != !a->k_out.p ||
-      (a->k.p && (!heads_ok(a->k, a->dtype) || !heads_ok(a->k_out, a->dtype))))
+  if (!heads_ok(a->q, a->dtype) || !out_ok(a->q_out, a->dtype, a->batch, a->L, a->H) || !a->k.p != !a->k_out.p ||
+      (a->k.p && (!heads_ok(a->k, a->dtype) || !out_ok(a->k_out, a->dtype, a->batch, a->L, a->G))))
     return S4_ERR_INVALID_ARG;
   // in place: each head at its own address (else one would replace another that is still needed)
   const auto in_place_ok = [&](const s4_heads& i, const s4_heads_out& o, int heads) {
@@ -125,7 +130,7 @@ s4_status s4_layer_norm_fwd(const s4_layer_norm_args* a, void* stream) {
     return S4_ERR_INVALID_ARG;
   const int e = s4impl::dtype_bytes(a->dtype);
   if (!a->x || !a->y || !aligned(a->x, e) || !aligned(a->y, e) || !aligned(a->w, 4) || !aligned(a->b, 4) || a->x_row < 0 ||
-      a->y_row < 0 || (a->y == a->x && a->rows > 1 && a->y_row != a->x_row))
+      a->y_row < 0 || (a->rows > 1 && (a->y_row == 0 || (a->y == a->x && a->y_row != a->x_row))))
     return S4_ERR_INVALID_ARG;
   return cuda_status(s4impl::launch_layer_norm(*a, static_cast<cudaStream_t>(stream)));
 }
@@ -142,7 +147,7 @@ s4_status s4_layer_norm_bwd(const s4_layer_norm_bwd_args* a, void* stream) {
   const int e = s4impl::dtype_bytes(a->dtype);
   if (!a->x || !a->dy || !a->dx || !aligned(a->x, e) || !aligned(a->dy, e) || !aligned(a->dx, e) || !aligned(a->w, 4) ||
       !aligned(a->dw, 4) || !aligned(a->db, 4) || a->x_row < 0 || a->dy_row < 0 || a->dx_row < 0 || a->dx == a->x ||
-      a->dx == a->dy)
+      a->dx == a->dy || (a->rows > 1 && a->dx_row == 0))
     return S4_ERR_INVALID_ARG;
   const s4_status w = ws_ok(a->ws, a->ws_bytes, s4_layer_norm_bwd_workspace_bytes(a->rows, a->H));
   if (w != S4_OK) return w;

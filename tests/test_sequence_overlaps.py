@@ -46,3 +46,39 @@ def test_a_states_gradient_is_neither_state(lib):
     assert gradients(lib, dstate0=9 * A) == 1
     assert gradients(lib, dstate0=8 * A) == 1
     assert gradients(lib, dstate0=8 * A, dstate=0) == 1
+
+
+def test_outputs_of_one_address_for_many_elements_are_refused(lib):
+    """A stride of 0 in a dimension of more than one: an output's elements would replace one another, and in place a
+    broadcast head would be turned once for each head that shares it."""
+    # attention: q, k, v, o; ...; ws, its bytes (too few); scale; batch L H G K V slots dtype
+    ok = [x for i in range(4) for x in (A * (i + 1), 64, 16, 8)] + [A, 0, 0, 0, 0, A, 100, 1.0, 2, 4, 2, 2, 8, 8, 0, 1]
+    assert call(lib, "s4_linear_attention_fwd", sequence._ATTENTION, ok) == 2
+    for at in (13, 14, 15):
+        v = list(ok)
+        v[at] = 0
+        assert call(lib, "s4_linear_attention_fwd", sequence._ATTENTION, v) == 1, at
+        v[at - 12] = 0
+        v[at] = ok[at]
+        assert call(lib, "s4_linear_attention_fwd", sequence._ATTENTION, v) == 2, at  # inputs may be broadcast
+        v[at], v[{13: 24, 14: 25, 15: 26}[at]] = 0, 1  # one element has any stride
+        v[27] = 1
+        if at != 14:  # (a token is another form, which takes this workspace)
+            assert call(lib, "s4_linear_attention_fwd", sequence._ATTENTION, v) == 2, at
+    for first in (16, 20, 24):
+        for at in range(first + 1, first + 4):
+            v = list(GRADIENTS)
+            v[at] = 0
+            assert call(lib, "s4_linear_attention_bwd", sequence._ATTENTION_BWD, v) == 1, at
+    # rotary, in place: q, k, q_out, k_out; freqs, positions, batch stride; amplitude; batch L H G D R pairs inverse dtype
+    ok = [A, 64, 16, 8, 2 * A, 64, 16, 8, A, 64, 16, 8, 2 * A, 64, 16, 8, A, 0, 0, 1.0, 2, 4, 2, 2, 8, 4, 0, 0, 1]
+    for at in (1, 2, 3, 5, 6, 7):
+        v = list(ok)
+        v[at] = v[at + 8] = 0
+        assert call(lib, "s4_rotary", sequence._ROTARY, v) == 1, at
+    # layer norm: x, y, w, b; x_row, y_row, rows; eps; H dtype
+    assert call(lib, "s4_layer_norm_fwd", sequence._LAYER_NORM, [A, 2 * A, 0, 0, 8, 0, 4, 1e-5, 8, 1]) == 1
+    assert call(lib, "s4_layer_norm_fwd", sequence._LAYER_NORM, [A, A, 0, 0, 0, 0, 4, 1e-5, 8, 1]) == 1
+    ok = [A, 2 * A, 3 * A, 0, 4 * A, 5 * A, A, 100, 8, 8, 8, 4, 1e-5, 8, 1]
+    assert call(lib, "s4_layer_norm_bwd", sequence._LAYER_NORM_BWD, ok) == 2
+    assert call(lib, "s4_layer_norm_bwd", sequence._LAYER_NORM_BWD, ok[:10] + [0] + ok[11:]) == 1
