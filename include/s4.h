@@ -508,7 +508,7 @@ typedef struct {
     float* dstate0;           /* neither the array dstate nor state0 */
     void* ws;                 /* s4_linear_attention_bwd_workspace_bytes */
     size_t ws_bytes;
-    float scale;              /* not 0 */
+    float scale;              /* finite, and 1 / scale too (states' gradients go in units of it) */
     int batch, L, H, G, K, V, dtype;
 } s4_linear_attention_bwd_args;
 size_t s4_linear_attention_bwd_workspace_bytes(int batch, int L, int H, int G, int K, int V);

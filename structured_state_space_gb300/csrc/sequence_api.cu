@@ -3,6 +3,8 @@
 #include <limits.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "s4.h"
 #include "s4_sequence.h"
 
@@ -82,7 +84,8 @@ size_t s4_linear_attention_bwd_workspace_bytes(int batch, int L, int H, int G, i
 }
 
 s4_status s4_linear_attention_bwd(const s4_linear_attention_bwd_args* a, void* stream) {
-  if (!a || !s4impl::dtype_ok(a->dtype) || !attention_ok(a->batch, a->L, a->H, a->G, a->K, a->V) || a->scale == 0.f)
+  if (!a || !s4impl::dtype_ok(a->dtype) || !attention_ok(a->batch, a->L, a->H, a->G, a->K, a->V) ||
+      !std::isfinite(a->scale) || !std::isfinite(1.f / a->scale))
     return S4_ERR_INVALID_ARG;
   const s4_heads* in[] = {&a->q, &a->k, &a->v, &a->dout};
   const s4_heads_out* out[] = {&a->dq, &a->dk, &a->dv};

@@ -82,3 +82,10 @@ def test_outputs_of_one_address_for_many_elements_are_refused(lib):
     ok = [A, 2 * A, 3 * A, 0, 4 * A, 5 * A, A, 100, 8, 8, 8, 4, 1e-5, 8, 1]
     assert call(lib, "s4_layer_norm_bwd", sequence._LAYER_NORM_BWD, ok) == 2
     assert call(lib, "s4_layer_norm_bwd", sequence._LAYER_NORM_BWD, ok[:10] + [0] + ok[11:]) == 1
+
+
+def test_a_gradients_scale_has_an_inverse(lib):
+    """The state's gradient goes through the walks in units of the scale; 1 / 2e-39 is an infinity in 32 bits."""
+    at = 35
+    for scale, code in ((1.0, 2), (-0.3, 2), (3e-39, 2), (0.0, 1), (2e-39, 1), (-1e-45, 1), (float("nan"), 1), (float("inf"), 1)):
+        assert call(lib, "s4_linear_attention_bwd", sequence._ATTENTION_BWD, GRADIENTS[:at] + [scale] + GRADIENTS[at + 1:]) == code, scale
