@@ -571,7 +571,8 @@ s4_status s4_layer_norm_bwd(const s4_layer_norm_bwd_args* a, void* stream);
  * weights w [V][H], without keeping the logits:
  *     x = w h,  lse = log sum_v exp(x_v),  loss = lse - x_target.
  * A row whose target is negative has a loss of 0 (its lse is formed all the same); a target
- * >= V is recorded as S4_ERR_INVALID_INDEX and counts as a negative one.
+ * >= V is recorded as S4_ERR_INVALID_INDEX and counts as a negative one.  Hidden states of rows without a
+ * target may hold anything (padding): what they hold, NaN too, reaches their own lse only.
  * 1 <= rows <= 2^22, 1 <= H <= 16384, 1 <= V <= 2^22.
  */
 typedef struct {

@@ -118,13 +118,21 @@ struct Shape {
   static constexpr int COLS = 2 * BN;                                       // of tensor memory: two accumulators
 };
 
+// Which k of a product do not count, a bit for each of a chunk's, and whether there are any in chunks [from, to): none.
+struct AllCount {
+  __device__ __forceinline__ unsigned long long out(int) const { return 0; }
+  __device__ __forceinline__ bool any(int, int) const { return false; }
+};
+
 // 256 threads: warp 0 brings the operands, warp 1 issues the products, warps 4 to 7 take the results
-// from one accumulator while the other is filled.  Every wait is bounded; where one gives up the CTA
-// records a stall, waits for its copies and products in flight, frees its tensor memory and leaves.
-template <int BN, bool A_MN, bool B_MN, typename Epilogue>
+// from one accumulator while the other is filled.  Where some k do not count (with an MN-major B), A is zero there
+// and B may hold anything, NaN too: warp 1 blanks B's rows of them in shared memory before it multiplies.  Every wait
+// is bounded; where one gives up the CTA records a stall, waits for its copies and products in flight, frees
+// its tensor memory and leaves.
+template <int BN, bool A_MN, bool B_MN, typename Epilogue, typename Counts>
 __global__ void __launch_bounds__(256, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Product p,
-                   const Epilogue ep, s4impl::St st) {
+                   const Epilogue ep, const Counts counts, s4impl::St st) {
   using S = Shape<BN>;
   extern __shared__ char raw[];
   __shared__ unsigned long long full[S::STAGES], empty[S::STAGES], ready[2], taken[2], idle;
@@ -209,6 +217,7 @@ __global__ void __launch_bounds__(256, 1)
     bool ok = true;
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
       const Tile at = tile_of(t);
+      const bool blanks = counts.any(at.from, at.to);
       ok = wait_warp(&taken[buf], buf_phase ^ 1);
       fence_after();
       const uint32_t d = tmem + buf * BN;
@@ -218,6 +227,14 @@ __global__ void __launch_bounds__(256, 1)
         if (!ok) break;
         fence_after();
         const uint32_t a = s4dev::smem_u32(smem) + stage * S::STAGE, b = a + S::A;
+        if (blanks) {
+          // a row of k has 128 bytes in each block of 64 columns: 16 bytes a lane
+          char* at_lane = smem + stage * S::STAGE + S::A + lane / 8 * 8192 + lane % 8 * 16;
+          for (unsigned long long left = counts.out(at.from + i % (at.to - at.from)); left; left &= left - 1)
+            if (lane < BN / 8) *reinterpret_cast<uint4*>(at_lane + (__ffsll(left) - 1) * 128) = make_uint4(0, 0, 0, 0);
+          s4dev::fence_proxy_async();
+          __syncwarp();
+        }
         const uint64_t da = tile_desc(a, A_MN ? 8192 : 16), db = tile_desc(b, B_MN ? 8192 : 16);
 #pragma unroll
         for (int k = 0; k < kBK / 16; ++k)

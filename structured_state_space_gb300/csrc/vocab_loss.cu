@@ -32,6 +32,19 @@ __device__ __forceinline__ long long target_of(const void* targets, int wide, lo
   return t < 0 ? -1 : t;
 }
 
+// Rows without a target whose hidden states are not finite, a bit each: their gradients of logits are zeros, and what they
+// hold (padding may be NaN) is not to reach dw.
+struct Padding {
+  const unsigned long long* bits;  // [rows / 64, rounded up]
+  __device__ __forceinline__ unsigned long long out(int chunk) const { return rd(bits + chunk); }
+  __device__ __forceinline__ bool any(int from, int to) const {
+    bool some = false;
+    for (int c = from + (int)(threadIdx.x & 31); c < to; c += 32) some |= rd(bits + c) != 0;
+    return __any_sync(0xffffffffu, some);
+  }
+};
+size_t padding_bytes(long long rows) { return s4impl::align256((size_t)(rows + 127) / 128 * 16); }
+
 // ---- what becomes of a tile ---------------------------------------------------------------------------
 // The maximum and the sum of exponentials (from it) of a row's logits in the tile, and the target's logit.
 struct ToSums {
@@ -75,6 +88,7 @@ struct ToSums {
 template <int NP>
 struct ToGrads {
   __nv_bfloat16* g;
+  unsigned* padding;    // see Padding, a word for the rows of a warp
   const float *lse, *dloss;
   const void* targets;
   int wide, V, first;   // the piece's first word
@@ -85,7 +99,12 @@ struct ToGrads {
     const long long t = live ? target_of(targets, wide, row, V, st) : -1;
     const int base = first + n * kBN, have = V - base < kBN ? V - base : kBN;
     const int want = t >= base && t < base + kBN ? (int)(t - base) : -1;
-    const float by = t >= 0 ? rd(dloss + row) : 0.f, off = t >= 0 ? rd(lse + row) * -kLog2e : 0.f;
+    const float by = t >= 0 ? rd(dloss + row) : 0.f, off = live ? rd(lse + row) * -kLog2e : 0.f;
+    if (n == 0) {
+      // a row that is not finite has no finite logit, so no finite lse
+      const unsigned bits = __ballot_sync(0xffffffffu, live && t < 0 && !(fabsf(off) < INFINITY));
+      if ((threadIdx.x & 31) == 0) wr(padding + row / 32, bits);
+    }
     __nv_bfloat16* to = g + row * pitch + n * kBN;
     uint32_t r[32];
 #pragma unroll 1
@@ -292,10 +311,10 @@ void pairs_of(int n, Product* p) {
 }
 
 // result [M][N] = sum over k of A and B, in 64 k from chunk `first` on: A [M][k] or, A_MN, [k][M]; B likewise.
-template <bool A_MN, bool B_MN, int BN = kBN, typename Epilogue>
+template <bool A_MN, bool B_MN, int BN = kBN, typename Epilogue, typename Counts = AllCount>
 cudaError_t multiply(const Operand& a, const Operand& b, long long M, long long N, int first, int chunks, int splits,
-                     const Epilogue& ep, St st, cudaStream_t s) {
-  constexpr auto kernel = product_kernel<BN, A_MN, B_MN, Epilogue>;
+                     const Epilogue& ep, St st, cudaStream_t s, const Counts& counts = {}) {
+  constexpr auto kernel = product_kernel<BN, A_MN, B_MN, Epilogue, Counts>;
   CUtensorMap ma, mb;
   if (!make_map(&ma, a.p, a.bf16, a.H, a.rows, a.planes, a.row, a.plane, A_MN ? kBK : 128) ||
       !make_map(&mb, b.p, b.bf16, b.H, b.rows, b.planes, b.row, b.plane, B_MN ? kBK : BN))
@@ -311,7 +330,7 @@ cudaError_t multiply(const Operand& a, const Operand& b, long long M, long long 
   const long long tiles = (long long)p.tiles_m * p.tiles_n * splits;
   allow_shared<kernel>(Shape<BN>::BYTES);
   s4impl::TimedLaunch tl("vocab_loss", s);
-  kernel<<<(unsigned)(tiles < s4impl::num_sms() ? tiles : s4impl::num_sms()), 256, Shape<BN>::BYTES, s>>>(ma, mb, p, ep, st);
+  kernel<<<(unsigned)(tiles < s4impl::num_sms() ? tiles : s4impl::num_sms()), 256, Shape<BN>::BYTES, s>>>(ma, mb, p, ep, counts, st);
   return cudaGetLastError();
 }
 
@@ -393,32 +412,32 @@ constexpr int kExact = 64;  // chunks
 
 // out (+)= A B: in one product where it can go straight out (`part` is then not used, and nothing may be added later),
 // else as `splits` partial results in part [splits][M][N].
-template <typename T, bool A_MN, int BN>
+template <typename T, bool A_MN, int BN, typename Counts>
 cudaError_t sum_products_n(const Operand& a, const Operand& b, long long M, long long N, long long K, int splits, bool add,
-                           bool direct, T* out, float* part, St st, cudaStream_t s) {
+                           bool direct, T* out, float* part, St st, cudaStream_t s, const Counts& counts) {
   const int chunks = chunks_of(K), most = sizeof(T) == 4 ? kExact * splits : chunks;
   if (direct && chunks <= most) {
     const ToMatrix<T, false, BN> ep{out, (int)M, (int)N, N % 8 == 0 && vec_ok(out, sizeof(T), 16)};
-    return multiply<A_MN, true, BN>(a, b, M, N, 0, chunks, 1, ep, st, s);
+    return multiply<A_MN, true, BN>(a, b, M, N, 0, chunks, 1, ep, st, s, counts);
   }
   const bool vec = N % 4 == 0 && vec_ok(part, 4, 16);
   for (int first = 0; first < chunks; first += most, add = true) {
     const int n = chunks - first < most ? chunks - first : most;
     const ToMatrix<float, true, BN> more{part, (int)M, (int)N, vec};
     const ToMatrix<float, false, BN> begin{part, (int)M, (int)N, vec};
-    const cudaError_t err = add ? multiply<A_MN, true, BN>(a, b, M, N, first, n, splits, more, st, s)
-                                : multiply<A_MN, true, BN>(a, b, M, N, first, n, splits, begin, st, s);
+    const cudaError_t err = add ? multiply<A_MN, true, BN>(a, b, M, N, first, n, splits, more, st, s, counts)
+                                : multiply<A_MN, true, BN>(a, b, M, N, first, n, splits, begin, st, s, counts);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;
 }
-template <typename T, bool A_MN>
+template <typename T, bool A_MN, typename Counts = AllCount>
 cudaError_t sum_products(const Operand& a, const Operand& b, long long M, long long N, long long K, int splits, bool add,
-                         bool direct, T* out, float* part, St st, cudaStream_t s) {
+                         bool direct, T* out, float* part, St st, cudaStream_t s, const Counts& counts = {}) {
   switch (columns(N)) {
-    case 64: return sum_products_n<T, A_MN, 64>(a, b, M, N, K, splits, add, direct, out, part, st, s);
-    case 128: return sum_products_n<T, A_MN, 128>(a, b, M, N, K, splits, add, direct, out, part, st, s);
-    default: return sum_products_n<T, A_MN, 256>(a, b, M, N, K, splits, add, direct, out, part, st, s);
+    case 64: return sum_products_n<T, A_MN, 64>(a, b, M, N, K, splits, add, direct, out, part, st, s, counts);
+    case 128: return sum_products_n<T, A_MN, 128>(a, b, M, N, K, splits, add, direct, out, part, st, s, counts);
+    default: return sum_products_n<T, A_MN, 256>(a, b, M, N, K, splits, add, direct, out, part, st, s, counts);
   }
 }
 template <typename T>
@@ -432,7 +451,7 @@ cudaError_t add_up(const float* part, int splits, long long n, T* out, cudaStrea
 struct Plan {
   long long words, pieces;
   int dh_splits, dw_splits;
-  size_t g, dh, dw;  // bytes
+  size_t g, dh, dw, padding;  // bytes
 };
 template <typename Args>
 Plan plan_of(const Args& a) {
@@ -443,6 +462,7 @@ Plan plan_of(const Args& a) {
   p.g = s4impl::align256(2ull * np * a.rows * p.words);
   p.dh = p.pieces > 1 || p.dh_splits > 1 || a.dtype == S4_F32 ? s4impl::align256(4ull * p.dh_splits * a.rows * a.H) : 0;
   p.dw = p.dw_splits > 1 ? s4impl::align256(4ull * p.dw_splits * p.words * a.H) : 0;
+  p.padding = padding_bytes(a.rows);
   return p;
 }
 
@@ -458,6 +478,8 @@ cudaError_t bwd_t(const s4_vocab_loss_bwd_args& a, St st, cudaStream_t s) {
   at += p.dh;
   float* dw = reinterpret_cast<float*>(at);
   at += p.dw;
+  unsigned* padding = reinterpret_cast<unsigned*>(at);
+  at += p.padding;
   Operand h, w, lh, lw;
   cudaError_t err = operand<T>(a.h, a.h_row, a.rows, a.H, NP, &at, &h, s);
   if (err != cudaSuccess) return err;
@@ -479,6 +501,7 @@ cudaError_t bwd_t(const s4_vocab_loss_bwd_args& a, St st, cudaStream_t s) {
   x.scratch(g, 2, NP * a.rows * words);
   if (p.dh) x.scratch(dh, 4, p.dh_splits * a.rows * a.H);
   if (p.dw) x.scratch(dw, 4, p.dw_splits * words * a.H);
+  x.scratch(padding, 8, (long long)p.padding / 8);
   x.out(a.dh, sizeof(T), a.rows * a.H);
   x.add(a.dw, sizeof(T), std::is_same_v<T, float>, true, (long long)a.V * a.H);
   if (const cudaError_t e = set_extents(x, s); e != cudaSuccess) return e;
@@ -489,16 +512,17 @@ cudaError_t bwd_t(const s4_vocab_loss_bwd_args& a, St st, cudaStream_t s) {
     r.rows = n;
     return r;
   };
+  const Padding counts{reinterpret_cast<const unsigned long long*>(padding)};
   for (long long first = 0; first < a.V; first += words) {
     const long long n = a.V - first < words ? a.V - first : words;
-    const ToGrads<NP> grads{g, a.lse, a.dloss, a.targets, a.wide_targets, a.V, (int)first, a.rows, words, st};
+    const ToGrads<NP> grads{g, padding, a.lse, a.dloss, a.targets, a.wide_targets, a.V, (int)first, a.rows, words, st};
     err = multiply<false, false>(lh, rows_from(lw, first, n), a.rows, n, 0, chunks_of(a.H), 1, grads, st, s);
     if (err != cudaSuccess) return err;
     const Operand gr{g, words, words * a.rows, a.rows, (int)n, NP, true};
     // the words' gradients: partial sums where there are shares; in fp32 else straight into dw, piece by piece of the rows
     T* to_w = static_cast<T*>(a.dw) + first * a.H;
     float* part_w = p.dw ? dw : std::is_same_v<T, float> ? reinterpret_cast<float*>(to_w) : nullptr;
-    err = sum_products<T, true>(gr, h, n, a.H, a.rows, p.dw_splits, false, !p.dw, to_w, part_w, st, s);
+    err = sum_products<T, true>(gr, h, n, a.H, a.rows, p.dw_splits, false, !p.dw, to_w, part_w, st, s, counts);
     if (err == cudaSuccess && p.dw) err = add_up<T>(dw, p.dw_splits, n * a.H, to_w, s);
     if (err != cudaSuccess) return err;
     err = sum_products<T, false>(gr, rows_from(w, first, n), a.rows, a.H, n, p.dh_splits, first > 0, !p.dh,
@@ -528,7 +552,7 @@ cudaError_t launch_vocab_loss(const s4_vocab_loss_args& a, St st, cudaStream_t s
 
 size_t vocab_loss_bwd_scratch(const s4_vocab_loss_bwd_args& a) {
   const Plan p = plan_of(a);
-  size_t n = p.g + p.dh + p.dw + copies(a, terms_of(a.dtype));
+  size_t n = p.g + p.dh + p.dw + p.padding + copies(a, terms_of(a.dtype));
   if (a.dtype == S4_F16) n += copies(a, 1);
   return n;
 }
