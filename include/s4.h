@@ -452,8 +452,9 @@ s4_status s4_block_norm_bwd(const s4_block_norm_bwd_args* a, void* stream);
  *    digits on the way (the keys that enter an fp32 state), as sums of two or three
  *    bfloat16 terms.  With bfloat16 inputs the weights between the two products of a
  *    pass, and the state where it is multiplied, are rounded to bfloat16 on the way.
- *  - Attention multiplies a chunk's later tokens by zeros: an infinite or NaN value of a
- *    real token makes outputs of up to 127 tokens before it NaN (padding never does).
+ *  - An infinite or NaN value of a real token reaches what the formulas make infinite or NaN (of which
+ *    of the two it becomes they may differ) and nothing else; padding reaches nothing.  Attention then goes through
+ *    that head's tokens one by one (for 4 x 1500 tokens in bfloat16 2.7 ms instead of 0.06).
  * ====================================================================== */
 typedef struct {
     const void* p;

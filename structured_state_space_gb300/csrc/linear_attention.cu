@@ -56,6 +56,8 @@ constexpr int kTerms = std::is_same_v<T, float> ? 3 : std::is_same_v<T, __half> 
 
 template <typename T, int D, int C>
 constexpr int kWalkBytes = 2 * kTerms<T> * (2 * C * (D + 8) + (C + D) * (kCols + 8));
+template <typename T, int D, int C>
+constexpr bool kTokensFit = kWalkBytes<T, D, C> >= 4 * (D * (kCols + 2) + kThreads);  // see walk_tokens
 
 // Rows [i0, i0 + n) of the walk, columns [c0, c0 + W) of `width`, as terms in shared memory [terms][C][W + 8].
 template <typename T, int W, int C>
@@ -85,10 +87,67 @@ __device__ __forceinline__ void load_rows(__nv_bfloat16* s, const T* p, long lon
   }
 }
 
+// The CTA's walk once more, its tokens one after the other, a column of the state for every two threads: for inputs with
+// infinities or NaN, which the products of a chunk multiply by the zeros of the tokens before them too.  (It finds its
+// place again by itself: what it would be handed would hold registers through the whole kernel.)
+template <typename T>
+__device__ __noinline__ void walk_tokens(const Walk& w, float* m) {
+  const int nc = (w.dc + kCols - 1) / kCols, c0 = (int)(blockIdx.x % nc) * kCols, h = (int)(blockIdx.x / nc) % w.H;
+  const int b = (int)(blockIdx.x / nc) / w.H, seg = blockIdx.y, cols = w.dc - c0 < kCols ? w.dc - c0 : kCols, da = w.da;
+  const Seq q = seq_of(w.lengths, w.index, b, w.L, w.slots, St{nullptr, 0u});
+  const int begin = seg * w.seg, end = begin + w.seg < q.len ? begin + w.seg : q.len;
+  const int c = threadIdx.x % kCols, half = threadIdx.x / kCols;
+  const bool column = c < cols;
+  const long long cells = (long long)da * w.dc, slot = (q.slot * w.H + h) * cells;
+  const float g = decay_of(w.log_decay, h), less = expm1f(g);
+  float *sa = m + da * kCols, *sb = sa + da, *part = sb + da;
+  if (column) {
+    const float* local = w.local + (((long long)b * w.H + h) * w.segs + seg) * cells;
+    const float by = w.init_scale * (w.reverse ? 1.f : power(g, 1));
+    for (int r = half; r < da; r += 2)
+      m[r * kCols + c] = w.segs > 1 ? rd(local + (long long)r * w.dc + c0 + c)
+                                    : w.init && q.slot >= 0 ? by * rd(w.init + slot + r * w.init_r + (c0 + c) * w.init_c) : 0.f;
+  }
+  for (int i = begin; i < end; ++i) {
+    const long long t = w.reverse ? q.len - 1 - i : i;
+    __syncthreads();
+    for (int r = threadIdx.x; r < da; r += kThreads) {
+      sa[r] = to_f(rd(at_head<T>(w.a, b, h) + t * w.a.row + r));
+      sb[r] = to_f(rd(at_head<T>(w.b, b, h) + t * w.b.row + r));
+    }
+    __syncthreads();
+    float sum = 0.f;
+    if (column) {
+      const float x = to_f(rd(at_head<T>(w.c, b, h) + t * w.c.row + c0 + c));
+      for (int r = half; r < da; r += 2) {
+        float v = m[r * kCols + c];
+        v = fmaf(sb[r], x, i == begin ? v : fmaf(v, less, v));
+        sum = fmaf(sa[r], v, sum);
+        m[r * kCols + c] = v;
+      }
+    }
+    part[threadIdx.x] = sum;
+    __syncthreads();
+    if (!column || half) continue;
+    const long long at = b * w.out_batch + t * w.out_row + h * w.out_head + c0 + c;
+    sum = w.scale * (part[c] + part[kCols + c]);
+    if (w.out_f32)
+      wr(static_cast<float*>(w.out) + at, sum);
+    else
+      wr(static_cast<T*>(w.out) + at, from_f<T>(sum));
+  }
+  if (end == q.len && w.last && q.slot >= 0 && column)
+    for (int r = half; r < da; r += 2) {
+      const float v = m[r * kCols + c];
+      wr(w.last + slot + r * w.init_r + (c0 + c) * w.init_c, w.last_scale * (w.reverse ? fmaf(v, less, v) : v));
+    }
+}
+
 // The walk of one sequence, head and 64 columns of c, over one segment of the sequence, in chunks of C
 // tokens: the sums over a chunk's own tokens are products of its tiles, those over earlier tokens go
 // through M, in registers (warp w has rows w D/4 on).  D: da rounded up.  STATE: only M, from zero, for
-// the segments after it.
+// the segments after it.  Where outputs are not finite the walk is made once more, token by token: a later token's
+// weight of 0 times an infinity or NaN is NaN.
 template <typename T, int D, int C, bool STATE>
 __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ Walks ws, St st) {
   const Walk& w = ws.w[blockIdx.z];
@@ -154,6 +213,7 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ 
     each([&](float& v, int r, int c, bool in) { v = in ? rd(local + (long long)r * w.dc + c) : 0.f; });
   }
 
+  float zero = 0.f;  // or NaN, where an output is not finite
   for (int i0 = begin; i0 < end; i0 += C) {
     const int n = end - i0 < C ? end - i0 : C, first = w.reverse ? q.len - 1 - i0 : i0, step = w.reverse ? -1 : 1;
     const bool at_end = i0 + n >= q.len;
@@ -262,6 +322,7 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ 
             const int c = n0 + 8 * j + 2 * t4;
             const float v[2] = {w.scale * o[j][2 * half], w.scale * o[j][2 * half + 1]};
             if (c >= cols) continue;
+            zero = fmaf(v[0], 0.f, fmaf(v[1], 0.f, zero));
             if (w.out_f32)
               st_f<float, 2>(static_cast<float*>(w.out) + at + c, cols - c, w.vec, v);
             else
@@ -331,6 +392,8 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ 
     each([&](float& v, int r, int c, bool in) {
       if (in) wr(to + (long long)r * w.dc + c, v);
     });
+  } else if (__syncthreads_or(!(zero == 0.f))) {
+    walk_tokens<T>(ws.w[blockIdx.z], reinterpret_cast<float*>(walk_smem));
   } else if (last && end == q.len) {
     each([&](float& v, int r, int c, bool in) {
       if (in) wr(last + r * w.init_r + (c0 + c) * w.init_c, w.last_scale * v);
@@ -532,6 +595,7 @@ cudaError_t walk_d(const Walks& ws, int n, St st, cudaStream_t s) {
     const unsigned own = (unsigned)((long long)ws.w[i].batch * ws.w[i].H * ((ws.w[i].dc + kCols - 1) / kCols));
     walks = own > walks ? own : walks;
   }
+  static_assert(kTokensFit<T, D, C>, "shared memory");
   constexpr auto kernel = walk_kernel<T, D, C, false>;
   allow_shared<kernel>(bytes);
   const int segs = ws.w[0].segs;

@@ -146,13 +146,108 @@ __device__ __forceinline__ Span span_of(const Walk& w, int seg, int len) {
   return p;
 }
 
+// The CTA's walk once more, its tokens one after the other, by 128 threads with a column of the state each: for inputs with
+// infinities or NaN, which the tiles' products multiply by the zeros of the tokens before them too.  (It finds its place
+// again by itself: what it would be handed would hold registers through the whole kernel, which took 3 % longer.)
+__device__ __noinline__ void walk_tokens(const Walk& w, float* m) {
+  using T = __nv_bfloat16;
+  const int h = blockIdx.x % w.H, b = blockIdx.x / w.H, c = threadIdx.x, da = w.da;
+  const Seq q = seq_of(w.lengths, w.index, b, w.L, w.slots, St{nullptr, 0u});
+  const Span sp = span_of(w, blockIdx.y, q.len);
+  const long long cells = (long long)da * w.dc, slot = (q.slot * w.H + h) * cells;
+  const float g = decay_of(w.log_decay, h), less = expm1f(g);
+  float *sa = m + da * kC, *sb = sa + kC;
+  if (c < w.dc) {
+    const float* local = w.local + (((long long)b * w.H + h) * w.segs + blockIdx.y) * cells;
+    const float by = w.init_scale * (w.reverse ? 1.f : power(g, 1));
+    for (int r = 0; r < da; ++r)
+      m[r * kC + c] = w.segs > 1 ? rd(local + r + (long long)c * da)
+                                 : w.init && q.slot >= 0 ? by * rd(w.init + slot + r * w.init_r + c * w.init_c) : 0.f;
+  }
+  const int n = sp.end - sp.begin;
+  // a token's values are on their way while the one before is worked on
+  const auto token = [&](int i) { return (long long)(w.reverse ? sp.end - 1 - i : sp.begin + i); };
+  T xa, xb, xc;
+  const auto load = [&](int i) {
+    if (c < da) xa = rd(at_head<T>(w.a, b, h) + token(i) * w.a.row + c), xb = rd(at_head<T>(w.b, b, h) + token(i) * w.b.row + c);
+    if (c < w.dc) xc = rd(at_head<T>(w.c, b, h) + token(i) * w.c.row + c);
+  };
+  load(0);
+  for (int i = 0; i < n; ++i) {
+    const long long t = token(i);
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (c < da) sa[c] = to_f(xa), sb[c] = to_f(xb);
+    const float x = to_f(xc);
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (i + 1 < n) load(i + 1);
+    if (c >= w.dc) continue;
+    float sum[4] = {};
+    const float keep = i == 0 ? 0.f : less;
+    const auto rows = [&](auto count, int r0) {
+      constexpr int N = decltype(count)::value;
+      float v[N];
+#pragma unroll
+      for (int y = 0; y < N; ++y) v[y] = m[(r0 + y) * kC + c];
+#pragma unroll
+      for (int y = 0; y < N; ++y) {
+        v[y] = fmaf(sb[r0 + y], x, fmaf(v[y], keep, v[y]));
+        sum[y & 3] = fmaf(sa[r0 + y], v[y], sum[y & 3]);
+      }
+#pragma unroll
+      for (int y = 0; y < N; ++y) m[(r0 + y) * kC + c] = v[y];
+    };
+    int r0 = 0;
+    for (; r0 + 16 <= da; r0 += 16) rows(std::integral_constant<int, 16>{}, r0);
+    for (; r0 < da; ++r0) rows(std::integral_constant<int, 1>{}, r0);
+    const float out = w.scale * ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+    const long long at = b * w.out_batch + t * w.out_row + h * w.out_head + c;
+    if (w.out_f32)
+      wr(static_cast<float*>(w.out) + at, out);
+    else
+      wr(static_cast<T*>(w.out) + at, from_f<T>(out));
+  }
+  if (sp.last && w.last && q.slot >= 0 && c < w.dc)
+    for (int r = 0; r < da; ++r) {
+      const float v = m[r * kC + c];
+      wr(w.last + slot + r * w.init_r + c * w.init_c, w.last_scale * (w.reverse ? fmaf(v, less, v) : v));
+    }
+}
+
+// Whether a chunk's sums that the state has not taken up are not finite: those of the walk's last chunk, where no state is
+// returned.
+template <int DV>
+__device__ __noinline__ bool last_lost(const Walk& w, uint32_t o1) {
+  const int b = blockIdx.x / w.H;
+  const Seq q = seq_of(w.lengths, w.index, b, w.L, w.slots, St{nullptr, 0u});
+  const Span sp = span_of(w, blockIdx.y, q.len);
+  if (sp.last && w.last && q.slot >= 0) return false;
+  const int n = w.reverse ? sp.end - sp.begin : sp.end - sp.begin - kC * (sp.chunks - 1);  // rows of the chunk: that many, or all
+  float2 zero = make_float2(0.f, 0.f);  // or NaN
+#pragma unroll 1
+  for (int c = 0; c < DV; c += 32) {
+    uint32_t u[32];
+    tmem_ld32(o1 + c, u);
+#pragma unroll
+    for (int x = 0; x < 16; ++x)
+      zero = fma2(make_float2(__uint_as_float(u[2 * x]), __uint_as_float(u[2 * x + 1])), make_float2(0.f, 0.f), zero);
+  }
+  return (int)threadIdx.x < n && !(zero.x + zero.y == 0.f);
+}
+
 // 512 threads: warps 0 to 3 form P and put out O, warps 4 to 7 hold the state (with more registers: 208 a thread of the
 // 4 x 128 that the four warpgroups start with), warp 8 brings the tiles, warp 9 issues the products, warps 12 to
 // 15 scale the keys.  Every wait is bounded; where one gives up the CTA records a stall,
 // waits for its copies and products in flight, frees its tensor memory and leaves.
+//
+// A later token's weight of 0 times an infinity or NaN is NaN, so outputs before it in its chunk are lost.  Any such value
+// leaves the state infinite or NaN in its column for good: the state's warps look once, at the end (warps 0 to 3 at the
+// sums of a last chunk that the state does not take up), and warps 0 to 3 then go through the tokens again one by one
+// (looking at every chunk's sums, with a call there to form them again, took 4 to 13 % longer; this way
+// 0 to 3 %).
 template <int DK, int DV, int NK, bool STATE>
 __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constant__ Passes ps, s4impl::St st) {
   using R = Room<DK, DV, NK, STATE>;
+  static_assert(R::BYTES - 1024 >= 4 * kC * (DK + 2), "shared memory of walk_tokens");
   const Walk& w = ps.walks.w[blockIdx.z];
   const Maps& maps = ps.maps[blockIdx.z];
   extern __shared__ char raw[];
@@ -160,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   __shared__ unsigned long long keys_ready[4], keys_free[4];
   __shared__ unsigned long long s_ready, p_ready, c_clean, d_ready, d_free, m_ready, m_free, o_ready, o_free, idle;
   __shared__ uint32_t tmem_slot;
-  __shared__ volatile int failed;
+  __shared__ volatile int failed, lost;
   __shared__ __align__(16) float tab[32];
   char* smem = raw + (-s4dev::smem_u32(raw) & 1023);  // (still a shared-memory address to the compiler)
   const int wid = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (uniform)
@@ -190,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     s4dev::mbar_init(&s_ready, 1), s4dev::mbar_init(&p_ready, 4), s4dev::mbar_init(&c_clean, 4);
     s4dev::mbar_init(&d_ready, 1), s4dev::mbar_init(&d_free, 4), s4dev::mbar_init(&m_ready, 4), s4dev::mbar_init(&m_free, 1);
     s4dev::mbar_init(&o_ready, 1), s4dev::mbar_init(&o_free, 4), s4dev::mbar_init(&idle, 1);
-    failed = 0;
+    failed = lost = 0;
     s4dev::fence_mbar_init();
   }
   if (threadIdx.x < 32) tab[threadIdx.x] = power(g, threadIdx.x);
@@ -500,8 +595,16 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         put();
       }
     }
+    if (!STATE) {
+      float2 zero = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < DV / 2; ++c) zero = fma2(m[c], make_float2(0.f, 0.f), zero);
+      if (!(zero.x + zero.y == 0.f)) lost = 1;
+      asm volatile("bar.sync 2, 128;" ::: "memory");
+    }
+    // (where it is lost the state on return, which may go where the one on entry is, comes from the second walk)
     float* to = STATE ? local + cells + r : last && sp.last ? last + r * w.init_r : nullptr;  // (STATE: the next segment's)
-    if (row && to && !failed) {
+    if (row && to && !failed && (STATE || !lost)) {
       const long long step = STATE ? w.da : w.init_c;
       const float by = STATE ? 1.f : w.last_scale;
       if (step == 1 && dc % 4 == 0 && (uintptr_t)to % 16 == 0) {
@@ -591,6 +694,14 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   fence_before();
   __syncthreads();
   fence_after();
+  if (!STATE && wid < 4 && !failed) {
+    if (last_lost<DV>(ps.walks.w[blockIdx.z], tmem + ((threadIdx.x & 96) << 16) + R::O1)) lost = 1;
+    fence_before();
+  }
+  if (!STATE) {
+    __syncthreads();
+    fence_after();
+  }
   if (failed) {
     // the copies and products in flight
     if (threadIdx.x == 0 && st.w) s4dev::st_flag(st, s4dev::ST_STALL);
@@ -610,6 +721,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     fence_after();
   }
   if (wid == 9) tmem_free(tmem, R::COLS);
+  if (!STATE && lost && !failed && threadIdx.x < 128)
+    walk_tokens(ps.walks.w[blockIdx.z], reinterpret_cast<float*>(raw + (-s4dev::smem_u32(raw) & 1023)));
 }
 
 // ---- host side -----------------------------------------------------------------------------------------
@@ -717,6 +830,10 @@ cudaError_t launch_tiles(const Walks& ws, int passes, int dtype, St st, cudaStre
     ps.by_map[i] = !p.out_f32 && (uintptr_t)p.out % 16 == 0 && stride_ok(p.out_head, p.H) && stride_ok(p.out_row, p.L) &&
                    stride_ok(p.out_batch, p.batch) && make_map(&m.out, out, p.dc, p.H, p.L, p.batch);
 #ifdef S4_BOUNDS_CHECK
+    const auto in = [&](const In& r, int d) {
+      x.add(r.p, 2, true, false, d, p.batch, r.batch, p.L, r.row, p.H / r.per, r.head);
+    };
+    in(p.a, p.da), in(p.b, p.da), in(p.c, p.dc);
     x.add(p.out, e, false, true, p.dc, p.batch, p.out_batch, p.L, p.out_row, p.H, p.out_head);
     x.in(p.init, 4, (long long)p.H * p.da * p.dc, p.slots);
     x.out(p.last, 4, (long long)p.H * p.da * p.dc, p.slots);
