@@ -2,12 +2,13 @@
 backward are the library's calls (block.py, sequence.py).  Nothing beside the inputs is kept for the backward
 pass (the vocabulary loss keeps its lse).  Activations and parameters as there; sequences start from a state of zeros.
 There are no second derivatives: gradients taken with create_graph=True raise where they are differentiated.
+What is a constant of an operator and requires a gradient all the same is refused.
 
     short_conv(x, w, bias, lengths)                               -> y
     selective_scan(x, dt, A, B, C, D, z, dt_bias, lengths)        -> y
     block_norm(o, gate, h, w_post, scale, w_pre, eps)             -> h_out, y
-    linear_attention(q, k, v, log_decay, scale, lengths)          -> o          (no gradient for log_decay)
-    rotary(q, k, freqs, positions, pairs, amplitude)              -> q, k       (k may be None)
+    linear_attention(q, k, v, log_decay, scale, lengths)          -> o          (log_decay is a constant)
+    rotary(q, k, freqs, positions, pairs, amplitude)              -> q, k       (k may be None; freqs are constants)
     layer_norm(x, w, b, eps)                                      -> y
     vocab_loss(h, w, targets)                                     -> losses     (one per row)
 """
@@ -166,12 +167,20 @@ class _VocabLoss(torch.autograd.Function):
         return _final((g["dh"], g["dw"], None), (h, w, dloss))
 
 
+def _constant(t, name):
+    """Raises where a gradient is wanted of what has none: a parameter would silently stay as it is."""
+    if isinstance(t, torch.Tensor) and t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} has no gradient here: pass {name}.detach()")
+
+
 def linear_attention(q, k, v, log_decay, scale=None, lengths=None):
+    _constant(log_decay, "log_decay")
     return _LinearAttention.apply(q, k, v, log_decay, scale, lengths)
 
 
 def rotary(q, k, freqs, positions=None, pairs=False, amplitude=1.0):
     """(q, k), turned; k may be None."""
+    _constant(freqs, "freqs")
     return _Rotary.apply(q, k, freqs, positions, pairs, amplitude)
 
 
