@@ -7,10 +7,10 @@ What is a constant of an operator and requires a gradient all the same is refuse
     short_conv(x, w, bias, lengths)                               -> y
     selective_scan(x, dt, A, B, C, D, z, dt_bias, lengths)        -> y
     block_norm(o, gate, h, w_post, scale, w_pre, eps)             -> h_out, y
-    linear_attention(q, k, v, log_decay, scale, lengths)          -> o          (log_decay is a constant)
+    linear_attention(q, k, v, log_decay, scale, lengths, ws)      -> o          (log_decay is a constant)
     rotary(q, k, freqs, positions, pairs, amplitude)              -> q, k       (k may be None; freqs are constants)
     layer_norm(x, w, b, eps)                                      -> y
-    vocab_loss(h, w, targets)                                     -> losses     (one per row)
+    vocab_loss(h, w, targets, ws)                                 -> losses     (one per row)
 """
 from __future__ import annotations
 
@@ -104,16 +104,16 @@ def block_norm(o, gate=None, h=None, w_post=None, scale=None, w_pre=None, eps=1e
 
 class _LinearAttention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, log_decay, scale, lengths):
+    def forward(ctx, q, k, v, log_decay, scale, lengths, ws):
         ctx.save_for_backward(q, k, v, log_decay, lengths)
         ctx.scale = scale
-        return sequence.s4_linear_attention_fwd(q, k, v, log_decay, scale=scale, lengths=lengths)
+        return sequence.s4_linear_attention_fwd(q, k, v, log_decay, scale=scale, lengths=lengths, ws=ws)
 
     @staticmethod
     def backward(ctx, do):
         q, k, v, log_decay, lengths = ctx.saved_tensors
         g = sequence.s4_linear_attention_bwd(q, k, v, log_decay, do.contiguous(), scale=ctx.scale, lengths=lengths)
-        return _final((g["dq"], g["dk"], g["dv"], None, None, None), (q, k, v, do))
+        return _final((g["dq"], g["dk"], g["dv"], None, None, None, None), (q, k, v, do))
 
 
 class _Rotary(torch.autograd.Function):
@@ -155,8 +155,8 @@ class _LayerNorm(torch.autograd.Function):
 
 class _VocabLoss(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, h, w, targets):
-        loss, lse = sequence.s4_vocab_loss_fwd(h, w, targets)
+    def forward(ctx, h, w, targets, ws):
+        loss, lse = sequence.s4_vocab_loss_fwd(h, w, targets, ws=ws)
         ctx.save_for_backward(h, w, targets, lse)
         return loss
 
@@ -164,7 +164,7 @@ class _VocabLoss(torch.autograd.Function):
     def backward(ctx, dloss):
         h, w, targets, lse = ctx.saved_tensors
         g = sequence.s4_vocab_loss_bwd(h, w, targets, lse, dloss.contiguous())
-        return _final((g["dh"], g["dw"], None), (h, w, dloss))
+        return _final((g["dh"], g["dw"], None, None), (h, w, dloss))
 
 
 def _constant(t, name):
@@ -173,9 +173,10 @@ def _constant(t, name):
         raise ValueError(f"{name} has no gradient here: pass {name}.detach()")
 
 
-def linear_attention(q, k, v, log_decay, scale=None, lengths=None):
+def linear_attention(q, k, v, log_decay, scale=None, lengths=None, ws=None):
+    """o.  A length out of range is recorded in ws, the forward call's workspace (see s4_get_status)."""
     _constant(log_decay, "log_decay")
-    return _LinearAttention.apply(q, k, v, log_decay, scale, lengths)
+    return _LinearAttention.apply(q, k, v, log_decay, scale, lengths, ws)
 
 
 def rotary(q, k, freqs, positions=None, pairs=False, amplitude=1.0):
@@ -188,6 +189,7 @@ def layer_norm(x, w=None, b=None, eps=1e-5):
     return _LayerNorm.apply(x, w, b, eps)
 
 
-def vocab_loss(h, w, targets):
-    """One loss per row of h (0 where the target is negative)."""
-    return _VocabLoss.apply(h, w, targets)
+def vocab_loss(h, w, targets, ws=None):
+    """One loss per row of h (0 where the target is negative).  A target beyond the vocabulary counts as a negative one and is
+    recorded in ws, the forward call's workspace (see s4_get_status)."""
+    return _VocabLoss.apply(h, w, targets, ws)
