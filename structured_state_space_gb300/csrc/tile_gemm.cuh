@@ -81,6 +81,27 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t at2, uint32_t (&
       : "r"(at), "r"(at2)
       : "memory");
 }
+// 16 columns of two places, on their way at once, and 16 written.
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t at2, uint32_t (&r)[16], uint32_t (&q)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(q[0]), "=r"(q[1]), "=r"(q[2]),
+        "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]), "=r"(q[7]), "=r"(q[8]), "=r"(q[9]), "=r"(q[10]), "=r"(q[11]),
+        "=r"(q[12]), "=r"(q[13]), "=r"(q[14]), "=r"(q[15])
+      : "r"(at), "r"(at2)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, int z, unsigned long long* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
@@ -104,6 +125,7 @@ struct Product {
   int tiles_m, tiles_n;     // of 128 x BN
   int first, chunks;        // of 64 k: where they begin, how many
   int splits;               // the chunks are shared out among so many partial results
+  int part;                 // chunks that an accumulator takes up before it is added to the sum (SUMMED)
   int pairs;                // plane pairs: nibble p of each list
   uint32_t planes_a, planes_b;
   uint32_t what;            // instruction descriptor
@@ -128,8 +150,9 @@ struct AllCount {
 // from one accumulator while the other is filled.  Where some k do not count (with an MN-major B), A is zero there
 // and B may hold anything, NaN too: warp 1 blanks B's rows of them in shared memory before it multiplies.  Every wait
 // is bounded; where one gives up the CTA records a stall, waits for its copies and products in flight, frees
-// its tensor memory and leaves.
-template <int BN, bool A_MN, bool B_MN, typename Epilogue, typename Counts>
+// its tensor memory and leaves.  SUMMED: an accumulator takes up a part of the chunks at a time, and the second one is the sum
+// of the parts, added rounded (the tensor cores cut what an addition shifts out, so long sums in one drift).
+template <int BN, bool A_MN, bool B_MN, bool SUMMED, typename Epilogue, typename Counts>
 __global__ void __launch_bounds__(256, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Product p,
                    const Epilogue ep, const Counts counts, s4impl::St st) {
@@ -179,28 +202,29 @@ __global__ void __launch_bounds__(256, 1)
     return r;
   };
 
+  const int part = SUMMED ? p.part : p.chunks;
   int issued = 0;  // rounds of copies
   if (wid == 0 && elected()) {
     int stage = 0;
     unsigned phase = 0;
     for (int t = blockIdx.x; t < tiles && !failed; t += gridDim.x) {
       const Tile at = tile_of(t);
-      for (int pair = 0; pair < p.pairs && !failed; ++pair) {
-        const int za = p.planes_a >> (4 * pair) & 15, zb = p.planes_b >> (4 * pair) & 15;
-        for (int c = at.from; c < at.to; ++c) {
+      for (int from = at.from, i = 0; from < at.to && !failed; i = i + 1 == p.pairs ? 0 : i + 1, from += i == 0 ? part : 0) {
+        const int za = p.planes_a >> (4 * i) & 15, zb = p.planes_b >> (4 * i) & 15, to = from + part < at.to ? from + part : at.to;
+        for (int c = from; c < to; ++c) {
           if (!wait(&empty[stage], phase ^ 1)) break;
           char* a = smem + stage * S::STAGE;
           char* b = a + S::A;
           s4dev::mbar_expect_tx(&full[stage], S::STAGE);
           if (A_MN) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) tma_load(a + i * 8192, &map_a, at.m * 128 + 64 * i, c * kBK, za, &full[stage]);
+            for (int x = 0; x < 2; ++x) tma_load(a + x * 8192, &map_a, at.m * 128 + 64 * x, c * kBK, za, &full[stage]);
           } else {
             tma_load(a, &map_a, c * kBK, at.m * 128, za, &full[stage]);
           }
           if (B_MN) {
 #pragma unroll
-            for (int i = 0; i < BN / 64; ++i) tma_load(b + i * 8192, &map_b, at.n * BN + 64 * i, c * kBK, zb, &full[stage]);
+            for (int x = 0; x < BN / 64; ++x) tma_load(b + x * 8192, &map_b, at.n * BN + 64 * x, c * kBK, zb, &full[stage]);
           } else {
             tma_load(b, &map_b, c * kBK, at.n * BN, zb, &full[stage]);
           }
@@ -218,46 +242,77 @@ __global__ void __launch_bounds__(256, 1)
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
       const Tile at = tile_of(t);
       const bool blanks = counts.any(at.from, at.to);
-      ok = wait_warp(&taken[buf], buf_phase ^ 1);
-      fence_after();
-      const uint32_t d = tmem + buf * BN;
-      const int steps = ok ? p.pairs * (at.to - at.from) : 0;
-      for (int i = 0; i < steps; ++i) {
-        ok = wait_warp(&full[stage], phase);
-        if (!ok) break;
+      for (int from = at.from; ok && (from == at.from || from < at.to); from += part) {
+        const int n = (from + part < at.to ? from + part : at.to) - from;
+        ok = wait_warp(&taken[buf], buf_phase ^ 1);
         fence_after();
-        const uint32_t a = s4dev::smem_u32(smem) + stage * S::STAGE, b = a + S::A;
-        if (blanks) {
-          // a row of k has 128 bytes in each block of 64 columns: 16 bytes a lane
-          char* at_lane = smem + stage * S::STAGE + S::A + lane / 8 * 8192 + lane % 8 * 16;
-          for (unsigned long long left = counts.out(at.from + i % (at.to - at.from)); left; left &= left - 1)
-            if (lane < BN / 8) *reinterpret_cast<uint4*>(at_lane + (__ffsll(left) - 1) * 128) = make_uint4(0, 0, 0, 0);
-          s4dev::fence_proxy_async();
-          __syncwarp();
-        }
-        const uint64_t da = tile_desc(a, A_MN ? 8192 : 16), db = tile_desc(b, B_MN ? 8192 : 16);
+        const uint32_t d = tmem + buf * BN;
+        const int steps = ok ? p.pairs * n : 0;
+        for (int i = 0; i < steps; ++i) {
+          ok = wait_warp(&full[stage], phase);
+          if (!ok) break;
+          fence_after();
+          const uint32_t a = s4dev::smem_u32(smem) + stage * S::STAGE, b = a + S::A;
+          if (blanks) {
+            // a row of k has 128 bytes in each block of 64 columns: 16 bytes a lane
+            char* at_lane = smem + stage * S::STAGE + S::A + lane / 8 * 8192 + lane % 8 * 16;
+            for (unsigned long long left = counts.out(from + i % n); left; left &= left - 1)
+              if (lane < BN / 8) *reinterpret_cast<uint4*>(at_lane + (__ffsll(left) - 1) * 128) = make_uint4(0, 0, 0, 0);
+            s4dev::fence_proxy_async();
+            __syncwarp();
+          }
+          const uint64_t da = tile_desc(a, A_MN ? 8192 : 16), db = tile_desc(b, B_MN ? 8192 : 16);
 #pragma unroll
-        for (int k = 0; k < kBK / 16; ++k)
-          mma_f16(d, da + k * (A_MN ? 2048 >> 4 : 32 >> 4), db + k * (B_MN ? 2048 >> 4 : 32 >> 4), p.what, i + k > 0, one);
-        mma_commit(&empty[stage], one);
-        if (++stage == S::STAGES) stage = 0, phase ^= 1;
+          for (int k = 0; k < kBK / 16; ++k)
+            mma_f16(d, da + k * (A_MN ? 2048 >> 4 : 32 >> 4), db + k * (B_MN ? 2048 >> 4 : 32 >> 4), p.what, i + k > 0, one);
+          mma_commit(&empty[stage], one);
+          if (++stage == S::STAGES) stage = 0, phase ^= 1;
+        }
+        if (ok) mma_commit(&ready[buf], one);
+        if (SUMMED || ++buf == 2) buf = 0, buf_phase ^= 1;
       }
-      if (ok) mma_commit(&ready[buf], one);
-      if (++buf == 2) buf = 0, buf_phase ^= 1;
     }
   } else if (wid >= 4) {
     int buf = 0;
     unsigned buf_phase = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const uint32_t lanes = tmem + ((uint32_t)(wid & 3) * 32 << 16);
+    bool ok = true;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
       const Tile at = tile_of(t);
-      if (!wait_warp(&ready[buf], buf_phase)) break;
-      fence_after();
-      if (at.from < at.to)  // (a last piece may have fewer chunks than splits)
-        ep(at.m * 128 + (wid & 3) * 32 + lane, at.n, at.split, tmem + ((uint32_t)(wid & 3) * 32 << 16) + buf * BN);
-      fence_before();
-      __syncwarp();
-      if (lane == 0) arrive(&taken[buf]);
-      if (++buf == 2) buf = 0, buf_phase ^= 1;
+      const int row = at.m * 128 + (wid & 3) * 32 + lane;
+      if constexpr (SUMMED) {
+        for (int from = at.from; from < at.to; from += part) {
+          ok = wait_warp(&ready[0], buf_phase);
+          if (!ok) break;
+          buf_phase ^= 1;
+          fence_after();
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 16) {
+            uint32_t r[16], q[16];
+            tmem_ld16(lanes + c, lanes + BN + c, r, q);
+            if (from > at.from) {
+#pragma unroll
+              for (int x = 0; x < 16; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) + __uint_as_float(q[x]));
+            }
+            tmem_st16(lanes + BN + c, r);
+          }
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          fence_before();
+          __syncwarp();
+          if (lane == 0) arrive(&taken[0]);
+        }
+        if (ok) ep(row, at.n, at.split, lanes + BN);
+      } else {
+        ok = wait_warp(&ready[buf], buf_phase);
+        if (!ok) break;
+        fence_after();
+        if (at.from < at.to)  // (a last piece may have fewer chunks than splits)
+          ep(row, at.n, at.split, lanes + buf * BN);
+        fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(&taken[buf]);
+        if (++buf == 2) buf = 0, buf_phase ^= 1;
+      }
     }
   }
   __syncwarp();

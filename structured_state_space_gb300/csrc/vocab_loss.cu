@@ -310,11 +310,17 @@ void pairs_of(int n, Product* p) {
     }
 }
 
+// Sums in an accumulator drift, as the tensor cores cut off what an addition shifts out: about 1e-8 per addition of 16 k
+// (measured).  With fp32 results no accumulator takes up more than 4096 k, which stays below 3e-6; the parts are added
+// rounded.  Logits of 16-bit inputs, whose lse is fp32 too, are summed in parts of 8192.
+constexpr int kExact = 64;  // chunks
+int logits_part(int dtype) { return dtype == S4_F32 ? kExact : 2 * kExact; }
+
 // result [M][N] = sum over k of A and B, in 64 k from chunk `first` on: A [M][k] or, A_MN, [k][M]; B likewise.
-template <bool A_MN, bool B_MN, int BN = kBN, typename Epilogue, typename Counts = AllCount>
+template <bool A_MN, bool B_MN, int BN = kBN, bool SUMMED = false, typename Epilogue, typename Counts = AllCount>
 cudaError_t multiply(const Operand& a, const Operand& b, long long M, long long N, int first, int chunks, int splits,
-                     const Epilogue& ep, St st, cudaStream_t s, const Counts& counts = {}) {
-  constexpr auto kernel = product_kernel<BN, A_MN, B_MN, Epilogue, Counts>;
+                     const Epilogue& ep, St st, cudaStream_t s, const Counts& counts = {}, int part = 0) {
+  constexpr auto kernel = product_kernel<BN, A_MN, B_MN, SUMMED, Epilogue, Counts>;
   CUtensorMap ma, mb;
   if (!make_map(&ma, a.p, a.bf16, a.H, a.rows, a.planes, a.row, a.plane, A_MN ? kBK : 128) ||
       !make_map(&mb, b.p, b.bf16, b.H, b.rows, b.planes, b.row, b.plane, B_MN ? kBK : BN))
@@ -323,7 +329,7 @@ cudaError_t multiply(const Operand& a, const Operand& b, long long M, long long 
   p.M = (int)M, p.N = (int)N;
   p.tiles_m = (int)((M + 127) / 128), p.tiles_n = (int)((N + BN - 1) / BN);
   p.first = first, p.chunks = chunks;
-  p.splits = splits;
+  p.splits = splits, p.part = part;
   pairs_of(a.planes, &p);
   p.what = instruction(a.bf16, A_MN, B_MN, 128, BN);
   p.limit = s4impl::wait_limit();
@@ -332,6 +338,14 @@ cudaError_t multiply(const Operand& a, const Operand& b, long long M, long long 
   s4impl::TimedLaunch tl("vocab_loss", s);
   kernel<<<(unsigned)(tiles < s4impl::num_sms() ? tiles : s4impl::num_sms()), 256, Shape<BN>::BYTES, s>>>(ma, mb, p, ep, counts, st);
   return cudaGetLastError();
+}
+
+// The logits h w^T into `ep`.
+template <typename Epilogue>
+cudaError_t logits(const Operand& h, const Operand& w, int dtype, const Epilogue& ep, St st, cudaStream_t s) {
+  const int chunks = chunks_of(h.H), part = logits_part(dtype);
+  if (chunks > part) return multiply<false, false, kBN, true>(h, w, h.rows, w.rows, 0, chunks, 1, ep, st, s, AllCount{}, part);
+  return multiply<false, false>(h, w, h.rows, w.rows, 0, chunks, 1, ep, st, s);
 }
 
 int terms_of(int dtype) { return dtype == S4_F32 ? 3 : dtype == S4_F16 ? 2 : 1; }
@@ -380,7 +394,7 @@ cudaError_t fwd_t(const s4_vocab_loss_args& a, St st, cudaStream_t s) {
   if (const cudaError_t e = set_extents(x, s); e != cudaSuccess) return e;
 #endif
   const ToSums ep{part, hit, a.targets, a.wide_targets, a.V, a.rows, st};
-  err = multiply<false, false>(h, w, a.rows, a.V, 0, chunks_of(a.H), 1, ep, st, s);
+  err = logits(h, w, a.dtype, ep, st, s);
   if (err != cudaSuccess) return err;
   s4impl::TimedLaunch tl("vocab_loss", s);
   join_kernel<<<(unsigned)((a.rows + 7) / 8), 256, 0, s>>>(part, hit, a, tiles_n, st);
@@ -406,10 +420,6 @@ int shares(long long M, long long N, long long k) {
   if (n > chunks / 8) n = chunks / 8;
   return n < 1 ? 1 : (int)n;
 }
-// With fp32 results no accumulator sums up more than 4096 k: what the tensor cores cut off then stays below 3e-6
-// (measured about 1e-8 per addition of 16 k); the parts are added rounded.
-constexpr int kExact = 64;  // chunks
-
 // out (+)= A B: in one product where it can go straight out (`part` is then not used, and nothing may be added later),
 // else as `splits` partial results in part [splits][M][N].
 template <typename T, bool A_MN, int BN, typename Counts>
@@ -516,7 +526,7 @@ cudaError_t bwd_t(const s4_vocab_loss_bwd_args& a, St st, cudaStream_t s) {
   for (long long first = 0; first < a.V; first += words) {
     const long long n = a.V - first < words ? a.V - first : words;
     const ToGrads<NP> grads{g, padding, a.lse, a.dloss, a.targets, a.wide_targets, a.V, (int)first, a.rows, words, st};
-    err = multiply<false, false>(lh, rows_from(lw, first, n), a.rows, n, 0, chunks_of(a.H), 1, grads, st, s);
+    err = logits(lh, rows_from(lw, first, n), a.dtype, grads, st, s);
     if (err != cudaSuccess) return err;
     const Operand gr{g, words, words * a.rows, a.rows, (int)n, NP, true};
     // the words' gradients: partial sums where there are shares; in fp32 else straight into dw, piece by piece of the rows

@@ -1,0 +1,45 @@
+"""The vocabulary loss of many channels: logits that one accumulator of the tensor cores, which cuts off what its additions shift
+out, would let drift (16384 channels in float32 1.2e-5 in lse, all of one sign).
+
+Tolerances, relative in the 2-norm, as in test_gpu_vocab_loss.py: an accumulator that takes up 4096 products, the most in
+float32, is off by 3e-6 at most, one of 8192 (16-bit inputs) by 6e-6, both within the 1e-5 of float32 results."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import structured_state_space_gb300 as s4  # noqa: E402
+from block_util import DTYPES, close, need_gpu, to64  # noqa: E402
+from test_gpu_vocab_loss import GRAD  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    need_gpu()
+
+
+# rows, channels, words: two parts (the second of one channel, or one of eight), four; more tiles than SMs
+@pytest.mark.parametrize("size", [(100, 4097, 700), (200, 8200, 300), (300, 16384, 2000), (2500, 9000, 2600)])
+@pytest.mark.parametrize("shift", [0.0, 0.3])
+@pytest.mark.parametrize("dt", DTYPES)
+def test_many_channels(size, shift, dt):
+    rows, H, V = size
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    h = (torch.randn(rows, H, device="cuda", generator=gen) + shift).to(DTYPES[dt])
+    w = ((torch.randn(V, H, device="cuda", generator=gen) * 2 + shift) * H ** -0.5).to(DTYPES[dt])
+    t = torch.randint(-1, V, (rows,), device="cuda", generator=gen)
+    dl = torch.rand(rows, device="cuda", generator=gen)
+    loss, lse = s4.s4_vocab_loss_fwd(h, w, t)
+    got = s4.s4_vocab_loss_bwd(h, w, t, lse, dl)
+    x = h.double() @ w.double().t()
+    l64 = torch.logsumexp(x, -1)
+    close(lse, to64(l64), "lse")
+    at = torch.arange(rows, device="cuda")
+    want = torch.where(t >= 0, l64 - x[at, t.clamp(min=0)], 0.0)
+    assert (loss.double() - want).norm() <= 1e-5 * (want.norm() + l64.norm())
+    d = torch.exp(x - l64[:, None])
+    d[at, t.clamp(min=0)] -= 1
+    d *= torch.where(t >= 0, dl.double(), 0.0)[:, None]
+    close(got["dh"], to64(d @ w.double()), "dh", GRAD[h.dtype])
+    close(got["dw"], to64(d.t() @ h.double()), "dw", GRAD[h.dtype])
