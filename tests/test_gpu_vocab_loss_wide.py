@@ -1,8 +1,9 @@
 """The vocabulary loss of many channels: logits that one accumulator of the tensor cores, which cuts off what its additions shift
 out, would let drift (16384 channels in float32 1.2e-5 in lse, all of one sign).
 
-Tolerances, relative in the 2-norm, as in test_gpu_vocab_loss.py: an accumulator that takes up 4096 products, the most in
-float32, is off by 3e-6 at most, one of 8192 (16-bit inputs) by 6e-6, both within the 1e-5 of float32 results."""
+Tolerances, relative in the 2-norm, as in test_gpu_vocab_loss.py: an accumulator that takes up 4096 products (gradients in float32) is
+off by 3e-6 at most, one of 8192 (logits of 16-bit inputs) by 6e-6, both within the 1e-5 of float32 results; logits in float32 go in
+parts of 1024, so below 1e-6."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -34,7 +35,7 @@ def test_many_channels(size, shift, dt):
     got = s4.s4_vocab_loss_bwd(h, w, t, lse, dl)
     x = h.double() @ w.double().t()
     l64 = torch.logsumexp(x, -1)
-    close(lse, to64(l64), "lse")
+    close(lse, to64(l64), "lse", 1e-6 if dt == "f32" else None)
     at = torch.arange(rows, device="cuda")
     want = torch.where(t >= 0, l64 - x[at, t.clamp(min=0)], 0.0)
     assert (loss.double() - want).norm() <= 1e-5 * (want.norm() + l64.norm())
