@@ -312,8 +312,9 @@ void pairs_of(int n, Product* p) {
 
 // Sums in an accumulator drift, as the tensor cores cut off what an addition shifts out: about 1e-8 per addition of 16 k
 // (measured).  With fp32 results no accumulator takes up more than 4096 k, which stays below 3e-6; the parts are added
-// rounded.
+// rounded.  With float16 and bfloat16 results, off by up to 2^-11 and 2^-8 themselves, it is 65536 and 262144 (4e-5 and 2e-4).
 constexpr int kExact = 64;  // chunks
+int most_chunks(int dtype) { return dtype == S4_F32 ? kExact : dtype == S4_F16 ? 1024 : 4096; }
 // Logits, whose lse is fp32, in parts of 1024 k, where their six products hide the additions (1000 rows, 8000 words of 16384
 // channels 1295 us; in parts of 4096 1298, and off by 1.4e-6 instead of 3e-7), and of 8192 for 16-bit inputs.
 int logits_part(int dtype) { return dtype == S4_F32 ? 16 : 2 * kExact; }
@@ -427,7 +428,8 @@ int shares(long long M, long long N, long long k) {
 template <typename T, bool A_MN, int BN, typename Counts>
 cudaError_t sum_products_n(const Operand& a, const Operand& b, long long M, long long N, long long K, int splits, bool add,
                            bool direct, T* out, float* part, St st, cudaStream_t s, const Counts& counts) {
-  const int chunks = chunks_of(K), most = sizeof(T) == 4 ? kExact * splits : chunks;
+  constexpr int code = std::is_same_v<T, float> ? S4_F32 : std::is_same_v<T, __half> ? S4_F16 : S4_BF16;
+  const int chunks = chunks_of(K), most = most_chunks(code) * splits;
   if (direct && chunks <= most) {
     const ToMatrix<T, false, BN> ep{out, (int)M, (int)N, N % 8 == 0 && vec_ok(out, sizeof(T), 16)};
     return multiply<A_MN, true, BN>(a, b, M, N, 0, chunks, 1, ep, st, s, counts);
@@ -472,8 +474,9 @@ Plan plan_of(const Args& a) {
   p.words = piece_words(a.rows, a.V, np), p.pieces = (a.V + p.words - 1) / p.words;
   p.dh_splits = shares(a.rows, a.H, p.words), p.dw_splits = shares(p.words, a.H, a.rows);
   p.g = s4impl::align256(2ull * np * a.rows * p.words);
-  p.dh = p.pieces > 1 || p.dh_splits > 1 || a.dtype == S4_F32 ? s4impl::align256(4ull * p.dh_splits * a.rows * a.H) : 0;
-  p.dw = p.dw_splits > 1 ? s4impl::align256(4ull * p.dw_splits * p.words * a.H) : 0;
+  const int most = most_chunks(a.dtype);
+  p.dh = p.pieces > 1 || p.dh_splits > 1 || a.dtype == S4_F32 || chunks_of(p.words) > most ? s4impl::align256(4ull * p.dh_splits * a.rows * a.H) : 0;
+  p.dw = p.dw_splits > 1 || (a.dtype != S4_F32 && chunks_of(a.rows) > most) ? s4impl::align256(4ull * p.dw_splits * p.words * a.H) : 0;
   p.padding = padding_bytes(a.rows);
   return p;
 }
