@@ -720,12 +720,16 @@ cudaError_t bwd_t(const s4_linear_attention_bwd_args& a, St st, cudaStream_t s) 
       w.out = out.p, w.out_batch = out.batch, w.out_row = out.row, w.out_head = out.head;
     }
   }
-  // All in one launch where that does not cost more than the launches that it saves: tiles of one shape, or so few walks that
-  // they leave SMs idle (2 x 333 tokens of 6 heads of 48 and 80 in fp32 74 us; a launch each 215).
+  // All in one launch where their tiles have one shape, or where all segments of 64 tokens of all walks fit the SMs, a CTA each (of
+  // widths up to 128 two, one after the other): it then saves launches; else the narrower walks are better off with tiles of
+  // their own.  48 and 80 channels in fp32: 8 heads of 64 tokens (32 CTAs) 21 us in one, 34 in two launches; 12 of 333
+  // (288) 68 and 63 in a captured graph, 77 and 80 in a stream; 8 of 2000 (1024) 209 and 163, of 16000 1781 and 1172.  40
+  // and 256 channels: 4 heads of 333 tokens (144) 61 and 85, 8 (288) 111 and 87.
   const auto size = [](int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; };
-  const long long walks = 3ll * a.batch * a.H * ((a.K < a.V ? a.K : a.V) + kCols - 1) / kCols;
+  const auto columns = [](int d) { return (d + kCols - 1) / kCols; };
+  const long long ctas = (long long)a.batch * a.H * (2 * columns(a.K) + columns(a.V)) * ((a.L + 63) / 64);
   cudaError_t err;
-  if (size(a.K) == size(a.V) || (!s4impl::tiles_take(dk, code) && walks * segments(walks, a.L) <= 3ll * s4impl::num_sms())) {
+  if (size(a.K) == size(a.V) || (!s4impl::tiles_take(dk, code) && ctas <= (a.K > 128 || a.V > 128 ? 1ll : 2ll) * s4impl::num_sms())) {
     err = walk_t<T>(ws, 3, st, s);
   } else {
     Walks two = ws, one{};
