@@ -520,7 +520,7 @@ s4_status s4_linear_attention_bwd(const s4_linear_attention_bwd_args* a, void* s
  * (x[i], x[R + i]), or (x[2i], x[2i + 1]) with pairs = 1, as a complex number times
  * amplitude exp(+-1i position freqs[i]) (inverse = 1: minus, the gradients' rotation); the other
  * D - 2 R channels are copied.  freqs are angles in radians (fp64, |freq| < 2^10, finite); the angle
- * is reduced exactly, to 2^-32 turns, at any position of 32 bits.  q and k (k.p may be NULL) in
+ * is reduced in integers, to 2^-30 turns at any position of 32 bits.  q and k (k.p may be NULL) in
  * one call; an output may be its input, at the same strides.  1 <= D <= 256, 2 <= 2 R <= D.
  */
 typedef struct {

@@ -2,8 +2,9 @@
 //
 //   (a, b) -> amplitude (a cos t - b sin t, a sin t + b cos t),  t = position freq  (the gradients: -t).
 //
-// The angle is formed in turns, as 64-bit fractions: position (freq / 2 pi 2^64) mod 2^64 by integer products is
-// exact but for the fraction's own last bit, at any position; its upper 32 bits then go through sincospi.
+// The angle is formed in turns, as 64-bit fractions: position (freq / 2 pi 2^64) mod 2^64 by integer products.  The fraction of
+// one position is off by its own last bit and, for large frequencies, by the last place of 1 / 2 pi (0.015 of it): 5 units
+// of 2^-64 for |freq| < 2^10, 2^-30.7 turns at a position of 2^31.  Its upper 32 bits then go through sincospi: 2^-30 turns in all.
 // 6 operations per pair on 8 bytes of 16-bit data: the bound is memory.  The sines and cosines are
 // shared by a token's heads: a thread keeps those of its pairs and walks over heads.
 #include "s4_block.cuh"
