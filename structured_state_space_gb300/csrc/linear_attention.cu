@@ -563,7 +563,7 @@ size_t local_bytes(int batch, int L, int H, int da, int dc) {
     const int n = da <= 128 && dc <= 128 ? s4impl::tile_segments((long long)batch * H, L, passes) : 1;
     segs = n > segs ? n : segs;
   }
-  return s4impl::align256(segs == 1 ? 0 : sizeof(float) * (size_t)batch * H * segs * da * dc);
+  return s4impl::section(segs == 1 ? 0 : sizeof(float) * (size_t)batch * H * segs * da * dc);
 }
 
 #ifdef S4_BOUNDS_CHECK
@@ -713,7 +713,7 @@ cudaError_t bwd_t(const s4_linear_attention_bwd_args& a, St st, cudaStream_t s) 
     const int d = w.dc;
     w.reverse = true, w.init_scale = 1.f / a.scale;
     if (each > 1) {
-      float* part = take(s4impl::align256(sizeof(float) * (size_t)a.batch * a.L * a.H * d));
+      float* part = take(s4impl::section(sizeof(float) * (size_t)a.batch * a.L * a.H * d));
       w.out = part, w.out_f32 = true, w.out_head = d, w.out_row = (long long)a.H * d, w.out_batch = w.out_row * a.L;
       shared[i] = {part, out.p, out.batch, out.row, out.head, d};
     } else {
@@ -781,7 +781,7 @@ cudaError_t launch_linear_attention(const s4_linear_attention_args& a, St st, cu
 }
 
 size_t linear_attention_bwd_scratch(int batch, int L, int H, int G, int K, int V) {
-  const size_t part = H == G ? 0 : align256(sizeof(float) * (size_t)batch * L * H * K) + align256(sizeof(float) * (size_t)batch * L * H * V);
+  const size_t part = H == G ? 0 : section(sizeof(float) * (size_t)batch * L * H * K) + section(sizeof(float) * (size_t)batch * L * H * V);
   return 2 * local_bytes(batch, L, H, V, K) + local_bytes(batch, L, H, K, V) + part;
 }
 

@@ -5,6 +5,9 @@
 
 namespace s4impl {
 
+// A workspace's section of so many bytes, with what keeps it from the next.
+inline size_t section(size_t bytes) { return bytes ? align256(bytes) + kGap : 0; }
+
 size_t linear_attention_scratch(int batch, int L, int H, int K, int V);
 cudaError_t launch_linear_attention(const s4_linear_attention_args& a, St st, cudaStream_t s);
 size_t linear_attention_bwd_scratch(int batch, int L, int H, int G, int K, int V);

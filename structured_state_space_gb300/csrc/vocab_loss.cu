@@ -43,7 +43,7 @@ struct Padding {
     return __any_sync(0xffffffffu, some);
   }
 };
-size_t padding_bytes(long long rows) { return s4impl::align256((size_t)(rows + 127) / 128 * 16); }
+size_t padding_bytes(long long rows) { return s4impl::section((size_t)(rows + 127) / 128 * 16); }
 
 // ---- what becomes of a tile ---------------------------------------------------------------------------
 // The maximum and the sum of exponentials (from it) of a row's logits in the tile, and the target's logit.
@@ -268,7 +268,7 @@ bool maps_take(const void* p, long long row, long long rows, int H, int e) {
   return e == 2 && (uintptr_t)p % 16 == 0 && (rows == 1 || (row >= H && row % 8 == 0 && row < (1ll << 36)));
 }
 int pitch_of(int H) { return (H + 7) / 8 * 8; }
-size_t terms_bytes(long long rows, int H, int planes) { return s4impl::align256((size_t)planes * rows * pitch_of(H) * 2); }
+size_t terms_bytes(long long rows, int H, int planes) { return s4impl::section((size_t)planes * rows * pitch_of(H) * 2); }
 
 // What the products take of rows of T: themselves, or a copy in `planes` terms at `at` (1: of the same type).
 template <typename T>
@@ -379,9 +379,9 @@ cudaError_t fwd_t(const s4_vocab_loss_args& a, St st, cudaStream_t s) {
   char* at = static_cast<char*>(a.ws) + s4impl::kStatusBytes;
   const int tiles_n = (a.V + kBN - 1) / kBN, n = logits_terms(a.dtype);
   float2* part = reinterpret_cast<float2*>(at);
-  at += s4impl::align256(sizeof(float2) * tiles_n * a.rows);
+  at += s4impl::section(sizeof(float2) * tiles_n * a.rows);
   float* hit = reinterpret_cast<float*>(at);
-  at += s4impl::align256(sizeof(float) * a.rows);
+  at += s4impl::section(sizeof(float) * a.rows);
   Operand h, w;
   cudaError_t err = operand<T>(a.h, a.h_row, a.rows, a.H, n, &at, &h, s);
   if (err != cudaSuccess) return err;
@@ -473,10 +473,10 @@ Plan plan_of(const Args& a) {
   const int np = terms_of(a.dtype);
   p.words = piece_words(a.rows, a.V, np), p.pieces = (a.V + p.words - 1) / p.words;
   p.dh_splits = shares(a.rows, a.H, p.words), p.dw_splits = shares(p.words, a.H, a.rows);
-  p.g = s4impl::align256(2ull * np * a.rows * p.words);
+  p.g = s4impl::section(2ull * np * a.rows * p.words);
   const int most = most_chunks(a.dtype);
-  p.dh = p.pieces > 1 || p.dh_splits > 1 || a.dtype == S4_F32 || chunks_of(p.words) > most ? s4impl::align256(4ull * p.dh_splits * a.rows * a.H) : 0;
-  p.dw = p.dw_splits > 1 || (a.dtype != S4_F32 && chunks_of(a.rows) > most) ? s4impl::align256(4ull * p.dw_splits * p.words * a.H) : 0;
+  p.dh = p.pieces > 1 || p.dh_splits > 1 || a.dtype == S4_F32 || chunks_of(p.words) > most ? s4impl::section(4ull * p.dh_splits * a.rows * a.H) : 0;
+  p.dw = p.dw_splits > 1 || (a.dtype != S4_F32 && chunks_of(a.rows) > most) ? s4impl::section(4ull * p.dw_splits * p.words * a.H) : 0;
   p.padding = padding_bytes(a.rows);
   return p;
 }
@@ -516,7 +516,7 @@ cudaError_t bwd_t(const s4_vocab_loss_bwd_args& a, St st, cudaStream_t s) {
   x.scratch(g, 2, NP * a.rows * words);
   if (p.dh) x.scratch(dh, 4, p.dh_splits * a.rows * a.H);
   if (p.dw) x.scratch(dw, 4, p.dw_splits * words * a.H);
-  x.scratch(padding, 8, (long long)p.padding / 8);
+  x.scratch(padding, 4, (a.rows + 127) / 128 * 4);
   x.out(a.dh, sizeof(T), a.rows * a.H);
   x.add(a.dw, sizeof(T), std::is_same_v<T, float>, true, (long long)a.V * a.H);
   if (const cudaError_t e = set_extents(x, s); e != cudaSuccess) return e;
@@ -556,7 +556,7 @@ S4_OOB_COUNTER(oob_vocab_loss)
 #endif
 
 size_t vocab_loss_scratch(const s4_vocab_loss_args& a) {
-  return align256(sizeof(float2) * ((a.V + kBN - 1) / kBN) * a.rows) + align256(sizeof(float) * a.rows) +
+  return section(sizeof(float2) * ((a.V + kBN - 1) / kBN) * a.rows) + section(sizeof(float) * a.rows) +
          copies(a, logits_terms(a.dtype));
 }
 
