@@ -212,7 +212,8 @@ __global__ void __launch_bounds__(128) layer_norm_warp_kernel(s4_layer_norm_args
 // Q rows of a group go through the rounds together, which halves the barriers of a CTA's rows.
 template <typename T, int V, int NV, int MAX, bool AHEAD, int Q>
 __global__ void __launch_bounds__(MAX, NV == 1 ? 512 / MAX : 1)
-    layer_norm_bwd_kernel(s4_layer_norm_bwd_args a, bool vec, int lanes, float* part) {
+    layer_norm_bwd_kernel(s4_layer_norm_bwd_args a, bool vec, int lanes, float* part, St st) {
+  record_gen(st);
   __shared__ float red[2][4][32];
   extern __shared__ __align__(16) char norm_smem[];
   int phase = 0, stage = 0;
@@ -439,7 +440,7 @@ cudaError_t fwd_t(const s4_layer_norm_args& a, cudaStream_t s) {
 }
 
 template <typename T, int V>
-cudaError_t bwd_t(const s4_layer_norm_bwd_args& a, cudaStream_t s) {
+cudaError_t bwd_t(const s4_layer_norm_bwd_args& a, St st, cudaStream_t s) {
   const int e = sizeof(T), b = sizeof(Pack<T, V>);
   const bool vec = vec_ok(a.x, e, b, a.x_row) && vec_ok(a.dy, e, b, a.dy_row) && vec_ok(a.dx, e, b, a.dx_row) &&
                    vec_ok(a.w, 4, 16);
@@ -468,13 +469,13 @@ cudaError_t bwd_t(const s4_layer_norm_bwd_args& a, cudaStream_t s) {
         if (vec && a.H % V == 0 && bytes <= kMaxAhead) {
           constexpr auto kernel = layer_norm_bwd_kernel<T, V, NV, MAX, true, Q>;
           grid = grid_for<kernel>(a.rows, sh, lanes, bytes);
-          kernel<<<grid, sh.threads, bytes, s>>>(a, vec, lanes, part);
+          kernel<<<grid, sh.threads, bytes, s>>>(a, vec, lanes, part, st);
           return;
         }
       }
       constexpr auto kernel = layer_norm_bwd_kernel<T, V, NV, MAX, false, 1>;
       grid = grid_for<kernel>(a.rows, sh, lanes, 0);
-      kernel<<<grid, sh.threads, 0, s>>>(a, vec, lanes, part);
+      kernel<<<grid, sh.threads, 0, s>>>(a, vec, lanes, part, st);
     });
   }
   if (!sums) return cudaGetLastError();
@@ -506,9 +507,9 @@ size_t layer_norm_bwd_scratch(long long rows, int H) {
   return sizeof(float) * 2 * most * (size_t)H;
 }
 
-cudaError_t launch_layer_norm_bwd(const s4_layer_norm_bwd_args& a, cudaStream_t s) {
-  if (a.dtype == S4_F32) return bwd_t<float, 4>(a, s);
-  return a.dtype == S4_BF16 ? bwd_t<__nv_bfloat16, 8>(a, s) : bwd_t<__half, 8>(a, s);
+cudaError_t launch_layer_norm_bwd(const s4_layer_norm_bwd_args& a, St st, cudaStream_t s) {
+  if (a.dtype == S4_F32) return bwd_t<float, 4>(a, st, s);
+  return a.dtype == S4_BF16 ? bwd_t<__nv_bfloat16, 8>(a, st, s) : bwd_t<__half, 8>(a, st, s);
 }
 
 }  // namespace s4impl

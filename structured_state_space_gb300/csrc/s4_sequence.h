@@ -15,7 +15,7 @@ cudaError_t launch_linear_attention_bwd(const s4_linear_attention_bwd_args& a, S
 cudaError_t launch_rotary(const s4_rotary_args& a, cudaStream_t s);
 cudaError_t launch_layer_norm(const s4_layer_norm_args& a, cudaStream_t s);
 size_t layer_norm_bwd_scratch(long long rows, int H);
-cudaError_t launch_layer_norm_bwd(const s4_layer_norm_bwd_args& a, cudaStream_t s);
+cudaError_t launch_layer_norm_bwd(const s4_layer_norm_bwd_args& a, St st, cudaStream_t s);
 size_t vocab_loss_scratch(const s4_vocab_loss_args& a);
 cudaError_t launch_vocab_loss(const s4_vocab_loss_args& a, St st, cudaStream_t s);
 size_t vocab_loss_bwd_scratch(const s4_vocab_loss_bwd_args& a);

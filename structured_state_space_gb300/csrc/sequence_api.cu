@@ -154,7 +154,11 @@ s4_status s4_layer_norm_bwd(const s4_layer_norm_bwd_args* a, void* stream) {
     return S4_ERR_INVALID_ARG;
   const s4_status w = ws_ok(a->ws, a->ws_bytes, s4_layer_norm_bwd_workspace_bytes(a->rows, a->H));
   if (w != S4_OK) return w;
-  return cuda_status(s4impl::launch_layer_norm_bwd(*a, static_cast<cudaStream_t>(stream)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  s4impl::St st;  // nothing goes wrong there, but the status in ws is to be this call's
+  bool chain;
+  if (!s4impl::call_status(a->ws, s, &st, &chain)) return S4_ERR_CUDA;
+  return cuda_status(s4impl::launch_layer_norm_bwd(*a, st, s));
 }
 
 size_t s4_vocab_loss_workspace_bytes(const s4_vocab_loss_args* a) {

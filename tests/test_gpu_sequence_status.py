@@ -36,3 +36,13 @@ def test_what_is_out_of_range_is_recorded(dtype):
     assert not q.grad[1].any() and q.grad[0].any()
     ops.linear_attention(q, q, q, g, lengths=torch.tensor([70, 69], dtype=torch.int32, device="cuda"), ws=ws)
     assert s4.s4_get_status(ws) == 0
+
+
+def test_a_workspace_used_again_has_the_last_calls_status():
+    ws = torch.zeros(1 << 22, dtype=torch.uint8, device="cuda")
+    h, w = torch.randn(9, 64, device="cuda"), torch.randn(50, 64, device="cuda")
+    for _ in range(2):
+        s4.s4_vocab_loss_fwd(h, w, torch.full((9,), 50, device="cuda"), ws=ws)
+        assert s4.STATUS[s4.s4_get_status(ws)] == "S4_ERR_INVALID_INDEX"
+        s4.s4_layer_norm_bwd(h, h, w[0], w[1], ws=ws)
+        assert s4.s4_get_status(ws) == 0
