@@ -96,3 +96,19 @@ def test_one_launch_where_all_walks_fit_the_gpu(heads, L, launches):
         want = O.linear_attention_grad(*wide(q, k, v, g), to64(do), 48 ** -0.5)
         for n in ("dq", "dk", "dv"):
             close(got[n], want[n], n)
+
+
+@pytest.mark.parametrize("size", [(2, 333, 2, 2, 48, 80), (1, 400, 2, 1, 64, 64), (1, 400, 2, 2, 128, 128), (1, 300, 1, 1, 256, 256)])
+def test_float32_keeps_its_digits(size):
+    """Relative in the 2-norm: weights off by the exponential's 2^-22, and what the tensor cores cut off their accumulators: 2e-8 for each of the
+    additions of 16 products, K / 16 and V / 16 of them in a row and 4 for a chunk's tokens."""
+    batch, L, H, G, K, V = size
+    r, q, k, v, _ = make(5, *size, torch.float32)
+    g = torch.tensor([-0.03, -0.0005], device="cuda")[:H]
+    do = r.normal(batch, L, H, V)
+    most = 2.0 ** -22 + 2e-8 * (K / 16 + V / 16 + 4)
+    close(s4.s4_linear_attention_fwd(q, k, v, g), O.linear_attention(*wide(q, k, v, g), K ** -0.5)[0], "o", most)
+    got = s4.s4_linear_attention_bwd(q, k, v, g, do)
+    want = O.linear_attention_grad(*wide(q, k, v, g), to64(do), K ** -0.5)
+    for n in ("dq", "dk", "dv"):
+        close(got[n], want[n], n, most)
