@@ -242,7 +242,8 @@ __global__ void __launch_bounds__(256, 1)
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
       const Tile at = tile_of(t);
       const bool blanks = counts.any(at.from, at.to);
-      for (int from = at.from; ok && (from == at.from || from < at.to); from += part) {
+      // (where there is nothing to sum up the results' warps are told so once, but not of parts)
+      for (int from = at.from; ok && (from < at.to || (!SUMMED && from == at.from)); from += part) {
         const int n = (from + part < at.to ? from + part : at.to) - from;
         ok = wait_warp(&taken[buf], buf_phase ^ 1);
         fence_after();
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(256, 1)
           __syncwarp();
           if (lane == 0) arrive(&taken[0]);
         }
-        if (ok) ep(row, at.n, at.split, lanes + BN);
+        if (ok && at.from < at.to) ep(row, at.n, at.split, lanes + BN);
       } else {
         ok = wait_warp(&ready[buf], buf_phase);
         if (!ok) break;

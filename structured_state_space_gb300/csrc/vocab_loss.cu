@@ -311,13 +311,12 @@ void pairs_of(int n, Product* p) {
 }
 
 // Sums in an accumulator drift, as the tensor cores cut off what an addition shifts out: about 1e-8 per addition of 16 k
-// (measured).  With fp32 results no accumulator takes up more than 4096 k, which stays below 3e-6; the parts are added
-// rounded.  With float16 and bfloat16 results, off by up to 2^-11 and 2^-8 themselves, it is 65536 and 262144 (4e-5 and 2e-4).
-constexpr int kExact = 64;  // chunks
-int most_chunks(int dtype) { return dtype == S4_F32 ? kExact : dtype == S4_F16 ? 1024 : 4096; }
-// Logits, whose lse is fp32, in parts of 1024 k, where their six products hide the additions (1000 rows, 8000 words of 16384
-// channels 1295 us; in parts of 4096 1298, and off by 1.4e-6 instead of 3e-7), and of 8192 for 16-bit inputs.
-int logits_part(int dtype) { return dtype == S4_F32 ? 16 : 2 * kExact; }
+// (measured).  In fp32 an accumulator takes up 1024 k and is then added, rounded, to a second one (off by 3e-7 to 6e-7; their six products
+// hide the additions).  Logits of 16-bit inputs, whose lse is fp32 too, are summed in parts of 8192, gradients of float16 and bfloat16, off by up
+// to 2^-11 and 2^-8 themselves, in products of 65536 and 262144 k (4e-5 and 2e-4).
+constexpr int kPart = 16;  // chunks
+int logits_part(int dtype) { return dtype == S4_F32 ? kPart : 128; }
+int most_chunks(int dtype) { return dtype == S4_F32 ? 1 << 30 : dtype == S4_F16 ? 1024 : 4096; }
 
 // result [M][N] = sum over k of A and B, in 64 k from chunk `first` on: A [M][k] or, A_MN, [k][M]; B likewise.
 template <bool A_MN, bool B_MN, int BN = kBN, bool SUMMED = false, typename Epilogue, typename Counts = AllCount>
@@ -428,20 +427,23 @@ int shares(long long M, long long N, long long k) {
 template <typename T, bool A_MN, int BN, typename Counts>
 cudaError_t sum_products_n(const Operand& a, const Operand& b, long long M, long long N, long long K, int splits, bool add,
                            bool direct, T* out, float* part, St st, cudaStream_t s, const Counts& counts) {
-  constexpr int code = std::is_same_v<T, float> ? S4_F32 : std::is_same_v<T, __half> ? S4_F16 : S4_BF16;
-  const int chunks = chunks_of(K), most = most_chunks(code) * splits;
+  constexpr bool F32 = sizeof(T) == 4;
+  constexpr int code = F32 ? S4_F32 : std::is_same_v<T, __half> ? S4_F16 : S4_BF16;
+  const int chunks = chunks_of(K);
+  const long long most = (long long)most_chunks(code) * splits;
   if (direct && chunks <= most) {
     const ToMatrix<T, false, BN> ep{out, (int)M, (int)N, N % 8 == 0 && vec_ok(out, sizeof(T), 16)};
-    return multiply<A_MN, true, BN>(a, b, M, N, 0, chunks, 1, ep, st, s, counts);
+    return multiply<A_MN, true, BN, F32>(a, b, M, N, 0, chunks, 1, ep, st, s, counts, kPart);
   }
   const bool vec = N % 4 == 0 && vec_ok(part, 4, 16);
-  for (int first = 0; first < chunks; first += most, add = true) {
-    const int n = chunks - first < most ? chunks - first : most;
+  for (int first = 0; first < chunks; first += (int)most, add = true) {
+    const int n = chunks - first < most ? chunks - first : (int)most;
     const ToMatrix<float, true, BN> more{part, (int)M, (int)N, vec};
     const ToMatrix<float, false, BN> begin{part, (int)M, (int)N, vec};
-    const cudaError_t err = add ? multiply<A_MN, true, BN>(a, b, M, N, first, n, splits, more, st, s, counts)
-                                : multiply<A_MN, true, BN>(a, b, M, N, first, n, splits, begin, st, s, counts);
+    const cudaError_t err = add ? multiply<A_MN, true, BN, F32>(a, b, M, N, first, n, splits, more, st, s, counts, kPart)
+                                : multiply<A_MN, true, BN, F32>(a, b, M, N, first, n, splits, begin, st, s, counts, kPart);
     if (err != cudaSuccess) return err;
+    if (n == chunks - first) break;
   }
   return cudaSuccess;
 }
@@ -475,8 +477,8 @@ Plan plan_of(const Args& a) {
   p.dh_splits = shares(a.rows, a.H, p.words), p.dw_splits = shares(p.words, a.H, a.rows);
   p.g = s4impl::section(2ull * np * a.rows * p.words);
   const int most = most_chunks(a.dtype);
-  p.dh = p.pieces > 1 || p.dh_splits > 1 || a.dtype == S4_F32 || chunks_of(p.words) > most ? s4impl::section(4ull * p.dh_splits * a.rows * a.H) : 0;
-  p.dw = p.dw_splits > 1 || (a.dtype != S4_F32 && chunks_of(a.rows) > most) ? s4impl::section(4ull * p.dw_splits * p.words * a.H) : 0;
+  p.dh = p.pieces > 1 || p.dh_splits > 1 || chunks_of(p.words) > most ? s4impl::section(4ull * p.dh_splits * a.rows * a.H) : 0;
+  p.dw = p.dw_splits > 1 || chunks_of(a.rows) > most ? s4impl::section(4ull * p.dw_splits * p.words * a.H) : 0;
   p.padding = padding_bytes(a.rows);
   return p;
 }
@@ -518,7 +520,7 @@ cudaError_t bwd_t(const s4_vocab_loss_bwd_args& a, St st, cudaStream_t s) {
   if (p.dw) x.scratch(dw, 4, p.dw_splits * words * a.H);
   x.scratch(padding, 4, (a.rows + 127) / 128 * 4);
   x.out(a.dh, sizeof(T), a.rows * a.H);
-  x.add(a.dw, sizeof(T), std::is_same_v<T, float>, true, (long long)a.V * a.H);
+  x.out(a.dw, sizeof(T), (long long)a.V * a.H);
   if (const cudaError_t e = set_extents(x, s); e != cudaSuccess) return e;
 #endif
   const auto rows_from = [](const Operand& o, long long first, long long n) {
@@ -534,10 +536,8 @@ cudaError_t bwd_t(const s4_vocab_loss_bwd_args& a, St st, cudaStream_t s) {
     err = logits(lh, rows_from(lw, first, n), a.dtype, grads, st, s);
     if (err != cudaSuccess) return err;
     const Operand gr{g, words, words * a.rows, a.rows, (int)n, NP, true};
-    // the words' gradients: partial sums where there are shares; in fp32 else straight into dw, piece by piece of the rows
     T* to_w = static_cast<T*>(a.dw) + first * a.H;
-    float* part_w = p.dw ? dw : std::is_same_v<T, float> ? reinterpret_cast<float*>(to_w) : nullptr;
-    err = sum_products<T, true>(gr, h, n, a.H, a.rows, p.dw_splits, false, !p.dw, to_w, part_w, st, s, counts);
+    err = sum_products<T, true>(gr, h, n, a.H, a.rows, p.dw_splits, false, !p.dw, to_w, dw, st, s, counts);
     if (err == cudaSuccess && p.dw) err = add_up<T>(dw, p.dw_splits, n * a.H, to_w, s);
     if (err != cudaSuccess) return err;
     err = sum_products<T, false>(gr, rows_from(w, first, n), a.rows, a.H, n, p.dh_splits, first > 0, !p.dh,

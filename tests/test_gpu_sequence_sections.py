@@ -40,12 +40,11 @@ def test_sections_lie_apart(checked):
     assert more("s4_linear_attention_workspace_bytes", 1, 2000, 2, 1, 64, 64) == GAP
     assert more("s4_linear_attention_bwd_workspace_bytes", 1, 2000, 2, 2, 64, 64) == 3 * GAP
     assert more("s4_linear_attention_bwd_workspace_bytes", 1, 2000, 2, 1, 64, 64) == 5 * GAP
-    # partial sums, targets' logits, copies of h and w; logits' gradients, partial dh and dw, padding, copies
+    # partial sums, targets' logits, copies of h and w; logits' gradients, partial dw, padding, copies
     for dtype, copies in ((0, 2), (1, 0)):
         assert more("s4_vocab_loss_workspace_bytes", sequence._LOSS.pack(A, A, A, A, A, 0, 0, 64, 64, 3000, 64, 300, 1, dtype)) == (2 + copies) * GAP
         assert more("s4_vocab_loss_bwd_workspace_bytes",
-                    sequence._LOSS_BWD.pack(A, A, A, A, A, A, A, 0, 0, 64, 64, 3000, 64, 300, 1, dtype)) == (
-                        2 + copies + (2 if dtype == 0 else 1)) * GAP
+                    sequence._LOSS_BWD.pack(A, A, A, A, A, A, A, 0, 0, 64, 64, 3000, 64, 300, 1, dtype)) == (3 + copies) * GAP
 
 
 def test_no_index_leaves_its_section(checked):

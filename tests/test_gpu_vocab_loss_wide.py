@@ -1,9 +1,8 @@
 """The vocabulary loss of many channels: logits that one accumulator of the tensor cores, which cuts off what its additions shift
 out, would let drift (16384 channels in float32 1.2e-5 in lse, all of one sign).
 
-Tolerances, relative in the 2-norm, as in test_gpu_vocab_loss.py: an accumulator that takes up 4096 products (gradients in float32) is
-off by 3e-6 at most, one of 8192 (logits of 16-bit inputs) by 6e-6, both within the 1e-5 of float32 results; logits in float32 go in
-parts of 1024, so below 1e-6."""
+Tolerances, relative in the 2-norm, as in test_gpu_vocab_loss.py: an accumulator that takes up 8192 products (logits of 16-bit inputs)
+is off by 6e-6 at most, within the 1e-5 of float32 results; in float32 they go in parts of 1024, so below 1e-6."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -71,3 +70,23 @@ def test_many_rows_in_16_bits():
     close(got, to64(want), "dw", GRAD[torch.float16])
     short = ((got * want).sum() / (want * want).sum() - 1).abs().item()
     assert short <= 4096 * 1e-8 + 2.0 ** -12 * (V * some) ** -0.5 + 2 * 12 * (H / 16) * 1e-8, short
+
+
+@pytest.mark.parametrize("rows,H,V", [(16384, 48, 300), (40, 64, 40000), (6000, 130, 700), (300, 1500, 9000), (4096, 64, 66000)])
+def test_gradients_in_float32_keep_their_digits(rows, H, V):
+    """Sums over many rows and words in parts of 1024: 64 additions of 1e-8, and as much from the logits (|x - lse| below 16, whose 3e-7
+    are 5e-6 of the smallest gradients, 1e-6 of those that count): 2e-6 in the 2-norm."""
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    h = torch.randn(rows, H, device="cuda", generator=gen)
+    w = torch.randn(V, H, device="cuda", generator=gen) * 2 * H ** -0.5
+    t = torch.randint(-1, V, (rows,), device="cuda", generator=gen)
+    dl = torch.rand(rows, device="cuda", generator=gen)
+    loss, lse = s4.s4_vocab_loss_fwd(h, w, t)
+    got = s4.s4_vocab_loss_bwd(h, w, t, lse, dl)
+    x = h.double() @ w.double().t()
+    d = torch.exp(x - torch.logsumexp(x, -1, keepdim=True))
+    at = torch.arange(rows, device="cuda")
+    d[at, t.clamp(min=0)] -= 1
+    d *= torch.where(t >= 0, dl.double(), 0.0)[:, None]
+    close(got["dh"], to64(d @ w.double()), "dh", 2e-6)
+    close(got["dw"], to64(d.t() @ h.double()), "dw", 2e-6)
