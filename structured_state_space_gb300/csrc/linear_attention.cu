@@ -8,8 +8,10 @@
 //
 // Here the walks for all types, widths up to 256 and any strides, on warp-wide products; bfloat16 up to widths of
 // 128 at aligned strides goes to linear_attention_tiles.cu.  What bounds these is the latency of their
-// products and shared memory: 4 x 4096 tokens of 16 heads of 128 in bfloat16 1982 us for the three walks of a backward
-// pass (tiles: 215), 2 x 333 tokens of 6 heads of 48 and 80 in fp32 74 us.
+// products and shared memory: 4 x 4096 tokens of 16 heads of 128 in bfloat16 at an odd address 0.88 ms, 2.3 for the three walks of a
+// backward pass (tiles: 0.12 and 0.22), in float16 1.7 and 4.4, in fp32 2.1 and 5.5; of 256 in bfloat16 2.3 and 4.9;
+// gradients of 2 x 333 tokens of 6 heads of 48 and 80 in fp32 73 us.  Outputs of widths above 128 spill 64 to 130 bytes a thread at 255
+// registers.
 #include "linear_attention.cuh"
 
 namespace {

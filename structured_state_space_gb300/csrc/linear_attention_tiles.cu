@@ -10,11 +10,12 @@
 //
 // Per chunk at widths 128: S, P C and A M 2^22 operations each, D 2^22 a term, which takes 1.7 to 2 us of an SM's share of
 // the measured rate; the inputs and the output are 128 KB, 2.9 us of an SM's share of the memory's.  Measured on 4 x 4096
-// tokens of 16 heads of 128: 215 us for the three walks of a backward pass, 3.4 us a chunk on 152 SMs at once; what is
+// tokens of 16 heads of 128: 217 us for the three walks of a backward pass, 3.4 us a chunk on 152 SMs at once; what is
 // above the memory's share are 40 of 192 walks left for a second round, and three walks that read 12 arrays
-// where one would read 7.  65536 tokens of 16 heads of 64 take 275 us, 3.0 us a chunk (64 KB, 1.4 us): there
+// where one would read 7.  65536 tokens of 16 heads of 64 take 284 us, 3.0 us a chunk (64 KB, 1.4 us): there
 // the warp that issues the products is the bound, 40 of them per chunk at 90 cycles or so (a right operand of 64
-// columns does not feed the tensor cores), and a walk over segments reads keys and values twice.
+// columns does not feed the tensor cores), and a walk over segments reads keys and values twice.  Outputs spill 24 to 48
+// bytes a thread at the 128 registers that four warpgroups start with (140 to 236 bytes loaded again).
 #include "linear_attention.cuh"
 #include "tile_gemm.cuh"
 
@@ -774,7 +775,8 @@ bool tiles_take(const Walk& w, int dtype) {
 
 // Segments of a sequence: the number with the least time in chunks one after the other on an SM, a CTA on each.  A
 // segment costs about 3 chunks more than its own, one that only leaves its state half as much, two more launches as
-// much as 3 chunks.
+// much as 3 chunks.  64 at most, as they are joined one after the other: one head of 128 and 16384 tokens takes 46 us in 64
+// segments, 56 in 128; above a million tokens more would pay (2^20: 638 us in 64, 345 in 152).
 int tile_segments(long long walks, int L, int passes) {
   const int chunks = (L + kC - 1) / kC;
   const long long sms = num_sms();

@@ -64,7 +64,8 @@ struct Turned {
 };
 
 // Heads whose channels a thread has on their way, and CTAs per SM: 4 x 4096 tokens of 32 heads of 128 channels in bfloat16 take
-// 50 us (a plain copy 44); with one head or four at once 55 and 64, without the bound on registers 70.
+// 50 us (a plain copy 44); with one head or four at once 55 and 64, without the bound on registers 70
+// (which spills 64 to 104 bytes a thread where halves of 16 bits go in packs of 8).
 constexpr int kAtOnce = 2, kPerSm = 4;
 
 // Threads: `units` per token and head lane (packs of P pairs, and packs of W copied channels), `lanes`
@@ -192,6 +193,8 @@ cudaError_t with_packs(const s4_rotary_args& a, cudaStream_t s) {
   if (a.R % P == 0 && (PAIRS ? 2 * a.R % most == 0 : true) && tail % most == 0 && units >= 1 && units <= 256 &&
       packs_ok(a, e, most))
     return launch<T, P, most, PAIRS>(a, s);
+  // pair by pair, element by element (4 x 4096 tokens of 32 heads of 128 channels in bfloat16: 49 us in packs, 134 at an odd
+  // address, 176 with 126 channels turned)
   return launch<T, 1, 1, PAIRS>(a, s);
 }
 

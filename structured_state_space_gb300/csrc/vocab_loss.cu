@@ -11,7 +11,9 @@
 //
 // Measured in bfloat16: 1001 rows of 1024 channels and 32000 words 57 us forward (1.15 PFLOP/s), 8192 rows of 2048 and 50257 words
 // 4.79 ms for losses and gradients (1.41 PFLOP/s; the forward product alone 1.77, of 1.71 that a library's
-// sustains and 1.89 that it reaches in a burst).
+// sustains and 1.89 that it reaches in a burst); in float16 9.5 ms (g, h and w in two terms, three products each for dh and dw), in
+// fp32 27 (six products each).  In fp32 with few channels the bound is g, three terms of it written once and read twice: 8192 rows
+// of 64 and 32000 words 2.3 ms.
 #include "s4_block.cuh"
 #include "s4_sequence.h"
 #include "tile_gemm.cuh"
