@@ -8,10 +8,10 @@
 //
 // Here the walks for all types, widths up to 256 and any strides, on warp-wide products; bfloat16 up to widths of
 // 128 at aligned strides goes to linear_attention_tiles.cu.  What bounds these is the latency of their
-// products and shared memory: 4 x 4096 tokens of 16 heads of 128 in bfloat16 at an odd address 0.88 ms, 2.3 for the three walks of a
-// backward pass (tiles: 0.12 and 0.22), in float16 1.7 and 4.4, in fp32 2.1 and 5.5; of 256 in bfloat16 2.3 and 4.9;
-// gradients of 2 x 333 tokens of 6 heads of 48 and 80 in fp32 73 us.  Outputs of widths above 128 spill 64 to 130 bytes a thread at 255
-// registers.
+// products and shared memory: 4 x 4096 tokens of 16 heads of 128 in bfloat16 at an odd address 0.88 ms, 2.3 for the three
+// walks of a backward pass (tiles: 0.12 and 0.22), in float16 1.7 and 4.4, in fp32 2.1 and 5.5; of 256 in bfloat16 2.3
+// and 4.9; gradients of 2 x 333 tokens of 6 heads of 48 and 80 in fp32 73 us.  Outputs of widths above 128 spill 64 to 130
+// bytes a thread at 255 registers.
 #include "linear_attention.cuh"
 
 namespace {
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ 
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           o[j][0] *= d_lo, o[j][1] *= d_lo, o[j][2] *= d_hi, o[j][3] *= d_hi;
-          if (APART) low[APART ? j : 0][0] *= d_lo, low[APART ? j : 0][1] *= d_lo, low[APART ? j : 0][2] *= d_hi, low[APART ? j : 0][3] *= d_hi;
+          if constexpr (APART) low[j][0] *= d_lo, low[j][1] *= d_lo, low[j][2] *= d_hi, low[j][3] *= d_hi;
         }
         for (int j0 = 0; j0 <= r0; j0 += 16) {
           float s[2][4] = {}, s_low[APART ? 2 : 1][4] = {};
@@ -751,8 +751,9 @@ cudaError_t bwd_t(const s4_linear_attention_bwd_args& a, St st, cudaStream_t s) 
   const auto size = [](int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; };
   const auto columns = [](int d) { return (d + kCols - 1) / kCols; };
   const long long ctas = (long long)a.batch * a.H * (2 * columns(a.K) + columns(a.V)) * ((a.L + 63) / 64);
+  const long long fit = (a.K > 128 || a.V > 128 ? 1ll : 2ll) * s4impl::num_sms();
   cudaError_t err;
-  if (size(a.K) == size(a.V) || (!s4impl::tiles_take(dk, code) && ctas <= (a.K > 128 || a.V > 128 ? 1ll : 2ll) * s4impl::num_sms())) {
+  if (size(a.K) == size(a.V) || (!s4impl::tiles_take(dk, code) && ctas <= fit)) {
     err = walk_t<T>(ws, 3, st, s);
   } else {
     Walks two = ws, one{};
@@ -804,7 +805,7 @@ cudaError_t launch_linear_attention(const s4_linear_attention_args& a, St st, cu
 }
 
 size_t linear_attention_bwd_scratch(int batch, int L, int H, int G, int K, int V) {
-  const size_t part = H == G ? 0 : section(sizeof(float) * (size_t)batch * L * H * K) + section(sizeof(float) * (size_t)batch * L * H * V);
+  const size_t each = sizeof(float) * (size_t)batch * L * H, part = H == G ? 0 : section(each * K) + section(each * V);
   return 2 * local_bytes(batch, L, H, V, K) + local_bytes(batch, L, H, K, V) + part;
 }
 

@@ -313,9 +313,9 @@ void pairs_of(int n, Product* p) {
 }
 
 // Sums in an accumulator drift, as the tensor cores cut off what an addition shifts out: about 1e-8 per addition of 16 k
-// (measured).  In fp32 an accumulator takes up 1024 k and is then added, rounded, to a second one (off by 3e-7 to 6e-7; their six products
-// hide the additions).  Logits of 16-bit inputs, whose lse is fp32 too, are summed in parts of 8192, gradients of float16 and bfloat16, off by up
-// to 2^-11 and 2^-8 themselves, in products of 65536 and 262144 k (4e-5 and 2e-4).
+// (measured).  In fp32 an accumulator takes up 1024 k and is then added, rounded, to a second one (off by 3e-7 to 6e-7; their
+// six products hide the additions).  Logits of 16-bit inputs, whose lse is fp32 too, are summed in parts of 8192; gradients
+// of float16 and bfloat16, off by up to 2^-11 and 2^-8 themselves, in products of 65536 and 262144 k (4e-5 and 2e-4).
 constexpr int kPart = 16;  // chunks
 int logits_part(int dtype) { return dtype == S4_F32 ? kPart : 128; }
 int most_chunks(int dtype) { return dtype == S4_F32 ? 1 << 30 : dtype == S4_F16 ? 1024 : 4096; }
@@ -340,7 +340,8 @@ cudaError_t multiply(const Operand& a, const Operand& b, long long M, long long 
   const long long tiles = (long long)p.tiles_m * p.tiles_n * splits;
   allow_shared<kernel>(Shape<BN>::BYTES);
   s4impl::TimedLaunch tl("vocab_loss", s);
-  kernel<<<(unsigned)(tiles < s4impl::num_sms() ? tiles : s4impl::num_sms()), 256, Shape<BN>::BYTES, s>>>(ma, mb, p, ep, counts, st);
+  const unsigned grid = (unsigned)(tiles < s4impl::num_sms() ? tiles : s4impl::num_sms());
+  kernel<<<grid, 256, Shape<BN>::BYTES, s>>>(ma, mb, p, ep, counts, st);
   return cudaGetLastError();
 }
 
