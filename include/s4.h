@@ -593,7 +593,8 @@ s4_status s4_vocab_loss_fwd(const s4_vocab_loss_args* a, void* stream);
  * s4_vocab_loss_bwd -- gradients of sum_rows dloss loss from the forward's inputs and its lse:
  *     g_v = dloss (exp(x_v - lse) - [v = target])  (0 for rows without a target),
  *     dh = sum_v g_v w_v,   dw_v = sum_rows g_v h.
- * The logits are formed again, a piece of the vocabulary at a time.
+ * The logits are formed again, a piece of the vocabulary at a time.  Hidden states of rows without a target may
+ * hold anything: the lse of one that is not finite is not finite either, by which the row is left out of dw.
  */
 typedef struct {
     const void *h, *w, *targets;

@@ -3,6 +3,8 @@ backward are the library's calls (block.py, sequence.py).  Nothing beside the in
 pass (the vocabulary loss keeps its lse).  Activations and parameters as there; sequences start from a state of zeros.
 There are no second derivatives: gradients taken with create_graph=True raise where they are differentiated.
 What is a constant of an operator and requires a gradient all the same is refused.
+A backward pass that is captured into a CUDA graph needs leaves of its own: torch accumulates a leaf's gradient on the stream of
+the first graph that still holds it, which may not be captured.
 
     short_conv(x, w, bias, lengths)                               -> y
     selective_scan(x, dt, A, B, C, D, z, dt_bias, lengths)        -> y
