@@ -10,9 +10,9 @@
 //
 // Per chunk at widths 128: S, P C and A M 2^22 operations each, D 2^22 a term, which takes 1.7 to 2 us of an SM's share of
 // the measured rate; the inputs and the output are 128 KB, 2.9 us of an SM's share of the memory's.  Measured on 4 x 4096
-// tokens of 16 heads of 128: 217 us for the three walks of a backward pass, 3.4 us a chunk on 152 SMs at once; what is
+// tokens of 16 heads of 128: 219 us for the three walks of a backward pass, 3.4 us a chunk on 152 SMs at once; what is
 // above the memory's share are 40 of 192 walks left for a second round, and three walks that read 12 arrays
-// where one would read 7.  65536 tokens of 16 heads of 64 take 284 us, 3.0 us a chunk (64 KB, 1.4 us): there
+// where one would read 7.  65536 tokens of 16 heads of 64 take 266 us, 2.8 us a chunk (64 KB, 1.4 us): there
 // the warp that issues the products is the bound, 40 of them per chunk at 90 cycles or so (a right operand of 64
 // columns does not feed the tensor cores), and a walk over segments reads keys and values twice.  Outputs spill 24 to 48
 // bytes a thread at the 128 registers that four warpgroups start with (140 to 236 bytes loaded again).
@@ -235,7 +235,8 @@ __device__ __noinline__ bool last_lost(const Walk& w, uint32_t o1) {
 // leaves the state infinite or NaN in its column for good: the state's warps look once, at the end (warps 0 to 3 at the
 // sums of a last chunk that the state does not take up), and warps 0 to 3 then go through the tokens again one by one
 // (looking at every chunk's sums, with a call there to form them again, took 4 to 13 % longer; this way
-// 0 to 3 %).
+// 0 to 3 %).  The roles lie in the order in which the instruction caches take them best: with the keys behind the state 65536 tokens
+// of 16 heads of 64 took 284 us instead of 266, the other cases 1 % less.
 template <int DK, int DV, int NK, bool STATE>
 __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constant__ Passes ps, s4impl::St st) {
   using R = Room<DK, DV, NK, STATE>;
@@ -519,6 +520,74 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       rows(std::true_type{});
     else
       rows(std::false_type{});
+  } else if (wid >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    // The keys of a chunk, scaled: four lanes to a token (odd tokens take the halves of 64 columns in the other
+    // order, so that the lanes' packs lie in different banks).
+    const int r = (wid - 12) * 32 + lane, chunks = sp.chunks;
+    const bool rev = w.reverse;
+    int slots = 0;
+    bool ok = true;
+    for (int k = 0; k < chunks; ++k) {
+      const int t = start_of(k), n = sp.end - t < kC ? sp.end - t : kC, sb = k % R::SB, sc = k % R::SC;
+      const int less = !STATE && sp.last && k + 1 == chunks && !rev ? 1 : 0;
+      if (n < kC) {
+        // first of all: the products wait for it before they free the keys' slots
+        if (!wait_warp(&full_c[sc], k / R::SC)) break;
+        if (r >= n)
+#pragma unroll 1
+          for (int c = 0; c < DV / 8; ++c)
+            *reinterpret_cast<uint4*>(smem + R::C + sc * R::TC + c / 8 * 16384 + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+        s4dev::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) arrive(&c_clean);
+      }
+      if (!wait_warp(&full_b[sb], k / R::SB)) break;
+      if (updates(k)) {
+        const int token = r >> 2, quarter = r & 3;
+#pragma unroll 1
+        for (int j = 0; j < kC; j += kSlot, ++slots) {
+          const int sk = slots % R::SK, at = j + token;
+          ok = wait_warp(&keys_free[sk], slots / R::SK + 1);
+          if (!ok) break;
+          const float f = at < n ? power(g, rev ? at + 1 : n - less - at) : 0.f;
+          const float2 ff = make_float2(f, f);
+          const char* from = smem + R::B + sb * R::TA + at * 128;
+          char* to = smem + R::K + sk * NK * R::TK + token * 128;
+          const int c0 = ((quarter + 4 * (token & 1)) ^ (token & 7)) * 16, c1 = ((quarter + 4 * (~token & 1)) ^ (token & 7)) * 16;
+          uint4 v[DK / 32];
+#pragma unroll
+          for (int y = 0; y < DK / 32; ++y) v[y] = *reinterpret_cast<const uint4*>(from + y / 2 * 16384 + (y & 1 ? c1 : c0));
+#pragma unroll
+          for (int y = 0; y < DK / 32; ++y) {
+            if (at >= n) v[y] = make_uint4(0, 0, 0, 0);  // behind the last token: anything, NaN too
+            const unsigned x[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
+            unsigned o[NK][4];
+#pragma unroll
+            for (int w4 = 0; w4 < 4; ++w4) {
+              float2 z = mul2(make_float2(__uint_as_float(x[w4] << 16), __uint_as_float(x[w4] & 0xffff0000u)), ff);
+#pragma unroll
+              for (int p = 0; p < NK; ++p) {
+                o[p][w4] = two_of<__nv_bfloat16>(z.x, z.y);
+                if (p + 1 < NK)
+                  z = fma2(make_float2(__uint_as_float(o[p][w4] << 16), __uint_as_float(o[p][w4] & 0xffff0000u)),
+                           make_float2(-1.f, -1.f), z);
+              }
+            }
+#pragma unroll
+            for (int p = 0; p < NK; ++p)
+              *reinterpret_cast<uint4*>(to + p * R::TK + y / 2 * (kSlot * 128) + (y & 1 ? c1 : c0)) =
+                  make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
+          }
+          s4dev::fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) arrive(&keys_ready[sk]);
+        }
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) arrive(&empty_b[sb]);
+    }
   } else if (wid >= 4 && wid < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int r = (wid - 4) * 32 + lane;  // a row of the state
@@ -612,74 +681,6 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
           if (2 * c + 1 < dc) wr(to + (2 * c + 1) * step, by * m[c].y);
         }
       }
-    }
-  } else if (wid >= 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    // The keys of a chunk, scaled: four lanes to a token (odd tokens take the halves of 64 columns in the other
-    // order, so that the lanes' packs lie in different banks).
-    const int r = (wid - 12) * 32 + lane, chunks = sp.chunks;
-    const bool rev = w.reverse;
-    int slots = 0;
-    bool ok = true;
-    for (int k = 0; k < chunks; ++k) {
-      const int t = start_of(k), n = sp.end - t < kC ? sp.end - t : kC, sb = k % R::SB, sc = k % R::SC;
-      const int less = !STATE && sp.last && k + 1 == chunks && !rev ? 1 : 0;
-      if (n < kC) {
-        // first of all: the products wait for it before they free the keys' slots
-        if (!wait_warp(&full_c[sc], k / R::SC)) break;
-        if (r >= n)
-#pragma unroll 1
-          for (int c = 0; c < DV / 8; ++c)
-            *reinterpret_cast<uint4*>(smem + R::C + sc * R::TC + c / 8 * 16384 + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-        s4dev::fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) arrive(&c_clean);
-      }
-      if (!wait_warp(&full_b[sb], k / R::SB)) break;
-      if (updates(k)) {
-        const int token = r >> 2, quarter = r & 3;
-#pragma unroll 1
-        for (int j = 0; j < kC; j += kSlot, ++slots) {
-          const int sk = slots % R::SK, at = j + token;
-          ok = wait_warp(&keys_free[sk], slots / R::SK + 1);
-          if (!ok) break;
-          const float f = at < n ? power(g, rev ? at + 1 : n - less - at) : 0.f;
-          const float2 ff = make_float2(f, f);
-          const char* from = smem + R::B + sb * R::TA + at * 128;
-          char* to = smem + R::K + sk * NK * R::TK + token * 128;
-          const int c0 = ((quarter + 4 * (token & 1)) ^ (token & 7)) * 16, c1 = ((quarter + 4 * (~token & 1)) ^ (token & 7)) * 16;
-          uint4 v[DK / 32];
-#pragma unroll
-          for (int y = 0; y < DK / 32; ++y) v[y] = *reinterpret_cast<const uint4*>(from + y / 2 * 16384 + (y & 1 ? c1 : c0));
-#pragma unroll
-          for (int y = 0; y < DK / 32; ++y) {
-            if (at >= n) v[y] = make_uint4(0, 0, 0, 0);  // behind the last token: anything, NaN too
-            const unsigned x[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
-            unsigned o[NK][4];
-#pragma unroll
-            for (int w4 = 0; w4 < 4; ++w4) {
-              float2 z = mul2(make_float2(__uint_as_float(x[w4] << 16), __uint_as_float(x[w4] & 0xffff0000u)), ff);
-#pragma unroll
-              for (int p = 0; p < NK; ++p) {
-                o[p][w4] = two_of<__nv_bfloat16>(z.x, z.y);
-                if (p + 1 < NK)
-                  z = fma2(make_float2(__uint_as_float(o[p][w4] << 16), __uint_as_float(o[p][w4] & 0xffff0000u)),
-                           make_float2(-1.f, -1.f), z);
-              }
-            }
-#pragma unroll
-            for (int p = 0; p < NK; ++p)
-              *reinterpret_cast<uint4*>(to + p * R::TK + y / 2 * (kSlot * 128) + (y & 1 ? c1 : c0)) =
-                  make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
-          }
-          s4dev::fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) arrive(&keys_ready[sk]);
-        }
-      }
-      if (!ok) break;
-      __syncwarp();
-      if (lane == 0) arrive(&empty_b[sb]);
     }
   }
   __syncwarp();
